@@ -179,10 +179,8 @@ def _pool(case, blocks, gen, dev):
     """A cache that has been in use: every slot holds something."""
     shape = (blocks, case["block"], case["kv_heads"], case["head_dim"])
     if case.get("fp8"):
-        codes = torch.randint(0, 127, shape, generator=gen, device=dev, dtype=torch.uint8)
-        # magnitudes up to 2^4 (codes 0x00 to 0x58) and a sign
-        return (codes * 0x58 // 127) | (torch.randint(0, 2, shape, generator=gen, device=dev,
-                                                      dtype=torch.uint8) << 7)
+        x = torch.randn(shape, generator=gen, device=dev, dtype=torch.float32)
+        return (x * 8).clamp(-_E4M3_MAX, _E4M3_MAX).to(torch.float8_e4m3fn).view(torch.uint8)
     return torch.randn(shape, generator=gen, device=dev, dtype=torch.float32).to(_DTYPES[case["dtype"]])
 
 
