@@ -407,6 +407,159 @@ int pa_decode_step(const void* q, const void* k, const void* v, const int64_t* s
                    float* exp_sums, int32_t* counters, void* out, const pa_shape* shp,
                    void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * A cache within a budget of tokens
+ * ---------------------------------------------------------------------------
+ * Long contexts outgrow the pool, and the pages' only answers are preemption
+ * and swapping (tcdigital article, --swap-space; ta-paperlens scheduler).
+ * The entry points below let a sequence stay on the device with fewer
+ * tokens: keys are turned to their positions before they are cached
+ * (pa_rope_and_cache), so that a token's place in the cache is free to
+ * change; decode and prefill account for the attention weight each cached
+ * token receives (pa_decode_weights, pa_prefill_weights); and pa_evict keeps
+ * the first, the newest and the most attended tokens and closes the gaps.
+ *
+ * State of a batch, device memory owned by the caller, per (sequence, KV
+ * head) one row of `stride` elements (stride >= max_blocks_per_seq *
+ * block_size; entry i belongs to the token at cache index i):
+ *   weights    [num_seqs][num_kv_heads][stride]  fp32   weight added up so far
+ *   positions  [num_seqs][num_kv_heads][stride]  int32  the token's position
+ * Each call takes the state to read and the state to write; the two may be
+ * the same arrays, and must not overlap otherwise.  Entries at or past the
+ * context length are neither read nor written.
+ */
+
+/*
+ * pa_rope_and_cache: rotary positions, and the cache write of
+ * pa_reshape_and_cache, in one launch.  For t < num_tokens, head h and pair
+ * i < rotary_dim / 2 of its first rotary_dim dims, with the angle
+ * a = positions[t] * inv_freq[i]:
+ *   x' = factor * (x cos a - y sin a),   y' = factor * (y cos a + x sin a),
+ * (x, y) being dims (i, i + rotary_dim / 2), or (2i, 2i + 1) with
+ * interleaved = 1; dims past rotary_dim are copied.  Turned q rows go to
+ * q_out, turned k rows and v rows to cache slot slot_mapping[t], which is
+ * treated as in pa_reshape_and_cache (slots that are not negative must
+ * differ).  Scaling of the positions for long contexts is part of inv_freq
+ * and factor.  Angles are reduced exactly for any int64 position and any
+ * inv_freq; the products are in fp32 and each result is rounded once.
+ * q, k, v: row t starts t * stride elements on, [heads][head_dim] inside (so
+ * they may be slices of one projection's output); strides are multiples of 8
+ * elements, of at least a row.  q may be null (keys only: q_stride, q_out
+ * and num_q_heads are not used).  q_out may be q itself with the same stride,
+ * and must not overlap the inputs otherwise.  positions, slot_mapping [T]
+ * int64, inv_freq [rotary_dim / 2] fp32: device.
+ * rotary_dim: a multiple of 16 (else PA_ERR_UNSUPPORTED), 0 to head_dim.
+ * shp: num_q_heads, num_kv_heads (any ratio), head_dim, block_size,
+ * num_blocks, dtype.
+ */
+int pa_rope_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                      const void* v, int64_t v_stride, const int64_t* positions,
+                      const int64_t* slot_mapping, const float* inv_freq, int32_t rotary_dim,
+                      int32_t interleaved, float factor, void* q_out, int64_t q_out_stride,
+                      void* k_cache, void* v_cache, int64_t num_tokens, const pa_shape* shp,
+                      void* stream);
+
+/* pa_rope_and_cache into an E4M3 cache: the turned key is quantised from
+ * fp32, without a rounding to the 16-bit type before. */
+int pa_rope_and_cache_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          const void* v, int64_t v_stride, const int64_t* positions,
+                          const int64_t* slot_mapping, const float* inv_freq, int32_t rotary_dim,
+                          int32_t interleaved, float factor, void* q_out, int64_t q_out_stride,
+                          void* k_cache, void* v_cache, int64_t num_tokens, float k_scale,
+                          float v_scale, const pa_shape* shp, void* stream);
+
+/*
+ * pa_decode_weights: decode attention (the result of pa_decode_split +
+ * pa_reduce) that also adds up what it attends to.  With p[h][i] the softmax
+ * weight of token i for query head h, and g the KV head of a group of heads:
+ *   weights_out[b][g][i] = weights[b][g][i] + sum over the group of p[h][i]
+ * for i < L_b; the newest token, i = L_b - 1, has nothing added up yet and
+ * gets the sum alone.  weights may be null (nothing added up yet).
+ * max_context_len >= every L_b (tokens past it are not attended),
+ * partition_size a multiple of block_size.  workspace: device memory of at
+ * least pa_decode_weights_workspace_size bytes, 16-byte aligned, no initial
+ * contents; calls that overlap on the GPU must not share it.  Two launches.
+ */
+size_t pa_decode_weights_workspace_size(const pa_shape* shp, int32_t max_context_len,
+                                        int32_t partition_size);
+int pa_decode_weights(const void* q, const void* k_cache, const void* v_cache,
+                      const int32_t* block_tables, const int32_t* context_lens, float scale,
+                      int32_t max_context_len, int32_t partition_size, const float* weights,
+                      float* weights_out, int64_t weights_stride, void* workspace,
+                      size_t workspace_bytes, void* out, const pa_shape* shp, void* stream);
+
+/* pa_decode_weights over an E4M3 cache. */
+int pa_decode_weights_fp8(const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* block_tables, const int32_t* context_lens, float scale,
+                          float k_scale, float v_scale, int32_t max_context_len,
+                          int32_t partition_size, const float* weights, float* weights_out,
+                          int64_t weights_stride, void* workspace, size_t workspace_bytes,
+                          void* out, const pa_shape* shp, void* stream);
+
+/*
+ * pa_prefill_weights: the attention weights that a chunk's queries give to
+ * the cached tokens (attention itself is pa_prefill, on the same q,
+ * query_start and cache).  Queries are those of pa_prefill: new token i of
+ * sequence b sits at cache index L_b - C_b + i and sees the tokens up to its
+ * own.  The last min(window, C_b) of them are counted, all with window = 0:
+ *   weights_out[b][g][j] = weights[b][g][j]
+ *       + sum over the group's heads h and the counted i of p[i][h][j]
+ * for j < L_b, with weights taken as zero for the chunk's own tokens
+ * (j >= L_b - C_b) and where weights is null.
+ * num_tokens: rows of q; max_query_len >= every C_b; max_context_len >= every
+ * L_b.  Values outside these bounds are clamped and set
+ * PA_DEVERR_BAD_CONTEXT.  scale must be finite and > 0.  16-bit caches.
+ * workspace as in pa_decode_weights, of pa_prefill_weights_workspace_size
+ * bytes.
+ */
+size_t pa_prefill_weights_workspace_size(const pa_shape* shp, int32_t max_query_len,
+                                         int32_t window);
+int pa_prefill_weights(const void* q, const void* k_cache, const int32_t* block_tables,
+                       const int32_t* context_lens, const int32_t* query_start, float scale,
+                       int64_t num_tokens, int32_t max_query_len, int32_t max_context_len,
+                       int32_t window, const float* weights, float* weights_out,
+                       int64_t weights_stride, void* workspace, size_t workspace_bytes,
+                       const pa_shape* shp, void* stream);
+
+/*
+ * pa_evict: cut every sequence of more than `trigger` tokens down to
+ * `budget`.  Token i of (b, g) has the position
+ *   pos = i < known_lens[b] ? positions[b][g][i] : i + seen_lens[b] - L_b,
+ * seen_lens[b] being the tokens the sequence has had in all (tokens appended
+ * since the last cut are in order; known_lens null: 0).  Of a sequence with
+ * L_b > trigger each KV head keeps `budget` tokens: those with pos < sinks or
+ * pos >= seen_lens[b] - recent, then those of the largest weight, ties (-0
+ * and +0 are equal) to the lowest index, NaN below every number.  Kept tokens
+ * at index < budget stay in place; the n-th kept token at index >= budget
+ * moves to the n-th gap (K and V rows, weight, position).  Afterwards
+ *   new_lens[b]      = budget, or L_b where nothing was cut
+ *   weights_out, positions_out hold the entries i < new_lens[b],
+ * and the next calls take new_lens as context_lens and known_lens (advanced
+ * by the tokens appended in the case of context_lens alone).  Every KV head
+ * keeps tokens of its own choice, so the caches' rows of one index belong to
+ * different positions in different heads.
+ * k_cache and v_cache are changed in place: the blocks of a sequence that is
+ * cut must not be shared with another (pa_copy_blocks gives it its own).  A
+ * block id outside the pool sets PA_DEVERR_BAD_CONTEXT and its rows are not
+ * moved.  budget >= 1, budget >= sinks + recent, trigger >= budget; new_lens
+ * must not be one of the input arrays.  workspace as in pa_decode_weights,
+ * of pa_evict_workspace_size bytes.  pa_evict_fp8: the same on an E4M3 cache.
+ */
+size_t pa_evict_workspace_size(const pa_shape* shp, int32_t budget);
+int pa_evict(void* k_cache, void* v_cache, const int32_t* block_tables,
+             const int32_t* context_lens, const int32_t* seen_lens, const int32_t* known_lens,
+             const float* weights, const int32_t* positions, int64_t stride, int32_t budget,
+             int32_t trigger, int32_t sinks, int32_t recent, float* weights_out,
+             int32_t* positions_out, int32_t* new_lens, void* workspace, size_t workspace_bytes,
+             const pa_shape* shp, void* stream);
+int pa_evict_fp8(void* k_cache, void* v_cache, const int32_t* block_tables,
+                 const int32_t* context_lens, const int32_t* seen_lens, const int32_t* known_lens,
+                 const float* weights, const int32_t* positions, int64_t stride, int32_t budget,
+                 int32_t trigger, int32_t sinks, int32_t recent, float* weights_out,
+                 int32_t* positions_out, int32_t* new_lens, void* workspace,
+                 size_t workspace_bytes, const pa_shape* shp, void* stream);
+
 /* Static description of a status code. */
 const char* pa_status_string(int status);
 

@@ -191,6 +191,38 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
+cudaError_t pa::error_word(int** out) { return ::error_word(out); }
+
+int pa::check_shape(const pa_shape* shp, bool need_q_heads) { return ::check_shape(shp, need_q_heads); }
+
+int pa::check_decode_args(const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* block_tables, const int32_t* context_lens,
+                          const pa_shape* shp) {
+    return ::check_decode_args(q, k_cache, v_cache, block_tables, context_lens, shp);
+}
+
+int pa::encode_cache_map(CUtensorMap* map, const void* base, const pa_shape* shp, bool fp8) {
+    return ::encode_cache_map(map, base, shp, fp8);
+}
+
+int pa::encode_query_map(CUtensorMap* map, const void* q, const pa_shape* s, int64_t tokens,
+                         int box_heads, int box_tokens) {
+    EncodeTiledFn enc = nullptr;
+    cudaError_t e = get_encoder(&enc);
+    if (e != cudaSuccess) return cuda_fail(e);
+    cuuint64_t dims[3] = {(cuuint64_t)s->head_dim, (cuuint64_t)s->num_q_heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)s->head_dim * 2,
+                             (cuuint64_t)s->num_q_heads * s->head_dim * 2};
+    cuuint32_t box[3] = {(cuuint32_t)pa::kBoxElems, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, s->dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                     3, const_cast<void*>(q), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PA_OK : PA_ERR_INVALID_ARG;
+}
+
 void pa::record_cuda_error(int cuda_error) { t_last_cuda_error = cuda_error; }
 
 cudaError_t pa::current_context(void** ctx) {
@@ -209,6 +241,13 @@ cudaError_t pa::current_context(void** ctx) {
     if (g_ctx_get(&c) != CUDA_SUCCESS) return cudaErrorDeviceUninitialized;   // "invalid device context"
     *ctx = static_cast<void*>(c);
     return cudaSuccess;
+}
+
+int pa::check_fp8(const pa_shape* shp, float k_scale, float v_scale) {
+    if (shp->head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (!(k_scale > 0.f) || !(v_scale > 0.f) || k_scale == INFINITY || v_scale == INFINITY)
+        return PA_ERR_INVALID_ARG;
+    return PA_OK;
 }
 
 int pa::check_split_request(const void* q, const void* k_cache, const void* v_cache,
@@ -294,12 +333,7 @@ int pa_reshape_and_cache(const void* k, const void* v, const int64_t* slot_mappi
 namespace {
 
 int check_kind(const pa_shape* shp, const CacheKind& ck) {
-    if (!ck.fp8) return PA_OK;
-    if (shp->head_dim != 128) return PA_ERR_UNSUPPORTED;
-    if (!(ck.k_scale > 0.f) || !(ck.v_scale > 0.f) || ck.k_scale == INFINITY ||
-        ck.v_scale == INFINITY)
-        return PA_ERR_INVALID_ARG;
-    return PA_OK;
+    return ck.fp8 ? pa::check_fp8(shp, ck.k_scale, ck.v_scale) : PA_OK;
 }
 
 cudaError_t launch(int mode, const pa_shape* shp, const CacheKind& ck, const CUtensorMap& tmk,

@@ -96,6 +96,31 @@ __device__ __forceinline__ uint4 new_token_chunk(const DecodeParams& p, int b, i
 #define PA_DECODE_WAIT_LIMIT(p) kWaitLimitNs
 #endif
 
+// Weights mode: every score of the tile (log2 units) to its place in
+// scores [.., token][head of the group], for the attention weights that are
+// added up once the row sums are known.
+struct KeepScores {
+    static constexpr bool kKeep = true;
+    float* scores;                 // the (sequence, KV head)'s
+    int group, t_end, lane;
+    __device__ __forceinline__ void operator()(int tok0, const float (&x)[4]) const {
+        const int r8 = lane >> 2, h = 2 * (lane & 3);
+        if (h >= group) return;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int tok = tok0 + r8 + 8 * i;
+            if (tok >= t_end) return;
+            float* dst = scores + (size_t)tok * group + h;
+            if ((group & 1) == 0) {
+                *reinterpret_cast<float2*>(dst) = make_float2(x[2 * i], x[2 * i + 1]);
+            } else {
+                dst[0] = x[2 * i];
+                if (h + 1 < group) dst[1] = x[2 * i + 1];
+            }
+        }
+    }
+};
+
 template <typename T, int D, int kMode, bool kFp8 = false>
 __global__ void __launch_bounds__(kDecodeThreads, kFp8 ? kMinCtasPerSmFp8 : kMinCtasPerSm)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
@@ -283,6 +308,11 @@ __global__ void __launch_bounds__(kDecodeThreads, kFp8 ? kMinCtasPerSmFp8 : kMin
     auto qfrag = [&](int kk, uint32_t& b0, uint32_t& b1) { lds64(q_lane + kk * 256, b0, b1); };
     TileState<D> ts;
     ts.reset();
+    using Emit = std::conditional_t<kMode == kModeWeights, KeepScores, NoScores>;
+    Emit emit;
+    if constexpr (kMode == kModeWeights)
+        emit = {p.scores + ((size_t)b * p.num_kv_heads + g) * p.max_parts * p.partition_tokens * G,
+                G, t_end, lane};
 
     // Fused step: the CTA of the last partition owns the sequence's new token
     // (position L - 1).  It checks that slot_mapping[b] is that position's
@@ -345,10 +375,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kFp8 ? kMinCtasPerSmFp8 : kMin
                                         mbar_arrive(&empty_bar[st0]);
                                         mbar_arrive(&empty_bar[st1]);
                                     }
-                                });
+                                }, emit);
             } else {
                 attend_tile_fp8(ts, qfrag, ktile0, vtile0, tok0, t_end, scale_log2, lane,
-                                [&] { release_stage(&empty_bar[st0], lane); });
+                                [&] { release_stage(&empty_bar[st0], lane); }, emit);
             }
         }
     } else {
@@ -373,7 +403,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kFp8 ? kMinCtasPerSmFp8 : kMin
                 __syncwarp();
             }
             attend_tile<T, D>(ts, qfrag, ktile, vtile, (tile_begin + it) * kTileTokens, t_end,
-                              scale_log2, lane);
+                              scale_log2, lane, emit);
             release_stage(&empty_bar[st], lane);
         }
     }
@@ -445,12 +475,12 @@ __global__ void __launch_bounds__(kDecodeThreads, kFp8 ? kMinCtasPerSmFp8 : kMin
         }
         const float inv = (kFp8 ? p.v_scale : 1.f) / den;
         const size_t qh = (size_t)b * p.num_q_heads + (size_t)g * G + h;
-        if (kMode == kModeSplit || (kMode == kModeStep && parts > 1)) {
+        if (kMode == kModeSplit || kMode == kModeWeights || (kMode == kModeStep && parts > 1)) {
             const size_t idx = qh * p.max_parts + part;
             *reinterpret_cast<float4*>(p.tmp_out + idx * D + d) =
                 make_float4(o0 * inv, o1 * inv, o2 * inv, o3 * inv);
             if (d == 0) {
-                p.max_logits[idx] = mt * kLn2;
+                p.max_logits[idx] = kMode == kModeWeights ? mt : mt * kLn2;
                 p.exp_sums[idx] = den * ex2(mref - mt);
             }
         } else {
@@ -546,6 +576,8 @@ cudaError_t launch_decode_t(int mode, const CUtensorMap& tmk, const CUtensorMap&
                             const DecodeParams& p, dim3 grid, cudaStream_t stream) {
     if (mode == kModeSplit) return launch_decode_mode<T, D, kModeSplit>(tmk, tmv, p, grid, stream);
     if (mode == kModeStep) return launch_decode_mode<T, D, kModeStep>(tmk, tmv, p, grid, stream);
+    if (mode == kModeWeights)
+        return launch_decode_mode<T, D, kModeWeights>(tmk, tmv, p, grid, stream);
     return launch_decode_mode<T, D, kModeSingle>(tmk, tmv, p, grid, stream);
 }
 
@@ -556,6 +588,8 @@ cudaError_t launch_decode_fp8_t(int mode, const CUtensorMap& tmk, const CUtensor
         return launch_decode_mode<T, 128, kModeSplit, true>(tmk, tmv, p, grid, stream);
     if (mode == kModeStep)
         return launch_decode_mode<T, 128, kModeStep, true>(tmk, tmv, p, grid, stream);
+    if (mode == kModeWeights)
+        return launch_decode_mode<T, 128, kModeWeights, true>(tmk, tmv, p, grid, stream);
     return launch_decode_mode<T, 128, kModeSingle, true>(tmk, tmv, p, grid, stream);
 }
 

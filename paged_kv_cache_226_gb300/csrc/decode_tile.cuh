@@ -28,6 +28,14 @@ namespace pa {
 constexpr int kBox16Bytes = kTileTokens * 128;       // one [16][128 B] box
 constexpr float kRescaleThresholdLog2 = 8.0f;        // rescale when the max grows > 2^8
 
+// What attend_tile and its FP8 forms hand each tile's masked scores to:
+// emit(tok0, x) with x[0], x[1] token tok0 + r8 and x[2], x[3] token
+// tok0 + r8 + 8, heads 2c4 and 2c4 + 1, in log2 units.  This one keeps none.
+struct NoScores {
+    static constexpr bool kKeep = false;      // row sums of the rounded P where P is fp16
+    __device__ __forceinline__ void operator()(int, const float (&)[4]) const {}
+};
+
 template <int D>
 struct TileState {
     float acc[D / 16][4];     // O^T slabs of 16 dims
@@ -257,15 +265,24 @@ __device__ __forceinline__ void fp8_mask(float (&x)[4], const float (&sc)[4], in
     }
 }
 
-// P of a tile in fp16 (added into the row sums), transposed into P^T fragments.
+// P of a tile in fp16 (added into the row sums: the rounded values, or with
+// kExactSums the values before rounding), transposed into P^T fragments.
+template <bool kExactSums>
 __device__ __forceinline__ void fp8_probs(TileState<128>& s, const float (&x)[4], uint32_t& pb0,
                                           uint32_t& pb1) {
     using M = Mma<__half>;
-    const uint32_t p01 = M::pack(ex2(x[0] - s.mA), ex2(x[1] - s.mB));
-    const uint32_t p23 = M::pack(ex2(x[2] - s.mA), ex2(x[3] - s.mB));
-    const float2 u = M::unpack(p01), w = M::unpack(p23);
-    s.lA += u.x + w.x;
-    s.lB += u.y + w.y;
+    const float e0 = ex2(x[0] - s.mA), e1 = ex2(x[1] - s.mB);
+    const float e2 = ex2(x[2] - s.mA), e3 = ex2(x[3] - s.mB);
+    const uint32_t p01 = M::pack(e0, e1);
+    const uint32_t p23 = M::pack(e2, e3);
+    if (kExactSums) {
+        s.lA += e0 + e2;
+        s.lB += e1 + e3;
+    } else {
+        const float2 u = M::unpack(p01), w = M::unpack(p23);
+        s.lA += u.x + w.x;
+        s.lB += u.y + w.y;
+    }
     pb0 = movmatrix_trans(p01);
     pb1 = movmatrix_trans(p23);
 }
@@ -282,11 +299,11 @@ __device__ __forceinline__ void warp_max_pairs(float& xa, float& xb) {
 // qfrag(kk, b0, b1) supplies the fp16 q^T fragments of k-step kk.
 // release() runs once the warp has read the staged codes into registers, so
 // the stage can be refilled while the P V products run.
-template <typename QFrag, typename Release>
+template <typename QFrag, typename Release, typename Emit = NoScores>
 __device__ __forceinline__ void attend_tile_fp8(TileState<128>& s, QFrag&& qfrag,
                                                 const uint8_t* ktile, const uint8_t* vtile,
                                                 int tok0, int t_end, float scale_log2, int lane,
-                                                Release&& release) {
+                                                Release&& release, Emit emit = Emit()) {
     uint4 klo[2], khi[2];
     fp8_load_k(klo, khi, ktile, lane);
     float sc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -302,11 +319,12 @@ __device__ __forceinline__ void attend_tile_fp8(TileState<128>& s, QFrag&& qfrag
 
     float x[4];
     fp8_mask(x, sc, tok0, t_end, scale_log2, lane);
+    emit(tok0, x);
     float xa = fmaxf(x[0], x[2]), xb = fmaxf(x[1], x[3]);
     warp_max_pairs(xa, xb);
     fp8_raise(s, xa, xb);
     uint32_t pb0, pb1;
-    fp8_probs(s, x, pb0, pb1);
+    fp8_probs<Emit::kKeep>(s, x, pb0, pb1);
 #pragma unroll
     for (int n = 0; n < 8; ++n) fp8_pv_slab(s.acc[n], v, n, pb0, pb1);
 }
@@ -316,12 +334,12 @@ __device__ __forceinline__ void attend_tile_fp8(TileState<128>& s, QFrag&& qfrag
 // one max reduction and one rescale test cover both, and each accumulator
 // slab takes both P V products, so the per-tile chain of dependent steps is
 // about halved.  release() runs once both tiles' codes are in registers.
-template <typename QFrag, typename Release>
+template <typename QFrag, typename Release, typename Emit = NoScores>
 __device__ __forceinline__ void attend_pair_fp8(TileState<128>& s, QFrag&& qfrag,
                                                 const uint8_t* ktile0, const uint8_t* vtile0,
                                                 const uint8_t* ktile1, const uint8_t* vtile1,
                                                 int tok0, int t_end, float scale_log2, int lane,
-                                                Release&& release) {
+                                                Release&& release, Emit emit = Emit()) {
     uint4 klo0[2], khi0[2], klo1[2], khi1[2];
     fp8_load_k(klo0, khi0, ktile0, lane);
     fp8_load_k(klo1, khi1, ktile1, lane);
@@ -341,13 +359,15 @@ __device__ __forceinline__ void attend_pair_fp8(TileState<128>& s, QFrag&& qfrag
     float x[4], y[4];
     fp8_mask(x, sc0, tok0, t_end, scale_log2, lane);
     fp8_mask(y, sc1, tok0 + kTileTokens, t_end, scale_log2, lane);
+    emit(tok0, x);
+    emit(tok0 + kTileTokens, y);
     float xa = fmaxf(fmaxf(x[0], x[2]), fmaxf(y[0], y[2]));
     float xb = fmaxf(fmaxf(x[1], x[3]), fmaxf(y[1], y[3]));
     warp_max_pairs(xa, xb);
     fp8_raise(s, xa, xb);
     uint32_t pb0, pb1, qb0, qb1;
-    fp8_probs(s, x, pb0, pb1);
-    fp8_probs(s, y, qb0, qb1);
+    fp8_probs<Emit::kKeep>(s, x, pb0, pb1);
+    fp8_probs<Emit::kKeep>(s, y, qb0, qb1);
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
         fp8_pv_slab(s.acc[n], v0, n, pb0, pb1);
@@ -366,13 +386,14 @@ __device__ __forceinline__ void put_tile_chunk(uint8_t* tile, int r, int c, uint
 // Attends the 16 tokens tok0 .. tok0+15 of a tile; tokens >= t_end are masked
 // (their V rows are zeroed in shared memory, since they may hold stale
 // non-finite bits).
-template <typename T, int D, typename QFrag>
+template <typename T, int D, typename QFrag, typename Emit = NoScores>
 __device__ __forceinline__ void attend_tile(TileState<D>& s, QFrag&& qfrag,
                                             uint8_t* ktile, uint8_t* vtile, int tok0, int t_end,
-                                            float scale_log2, int lane) {
+                                            float scale_log2, int lane, Emit emit = Emit()) {
     using M = Mma<T>;
     constexpr int kKSteps = D / 16;
     constexpr bool kSplitP = std::is_same<T, __nv_bfloat16>::value;
+    constexpr bool kExactSums = kSplitP || Emit::kKeep;
     const int r8 = lane >> 2;
     // ldmatrix row addresses: matrix j = lane/8 supplies row lane%8.
     // K (A operand, no transpose): j -> (tokens 8*(j&1).., dims hi = j>>1)
@@ -404,6 +425,7 @@ __device__ __forceinline__ void attend_tile(TileState<D>& s, QFrag&& qfrag,
     const float x1 = v_lo ? sc[1] * scale_log2 : -INFINITY;    // (r8,   hB)
     const float x2 = v_hi8 ? sc[2] * scale_log2 : -INFINITY;   // (r8+8, hA)
     const float x3 = v_hi8 ? sc[3] * scale_log2 : -INFINITY;   // (r8+8, hB)
+    emit(tok0, {x0, x1, x2, x3});
     float xa = fmaxf(x0, x2), xb = fmaxf(x1, x3);
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
@@ -441,6 +463,8 @@ __device__ __forceinline__ void attend_tile(TileState<D>& s, QFrag&& qfrag,
         const float2 u = M::unpack(p01), w = M::unpack(p23);
         pl0 = movmatrix_trans(M::pack(e0 - u.x, e1 - u.y));
         pl1 = movmatrix_trans(M::pack(e2 - w.x, e3 - w.y));
+    }
+    if (kExactSums) {
         s.lA += e0 + e2;
         s.lB += e1 + e3;
     } else {

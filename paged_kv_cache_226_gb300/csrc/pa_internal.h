@@ -83,6 +83,8 @@ struct DecodeParams {
     // FP8 (E4M3) cache only: per-tensor scales (k_scale is also folded into scale_log2)
     float k_scale;
     float v_scale;
+    // weights mode only: [B][Hkv][S * partition_tokens][G] scores in log2 units
+    float* scores;
 #ifdef PA_TEST_HOOKS
     // Test builds only (libpa_test.so): the producer of CTA test_cta (linear
     // index, -1: none) issues no tile from test_tile on, and every pipeline
@@ -136,6 +138,7 @@ cudaError_t launch_copy16(void* dst, const void* src, size_t n16, cudaStream_t s
 constexpr int kModeSingle = 0;   // one CTA per (sequence, KV head), final output
 constexpr int kModeSplit = 1;    // one CTA per partition, partial outputs
 constexpr int kModeStep = 2;     // split + cache write of the new token + in-kernel merge
+constexpr int kModeWeights = 3;  // split that also keeps every score (max_logits in log2 units)
 
 struct ReduceParams {
     const float* tmp_out;
@@ -174,6 +177,23 @@ cudaError_t launch_copy_blocks(const void* k_src, const void* v_src, int64_t src
                                void* k_dst, void* v_dst, int64_t dst_blocks,
                                const int64_t* mapping, int64_t num_pairs, int64_t block_bytes,
                                int* err, cudaStream_t stream);
+
+// Shape checks of every entry point: PA_OK or the status to return.
+int check_shape(const pa_shape* shp, bool need_q_heads);
+// The checks of the decode entry points: shape, pointers, alignment.
+int check_decode_args(const void* q, const void* k_cache, const void* v_cache,
+                      const int32_t* block_tables, const int32_t* context_lens,
+                      const pa_shape* shp);
+// head_dim and scales of an E4M3 cache.
+int check_fp8(const pa_shape* shp, float k_scale, float v_scale);
+// TMA map of a cache's [16 tokens][128 bytes] boxes; a status.
+int encode_cache_map(CUtensorMap* map, const void* base, const pa_shape* shp, bool fp8);
+// TMA map of q [tokens][Hq][D] (16-bit): boxes of [box_tokens][box_heads][64
+// dims], 128-byte swizzle; a status.
+int encode_query_map(CUtensorMap* map, const void* q, const pa_shape* shp, int64_t tokens,
+                     int box_heads, int box_tokens);
+// Device address of the error word on the current device.
+cudaError_t error_word(int** out);
 
 // Sets the value pa_last_cuda_error() reports on this host thread.
 void record_cuda_error(int cuda_error);

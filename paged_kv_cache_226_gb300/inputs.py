@@ -189,6 +189,19 @@ class PagedKVAllocator:
             held += self.block_size
         self.token_counts[seq_id] = count + n
 
+    def truncate(self, seq_id: int, n: int) -> None:
+        """The request keeps its first ``n`` cache entries (after an eviction
+        that moved what stays there): blocks past them return to the pool.
+        Blocks that other requests share cannot have been compacted."""
+        if not 0 <= n <= self.token_counts[seq_id]:
+            raise ValueError("n must be between 0 and the request's tokens")
+        table = self.page_tables[seq_id]
+        if any(self.pool.ref_count[p] > 1 for p in table):
+            raise ValueError("cannot truncate a request with shared blocks")
+        while len(table) > max(1, -(-n // self.block_size)):
+            self.pool.free(table.pop())
+        self.token_counts[seq_id] = n
+
     def free_sequence(self, seq_id: int) -> None:
         for p in self.page_tables.pop(seq_id):
             self.pool.free(p)

@@ -97,6 +97,23 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.pa_decode_step.restype = ctypes.c_int
         lib.pa_decode_static_workspace.argtypes = [V, V, V, V, V, F, I32, I32, V, S, V]
         lib.pa_decode_static_workspace.restype = ctypes.c_int
+        Z = ctypes.c_size_t
+        rope = [V, I64, V, I64, V, I64, V, V, V, I32, I32, F, V, I64, V, V, I64]
+        lib.pa_rope_and_cache.argtypes = [*rope, S, V]
+        lib.pa_rope_and_cache_fp8.argtypes = [*rope, F, F, S, V]
+        lib.pa_decode_weights_workspace_size.argtypes = [S, I32, I32]
+        lib.pa_decode_weights.argtypes = [V, V, V, V, V, F, I32, I32, V, V, I64, V, Z, V, S, V]
+        lib.pa_decode_weights_fp8.argtypes = [V, V, V, V, V, F, F, F, I32, I32, V, V, I64, V, Z, V,
+                                              S, V]
+        lib.pa_prefill_weights_workspace_size.argtypes = [S, I32, I32]
+        lib.pa_prefill_weights.argtypes = [V, V, V, V, V, F, I64, I32, I32, I32, V, V, I64, V, Z, S,
+                                           V]
+        lib.pa_evict_workspace_size.argtypes = [S, I32]
+        for fn in (lib.pa_evict, lib.pa_evict_fp8):
+            fn.argtypes = [V, V, V, V, V, V, V, V, I64, I32, I32, I32, I32, V, V, V, V, Z, S, V]
+        for fn in ("pa_decode_weights_workspace_size", "pa_prefill_weights_workspace_size",
+                   "pa_evict_workspace_size"):
+            getattr(lib, fn).restype = Z
         lib.pa_status_string.argtypes = [ctypes.c_int]
         lib.pa_status_string.restype = ctypes.c_char_p
         lib.pa_last_cuda_error.argtypes = []
@@ -574,6 +591,314 @@ def prefill(q, k_cache, v_cache, block_tables, context_lens, query_start, scale:
 def prefill_workspace_size(shp, max_query_len: int) -> int:
     """Bytes of the work-ordering workspace pa_prefill_ws needs (0: none)."""
     return int(load().pa_prefill_workspace_size(ctypes.byref(shp), int(max_query_len)))
+
+
+# ---- a cache within a budget of tokens --------------------------------------
+#
+# State of a batch: weights (fp32) and positions (int32), [B][Hkv][W] with W at
+# least the tokens a block table holds; entry i belongs to cache index i.
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
+                     factor: float = 1.0, original_len: int = 0, slow: float = 1.0,
+                     fast: float = 32.0, device=None) -> Tuple[torch.Tensor, float]:
+    """(inv_freq, factor) for ``rope_and_cache``: inv_freq[i] = base^(-2i/R),
+    stretched for contexts ``factor`` times the ``original_len`` trained on.
+
+    scaling: ``"none"``; ``"linear"`` (every angle divided by factor);
+    ``"ntk"`` (the base raised so that the slowest angle is divided by factor
+    and the fastest stays); ``"bands"`` (pairs that turn fewer than ``slow``
+    times over original_len are divided by factor, those that turn more than
+    ``fast`` times stay, a linear ramp in turns between); ``"yarn"`` (the
+    ramp linear in the pair's index, and cos / sin scaled by
+    0.1 ln(factor) + 1)."""
+    if rotary_dim <= 0 or rotary_dim % 2 or base <= 0:
+        raise ValueError("rotary_dim must be even and positive, base positive")
+    if factor < 1.0:
+        raise ValueError("factor must be at least 1")
+    half = rotary_dim // 2
+    i = torch.arange(half, dtype=torch.float64)
+    mult = 1.0
+    if scaling == "ntk" and half > 1:
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    inv = float(base) ** (-2.0 * i / rotary_dim)
+    if scaling == "linear":
+        inv = inv / factor
+    elif scaling in ("bands", "yarn"):
+        if original_len <= 0 or not 0 < slow < fast:
+            raise ValueError("bands and yarn need original_len > 0 and 0 < slow < fast")
+        turns = original_len * inv / (2 * np.pi)
+        if scaling == "bands":
+            keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)
+        else:
+            def pair_of(n):             # the pair that turns n times over original_len
+                return rotary_dim * np.log(original_len / (n * 2 * np.pi)) / (2 * np.log(base))
+            lo = max(np.floor(pair_of(fast)), 0.0)
+            hi = min(np.ceil(pair_of(slow)), half - 1.0)
+            keep = 1.0 - ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+            mult = 0.1 * float(np.log(factor)) + 1.0
+        inv = inv * keep + inv / factor * (1.0 - keep)
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return inv.to(torch.float32).to(device or "cpu"), mult
+
+
+def _rows(t: torch.Tensor, name: str, heads: int, dim: int, dtype, device) -> int:
+    """Token stride of a [T][heads][dim] tensor whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [num_tokens][{heads}][{dim}]")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and dim > 1) or (s1 != dim and heads > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return s0 if t.shape[0] > 1 else heads * dim
+
+
+def _scales(k_cache: torch.Tensor, k_scale, v_scale) -> bool:
+    """Whether the cache is E4M3; the scales go with it or not at all."""
+    fp8 = k_cache.dtype == torch.uint8
+    if fp8 and (k_scale is None or v_scale is None):
+        raise ValueError("an FP8 cache needs k_scale and v_scale")
+    if not fp8 and (k_scale is not None or v_scale is not None):
+        raise ValueError("k_scale and v_scale belong to an FP8 cache")
+    return fp8
+
+
+def _caches(k_cache: torch.Tensor, v_cache: torch.Tensor) -> torch.device:
+    dev = k_cache.device
+    _need(k_cache, "k_cache")
+    _need(v_cache, "v_cache", k_cache.dtype, dev)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("caches must be [num_blocks][block_size][num_kv_heads][head_dim]")
+    return dev
+
+
+def _state(t: torch.Tensor, name: str, num_seqs: int, num_kv_heads: int, tokens: int, dtype,
+           device) -> int:
+    """Row stride of a [B][Hkv][W] state tensor that covers the block table."""
+    _need(t, name, dtype, device)
+    if t.dim() != 3 or t.shape[0] != num_seqs or t.shape[1] != num_kv_heads or t.shape[2] < tokens:
+        raise ValueError(f"{name} must be [{num_seqs}][{num_kv_heads}][>= {tokens}]")
+    return t.shape[2]
+
+
+def _workspace(workspace: Optional[torch.Tensor], nbytes: int, fn: str, device) -> torch.Tensor:
+    if nbytes == 0:
+        raise PaError(fn, PA_ERR_INVALID_ARG)
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _need(workspace, "workspace", None, device)
+    return workspace
+
+
+def _launch(name: str, device: torch.device, *args) -> None:
+    """Calls an entry point on the device's current stream, with that device current."""
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == device.index:
+        _check(name, fn(*args, _stream_handle(device)))
+        return
+    with torch.cuda.device(device):
+        _check(name, fn(*args, _stream_handle(device)))
+
+
+def rope_and_cache(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                   positions: torch.Tensor, slot_mapping: torch.Tensor, inv_freq: torch.Tensor,
+                   k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   q_out: Optional[torch.Tensor] = None, interleaved: bool = False,
+                   factor: float = 1.0, k_scale: Optional[float] = None,
+                   v_scale: Optional[float] = None) -> Optional[torch.Tensor]:
+    """Rotary positions on the new tokens' q and k, and the cache write of k
+    and v (pa_rope_and_cache, or its E4M3 form for a uint8 cache); returns the
+    turned q.
+
+    q, k, v: [T][heads][D], a token's heads contiguous (slices of one
+    projection's output will do); ``q=None`` writes the cache only.
+    positions, slot_mapping: int64 [T]; inv_freq: fp32 [R/2], the first R dims
+    of a head turn (``rope_frequencies``).  ``q_out=q`` turns q in place."""
+    dev = _caches(k_cache, v_cache)
+    fp8 = _scales(k_cache, k_scale, v_scale)
+    hkv, d = k_cache.shape[2], k_cache.shape[3]
+    if k.dtype not in _DTYPE_CODES or (not fp8 and k.dtype != k_cache.dtype):
+        raise TypeError(f"k must have the cache's 16-bit dtype, got {k.dtype}")
+    ks = _rows(k, "k", hkv, d, k.dtype, dev)
+    vs = _rows(v, "v", hkv, d, k.dtype, dev)
+    _need(positions, "positions", torch.int64, dev)
+    _need(slot_mapping, "slot_mapping", torch.int64, dev)
+    _need(inv_freq, "inv_freq", torch.float32, dev)
+    T = k.shape[0]
+    if v.shape[0] != T or positions.shape != (T,) or slot_mapping.shape != (T,) or \
+            inv_freq.dim() != 1:
+        raise ValueError("v, positions and slot_mapping must have a row per token of k, "
+                         "inv_freq one dimension")
+    hq = qs = os_ = 0
+    if q is not None:
+        hq = q.shape[1] if q.dim() == 3 else 0
+        qs = _rows(q, "q", hq, d, k.dtype, dev)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        os_ = _rows(q_out, "q_out", hq, d, k.dtype, dev)
+        if q.shape[0] != T or q_out.shape[0] != T:
+            raise ValueError("q and q_out must have a row per token of k")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    shp = _fp8_shape(0, hq, k_cache, 1, k.dtype) if fp8 else make_shape(0, hq, k_cache, 1)
+    args = (_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(positions), _ptr(slot_mapping),
+            _ptr(inv_freq), 2 * inv_freq.shape[0], int(bool(interleaved)), float(factor),
+            _ptr(q_out), os_, _ptr(k_cache), _ptr(v_cache), T)
+    if fp8:
+        _launch("pa_rope_and_cache_fp8", dev, *args, float(k_scale), float(v_scale),
+                ctypes.byref(shp))
+    else:
+        _launch("pa_rope_and_cache", dev, *args, ctypes.byref(shp))
+    return q_out
+
+
+def weights_partition(num_seqs: int, num_kv_heads: int, max_context_len: int,
+                      block_size: int = 16) -> int:
+    """Partition size of ``decode_weights``."""
+    return DEFAULT_PARTITION
+
+
+def decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                   max_context_len: int, weights: Optional[torch.Tensor] = None,
+                   weights_out: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None, partition_size: Optional[int] = None,
+                   workspace: Optional[torch.Tensor] = None, k_scale: Optional[float] = None,
+                   v_scale: Optional[float] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Decode attention that adds each cached token's attention weight to
+    ``weights`` [B][Hkv][W] (pa_decode_weights, or its E4M3 form for a uint8
+    cache); returns (out, weights_out).  The newest token's entry is set, not
+    added to; ``weights=None`` starts at zero.  ``weights_out`` defaults to
+    ``weights`` (in place), or a new tensor of zeros."""
+    lib = load()
+    fp8 = _scales(k_cache, k_scale, v_scale)
+    common = _fp8_common if fp8 else _decode_common
+    shp, dev = common(q, k_cache, v_cache, block_tables, context_lens)
+    B, hkv, tokens = q.shape[0], k_cache.shape[2], block_tables.shape[1] * k_cache.shape[1]
+    if weights_out is None:
+        weights_out = weights if weights is not None else \
+            torch.zeros((B, hkv, tokens), dtype=torch.float32, device=dev)
+    stride = _state(weights_out, "weights_out", B, hkv, tokens, torch.float32, dev)
+    if weights is not None and \
+            _state(weights, "weights", B, hkv, tokens, torch.float32, dev) != stride:
+        raise ValueError("weights and weights_out must have the same shape")
+    out = torch.empty_like(q) if out is None else out
+    _need(out, "out", q.dtype, dev)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if partition_size is None:
+        partition_size = weights_partition(B, hkv, max_context_len, k_cache.shape[1])
+    ref = ctypes.byref(shp)
+    name = "pa_decode_weights_fp8" if fp8 else "pa_decode_weights"
+    ws = _workspace(workspace, lib.pa_decode_weights_workspace_size(
+        ref, int(max_context_len), int(partition_size)) if B else 1, name, dev)
+    _launch(name, dev, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+            _ptr(context_lens), float(scale), *((float(k_scale), float(v_scale)) if fp8 else ()),
+            int(max_context_len), int(partition_size), _ptr(weights), _ptr(weights_out), stride,
+            _ptr(ws), ws.numel() * ws.element_size(), _ptr(out), ref)
+    return out, weights_out
+
+
+def prefill_weights(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor,
+                    context_lens: torch.Tensor, query_start: torch.Tensor, scale: float,
+                    max_query_len: int, max_context_len: int, window: int = 0,
+                    weights: Optional[torch.Tensor] = None,
+                    weights_out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention weights that a chunk's queries (all, or the last ``window``)
+    give to the cached tokens, added to ``weights`` [B][Hkv][W]
+    (pa_prefill_weights; ``prefill`` gives the attention itself).  The chunk's
+    own tokens are set, not added to.  ``weights_out`` defaults to ``weights``
+    (in place), or a new tensor of zeros; returned."""
+    lib = load()
+    dev = _caches(k_cache, k_cache)
+    _need(q, "q", k_cache.dtype, dev)
+    _need(block_tables, "block_tables", torch.int32, dev)
+    _need(context_lens, "context_lens", torch.int32, dev)
+    _need(query_start, "query_start", torch.int32, dev)
+    B, hkv = context_lens.shape[0], k_cache.shape[2]
+    if q.dim() != 3 or q.shape[2] != k_cache.shape[3] or block_tables.dim() != 2 or \
+            block_tables.shape[0] != B or query_start.shape != (B + 1,):
+        raise ValueError("q must be [total_tokens][Hq][D], block_tables [num_seqs][blocks], "
+                         "query_start [num_seqs + 1]")
+    tokens = block_tables.shape[1] * k_cache.shape[1]
+    if weights_out is None:
+        weights_out = weights if weights is not None else \
+            torch.zeros((B, hkv, tokens), dtype=torch.float32, device=dev)
+    stride = _state(weights_out, "weights_out", B, hkv, tokens, torch.float32, dev)
+    if weights is not None and \
+            _state(weights, "weights", B, hkv, tokens, torch.float32, dev) != stride:
+        raise ValueError("weights and weights_out must have the same shape")
+    shp = make_shape(B, q.shape[1], k_cache, block_tables.shape[1])
+    ref = ctypes.byref(shp)
+    ws = _workspace(workspace, lib.pa_prefill_weights_workspace_size(
+        ref, int(max_query_len), int(window)), "pa_prefill_weights", dev)
+    _launch("pa_prefill_weights", dev, _ptr(q), _ptr(k_cache), _ptr(block_tables),
+            _ptr(context_lens), _ptr(query_start), float(scale), q.shape[0], int(max_query_len),
+            int(max_context_len), int(window), _ptr(weights), _ptr(weights_out), stride, _ptr(ws),
+            ws.numel() * ws.element_size(), ref)
+    return weights_out
+
+
+def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+          context_lens: torch.Tensor, seen_lens: torch.Tensor, budget: int,
+          weights: torch.Tensor, positions: torch.Tensor,
+          known_lens: Optional[torch.Tensor] = None, trigger: Optional[int] = None,
+          sinks: int = 0, recent: int = 0, weights_out: Optional[torch.Tensor] = None,
+          positions_out: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+          workspace: Optional[torch.Tensor] = None
+          ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Cut every sequence of more than ``trigger`` (default: budget) tokens to
+    ``budget`` per KV head: the first ``sinks`` positions, the ``recent``
+    newest and the largest weights stay, and the gaps are closed in the caches
+    (pa_evict; pa_evict_fp8 for a uint8 cache).  Returns (new_lens, weights,
+    positions); the state tensors are updated in place unless ``weights_out``
+    / ``positions_out`` are given.  seen_lens: int32 [B], tokens the sequence
+    has had in all; known_lens: int32 [B], the new_lens of the previous call
+    (entries of ``positions`` that are set; None: none).  Blocks past
+    ceil(new_len / block_size) are free afterwards
+    (``PagedKVAllocator.truncate``)."""
+    lib = load()
+    dev = _caches(k_cache, v_cache)
+    fp8 = k_cache.dtype == torch.uint8
+    _need(block_tables, "block_tables", torch.int32, dev)
+    _need(context_lens, "context_lens", torch.int32, dev)
+    _need(seen_lens, "seen_lens", torch.int32, dev)
+    B, hkv = context_lens.shape[0], k_cache.shape[2]
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.dim() != 1 or \
+            seen_lens.shape != (B,):
+        raise ValueError("block_tables must be [num_seqs][blocks], context_lens and seen_lens "
+                         "[num_seqs]")
+    tokens = block_tables.shape[1] * k_cache.shape[1]
+    weights_out = weights if weights_out is None else weights_out
+    positions_out = positions if positions_out is None else positions_out
+    strides = {_state(t, n, B, hkv, tokens, dt, dev) for t, n, dt in (
+        (weights, "weights", torch.float32), (weights_out, "weights_out", torch.float32),
+        (positions, "positions", torch.int32), (positions_out, "positions_out", torch.int32))}
+    if len(strides) != 1:
+        raise ValueError("weights, positions and their outputs must have the same shape")
+    new_lens = torch.empty_like(context_lens) if new_lens is None else new_lens
+    for t, n in ((known_lens, "known_lens"), (new_lens, "new_lens")):
+        if t is not None:
+            _need(t, n, torch.int32, dev)
+            if t.shape != (B,):
+                raise ValueError(f"{n} must be [num_seqs]")
+    trigger = budget if trigger is None else trigger
+    shp = _fp8_shape(B, hkv, k_cache, block_tables.shape[1], torch.float16) if fp8 else \
+        make_shape(B, hkv, k_cache, block_tables.shape[1])
+    ref = ctypes.byref(shp)
+    name = "pa_evict_fp8" if fp8 else "pa_evict"
+    ws = _workspace(workspace, lib.pa_evict_workspace_size(ref, int(budget)) if B else 1, name, dev)
+    _launch(name, dev, _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
+            _ptr(seen_lens), _ptr(known_lens), _ptr(weights), _ptr(positions), strides.pop(),
+            int(budget), int(trigger), int(sinks), int(recent), _ptr(weights_out),
+            _ptr(positions_out), _ptr(new_lens), _ptr(ws), ws.numel() * ws.element_size(), ref)
+    return new_lens, weights_out, positions_out
 
 
 STATIC_WORKSPACE_BYTES = 32 << 20

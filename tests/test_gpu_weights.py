@@ -1,0 +1,256 @@
+"""GPU parity of pa_decode_weights and pa_prefill_weights against the
+definition in 64 bits (bounds: bounded_util), with NaN in every cache slot and
+state entry that no result may depend on."""
+import numpy as np
+import pytest
+import torch
+
+from bounded_util import Batch, decode_reference, prefill_reference, same_bits, within
+from paged_kv_cache_226_gb300 import build, lib
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    build.build()
+    lib.load()
+    d = torch.device("cuda:0")
+    lib.read_device_errors(d)
+    return d
+
+
+def _past(x, w, filler):
+    """Entries past each length must still hold the filler."""
+    at = torch.arange(w.shape[2])
+    past = (at >= x.lens[:, None, None]).expand(w.shape)
+    assert bool((w.cpu()[past] == filler).all()), "an entry past the length was written"
+    return torch.where(past, torch.zeros_like(w.cpu()), w.cpu())
+
+
+def run_decode(dev, x, before, **kw):
+    want, ww, ob, wb = decode_reference(x, before)
+    after = torch.full((x.num_seqs, x.hkv, x.tokens), -7.0, device=dev)
+    out, got = lib.decode_weights(x.q.to(dev), x.k.to(dev), x.v.to(dev), x.tables.to(dev),
+                                  x.lens.to(dev), x.scale, max([1, *x.lens.tolist()]),
+                                  weights=before.to(dev) if before is not None else None,
+                                  weights_out=after, **x.scales(), **kw)
+    torch.cuda.synchronize(dev)
+    assert lib.read_device_errors(dev) == 0
+    within(out, want, ob, "out")
+    within(_past(x, got, -7.0), ww, wb, "weights")
+
+
+RAGGED = [1, 2, 15, 16, 17, 0, 33, 100, 257, 700]
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d,bs", [
+    (F16, 8, 2, 64, 16), (BF16, 32, 8, 128, 16), (F16, 8, 1, 128, 32), (BF16, 4, 4, 128, 16),
+    (F16, 6, 2, 64, 32), (BF16, 10, 2, 128, 16), (F16, 14, 2, 128, 16), (BF16, 2, 1, 64, 16)])
+@pytest.mark.parametrize("partition", [None, 32, 256])
+def test_decode_weights(dev, dtype, hq, hkv, d, bs, partition):
+    x = Batch(RAGGED, hq, hkv, d, bs, dtype, seed=hq + d)
+    run_decode(dev, x, x.state(), partition_size=partition)
+    if partition is None:
+        run_decode(dev, x, None)
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,bs", [(F16, 8, 2, 16), (BF16, 8, 1, 32), (F16, 3, 1, 16), (BF16, 4, 4, 16)])
+@pytest.mark.parametrize("partition", [None, 64])
+def test_decode_weights_e4m3(dev, dtype, hq, hkv, bs, partition):
+    x = Batch(RAGGED, hq, hkv, 128, bs, dtype, seed=hq, fp8=True)
+    run_decode(dev, x, x.state(), partition_size=partition)
+
+
+def test_decode_weights_long(dev):
+    run_decode(dev, Batch([20000, 3], 4, 1, 128, 16, BF16, seed=4), None)
+    run_decode(dev, Batch([9001], 8, 1, 128, 32, F16, seed=5, fp8=True), None)
+
+
+def test_decode_weights_sharp_scores(dev):
+    """One token takes nearly all the weight, the others underflow to zero."""
+    x = Batch([600, 33], 4, 1, 128, 16, F16, seed=6)
+    x.scale = 8.0
+    run_decode(dev, x, None)
+
+
+def test_decode_weights_in_place_and_defaults(dev):
+    x = Batch([40, 1, 300], 4, 2, 64, 16, F16, seed=7)
+    before = x.state()
+    _, ww, _, wb = decode_reference(x, before)
+    w = torch.where(torch.isnan(before), torch.full_like(before, -7.0), before).to(dev)
+    args = (x.q.to(dev), x.k.to(dev), x.v.to(dev), x.tables.to(dev), x.lens.to(dev), x.scale, 300)
+    out, got = lib.decode_weights(*args, weights=w)
+    assert got.data_ptr() == w.data_ptr()
+    within(_past(x, got, -7.0), ww, wb, "in place")
+    out2, fresh = lib.decode_weights(*args)
+    within(fresh, decode_reference(x)[1], decode_reference(x)[3], "from nothing")
+    assert same_bits(out, out2)
+
+
+def test_decode_weights_all_empty(dev):
+    x = Batch([0, 0], 4, 2, 64, 16, F16, seed=8)
+    run_decode(dev, x, None)
+
+
+def test_decode_matches_decode_split(dev):
+    """Beside the weights, the output is that of the split decode (up to P's
+    row sums, taken before their rounding here)."""
+    x = Batch([700, 60], 8, 2, 128, 16, BF16, seed=9, stale=False)
+    args = (x.q.to(dev), x.k.to(dev), x.v.to(dev), x.tables.to(dev), x.lens.to(dev), x.scale, 700)
+    a = lib.paged_attention(*args, mode="split", partition_size=256)
+    b, _ = lib.decode_weights(*args, partition_size=256)
+    assert float((a.float() - b.float()).abs().max()) <= 2.0 ** -8 * float(a.float().abs().max()) * 1.01
+
+
+def test_bad_tables_and_lengths_are_bounded(dev):
+    """A block id outside the pool reads as zeros, a length past the table is
+    clamped; both are reported."""
+    x = Batch([64, 64], 2, 1, 64, 16, F16, seed=10, stale=False, slack_width=0)
+    tables = x.tables.clone()
+    tables[0, 1] = -1
+    tables[1, 3] = x.k.shape[0]
+    x.k[x.tables[0, 1].long()] = 0
+    x.v[x.tables[0, 1].long()] = 0
+    x.k[x.tables[1, 3].long()] = 0
+    x.v[x.tables[1, 3].long()] = 0
+    want, ww, ob, wb = decode_reference(x)
+    lens = torch.tensor([64, 1000], dtype=torch.int32)
+    out, got = lib.decode_weights(x.q.to(dev), x.k.to(dev), x.v.to(dev), tables.to(dev), lens.to(dev),
+                                  x.scale, 64)
+    assert lib.read_device_errors(dev) == lib.PA_DEVERR_BAD_CONTEXT
+    within(out, want, ob, "out")
+    within(got, ww, wb, "weights")
+
+
+def test_decode_weights_two_streams_and_graph(dev):
+    """Two calls at once with workspaces of their own, and a captured call
+    replayed on changed contents."""
+    x, y = (Batch([500, 77, 1], 8, 2, 128, 16, F16, seed=s) for s in (11, 12))
+    streams = [torch.cuda.Stream(dev) for _ in range(2)]
+    got = []
+    for b, s in zip((x, y), streams):
+        s.wait_stream(torch.cuda.current_stream(dev))
+        with torch.cuda.stream(s):
+            got.append(lib.decode_weights(b.q.to(dev), b.k.to(dev), b.v.to(dev), b.tables.to(dev),
+                                          b.lens.to(dev), b.scale, 500))
+    torch.cuda.synchronize(dev)
+    for b, (out, w) in zip((x, y), got):
+        want, ww, ob, wb = decode_reference(b)
+        within(out, want, ob, "out")
+        within(w, ww, wb, "weights")
+    d = dict(q=x.q.to(dev), k_cache=x.k.to(dev), v_cache=x.v.to(dev), block_tables=x.tables.to(dev),
+             context_lens=x.lens.to(dev), scale=x.scale, max_context_len=500,
+             weights_out=torch.zeros(3, 2, x.tokens, device=dev), out=torch.zeros_like(x.q, device=dev))
+    lib.decode_weights(**d)
+    torch.cuda.synchronize(dev)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lib.decode_weights(**d)
+    d["q"].copy_(y.q)
+    d["context_lens"].copy_(torch.tensor([300, 77, 0]))
+    d["weights_out"].zero_()
+    g.replay()
+    torch.cuda.synchronize(dev)
+    x.q, x.lens = y.q, torch.tensor([300, 77, 0], dtype=torch.int32)
+    want, ww, ob, wb = decode_reference(x)
+    within(d["out"], want, ob, "replayed out")
+    within(d["weights_out"], ww, wb, "replayed weights")
+
+
+def run_prefill(dev, x, chunks, window, before, max_q=None):
+    q = torch.randn(sum(chunks) + 3, x.hq, x.d, generator=x.gen).to(x.dtype)
+    q[sum(chunks):] = float("nan")                      # rows behind the last sequence
+    ww, wb = prefill_reference(x, q, chunks, window, before)
+    start = torch.tensor([0, *chunks]).cumsum(0).to(torch.int32)
+    after = torch.full((x.num_seqs, x.hkv, x.tokens), -7.0, device=dev)
+    got = lib.prefill_weights(q.to(dev), x.k.to(dev), x.tables.to(dev), x.lens.to(dev), start.to(dev),
+                              x.scale, max_q or max([1, *chunks]), max([1, *x.lens.tolist()]),
+                              window=window, weights=before.to(dev) if before is not None else None,
+                              weights_out=after)
+    torch.cuda.synchronize(dev)
+    assert lib.read_device_errors(dev) == 0
+    within(_past(x, got, -7.0), ww, wb, "weights")
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d,bs", [
+    (F16, 8, 2, 64, 16), (BF16, 32, 8, 128, 16), (F16, 8, 1, 128, 32), (BF16, 4, 4, 128, 16),
+    (F16, 6, 2, 64, 32), (BF16, 10, 2, 128, 16), (F16, 14, 2, 128, 16), (BF16, 6, 1, 64, 16)])
+@pytest.mark.parametrize("window", [0, 1, 9])
+def test_prefill_weights(dev, dtype, hq, hkv, d, bs, window):
+    lens = [1, 15, 16, 17, 0, 33, 100, 257, 300, 40, 128, 129]
+    chunks = [1, 15, 1, 17, 0, 16, 37, 257, 150, 0, 128, 128]
+    x = Batch(lens, hq, hkv, d, bs, dtype, seed=hq + d + window)
+    run_prefill(dev, x, chunks, window, x.state())
+
+
+def test_prefill_weights_long(dev):
+    x = Batch([3001, 700], 4, 1, 128, 16, BF16, seed=21)
+    run_prefill(dev, x, [513, 700], 0, None)
+    x = Batch([5000, 2000, 31], 8, 2, 128, 16, F16, seed=22)
+    run_prefill(dev, x, [64, 300, 31], 32, x.state(), max_q=512)
+
+
+def test_prefill_weights_sharp_scores(dev):
+    x = Batch([400, 150], 8, 2, 128, 16, F16, seed=23)
+    x.scale = 6.0
+    run_prefill(dev, x, [200, 150], 0, None)
+
+
+def test_prefill_weights_no_queries(dev):
+    """No chunk at all: what was added up before is carried over."""
+    x = Batch([30, 1], 4, 2, 64, 16, F16, seed=24)
+    run_prefill(dev, x, [0, 0], 0, x.state())
+
+
+def test_one_query_equals_decode(dev):
+    x = Batch([300, 17, 1000], 8, 2, 128, 16, BF16, seed=25)
+    start = torch.arange(4, dtype=torch.int32)
+    a = lib.prefill_weights(x.q.to(dev), x.k.to(dev), x.tables.to(dev), x.lens.to(dev), start.to(dev),
+                            x.scale, 1, 1000)
+    _, ww, _, wb = decode_reference(x)
+    within(a, ww, wb, "one query")
+
+
+def test_prefill_weights_bad_bounds_are_reported(dev):
+    """A chunk longer than its context, rows past q, a length past the bound."""
+    x = Batch([20, 40], 2, 1, 64, 16, F16, seed=26, stale=False)
+    q = torch.randn(30, 2, 64, generator=x.gen).to(F16)
+    args = (q.to(dev), x.k.to(dev), x.tables.to(dev), x.lens.to(dev))
+    for start, bound in (([0, 25, 26], 40), ([0, 5, 40], 40), ([0, 5, 10], 39)):
+        w = lib.prefill_weights(*args, torch.tensor(start, dtype=torch.int32, device=dev), x.scale, 32, bound)
+        assert lib.read_device_errors(dev) == lib.PA_DEVERR_BAD_CONTEXT
+        assert bool(torch.isfinite(w).all())
+
+
+def test_refusals(dev):
+    x = Batch([20, 40], 4, 2, 64, 16, F16, seed=27, stale=False)
+    d = dict(q=x.q.to(dev), k_cache=x.k.to(dev), v_cache=x.v.to(dev), block_tables=x.tables.to(dev),
+             context_lens=x.lens.to(dev), scale=x.scale, max_context_len=40)
+    w = torch.zeros(2, 2, x.tokens, device=dev)
+    for bad in (dict(weights=w.double()), dict(weights=w[:, :, :16].contiguous()), dict(weights=w[:1]),
+                dict(weights=w, weights_out=torch.zeros(2, 2, x.tokens + 1, device=dev)),
+                dict(k_scale=1.0, v_scale=1.0), dict(out=d["q"][:1]), dict(weights=w.cpu())):
+        with pytest.raises((ValueError, TypeError)):
+            lib.decode_weights(**d, **bad)
+    for bad, status in ((dict(partition_size=24), lib.PA_ERR_INVALID_ARG),
+                        (dict(max_context_len=-1), lib.PA_ERR_INVALID_ARG),
+                        (dict(workspace=torch.zeros(64, dtype=torch.uint8, device=dev)), lib.PA_ERR_WORKSPACE)):
+        with pytest.raises(lib.PaError) as e:
+            lib.decode_weights(**{**d, **bad})
+        assert e.value.status == status
+    start = torch.tensor([0, 1, 2], dtype=torch.int32, device=dev)
+    p = dict(q=d["q"], k_cache=d["k_cache"], block_tables=d["block_tables"], context_lens=d["context_lens"],
+             query_start=start, scale=x.scale, max_query_len=1, max_context_len=40)
+    for bad in (dict(query_start=start.long()), dict(q=d["q"].bfloat16()), dict(weights=w[:1]),
+                dict(k_cache=torch.zeros(x.k.shape, dtype=torch.uint8, device=dev))):
+        with pytest.raises((ValueError, TypeError)):
+            lib.prefill_weights(**{**p, **bad})
+    for bad in (dict(scale=0.0), dict(scale=float("inf")), dict(window=-1), dict(max_query_len=-1),
+                dict(workspace=torch.zeros(1, dtype=torch.uint8, device=dev))):
+        with pytest.raises(lib.PaError):
+            lib.prefill_weights(**{**p, **bad})
