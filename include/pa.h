@@ -511,10 +511,10 @@ int pa_decode_weights_fp8(const void* q, const void* k_cache, const void* v_cach
  * L_b.  Values outside these bounds are clamped and set
  * PA_DEVERR_BAD_CONTEXT.  scale must be finite and > 0.  16-bit caches.
  * workspace as in pa_decode_weights, of pa_prefill_weights_workspace_size
- * bytes.
+ * bytes.  Two to four launches.
  */
 size_t pa_prefill_weights_workspace_size(const pa_shape* shp, int32_t max_query_len,
-                                         int32_t window);
+                                         int32_t max_context_len, int32_t window);
 int pa_prefill_weights(const void* q, const void* k_cache, const int32_t* block_tables,
                        const int32_t* context_lens, const int32_t* query_start, float scale,
                        int64_t num_tokens, int32_t max_query_len, int32_t max_context_len,

@@ -145,6 +145,20 @@ int decode_weights(const void* q, const void* k_cache, const void* v_cache,
     return finish(pa::launch_weights_merge(shp->dtype, shp->head_dim, m, shp->num_seqs, s));
 }
 
+// The sizes that the plan of pa_prefill_weights depends on.
+pa::PrefillWeightsParams prefill_weights_sizes(const pa_shape* shp, int32_t max_query_len,
+                                               int32_t max_context_len, int32_t window) {
+    pa::PrefillWeightsParams p{};
+    const int table = shp->max_blocks_per_seq * shp->block_size;
+    p.num_seqs = shp->num_seqs, p.num_kv_heads = shp->num_kv_heads;
+    p.group = shp->num_q_heads / shp->num_kv_heads;
+    p.max_context = max_context_len < table ? max_context_len : table;
+    const int longest = max_query_len < p.max_context ? max_query_len : p.max_context;
+    p.max_counted = window > 0 && window < longest ? window : longest;
+    p.window = window;
+    return p;
+}
+
 int evict_counted(const pa_shape* s, int32_t budget) {
     const int64_t over = (int64_t)s->max_blocks_per_seq * s->block_size - budget;
     return over <= 0 ? 0 : (int)(over < budget ? over : budget);
@@ -241,10 +255,11 @@ int pa_decode_weights_fp8(const void* q, const void* k_cache, const void* v_cach
 }
 
 size_t pa_prefill_weights_workspace_size(const pa_shape* shp, int32_t max_query_len,
-                                         int32_t window) {
-    if (pa::check_shape(shp, true) != PA_OK || max_query_len < 0 || window < 0) return 0;
-    const int counted = window > 0 && window < max_query_len ? window : max_query_len;
-    return round256((size_t)shp->num_seqs * counted * shp->num_q_heads * 2 * sizeof(float) + 1);
+                                         int32_t max_context_len, int32_t window) {
+    if (pa::check_shape(shp, true) != PA_OK || max_query_len < 0 || max_context_len < 0 || window < 0)
+        return 0;
+    pa::PrefillWeightsParams p = prefill_weights_sizes(shp, max_query_len, max_context_len, window);
+    return pa::prefill_weights_plan(p, nullptr);
 }
 
 int pa_prefill_weights(const void* q, const void* k_cache, const int32_t* block_tables,
@@ -255,35 +270,32 @@ int pa_prefill_weights(const void* q, const void* k_cache, const int32_t* block_
                        const pa_shape* shp, void* stream) {
     int st = pa::check_decode_args(k_cache, k_cache, k_cache, block_tables, context_lens, shp);
     if (st != PA_OK) return st;
-    if (num_tokens < 0 || max_query_len < 0 || max_context_len < 0 || window < 0 ||
-        !(scale > 0.f) || !std::isfinite(scale))
+    if (num_tokens < 0 || num_tokens > 0x7fffffffll || max_query_len < 0 || max_context_len < 0 ||
+        window < 0 || !(scale > 0.f) || !std::isfinite(scale))
         return PA_ERR_INVALID_ARG;
     if (shp->num_seqs == 0) return PA_OK;
     if (!query_start || !aligned4(query_start) || (num_tokens > 0 && !q) || !aligned16(q))
         return PA_ERR_INVALID_ARG;
     if ((st = check_state(weights, weights_out, weights_stride, shp)) != PA_OK) return st;
-    if (!workspace ||
-        workspace_bytes < pa_prefill_weights_workspace_size(shp, max_query_len, window))
-        return PA_ERR_WORKSPACE;
+    pa::PrefillWeightsParams p = prefill_weights_sizes(shp, max_query_len, max_context_len, window);
+    if (!workspace || workspace_bytes < pa::prefill_weights_plan(p, workspace)) return PA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return PA_ERR_INVALID_ARG;
-    pa::PrefillWeightsParams p{};
+    if (p.max_context == 0) return PA_OK;
+    if (num_tokens == 0) p.max_counted = 0;
+    CUtensorMap tmk, tmq;
+    if ((st = pa::encode_cache_map(&tmk, k_cache, shp, false)) != PA_OK) return st;
+    // no queries: the map is not used, any address will do
+    if ((st = pa::encode_query_map(&tmq, num_tokens > 0 ? q : k_cache, shp,
+                                   num_tokens > 0 ? num_tokens : 1, p.group, p.tile_tokens)) != PA_OK)
+        return st;
     cudaError_t e = pa::error_word(&p.err);
     if (e != cudaSuccess) return finish(e);
-    p.q = q, p.k_cache = k_cache, p.block_tables = block_tables, p.context_lens = context_lens;
-    p.query_start = query_start, p.weights = weights, p.weights_out = weights_out;
-    p.weights_stride = weights_stride, p.stats = static_cast<float*>(workspace);
+    p.block_tables = block_tables, p.context_lens = context_lens, p.query_start = query_start;
+    p.weights = weights, p.weights_out = weights_out, p.weights_stride = weights_stride;
     p.scale_log2 = scale * pa::kLog2e;
-    p.num_seqs = shp->num_seqs, p.num_q_heads = shp->num_q_heads;
-    p.num_kv_heads = shp->num_kv_heads, p.group = shp->num_q_heads / shp->num_kv_heads;
     p.max_blocks_per_seq = shp->max_blocks_per_seq, p.block_size = shp->block_size;
     p.num_blocks = shp->num_blocks, p.num_tokens = num_tokens;
-    const int table = shp->max_blocks_per_seq * shp->block_size;
-    p.max_context = max_context_len < table ? max_context_len : table;
-    if (p.max_context == 0) return PA_OK;
-    p.max_counted = num_tokens == 0 ? 0
-                    : window > 0 && window < max_query_len ? window : max_query_len;
-    p.window = window;
-    return finish(pa::launch_prefill_weights(shp->dtype, shp->head_dim, p,
+    return finish(pa::launch_prefill_weights(shp->dtype, shp->head_dim, tmk, tmq, p,
                                              static_cast<cudaStream_t>(stream)));
 }
 

@@ -52,27 +52,37 @@ cudaError_t launch_weights_merge(int dtype, int head_dim, const WeightsMergePara
                                  int num_seqs, cudaStream_t stream);
 
 struct PrefillWeightsParams {
-    const void* q;                 // [T][Hq][D]
-    const void* k_cache;
     const int32_t* block_tables;
     const int32_t* context_lens;
     const int32_t* query_start;    // [B + 1]
     const float* weights;          // [B][Hkv][stride], null: none yet
     float* weights_out;
     int64_t weights_stride;
-    float* stats;                  // per counted query row and head: reference max, 1 / sum
     int* err;
     float scale_log2;
-    int num_seqs, num_q_heads, num_kv_heads, group;
+    int num_seqs, num_kv_heads, group;
     int max_blocks_per_seq, block_size;
     int64_t num_blocks;
-    int64_t num_tokens;
+    int64_t num_tokens;            // rows of q
     int max_context;               // smaller of the table's and the caller's bound
     int max_counted;               // queries counted per sequence at most
     int window;                    // 0: every query of the chunk
+    // filled by prefill_weights_plan
+    int tile_tokens;               // query tokens per tile of 128 rows
+    int max_query_tiles;
+    int key_chunk, key_chunks;     // key tiles per unit of pass 1, units of the longest row
+    int query_chunk, query_chunks; // query tiles per unit of pass 2, units of a column
+    float* lse;                    // [B][Hkv][max_query_tiles][128], log2 units
+    float2* stats;                 // [key_chunks] x the same: maximum and sum
+    float* columns;                // [query_chunks][B][Hkv][columns_stride]
+    int columns_stride;
 };
 
-cudaError_t launch_prefill_weights(int dtype, int head_dim, const PrefillWeightsParams& p,
+// Chooses the chunks, lays out the workspace and returns its bytes (needs
+// the sizes: group, num_seqs, num_kv_heads, max_context, max_counted).
+size_t prefill_weights_plan(PrefillWeightsParams& p, void* workspace);
+cudaError_t launch_prefill_weights(int dtype, int head_dim, const CUtensorMap& tmk,
+                                   const CUtensorMap& tmq, const PrefillWeightsParams& p,
                                    cudaStream_t stream);
 
 struct EvictParams {

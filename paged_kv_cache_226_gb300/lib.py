@@ -105,7 +105,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.pa_decode_weights.argtypes = [V, V, V, V, V, F, I32, I32, V, V, I64, V, Z, V, S, V]
         lib.pa_decode_weights_fp8.argtypes = [V, V, V, V, V, F, F, F, I32, I32, V, V, I64, V, Z, V,
                                               S, V]
-        lib.pa_prefill_weights_workspace_size.argtypes = [S, I32, I32]
+        lib.pa_prefill_weights_workspace_size.argtypes = [S, I32, I32, I32]
         lib.pa_prefill_weights.argtypes = [V, V, V, V, V, F, I64, I32, I32, I32, V, V, I64, V, Z, S,
                                            V]
         lib.pa_evict_workspace_size.argtypes = [S, I32]
@@ -837,7 +837,7 @@ def prefill_weights(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.
     shp = make_shape(B, q.shape[1], k_cache, block_tables.shape[1])
     ref = ctypes.byref(shp)
     ws = _workspace(workspace, lib.pa_prefill_weights_workspace_size(
-        ref, int(max_query_len), int(window)), "pa_prefill_weights", dev)
+        ref, int(max_query_len), int(max_context_len), int(window)), "pa_prefill_weights", dev)
     _launch("pa_prefill_weights", dev, _ptr(q), _ptr(k_cache), _ptr(block_tables),
             _ptr(context_lens), _ptr(query_start), float(scale), q.shape[0], int(max_query_len),
             int(max_context_len), int(window), _ptr(weights), _ptr(weights_out), stride, _ptr(ws),

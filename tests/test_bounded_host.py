@@ -100,10 +100,10 @@ def test_prefill_weights_checks(pa):
                dict(wo=None), dict(stride=10), dict(ws=ODD)):
         assert prefill(pa, **kw) == bad, kw
     assert prefill(pa, ws=None) == lib.PA_ERR_WORKSPACE
-    n = pa.pa_prefill_weights_workspace_size(shape(), 8, 0)
+    n = pa.pa_prefill_weights_workspace_size(shape(), 8, 64, 0)
     assert n > 0 and prefill(pa, n=n - 1) == lib.PA_ERR_WORKSPACE
-    assert pa.pa_prefill_weights_workspace_size(shape(), 4096, 4) <= n
-    assert pa.pa_prefill_weights_workspace_size(shape(), -1, 0) == 0
+    assert pa.pa_prefill_weights_workspace_size(shape(), 4096, 64, 4) <= n
+    assert pa.pa_prefill_weights_workspace_size(shape(), -1, 64, 0) == 0
     assert prefill(pa, shape(num_seqs=0), qs=None, ws=None) == lib.PA_OK
 
 
