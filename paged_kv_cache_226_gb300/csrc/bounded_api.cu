@@ -281,6 +281,11 @@ int pa_prefill_weights(const void* q, const void* k_cache, const int32_t* block_
     if (!workspace || workspace_bytes < pa::prefill_weights_plan(p, workspace)) return PA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return PA_ERR_INVALID_ARG;
     if (p.max_context == 0) return PA_OK;
+    // units of either pass are counted in 32 bits
+    const int64_t tiles = ((int64_t)p.max_context + 127) / 128 * p.num_seqs * p.num_kv_heads;
+    if (tiles * p.query_chunks >= (1ll << 31) ||
+        (int64_t)p.max_query_tiles * p.key_chunks * p.num_seqs * p.num_kv_heads >= (1ll << 31))
+        return PA_ERR_UNSUPPORTED;
     if (num_tokens == 0) p.max_counted = 0;
     CUtensorMap tmk, tmq;
     if ((st = pa::encode_cache_map(&tmk, k_cache, shp, false)) != PA_OK) return st;

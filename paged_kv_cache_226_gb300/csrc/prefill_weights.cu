@@ -23,12 +23,11 @@
 // Both passes are one kernel with the operands exchanged.  A unit holds one
 // resident tile (operand A) and streams others (operand B); one persistent
 // CTA per SM walks its units, its rings running on from one unit to the next.
-// Warp 0 loads tiles with TMA (K through the block table in 16-token boxes,
-// Q in one box of tokens x heads), one thread of warp 1 issues the MMAs into
-// four 128-column buffers, and two groups of four warps take the finished
-// tiles in turn.  Rows of Q past a sequence's chunk and K rows past its end
-// may hold anything: they only reach their own lane or column, which is
-// masked.
+// Warps 1-3 load tiles with TMA (K through the block table in 16-token boxes,
+// Q in one box of tokens x heads), warp 0 issues the MMAs into four
+// 128-column buffers, and four groups of four warps take the finished tiles
+// in turn.  Rows of Q past a sequence's chunk and K rows past its end may
+// hold anything: they only reach their own lane or column, which is masked.
 //
 // Every mbarrier wait gives up after 1 s and flags PA_DEVERR_WAIT_TIMEOUT;
 // the epilogue warps then run their remaining steps without waiting, and
@@ -44,7 +43,9 @@ namespace pa {
 constexpr int kPwRows = 128;                   // lanes: rows of the resident tile
 constexpr int kPwCols = 128;                   // columns: rows of a streamed tile
 constexpr int kPwBufs = 4;                     // accumulators in tensor memory
-constexpr int kPwThreads = 384;                // producer, MMA, two idle warps, 2 x 4 epilogue
+constexpr int kPwProducers = 3;                // warps that load
+constexpr int kPwGroups = 4;                   // epilogue groups of four warps, one per buffer
+constexpr int kPwThreads = (1 + kPwProducers + 4 * kPwGroups) * 32;
 constexpr int kPwJoinThreads = 256;
 
 template <int D>
@@ -97,11 +98,14 @@ struct PwUnit {
     int b, g, a, chunk, first, last;
 };
 
-// Walks the units u = blockIdx.x, + gridDim.x, ... in order.
+// Walks the units u = blockIdx.x, + gridDim.x, ... in order (their number
+// fits 31 bits: checked on the host).  All lanes of a warp walk together;
+// the unit's fields are broadcast so that what depends on them is known to be
+// uniform.
 template <bool kStats>
 struct PwWalk {
     int b = -1;
-    int64_t u, base = 0, count = 0;
+    unsigned u, base = 0, count = 0;
     PwSeq s;
 
     __device__ __forceinline__ PwWalk() : u(blockIdx.x) {}
@@ -111,18 +115,17 @@ struct PwWalk {
             base += count;
             if (++b >= p.num_seqs) return false;
             pw_sequence(p, b, kStats && blockIdx.x == 0 && threadIdx.x == 0, s);
-            count = kStats ? (int64_t)s.n_qt * ((s.n_kt + p.key_chunk - 1) / p.key_chunk)
-                           : (int64_t)s.n_kt * max(1, (s.n_qt + p.query_chunk - 1) / p.query_chunk);
-            count *= p.num_kv_heads;
+            count = kStats ? s.n_qt * ((s.n_kt + p.key_chunk - 1) / p.key_chunk)
+                           : s.n_kt * max(1, (s.n_qt + p.query_chunk - 1) / p.query_chunk);
+            count = __shfl_sync(0xffffffffu, count * p.num_kv_heads, 0);
         }
-        int64_t r = u - base;
+        const unsigned r = u - base, rest = r / (unsigned)p.num_kv_heads;
         u += gridDim.x;
+        const unsigned tiles = kStats ? s.n_qt : s.n_kt;
         U.b = b;
-        U.g = (int)(r % p.num_kv_heads);
-        r /= p.num_kv_heads;
-        const int tiles = kStats ? s.n_qt : s.n_kt;
-        U.a = (int)(r % tiles);
-        U.chunk = (int)(r / tiles);
+        U.g = __shfl_sync(0xffffffffu, (int)(r - rest * (unsigned)p.num_kv_heads), 0);
+        U.chunk = __shfl_sync(0xffffffffu, (int)(rest / tiles), 0);
+        U.a = __shfl_sync(0xffffffffu, (int)(rest % tiles), 0);
         if (kStats) {
             U.first = U.chunk * p.key_chunk;
             U.last = min(U.first + p.key_chunk, pw_key_tiles(p, s, U.a));
@@ -130,9 +133,55 @@ struct PwWalk {
             U.first = max(U.chunk * p.query_chunk, pw_first_query_tile(p, s, U.a));
             U.last = min((U.chunk + 1) * p.query_chunk, s.n_qt);
         }
+        U.first = __shfl_sync(0xffffffffu, U.first, 0);
+        U.last = __shfl_sync(0xffffffffu, U.last, 0);
         return true;
     }
 };
+
+__device__ __forceinline__ float sum8(const uint64_t (&ps)[4]) {
+    float t[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f32x2_unpack(ps[e], t[2 * e], t[2 * e + 1]);
+    return ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+}
+
+// (m, z) and another chunk's: the maximum, and the sum taken against it.
+__device__ __forceinline__ void join_stats(float& m, float& z, float2 o) {
+    const float n = fmaxf(m, o.x), ref = n == -INFINITY ? 0.f : n;
+    z = z * ex2(m - ref) + o.y * ex2(o.x - ref);
+    m = n;
+}
+
+// Pass 2: adds 2^(x - lse) over the tile's columns (of [lo, hi) with kMask);
+// `neg_lse` in shared memory, `release` called once the tile is read.
+template <bool kMask, typename Release>
+__device__ __forceinline__ void column_sums(uint64_t (&ps)[4], uint32_t tile_addr, const float* neg_lse,
+                                            uint64_t sl2, int lo, int hi, Release&& release) {
+#pragma unroll
+    for (int c = 0; c < kPwCols; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(tile_addr + c, v);
+        tmem_wait_ld();
+        if (c == kPwCols - 32) release();
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(neg_lse + c + e);
+            float a[4];
+            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2,
+                                   f32x2_pack(l.x, l.y)), a[0], a[1]);
+            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sl2,
+                                   f32x2_pack(l.z, l.w)), a[2], a[3]);
+            if (kMask) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    a[i] = c + e + i >= lo && c + e + i < hi ? a[i] : -INFINITY;
+            }
+            ps[(e >> 1) & 3] = f32x2_add(ps[(e >> 1) & 3], f32x2_pack(ex2(a[0]), ex2(a[1])));
+            ps[((e >> 1) + 1) & 3] = f32x2_add(ps[((e >> 1) + 1) & 3], f32x2_pack(ex2(a[2]), ex2(a[3])));
+        }
+    }
+}
 
 template <typename T, int D, bool kStats>
 __global__ void __launch_bounds__(kPwThreads, 1)
@@ -146,22 +195,24 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     __shared__ __align__(8) uint64_t a_full[kA], a_empty[kA], b_full[kB], b_empty[kB];
     __shared__ __align__(8) uint64_t s_full[kPwBufs], s_empty[kPwBufs];
     __shared__ uint32_t tmem_base;
-    __shared__ __align__(16) float lse_s[2][2][kPwCols];     // pass 2: [group][step parity]
-    __shared__ float2 other[2][kPwRows];                     // the second group's result
+    __shared__ __align__(16) float lse_s[kPwGroups][2][kPwCols];     // pass 2: [group][tile parity]
+    __shared__ float2 other[2][kPwGroups - 1][kPwRows];              // the other groups' results
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int G = p.group;
     const int q_rows = p.tile_tokens * G;                    // rows of a query tile, <= 128
+    // K tiles are loaded by every producer warp, Q tiles by the first
+    constexpr int kALoaders = kStats ? 1 : kPwProducers, kBLoaders = kStats ? kPwProducers : 1;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kA; ++i) mbar_init(&a_full[i], 1), mbar_init(&a_empty[i], 1);
-        for (int i = 0; i < kB; ++i) mbar_init(&b_full[i], 1), mbar_init(&b_empty[i], 1);
+        for (int i = 0; i < kA; ++i) mbar_init(&a_full[i], kALoaders), mbar_init(&a_empty[i], 1);
+        for (int i = 0; i < kB; ++i) mbar_init(&b_full[i], kBLoaders), mbar_init(&b_empty[i], 1);
         for (int i = 0; i < kPwBufs; ++i) mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4);
         fence_barrier_init();
     }
-    if (warp == 1) tmem_alloc(&tmem_base, kPwBufs * kPwCols);
+    if (warp == 0) tmem_alloc(&tmem_base, kPwBufs * kPwCols);
     if (!kStats && q_rows < kPwCols) {
         // rows that no query box fills stay zero (their lse is +inf)
         for (int i = threadIdx.x; i < kB * Lay::kTile / 16; i += kPwThreads)
@@ -171,24 +222,19 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem = tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
     grid_dependency_wait();
     allow_dependent_launch();
 
-    if (warp == 0) {
+    if (warp >= 1 && warp <= kPwProducers) {
         // ------------------------------------------------------------------
-        // producer
+        // producers: all lanes run along, one issues
         // ------------------------------------------------------------------
-        if (lane == 0) prefetch_tensor_map(&tmap_k), prefetch_tensor_map(&tmap_q);
-        // waits for stage n % stages to be free and registers the bytes
-        auto open = [&](uint64_t* full, uint64_t* empty, int stages, int n, uint32_t bytes) -> bool {
-            bool ok = true;
-            if (lane == 0) {
-                if (n >= stages) ok = mbar_wait(&empty[n % stages], ((n / stages) - 1) & 1);
-                if (ok) mbar_arrive_expect_tx(&full[n % stages], bytes);
-                else flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
-            }
-            return __shfl_sync(0xffffffffu, ok, 0);
+        const int who = warp - 1;
+        if (lane == 0) prefetch_tensor_map(who == 0 ? &tmap_q : &tmap_k);
+        // waits for stage n % stages to be free
+        auto open = [&](uint64_t* empty, int stages, int n) -> bool {
+            return n < stages || __all_sync(0xffffffffu, mbar_wait(&empty[n % stages], ((n / stages) - 1) & 1));
         };
         auto blocks_of = [&](const PwSeq& s, int b, int kt) {     // lane i: block of box i
             const int tok = kt * kPwCols + 16 * lane;
@@ -197,27 +243,45 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             if (blk < 0 || blk >= p.num_blocks) flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
             return blk;
         };
+        // this warp's boxes of a K tile: every kPwProducers-th
         auto load_k = [&](uint8_t* dst, uint64_t* full, uint64_t* empty, int stages, int n,
                           const PwSeq& s, const PwUnit& U, int kt, int blk) -> bool {
-            const int nbox = min(8, (s.L - kt * kPwCols + 15) / 16);
-            if (!open(full, empty, stages, n, (uint32_t)(nbox * Lay::kHalves * kBox16Bytes))) return false;
+            if (!open(empty, stages, n)) return false;
+            const int nbox = __shfl_sync(0xffffffffu, min(8, (s.L - kt * kPwCols + 15) / 16), 0);
+            const int own = nbox > who ? (nbox - who + kPwProducers - 1) / kPwProducers : 0;
+            uint64_t* bar = &full[n % stages];
+            if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(own * Lay::kHalves * kBox16Bytes));
+            __syncwarp();
             dst += (n % stages) * Lay::kTile;
-            if (lane < nbox) {
-                const int sub = (kt * kPwCols + 16 * lane) % p.block_size;
 #pragma unroll
-                for (int h = 0; h < Lay::kHalves; ++h)
-                    tma_load_4d(dst + h * Lay::kHalf + lane * kBox16Bytes, &tmap_k, &full[n % stages],
-                                h * kBoxElems, U.g, sub, blk);
+            for (int i = 0; i < (8 + kPwProducers - 1) / kPwProducers; ++i) {
+                const int box = who + i * kPwProducers;
+                if (box >= nbox) break;
+                const int pblk = __shfl_sync(0xffffffffu, blk, box);
+                const int sub = (kt * kPwCols + 16 * box) % p.block_size;
+                if (elect_one()) {
+#pragma unroll
+                    for (int h = 0; h < Lay::kHalves; ++h)
+                        tma_load_4d(dst + h * Lay::kHalf + box * kBox16Bytes, &tmap_k, bar,
+                                    h * kBoxElems, U.g, sub, pblk);
+                }
+                __syncwarp();
             }
             return true;
         };
         auto load_q = [&](uint8_t* dst, uint64_t* full, uint64_t* empty, int stages, int n,
                           const PwSeq& s, const PwUnit& U, int qt) -> bool {
-            if (!open(full, empty, stages, n, (uint32_t)(q_rows * Lay::kHalves * 128))) return false;
+            if (!open(empty, stages, n)) return false;
+            uint64_t* bar = &full[n % stages];
+            const int row = __shfl_sync(0xffffffffu, (int)(s.q0 + (int64_t)qt * p.tile_tokens), 0);
             dst += (n % stages) * Lay::kTile;
-            if (lane < Lay::kHalves)
-                tma_load_3d(dst + lane * Lay::kHalf, &tmap_q, &full[n % stages], lane * kBoxElems,
-                            U.g * G, (int)(s.q0 + (int64_t)qt * p.tile_tokens));
+            if (elect_one()) {
+                mbar_arrive_expect_tx(bar, (uint32_t)(q_rows * Lay::kHalves * 128));
+#pragma unroll
+                for (int h = 0; h < Lay::kHalves; ++h)
+                    tma_load_3d(dst + h * Lay::kHalf, &tmap_q, bar, h * kBoxElems, U.g * G, row);
+            }
+            __syncwarp();
             return true;
         };
         uint8_t* a_ring = smem;
@@ -230,7 +294,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             if (U.first >= U.last) continue;
             if constexpr (kStats) {
                 int blk = blocks_of(walk.s, U.b, U.first);
-                ok = load_q(a_ring, a_full, a_empty, kA, na++, walk.s, U, U.a);
+                if (who == 0) ok = load_q(a_ring, a_full, a_empty, kA, na++, walk.s, U, U.a);
                 for (int kt = U.first; ok && kt < U.last; ++kt) {
                     const int now = blk;                     // the next tile's blocks a step ahead
                     if (kt + 1 < U.last) blk = blocks_of(walk.s, U.b, kt + 1);
@@ -239,73 +303,81 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             } else {
                 ok = load_k(a_ring, a_full, a_empty, kA, na++, walk.s, U, U.a,
                             blocks_of(walk.s, U.b, U.a));
-                for (int qt = U.first; ok && qt < U.last; ++qt) {
+                for (int qt = U.first; ok && who == 0 && qt < U.last; ++qt) {
                     if (U.b == at_b && U.g == at_g && qt == at_qt) continue;     // still there
                     at_b = U.b, at_g = U.g, at_qt = qt;
                     ok = load_q(b_ring, b_full, b_empty, kB, nb++, walk.s, U, qt);
                 }
             }
         }
-    } else if (warp == 1) {
+        if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
+    } else if (warp == 0) {
         // ------------------------------------------------------------------
-        // MMA issuer
+        // MMA issuer: all lanes run along, one issues
         // ------------------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t kId = idesc_f16(kPwRows, kPwCols, kBf16, false);
-            const uint32_t a_ring = smem_u32(smem), b_ring = a_ring + kA * Lay::kTile;
-            PwWalk<kStats> walk;
-            PwUnit U;
-            int na = 0, nb = -1, step = 0, at_b = -1, at_g = -1, at_qt = -1;
-            bool ok = true;
-            while (ok && walk.next(p, U)) {
-                if (U.first >= U.last) continue;
-                ok = mbar_wait(&a_full[na % kA], (na / kA) & 1);
-                for (int i = U.first; ok && i < U.last; ++i, ++step) {
-                    if (kStats || U.b != at_b || U.g != at_g || i != at_qt) {
-                        // the previous streamed tile is free once the products so far are done
-                        if (nb >= 0) mma_commit(&b_empty[nb % kB]);
-                        ++nb;
-                        at_b = U.b, at_g = U.g, at_qt = i;
-                        ok = mbar_wait(&b_full[nb % kB], (nb / kB) & 1);
-                    }
-                    if (ok && step >= kPwBufs)
-                        ok = mbar_wait(&s_empty[step % kPwBufs], ((step / kPwBufs) - 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint32_t a = a_ring + (na % kA) * Lay::kTile, b = b_ring + (nb % kB) * Lay::kTile;
-                    const uint32_t d = tmem + kPwCols * (step % kPwBufs);
+        constexpr uint32_t kId = idesc_f16(kPwRows, kPwCols, kBf16, false);
+        const uint64_t a_ring = smem_desc_sw128(smem_u32(smem), 16, 1024);
+        const uint64_t b_ring = smem_desc_sw128(smem_u32(smem) + kA * Lay::kTile, 16, 1024);
+        PwWalk<kStats> walk;
+        PwUnit U;
+        int na = 0, nb = -1, step = 0, at_b = -1, at_g = -1, at_qt = -1;
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, int phase) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1));
+        };
+        while (ok && walk.next(p, U)) {
+            if (U.first >= U.last) continue;
+            wait(&a_full[na % kA], na / kA);
+            for (int i = U.first; ok && i < U.last; ++i, ++step) {
+                if (kStats || U.b != at_b || U.g != at_g || i != at_qt) {
+                    // the previous streamed tile is free once the products so far are done
+                    if (nb >= 0 && elect_one()) mma_commit(&b_empty[nb % kB]);
+                    __syncwarp();
+                    ++nb;
+                    at_b = U.b, at_g = U.g, at_qt = i;
+                    wait(&b_full[nb % kB], nb / kB);
+                }
+                if (step >= kPwBufs) wait(&s_empty[step % kPwBufs], step / kPwBufs - 1);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint64_t a = a_ring + (na % kA) * (Lay::kTile >> 4);
+                const uint64_t b = b_ring + (nb % kB) * (Lay::kTile >> 4);
+                const uint32_t d = tmem + kPwCols * (step % kPwBufs);
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * Lay::kHalf + (kk & 3) * 32;
-                        mma_f16_ss(d, smem_desc_sw128(a + off, 16, 1024),
-                                   smem_desc_sw128(b + off, 16, 1024), kId, kk > 0);
+                        constexpr int kHalf16 = Lay::kHalf >> 4;
+                        const uint64_t off = (kk >> 2) * kHalf16 + (kk & 3) * 2;
+                        mma_f16_ss(d, a + off, b + off, kId, kk > 0);
                     }
                     mma_commit(&s_full[step % kPwBufs]);
                 }
-                if (ok) mma_commit(&a_empty[na % kA]);
-                ++na;
+                __syncwarp();
             }
-            if (!ok) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
+            if (ok && elect_one()) mma_commit(&a_empty[na % kA]);
+            __syncwarp();
+            ++na;
         }
-    } else if (warp >= 4) {
+        if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
+    } else {
         // ------------------------------------------------------------------
-        // epilogue: group w takes the steps of parity w; this thread owns
-        // lane r of every tile
+        // epilogue: group w takes the steps w, w + 4, ... (buffer w); this
+        // thread owns lane r of every tile
         // ------------------------------------------------------------------
         const int group = (warp >> 2) - 1;
         const int r = (warp & 3) * 32 + lane;
-        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tile_addr = tmem + kPwCols * group + ((uint32_t)((warp & 3) * 32) << 16);
         const float sl = p.scale_log2;
+        const uint64_t sl2 = f32x2_pack(sl, sl);
         bool failed = false;
-        auto wait = [&](int step) {
-            if (!failed && !__all_sync(0xffffffffu, mbar_wait(&s_full[step % kPwBufs], (step / kPwBufs) & 1)))
-                failed = true;
+        auto wait = [&](int n) {                // the group's n-th tile
+            if (!failed && !__all_sync(0xffffffffu, mbar_wait(&s_full[group], n & 1))) failed = true;
             tc_fence_after_sync();
         };
-        auto release = [&](int step) {          // the tile is in registers
+        auto release = [&] {                    // the tile is in registers
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[step % kPwBufs]);
+            if (lane == 0) mbar_arrive(&s_empty[group]);
         };
         PwWalk<kStats> walk;
         PwUnit U;
@@ -315,115 +387,83 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             const int steps = max(0, U.last - U.first);
             if (kStats && steps == 0) continue;
             const size_t pair = (size_t)U.b * p.num_kv_heads + U.g;
+            const int key = U.a * kPwCols + r;
+            // a unit of one step is its group's alone, others are joined by group 0
+            const bool writer = steps == 1 ? (step & (kPwGroups - 1)) == group : group == 0;
+            float before = 0.f;
+            if (!kStats && writer && p.query_chunks == 1 && p.weights && key < s.L - s.C)
+                before = p.weights[pair * p.weights_stride + key];
             float m = -INFINITY, z = 0.f;
+            // first step of this unit that is the group's
+            const int skip = (group - step) & (kPwGroups - 1);
+            step += steps;
             if constexpr (kStats) {
                 const int pos = min(s.L - s.counted + U.a * p.tile_tokens + r / G, s.L - 1);
-                for (int kt = U.first; kt < U.last; ++kt, ++step) {
-                    if ((step & 1) != group) continue;
-                    wait(step);
-                    float x[kPwCols];
-                    {
-                        uint32_t v[kPwCols];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            tmem_ld32(tmem + kPwCols * (step % kPwBufs) + lane_addr + 32 * c,
-                                      *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < kPwCols; ++e) x[e] = __uint_as_float(v[e]);
-                    }
-                    release(step);
+                for (int kt = U.first + skip; kt < U.last; kt += kPwGroups) {
+                    wait(mine++);
                     const int visible = pos - kt * kPwCols;           // keys 0 .. visible of the tile
-                    float pm[8];
+                    const bool whole = __all_sync(0xffffffffu, visible >= kPwCols - 1);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) pm[e] = -INFINITY;
-                    if (visible < kPwCols - 1) {
+                    for (int c = 0; c < kPwCols; c += 64) {
+                        uint32_t v[64];
+                        tmem_ld32(tile_addr + c, *reinterpret_cast<uint32_t(*)[32]>(v));
+                        tmem_ld32(tile_addr + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+                        tmem_wait_ld();
+                        if (c == 64) release();
+                        if (!whole) {
 #pragma unroll
-                        for (int e = 0; e < kPwCols; ++e) x[e] = e <= visible ? x[e] : -INFINITY;
+                            for (int e = 0; e < 64; ++e)
+                                if (c + e > visible) v[e] = 0xff800000u;
+                        }
+                        float pm[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) pm[e] = __uint_as_float(v[e]);
+#pragma unroll
+                        for (int e = 4; e < 64; ++e) pm[e & 3] = fmaxf(pm[e & 3], __uint_as_float(v[e]));
+                        const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * sl;
+                        if (mx > m + kRescaleThresholdLog2) {         // also the first finite maximum
+                            z *= ex2(m - mx);
+                            m = mx;
+                        }
+                        const float ref = m == -INFINITY ? 0.f : m;   // nothing visible yet
+                        const uint64_t neg2 = f32x2_pack(-ref, -ref);
+                        uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float a0, a1;
+                            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
+                                                   sl2, neg2), a0, a1);
+                            ps[e & 3] = f32x2_add(ps[e & 3], f32x2_pack(ex2(a0), ex2(a1)));
+                        }
+                        z += sum8(ps);
                     }
-#pragma unroll
-                    for (int e = 0; e < kPwCols; ++e) pm[e & 7] = fmaxf(pm[e & 7], x[e]);
-                    const float mx = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
-                                           fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7]))) * sl;
-                    if (mx > m + kRescaleThresholdLog2) {             // also the first finite maximum
-                        z *= ex2(m - mx);
-                        m = mx;
-                    }
-                    const float ref = m == -INFINITY ? 0.f : m;       // nothing visible yet
-                    const uint64_t sl2 = f32x2_pack(sl, sl), neg2 = f32x2_pack(-ref, -ref);
-                    uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-                    for (int e = 0; e < kPwCols / 2; ++e) {
-                        float a0, a1;
-                        f32x2_unpack(f32x2_fma(f32x2_pack(x[2 * e], x[2 * e + 1]), sl2, neg2), a0, a1);
-                        ps[e & 3] = f32x2_add(ps[e & 3], f32x2_pack(ex2(a0), ex2(a1)));
-                    }
-                    float t[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) f32x2_unpack(ps[e], t[2 * e], t[2 * e + 1]);
-                    z += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
                 }
             } else {
-                const int key = U.a * kPwCols + r;
-                for (int qt = U.first; qt < U.last; ++qt, ++step) {
-                    if ((step & 1) != group) continue;
-                    const float* src = p.lse + (pair * p.max_query_tiles + qt) * kPwCols;
-                    const float mine_lse = src[r];
+                for (int qt = U.first + skip; qt < U.last; qt += kPwGroups) {
+                    const float lse = p.lse[(pair * p.max_query_tiles + qt) * kPwCols + r];
                     float* ls = lse_s[group][mine & 1];
-                    ++mine;
-                    wait(step);
-                    ls[r] = -mine_lse;
+                    wait(mine++);
+                    ls[r] = -lse;
                     asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
                     const int tokens = min(p.tile_tokens, s.counted - qt * p.tile_tokens);
                     // columns that see this key: from `lo` on, up to the chunk's end
                     const int lo = (key - (s.L - s.counted + qt * p.tile_tokens)) * G, hi = tokens * G;
-                    const bool whole = __all_sync(0xffffffffu, lo <= 0) && tokens == p.tile_tokens;
-                    const uint64_t sl2 = f32x2_pack(sl, sl);
+                    const bool whole = tokens == p.tile_tokens && __all_sync(0xffffffffu, lo <= 0);
                     uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32(tmem + kPwCols * (step % kPwBufs) + lane_addr + 32 * c, v);
-                        tmem_wait_ld();
-                        if (c == 3) release(step);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 l = *reinterpret_cast<const float4*>(ls + 32 * c + e);
-                            float a[4];
-                            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
-                                                   sl2, f32x2_pack(l.x, l.y)), a[0], a[1]);
-                            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
-                                                   sl2, f32x2_pack(l.z, l.w)), a[2], a[3]);
-                            if (!whole) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    a[i] = 32 * c + e + i >= lo && 32 * c + e + i < hi ? a[i] : -INFINITY;
-                            }
-                            ps[(e >> 1) & 3] = f32x2_add(ps[(e >> 1) & 3], f32x2_pack(ex2(a[0]), ex2(a[1])));
-                            ps[((e >> 1) + 1) & 3] = f32x2_add(ps[((e >> 1) + 1) & 3], f32x2_pack(ex2(a[2]), ex2(a[3])));
-                        }
-                    }
-                    float t[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) f32x2_unpack(ps[e], t[2 * e], t[2 * e + 1]);
-                    z += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+                    if (whole) column_sums<false>(ps, tile_addr, ls, sl2, lo, hi, release);
+                    else column_sums<true>(ps, tile_addr, ls, sl2, lo, hi, release);
+                    z += sum8(ps);
                 }
             }
-            // join the groups: a unit of one step is its group's alone
-            bool writer = group == 0;
-            if (steps == 1) {
-                writer = ((step - 1) & 1) == group;
-            } else if (steps > 1) {
-                if (group == 1) other[units & 1][r] = make_float2(m, z);
-                asm volatile("bar.sync 3, 256;" ::: "memory");
+            if (steps > 1) {
+                if (group > 0) other[units & 1][group - 1][r] = make_float2(m, z);
+                asm volatile("bar.sync 5, %0;" ::"n"(kPwGroups * 128) : "memory");
                 if (group == 0) {
-                    const float2 o = other[units & 1][r];
-                    if (kStats) {
-                        const float n = fmaxf(m, o.x), ref = n == -INFINITY ? 0.f : n;
-                        z = z * ex2(m - ref) + o.y * ex2(o.x - ref);
-                        m = n;
-                    } else {
-                        z += o.y;
+#pragma unroll
+                    for (int i = 0; i < kPwGroups - 1; ++i) {
+                        const float2 o = other[units & 1][i][r];
+                        if (kStats) join_stats(m, z, o);
+                        else z += o.y;
                     }
                 }
                 ++units;
@@ -435,15 +475,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                 if (p.key_chunks == 1) p.lse[at] = r < tokens * G ? m + log2f(z) : INFINITY;
                 else p.stats[(size_t)U.chunk * p.num_seqs * p.num_kv_heads * p.max_query_tiles * kPwRows + at] =
                     make_float2(m, z);
-            } else {
-                const int key = U.a * kPwCols + r;
-                if (key >= s.L) continue;
-                if (p.query_chunks == 1) {
-                    const size_t at = pair * p.weights_stride + key;
-                    p.weights_out[at] = z + (p.weights && key < s.L - s.C ? p.weights[at] : 0.f);
-                } else {
+            } else if (key < s.L) {
+                if (p.query_chunks == 1)
+                    p.weights_out[pair * p.weights_stride + key] = before + z;
+                else
                     p.columns[((size_t)U.chunk * p.num_seqs * p.num_kv_heads + pair) * p.columns_stride + key] = z;
-                }
             }
         }
         if (failed && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
@@ -451,7 +487,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
 
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == 0) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, kPwBufs * kPwCols);
     }
@@ -471,10 +507,7 @@ __global__ void __launch_bounds__(kPwRows)
     const int chunks = (pw_key_tiles(p, s, qt) + p.key_chunk - 1) / p.key_chunk;
     float m = -INFINITY, z = 0.f;
     for (int c = 0; c < chunks; ++c) {
-        const float2 v = p.stats[c * rows + at];
-        const float n = fmaxf(m, v.x), ref = n == -INFINITY ? 0.f : n;
-        z = z * ex2(m - ref) + v.y * ex2(v.x - ref);
-        m = n;
+        join_stats(m, z, p.stats[c * rows + at]);
     }
     const int tokens = min(p.tile_tokens, s.counted - qt * p.tile_tokens);
     p.lse[at] = r < tokens * p.group ? m + log2f(z) : INFINITY;
