@@ -20,14 +20,18 @@
 // joins the chunks in a fixed order.  No atomics: results do not depend on
 // the schedule.
 //
-// Both passes are one kernel with the operands exchanged.  A unit holds one
-// resident tile (operand A) and streams others (operand B); one persistent
-// CTA per SM walks its units, its rings running on from one unit to the next.
-// Warps 1-3 load tiles with TMA (K through the block table in 16-token boxes,
-// Q in one box of tokens x heads), warp 0 issues the MMAs into four
-// 128-column buffers, and four groups of four warps take the finished tiles
-// in turn.  Rows of Q past a sequence's chunk and K rows past its end may
-// hold anything: they only reach their own lane or column, which is masked.
+// Both passes are one kernel with the operands exchanged.  A unit holds two
+// resident tiles (operand A) and streams others (operand B) past both, so
+// that a streamed tile is loaded once for two products; one persistent CTA
+// per SM walks its units, its rings running on from one unit to the next.
+// Six warps load whole tiles, one for each stage, with TMA (K through the block table in
+// 16-token boxes, Q in one box of tokens x heads per 64 dims); two warps
+// issue the MMAs, one for each resident tile, into two 128-column buffers
+// each (a single issuer spends 1,060 cycles on its waits and commits per
+// tile, twice what the product takes); and four groups of four warps take the
+// finished tiles.  Rows of Q past a sequence's chunk and K rows past its end
+// may hold anything: they only reach their own lane or column, which is
+// masked.
 //
 // Every mbarrier wait gives up after 1 s and flags PA_DEVERR_WAIT_TIMEOUT;
 // the epilogue warps then run their remaining steps without waiting, and
@@ -40,12 +44,13 @@
 
 namespace pa {
 
-constexpr int kPwRows = 128;                   // lanes: rows of the resident tile
+constexpr int kPwRows = 128;                   // lanes: rows of a resident tile
 constexpr int kPwCols = 128;                   // columns: rows of a streamed tile
 constexpr int kPwBufs = 4;                     // accumulators in tensor memory
-constexpr int kPwProducers = 3;                // warps that load
 constexpr int kPwGroups = 4;                   // epilogue groups of four warps, one per buffer
-constexpr int kPwThreads = (1 + kPwProducers + 4 * kPwGroups) * 32;
+constexpr int kPwLoadersAfter = 4 + 4 * kPwGroups;   // warps 0, 1 issue MMAs; 2, 3, 20 .. 23 load
+constexpr int kPwLoaders = 6;                  // one for each stage of the two rings
+constexpr int kPwThreads = (kPwLoadersAfter + kPwLoaders - 2) * 32;
 constexpr int kPwJoinThreads = 256;
 
 template <int D>
@@ -53,13 +58,14 @@ struct PwLayout {
     static constexpr int kHalf = kPwRows * 128;               // 64 dims of 128 rows
     static constexpr int kHalves = D / kBoxElems;
     static constexpr int kTile = kHalves * kHalf;
-    static constexpr int kStages = 6;                         // of both rings
-    static constexpr int kDynamicSmem = kStages * kTile + 1024;
+    static constexpr int kA = 3;                              // resident tiles: a unit's and the next's
+    static constexpr int kB = 3;                              // streamed tiles
+    static constexpr int kDynamicSmem = (kA + kB) * kTile + 1024;
 };
 
 struct PwSeq {
     int L, C, counted;             // context, chunk, counted queries
-    int64_t q0;                    // row of the first counted query in q
+    int q0;                        // row of the first counted query in q
     int n_qt, n_kt;                // query and key tiles
 };
 
@@ -75,7 +81,7 @@ __device__ __forceinline__ void pw_sequence(const PrefillWeightsParams& p, int b
     s.L = L, s.C = (int)C;
     s.counted = p.window > 0 ? min(p.window, s.C) : s.C;
     if (s.counted > p.max_counted) bad = true, s.counted = p.max_counted;
-    s.q0 = start + s.C - s.counted;
+    s.q0 = (int)start + s.C - s.counted;
     s.n_qt = (s.counted + p.tile_tokens - 1) / p.tile_tokens;
     s.n_kt = (L + kPwCols - 1) / kPwCols;
     if (bad && report) flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
@@ -93,49 +99,88 @@ __device__ __forceinline__ int pw_first_query_tile(const PrefillWeightsParams& p
     return max(0, kt * kPwCols - (s.L - s.counted)) / p.tile_tokens;
 }
 
-// One unit: resident tile `a` of (b, g), streamed tiles [first, last).
+// One unit of (b, g): pairs of resident tiles [a0, a1) (pair a is the tiles
+// 2a and 2a + 1), each with the streamed tiles of its chunk.
 struct PwUnit {
-    int b, g, a, chunk, first, last;
+    int b, g, a0, a1, chunk;
 };
 
 // Walks the units u = blockIdx.x, + gridDim.x, ... in order (their number
-// fits 31 bits: checked on the host).  All lanes of a warp walk together;
-// the unit's fields are broadcast so that what depends on them is known to be
-// uniform.
+// fits 31 bits: checked on the host), all lanes of a warp together.  Lane i
+// holds the lengths and the unit count of sequence base_b + i, so that 32
+// sequences cost one round of loads.  Pass 2 takes the sequences from the
+// last on: their keys are those that pass 1 left in L2.
 template <bool kStats>
 struct PwWalk {
-    int b = -1;
-    unsigned u, base = 0, count = 0;
-    PwSeq s;
+    unsigned u, base = 0;
+    int base_b = -32;
+    unsigned ends = 0;             // lane: units up to and with its sequence, from base on
+    unsigned total = 0;
+    PwSeq mine, s;
 
     __device__ __forceinline__ PwWalk() : u(blockIdx.x) {}
 
     __device__ __forceinline__ bool next(const PrefillWeightsParams& p, PwUnit& U) {
-        while (u >= base + count) {
-            base += count;
-            if (++b >= p.num_seqs) return false;
-            pw_sequence(p, b, kStats && blockIdx.x == 0 && threadIdx.x == 0, s);
-            count = kStats ? s.n_qt * ((s.n_kt + p.key_chunk - 1) / p.key_chunk)
-                           : s.n_kt * max(1, (s.n_qt + p.query_chunk - 1) / p.query_chunk);
-            count = __shfl_sync(0xffffffffu, count * p.num_kv_heads, 0);
+        const int lane = threadIdx.x & 31;
+        while (u >= base + total) {
+            base += total;
+            base_b += 32;
+            if (base_b >= p.num_seqs) return false;
+            const int i = base_b + lane;
+            unsigned count = 0;
+            if (i < p.num_seqs) {
+                pw_sequence(p, kStats ? i : p.num_seqs - 1 - i, (kStats || p.max_counted == 0) && blockIdx.x == 0 && threadIdx.x < 32, mine);
+                const int kt2 = (mine.n_kt + 1) / 2, qt2 = (mine.n_qt + 1) / 2;
+                count = kStats ? qt2 * ((mine.n_kt + p.key_chunk - 1) / p.key_chunk)
+                               : ((kt2 + p.key_run - 1) / p.key_run) *
+                                     max(1, (mine.n_qt + p.query_chunk - 1) / p.query_chunk);
+                count *= p.num_kv_heads;
+            }
+            ends = count;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const unsigned v = __shfl_up_sync(0xffffffffu, ends, d);
+                if (lane >= d) ends += v;
+            }
+            total = __shfl_sync(0xffffffffu, ends, 31);
         }
-        const unsigned r = u - base, rest = r / (unsigned)p.num_kv_heads;
+        const int at = __ffs(__ballot_sync(0xffffffffu, u - base < ends)) - 1;
+        const unsigned before = __shfl_sync(0xffffffffu, ends, max(at - 1, 0));
+        const unsigned r = u - base - (at > 0 ? before : 0u), rest = r / (unsigned)p.num_kv_heads;
         u += gridDim.x;
-        const unsigned tiles = kStats ? s.n_qt : s.n_kt;
-        U.b = b;
-        U.g = __shfl_sync(0xffffffffu, (int)(r - rest * (unsigned)p.num_kv_heads), 0);
-        U.chunk = __shfl_sync(0xffffffffu, (int)(rest / tiles), 0);
-        U.a = __shfl_sync(0xffffffffu, (int)(rest % tiles), 0);
-        if (kStats) {
-            U.first = U.chunk * p.key_chunk;
-            U.last = min(U.first + p.key_chunk, pw_key_tiles(p, s, U.a));
-        } else {
-            U.first = max(U.chunk * p.query_chunk, pw_first_query_tile(p, s, U.a));
-            U.last = min((U.chunk + 1) * p.query_chunk, s.n_qt);
+        U.b = kStats ? base_b + at : p.num_seqs - 1 - (base_b + at);
+        s.L = __shfl_sync(0xffffffffu, mine.L, at);
+        s.C = __shfl_sync(0xffffffffu, mine.C, at);
+        s.counted = __shfl_sync(0xffffffffu, mine.counted, at);
+        s.q0 = __shfl_sync(0xffffffffu, mine.q0, at);
+        s.n_qt = __shfl_sync(0xffffffffu, mine.n_qt, at);
+        s.n_kt = __shfl_sync(0xffffffffu, mine.n_kt, at);
+        U.g = r - rest * (unsigned)p.num_kv_heads;
+        const int runs = kStats ? (s.n_qt + 1) / 2 : ((s.n_kt + 1) / 2 + p.key_run - 1) / p.key_run;
+        U.chunk = rest / (unsigned)runs;
+        U.a0 = rest - U.chunk * runs;
+        U.a1 = U.a0 + 1;
+        if (!kStats) {
+            U.a0 *= p.key_run;
+            U.a1 = min(U.a0 + p.key_run, (s.n_kt + 1) / 2);
         }
-        U.first = __shfl_sync(0xffffffffu, U.first, 0);
-        U.last = __shfl_sync(0xffffffffu, U.last, 0);
         return true;
+    }
+
+    // streamed tiles [first, last) of the unit's pair a
+    __device__ __forceinline__ void streamed(const PrefillWeightsParams& p, const PwUnit& U, int a,
+                                             int& first, int& last) const {
+        if (kStats) {
+            first = U.chunk * p.key_chunk;
+            last = min(first + p.key_chunk, pw_key_tiles(p, s, min(2 * a + 1, s.n_qt - 1)));
+        } else {
+            first = max(U.chunk * p.query_chunk, pw_first_query_tile(p, s, 2 * a));
+            last = min((U.chunk + 1) * p.query_chunk, s.n_qt);
+        }
+    }
+
+    __device__ __forceinline__ int residents(int a) const {
+        return min(2, (kStats ? s.n_qt : s.n_kt) - 2 * a);
     }
 };
 
@@ -153,11 +198,52 @@ __device__ __forceinline__ void join_stats(float& m, float& z, float2 o) {
     m = n;
 }
 
-// Pass 2: adds 2^(x - lse) over the tile's columns (of [lo, hi) with kMask);
-// `neg_lse` in shared memory, `release` called once the tile is read.
+// Pass 1: folds a tile's row (keys up to `visible` with kMask) into (m, z).
 template <bool kMask, typename Release>
-__device__ __forceinline__ void column_sums(uint64_t (&ps)[4], uint32_t tile_addr, const float* neg_lse,
-                                            uint64_t sl2, int lo, int hi, Release&& release) {
+__device__ __forceinline__ void row_stats(float& m, float& z, uint32_t tile_addr, float sl,
+                                          uint64_t sl2, int visible, Release&& release) {
+#pragma unroll
+    for (int c = 0; c < kPwCols; c += 64) {
+        uint32_t v[64];
+        tmem_ld32(tile_addr + c, *reinterpret_cast<uint32_t(*)[32]>(v));
+        tmem_ld32(tile_addr + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+        tmem_wait_ld();
+        if (c == 64) release();
+        if (kMask) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+                if (c + e > visible) v[e] = 0xff800000u;
+        }
+        float pm[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pm[e] = __uint_as_float(v[e]);
+#pragma unroll
+        for (int e = 4; e < 64; ++e) pm[e & 3] = fmaxf(pm[e & 3], __uint_as_float(v[e]));
+        const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * sl;
+        if (mx > m + kRescaleThresholdLog2) {         // also the first finite maximum
+            z *= ex2(m - mx);
+            m = mx;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;   // nothing visible yet
+        const uint64_t neg2 = f32x2_pack(-ref, -ref);
+        uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            float a0, a1;
+            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sl2,
+                                   neg2), a0, a1);
+            ps[e & 3] = f32x2_add(ps[e & 3], f32x2_pack(ex2(a0), ex2(a1)));
+        }
+        z += sum8(ps);
+    }
+}
+
+// Pass 2: the sum of 2^(x - lse) over the tile's columns (of [lo, hi) with
+// kMask); `neg_lse` in shared memory, `release` called once the tile is read.
+template <bool kMask, typename Release>
+__device__ __forceinline__ float column_sums(uint32_t tile_addr, const float* neg_lse, uint64_t sl2,
+                                             int lo, int hi, Release&& release) {
+    uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
     for (int c = 0; c < kPwCols; c += 32) {
         uint32_t v[32];
@@ -181,6 +267,7 @@ __device__ __forceinline__ void column_sums(uint64_t (&ps)[4], uint32_t tile_add
             ps[((e >> 1) + 1) & 3] = f32x2_add(ps[((e >> 1) + 1) & 3], f32x2_pack(ex2(a[2]), ex2(a[3])));
         }
     }
+    return sum8(ps);
 }
 
 template <typename T, int D, bool kStats>
@@ -190,25 +277,22 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                            const __grid_constant__ PrefillWeightsParams p) {
     using Lay = PwLayout<D>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-    // resident tiles wait for a whole unit, unless units are single steps
-    constexpr int kA = kStats ? 2 : 3, kB = Lay::kStages - kA;
+    constexpr int kA = Lay::kA, kB = Lay::kB;
     __shared__ __align__(8) uint64_t a_full[kA], a_empty[kA], b_full[kB], b_empty[kB];
     __shared__ __align__(8) uint64_t s_full[kPwBufs], s_empty[kPwBufs];
     __shared__ uint32_t tmem_base;
     __shared__ __align__(16) float lse_s[kPwGroups][2][kPwCols];     // pass 2: [group][tile parity]
-    __shared__ float2 other[2][kPwGroups - 1][kPwRows];              // the other groups' results
+    __shared__ float2 other[2][2][kPwRows];                          // [join parity][resident tile]
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int G = p.group;
     const int q_rows = p.tile_tokens * G;                    // rows of a query tile, <= 128
-    // K tiles are loaded by every producer warp, Q tiles by the first
-    constexpr int kALoaders = kStats ? 1 : kPwProducers, kBLoaders = kStats ? kPwProducers : 1;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kA; ++i) mbar_init(&a_full[i], kALoaders), mbar_init(&a_empty[i], 1);
-        for (int i = 0; i < kB; ++i) mbar_init(&b_full[i], kBLoaders), mbar_init(&b_empty[i], 1);
+        for (int i = 0; i < kA; ++i) mbar_init(&a_full[i], 1), mbar_init(&a_empty[i], 1);
+        for (int i = 0; i < kB; ++i) mbar_init(&b_full[i], 1), mbar_init(&b_empty[i], 2);
         for (int i = 0; i < kPwBufs; ++i) mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4);
         fence_barrier_init();
     }
@@ -226,44 +310,46 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     grid_dependency_wait();
     allow_dependent_launch();
 
-    if (warp >= 1 && warp <= kPwProducers) {
+    if (warp == 2 || warp == 3 || warp >= kPwLoadersAfter) {
         // ------------------------------------------------------------------
-        // producers: all lanes run along, one issues
+        // loaders, one for each stage of the two rings; all lanes run along,
+        // one issues.  A stage has one loader so that every wait follows the
+        // wait for the stage's previous phase: a parity says no more than
+        // that, and a loader that had not waited for that phase would take
+        // the one before it for its own.
         // ------------------------------------------------------------------
-        const int who = warp - 1;
-        if (lane == 0) prefetch_tensor_map(who == 0 ? &tmap_q : &tmap_k);
+        const int who = warp < 4 ? warp - 2 : warp - kPwLoadersAfter + 2;
+        if (lane == 0) prefetch_tensor_map(&tmap_q), prefetch_tensor_map(&tmap_k);
         // waits for stage n % stages to be free
         auto open = [&](uint64_t* empty, int stages, int n) -> bool {
             return n < stages || __all_sync(0xffffffffu, mbar_wait(&empty[n % stages], ((n / stages) - 1) & 1));
         };
-        auto blocks_of = [&](const PwSeq& s, int b, int kt) {     // lane i: block of box i
-            const int tok = kt * kPwCols + 16 * lane;
-            if (lane >= 8 || tok >= s.L) return 0;
+        // block ids of key tiles 4 q .. 4 q + 3: lane i has box i % 8 of tile i / 8
+        auto blocks_of = [&](const PwSeq& s, int b, int q) {
+            const int tok = q * 4 * kPwCols + 16 * lane;
+            if (tok >= s.L) return 0;
             const int blk = __ldg(p.block_tables + (size_t)b * p.max_blocks_per_seq + tok / p.block_size);
             if (blk < 0 || blk >= p.num_blocks) flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
             return blk;
         };
-        // this warp's boxes of a K tile: every kPwProducers-th
         auto load_k = [&](uint8_t* dst, uint64_t* full, uint64_t* empty, int stages, int n,
                           const PwSeq& s, const PwUnit& U, int kt, int blk) -> bool {
             if (!open(empty, stages, n)) return false;
-            const int nbox = __shfl_sync(0xffffffffu, min(8, (s.L - kt * kPwCols + 15) / 16), 0);
-            const int own = nbox > who ? (nbox - who + kPwProducers - 1) / kPwProducers : 0;
+            const int nbox = min(8, (s.L - kt * kPwCols + 15) / 16);
             uint64_t* bar = &full[n % stages];
-            if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(own * Lay::kHalves * kBox16Bytes));
+            if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(nbox * Lay::kHalves * kBox16Bytes));
             __syncwarp();
             dst += (n % stages) * Lay::kTile;
+            const int sub_mask = p.block_size - 1;               // 16 or 32
 #pragma unroll
-            for (int i = 0; i < (8 + kPwProducers - 1) / kPwProducers; ++i) {
-                const int box = who + i * kPwProducers;
+            for (int box = 0; box < 8; ++box) {
                 if (box >= nbox) break;
-                const int pblk = __shfl_sync(0xffffffffu, blk, box);
-                const int sub = (kt * kPwCols + 16 * box) % p.block_size;
+                const int pblk = __shfl_sync(0xffffffffu, blk, (kt & 3) * 8 + box);
                 if (elect_one()) {
 #pragma unroll
                     for (int h = 0; h < Lay::kHalves; ++h)
                         tma_load_4d(dst + h * Lay::kHalf + box * kBox16Bytes, &tmap_k, bar,
-                                    h * kBoxElems, U.g, sub, pblk);
+                                    h * kBoxElems, U.g, (16 * box) & sub_mask, pblk);
                 }
                 __syncwarp();
             }
@@ -273,7 +359,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                           const PwSeq& s, const PwUnit& U, int qt) -> bool {
             if (!open(empty, stages, n)) return false;
             uint64_t* bar = &full[n % stages];
-            const int row = __shfl_sync(0xffffffffu, (int)(s.q0 + (int64_t)qt * p.tile_tokens), 0);
+            const int row = s.q0 + qt * p.tile_tokens;
             dst += (n % stages) * Lay::kTile;
             if (elect_one()) {
                 mbar_arrive_expect_tx(bar, (uint32_t)(q_rows * Lay::kHalves * 128));
@@ -290,81 +376,111 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         PwUnit U;
         int na = 0, nb = 0, at_b = -1, at_g = -1, at_qt = -1;
         bool ok = true;
+        static_assert(kA + kB == kPwLoaders, "a loader for each stage");
         while (ok && walk.next(p, U)) {
-            if (U.first >= U.last) continue;
-            if constexpr (kStats) {
-                int blk = blocks_of(walk.s, U.b, U.first);
-                if (who == 0) ok = load_q(a_ring, a_full, a_empty, kA, na++, walk.s, U, U.a);
-                for (int kt = U.first; ok && kt < U.last; ++kt) {
-                    const int now = blk;                     // the next tile's blocks a step ahead
-                    if (kt + 1 < U.last) blk = blocks_of(walk.s, U.b, kt + 1);
-                    ok = load_k(b_ring, b_full, b_empty, kB, nb++, walk.s, U, kt, now);
+            // block ids of the current four key tiles and of the next four
+            int quad = -2, blk = 0, blk_next = 0;
+            auto to_tile = [&](int kt) {
+                if ((kt >> 2) == quad) return;
+                blk = (kt >> 2) == quad + 1 ? blk_next : blocks_of(walk.s, U.b, kt >> 2);
+                quad = kt >> 2;
+                blk_next = blocks_of(walk.s, U.b, quad + 1);
+            };
+            for (int a = U.a0; ok && a < U.a1; ++a) {
+                int first, last;
+                walk.streamed(p, U, a, first, last);
+                if (first >= last) continue;
+                for (int j = 0; ok && j < walk.residents(a); ++j) {
+                    if (!kStats) to_tile(2 * a + j);
+                    if (na % kA == who)
+                        ok = kStats ? load_q(a_ring, a_full, a_empty, kA, na, walk.s, U, 2 * a + j)
+                                    : load_k(a_ring, a_full, a_empty, kA, na, walk.s, U, 2 * a + j, blk);
+                    ++na;
                 }
-            } else {
-                ok = load_k(a_ring, a_full, a_empty, kA, na++, walk.s, U, U.a,
-                            blocks_of(walk.s, U.b, U.a));
-                for (int qt = U.first; ok && who == 0 && qt < U.last; ++qt) {
-                    if (U.b == at_b && U.g == at_g && qt == at_qt) continue;     // still there
-                    at_b = U.b, at_g = U.g, at_qt = qt;
-                    ok = load_q(b_ring, b_full, b_empty, kB, nb++, walk.s, U, qt);
+                for (int i = first; ok && i < last; ++i) {
+                    if (kStats) {
+                        to_tile(i);
+                    } else {
+                        if (U.b == at_b && U.g == at_g && i == at_qt) continue;     // still there
+                        at_b = U.b, at_g = U.g, at_qt = i;
+                    }
+                    if (nb % kB == who - kA)
+                        ok = kStats ? load_k(b_ring, b_full, b_empty, kB, nb, walk.s, U, i, blk)
+                                    : load_q(b_ring, b_full, b_empty, kB, nb, walk.s, U, i);
+                    ++nb;
                 }
             }
         }
         if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
-    } else if (warp == 0) {
+    } else if (warp < 2) {
         // ------------------------------------------------------------------
-        // MMA issuer: all lanes run along, one issues
+        // MMA issuers, one per resident tile: all lanes run along, one issues
         // ------------------------------------------------------------------
         constexpr uint32_t kId = idesc_f16(kPwRows, kPwCols, kBf16, false);
         const uint64_t a_ring = smem_desc_sw128(smem_u32(smem), 16, 1024);
         const uint64_t b_ring = smem_desc_sw128(smem_u32(smem) + kA * Lay::kTile, 16, 1024);
         PwWalk<kStats> walk;
         PwUnit U;
-        int na = 0, nb = -1, step = 0, at_b = -1, at_g = -1, at_qt = -1;
+        int na = 0, nb = -1, tiles = 0, at_b = -1, at_g = -1, at_qt = -1;
+        int used[2] = {0, 0};                               // products so far in each buffer
         bool ok = true;
         auto wait = [&](uint64_t* bar, int phase) {
             ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1));
         };
         while (ok && walk.next(p, U)) {
-            if (U.first >= U.last) continue;
-            wait(&a_full[na % kA], na / kA);
-            for (int i = U.first; ok && i < U.last; ++i, ++step) {
-                if (kStats || U.b != at_b || U.g != at_g || i != at_qt) {
-                    // the previous streamed tile is free once the products so far are done
-                    if (nb >= 0 && elect_one()) mma_commit(&b_empty[nb % kB]);
-                    __syncwarp();
-                    ++nb;
-                    at_b = U.b, at_g = U.g, at_qt = i;
-                    wait(&b_full[nb % kB], nb / kB);
-                }
-                if (step >= kPwBufs) wait(&s_empty[step % kPwBufs], step / kPwBufs - 1);
-                if (!ok) break;
-                tc_fence_after_sync();
-                const uint64_t a = a_ring + (na % kA) * (Lay::kTile >> 4);
-                const uint64_t b = b_ring + (nb % kB) * (Lay::kTile >> 4);
-                const uint32_t d = tmem + kPwCols * (step % kPwBufs);
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        constexpr int kHalf16 = Lay::kHalf >> 4;
-                        const uint64_t off = (kk >> 2) * kHalf16 + (kk & 3) * 2;
-                        mma_f16_ss(d, a + off, b + off, kId, kk > 0);
+            for (int a = U.a0; ok && a < U.a1; ++a) {
+                int first, last;
+                walk.streamed(p, U, a, first, last);
+                if (first >= last) continue;
+                const int residents = walk.residents(a);
+                const bool active = warp < residents;
+                const int stage = (na + warp) % kA;
+                // both warps wait for both tiles: no phase of a stage is passed over
+                for (int j = 0; j < residents; ++j) wait(&a_full[(na + j) % kA], (na + j) / kA);
+                for (int i = first; ok && i < last; ++i, ++tiles) {
+                    if (kStats || U.b != at_b || U.g != at_g || i != at_qt) {
+                        // the previous streamed tile is free once this warp's products are done
+                        if (nb >= 0 && elect_one()) mma_commit(&b_empty[nb % kB]);
+                        __syncwarp();
+                        ++nb;
+                        at_b = U.b, at_g = U.g, at_qt = i;
+                        // also where this warp has no tile to multiply: it may not run ahead
+                        wait(&b_full[nb % kB], nb / kB);
                     }
-                    mma_commit(&s_full[step % kPwBufs]);
+                    if (!active) continue;
+                    // the group of (resident, parity of the streamed tile) owns the buffer
+                    const int odd = tiles & 1, buf = warp + 2 * odd;
+                    const int n = odd ? used[1]++ : used[0]++;
+                    if (n > 0) wait(&s_empty[buf], n - 1);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint64_t da = a_ring + stage * (Lay::kTile >> 4);
+                    const uint64_t db = b_ring + (nb % kB) * (Lay::kTile >> 4);
+                    const uint32_t d = tmem + kPwCols * buf;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            constexpr int kHalf16 = Lay::kHalf >> 4;
+                            const uint64_t off = (kk >> 2) * kHalf16 + (kk & 3) * 2;
+                            mma_f16_ss(d, da + off, db + off, kId, kk > 0);
+                        }
+                        mma_commit(&s_full[buf]);
+                    }
+                    __syncwarp();
                 }
+                if (ok && active && elect_one()) mma_commit(&a_empty[stage]);
                 __syncwarp();
+                na += residents;
             }
-            if (ok && elect_one()) mma_commit(&a_empty[na % kA]);
-            __syncwarp();
-            ++na;
         }
         if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
     } else {
         // ------------------------------------------------------------------
-        // epilogue: group w takes the steps w, w + 4, ... (buffer w); this
-        // thread owns lane r of every tile
+        // epilogue: group w takes the products of resident tile w % 2 with
+        // the streamed tiles of parity w / 2 (buffer w); this thread owns
+        // lane r of every tile
         // ------------------------------------------------------------------
-        const int group = (warp >> 2) - 1;
+        const int group = (warp >> 2) - 1, res = group & 1, parity = group >> 1;
         const int r = (warp & 3) * 32 + lane;
         const uint32_t tile_addr = tmem + kPwCols * group + ((uint32_t)((warp & 3) * 32) << 16);
         const float sl = p.scale_log2;
@@ -381,105 +497,74 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         };
         PwWalk<kStats> walk;
         PwUnit U;
-        int step = 0, units = 0, mine = 0;
+        int tiles = 0, mine = 0, joins = 0;
         while (walk.next(p, U)) {
             const PwSeq& s = walk.s;
-            const int steps = max(0, U.last - U.first);
-            if (kStats && steps == 0) continue;
             const size_t pair = (size_t)U.b * p.num_kv_heads + U.g;
-            const int key = U.a * kPwCols + r;
-            // a unit of one step is its group's alone, others are joined by group 0
-            const bool writer = steps == 1 ? (step & (kPwGroups - 1)) == group : group == 0;
-            float before = 0.f;
-            if (!kStats && writer && p.query_chunks == 1 && p.weights && key < s.L - s.C)
-                before = p.weights[pair * p.weights_stride + key];
-            float m = -INFINITY, z = 0.f;
-            // first step of this unit that is the group's
-            const int skip = (group - step) & (kPwGroups - 1);
-            step += steps;
-            if constexpr (kStats) {
-                const int pos = min(s.L - s.counted + U.a * p.tile_tokens + r / G, s.L - 1);
-                for (int kt = U.first + skip; kt < U.last; kt += kPwGroups) {
-                    wait(mine++);
-                    const int visible = pos - kt * kPwCols;           // keys 0 .. visible of the tile
-                    const bool whole = __all_sync(0xffffffffu, visible >= kPwCols - 1);
-#pragma unroll
-                    for (int c = 0; c < kPwCols; c += 64) {
-                        uint32_t v[64];
-                        tmem_ld32(tile_addr + c, *reinterpret_cast<uint32_t(*)[32]>(v));
-                        tmem_ld32(tile_addr + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-                        tmem_wait_ld();
-                        if (c == 64) release();
-                        if (!whole) {
-#pragma unroll
-                            for (int e = 0; e < 64; ++e)
-                                if (c + e > visible) v[e] = 0xff800000u;
-                        }
-                        float pm[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) pm[e] = __uint_as_float(v[e]);
-#pragma unroll
-                        for (int e = 4; e < 64; ++e) pm[e & 3] = fmaxf(pm[e & 3], __uint_as_float(v[e]));
-                        const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * sl;
-                        if (mx > m + kRescaleThresholdLog2) {         // also the first finite maximum
-                            z *= ex2(m - mx);
-                            m = mx;
-                        }
-                        const float ref = m == -INFINITY ? 0.f : m;   // nothing visible yet
-                        const uint64_t neg2 = f32x2_pack(-ref, -ref);
-                        uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float a0, a1;
-                            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
-                                                   sl2, neg2), a0, a1);
-                            ps[e & 3] = f32x2_add(ps[e & 3], f32x2_pack(ex2(a0), ex2(a1)));
-                        }
-                        z += sum8(ps);
+            for (int a = U.a0; a < U.a1; ++a) {
+                int first, last;
+                walk.streamed(p, U, a, first, last);
+                const int steps = max(0, last - first);
+                if (kStats && steps == 0) continue;
+                const int skip = (parity - tiles) & 1;       // to the group's first streamed tile
+                tiles += steps;
+                if (res >= walk.residents(a)) continue;
+                const int tile = 2 * a + res, key = tile * kPwCols + r;
+                // one streamed tile is its group's alone; two groups are joined by the first
+                const bool writer = steps == 1 ? skip == 0 : parity == 0;
+                float before = 0.f;
+                if (!kStats && writer && p.query_chunks == 1 && p.weights && key < s.L - s.C)
+                    before = p.weights[pair * p.weights_stride + key];
+                float m = -INFINITY, z = 0.f;
+                if constexpr (kStats) {
+                    const int pos = min(s.L - s.counted + tile * p.tile_tokens + r / G, s.L - 1);
+                    for (int kt = first + skip; kt < last; kt += 2) {
+                        wait(mine++);
+                        const int visible = pos - kt * kPwCols;           // keys 0 .. visible of the tile
+                        if (__all_sync(0xffffffffu, visible >= kPwCols - 1))
+                            row_stats<false>(m, z, tile_addr, sl, sl2, visible, release);
+                        else
+                            row_stats<true>(m, z, tile_addr, sl, sl2, visible, release);
+                    }
+                } else {
+                    for (int qt = first + skip; qt < last; qt += 2) {
+                        const float lse = p.lse[(pair * p.max_query_tiles + qt) * kPwCols + r];
+                        float* ls = lse_s[group][mine & 1];
+                        wait(mine++);
+                        ls[r] = -lse;
+                        asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+                        const int tokens = min(p.tile_tokens, s.counted - qt * p.tile_tokens);
+                        // columns that see this key: from `lo` on, up to the chunk's end
+                        const int lo = (key - (s.L - s.counted + qt * p.tile_tokens)) * G, hi = tokens * G;
+                        if (tokens == p.tile_tokens && __all_sync(0xffffffffu, lo <= 0))
+                            z += column_sums<false>(tile_addr, ls, sl2, lo, hi, release);
+                        else
+                            z += column_sums<true>(tile_addr, ls, sl2, lo, hi, release);
                     }
                 }
-            } else {
-                for (int qt = U.first + skip; qt < U.last; qt += kPwGroups) {
-                    const float lse = p.lse[(pair * p.max_query_tiles + qt) * kPwCols + r];
-                    float* ls = lse_s[group][mine & 1];
-                    wait(mine++);
-                    ls[r] = -lse;
-                    asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
-                    const int tokens = min(p.tile_tokens, s.counted - qt * p.tile_tokens);
-                    // columns that see this key: from `lo` on, up to the chunk's end
-                    const int lo = (key - (s.L - s.counted + qt * p.tile_tokens)) * G, hi = tokens * G;
-                    const bool whole = tokens == p.tile_tokens && __all_sync(0xffffffffu, lo <= 0);
-                    uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
-                    if (whole) column_sums<false>(ps, tile_addr, ls, sl2, lo, hi, release);
-                    else column_sums<true>(ps, tile_addr, ls, sl2, lo, hi, release);
-                    z += sum8(ps);
-                }
-            }
-            if (steps > 1) {
-                if (group > 0) other[units & 1][group - 1][r] = make_float2(m, z);
-                asm volatile("bar.sync 5, %0;" ::"n"(kPwGroups * 128) : "memory");
-                if (group == 0) {
-#pragma unroll
-                    for (int i = 0; i < kPwGroups - 1; ++i) {
-                        const float2 o = other[units & 1][i][r];
+                if (steps > 1) {
+                    if (parity == 1) other[joins & 1][res][r] = make_float2(m, z);
+                    asm volatile("bar.sync %0, 256;" ::"r"(5 + res) : "memory");
+                    if (parity == 0) {
+                        const float2 o = other[joins & 1][res][r];
                         if (kStats) join_stats(m, z, o);
                         else z += o.y;
                     }
+                    ++joins;
                 }
-                ++units;
-            }
-            if (!writer || failed) continue;
-            if constexpr (kStats) {
-                const int tokens = min(p.tile_tokens, s.counted - U.a * p.tile_tokens);
-                const size_t at = (pair * p.max_query_tiles + U.a) * kPwRows + r;
-                if (p.key_chunks == 1) p.lse[at] = r < tokens * G ? m + log2f(z) : INFINITY;
-                else p.stats[(size_t)U.chunk * p.num_seqs * p.num_kv_heads * p.max_query_tiles * kPwRows + at] =
-                    make_float2(m, z);
-            } else if (key < s.L) {
-                if (p.query_chunks == 1)
-                    p.weights_out[pair * p.weights_stride + key] = before + z;
-                else
-                    p.columns[((size_t)U.chunk * p.num_seqs * p.num_kv_heads + pair) * p.columns_stride + key] = z;
+                if (!writer || failed) continue;
+                if constexpr (kStats) {
+                    const int tokens = min(p.tile_tokens, s.counted - tile * p.tile_tokens);
+                    const size_t at = (pair * p.max_query_tiles + tile) * kPwRows + r;
+                    if (p.key_chunks == 1) p.lse[at] = r < tokens * G ? m + log2f(z) : INFINITY;
+                    else p.stats[(size_t)U.chunk * p.num_seqs * p.num_kv_heads * p.max_query_tiles * kPwRows + at] =
+                        make_float2(m, z);
+                } else if (key < s.L) {
+                    if (p.query_chunks == 1)
+                        p.weights_out[pair * p.weights_stride + key] = before + z;
+                    else
+                        p.columns[((size_t)U.chunk * p.num_seqs * p.num_kv_heads + pair) * p.columns_stride + key] = z;
+                }
             }
         }
         if (failed && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
@@ -504,10 +589,17 @@ __global__ void __launch_bounds__(kPwRows)
     if (qt >= s.n_qt) return;
     const size_t rows = (size_t)p.num_seqs * p.num_kv_heads * p.max_query_tiles * kPwRows;
     const size_t at = (((size_t)b * p.num_kv_heads + g) * p.max_query_tiles + qt) * kPwRows + r;
-    const int chunks = (pw_key_tiles(p, s, qt) + p.key_chunk - 1) / p.key_chunk;
+    // chunks of this tile: up to the last key tile that the pair it was resident in reaches
+    const int seen = pw_key_tiles(p, s, min(qt | 1, s.n_qt - 1));
+    const int chunks = (seen + p.key_chunk - 1) / p.key_chunk;
     float m = -INFINITY, z = 0.f;
-    for (int c = 0; c < chunks; ++c) {
-        join_stats(m, z, p.stats[c * rows + at]);
+    for (int c0 = 0; c0 < chunks; c0 += 8) {                 // eight loads in flight
+        float2 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = c0 + i < chunks ? p.stats[(c0 + i) * rows + at] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) join_stats(m, z, v[i]);
     }
     const int tokens = min(p.tile_tokens, s.counted - qt * p.tile_tokens);
     p.lse[at] = r < tokens * p.group ? m + log2f(z) : INFINITY;
@@ -525,7 +617,8 @@ __global__ void __launch_bounds__(kPwJoinThreads)
     const size_t pair = (size_t)b * p.num_kv_heads + g, pairs = (size_t)p.num_seqs * p.num_kv_heads;
     const size_t at = pair * p.weights_stride + j;
     float w = p.weights && j < s.L - s.C ? p.weights[at] : 0.f;
-    const int first = pw_first_query_tile(p, s, j / kPwCols) / p.query_chunk;
+    // chunks whose queries reach the pair of key tiles that this key was resident in
+    const int first = pw_first_query_tile(p, s, j / kPwCols & ~1) / p.query_chunk;
     const int chunks = (s.n_qt + p.query_chunk - 1) / p.query_chunk;
     float sum = 0.f;
     for (int c = first; c < chunks; ++c) sum += p.columns[(c * pairs + pair) * p.columns_stride + j];
@@ -538,14 +631,18 @@ size_t prefill_weights_plan(PrefillWeightsParams& p, void* workspace) {
     p.max_query_tiles = (p.max_counted + p.tile_tokens - 1) / p.tile_tokens;
     const int64_t key_tiles = ((int64_t)p.max_context + kPwCols - 1) / kPwCols;
     const int64_t pairs = (int64_t)p.num_seqs * p.num_kv_heads;
-    // Pass 1 in chunks of so many key tiles that each SM gets some 16 units
-    // (the batch taken at its bounds), but not below four tiles (a unit's
-    // load of its queries) nor above 64; pass 2 in chunks of 16 query tiles.
-    const int64_t share = pairs * p.max_query_tiles * key_tiles / (152 * 16);
-    p.key_chunk = (int)std::min<int64_t>(64, std::max<int64_t>(4, share));
+    // Units of some sixteenth of an SM's share (the batch taken at its
+    // bounds): pass 1 in chunks of 4 to 64 key tiles, pass 2 in chunks of 8
+    // to 64 query tiles; where one query tile is all there is, pass 2 takes
+    // runs of key tile pairs past it instead.
+    const int64_t per_sm = 152 * 16;
+    const int64_t share1 = pairs * ((p.max_query_tiles + 1) / 2) * key_tiles / per_sm;
+    const int64_t share2 = pairs * ((key_tiles + 1) / 2) * p.max_query_tiles / per_sm;
+    p.key_chunk = (int)std::min<int64_t>(64, std::max<int64_t>(4, share1));
     p.key_chunks = (int)std::max<int64_t>(1, (key_tiles + p.key_chunk - 1) / p.key_chunk);
-    p.query_chunk = 16;
+    p.query_chunk = (int)std::min<int64_t>(64, std::max<int64_t>(8, share2));
     p.query_chunks = std::max(1, (p.max_query_tiles + p.query_chunk - 1) / p.query_chunk);
+    p.key_run = p.max_query_tiles > 1 ? 1 : (int)std::min<int64_t>(8, std::max<int64_t>(1, share2));
     p.columns_stride = (int)(key_tiles * kPwCols);
     const size_t rows = (size_t)pairs * p.max_query_tiles * kPwRows;
     char* base = static_cast<char*>(workspace);
