@@ -108,6 +108,7 @@ struct EvictParams {
     int row_bytes;                 // of one head's K (or V) of one token
     int budget, trigger, sinks, recent;
     int moves_stride;
+    int cluster;                   // CTAs of the select kernel per (sequence, KV head)
 };
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);

@@ -9,14 +9,24 @@
 // of the tokens in the cache; their positions travel with them.
 //
 // The choice is a radix select on an order-preserving 32-bit image of the
-// weight (protected tokens above every weight), 8 bits a pass.
+// weight (protected tokens above every weight) in digits of 11, 11 and 10
+// bits.  A cluster of CTAs serves one (sequence, KV head), each CTA a
+// contiguous slice of the tokens with its images in registers; histograms
+// and counts are exchanged through distributed shared memory, and every CTA
+// draws the same conclusions from them.  Few moves are made by the cluster
+// itself; many are left to a second kernel that spreads them over the GPU.
 #include "bounded_internal.h"
 #include "pa_device.cuh"
 
 namespace pa {
 
-constexpr int kEvictThreads = 1024;
 constexpr uint32_t kProtected = 0xffffffffu;
+constexpr int kEvictKeys = 8;                // images a thread holds
+constexpr int kEvictBins = 2048;
+constexpr int kEvictMaxCluster = 8;
+// Moves per CTA that the select kernel makes itself: one round of rows for
+// its warps; more are spread by the move kernel.
+constexpr int kEvictOwnMoves = 64;
 
 // Larger weight, larger image: -0 equals +0, NaN lies below everything.
 __device__ __forceinline__ uint32_t weight_image(float w) {
@@ -48,8 +58,22 @@ __device__ __forceinline__ int evict_position(const EvictSeq& s, const int32_t* 
     return i < s.known ? positions[i] : i + (s.seen - s.L);
 }
 
-// Exclusive prefix of one packed count per thread over the block, and the
-// total; `sums` holds a word per warp.
+// ---- clusters -------------------------------------------------------------
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Word at the same shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_word(const uint32_t* local, int rank) {
+    uint32_t addr, v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Exclusive prefix of one count per thread over the block, and the total;
+// `sums` holds a word per warp.  Ends with the block in step.
+template <int kThreads>
 __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* sums, uint32_t* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t incl = v;
@@ -61,7 +85,7 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* sums, uin
     __syncthreads();                            // the previous call's reads of sums
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    uint32_t w = lane < kEvictThreads / 32 ? sums[lane] : 0u, wi = w;
+    uint32_t w = lane < kThreads / 32 ? sums[lane] : 0u, wi = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const uint32_t u = __shfl_up_sync(0xffffffffu, wi, d);
@@ -71,125 +95,294 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* sums, uin
     return __shfl_sync(0xffffffffu, wi - w, warp) + incl - v;
 }
 
-// One CTA per (sequence, KV head): which tokens stay, the gap and mover
-// lists, and the state of the tokens that stay in place.
-__global__ void __launch_bounds__(kEvictThreads)
+// ---- moves ----------------------------------------------------------------
+// Moves [n0, n1) of the lists, at most kMoveBatch: K and V rows, weight and
+// position of each mover into its gap.  The rows' addresses go through shared
+// memory first, so that a thread then has eight 16-byte loads in flight.
+constexpr int kMoveBatch = 64;
+
+struct MoveRows {
+    int64_t src[kMoveBatch], dst[kMoveBatch];
+};
+
+template <int kThreads>
+__device__ __forceinline__ void move_rows(const EvictParams& p, const EvictSeq& s, int b, int g,
+                                          size_t pair, const int32_t* gaps, const int32_t* movers,
+                                          int n0, int n1, MoveRows& rows) {
+    const int tid = threadIdx.x, vecs = p.row_bytes / 16, count = n1 - n0;
+    const int32_t* table = p.block_tables + (size_t)b * p.max_blocks_per_seq;
+    __syncthreads();                            // the previous batch's reads of rows
+    for (int i = tid; i < count; i += kThreads) {
+        const int from = movers[n0 + i], to = gaps[n0 + i];
+        p.weights_out[pair * p.stride + to] = p.weights[pair * p.stride + from];
+        p.positions_out[pair * p.stride + to] = evict_position(s, p.positions + pair * p.stride, from);
+        const int fb = table[from / p.block_size], tb = table[to / p.block_size];
+        const bool ok = fb >= 0 && fb < p.num_blocks && tb >= 0 && tb < p.num_blocks;
+        if (!ok) flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
+        rows.src[i] = ok ? (((int64_t)fb * p.block_size + from % p.block_size) * p.num_kv_heads + g) * vecs : -1;
+        rows.dst[i] = (((int64_t)tb * p.block_size + to % p.block_size) * p.num_kv_heads + g) * vecs;
+    }
+    __syncthreads();
+    // items of a batch: move, K or V, 16-byte vector (vecs is 8 or 16)
+    const int items = count * 2 * vecs, shift = vecs == 16 ? 4 : 3;
+    for (int i0 = tid; i0 < items; i0 += 8 * kThreads) {
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * kThreads;
+            if (i >= items || rows.src[i >> (shift + 1)] < 0) continue;
+            const uint4* cache = static_cast<const uint4*>((i >> shift) & 1 ? p.v_cache : p.k_cache);
+            v[k] = cache[rows.src[i >> (shift + 1)] + (i & (vecs - 1))];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * kThreads;
+            if (i >= items || rows.src[i >> (shift + 1)] < 0) continue;
+            uint4* cache = static_cast<uint4*>((i >> shift) & 1 ? p.v_cache : p.k_cache);
+            cache[rows.dst[i >> (shift + 1)] + (i & (vecs - 1))] = v[k];
+        }
+    }
+}
+
+// ---- select ---------------------------------------------------------------
+// Grid (KV heads * cluster, sequences): which tokens stay, the gap and mover
+// lists, the state of the tokens that stay in place, and few moves.
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
     evict_select_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ uint32_t hist[256];
+    constexpr int kWarps = kThreads / 32, kChunk = kThreads * kEvictKeys;
+    __shared__ uint32_t hist[3][kEvictBins];
     __shared__ uint32_t sums[32];
+    __shared__ uint32_t counts[4];              // below left: above T, equal to T; past left: the same
     __shared__ uint32_t digit_s, above_s;
+    __shared__ uint32_t line[2][kEvictKeys * kWarps];
+    __shared__ MoveRows rows;
+    const int C = p.cluster, rank = blockIdx.x % C;
+    const int g = blockIdx.x / C, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < 3 * kEvictBins; i += kThreads) (&hist[0][0])[i] = 0;
+    if (tid < 4) counts[tid] = 0;
     grid_dependency_wait();
     allow_dependent_launch();
-    const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-    const EvictSeq s = evict_sequence(p, b, tid == 0 && g == 0);
+    const EvictSeq s = evict_sequence(p, b, tid == 0 && blockIdx.x == 0);
     const size_t pair = (size_t)b * p.num_kv_heads + g;
     const float* w = p.weights + pair * p.stride;
     const int32_t* pos = p.positions + pair * p.stride;
     float* wo = p.weights_out + pair * p.stride;
     int32_t* po = p.positions_out + pair * p.stride;
-    if (g == 0 && tid == 0) p.new_lens[b] = s.left;
+    if (blockIdx.x == 0 && tid == 0) p.new_lens[b] = s.left;
+    // this CTA's slice, in chunks that fit the registers
+    const int slice = ((s.L + C - 1) / C + 31) / 32 * 32;
+    const int lo = min(rank * slice, s.L), hi = min(lo + slice, s.L);
     if (s.left == s.L) {
-        if (tid == 0) p.num_moves[pair] = 0;
-        for (int i = tid; i < s.L; i += kEvictThreads) {
-            wo[i] = w[i];
-            po[i] = evict_position(s, pos, i);
+        if (rank == 0 && tid == 0) p.num_moves[pair] = 0;
+        const bool copy = p.weights_out != p.weights, move = p.positions_out != p.positions;
+        for (int i = lo + tid; i < hi; i += kThreads) {
+            if (copy) wo[i] = w[i];
+            if (move || i >= s.known) po[i] = evict_position(s, pos, i);
         }
         return;
     }
-    auto image = [&](int i) {
-        const int at = evict_position(s, pos, i);
-        return at < p.sinks || at >= s.seen - p.recent ? kProtected : weight_image(w[i]);
+    uint32_t key[kEvictKeys];
+    auto load = [&](int c0) {                   // images of tokens c0 + tid, + kThreads, ...
+#pragma unroll
+        for (int e = 0; e < kEvictKeys; ++e) {
+            const int i = c0 + e * kThreads + tid;
+            key[e] = 0;
+            if (i < hi) {
+                const int at = evict_position(s, pos, i);
+                key[e] = at < p.sinks || at >= s.seen - p.recent ? kProtected : weight_image(w[i]);
+            }
+        }
     };
-    // the image of the left-th largest, and how many of its equals stay
-    uint32_t prefix = 0, want = s.left;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kEvictThreads) hist[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < s.L; i += kEvictThreads) {
-            const uint32_t k = image(i);
-            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-                atomicAdd(&hist[(k >> shift) & 255u], 1u);
+    auto barrier = [&] {
+        if (C > 1) cluster_barrier();
+        else __syncthreads();
+    };
+    const bool once = hi - lo <= kChunk;
+    if (once) load(lo);
+    __syncthreads();                            // histograms cleared
+    // T, the image of the left-th largest, and how many of its equals stay
+    uint32_t T = 0, want = s.left;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), top = pass == 0 ? 32 : (pass == 1 ? 21 : 10);
+        for (int c0 = lo; c0 < hi; c0 += kChunk) {
+            if (!once) load(c0);
+#pragma unroll
+            for (int e = 0; e < kEvictKeys; ++e) {
+                if (c0 + e * kThreads + tid < hi && (pass == 0 || (key[e] >> top) == (T >> top)))
+                    atomicAdd(&hist[pass][(key[e] >> shift) & (pass == 2 ? 1023u : 2047u)], 1u);
+            }
+        }
+        barrier();
+        // bins from the top one down, kEvictBins / kThreads to a thread
+        constexpr int kPer = kEvictBins / kThreads;
+        uint32_t mine[kPer], sum = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const uint32_t* bin = &hist[pass][kEvictBins - 1 - (kPer * tid + k)];
+            mine[k] = 0;
+            if (C == 1) mine[k] = *bin;
+            else for (int r = 0; r < C; ++r) mine[k] += cluster_word(bin, r);
+            sum += mine[k];
+        }
+        uint32_t total;
+        uint32_t before = block_prefix<kThreads>(sum, sums, &total);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            if (before < want && before + mine[k] >= want)
+                digit_s = kEvictBins - 1 - (kPer * tid + k), above_s = before;
+            before += mine[k];
         }
         __syncthreads();
-        const uint32_t mine = tid < 256 ? hist[255 - tid] : 0u;
-        uint32_t total;
-        const uint32_t before = block_prefix(mine, sums, &total);
-        if (tid < 256 && before < want && before + mine >= want) digit_s = 255 - tid, above_s = before;
-        __syncthreads();
-        prefix |= digit_s << shift;
+        T |= digit_s << shift;
         want -= above_s;
     }
+    // counts of the slice, then of the slices before it
+    {
+        uint32_t n[4] = {0, 0, 0, 0};
+        for (int c0 = lo; c0 < hi; c0 += kChunk) {
+            if (!once) load(c0);
+#pragma unroll
+            for (int e = 0; e < kEvictKeys; ++e) {
+                const int i = c0 + e * kThreads + tid;
+                const int past = i >= s.left ? 2 : 0;
+                const bool gt = i < hi && key[e] > T, eq = i < hi && key[e] == T;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) n[q] += (q & 2) == past && (q & 1 ? eq : gt);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t t = __reduce_add_sync(0xffffffffu, n[q]);
+            if (lane == 0) atomicAdd(&counts[q], t);
+        }
+    }
+    barrier();
+    uint32_t equal = 0, n_gaps = 0, n_movers = 0, moves = 0;
+    for (int r = 0; r < C; ++r) {
+        uint32_t n[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) n[q] = C == 1 ? counts[q] : cluster_word(&counts[q], r);
+        const int r0 = min(r * slice, s.L), r1 = min(r0 + slice, s.L);
+        const uint32_t below = max(0, min(r1, s.left) - r0);
+        // equals stay from the lowest index on
+        const uint32_t free = want > equal ? want - equal : 0u;
+        const uint32_t eq_below = min(free, n[1]), eq_past = min(free - eq_below, n[3]);
+        if (r == rank) n_gaps = moves, n_movers = 0;
+        moves += below - n[0] - eq_below;
+        line[0][r] = n[2] + eq_past;            // every thread writes the same
+        equal += n[1] + n[3];
+    }
+    for (int r = 0; r < rank; ++r) n_movers += line[0][r];
+    equal = 0;
+    for (int r = 0; r < rank; ++r)
+        equal += (C == 1 ? counts[1] : cluster_word(&counts[1], r)) + (C == 1 ? counts[3] : cluster_word(&counts[3], r));
+    __syncthreads();                            // line is used again
     // gaps below left and movers from left on, in order
     int32_t* gaps = p.moves + pair * 2 * p.moves_stride;
     int32_t* movers = gaps + p.moves_stride;
-    uint32_t equal = 0, n_gaps = 0, n_movers = 0;
-    for (int i0 = 0; i0 < s.L; i0 += kEvictThreads) {
-        const int i = i0 + tid;
-        const uint32_t k = i < s.L ? image(i) : 0u;
-        const bool eq = i < s.L && k == prefix;
-        uint32_t total;
-        const uint32_t rank = equal + block_prefix(eq, sums, &total);
-        equal += total;
-        const bool keep = i < s.L && (k > prefix || (eq && rank < want));
-        const bool gap = i < s.left && !keep, mover = i >= s.left && keep;
-        // both counts of the block's 1024 tokens fit 16 bits
-        const uint32_t at = block_prefix((uint32_t)gap | ((uint32_t)mover << 16), sums, &total);
-        if (gap) gaps[n_gaps + (at & 0xffffu)] = i;
-        if (mover) movers[n_movers + (at >> 16)] = i;
-        n_gaps += total & 0xffffu, n_movers += total >> 16;
-        if (i < s.left && keep) {
-            wo[i] = w[i];
-            po[i] = evict_position(s, pos, i);
+    for (int c0 = lo; c0 < hi; c0 += kChunk) {
+        if (!once) load(c0);
+        // rank among the equals: rows of kThreads tokens, warps, lanes
+#pragma unroll
+        for (int e = 0; e < kEvictKeys; ++e) {
+            const uint32_t eq = __ballot_sync(0xffffffffu, c0 + e * kThreads + tid < hi && key[e] == T);
+            if (lane == 0) line[0][e * kWarps + warp] = __popc(eq);
         }
+        __syncthreads();
+        uint32_t total;
+        uint32_t at = block_prefix<kThreads>(tid < kEvictKeys * kWarps ? line[0][tid] : 0u, sums, &total);
+        if (tid < kEvictKeys * kWarps) line[0][tid] = at;
+        __syncthreads();
+        uint32_t gap_bits = 0, mover_bits = 0, gap_mask[kEvictKeys], mover_mask[kEvictKeys];
+#pragma unroll
+        for (int e = 0; e < kEvictKeys; ++e) {
+            const int i = c0 + e * kThreads + tid;
+            const bool in = i < hi, is_eq = in && key[e] == T;
+            const uint32_t eq = __ballot_sync(0xffffffffu, is_eq);
+            const uint32_t nth = equal + line[0][e * kWarps + warp] + __popc(eq & ((1u << lane) - 1u));
+            const bool keep = in && (key[e] > T || (is_eq && nth < want));
+            const bool gap = in && i < s.left && !keep, mover = keep && i >= s.left;
+            gap_mask[e] = __ballot_sync(0xffffffffu, gap);
+            mover_mask[e] = __ballot_sync(0xffffffffu, mover);
+            gap_bits |= (uint32_t)gap << e, mover_bits |= (uint32_t)mover << e;
+            // both counts of a chunk fit 16 bits
+            if (lane == 0) line[1][e * kWarps + warp] = __popc(gap_mask[e]) | (__popc(mover_mask[e]) << 16);
+            if (keep && i < s.left) {
+                if (p.weights_out != p.weights) wo[i] = w[i];
+                if (p.positions_out != p.positions || i >= s.known) po[i] = evict_position(s, pos, i);
+            }
+        }
+        equal += total;
+        __syncthreads();
+        at = block_prefix<kThreads>(tid < kEvictKeys * kWarps ? line[1][tid] : 0u, sums, &total);
+        if (tid < kEvictKeys * kWarps) line[1][tid] = at;
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kEvictKeys; ++e) {
+            const int i = c0 + e * kThreads + tid;
+            const uint32_t before = line[1][e * kWarps + warp];
+            if ((gap_bits >> e) & 1u) gaps[n_gaps + (before & 0xffffu) + __popc(gap_mask[e] & ((1u << lane) - 1u))] = i;
+            if ((mover_bits >> e) & 1u) movers[n_movers + (before >> 16) + __popc(mover_mask[e] & ((1u << lane) - 1u))] = i;
+        }
+        n_gaps += total & 0xffffu, n_movers += total >> 16;
     }
-    if (tid == 0) p.num_moves[pair] = n_gaps;
+    const bool own = moves <= (uint32_t)(kEvictOwnMoves * C);
+    if (rank == 0 && tid == 0) p.num_moves[pair] = own ? 0 : moves;
+    // the lists are complete; also no CTA leaves while another reads its shared memory
+    barrier();
+    if (!own) return;
+    const int per = ((int)moves + C - 1) / C, n0 = min(rank * per, (int)moves);
+    move_rows<kThreads>(p, s, b, g, pair, gaps, movers, n0, min(n0 + per, (int)moves), rows);
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMovesPerCta = 64;
 
-// Grid (move chunks, KV heads, sequences): K and V rows, weight and position
-// of each mover into its gap.
+// Grid (move batches, KV heads, sequences).
 __global__ void __launch_bounds__(kMoveThreads)
     evict_move_kernel(const __grid_constant__ EvictParams p) {
+    __shared__ MoveRows rows;
     grid_dependency_wait();
     allow_dependent_launch();
-    const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+    const int g = blockIdx.y, b = blockIdx.z;
     const size_t pair = (size_t)b * p.num_kv_heads + g;
-    const int n0 = blockIdx.x * kMovesPerCta, n1 = min(n0 + kMovesPerCta, p.num_moves[pair]);
+    const int n0 = blockIdx.x * kMoveBatch, n1 = min(n0 + kMoveBatch, p.num_moves[pair]);
     if (n0 >= n1) return;
-    const EvictSeq s = evict_sequence(p, b, false);
     const int32_t* gaps = p.moves + pair * 2 * p.moves_stride;
-    const int32_t* movers = gaps + p.moves_stride;
-    const int32_t* table = p.block_tables + (size_t)b * p.max_blocks_per_seq;
-    const int vecs = p.row_bytes / 16;
-    auto row = [&](int i) -> int64_t {           // row of token i and this head, or -1
-        const int blk = table[i / p.block_size];
-        if (blk < 0 || blk >= p.num_blocks) return -1;
-        return (((int64_t)blk * p.block_size + i % p.block_size) * p.num_kv_heads + g) * vecs;
-    };
-    for (int item = tid; item < (n1 - n0) * 2 * vecs; item += kMoveThreads) {
-        const int n = n0 + item / (2 * vecs), c = item % vecs;
-        const int64_t src = row(movers[n]), dst = row(gaps[n]);
-        if (src < 0 || dst < 0) {
-            flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
-            continue;
-        }
-        uint4* cache = static_cast<uint4*>((item / vecs) & 1 ? p.v_cache : p.k_cache);
-        cache[dst + c] = cache[src + c];
-    }
-    for (int n = n0 + tid; n < n1; n += kMoveThreads) {
-        const int from = movers[n], to = gaps[n];
-        p.weights_out[pair * p.stride + to] = p.weights[pair * p.stride + from];
-        p.positions_out[pair * p.stride + to] = evict_position(s, p.positions + pair * p.stride, from);
-    }
+    move_rows<kMoveThreads>(p, evict_sequence(p, b, false), b, g, pair, gaps, gaps + p.moves_stride, n0, n1,
+                            rows);
 }
 
-cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
-    cudaError_t e = launch_with_pdl(evict_select_kernel, dim3(p.num_kv_heads, p.num_seqs),
-                                    dim3(kEvictThreads), 0, stream, p);
-    if (e != cudaSuccess || p.moves_stride == 0) return e;
-    const dim3 grid((p.moves_stride + kMovesPerCta - 1) / kMovesPerCta, p.num_kv_heads, p.num_seqs);
+template <int kThreads>
+cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.num_kv_heads * p.cluster, p.num_seqs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<kThreads>, p);
+}
+
+cudaError_t launch_evict(const EvictParams& params, cudaStream_t stream) {
+    EvictParams p = params;
+    // What the tables can hold decides: 256 threads where that fits their
+    // registers (four such CTAs or more share an SM), else 1024, and a cluster that
+    // holds the longest context in registers, up to the portable size.
+    const int64_t longest = (int64_t)p.max_blocks_per_seq * p.block_size;
+    const bool small = longest <= 256 * kEvictKeys;
+    const int64_t ctas = (longest + 1024 * kEvictKeys - 1) / (1024 * kEvictKeys);
+    p.cluster = small ? 1 : (int)(ctas < kEvictMaxCluster ? ctas : kEvictMaxCluster);
+    cudaError_t e = small ? launch_evict_select<256>(p, stream) : launch_evict_select<1024>(p, stream);
+    if (e != cudaSuccess || p.moves_stride <= kEvictOwnMoves * p.cluster) return e;
+    const dim3 grid((p.moves_stride + kMoveBatch - 1) / kMoveBatch, p.num_kv_heads, p.num_seqs);
     return launch_with_pdl(evict_move_kernel, grid, dim3(kMoveThreads), 0, stream, p);
 }
 

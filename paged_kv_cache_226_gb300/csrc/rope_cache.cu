@@ -9,6 +9,8 @@
 // position in wrapping integer arithmetic, so whole turns drop out exactly
 // and the error is 2^-53 of the unreduced angle plus 2^-33 turns, at any
 // position.  Products and sums are in fp32; each result is rounded once.
+#include <type_traits>
+
 #include "bounded_internal.h"
 #include "pa_device.cuh"
 
@@ -53,91 +55,154 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale) {
     return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
 }
 
-// One CTA per token.  A thread's unit of work is 16 dims of one head, two
-// 16-byte chunks: the two halves of eight pairs, or two chunks past the
-// rotated dims.
-template <typename T, int D, bool kFp8, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads)
+// A CTA serves kTokens tokens.  A thread's item is 16 dims of one head of one
+// token, two 16-byte chunks: the two halves of eight pairs, or two chunks
+// past the rotated dims.  A thread keeps its place u inside the head and
+// walks the heads of its CTA's tokens, q first, kRopeBatch at a time with all
+// their loads in flight; the first batch is requested before the positions
+// have arrived and while cos and sin are formed.
+constexpr int kRopeBatch = 4;
+enum RopeRows { kRopeQ, kRopeK, kRopeV };
+
+template <typename T, int D, bool kFp8, bool kInterleaved, int kTokens>
+__global__ void __launch_bounds__(kRopeThreads, 4)
     rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int kUnits = D / 16;
-    __shared__ float2 cs[D / 2];
+    constexpr int kUnits = D / 16, kHeads = kRopeThreads / kUnits;      // items side by side
+    __shared__ __align__(16) float2 cs[kTokens][D / 2];
+    __shared__ int64_t slot_s[kTokens];
     grid_dependency_wait();
     allow_dependent_launch();
-    const int64_t t = blockIdx.x;
+    const int tid = threadIdx.x, u = tid % kUnits, first = tid / kUnits;
+    const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+    const int tokens = (int)min((int64_t)kTokens, p.num_tokens - t0);
     const int turned = p.rotary_dim / 16;              // units with rotated pairs
-    const int64_t position = p.positions[t];
-    const int64_t slot = p.slots[t];
-    if (slot >= p.num_slots && threadIdx.x == 0) flag_error(p.err, PA_DEVERR_BAD_SLOT);
-    const bool cached = slot >= 0 && slot < p.num_slots;
-    for (int i = threadIdx.x; i < p.rotary_dim / 2; i += kRopeThreads)
-        cs[i] = rope_cos_sin(rope_turns(p.inv_freq[i]), position, p.factor);
-    __syncthreads();
-    const int hq = p.num_q_heads, hkv = p.num_kv_heads;
-    const int units = (hq + (cached ? 2 * hkv : 0)) * kUnits;
-    for (int i = threadIdx.x; i < units; i += kRopeThreads) {
-        int h = i / kUnits;
-        const int u = i % kUnits;
-        const bool is_q = h < hq, is_v = h >= hq + hkv;
-        const bool rot = !is_v && u < turned;
-        const int c0 = rot && !kInterleaved ? u : 2 * u;
-        const int c1 = rot && !kInterleaved ? u + turned : 2 * u + 1;
-        h -= is_q ? 0 : (is_v ? hq + hkv : hq);
-        const T* src = static_cast<const T*>(is_q ? p.q : (is_v ? p.v : p.k)) +
-                       t * (is_q ? p.q_stride : (is_v ? p.v_stride : p.k_stride)) + h * D;
-        uint4 v0 = reinterpret_cast<const uint4*>(src)[c0];
-        uint4 v1 = reinterpret_cast<const uint4*>(src)[c1];
-        float x0[8], x1[8];
-        if (rot || kFp8) {
-            unpack8<T>(v0, x0);
-            unpack8<T>(v1, x1);
+    const bool rot = u < turned;
+    const int c0 = rot && !kInterleaved ? u : 2 * u;   // chunks of q and k; v: 2u, 2u + 1
+    const int c1 = rot && !kInterleaved ? u + turned : 2 * u + 1;
+    auto token_of = [&](int v, int heads) {
+        int tk = 0;
+#pragma unroll
+        for (int i = 1; i < kTokens; ++i) tk += v >= i * heads;
+        return tk;
+    };
+    uint4 v0[kRopeBatch], v1[kRopeBatch];
+    auto load = [&](auto rows, int at) {
+        constexpr int kRows = decltype(rows)::value;
+        const int heads = kRows == kRopeQ ? p.num_q_heads : p.num_kv_heads;
+        const T* base = static_cast<const T*>(kRows == kRopeQ ? p.q : (kRows == kRopeK ? p.k : p.v));
+        const int64_t stride = kRows == kRopeQ ? p.q_stride : (kRows == kRopeK ? p.k_stride : p.v_stride);
+#pragma unroll
+        for (int k = 0; k < kRopeBatch; ++k) {
+            const int v = at + k * kHeads;
+            if (v >= tokens * heads) break;
+            const int tk = token_of(v, heads);
+            const uint4* src = reinterpret_cast<const uint4*>(base + (t0 + tk) * stride + (v - tk * heads) * D);
+            v0[k] = src[kRows == kRopeV ? 2 * u : c0];
+            v1[k] = src[kRows == kRopeV ? 2 * u + 1 : c1];
         }
-        if (rot) {
-            const float2* a = cs + 8 * u;
-            if (kInterleaved) {
+    };
+    auto store = [&](auto rows, int at) {
+        constexpr int kRows = decltype(rows)::value;
+        const int heads = kRows == kRopeQ ? p.num_q_heads : p.num_kv_heads;
+#pragma unroll
+        for (int k = 0; k < kRopeBatch; ++k) {
+            const int v = at + k * kHeads;
+            if (v >= tokens * heads) break;
+            const int tk = token_of(v, heads), h = v - tk * heads;
+            const int64_t slot = kRows == kRopeQ ? 0 : slot_s[tk];
+            if (slot < 0) continue;
+            constexpr bool kCodes = kFp8 && kRows != kRopeQ;
+            float x0[8], x1[8];
+            if (kCodes || (kRows != kRopeV && rot)) {
+                unpack8<T>(v0[k], x0);
+                unpack8<T>(v1[k], x1);
+            }
+            if (kRows != kRopeV && rot) {
+                const float4* a = reinterpret_cast<const float4*>(&cs[tk][8 * u]);     // two pairs each
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 e = a[j], f = a[4 + j];
-                    const float r0 = x0[2 * j] * e.x - x0[2 * j + 1] * e.y;
-                    const float r1 = x1[2 * j] * f.x - x1[2 * j + 1] * f.y;
-                    x0[2 * j + 1] = x0[2 * j + 1] * e.x + x0[2 * j] * e.y;
-                    x1[2 * j + 1] = x1[2 * j + 1] * f.x + x1[2 * j] * f.y;
-                    x0[2 * j] = r0, x1[2 * j] = r1;
+                    const float4 w = a[j];
+                    if (kInterleaved) {
+                        float(&x)[8] = j < 2 ? x0 : x1;
+                        const int o = 4 * (j & 1);
+                        const float r0 = x[o] * w.x - x[o + 1] * w.y, r1 = x[o + 2] * w.z - x[o + 3] * w.w;
+                        x[o + 1] = x[o + 1] * w.x + x[o] * w.y;
+                        x[o + 3] = x[o + 3] * w.z + x[o + 2] * w.w;
+                        x[o] = r0, x[o + 2] = r1;
+                    } else {
+                        const float r0 = x0[2 * j] * w.x - x1[2 * j] * w.y;
+                        const float r1 = x0[2 * j + 1] * w.z - x1[2 * j + 1] * w.w;
+                        x1[2 * j] = x1[2 * j] * w.x + x0[2 * j] * w.y;
+                        x1[2 * j + 1] = x1[2 * j + 1] * w.z + x0[2 * j + 1] * w.w;
+                        x0[2 * j] = r0, x0[2 * j + 1] = r1;
+                    }
                 }
+                if (!kCodes) v0[k] = pack8<T>(x0), v1[k] = pack8<T>(x1);
+            }
+            const int d0 = kRows == kRopeV ? 2 * u : c0, d1 = kRows == kRopeV ? 2 * u + 1 : c1;
+            if (kRows == kRopeQ) {
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) + (t0 + tk) * p.q_out_stride + h * D);
+                dst[d0] = v0[k], dst[d1] = v1[k];
+            } else if (kCodes) {
+                const float sc = kRows == kRopeK ? p.k_scale : p.v_scale;
+                uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(kRows == kRopeK ? p.k_cache : p.v_cache) +
+                                                      (slot * heads + h) * D);
+                const uint2 q0 = quantise8(x0, sc), q1 = quantise8(x1, sc);
+                // two neighbouring chunks go out as one
+                if (kRows == kRopeV || kInterleaved || !rot)
+                    *reinterpret_cast<uint4*>(dst + d0) = make_uint4(q0.x, q0.y, q1.x, q1.y);
+                else
+                    dst[d0] = q0, dst[d1] = q1;
             } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 e = a[j];
-                    const float r = x0[j] * e.x - x1[j] * e.y;
-                    x1[j] = x1[j] * e.x + x0[j] * e.y;
-                    x0[j] = r;
-                }
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(kRows == kRopeK ? p.k_cache : p.v_cache) +
+                                                      (slot * heads + h) * D);
+                dst[d0] = v0[k], dst[d1] = v1[k];
             }
         }
-        if (rot && (is_q || !kFp8)) v0 = pack8<T>(x0), v1 = pack8<T>(x1);
-        if (is_q) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) + t * p.q_out_stride + h * D);
-            dst[c0] = v0, dst[c1] = v1;
-        } else {
-            const int64_t row = slot * hkv + h;
-            void* cache = is_v ? p.v_cache : p.k_cache;
-            if (kFp8) {
-                const float sc = is_v ? p.v_scale : p.k_scale;
-                uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * D);
-                dst[c0] = quantise8(x0, sc), dst[c1] = quantise8(x1, sc);
-            } else {
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(cache) + row * D);
-                dst[c0] = v0, dst[c1] = v1;
-            }
-        }
+    };
+    using Q = std::integral_constant<int, kRopeQ>;
+    using K = std::integral_constant<int, kRopeK>;
+    using V = std::integral_constant<int, kRopeV>;
+    load(Q(), first);
+    const int pairs = p.rotary_dim / 2;
+    for (int i = tid; i < tokens * pairs; i += kRopeThreads) {
+        const int tk = i / pairs, j = i - tk * pairs;
+        cs[tk][j] = rope_cos_sin(rope_turns(p.inv_freq[j]), p.positions[t0 + tk], p.factor);
     }
+    if (tid < tokens) {
+        const int64_t slot = p.slots[t0 + tid];
+        slot_s[tid] = slot < p.num_slots ? slot : -1;
+        if (slot >= p.num_slots) flag_error(p.err, PA_DEVERR_BAD_SLOT);
+    }
+    __syncthreads();
+    store(Q(), first);
+    for (int at = first + kRopeBatch * kHeads; at < tokens * p.num_q_heads; at += kRopeBatch * kHeads) {
+        load(Q(), at);
+        store(Q(), at);
+    }
+    for (int at = first; at < tokens * p.num_kv_heads; at += kRopeBatch * kHeads) {
+        load(K(), at);
+        store(K(), at);
+        load(V(), at);
+        store(V(), at);
+    }
+}
+
+// A token to a CTA while that leaves no SM without one of its eight, else
+// four (cos and sin of 64 pairs each are then one per thread).
+template <typename T, int D, bool kFp8, bool kInterleaved>
+cudaError_t launch_rope_i(const RopeParams& p, cudaStream_t stream) {
+    if (p.num_tokens < 4 * 8 * 152)
+        return launch_with_pdl(rope_and_cache_kernel<T, D, kFp8, kInterleaved, 1>, dim3((unsigned)p.num_tokens),
+                               dim3(kRopeThreads), 0, stream, p);
+    return launch_with_pdl(rope_and_cache_kernel<T, D, kFp8, kInterleaved, 4>,
+                           dim3((unsigned)((p.num_tokens + 3) / 4)), dim3(kRopeThreads), 0, stream, p);
 }
 
 template <typename T, int D, bool kFp8>
 cudaError_t launch_rope_t(bool interleaved, const RopeParams& p, cudaStream_t stream) {
-    const dim3 grid((unsigned)p.num_tokens), threads(kRopeThreads);
-    if (interleaved)
-        return launch_with_pdl(rope_and_cache_kernel<T, D, kFp8, true>, grid, threads, 0, stream, p);
-    return launch_with_pdl(rope_and_cache_kernel<T, D, kFp8, false>, grid, threads, 0, stream, p);
+    return interleaved ? launch_rope_i<T, D, kFp8, true>(p, stream)
+                       : launch_rope_i<T, D, kFp8, false>(p, stream);
 }
 
 cudaError_t launch_rope_and_cache(int dtype, int head_dim, bool fp8, bool interleaved,

@@ -8,6 +8,7 @@ every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -799,10 +800,19 @@ def rope_and_cache(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     return q_out
 
 
-def weights_partition(num_seqs: int, num_kv_heads: int, max_context_len: int,
-                      block_size: int = 16) -> int:
-    """Partition size of ``decode_weights``."""
-    return DEFAULT_PARTITION
+@functools.lru_cache(maxsize=1024)
+def weights_partition(num_seqs: int, num_kv_heads: int, max_context_len: int, index: int) -> int:
+    """Partition size of ``decode_weights`` on device ``index``: the rule of
+    ``choose_partition`` with every context at ``max_context_len``, in whole
+    numbers (asked per call)."""
+    sms = torch.cuda.get_device_properties(index).multi_processor_count
+    pairs = max(1, num_seqs * num_kv_heads)
+    if max_context_len <= 512:
+        return 512
+    if 2 * pairs >= sms * CTAS_PER_SM:
+        return 1024
+    pieces = max(1, (24 * sms) // 5 // pairs)              # per context
+    return 512 * -(-max_context_len // (512 * pieces))
 
 
 def _batch(block_tables: torch.Tensor, context_lens: torch.Tensor, device, index: int) -> Tuple[int, int]:
@@ -846,7 +856,7 @@ def decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
     if partition_size is None:
-        partition_size = weights_partition(B, pool[2], max_context_len, pool[1])
+        partition_size = weights_partition(B, pool[2], max_context_len, idx)
     ref = ctypes.byref(_pool_shape(B, q.shape[1], pool, blocks, qdt))
     name = "pa_decode_weights_fp8" if fp8 else "pa_decode_weights"
     ws, nbytes = _workspace(workspace, lib.pa_decode_weights_workspace_size(

@@ -81,14 +81,14 @@ def decode_reference(x: Batch, weights=None):
     Bounds: a score carries an error of at most 2^-20 (2 + A) in log2 units,
     A = log2(e) scale max_i sum_d |q_d K_id| (fp32 accumulation of D products,
     the scale and the exponential), so a weight is off by that share; out by
-    that share and by P's rounding (half a step of fp16, 2^-14 for bf16's
-    pair) of sum p |v|, and by its own rounding."""
+    that share and by P's rounding (2^-14 for the pair of a 16-bit cache, half
+    a step of fp16 for an E4M3 one) of sum p |v|, and by its own rounding."""
     out = torch.zeros(x.num_seqs, x.hq, x.d, dtype=torch.float64)
     ob = torch.zeros_like(out)
     w = torch.zeros(x.num_seqs, x.hkv, x.tokens, dtype=torch.float64)
     wb = torch.zeros_like(w)
     g = x.hq // x.hkv
-    p_step = half_step(torch.float16) if (x.dtype == torch.float16 or x.fp8) else 2.0 ** -14
+    p_step = half_step(torch.float16) if x.fp8 else 2.0 ** -14
     for b in range(x.num_seqs):
         n = int(x.lens[b])
         if n == 0:

@@ -104,6 +104,20 @@ def test_long_contexts(dev):
     positions = torch.zeros(3, 1, x.tokens, dtype=torch.int32)
     run(dev, x, x.state(), positions, None, x.lens.clone(), 30000, sinks=4, recent=1000)
     run(dev, x, x.state(), positions, None, x.lens.clone(), 512, sinks=4, recent=128)
+    # known positions and few moves on the same tables
+    positions, known, seen = earlier_cut(x, 20)
+    run(dev, x, x.state(), positions, known, seen, 39990, sinks=4, recent=128)
+
+
+@pytest.mark.parametrize("n,budget", [(2048, 1024), (2049, 2048), (8192, 100), (8193, 8192), (16385, 8000),
+                                      (70000, 69000), (140001, 1000)])
+def test_slices_of_every_cluster_size(dev, n, budget):
+    """Contexts around the sizes at which the threads, the cluster and the
+    passes over a slice change; equal weights put ties across the slices."""
+    x = Batch([n, n // 2 + 1], 1, 1, 64, 16, F16, seed=n, stale=False, slack_width=0)
+    w = torch.floor(torch.rand(2, 1, x.tokens, generator=x.gen) * 5)
+    positions = torch.zeros(2, 1, x.tokens, dtype=torch.int32)
+    run(dev, x, w, positions, None, x.lens.clone(), budget, sinks=2, recent=60)
 
 
 def test_bad_tables_and_lengths_are_bounded(dev):
