@@ -63,11 +63,15 @@ __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Word at the same shared-memory address in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t cluster_word(const uint32_t* local, int rank) {
-    uint32_t addr, v;
+// Four words at the same shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ uint4 cluster_words(const uint32_t* local, int rank) {
+    uint32_t addr;
+    uint4 v;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(local)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
@@ -151,11 +155,12 @@ template <int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
     evict_select_kernel(const __grid_constant__ EvictParams p) {
     constexpr int kWarps = kThreads / 32, kChunk = kThreads * kEvictKeys;
-    __shared__ uint32_t hist[3][kEvictBins];
+    __shared__ __align__(16) uint32_t hist[3][kEvictBins];
     __shared__ uint32_t sums[32];
-    __shared__ uint32_t counts[4];              // below left: above T, equal to T; past left: the same
-    __shared__ uint32_t digit_s, above_s;
+    __shared__ __align__(16) uint32_t counts[4];    // below left: above T, equal to T; past left: the same
+    __shared__ uint32_t digit_s, above_s, inside_s;
     __shared__ uint32_t line[2][kEvictKeys * kWarps];
+    __shared__ int32_t own_gaps[kEvictOwnMoves], own_movers[kEvictOwnMoves];
     __shared__ MoveRows rows;
     const int C = p.cluster, rank = blockIdx.x % C;
     const int g = blockIdx.x / C, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -218,28 +223,51 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
         // bins from the top one down, kEvictBins / kThreads to a thread
         constexpr int kPer = kEvictBins / kThreads;
         uint32_t mine[kPer], sum = 0;
+        {
+            // they end at bin kEvictBins - 1 - kPer * tid; 2 or 8 words, read whole
+            const uint32_t* low = &hist[pass][kEvictBins - kPer * (tid + 1)];
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const uint32_t* bin = &hist[pass][kEvictBins - 1 - (kPer * tid + k)];
-            mine[k] = 0;
-            if (C == 1) mine[k] = *bin;
-            else for (int r = 0; r < C; ++r) mine[k] += cluster_word(bin, r);
-            sum += mine[k];
+            for (int k = 0; k < kPer; ++k) mine[k] = 0;
+            for (int r = 0; r < C; ++r) {
+                if constexpr (kPer % 4 == 0) {
+#pragma unroll
+                    for (int k = 0; k < kPer; k += 4) {
+                        const uint4 v = C == 1 ? *reinterpret_cast<const uint4*>(low + k) : cluster_words(low + k, r);
+                        mine[kPer - 1 - k] += v.x, mine[kPer - 2 - k] += v.y;
+                        mine[kPer - 3 - k] += v.z, mine[kPer - 4 - k] += v.w;
+                    }
+                } else {
+                    static_assert(kPer == 2, "a pair of bins, from the half of a quad");
+                    uint2 v;
+                    if (C == 1) {
+                        v = *reinterpret_cast<const uint2*>(low);
+                    } else {
+                        const uint4 q = cluster_words(&hist[pass][(kEvictBins - kPer * (tid + 1)) & ~3], r);
+                        v = (tid & 1) ? make_uint2(q.x, q.y) : make_uint2(q.z, q.w);
+                    }
+                    mine[0] += v.y, mine[1] += v.x;
+                }
+            }
         }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) sum += mine[k];
         uint32_t total;
         uint32_t before = block_prefix<kThreads>(sum, sums, &total);
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             if (before < want && before + mine[k] >= want)
-                digit_s = kEvictBins - 1 - (kPer * tid + k), above_s = before;
+                digit_s = kEvictBins - 1 - (kPer * tid + k), above_s = before, inside_s = mine[k];
             before += mine[k];
         }
         __syncthreads();
         T |= digit_s << shift;
         want -= above_s;
     }
-    // counts of the slice, then of the slices before it
-    {
+    // where every equal stays, none needs its rank among them
+    const bool ranked = inside_s != want;
+    // the slices before this one: their equals, gaps and movers
+    uint32_t equal = 0, n_gaps = 0, n_movers = 0, moves = 0;
+    if (C > 1) {
         uint32_t n[4] = {0, 0, 0, 0};
         for (int c0 = lo; c0 < hi; c0 += kChunk) {
             if (!once) load(c0);
@@ -257,52 +285,50 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
             const uint32_t t = __reduce_add_sync(0xffffffffu, n[q]);
             if (lane == 0) atomicAdd(&counts[q], t);
         }
+        cluster_barrier();
+        uint32_t seen_equal = 0;
+        for (int r = 0; r < C; ++r) {
+            const uint4 c = cluster_words(counts, r);
+            const int r0 = min(r * slice, s.L), r1 = min(r0 + slice, s.L);
+            const uint32_t below = max(0, min(r1, s.left) - r0);
+            // equals stay from the lowest index on
+            const uint32_t free = want > seen_equal ? want - seen_equal : 0u;
+            const uint32_t eq_below = min(free, c.y), eq_past = min(free - eq_below, c.w);
+            if (r < rank) equal += c.y + c.w, n_gaps += below - c.x - eq_below, n_movers += c.z + eq_past;
+            moves += below - c.x - eq_below;
+            seen_equal += c.y + c.w;
+        }
     }
-    barrier();
-    uint32_t equal = 0, n_gaps = 0, n_movers = 0, moves = 0;
-    for (int r = 0; r < C; ++r) {
-        uint32_t n[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) n[q] = C == 1 ? counts[q] : cluster_word(&counts[q], r);
-        const int r0 = min(r * slice, s.L), r1 = min(r0 + slice, s.L);
-        const uint32_t below = max(0, min(r1, s.left) - r0);
-        // equals stay from the lowest index on
-        const uint32_t free = want > equal ? want - equal : 0u;
-        const uint32_t eq_below = min(free, n[1]), eq_past = min(free - eq_below, n[3]);
-        if (r == rank) n_gaps = moves, n_movers = 0;
-        moves += below - n[0] - eq_below;
-        line[0][r] = n[2] + eq_past;            // every thread writes the same
-        equal += n[1] + n[3];
-    }
-    for (int r = 0; r < rank; ++r) n_movers += line[0][r];
-    equal = 0;
-    for (int r = 0; r < rank; ++r)
-        equal += (C == 1 ? counts[1] : cluster_word(&counts[1], r)) + (C == 1 ? counts[3] : cluster_word(&counts[3], r));
-    __syncthreads();                            // line is used again
     // gaps below left and movers from left on, in order
     int32_t* gaps = p.moves + pair * 2 * p.moves_stride;
     int32_t* movers = gaps + p.moves_stride;
     for (int c0 = lo; c0 < hi; c0 += kChunk) {
         if (!once) load(c0);
-        // rank among the equals: rows of kThreads tokens, warps, lanes
+        if (c0 > lo) __syncthreads();           // the previous chunk's reads of line
+        uint32_t total, at;
+        if (ranked) {
+            // rank among the equals: rows of kThreads tokens, warps, lanes
 #pragma unroll
-        for (int e = 0; e < kEvictKeys; ++e) {
-            const uint32_t eq = __ballot_sync(0xffffffffu, c0 + e * kThreads + tid < hi && key[e] == T);
-            if (lane == 0) line[0][e * kWarps + warp] = __popc(eq);
+            for (int e = 0; e < kEvictKeys; ++e) {
+                const uint32_t eq = __ballot_sync(0xffffffffu, c0 + e * kThreads + tid < hi && key[e] == T);
+                if (lane == 0) line[0][e * kWarps + warp] = __popc(eq);
+            }
+            __syncthreads();
+            at = block_prefix<kThreads>(tid < kEvictKeys * kWarps ? line[0][tid] : 0u, sums, &total);
+            if (tid < kEvictKeys * kWarps) line[0][tid] = equal + at;
+            equal += total;
+            __syncthreads();
         }
-        __syncthreads();
-        uint32_t total;
-        uint32_t at = block_prefix<kThreads>(tid < kEvictKeys * kWarps ? line[0][tid] : 0u, sums, &total);
-        if (tid < kEvictKeys * kWarps) line[0][tid] = at;
-        __syncthreads();
         uint32_t gap_bits = 0, mover_bits = 0, gap_mask[kEvictKeys], mover_mask[kEvictKeys];
 #pragma unroll
         for (int e = 0; e < kEvictKeys; ++e) {
             const int i = c0 + e * kThreads + tid;
             const bool in = i < hi, is_eq = in && key[e] == T;
-            const uint32_t eq = __ballot_sync(0xffffffffu, is_eq);
-            const uint32_t nth = equal + line[0][e * kWarps + warp] + __popc(eq & ((1u << lane) - 1u));
-            const bool keep = in && (key[e] > T || (is_eq && nth < want));
+            bool keep = in && key[e] >= T;
+            if (ranked) {
+                const uint32_t eq = __ballot_sync(0xffffffffu, is_eq);
+                if (is_eq) keep = line[0][e * kWarps + warp] + __popc(eq & ((1u << lane) - 1u)) < want;
+            }
             const bool gap = in && i < s.left && !keep, mover = keep && i >= s.left;
             gap_mask[e] = __ballot_sync(0xffffffffu, gap);
             mover_mask[e] = __ballot_sync(0xffffffffu, mover);
@@ -314,7 +340,6 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
                 if (p.positions_out != p.positions || i >= s.known) po[i] = evict_position(s, pos, i);
             }
         }
-        equal += total;
         __syncthreads();
         at = block_prefix<kThreads>(tid < kEvictKeys * kWarps ? line[1][tid] : 0u, sums, &total);
         if (tid < kEvictKeys * kWarps) line[1][tid] = at;
@@ -323,18 +348,29 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
         for (int e = 0; e < kEvictKeys; ++e) {
             const int i = c0 + e * kThreads + tid;
             const uint32_t before = line[1][e * kWarps + warp];
-            if ((gap_bits >> e) & 1u) gaps[n_gaps + (before & 0xffffu) + __popc(gap_mask[e] & ((1u << lane) - 1u))] = i;
-            if ((mover_bits >> e) & 1u) movers[n_movers + (before >> 16) + __popc(mover_mask[e] & ((1u << lane) - 1u))] = i;
+            if ((gap_bits >> e) & 1u) {
+                const int n = n_gaps + (before & 0xffffu) + __popc(gap_mask[e] & ((1u << lane) - 1u));
+                gaps[n] = i;
+                if (n < kEvictOwnMoves) own_gaps[n] = i;
+            }
+            if ((mover_bits >> e) & 1u) {
+                const int n = n_movers + (before >> 16) + __popc(mover_mask[e] & ((1u << lane) - 1u));
+                movers[n] = i;
+                if (n < kEvictOwnMoves) own_movers[n] = i;
+            }
         }
         n_gaps += total & 0xffffu, n_movers += total >> 16;
     }
+    if (C == 1) moves = n_gaps;
     const bool own = moves <= (uint32_t)(kEvictOwnMoves * C);
     if (rank == 0 && tid == 0) p.num_moves[pair] = own ? 0 : moves;
     // the lists are complete; also no CTA leaves while another reads its shared memory
     barrier();
     if (!own) return;
     const int per = ((int)moves + C - 1) / C, n0 = min(rank * per, (int)moves);
-    move_rows<kThreads>(p, s, b, g, pair, gaps, movers, n0, min(n0 + per, (int)moves), rows);
+    // a CTA of its own has the lists in shared memory
+    move_rows<kThreads>(p, s, b, g, pair, C == 1 ? own_gaps : gaps, C == 1 ? own_movers : movers, n0,
+                        min(n0 + per, (int)moves), rows);
 }
 
 constexpr int kMoveThreads = 256;

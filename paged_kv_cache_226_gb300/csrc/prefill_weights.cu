@@ -24,12 +24,14 @@
 // resident tiles (operand A) and streams others (operand B) past both, so
 // that a streamed tile is loaded once for two products; one persistent CTA
 // per SM walks its units, its rings running on from one unit to the next.
-// Six warps load whole tiles, one for each stage, with TMA (K through the block table in
-// 16-token boxes, Q in one box of tokens x heads per 64 dims); two warps
-// issue the MMAs, one for each resident tile, into two 128-column buffers
-// each (a single issuer spends 1,060 cycles on its waits and commits per
-// tile, twice what the product takes); and four groups of four warps take the
-// finished tiles.  Rows of Q past a sequence's chunk and K rows past its end
+// Six warps load with TMA: two for each stage of the ring that holds K tiles
+// (half of the 16-token boxes each, through the block table: a box costs its
+// warp some 120 cycles), three of them also for a stage each of the Q ring
+// (one box of tokens x heads per 64 dims).  Two warps issue the MMAs, one for
+// each resident tile (where a unit has only one, streamed tiles in turn),
+// into two 128-column buffers each: a single issuer spends 1,060 cycles on
+// its waits and commits per tile, twice what the product takes.  Four groups
+// of four warps take the finished tiles.  Rows of Q past a sequence's chunk and K rows past its end
 // may hold anything: they only reach their own lane or column, which is
 // masked.
 //
@@ -49,7 +51,7 @@ constexpr int kPwCols = 128;                   // columns: rows of a streamed ti
 constexpr int kPwBufs = 4;                     // accumulators in tensor memory
 constexpr int kPwGroups = 4;                   // epilogue groups of four warps, one per buffer
 constexpr int kPwLoadersAfter = 4 + 4 * kPwGroups;   // warps 0, 1 issue MMAs; 2, 3, 20 .. 23 load
-constexpr int kPwLoaders = 6;                  // one for each stage of the two rings
+constexpr int kPwLoaders = 6;                  // two for each stage
 constexpr int kPwThreads = (kPwLoadersAfter + kPwLoaders - 2) * 32;
 constexpr int kPwJoinThreads = 256;
 
@@ -218,7 +220,13 @@ __device__ __forceinline__ void row_stats(float& m, float& z, uint32_t tile_addr
 #pragma unroll
         for (int e = 0; e < 4; ++e) pm[e] = __uint_as_float(v[e]);
 #pragma unroll
-        for (int e = 4; e < 64; ++e) pm[e & 3] = fmaxf(pm[e & 3], __uint_as_float(v[e]));
+        for (int e = 4; e < 60; e += 8) {                 // two at a time: one instruction
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                pm[i] = fmaxf(fmaxf(pm[i], __uint_as_float(v[e + i])), __uint_as_float(v[e + 4 + i]));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pm[i] = fmaxf(pm[i], __uint_as_float(v[60 + i]));
         const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * sl;
         if (mx > m + kRescaleThresholdLog2) {         // also the first finite maximum
             z *= ex2(m - mx);
@@ -282,7 +290,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     __shared__ __align__(8) uint64_t s_full[kPwBufs], s_empty[kPwBufs];
     __shared__ uint32_t tmem_base;
     __shared__ __align__(16) float lse_s[kPwGroups][2][kPwCols];     // pass 2: [group][tile parity]
-    __shared__ float2 other[2][2][kPwRows];                          // [join parity][resident tile]
+    __shared__ float2 other2[2][2][kPwRows];                         // [join parity][resident tile]
+    __shared__ float2 other4[2][3][kPwRows];                         // [join parity][sharer]
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -291,8 +300,9 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     const int q_rows = p.tile_tokens * G;                    // rows of a query tile, <= 128
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kA; ++i) mbar_init(&a_full[i], 1), mbar_init(&a_empty[i], 1);
-        for (int i = 0; i < kB; ++i) mbar_init(&b_full[i], 1), mbar_init(&b_empty[i], 2);
+        // K stages have two loaders; either issuer may read any tile
+        for (int i = 0; i < kA; ++i) mbar_init(&a_full[i], kStats ? 1 : 2), mbar_init(&a_empty[i], 2);
+        for (int i = 0; i < kB; ++i) mbar_init(&b_full[i], kStats ? 2 : 1), mbar_init(&b_empty[i], 2);
         for (int i = 0; i < kPwBufs; ++i) mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4);
         fence_barrier_init();
     }
@@ -312,13 +322,13 @@ __global__ void __launch_bounds__(kPwThreads, 1)
 
     if (warp == 2 || warp == 3 || warp >= kPwLoadersAfter) {
         // ------------------------------------------------------------------
-        // loaders, one for each stage of the two rings; all lanes run along,
-        // one issues.  A stage has one loader so that every wait follows the
-        // wait for the stage's previous phase: a parity says no more than
-        // that, and a loader that had not waited for that phase would take
-        // the one before it for its own.
+        // loaders; all lanes run along, one issues.  A loader keeps to its
+        // stages so that every wait follows its wait for the stage's previous
+        // phase: a parity says no more than that, and a loader that had not
+        // waited for that phase would take the one before it for its own.
         // ------------------------------------------------------------------
         const int who = warp < 4 ? warp - 2 : warp - kPwLoadersAfter + 2;
+        const int k_stage = who % 3, part = who / 3;
         if (lane == 0) prefetch_tensor_map(&tmap_q), prefetch_tensor_map(&tmap_k);
         // waits for stage n % stages to be free
         auto open = [&](uint64_t* empty, int stages, int n) -> bool {
@@ -335,14 +345,16 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         auto load_k = [&](uint8_t* dst, uint64_t* full, uint64_t* empty, int stages, int n,
                           const PwSeq& s, const PwUnit& U, int kt, int blk) -> bool {
             if (!open(empty, stages, n)) return false;
-            const int nbox = min(8, (s.L - kt * kPwCols + 15) / 16);
+            // boxes part, part + 2, ... of the tile's
+            const int nbox = min(8, (s.L - kt * kPwCols + 15) / 16), own = (nbox - part + 1) / 2;
             uint64_t* bar = &full[n % stages];
-            if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(nbox * Lay::kHalves * kBox16Bytes));
+            if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(own * Lay::kHalves * kBox16Bytes));
             __syncwarp();
             dst += (n % stages) * Lay::kTile;
             const int sub_mask = p.block_size - 1;               // 16 or 32
 #pragma unroll
-            for (int box = 0; box < 8; ++box) {
+            for (int i = 0; i < 4; ++i) {
+                const int box = 2 * i + part;
                 if (box >= nbox) break;
                 const int pblk = __shfl_sync(0xffffffffu, blk, (kt & 3) * 8 + box);
                 if (elect_one()) {
@@ -376,7 +388,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         PwUnit U;
         int na = 0, nb = 0, at_b = -1, at_g = -1, at_qt = -1;
         bool ok = true;
-        static_assert(kA + kB == kPwLoaders, "a loader for each stage");
+        static_assert(kA == 3 && kB == 3 && kPwLoaders == 6, "two loaders for each K stage");
         while (ok && walk.next(p, U)) {
             // block ids of the current four key tiles and of the next four
             int quad = -2, blk = 0, blk_next = 0;
@@ -392,7 +404,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                 if (first >= last) continue;
                 for (int j = 0; ok && j < walk.residents(a); ++j) {
                     if (!kStats) to_tile(2 * a + j);
-                    if (na % kA == who)
+                    if (na % kA == (kStats ? who : k_stage))
                         ok = kStats ? load_q(a_ring, a_full, a_empty, kA, na, walk.s, U, 2 * a + j)
                                     : load_k(a_ring, a_full, a_empty, kA, na, walk.s, U, 2 * a + j, blk);
                     ++na;
@@ -404,7 +416,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                         if (U.b == at_b && U.g == at_g && i == at_qt) continue;     // still there
                         at_b = U.b, at_g = U.g, at_qt = i;
                     }
-                    if (nb % kB == who - kA)
+                    if (nb % kB == (kStats ? k_stage : who))
                         ok = kStats ? load_k(b_ring, b_full, b_empty, kB, nb, walk.s, U, i, blk)
                                     : load_q(b_ring, b_full, b_empty, kB, nb, walk.s, U, i);
                     ++nb;
@@ -433,10 +445,9 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                 walk.streamed(p, U, a, first, last);
                 if (first >= last) continue;
                 const int residents = walk.residents(a);
-                const bool active = warp < residents;
-                const int stage = (na + warp) % kA;
-                // both warps wait for both tiles: no phase of a stage is passed over
+                // both warps wait for every tile: no phase of a stage is passed over
                 for (int j = 0; j < residents; ++j) wait(&a_full[(na + j) % kA], (na + j) / kA);
+                const int stage = (na + (residents == 2 ? warp : 0)) % kA;
                 for (int i = first; ok && i < last; ++i, ++tiles) {
                     if (kStats || U.b != at_b || U.g != at_g || i != at_qt) {
                         // the previous streamed tile is free once this warp's products are done
@@ -444,12 +455,12 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                         __syncwarp();
                         ++nb;
                         at_b = U.b, at_g = U.g, at_qt = i;
-                        // also where this warp has no tile to multiply: it may not run ahead
                         wait(&b_full[nb % kB], nb / kB);
                     }
-                    if (!active) continue;
-                    // the group of (resident, parity of the streamed tile) owns the buffer
-                    const int odd = tiles & 1, buf = warp + 2 * odd;
+                    // two resident tiles: one each, buffers by the streamed tile's parity;
+                    // one: streamed tiles in turn, buffers by the parity of the pair
+                    if (residents == 1 && (tiles & 1) != warp) continue;
+                    const int odd = (residents == 2 ? tiles : tiles >> 1) & 1, buf = warp + 2 * odd;
                     const int n = odd ? used[1]++ : used[0]++;
                     if (n > 0) wait(&s_empty[buf], n - 1);
                     if (!ok) break;
@@ -468,19 +479,21 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (ok && active && elect_one()) mma_commit(&a_empty[stage]);
-                __syncwarp();
+                for (int j = 0; j < residents; ++j) {
+                    if (ok && elect_one()) mma_commit(&a_empty[(na + j) % kA]);
+                    __syncwarp();
+                }
                 na += residents;
             }
         }
         if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
     } else {
         // ------------------------------------------------------------------
-        // epilogue: group w takes the products of resident tile w % 2 with
-        // the streamed tiles of parity w / 2 (buffer w); this thread owns
-        // lane r of every tile
+        // epilogue: group w owns buffer w.  Of two resident tiles it takes
+        // tile w % 2 with the streamed tiles of parity w / 2, of one every
+        // fourth streamed tile.  This thread owns lane r of every tile.
         // ------------------------------------------------------------------
-        const int group = (warp >> 2) - 1, res = group & 1, parity = group >> 1;
+        const int group = (warp >> 2) - 1;
         const int r = (warp & 3) * 32 + lane;
         const uint32_t tile_addr = tmem + kPwCols * group + ((uint32_t)((warp & 3) * 32) << 16);
         const float sl = p.scale_log2;
@@ -497,7 +510,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         };
         PwWalk<kStats> walk;
         PwUnit U;
-        int tiles = 0, mine = 0, joins = 0;
+        int tiles = 0, mine = 0, joins2 = 0, joins4 = 0, at_qt = -1, lse_at = 0;
+        size_t at_pair = 0;
         while (walk.next(p, U)) {
             const PwSeq& s = walk.s;
             const size_t pair = (size_t)U.b * p.num_kv_heads + U.g;
@@ -506,19 +520,25 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                 walk.streamed(p, U, a, first, last);
                 const int steps = max(0, last - first);
                 if (kStats && steps == 0) continue;
-                const int skip = (parity - tiles) & 1;       // to the group's first streamed tile
+                const bool two = walk.residents(a) == 2;
+                // the group's streamed tiles: first + skip, every `every`-th
+                const int every = two ? 2 : 4, skip = ((two ? group >> 1 : group) - tiles) & (every - 1);
                 tiles += steps;
-                if (res >= walk.residents(a)) continue;
-                const int tile = 2 * a + res, key = tile * kPwCols + r;
-                // one streamed tile is its group's alone; two groups are joined by the first
-                const bool writer = steps == 1 ? skip == 0 : parity == 0;
+                const int tile = 2 * a + (two ? group & 1 : 0), key = tile * kPwCols + r;
+                // one streamed tile is its group's alone; else the sharers are joined by the first
+                const int share = two ? group >> 1 : group;
+                const bool writer = steps == 1 ? skip == 0 : share == 0;
                 float before = 0.f;
                 if (!kStats && writer && p.query_chunks == 1 && p.weights && key < s.L - s.C)
                     before = p.weights[pair * p.weights_stride + key];
                 float m = -INFINITY, z = 0.f;
+                auto join = [&](float2 o) {
+                    if (kStats) join_stats(m, z, o);
+                    else z += o.y;
+                };
                 if constexpr (kStats) {
                     const int pos = min(s.L - s.counted + tile * p.tile_tokens + r / G, s.L - 1);
-                    for (int kt = first + skip; kt < last; kt += 2) {
+                    for (int kt = first + skip; kt < last; kt += every) {
                         wait(mine++);
                         const int visible = pos - kt * kPwCols;           // keys 0 .. visible of the tile
                         if (__all_sync(0xffffffffu, visible >= kPwCols - 1))
@@ -527,12 +547,16 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                             row_stats<true>(m, z, tile_addr, sl, sl2, visible, release);
                     }
                 } else {
-                    for (int qt = first + skip; qt < last; qt += 2) {
-                        const float lse = p.lse[(pair * p.max_query_tiles + qt) * kPwCols + r];
-                        float* ls = lse_s[group][mine & 1];
+                    for (int qt = first + skip; qt < last; qt += every) {
+                        // the rows' lse, kept while the query tile stays the same
+                        if (pair != at_pair || qt != at_qt) {
+                            const float lse = p.lse[(pair * p.max_query_tiles + qt) * kPwCols + r];
+                            at_pair = pair, at_qt = qt, ++lse_at;
+                            lse_s[group][lse_at & 1][r] = -lse;
+                            asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+                        }
+                        const float* ls = lse_s[group][lse_at & 1];
                         wait(mine++);
-                        ls[r] = -lse;
-                        asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
                         const int tokens = min(p.tile_tokens, s.counted - qt * p.tile_tokens);
                         // columns that see this key: from `lo` on, up to the chunk's end
                         const int lo = (key - (s.L - s.counted + qt * p.tile_tokens)) * G, hi = tokens * G;
@@ -543,14 +567,23 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                     }
                 }
                 if (steps > 1) {
-                    if (parity == 1) other[joins & 1][res][r] = make_float2(m, z);
-                    asm volatile("bar.sync %0, 256;" ::"r"(5 + res) : "memory");
-                    if (parity == 0) {
-                        const float2 o = other[joins & 1][res][r];
-                        if (kStats) join_stats(m, z, o);
-                        else z += o.y;
+                    // sharers of a tile: groups w and w + 2 of two resident tiles, all four of
+                    // one.  Each kind has its two buffers: what a group writes was read before
+                    // the barrier of that kind that it passed last.
+                    if (two) {
+                        float2* o = other2[joins2++ & 1][group & 1];
+                        if (share > 0) o[r] = make_float2(m, z);
+                        asm volatile("bar.sync %0, 256;" ::"r"(5 + (group & 1)) : "memory");
+                        if (share == 0) join(o[r]);
+                    } else {
+                        float2(*o)[kPwRows] = other4[joins4++ & 1];
+                        if (share > 0) o[share - 1][r] = make_float2(m, z);
+                        asm volatile("bar.sync 7, 512;" ::: "memory");
+                        if (share == 0) {
+#pragma unroll
+                            for (int i = 0; i < 3; ++i) join(o[i][r]);
+                        }
                     }
-                    ++joins;
                 }
                 if (!writer || failed) continue;
                 if constexpr (kStats) {
