@@ -73,6 +73,7 @@ struct PrefillWeightsParams {
     int key_chunk, key_chunks;     // key tiles per unit of pass 1, units of the longest row
     int query_chunk, query_chunks; // query tiles per unit of pass 2, units of a column
     int key_run;                   // pairs of key tiles per unit of pass 2
+    bool join_early;               // pass 2 joins the chunks of pass 1 itself
     float* lse;                    // [B][Hkv][max_query_tiles][128], log2 units
     float2* stats;                 // [key_chunks] x the same: maximum and sum
     float* columns;                // [query_chunks][B][Hkv][columns_stride]

@@ -200,6 +200,28 @@ __device__ __forceinline__ void join_stats(float& m, float& z, float2 o) {
     m = n;
 }
 
+// lse of row r of query tile qt from the tile's chunks (eight loads in
+// flight); +inf past the sequence's queries.
+__device__ __forceinline__ float joined_lse(const PrefillWeightsParams& p, const PwSeq& s, size_t pair,
+                                            int qt, int r) {
+    const size_t rows = (size_t)p.num_seqs * p.num_kv_heads * p.max_query_tiles * kPwRows;
+    const float2* src = p.stats + (pair * p.max_query_tiles + qt) * kPwRows + r;
+    // chunks of this tile: up to the last key tile that the pair it was resident in reaches
+    const int seen = pw_key_tiles(p, s, min(qt | 1, s.n_qt - 1));
+    const int chunks = (seen + p.key_chunk - 1) / p.key_chunk;
+    float m = -INFINITY, z = 0.f;
+    for (int c0 = 0; c0 < chunks; c0 += 8) {
+        float2 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = c0 + i < chunks ? src[(c0 + i) * rows] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) join_stats(m, z, v[i]);
+    }
+    const int tokens = min(p.tile_tokens, s.counted - qt * p.tile_tokens);
+    return r < tokens * p.group ? m + log2f(z) : INFINITY;
+}
+
 // Pass 1: folds a tile's row (keys up to `visible` with kMask) into (m, z).
 template <bool kMask, typename Release>
 __device__ __forceinline__ void row_stats(float& m, float& z, uint32_t tile_addr, float sl,
@@ -510,8 +532,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         };
         PwWalk<kStats> walk;
         PwUnit U;
-        int tiles = 0, mine = 0, joins2 = 0, joins4 = 0, at_qt = -1, lse_at = 0;
-        size_t at_pair = 0;
+        int tiles = 0, mine = 0, joins2 = 0, joins4 = 0, at_pair = -1, at_qt = -1, lse_at = 0;
         while (walk.next(p, U)) {
             const PwSeq& s = walk.s;
             const size_t pair = (size_t)U.b * p.num_kv_heads + U.g;
@@ -548,15 +569,20 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                     }
                 } else {
                     for (int qt = first + skip; qt < last; qt += every) {
-                        // the rows' lse, kept while the query tile stays the same
-                        if (pair != at_pair || qt != at_qt) {
-                            const float lse = p.lse[(pair * p.max_query_tiles + qt) * kPwCols + r];
-                            at_pair = pair, at_qt = qt, ++lse_at;
+                        // the rows' lse, requested before the wait for the tile and kept
+                        // while the query tile stays the same
+                        const bool fresh = (int)pair != at_pair || qt != at_qt;
+                        float lse = 0.f;
+                        if (fresh)
+                            lse = p.join_early ? joined_lse(p, s, pair, qt, r)
+                                               : p.lse[(pair * p.max_query_tiles + qt) * kPwCols + r];
+                        wait(mine++);
+                        if (fresh) {
+                            at_pair = (int)pair, at_qt = qt, ++lse_at;
                             lse_s[group][lse_at & 1][r] = -lse;
                             asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
                         }
                         const float* ls = lse_s[group][lse_at & 1];
-                        wait(mine++);
                         const int tokens = min(p.tile_tokens, s.counted - qt * p.tile_tokens);
                         // columns that see this key: from `lo` on, up to the chunk's end
                         const int lo = (key - (s.L - s.counted + qt * p.tile_tokens)) * G, hi = tokens * G;
@@ -620,22 +646,8 @@ __global__ void __launch_bounds__(kPwRows)
     PwSeq s;
     pw_sequence(p, b, false, s);
     if (qt >= s.n_qt) return;
-    const size_t rows = (size_t)p.num_seqs * p.num_kv_heads * p.max_query_tiles * kPwRows;
-    const size_t at = (((size_t)b * p.num_kv_heads + g) * p.max_query_tiles + qt) * kPwRows + r;
-    // chunks of this tile: up to the last key tile that the pair it was resident in reaches
-    const int seen = pw_key_tiles(p, s, min(qt | 1, s.n_qt - 1));
-    const int chunks = (seen + p.key_chunk - 1) / p.key_chunk;
-    float m = -INFINITY, z = 0.f;
-    for (int c0 = 0; c0 < chunks; c0 += 8) {                 // eight loads in flight
-        float2 v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = c0 + i < chunks ? p.stats[(c0 + i) * rows + at] : make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) join_stats(m, z, v[i]);
-    }
-    const int tokens = min(p.tile_tokens, s.counted - qt * p.tile_tokens);
-    p.lse[at] = r < tokens * p.group ? m + log2f(z) : INFINITY;
+    const size_t pair = (size_t)b * p.num_kv_heads + g;
+    p.lse[(pair * p.max_query_tiles + qt) * kPwRows + r] = joined_lse(p, s, pair, qt, r);
 }
 
 // weights from the column sums of the query chunks.
@@ -665,17 +677,19 @@ size_t prefill_weights_plan(PrefillWeightsParams& p, void* workspace) {
     const int64_t key_tiles = ((int64_t)p.max_context + kPwCols - 1) / kPwCols;
     const int64_t pairs = (int64_t)p.num_seqs * p.num_kv_heads;
     // Units of some sixteenth of an SM's share (the batch taken at its
-    // bounds): pass 1 in chunks of 4 to 64 key tiles, pass 2 in chunks of 8
+    // bounds): pass 1 in chunks of 8 to 64 key tiles, pass 2 in chunks of 8
     // to 64 query tiles; where one query tile is all there is, pass 2 takes
     // runs of key tile pairs past it instead.
     const int64_t per_sm = 152 * 16;
     const int64_t share1 = pairs * ((p.max_query_tiles + 1) / 2) * key_tiles / per_sm;
     const int64_t share2 = pairs * ((key_tiles + 1) / 2) * p.max_query_tiles / per_sm;
-    p.key_chunk = (int)std::min<int64_t>(64, std::max<int64_t>(4, share1));
+    p.key_chunk = (int)std::min<int64_t>(64, std::max<int64_t>(8, share1));
     p.key_chunks = (int)std::max<int64_t>(1, (key_tiles + p.key_chunk - 1) / p.key_chunk);
     p.query_chunk = (int)std::min<int64_t>(64, std::max<int64_t>(8, share2));
     p.query_chunks = std::max(1, (p.max_query_tiles + p.query_chunk - 1) / p.query_chunk);
-    p.key_run = p.max_query_tiles > 1 ? 1 : (int)std::min<int64_t>(8, std::max<int64_t>(1, share2));
+    p.key_run = p.max_query_tiles > 1 ? 1 : (int)std::min<int64_t>(8, std::max<int64_t>(2, share2));
+    // a lone query tile per sequence is read so seldom that pass 2 joins its chunks itself
+    p.join_early = p.max_query_tiles == 1 && p.key_chunks > 1;
     p.columns_stride = (int)(key_tiles * kPwCols);
     const size_t rows = (size_t)pairs * p.max_query_tiles * kPwRows;
     char* base = static_cast<char*>(workspace);
@@ -705,7 +719,7 @@ cudaError_t launch_prefill_weights_t(const CUtensorMap& tmk, const CUtensorMap& 
     const dim3 grid(sms), threads(kPwThreads);
     if (e == cudaSuccess && p.max_counted > 0) {
         e = launch_with_pdl(prefill_weights_kernel<T, D, true>, grid, threads, smem, stream, tmk, tmq, p);
-        if (e == cudaSuccess && p.key_chunks > 1)
+        if (e == cudaSuccess && p.key_chunks > 1 && !p.join_early)
             e = launch_with_pdl(prefill_stats_join_kernel,
                                 dim3(p.max_query_tiles, p.num_kv_heads, p.num_seqs), dim3(kPwRows), 0,
                                 stream, p);
