@@ -164,7 +164,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
     __shared__ MoveRows rows;
     const int C = p.cluster, rank = blockIdx.x % C;
     const int g = blockIdx.x / C, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < 3 * kEvictBins; i += kThreads) (&hist[0][0])[i] = 0;
+    for (int i = tid; i < 3 * kEvictBins / 4; i += kThreads)
+        reinterpret_cast<uint4*>(&hist[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
     if (tid < 4) counts[tid] = 0;
     grid_dependency_wait();
     allow_dependent_launch();
@@ -187,15 +188,20 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
         }
         return;
     }
+    const int newest = (int)max((int64_t)s.seen - p.recent, (int64_t)INT32_MIN);
     uint32_t key[kEvictKeys];
+    // rows of kThreads tokens that the chunk at c0 has
+    auto rows_of = [&](int c0) { return min(kEvictKeys, (hi - c0 + kThreads - 1) / kThreads); };
     auto load = [&](int c0) {                   // images of tokens c0 + tid, + kThreads, ...
+        const int n = rows_of(c0);
 #pragma unroll
         for (int e = 0; e < kEvictKeys; ++e) {
+            if (e >= n) break;
             const int i = c0 + e * kThreads + tid;
             key[e] = 0;
             if (i < hi) {
                 const int at = evict_position(s, pos, i);
-                key[e] = at < p.sinks || at >= s.seen - p.recent ? kProtected : weight_image(w[i]);
+                key[e] = at < p.sinks || at >= newest ? kProtected : weight_image(w[i]);
             }
         }
     };
@@ -213,8 +219,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), top = pass == 0 ? 32 : (pass == 1 ? 21 : 10);
         for (int c0 = lo; c0 < hi; c0 += kChunk) {
             if (!once) load(c0);
+            const int n = rows_of(c0);
 #pragma unroll
             for (int e = 0; e < kEvictKeys; ++e) {
+                if (e >= n) break;
                 if (c0 + e * kThreads + tid < hi && (pass == 0 || (key[e] >> top) == (T >> top)))
                     atomicAdd(&hist[pass][(key[e] >> shift) & (pass == 2 ? 1023u : 2047u)], 1u);
             }
@@ -271,8 +279,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
         uint32_t n[4] = {0, 0, 0, 0};
         for (int c0 = lo; c0 < hi; c0 += kChunk) {
             if (!once) load(c0);
+            const int held = rows_of(c0);
 #pragma unroll
             for (int e = 0; e < kEvictKeys; ++e) {
+                if (e >= held) break;
                 const int i = c0 + e * kThreads + tid;
                 const int past = i >= s.left ? 2 : 0;
                 const bool gt = i < hi && key[e] > T, eq = i < hi && key[e] == T;
@@ -305,23 +315,26 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
     for (int c0 = lo; c0 < hi; c0 += kChunk) {
         if (!once) load(c0);
         if (c0 > lo) __syncthreads();           // the previous chunk's reads of line
+        const int held = rows_of(c0);
         uint32_t total, at;
         if (ranked) {
             // rank among the equals: rows of kThreads tokens, warps, lanes
 #pragma unroll
             for (int e = 0; e < kEvictKeys; ++e) {
+                if (e >= held) break;
                 const uint32_t eq = __ballot_sync(0xffffffffu, c0 + e * kThreads + tid < hi && key[e] == T);
                 if (lane == 0) line[0][e * kWarps + warp] = __popc(eq);
             }
             __syncthreads();
-            at = block_prefix<kThreads>(tid < kEvictKeys * kWarps ? line[0][tid] : 0u, sums, &total);
-            if (tid < kEvictKeys * kWarps) line[0][tid] = equal + at;
+            at = block_prefix<kThreads>(tid < held * kWarps ? line[0][tid] : 0u, sums, &total);
+            if (tid < held * kWarps) line[0][tid] = equal + at;
             equal += total;
             __syncthreads();
         }
         uint32_t gap_bits = 0, mover_bits = 0, gap_mask[kEvictKeys], mover_mask[kEvictKeys];
 #pragma unroll
         for (int e = 0; e < kEvictKeys; ++e) {
+            if (e >= held) break;
             const int i = c0 + e * kThreads + tid;
             const bool in = i < hi, is_eq = in && key[e] == T;
             bool keep = in && key[e] >= T;
@@ -341,11 +354,12 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
             }
         }
         __syncthreads();
-        at = block_prefix<kThreads>(tid < kEvictKeys * kWarps ? line[1][tid] : 0u, sums, &total);
-        if (tid < kEvictKeys * kWarps) line[1][tid] = at;
+        at = block_prefix<kThreads>(tid < held * kWarps ? line[1][tid] : 0u, sums, &total);
+        if (tid < held * kWarps) line[1][tid] = at;
         __syncthreads();
 #pragma unroll
         for (int e = 0; e < kEvictKeys; ++e) {
+            if (e >= held) break;
             const int i = c0 + e * kThreads + tid;
             const uint32_t before = line[1][e * kWarps + warp];
             if ((gap_bits >> e) & 1u) {
