@@ -140,3 +140,129 @@ def test_serving_loop(dev, dtype, hq, hkv, d, window):
                 assert torch.equal(flat_k[slot, h], turned[b][t][h]) and torch.equal(flat_v[slot, h], values[b][t][h])
     assert pool.num_free == 64 - sum(max(1, -(-int(n) // bs)) for n in lens)
     assert lib.read_device_errors(dev) == 0
+
+
+def _batch_on(dev, x, blocks=None, shift=0):
+    """x's tensors on the device; with ``blocks`` in a pool of that many, x's blocks `shift` further on."""
+    def pool(t):
+        if blocks is None:
+            return t.to(dev)
+        big = torch.zeros((blocks, *t.shape[1:]), dtype=t.dtype, device=dev)
+        big[shift:shift + t.shape[0]] = t.to(dev)
+        return big
+    return dict(k=pool(x.k), v=pool(x.v), tables=(x.tables + shift).to(dev), lens=x.lens.to(dev), q=x.q.to(dev))
+
+
+def test_pool_offsets_past_32_bits(dev):
+    """The operators on blocks at the far end of a pool of 2.3 G elements (byte
+    offsets past 2^32, element offsets past 2^31) give what they give on the
+    same blocks in a small pool, bit for bit."""
+    hq, hkv, d, bs, far = 8, 8, 128, 16, 140_000
+    x = Batch([700, 33, 300], hq, hkv, d, bs, torch.bfloat16, seed=31, stale=False, slack_width=0)
+    small, big = _batch_on(dev, x), _batch_on(dev, x, far + x.k.shape[0], far)
+    g = torch.Generator().manual_seed(5)
+    qkv = torch.randn(9, 24 * d, generator=g).to(torch.bfloat16).to(dev)
+    q, k, v = (t.view(9, -1, d) for t in qkv.split([8 * d, 8 * d, 8 * d], dim=1))
+    pos = torch.arange(9, device=dev) + 1000
+    slots = torch.randperm(x.k.shape[0] * bs, generator=g)[:9].to(dev)
+    inv = lib.rope_frequencies(d)[0].to(dev)
+    w = x.state().nan_to_num(0.0).to(dev)
+    start = torch.tensor([0, 40, 73, 100], dtype=torch.int32, device=dev)
+    qc = torch.randn(100, hq, d, generator=g).to(torch.bfloat16).to(dev)
+    got = []
+    for m, first in ((small, 0), (big, far * bs)):
+        turned = lib.rope_and_cache(q, k, v, pos, slots + first, inv, m["k"], m["v"])
+        out, wd = lib.decode_weights(m["q"], m["k"], m["v"], m["tables"], m["lens"], x.scale, 700,
+                                     weights=w, weights_out=torch.zeros_like(w))
+        wp = lib.prefill_weights(qc, m["k"], m["tables"], m["lens"], start, x.scale, 40, 700, weights=w,
+                                 weights_out=torch.zeros_like(w))
+        new, we, pe = lib.evict(m["k"], m["v"], m["tables"], m["lens"], m["lens"], 200, w,
+                                torch.zeros(w.shape, dtype=torch.int32, device=dev), sinks=2, recent=30,
+                                weights_out=torch.zeros_like(w),
+                                positions_out=torch.zeros(w.shape, dtype=torch.int32, device=dev))
+        n = x.k.shape[0]
+        lo = first // bs
+        got.append((turned, out, wd, wp, new, we, pe, m["k"][lo:lo + n].clone(), m["v"][lo:lo + n].clone()))
+    torch.cuda.synchronize(dev)
+    assert lib.read_device_errors(dev) == 0
+    for a, b in zip(*got):
+        assert same_bits(a, b)
+    assert int(big["k"][:far].count_nonzero()) == 0 and int(big["v"][:far].count_nonzero()) == 0
+
+
+def test_a_step_in_one_graph(dev):
+    """Write, attend, weigh and cut, captured once and replayed on new
+    contents, equal the same calls made eagerly."""
+    hq, hkv, d, bs, B = 8, 2, 64, 16, 4
+    g = torch.Generator().manual_seed(77)
+    x = Batch([70, 33, 64, 1], hq, hkv, d, bs, torch.float16, seed=77, stale=False, slack_width=1)
+    width = x.tokens
+    inv = lib.rope_frequencies(d)[0].to(dev)
+    s = _batch_on(dev, x)
+    s.update(qkv=torch.zeros(B, (hq + 2 * hkv) * d, dtype=torch.float16, device=dev),
+             pos=torch.zeros(B, dtype=torch.int64, device=dev), slots=torch.zeros(B, dtype=torch.int64, device=dev),
+             seen=x.lens.to(dev), known=torch.zeros(B, dtype=torch.int32, device=dev),
+             w=torch.zeros(B, hkv, width, device=dev), p=torch.zeros(B, hkv, width, dtype=torch.int32, device=dev),
+             turned=torch.zeros(B, hq, d, dtype=torch.float16, device=dev), out=torch.zeros(B, hq, d, dtype=torch.float16, device=dev),
+             new=torch.zeros(B, dtype=torch.int32, device=dev))
+
+    def step(m):
+        q, k, v = (t.view(B, -1, d) for t in m["qkv"].split([hq * d, hkv * d, hkv * d], dim=1))
+        lib.rope_and_cache(q, k, v, m["pos"], m["slots"], inv, m["k"], m["v"], q_out=m["turned"])
+        lib.decode_weights(m["turned"], m["k"], m["v"], m["tables"], m["lens"], d ** -0.5, width,
+                           weights=m["w"], out=m["out"])
+        lib.evict(m["k"], m["v"], m["tables"], m["lens"], m["seen"], 32, m["w"], m["p"], known_lens=m["known"],
+                  trigger=64, sinks=1, recent=8, new_lens=m["new"])
+
+    def fill(m, seed):
+        g.manual_seed(seed)
+        lens = torch.randint(1, width + 1, (B,), generator=g).to(torch.int32)
+        lens = torch.minimum(lens, x.lens + 15 - (x.lens - 1) % 16)          # within the blocks held
+        m["k"].copy_(x.k), m["v"].copy_(x.v), m["lens"].copy_(lens), m["seen"].copy_(lens + 5)
+        m["qkv"].copy_(torch.randn(m["qkv"].shape, generator=g))
+        m["pos"].copy_(lens.long() + 4)
+        at = (lens - 1).long()
+        m["slots"].copy_(x.tables[torch.arange(B), at // bs].long() * bs + at % bs)
+        m["known"].copy_((lens - 3).clamp(min=0))
+        m["w"].copy_(torch.rand(m["w"].shape, generator=g)), m["p"].copy_(torch.arange(width).expand(m["p"].shape))
+
+    fill(s, 1)
+    step(s)                                              # set-up outside the capture
+    torch.cuda.synchronize(dev)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(s)
+    e = {n: t.clone() for n, t in s.items()}
+    for seed in (2, 3, 4):
+        fill(s, seed), fill(e, seed)
+        graph.replay()
+        step(e)
+        torch.cuda.synchronize(dev)
+        live = torch.arange(width, device=dev) < e["new"][:, None, None]
+        for n in ("k", "v", "turned", "out", "new"):
+            assert same_bits(s[n], e[n]), n
+        for n in ("w", "p"):
+            assert same_bits(torch.where(live, s[n], 0 * s[n]), torch.where(live, e[n], 0 * e[n])), n
+    assert lib.read_device_errors(dev) == 0
+
+
+def test_prefill_weights_on_two_streams(dev):
+    """Two persistent launches at once, each with its own workspace."""
+    xs = [Batch([900, 77], 8, 2, 128, 16, torch.float16, seed=s) for s in (41, 42)]
+    qs = [torch.randn(400, 8, 128, generator=x.gen).to(torch.float16) for x in xs]
+    start = torch.tensor([0, 323, 400], dtype=torch.int32, device=dev)
+    on = [_batch_on(dev, x) for x in xs]
+    qd = [q.to(dev) for q in qs]
+    torch.cuda.synchronize(dev)
+    streams = [torch.cuda.Stream(dev) for _ in xs]
+    got = []
+    for _ in range(3):
+        got = []
+        for x, m, q, s in zip(xs, on, qd, streams):
+            with torch.cuda.stream(s):
+                got.append(lib.prefill_weights(q, m["k"], m["tables"], m["lens"], start, x.scale, 323, 900))
+    torch.cuda.synchronize(dev)
+    for x, q, w in zip(xs, qs, got):
+        ww, wb = prefill_reference(x, q, [323, 77])
+        within(w, ww, wb, "weights")
+    assert lib.read_device_errors(dev) == 0
