@@ -282,10 +282,11 @@ int pa_prefill_weights(const void* q, const void* k_cache, const int32_t* block_
     if (!workspace || workspace_bytes < pa::prefill_weights_plan(p, workspace)) return PA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return PA_ERR_INVALID_ARG;
     if (p.max_context == 0) return PA_OK;
-    // units of either pass are counted in 32 bits
+    // units of either pass, or key tiles, are counted in 32 bits
     const int64_t tiles = ((int64_t)p.max_context + 127) / 128 * p.num_seqs * p.num_kv_heads;
-    if (tiles * p.query_chunks >= (1ll << 31) ||
-        (int64_t)p.max_query_tiles * p.key_chunks * p.num_seqs * p.num_kv_heads >= (1ll << 31))
+    const bool lone = p.max_query_tiles <= 1;
+    if (tiles * (lone ? 1 : p.query_chunks) >= (1ll << 31) ||
+        (!lone && (int64_t)p.max_query_tiles * p.key_chunks * p.num_seqs * p.num_kv_heads >= (1ll << 31)))
         return PA_ERR_UNSUPPORTED;
     if (num_tokens == 0) p.max_counted = 0;
     CUtensorMap tmk, tmq;
@@ -301,8 +302,8 @@ int pa_prefill_weights(const void* q, const void* k_cache, const int32_t* block_
     p.scale_log2 = scale * pa::kLog2e;
     p.max_blocks_per_seq = shp->max_blocks_per_seq, p.block_size = shp->block_size;
     p.num_blocks = shp->num_blocks, p.num_tokens = num_tokens;
-    return finish(pa::launch_prefill_weights(shp->dtype, shp->head_dim, tmk, tmq, p,
-                                             static_cast<cudaStream_t>(stream)));
+    return finish((lone ? pa::launch_window_weights : pa::launch_prefill_weights)(
+        shp->dtype, shp->head_dim, tmk, tmq, p, static_cast<cudaStream_t>(stream)));
 }
 
 size_t pa_evict_workspace_size(const pa_shape* shp, int32_t budget) {

@@ -72,8 +72,6 @@ struct PrefillWeightsParams {
     int max_query_tiles;
     int key_chunk, key_chunks;     // key tiles per unit of pass 1, units of the longest row
     int query_chunk, query_chunks; // query tiles per unit of pass 2, units of a column
-    int key_run;                   // pairs of key tiles per unit of pass 2
-    bool join_early;               // pass 2 joins the chunks of pass 1 itself
     float* lse;                    // [B][Hkv][max_query_tiles][128], log2 units
     float2* stats;                 // [key_chunks] x the same: maximum and sum
     float* columns;                // [query_chunks][B][Hkv][columns_stride]
@@ -83,6 +81,11 @@ struct PrefillWeightsParams {
 // Chooses the chunks, lays out the workspace and returns its bytes (needs
 // the sizes: group, num_seqs, num_kv_heads, max_context, max_counted).
 size_t prefill_weights_plan(PrefillWeightsParams& p, void* workspace);
+// The case of at most one query tile per sequence (prefill_window.cu).
+size_t window_weights_plan(PrefillWeightsParams& p, void* workspace);
+cudaError_t launch_window_weights(int dtype, int head_dim, const CUtensorMap& tmk,
+                                  const CUtensorMap& tmq, const PrefillWeightsParams& p,
+                                  cudaStream_t stream);
 cudaError_t launch_prefill_weights(int dtype, int head_dim, const CUtensorMap& tmk,
                                    const CUtensorMap& tmq, const PrefillWeightsParams& p,
                                    cudaStream_t stream);

@@ -40,71 +40,16 @@
 // tensor memory is always released.
 #include <algorithm>
 
-#include "bounded_internal.h"
-#include "decode_tile.cuh"
-#include "tc_device.cuh"
+#include "prefill_weights.cuh"
 
 namespace pa {
 
-constexpr int kPwRows = 128;                   // lanes: rows of a resident tile
-constexpr int kPwCols = 128;                   // columns: rows of a streamed tile
-constexpr int kPwBufs = 4;                     // accumulators in tensor memory
-constexpr int kPwGroups = 4;                   // epilogue groups of four warps, one per buffer
-constexpr int kPwLoadersAfter = 4 + 4 * kPwGroups;   // warps 0, 1 issue MMAs; 2, 3, 20 .. 23 load
-constexpr int kPwLoaders = 6;                  // two for each stage
-constexpr int kPwThreads = (kPwLoadersAfter + kPwLoaders - 2) * 32;
 constexpr int kPwJoinThreads = 256;
 
-template <int D>
-struct PwLayout {
-    static constexpr int kHalf = kPwRows * 128;               // 64 dims of 128 rows
-    static constexpr int kHalves = D / kBoxElems;
-    static constexpr int kTile = kHalves * kHalf;
-    static constexpr int kA = 3;                              // resident tiles: a unit's and the next's
-    static constexpr int kB = 3;                              // streamed tiles
-    static constexpr int kDynamicSmem = (kA + kB) * kTile + 1024;
-};
-
-struct PwSeq {
-    int L, C, counted;             // context, chunk, counted queries
-    int q0;                        // row of the first counted query in q
-    int n_qt, n_kt;                // query and key tiles
-};
-
-__device__ __forceinline__ void pw_sequence(const PrefillWeightsParams& p, int b, bool report,
-                                            PwSeq& s) {
-    int L = p.context_lens[b];
-    const int64_t start = p.query_start[b];
-    int64_t C = (int64_t)p.query_start[b + 1] - start;
-    bool bad = false;
-    if (L < 0 || L > p.max_context) bad = true, L = L < 0 ? 0 : p.max_context;
-    if (C < 0 || C > L) bad = true, C = C < 0 ? 0 : L;
-    if (start < 0 || start + C > p.num_tokens) bad = true, C = 0;
-    s.L = L, s.C = (int)C;
-    s.counted = p.window > 0 ? min(p.window, s.C) : s.C;
-    if (s.counted > p.max_counted) bad = true, s.counted = p.max_counted;
-    s.q0 = (int)start + s.C - s.counted;
-    s.n_qt = (s.counted + p.tile_tokens - 1) / p.tile_tokens;
-    s.n_kt = (L + kPwCols - 1) / kPwCols;
-    if (bad && report) flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
-}
-
-// Key tiles that query tile qt sees, and the first query tile that sees any
-// key of tile kt.
-__device__ __forceinline__ int pw_key_tiles(const PrefillWeightsParams& p, const PwSeq& s, int qt) {
-    const int last = min((qt + 1) * p.tile_tokens, s.counted) - 1;
-    return (s.L - s.counted + last) / kPwCols + 1;
-}
-
-__device__ __forceinline__ int pw_first_query_tile(const PrefillWeightsParams& p, const PwSeq& s,
-                                                   int kt) {
-    return max(0, kt * kPwCols - (s.L - s.counted)) / p.tile_tokens;
-}
-
-// One unit of (b, g): pairs of resident tiles [a0, a1) (pair a is the tiles
-// 2a and 2a + 1), each with the streamed tiles of its chunk.
+// One unit of (b, g): resident tiles 2a and 2a + 1 (where there are two) and
+// the streamed tiles [first, last).
 struct PwUnit {
-    int b, g, a0, a1, chunk;
+    int b, g, a, chunk, first, last;
 };
 
 // Walks the units u = blockIdx.x, + gridDim.x, ... in order (their number
@@ -132,10 +77,8 @@ struct PwWalk {
             unsigned count = 0;
             if (i < p.num_seqs) {
                 pw_sequence(p, kStats ? i : p.num_seqs - 1 - i, (kStats || p.max_counted == 0) && blockIdx.x == 0 && threadIdx.x < 32, mine);
-                const int kt2 = (mine.n_kt + 1) / 2, qt2 = (mine.n_qt + 1) / 2;
-                count = kStats ? qt2 * ((mine.n_kt + p.key_chunk - 1) / p.key_chunk)
-                               : ((kt2 + p.key_run - 1) / p.key_run) *
-                                     max(1, (mine.n_qt + p.query_chunk - 1) / p.query_chunk);
+                count = kStats ? (mine.n_qt + 1) / 2 * ((mine.n_kt + p.key_chunk - 1) / p.key_chunk)
+                               : (mine.n_kt + 1) / 2 * max(1, (mine.n_qt + p.query_chunk - 1) / p.query_chunk);
                 count *= p.num_kv_heads;
             }
             ends = count;
@@ -158,47 +101,23 @@ struct PwWalk {
         s.n_qt = __shfl_sync(0xffffffffu, mine.n_qt, at);
         s.n_kt = __shfl_sync(0xffffffffu, mine.n_kt, at);
         U.g = r - rest * (unsigned)p.num_kv_heads;
-        const int runs = kStats ? (s.n_qt + 1) / 2 : ((s.n_kt + 1) / 2 + p.key_run - 1) / p.key_run;
-        U.chunk = rest / (unsigned)runs;
-        U.a0 = rest - U.chunk * runs;
-        U.a1 = U.a0 + 1;
-        if (!kStats) {
-            U.a0 *= p.key_run;
-            U.a1 = min(U.a0 + p.key_run, (s.n_kt + 1) / 2);
+        const unsigned tile_pairs = ((kStats ? s.n_qt : s.n_kt) + 1) / 2;
+        U.chunk = rest / tile_pairs;
+        U.a = rest - U.chunk * tile_pairs;
+        if (kStats) {
+            U.first = U.chunk * p.key_chunk;
+            U.last = min(U.first + p.key_chunk, pw_key_tiles(p, s, min(2 * U.a + 1, s.n_qt - 1)));
+        } else {
+            U.first = max(U.chunk * p.query_chunk, pw_first_query_tile(p, s, 2 * U.a));
+            U.last = min((U.chunk + 1) * p.query_chunk, s.n_qt);
         }
         return true;
     }
 
-    // streamed tiles [first, last) of the unit's pair a
-    __device__ __forceinline__ void streamed(const PrefillWeightsParams& p, const PwUnit& U, int a,
-                                             int& first, int& last) const {
-        if (kStats) {
-            first = U.chunk * p.key_chunk;
-            last = min(first + p.key_chunk, pw_key_tiles(p, s, min(2 * a + 1, s.n_qt - 1)));
-        } else {
-            first = max(U.chunk * p.query_chunk, pw_first_query_tile(p, s, 2 * a));
-            last = min((U.chunk + 1) * p.query_chunk, s.n_qt);
-        }
-    }
-
-    __device__ __forceinline__ int residents(int a) const {
-        return min(2, (kStats ? s.n_qt : s.n_kt) - 2 * a);
+    __device__ __forceinline__ int residents(const PwUnit& U) const {
+        return min(2, (kStats ? s.n_qt : s.n_kt) - 2 * U.a);
     }
 };
-
-__device__ __forceinline__ float sum8(const uint64_t (&ps)[4]) {
-    float t[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f32x2_unpack(ps[e], t[2 * e], t[2 * e + 1]);
-    return ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
-}
-
-// (m, z) and another chunk's: the maximum, and the sum taken against it.
-__device__ __forceinline__ void join_stats(float& m, float& z, float2 o) {
-    const float n = fmaxf(m, o.x), ref = n == -INFINITY ? 0.f : n;
-    z = z * ex2(m - ref) + o.y * ex2(o.x - ref);
-    m = n;
-}
 
 // lse of row r of query tile qt from the tile's chunks (eight loads in
 // flight); +inf past the sequence's queries.
@@ -222,84 +141,6 @@ __device__ __forceinline__ float joined_lse(const PrefillWeightsParams& p, const
     return r < tokens * p.group ? m + log2f(z) : INFINITY;
 }
 
-// Pass 1: folds a tile's row (keys up to `visible` with kMask) into (m, z).
-template <bool kMask, typename Release>
-__device__ __forceinline__ void row_stats(float& m, float& z, uint32_t tile_addr, float sl,
-                                          uint64_t sl2, int visible, Release&& release) {
-#pragma unroll
-    for (int c = 0; c < kPwCols; c += 64) {
-        uint32_t v[64];
-        tmem_ld32(tile_addr + c, *reinterpret_cast<uint32_t(*)[32]>(v));
-        tmem_ld32(tile_addr + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-        tmem_wait_ld();
-        if (c == 64) release();
-        if (kMask) {
-#pragma unroll
-            for (int e = 0; e < 64; ++e)
-                if (c + e > visible) v[e] = 0xff800000u;
-        }
-        float pm[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) pm[e] = __uint_as_float(v[e]);
-#pragma unroll
-        for (int e = 4; e < 60; e += 8) {                 // two at a time: one instruction
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                pm[i] = fmaxf(fmaxf(pm[i], __uint_as_float(v[e + i])), __uint_as_float(v[e + 4 + i]));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pm[i] = fmaxf(pm[i], __uint_as_float(v[60 + i]));
-        const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * sl;
-        if (mx > m + kRescaleThresholdLog2) {         // also the first finite maximum
-            z *= ex2(m - mx);
-            m = mx;
-        }
-        const float ref = m == -INFINITY ? 0.f : m;   // nothing visible yet
-        const uint64_t neg2 = f32x2_pack(-ref, -ref);
-        uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            float a0, a1;
-            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sl2,
-                                   neg2), a0, a1);
-            ps[e & 3] = f32x2_add(ps[e & 3], f32x2_pack(ex2(a0), ex2(a1)));
-        }
-        z += sum8(ps);
-    }
-}
-
-// Pass 2: the sum of 2^(x - lse) over the tile's columns (of [lo, hi) with
-// kMask); `neg_lse` in shared memory, `release` called once the tile is read.
-template <bool kMask, typename Release>
-__device__ __forceinline__ float column_sums(uint32_t tile_addr, const float* neg_lse, uint64_t sl2,
-                                             int lo, int hi, Release&& release) {
-    uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-    for (int c = 0; c < kPwCols; c += 32) {
-        uint32_t v[32];
-        tmem_ld32(tile_addr + c, v);
-        tmem_wait_ld();
-        if (c == kPwCols - 32) release();
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(neg_lse + c + e);
-            float a[4];
-            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2,
-                                   f32x2_pack(l.x, l.y)), a[0], a[1]);
-            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sl2,
-                                   f32x2_pack(l.z, l.w)), a[2], a[3]);
-            if (kMask) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    a[i] = c + e + i >= lo && c + e + i < hi ? a[i] : -INFINITY;
-            }
-            ps[(e >> 1) & 3] = f32x2_add(ps[(e >> 1) & 3], f32x2_pack(ex2(a[0]), ex2(a[1])));
-            ps[((e >> 1) + 1) & 3] = f32x2_add(ps[((e >> 1) + 1) & 3], f32x2_pack(ex2(a[2]), ex2(a[3])));
-        }
-    }
-    return sum8(ps);
-}
-
 template <typename T, int D, bool kStats>
 __global__ void __launch_bounds__(kPwThreads, 1)
     prefill_weights_kernel(const __grid_constant__ CUtensorMap tmap_k,
@@ -307,7 +148,9 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                            const __grid_constant__ PrefillWeightsParams p) {
     using Lay = PwLayout<D>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-    constexpr int kA = Lay::kA, kB = Lay::kB;
+    // resident tiles (a unit's, and the next's first), streamed tiles
+    constexpr int kA = 3, kB = 3;
+    static_assert(kA + kB == Lay::kStages, "the rings share the CTA's tiles");
     __shared__ __align__(8) uint64_t a_full[kA], a_empty[kA], b_full[kB], b_empty[kB];
     __shared__ __align__(8) uint64_t s_full[kPwBufs], s_empty[kPwBufs];
     __shared__ uint32_t tmem_base;
@@ -356,52 +199,17 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         auto open = [&](uint64_t* empty, int stages, int n) -> bool {
             return n < stages || __all_sync(0xffffffffu, mbar_wait(&empty[n % stages], ((n / stages) - 1) & 1));
         };
-        // block ids of key tiles 4 q .. 4 q + 3: lane i has box i % 8 of tile i / 8
-        auto blocks_of = [&](const PwSeq& s, int b, int q) {
-            const int tok = q * 4 * kPwCols + 16 * lane;
-            if (tok >= s.L) return 0;
-            const int blk = __ldg(p.block_tables + (size_t)b * p.max_blocks_per_seq + tok / p.block_size);
-            if (blk < 0 || blk >= p.num_blocks) flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
-            return blk;
-        };
         auto load_k = [&](uint8_t* dst, uint64_t* full, uint64_t* empty, int stages, int n,
                           const PwSeq& s, const PwUnit& U, int kt, int blk) -> bool {
             if (!open(empty, stages, n)) return false;
-            // boxes part, part + 2, ... of the tile's
-            const int nbox = min(8, (s.L - kt * kPwCols + 15) / 16), own = (nbox - part + 1) / 2;
-            uint64_t* bar = &full[n % stages];
-            if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(own * Lay::kHalves * kBox16Bytes));
-            __syncwarp();
-            dst += (n % stages) * Lay::kTile;
-            const int sub_mask = p.block_size - 1;               // 16 or 32
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int box = 2 * i + part;
-                if (box >= nbox) break;
-                const int pblk = __shfl_sync(0xffffffffu, blk, (kt & 3) * 8 + box);
-                if (elect_one()) {
-#pragma unroll
-                    for (int h = 0; h < Lay::kHalves; ++h)
-                        tma_load_4d(dst + h * Lay::kHalf + box * kBox16Bytes, &tmap_k, bar,
-                                    h * kBoxElems, U.g, (16 * box) & sub_mask, pblk);
-                }
-                __syncwarp();
-            }
+            pw_load_keys<D>(&tmap_k, dst + (n % stages) * Lay::kTile, &full[n % stages], p, s, U.g, kt, blk,
+                            part, 8, 2);
             return true;
         };
         auto load_q = [&](uint8_t* dst, uint64_t* full, uint64_t* empty, int stages, int n,
                           const PwSeq& s, const PwUnit& U, int qt) -> bool {
             if (!open(empty, stages, n)) return false;
-            uint64_t* bar = &full[n % stages];
-            const int row = s.q0 + qt * p.tile_tokens;
-            dst += (n % stages) * Lay::kTile;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(bar, (uint32_t)(q_rows * Lay::kHalves * 128));
-#pragma unroll
-                for (int h = 0; h < Lay::kHalves; ++h)
-                    tma_load_3d(dst + h * Lay::kHalf, &tmap_q, bar, h * kBoxElems, U.g * G, row);
-            }
-            __syncwarp();
+            pw_load_queries<D>(&tmap_q, dst + (n % stages) * Lay::kTile, &full[n % stages], p, s, U.g, qt);
             return true;
         };
         uint8_t* a_ring = smem;
@@ -416,33 +224,29 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             int quad = -2, blk = 0, blk_next = 0;
             auto to_tile = [&](int kt) {
                 if ((kt >> 2) == quad) return;
-                blk = (kt >> 2) == quad + 1 ? blk_next : blocks_of(walk.s, U.b, kt >> 2);
+                blk = (kt >> 2) == quad + 1 ? blk_next : pw_blocks(p, walk.s, U.b, kt >> 2);
                 quad = kt >> 2;
-                blk_next = blocks_of(walk.s, U.b, quad + 1);
+                blk_next = pw_blocks(p, walk.s, U.b, quad + 1);
             };
-            for (int a = U.a0; ok && a < U.a1; ++a) {
-                int first, last;
-                walk.streamed(p, U, a, first, last);
-                if (first >= last) continue;
-                for (int j = 0; ok && j < walk.residents(a); ++j) {
-                    if (!kStats) to_tile(2 * a + j);
-                    if (na % kA == (kStats ? who : k_stage))
-                        ok = kStats ? load_q(a_ring, a_full, a_empty, kA, na, walk.s, U, 2 * a + j)
-                                    : load_k(a_ring, a_full, a_empty, kA, na, walk.s, U, 2 * a + j, blk);
-                    ++na;
+            if (U.first >= U.last) continue;
+            for (int j = 0; ok && j < walk.residents(U); ++j) {
+                if (!kStats) to_tile(2 * U.a + j);
+                if (na % kA == (kStats ? who : k_stage))
+                    ok = kStats ? load_q(a_ring, a_full, a_empty, kA, na, walk.s, U, 2 * U.a + j)
+                                : load_k(a_ring, a_full, a_empty, kA, na, walk.s, U, 2 * U.a + j, blk);
+                ++na;
+            }
+            for (int i = U.first; ok && i < U.last; ++i) {
+                if (kStats) {
+                    to_tile(i);
+                } else {
+                    if (U.b == at_b && U.g == at_g && i == at_qt) continue;     // still there
+                    at_b = U.b, at_g = U.g, at_qt = i;
                 }
-                for (int i = first; ok && i < last; ++i) {
-                    if (kStats) {
-                        to_tile(i);
-                    } else {
-                        if (U.b == at_b && U.g == at_g && i == at_qt) continue;     // still there
-                        at_b = U.b, at_g = U.g, at_qt = i;
-                    }
-                    if (nb % kB == (kStats ? k_stage : who))
-                        ok = kStats ? load_k(b_ring, b_full, b_empty, kB, nb, walk.s, U, i, blk)
-                                    : load_q(b_ring, b_full, b_empty, kB, nb, walk.s, U, i);
-                    ++nb;
-                }
+                if (nb % kB == (kStats ? k_stage : who))
+                    ok = kStats ? load_k(b_ring, b_full, b_empty, kB, nb, walk.s, U, i, blk)
+                                : load_q(b_ring, b_full, b_empty, kB, nb, walk.s, U, i);
+                ++nb;
             }
         }
         if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
@@ -462,51 +266,39 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1));
         };
         while (ok && walk.next(p, U)) {
-            for (int a = U.a0; ok && a < U.a1; ++a) {
-                int first, last;
-                walk.streamed(p, U, a, first, last);
-                if (first >= last) continue;
-                const int residents = walk.residents(a);
-                // both warps wait for every tile: no phase of a stage is passed over
-                for (int j = 0; j < residents; ++j) wait(&a_full[(na + j) % kA], (na + j) / kA);
-                const int stage = (na + (residents == 2 ? warp : 0)) % kA;
-                for (int i = first; ok && i < last; ++i, ++tiles) {
-                    if (kStats || U.b != at_b || U.g != at_g || i != at_qt) {
-                        // the previous streamed tile is free once this warp's products are done
-                        if (nb >= 0 && elect_one()) mma_commit(&b_empty[nb % kB]);
-                        __syncwarp();
-                        ++nb;
-                        at_b = U.b, at_g = U.g, at_qt = i;
-                        wait(&b_full[nb % kB], nb / kB);
-                    }
-                    // two resident tiles: one each, buffers by the streamed tile's parity;
-                    // one: streamed tiles in turn, buffers by the parity of the pair
-                    if (residents == 1 && (tiles & 1) != warp) continue;
-                    const int odd = (residents == 2 ? tiles : tiles >> 1) & 1, buf = warp + 2 * odd;
-                    const int n = odd ? used[1]++ : used[0]++;
-                    if (n > 0) wait(&s_empty[buf], n - 1);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint64_t da = a_ring + stage * (Lay::kTile >> 4);
-                    const uint64_t db = b_ring + (nb % kB) * (Lay::kTile >> 4);
-                    const uint32_t d = tmem + kPwCols * buf;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            constexpr int kHalf16 = Lay::kHalf >> 4;
-                            const uint64_t off = (kk >> 2) * kHalf16 + (kk & 3) * 2;
-                            mma_f16_ss(d, da + off, db + off, kId, kk > 0);
-                        }
-                        mma_commit(&s_full[buf]);
-                    }
+            const int first = U.first, last = U.last;
+            if (first >= last) continue;
+            const int residents = walk.residents(U);
+            // both warps wait for every tile: no phase of a stage is passed over
+            for (int j = 0; j < residents; ++j) wait(&a_full[(na + j) % kA], (na + j) / kA);
+            const int stage = (na + (residents == 2 ? warp : 0)) % kA;
+            for (int i = first; ok && i < last; ++i, ++tiles) {
+                if (kStats || U.b != at_b || U.g != at_g || i != at_qt) {
+                    // the previous streamed tile is free once this warp's products are done
+                    if (nb >= 0 && elect_one()) mma_commit(&b_empty[nb % kB]);
                     __syncwarp();
+                    ++nb;
+                    at_b = U.b, at_g = U.g, at_qt = i;
+                    wait(&b_full[nb % kB], nb / kB);
                 }
-                for (int j = 0; j < residents; ++j) {
-                    if (ok && elect_one()) mma_commit(&a_empty[(na + j) % kA]);
-                    __syncwarp();
-                }
-                na += residents;
+                // two resident tiles: one each, buffers by the streamed tile's parity;
+                // one: streamed tiles in turn, buffers by the parity of the pair
+                if (residents == 1 && (tiles & 1) != warp) continue;
+                const int odd = (residents == 2 ? tiles : tiles >> 1) & 1, buf = warp + 2 * odd;
+                const int n = odd ? used[1]++ : used[0]++;
+                if (n > 0) wait(&s_empty[buf], n - 1);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint64_t da = a_ring + stage * (Lay::kTile >> 4);
+                const uint64_t db = b_ring + (nb % kB) * (Lay::kTile >> 4);
+                const uint32_t d = tmem + kPwCols * buf;
+                pw_product<D>(d, da, db, kId, &s_full[buf]);
             }
+            for (int j = 0; j < residents; ++j) {
+                if (ok && elect_one()) mma_commit(&a_empty[(na + j) % kA]);
+                __syncwarp();
+            }
+            na += residents;
         }
         if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
     } else {
@@ -536,94 +328,90 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         while (walk.next(p, U)) {
             const PwSeq& s = walk.s;
             const size_t pair = (size_t)U.b * p.num_kv_heads + U.g;
-            for (int a = U.a0; a < U.a1; ++a) {
-                int first, last;
-                walk.streamed(p, U, a, first, last);
-                const int steps = max(0, last - first);
-                if (kStats && steps == 0) continue;
-                const bool two = walk.residents(a) == 2;
-                // the group's streamed tiles: first + skip, every `every`-th
-                const int every = two ? 2 : 4, skip = ((two ? group >> 1 : group) - tiles) & (every - 1);
-                tiles += steps;
-                const int tile = 2 * a + (two ? group & 1 : 0), key = tile * kPwCols + r;
-                // one streamed tile is its group's alone; else the sharers are joined by the first
-                const int share = two ? group >> 1 : group;
-                const bool writer = steps == 1 ? skip == 0 : share == 0;
-                float before = 0.f;
-                if (!kStats && writer && p.query_chunks == 1 && p.weights && key < s.L - s.C)
-                    before = p.weights[pair * p.weights_stride + key];
-                float m = -INFINITY, z = 0.f;
-                auto join = [&](float2 o) {
-                    if (kStats) join_stats(m, z, o);
-                    else z += o.y;
-                };
-                if constexpr (kStats) {
-                    const int pos = min(s.L - s.counted + tile * p.tile_tokens + r / G, s.L - 1);
-                    for (int kt = first + skip; kt < last; kt += every) {
-                        wait(mine++);
-                        const int visible = pos - kt * kPwCols;           // keys 0 .. visible of the tile
-                        if (__all_sync(0xffffffffu, visible >= kPwCols - 1))
-                            row_stats<false>(m, z, tile_addr, sl, sl2, visible, release);
-                        else
-                            row_stats<true>(m, z, tile_addr, sl, sl2, visible, release);
-                    }
-                } else {
-                    for (int qt = first + skip; qt < last; qt += every) {
-                        // the rows' lse, requested before the wait for the tile and kept
-                        // while the query tile stays the same
-                        const bool fresh = (int)pair != at_pair || qt != at_qt;
-                        float lse = 0.f;
-                        if (fresh)
-                            lse = p.join_early ? joined_lse(p, s, pair, qt, r)
-                                               : p.lse[(pair * p.max_query_tiles + qt) * kPwCols + r];
-                        wait(mine++);
-                        if (fresh) {
-                            at_pair = (int)pair, at_qt = qt, ++lse_at;
-                            lse_s[group][lse_at & 1][r] = -lse;
-                            asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
-                        }
-                        const float* ls = lse_s[group][lse_at & 1];
-                        const int tokens = min(p.tile_tokens, s.counted - qt * p.tile_tokens);
-                        // columns that see this key: from `lo` on, up to the chunk's end
-                        const int lo = (key - (s.L - s.counted + qt * p.tile_tokens)) * G, hi = tokens * G;
-                        if (tokens == p.tile_tokens && __all_sync(0xffffffffu, lo <= 0))
-                            z += column_sums<false>(tile_addr, ls, sl2, lo, hi, release);
-                        else
-                            z += column_sums<true>(tile_addr, ls, sl2, lo, hi, release);
-                    }
-                }
-                if (steps > 1) {
-                    // sharers of a tile: groups w and w + 2 of two resident tiles, all four of
-                    // one.  Each kind has its two buffers: what a group writes was read before
-                    // the barrier of that kind that it passed last.
-                    if (two) {
-                        float2* o = other2[joins2++ & 1][group & 1];
-                        if (share > 0) o[r] = make_float2(m, z);
-                        asm volatile("bar.sync %0, 256;" ::"r"(5 + (group & 1)) : "memory");
-                        if (share == 0) join(o[r]);
-                    } else {
-                        float2(*o)[kPwRows] = other4[joins4++ & 1];
-                        if (share > 0) o[share - 1][r] = make_float2(m, z);
-                        asm volatile("bar.sync 7, 512;" ::: "memory");
-                        if (share == 0) {
-#pragma unroll
-                            for (int i = 0; i < 3; ++i) join(o[i][r]);
-                        }
-                    }
-                }
-                if (!writer || failed) continue;
-                if constexpr (kStats) {
-                    const int tokens = min(p.tile_tokens, s.counted - tile * p.tile_tokens);
-                    const size_t at = (pair * p.max_query_tiles + tile) * kPwRows + r;
-                    if (p.key_chunks == 1) p.lse[at] = r < tokens * G ? m + log2f(z) : INFINITY;
-                    else p.stats[(size_t)U.chunk * p.num_seqs * p.num_kv_heads * p.max_query_tiles * kPwRows + at] =
-                        make_float2(m, z);
-                } else if (key < s.L) {
-                    if (p.query_chunks == 1)
-                        p.weights_out[pair * p.weights_stride + key] = before + z;
+            const int a = U.a, first = U.first, last = U.last;
+            const int steps = max(0, last - first);
+            if (kStats && steps == 0) continue;
+            const bool two = walk.residents(U) == 2;
+            // the group's streamed tiles: first + skip, every `every`-th
+            const int every = two ? 2 : 4, skip = ((two ? group >> 1 : group) - tiles) & (every - 1);
+            tiles += steps;
+            const int tile = 2 * a + (two ? group & 1 : 0), key = tile * kPwCols + r;
+            // one streamed tile is its group's alone; else the sharers are joined by the first
+            const int share = two ? group >> 1 : group;
+            const bool writer = steps == 1 ? skip == 0 : share == 0;
+            float before = 0.f;
+            if (!kStats && writer && p.query_chunks == 1 && p.weights && key < s.L - s.C)
+                before = p.weights[pair * p.weights_stride + key];
+            float m = -INFINITY, z = 0.f;
+            auto join = [&](float2 o) {
+                if (kStats) join_stats(m, z, o);
+                else z += o.y;
+            };
+            if constexpr (kStats) {
+                const int pos = min(s.L - s.counted + tile * p.tile_tokens + r / G, s.L - 1);
+                for (int kt = first + skip; kt < last; kt += every) {
+                    wait(mine++);
+                    const int visible = pos - kt * kPwCols;           // keys 0 .. visible of the tile
+                    if (__all_sync(0xffffffffu, visible >= kPwCols - 1))
+                        row_stats<false>(m, z, tile_addr, sl, sl2, visible, release);
                     else
-                        p.columns[((size_t)U.chunk * p.num_seqs * p.num_kv_heads + pair) * p.columns_stride + key] = z;
+                        row_stats<true>(m, z, tile_addr, sl, sl2, visible, release);
                 }
+            } else {
+                for (int qt = first + skip; qt < last; qt += every) {
+                    // the rows' lse, requested before the wait for the tile and kept
+                    // while the query tile stays the same
+                    const bool fresh = (int)pair != at_pair || qt != at_qt;
+                    float lse = 0.f;
+                    if (fresh)
+                        lse = p.lse[(pair * p.max_query_tiles + qt) * kPwCols + r];
+                    wait(mine++);
+                    if (fresh) {
+                        at_pair = (int)pair, at_qt = qt, ++lse_at;
+                        lse_s[group][lse_at & 1][r] = -lse;
+                        asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+                    }
+                    const float* ls = lse_s[group][lse_at & 1];
+                    const int tokens = min(p.tile_tokens, s.counted - qt * p.tile_tokens);
+                    // columns that see this key: from `lo` on, up to the chunk's end
+                    const int lo = (key - (s.L - s.counted + qt * p.tile_tokens)) * G, hi = tokens * G;
+                    if (tokens == p.tile_tokens && __all_sync(0xffffffffu, lo <= 0))
+                        z += column_sums<false>(tile_addr, ls, sl2, lo, hi, release);
+                    else
+                        z += column_sums<true>(tile_addr, ls, sl2, lo, hi, release);
+                }
+            }
+            if (steps > 1) {
+                // sharers of a tile: groups w and w + 2 of two resident tiles, all four of
+                // one.  Each kind has its two buffers: what a group writes was read before
+                // the barrier of that kind that it passed last.
+                if (two) {
+                    float2* o = other2[joins2++ & 1][group & 1];
+                    if (share > 0) o[r] = make_float2(m, z);
+                    asm volatile("bar.sync %0, 256;" ::"r"(5 + (group & 1)) : "memory");
+                    if (share == 0) join(o[r]);
+                } else {
+                    float2(*o)[kPwRows] = other4[joins4++ & 1];
+                    if (share > 0) o[share - 1][r] = make_float2(m, z);
+                    asm volatile("bar.sync 7, 512;" ::: "memory");
+                    if (share == 0) {
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) join(o[i][r]);
+                    }
+                }
+            }
+            if (!writer || failed) continue;
+            if constexpr (kStats) {
+                const int tokens = min(p.tile_tokens, s.counted - tile * p.tile_tokens);
+                const size_t at = (pair * p.max_query_tiles + tile) * kPwRows + r;
+                if (p.key_chunks == 1) p.lse[at] = r < tokens * G ? m + log2f(z) : INFINITY;
+                else p.stats[(size_t)U.chunk * p.num_seqs * p.num_kv_heads * p.max_query_tiles * kPwRows + at] =
+                    make_float2(m, z);
+            } else if (key < s.L) {
+                if (p.query_chunks == 1)
+                    p.weights_out[pair * p.weights_stride + key] = before + z;
+                else
+                    p.columns[((size_t)U.chunk * p.num_seqs * p.num_kv_heads + pair) * p.columns_stride + key] = z;
             }
         }
         if (failed && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
@@ -676,20 +464,17 @@ size_t prefill_weights_plan(PrefillWeightsParams& p, void* workspace) {
     p.max_query_tiles = (p.max_counted + p.tile_tokens - 1) / p.tile_tokens;
     const int64_t key_tiles = ((int64_t)p.max_context + kPwCols - 1) / kPwCols;
     const int64_t pairs = (int64_t)p.num_seqs * p.num_kv_heads;
+    if (p.max_query_tiles <= 1) return window_weights_plan(p, workspace);
     // Units of some sixteenth of an SM's share (the batch taken at its
-    // bounds): pass 1 in chunks of 8 to 64 key tiles, pass 2 in chunks of 8
-    // to 64 query tiles; where one query tile is all there is, pass 2 takes
-    // runs of key tile pairs past it instead.
+    // bounds): pass 1 in chunks of 4 to 64 key tiles, pass 2 in chunks of 8
+    // to 64 query tiles.
     const int64_t per_sm = 152 * 16;
     const int64_t share1 = pairs * ((p.max_query_tiles + 1) / 2) * key_tiles / per_sm;
     const int64_t share2 = pairs * ((key_tiles + 1) / 2) * p.max_query_tiles / per_sm;
-    p.key_chunk = (int)std::min<int64_t>(64, std::max<int64_t>(8, share1));
+    p.key_chunk = (int)std::min<int64_t>(64, std::max<int64_t>(4, share1));
     p.key_chunks = (int)std::max<int64_t>(1, (key_tiles + p.key_chunk - 1) / p.key_chunk);
     p.query_chunk = (int)std::min<int64_t>(64, std::max<int64_t>(8, share2));
     p.query_chunks = std::max(1, (p.max_query_tiles + p.query_chunk - 1) / p.query_chunk);
-    p.key_run = p.max_query_tiles > 1 ? 1 : (int)std::min<int64_t>(8, std::max<int64_t>(2, share2));
-    // a lone query tile per sequence is read so seldom that pass 2 joins its chunks itself
-    p.join_early = p.max_query_tiles == 1 && p.key_chunks > 1;
     p.columns_stride = (int)(key_tiles * kPwCols);
     const size_t rows = (size_t)pairs * p.max_query_tiles * kPwRows;
     char* base = static_cast<char*>(workspace);
@@ -719,7 +504,7 @@ cudaError_t launch_prefill_weights_t(const CUtensorMap& tmk, const CUtensorMap& 
     const dim3 grid(sms), threads(kPwThreads);
     if (e == cudaSuccess && p.max_counted > 0) {
         e = launch_with_pdl(prefill_weights_kernel<T, D, true>, grid, threads, smem, stream, tmk, tmq, p);
-        if (e == cudaSuccess && p.key_chunks > 1 && !p.join_early)
+        if (e == cudaSuccess && p.key_chunks > 1)
             e = launch_with_pdl(prefill_stats_join_kernel,
                                 dim3(p.max_query_tiles, p.num_kv_heads, p.num_seqs), dim3(kPwRows), 0,
                                 stream, p);
