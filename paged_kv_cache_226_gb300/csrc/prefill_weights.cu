@@ -28,12 +28,11 @@
 // (half of the 16-token boxes each, through the block table: a box costs its
 // warp some 120 cycles), three of them also for a stage each of the Q ring
 // (one box of tokens x heads per 64 dims).  Two warps issue the MMAs, one for
-// each resident tile (where a unit has only one, streamed tiles in turn),
-// into two 128-column buffers each: a single issuer spends 1,060 cycles on
-// its waits and commits per tile, twice what the product takes.  Four groups
-// of four warps take the finished tiles.  Rows of Q past a sequence's chunk and K rows past its end
-// may hold anything: they only reach their own lane or column, which is
-// masked.
+// each resident tile, into two 128-column buffers each: a single issuer
+// spends 1,060 cycles on its waits and commits per tile, twice what the
+// product takes.  Four groups of four warps take the finished tiles.  Rows of
+// Q past a sequence's chunk and K rows past its end may hold anything: they
+// only reach their own lane or column, which is masked.
 //
 // Every mbarrier wait gives up after 1 s and flags PA_DEVERR_WAIT_TIMEOUT;
 // the epilogue warps then run their remaining steps without waiting, and
@@ -155,8 +154,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     __shared__ __align__(8) uint64_t s_full[kPwBufs], s_empty[kPwBufs];
     __shared__ uint32_t tmem_base;
     __shared__ __align__(16) float lse_s[kPwGroups][2][kPwCols];     // pass 2: [group][tile parity]
-    __shared__ float2 other2[2][2][kPwRows];                         // [join parity][resident tile]
-    __shared__ float2 other4[2][3][kPwRows];                         // [join parity][sharer]
+    __shared__ float2 other[2][2][kPwRows];                          // [join parity][resident tile]
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -165,8 +163,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     const int q_rows = p.tile_tokens * G;                    // rows of a query tile, <= 128
 
     if (threadIdx.x == 0) {
-        // K stages have two loaders; either issuer may read any tile
-        for (int i = 0; i < kA; ++i) mbar_init(&a_full[i], kStats ? 1 : 2), mbar_init(&a_empty[i], 2);
+        // K stages have two loaders; a resident tile has one issuer, a streamed tile both
+        for (int i = 0; i < kA; ++i) mbar_init(&a_full[i], kStats ? 1 : 2), mbar_init(&a_empty[i], 1);
         for (int i = 0; i < kB; ++i) mbar_init(&b_full[i], kStats ? 2 : 1), mbar_init(&b_empty[i], 2);
         for (int i = 0; i < kPwBufs; ++i) mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4);
         fence_barrier_init();
@@ -266,48 +264,44 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1));
         };
         while (ok && walk.next(p, U)) {
-            const int first = U.first, last = U.last;
-            if (first >= last) continue;
+            if (U.first >= U.last) continue;
             const int residents = walk.residents(U);
+            const bool active = warp < residents;
             // both warps wait for every tile: no phase of a stage is passed over
             for (int j = 0; j < residents; ++j) wait(&a_full[(na + j) % kA], (na + j) / kA);
-            const int stage = (na + (residents == 2 ? warp : 0)) % kA;
-            for (int i = first; ok && i < last; ++i, ++tiles) {
+            const int stage = (na + warp) % kA;
+            for (int i = U.first; ok && i < U.last; ++i, ++tiles) {
                 if (kStats || U.b != at_b || U.g != at_g || i != at_qt) {
                     // the previous streamed tile is free once this warp's products are done
                     if (nb >= 0 && elect_one()) mma_commit(&b_empty[nb % kB]);
                     __syncwarp();
                     ++nb;
                     at_b = U.b, at_g = U.g, at_qt = i;
+                    // also where this warp has no tile to multiply: it may not run ahead
                     wait(&b_full[nb % kB], nb / kB);
                 }
-                // two resident tiles: one each, buffers by the streamed tile's parity;
-                // one: streamed tiles in turn, buffers by the parity of the pair
-                if (residents == 1 && (tiles & 1) != warp) continue;
-                const int odd = (residents == 2 ? tiles : tiles >> 1) & 1, buf = warp + 2 * odd;
+                if (!active) continue;
+                // the group of (resident tile, parity of the streamed tile) owns the buffer
+                const int odd = tiles & 1, buf = warp + 2 * odd;
                 const int n = odd ? used[1]++ : used[0]++;
                 if (n > 0) wait(&s_empty[buf], n - 1);
                 if (!ok) break;
                 tc_fence_after_sync();
-                const uint64_t da = a_ring + stage * (Lay::kTile >> 4);
-                const uint64_t db = b_ring + (nb % kB) * (Lay::kTile >> 4);
-                const uint32_t d = tmem + kPwCols * buf;
-                pw_product<D>(d, da, db, kId, &s_full[buf]);
+                pw_product<D>(tmem + kPwCols * buf, a_ring + stage * (Lay::kTile >> 4),
+                              b_ring + (nb % kB) * (Lay::kTile >> 4), kId, &s_full[buf]);
             }
-            for (int j = 0; j < residents; ++j) {
-                if (ok && elect_one()) mma_commit(&a_empty[(na + j) % kA]);
-                __syncwarp();
-            }
+            if (ok && active && elect_one()) mma_commit(&a_empty[stage]);
+            __syncwarp();
             na += residents;
         }
         if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
     } else {
         // ------------------------------------------------------------------
-        // epilogue: group w owns buffer w.  Of two resident tiles it takes
-        // tile w % 2 with the streamed tiles of parity w / 2, of one every
-        // fourth streamed tile.  This thread owns lane r of every tile.
+        // epilogue: group w takes the products of resident tile w % 2 with
+        // the streamed tiles of parity w / 2 (buffer w); this thread owns
+        // lane r of every tile
         // ------------------------------------------------------------------
-        const int group = (warp >> 2) - 1;
+        const int group = (warp >> 2) - 1, res = group & 1, parity = group >> 1;
         const int r = (warp & 3) * 32 + lane;
         const uint32_t tile_addr = tmem + kPwCols * group + ((uint32_t)((warp & 3) * 32) << 16);
         const float sl = p.scale_log2;
@@ -324,32 +318,25 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         };
         PwWalk<kStats> walk;
         PwUnit U;
-        int tiles = 0, mine = 0, joins2 = 0, joins4 = 0, at_pair = -1, at_qt = -1, lse_at = 0;
+        int tiles = 0, mine = 0, joins = 0;
         while (walk.next(p, U)) {
             const PwSeq& s = walk.s;
-            const size_t pair = (size_t)U.b * p.num_kv_heads + U.g;
-            const int a = U.a, first = U.first, last = U.last;
-            const int steps = max(0, last - first);
+            const int steps = max(0, U.last - U.first);
             if (kStats && steps == 0) continue;
-            const bool two = walk.residents(U) == 2;
-            // the group's streamed tiles: first + skip, every `every`-th
-            const int every = two ? 2 : 4, skip = ((two ? group >> 1 : group) - tiles) & (every - 1);
+            const int skip = (parity - tiles) & 1;           // to the group's first streamed tile
             tiles += steps;
-            const int tile = 2 * a + (two ? group & 1 : 0), key = tile * kPwCols + r;
-            // one streamed tile is its group's alone; else the sharers are joined by the first
-            const int share = two ? group >> 1 : group;
-            const bool writer = steps == 1 ? skip == 0 : share == 0;
+            if (res >= walk.residents(U)) continue;
+            const size_t pair = (size_t)U.b * p.num_kv_heads + U.g;
+            const int tile = 2 * U.a + res, key = tile * kPwCols + r;
+            // one streamed tile is its group's alone; two groups are joined by the first
+            const bool writer = steps == 1 ? skip == 0 : parity == 0;
             float before = 0.f;
             if (!kStats && writer && p.query_chunks == 1 && p.weights && key < s.L - s.C)
                 before = p.weights[pair * p.weights_stride + key];
             float m = -INFINITY, z = 0.f;
-            auto join = [&](float2 o) {
-                if (kStats) join_stats(m, z, o);
-                else z += o.y;
-            };
             if constexpr (kStats) {
                 const int pos = min(s.L - s.counted + tile * p.tile_tokens + r / G, s.L - 1);
-                for (int kt = first + skip; kt < last; kt += every) {
+                for (int kt = U.first + skip; kt < U.last; kt += 2) {
                     wait(mine++);
                     const int visible = pos - kt * kPwCols;           // keys 0 .. visible of the tile
                     if (__all_sync(0xffffffffu, visible >= kPwCols - 1))
@@ -358,20 +345,16 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                         row_stats<true>(m, z, tile_addr, sl, sl2, visible, release);
                 }
             } else {
-                for (int qt = first + skip; qt < last; qt += every) {
-                    // the rows' lse, requested before the wait for the tile and kept
-                    // while the query tile stays the same
-                    const bool fresh = (int)pair != at_pair || qt != at_qt;
-                    float lse = 0.f;
-                    if (fresh)
-                        lse = p.lse[(pair * p.max_query_tiles + qt) * kPwCols + r];
+                // the rows' lse, requested a tile ahead
+                const float* src = p.lse + (pair * p.max_query_tiles + U.first + skip) * kPwCols + r;
+                float lse = U.first + skip < U.last ? *src : 0.f;
+                for (int qt = U.first + skip; qt < U.last; qt += 2) {
+                    float* ls = lse_s[group][mine & 1];
+                    ls[r] = -lse;
+                    src += 2 * kPwCols;
+                    if (qt + 2 < U.last) lse = *src;
                     wait(mine++);
-                    if (fresh) {
-                        at_pair = (int)pair, at_qt = qt, ++lse_at;
-                        lse_s[group][lse_at & 1][r] = -lse;
-                        asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
-                    }
-                    const float* ls = lse_s[group][lse_at & 1];
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
                     const int tokens = min(p.tile_tokens, s.counted - qt * p.tile_tokens);
                     // columns that see this key: from `lo` on, up to the chunk's end
                     const int lo = (key - (s.L - s.counted + qt * p.tile_tokens)) * G, hi = tokens * G;
@@ -382,22 +365,13 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                 }
             }
             if (steps > 1) {
-                // sharers of a tile: groups w and w + 2 of two resident tiles, all four of
-                // one.  Each kind has its two buffers: what a group writes was read before
-                // the barrier of that kind that it passed last.
-                if (two) {
-                    float2* o = other2[joins2++ & 1][group & 1];
-                    if (share > 0) o[r] = make_float2(m, z);
-                    asm volatile("bar.sync %0, 256;" ::"r"(5 + (group & 1)) : "memory");
-                    if (share == 0) join(o[r]);
-                } else {
-                    float2(*o)[kPwRows] = other4[joins4++ & 1];
-                    if (share > 0) o[share - 1][r] = make_float2(m, z);
-                    asm volatile("bar.sync 7, 512;" ::: "memory");
-                    if (share == 0) {
-#pragma unroll
-                        for (int i = 0; i < 3; ++i) join(o[i][r]);
-                    }
+                // two buffers: what a group writes was read before the barrier that it passed last
+                float2* o = other[joins++ & 1][res];
+                if (parity == 1) o[r] = make_float2(m, z);
+                asm volatile("bar.sync %0, 256;" ::"r"(5 + res) : "memory");
+                if (parity == 0) {
+                    if (kStats) join_stats(m, z, o[r]);
+                    else z += o[r].y;
                 }
             }
             if (!writer || failed) continue;
