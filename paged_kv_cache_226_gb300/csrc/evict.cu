@@ -270,6 +270,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
         __syncthreads();
         T |= digit_s << shift;
         want -= above_s;
+        // the whole bin stays: its lower bits do not matter
+        if (inside_s == want) break;
     }
     // where every equal stays, none needs its rank among them
     const bool ranked = inside_s != want;
