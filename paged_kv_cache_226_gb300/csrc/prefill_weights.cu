@@ -24,10 +24,11 @@
 // resident tiles (operand A) and streams others (operand B) past both, so
 // that a streamed tile is loaded once for two products; one persistent CTA
 // per SM walks its units, its rings running on from one unit to the next.
-// Six warps load with TMA: two for each stage of the ring that holds K tiles
+// Pass 1 has six warps that load with TMA: two for each stage of the K ring
 // (half of the 16-token boxes each, through the block table: a box costs its
 // warp some 120 cycles), three of them also for a stage each of the Q ring
-// (one box of tokens x heads per 64 dims).  Two warps issue the MMAs, one for
+// (one box of tokens x heads per 64 dims); pass 2, whose K tiles stay for a
+// unit, has one warp for each ring.  Two warps issue the MMAs, one for
 // each resident tile, into two 128-column buffers each: a single issuer
 // spends 1,060 cycles on its waits and commits per tile, twice what the
 // product takes.  Four groups of four warps take the finished tiles.  Rows of
@@ -140,8 +141,13 @@ __device__ __forceinline__ float joined_lse(const PrefillWeightsParams& p, const
     return r < tokens * p.group ? m + log2f(z) : INFINITY;
 }
 
+// Pass 1 loads a K tile per step, pass 2 two per unit: six loading warps (80
+// registers a thread) and two (96, which the column sums need: 303 us against
+// 222 where they spill).
+__host__ __device__ constexpr int pw_loaders(bool stats) { return stats ? 6 : 2; }
+
 template <typename T, int D, bool kStats>
-__global__ void __launch_bounds__(kPwThreads, 1)
+__global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
     prefill_weights_kernel(const __grid_constant__ CUtensorMap tmap_k,
                            const __grid_constant__ CUtensorMap tmap_q,
                            const __grid_constant__ PrefillWeightsParams p) {
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     __shared__ __align__(8) uint64_t a_full[kA], a_empty[kA], b_full[kB], b_empty[kB];
     __shared__ __align__(8) uint64_t s_full[kPwBufs], s_empty[kPwBufs];
     __shared__ uint32_t tmem_base;
-    __shared__ __align__(16) float lse_s[kPwGroups][2][kPwCols];     // pass 2: [group][tile parity]
+    __shared__ __align__(16) float4 lse_s[4 * kPwGroups][2][kPwCols / 4];   // pass 2: [warp][tile parity]
     __shared__ float2 other[2][2][kPwRows];                          // [join parity][resident tile]
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -163,8 +169,9 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     const int q_rows = p.tile_tokens * G;                    // rows of a query tile, <= 128
 
     if (threadIdx.x == 0) {
-        // K stages have two loaders; a resident tile has one issuer, a streamed tile both
-        for (int i = 0; i < kA; ++i) mbar_init(&a_full[i], kStats ? 1 : 2), mbar_init(&a_empty[i], 1);
+        // pass 1 has two loaders for each K stage; a resident tile has one issuer, a streamed
+        // tile both
+        for (int i = 0; i < kA; ++i) mbar_init(&a_full[i], 1), mbar_init(&a_empty[i], 1);
         for (int i = 0; i < kB; ++i) mbar_init(&b_full[i], kStats ? 2 : 1), mbar_init(&b_empty[i], 2);
         for (int i = 0; i < kPwBufs; ++i) mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4);
         fence_barrier_init();
@@ -172,7 +179,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     if (warp == 0) tmem_alloc(&tmem_base, kPwBufs * kPwCols);
     if (!kStats && q_rows < kPwCols) {
         // rows that no query box fills stay zero (their lse is +inf)
-        for (int i = threadIdx.x; i < kB * Lay::kTile / 16; i += kPwThreads)
+        for (int i = threadIdx.x; i < kB * Lay::kTile / 16; i += pw_threads(pw_loaders(kStats)))
             reinterpret_cast<uint4*>(smem + kA * Lay::kTile)[i] = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
     }
@@ -190,8 +197,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         // phase: a parity says no more than that, and a loader that had not
         // waited for that phase would take the one before it for its own.
         // ------------------------------------------------------------------
+        // Pass 1: warp w has Q stage w (of three) and half of the boxes of K
+        // stage w % 3.  Pass 2: warp 0 has the Q stages, warp 1 the K stages.
         const int who = warp < 4 ? warp - 2 : warp - kPwLoadersAfter + 2;
-        const int k_stage = who % 3, part = who / 3;
+        auto mine_a = [&](int n) { return kStats ? n % kA == who : who == 1; };
+        auto mine_b = [&](int n) { return kStats ? n % kB == who % 3 : who == 0; };
         if (lane == 0) prefetch_tensor_map(&tmap_q), prefetch_tensor_map(&tmap_k);
         // waits for stage n % stages to be free
         auto open = [&](uint64_t* empty, int stages, int n) -> bool {
@@ -200,8 +210,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         auto load_k = [&](uint8_t* dst, uint64_t* full, uint64_t* empty, int stages, int n,
                           const PwSeq& s, const PwUnit& U, int kt, int blk) -> bool {
             if (!open(empty, stages, n)) return false;
-            pw_load_keys<D>(&tmap_k, dst + (n % stages) * Lay::kTile, &full[n % stages], p, s, U.g, kt, blk,
-                            part, 8, 2);
+            pw_load_keys<D, kStats ? 4 : 8>(&tmap_k, dst + (n % stages) * Lay::kTile, &full[n % stages], p, s,
+                                            U.g, kt, blk, kStats ? who / 3 : 0, 8, kStats ? 2 : 1);
             return true;
         };
         auto load_q = [&](uint8_t* dst, uint64_t* full, uint64_t* empty, int stages, int n,
@@ -216,7 +226,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         PwUnit U;
         int na = 0, nb = 0, at_b = -1, at_g = -1, at_qt = -1;
         bool ok = true;
-        static_assert(kA == 3 && kB == 3 && kPwLoaders == 6, "two loaders for each K stage");
+        static_assert(kA == 3 && kB == 3 && pw_loaders(true) == 6, "two loaders for each K stage");
         while (ok && walk.next(p, U)) {
             // block ids of the current four key tiles and of the next four
             int quad = -2, blk = 0, blk_next = 0;
@@ -229,7 +239,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             if (U.first >= U.last) continue;
             for (int j = 0; ok && j < walk.residents(U); ++j) {
                 if (!kStats) to_tile(2 * U.a + j);
-                if (na % kA == (kStats ? who : k_stage))
+                if (mine_a(na))
                     ok = kStats ? load_q(a_ring, a_full, a_empty, kA, na, walk.s, U, 2 * U.a + j)
                                 : load_k(a_ring, a_full, a_empty, kA, na, walk.s, U, 2 * U.a + j, blk);
                 ++na;
@@ -241,7 +251,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                     if (U.b == at_b && U.g == at_g && i == at_qt) continue;     // still there
                     at_b = U.b, at_g = U.g, at_qt = i;
                 }
-                if (nb % kB == (kStats ? k_stage : who))
+                if (mine_b(nb))
                     ok = kStats ? load_k(b_ring, b_full, b_empty, kB, nb, walk.s, U, i, blk)
                                 : load_q(b_ring, b_full, b_empty, kB, nb, walk.s, U, i);
                 ++nb;
@@ -345,16 +355,19 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                         row_stats<true>(m, z, tile_addr, sl, sl2, visible, release);
                 }
             } else {
-                // the rows' lse, requested a tile ahead
-                const float* src = p.lse + (pair * p.max_query_tiles + U.first + skip) * kPwCols + r;
-                float lse = U.first + skip < U.last ? *src : 0.f;
+                // the streamed rows' -lse, a copy to each warp (no barrier of the
+                // group), requested a tile ahead
+                const float4* src = reinterpret_cast<const float4*>(
+                    p.lse + (pair * p.max_query_tiles + U.first + skip) * kPwCols) + lane;
+                float4 lse = U.first + skip < U.last ? *src : make_float4(0.f, 0.f, 0.f, 0.f);
                 for (int qt = U.first + skip; qt < U.last; qt += 2) {
-                    float* ls = lse_s[group][mine & 1];
-                    ls[r] = -lse;
-                    src += 2 * kPwCols;
+                    float4* ls4 = lse_s[warp - 4][mine & 1];
+                    ls4[lane] = make_float4(-lse.x, -lse.y, -lse.z, -lse.w);
+                    src += 2 * (kPwCols / 4);
                     if (qt + 2 < U.last) lse = *src;
+                    __syncwarp();
+                    const float* ls = reinterpret_cast<const float*>(ls4);
                     wait(mine++);
-                    asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
                     const int tokens = min(p.tile_tokens, s.counted - qt * p.tile_tokens);
                     // columns that see this key: from `lo` on, up to the chunk's end
                     const int lo = (key - (s.L - s.counted + qt * p.tile_tokens)) * G, hi = tokens * G;
@@ -475,16 +488,16 @@ cudaError_t launch_prefill_weights_t(const CUtensorMap& tmk, const CUtensorMap& 
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(prefill_weights_kernel<T, D, false>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    const dim3 grid(sms), threads(kPwThreads);
+    const dim3 grid(sms), threads1(pw_threads(pw_loaders(true))), threads2(pw_threads(pw_loaders(false)));
     if (e == cudaSuccess && p.max_counted > 0) {
-        e = launch_with_pdl(prefill_weights_kernel<T, D, true>, grid, threads, smem, stream, tmk, tmq, p);
+        e = launch_with_pdl(prefill_weights_kernel<T, D, true>, grid, threads1, smem, stream, tmk, tmq, p);
         if (e == cudaSuccess && p.key_chunks > 1)
             e = launch_with_pdl(prefill_stats_join_kernel,
                                 dim3(p.max_query_tiles, p.num_kv_heads, p.num_seqs), dim3(kPwRows), 0,
                                 stream, p);
     }
     if (e == cudaSuccess)
-        e = launch_with_pdl(prefill_weights_kernel<T, D, false>, grid, threads, smem, stream, tmk, tmq, p);
+        e = launch_with_pdl(prefill_weights_kernel<T, D, false>, grid, threads2, smem, stream, tmk, tmq, p);
     if (e == cudaSuccess && p.query_chunks > 1)
         e = launch_with_pdl(prefill_columns_join_kernel,
                             dim3((p.max_context + kPwJoinThreads - 1) / kPwJoinThreads, p.num_kv_heads,

@@ -13,9 +13,12 @@ constexpr int kPwRows = 128;                   // lanes: rows of a resident tile
 constexpr int kPwCols = 128;                   // columns: rows of a streamed tile
 constexpr int kPwBufs = 4;                     // accumulators in tensor memory
 constexpr int kPwGroups = 4;                   // epilogue groups of four warps, one per buffer
-constexpr int kPwLoadersAfter = 4 + 4 * kPwGroups;   // warps 0, 1 issue MMAs; 2, 3, 20 .. 23 load
-constexpr int kPwLoaders = 6;
-constexpr int kPwThreads = (kPwLoadersAfter + kPwLoaders - 2) * 32;
+// Warps 0 and 1 issue MMAs, 2 and 3 load, 4 .. 19 are the epilogue's, and
+// where six warps load, 20 .. 23 do too.
+constexpr int kPwLoadersAfter = 4 + 4 * kPwGroups;
+__host__ __device__ constexpr int pw_threads(int loaders) {
+    return (kPwLoadersAfter + loaders - 2) * 32;
+}
 
 template <int D>
 struct PwLayout {
@@ -128,28 +131,31 @@ template <bool kMask, typename Release>
 __device__ __forceinline__ float column_sums(uint32_t tile_addr, const float* neg_lse, uint64_t sl2,
                                              int lo, int hi, Release&& release) {
     uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
+    uint32_t v[2][32];                       // the next 32 columns arrive while these are added
+    tmem_ld32(tile_addr, v[0]);
+    tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < kPwCols; c += 32) {
-        uint32_t v[32];
-        tmem_ld32(tile_addr + c, v);
-        tmem_wait_ld();
-        if (c == kPwCols - 32) release();
+    for (int c = 0; c < kPwCols / 32; ++c) {
+        if (c < 3) tmem_ld32(tile_addr + 32 * (c + 1), v[(c + 1) & 1]);
+        const uint32_t(&x)[32] = v[c & 1];
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(neg_lse + c + e);
+            const float4 l = *reinterpret_cast<const float4*>(neg_lse + 32 * c + e);
             float a[4];
-            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2,
+            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sl2,
                                    f32x2_pack(l.x, l.y)), a[0], a[1]);
-            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sl2,
+            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), sl2,
                                    f32x2_pack(l.z, l.w)), a[2], a[3]);
             if (kMask) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    a[i] = c + e + i >= lo && c + e + i < hi ? a[i] : -INFINITY;
+                    a[i] = 32 * c + e + i >= lo && 32 * c + e + i < hi ? a[i] : -INFINITY;
             }
             ps[(e >> 1) & 3] = f32x2_add(ps[(e >> 1) & 3], f32x2_pack(ex2(a[0]), ex2(a[1])));
             ps[((e >> 1) + 1) & 3] = f32x2_add(ps[((e >> 1) + 1) & 3], f32x2_pack(ex2(a[2]), ex2(a[3])));
         }
+        if (c < 3) tmem_wait_ld();
+        if (c == 2) release();
     }
     return sum8(ps);
 }
@@ -163,9 +169,9 @@ __device__ __forceinline__ int pw_blocks(const PrefillWeightsParams& p, const Pw
     return blk;
 }
 
-// Boxes [from, to) of key tile kt (its tokens through the block table: `blk`
+// Boxes from, from + step, ... below `to` (kMost at most) of key tile kt (its tokens through the block table: `blk`
 // as pw_blocks gives it), announced on `bar` and issued; all lanes run along.
-template <int D>
+template <int D, int kMost>
 __device__ __forceinline__ void pw_load_keys(const CUtensorMap* map, uint8_t* dst, uint64_t* bar,
                                              const PrefillWeightsParams& p, const PwSeq& s, int g,
                                              int kt, int blk, int from, int to, int step) {
@@ -176,7 +182,7 @@ __device__ __forceinline__ void pw_load_keys(const CUtensorMap* map, uint8_t* ds
     __syncwarp();
     const int sub_mask = p.block_size - 1;               // 16 or 32
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kMost; ++i) {
         const int box = from + i * step;
         if (i >= own) break;
         const int pblk = __shfl_sync(0xffffffffu, blk, (kt & 3) * 8 + box);

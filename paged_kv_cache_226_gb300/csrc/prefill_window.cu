@@ -27,6 +27,7 @@ namespace pa {
 
 constexpr int kWkStages = 4;                   // key tiles in flight
 constexpr int kWqStages = 2;                   // query tiles: a row's and the next's
+constexpr int kWindowThreads = pw_threads(6);
 constexpr int kMaxWindowCtas = 256;            // bounds the records of a row
 
 // A run of key tiles [k0, k1) of one row, counted in the walk's direction;
@@ -86,7 +87,7 @@ struct PwRuns {
 };
 
 template <typename T, int D, bool kStats>
-__global__ void __launch_bounds__(kPwThreads, 1)
+__global__ void __launch_bounds__(kWindowThreads, 1)
     window_weights_kernel(const __grid_constant__ CUtensorMap tmap_k,
                           const __grid_constant__ CUtensorMap tmap_q,
                           const __grid_constant__ PrefillWeightsParams p) {
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     if (warp == 0) tmem_alloc(&tmem_base, kPwBufs * kPwCols);
     if (!kStats && q_rows < kPwCols) {
         // rows that no query box fills stay zero (their lse is +inf)
-        for (int i = threadIdx.x; i < kWqStages * Lay::kTile / 16; i += kPwThreads)
+        for (int i = threadIdx.x; i < kWqStages * Lay::kTile / 16; i += kWindowThreads)
             reinterpret_cast<uint4*>(q_ring)[i] = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
     }
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     // key tiles of the batch (the count fits 31 bits: checked on the host)
     {
         unsigned n = 0;
-        for (int b = threadIdx.x; b < p.num_seqs; b += kPwThreads) {
+        for (int b = threadIdx.x; b < p.num_seqs; b += kWindowThreads) {
             PwSeq s;
             pw_sequence(p, b, (kStats || p.max_counted == 0) && blockIdx.x == 0, s);
             n += (unsigned)s.n_kt * p.num_kv_heads;
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                 if (who != st && who != 4 + (n & 1)) continue;
                 if (n >= kWkStages) ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[st], (n / kWkStages - 1) & 1));
                 if (ok)
-                    pw_load_keys<D>(&tmap_k, k_ring + st * Lay::kTile, &k_full[st], p, s, R.g, kt, blk,
+                    pw_load_keys<D, 4>(&tmap_k, k_ring + st * Lay::kTile, &k_full[st], p, s, R.g, kt, blk,
                                     who < 4 ? 0 : 4, who < 4 ? 4 : 8, 1);
             }
         }
@@ -362,7 +363,7 @@ cudaError_t launch_window_weights_t(const CUtensorMap& tmk, const CUtensorMap& t
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // both passes deal the tiles out to the same number of CTAs
-    const dim3 grid(std::min(sms, kMaxWindowCtas)), threads(kPwThreads);
+    const dim3 grid(std::min(sms, kMaxWindowCtas)), threads(kWindowThreads);
     if (p.max_counted > 0)
         e = launch_with_pdl(window_weights_kernel<T, D, true>, grid, threads, smem, stream, tmk, tmq, p);
     if (e == cudaSuccess)
