@@ -350,9 +350,9 @@ __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
                     wait(mine++);
                     const int visible = pos - kt * kPwCols;           // keys 0 .. visible of the tile
                     if (__all_sync(0xffffffffu, visible >= kPwCols - 1))
-                        row_stats<false>(m, z, tile_addr, sl, sl2, visible, release);
+                        row_stats<false, false>(m, z, tile_addr, sl, sl2, visible, release);
                     else
-                        row_stats<true>(m, z, tile_addr, sl, sl2, visible, release);
+                        row_stats<true, false>(m, z, tile_addr, sl, sl2, visible, release);
                 }
             } else {
                 // the streamed rows' -lse, a copy to each warp (no barrier of the

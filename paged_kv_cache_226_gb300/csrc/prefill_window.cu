@@ -273,9 +273,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                     wait(mine++);
                     const int visible = pos - k * kPwCols;
                     if (__all_sync(0xffffffffu, visible >= kPwCols - 1))
-                        row_stats<false>(m, z, tile_addr, sl, sl2, visible, release);
+                        row_stats<false, true>(m, z, tile_addr, sl, sl2, visible, release);
                     else
-                        row_stats<true>(m, z, tile_addr, sl, sl2, visible, release);
+                        row_stats<true, true>(m, z, tile_addr, sl, sl2, visible, release);
                 }
                 // one tile is its group's alone, more are joined by the first group
                 bool writer = group == 0;
