@@ -1134,8 +1134,10 @@ class StepPlan:
     Holds the C-ABI argument lists of the step for fixed tensors, so that
     each launch costs one ctypes call.  Modes: ``"fused"`` (the default: one
     pa_decode_step launch), ``"split"`` (reshape_and_cache, decode_split,
-    reduce) and ``"single"`` (reshape_and_cache, decode).  The work goes to the caller's current stream at
-    call time, which also makes a step capturable into a CUDA graph
+    reduce), ``"single"`` (reshape_and_cache, decode) and ``"weights"``
+    (reshape_and_cache, decode_weights: each step adds the attention weights
+    into ``weights``, or reads them there and writes ``weights_out``;
+    ``capture_graph`` makes one such step before it captures).  The work goes to the caller's current stream at call time, which also makes a step capturable into a CUDA graph
     (``capture_graph``).  The tensors must stay alive and keep their shapes;
     their contents (new tokens, tables, lengths) may change between steps as
     long as ``context_lens`` stays within ``max_context_len``.
@@ -1156,19 +1158,24 @@ class StepPlan:
     def __init__(self, q, k_new, v_new, slot_mapping, k_cache, v_cache, block_tables,
                  context_lens, scale: float, max_context_len: int, out=None,
                  mode: str = "auto", partition_size: Optional[int] = None, workspace=None,
-                 k_scale: Optional[float] = None, v_scale: Optional[float] = None):
+                 k_scale: Optional[float] = None, v_scale: Optional[float] = None,
+                 weights: Optional[torch.Tensor] = None,
+                 weights_out: Optional[torch.Tensor] = None):
         self._lib = load()
         self.fp8 = k_cache.dtype == torch.uint8
         if mode == "auto":
             mode = "fused"
-        if mode not in ("single", "split", "fused", "balanced"):
+        if mode not in ("single", "split", "fused", "balanced", "weights"):
             raise ValueError(f"unknown mode {mode!r}")
+        if (weights is None) == (mode == "weights") or (weights_out is not None and weights is None):
+            raise ValueError("weights belong to mode \"weights\", which needs them")
         host_ok = mode == "fused"            # pinned host inputs / output allowed
         if self.fp8:
             if k_scale is None or v_scale is None:
                 raise ValueError("an FP8 cache needs k_scale and v_scale")
-            if mode not in ("fused", "balanced"):
-                raise ValueError("StepPlan runs an FP8 cache through the fused steps only")
+            if mode not in ("fused", "balanced", "weights"):
+                raise ValueError("StepPlan runs an FP8 cache through the fused steps and "
+                                 "decode_weights only")
             shp, dev = _fp8_common(q, k_cache, v_cache, block_tables, context_lens, host_ok)
         else:
             shp, dev = _decode_common(q, k_cache, v_cache, block_tables, context_lens, host_ok)
@@ -1181,10 +1188,13 @@ class StepPlan:
         self.device = dev
         self.out = torch.empty(q.shape, dtype=q.dtype, device=dev) if out is None else out
         _need(self.out, "out", q.dtype, dev, host_ok)
-        if mode in ("fused", "balanced") and T != q.shape[0]:
-            raise ValueError("the fused step takes exactly one new token per sequence")
+        if mode in ("fused", "balanced", "weights") and T != q.shape[0]:
+            raise ValueError("the step takes exactly one new token per sequence")
         self.mode = mode
-        if partition_size is None:
+        if partition_size is None and mode == "weights":
+            partition_size = weights_partition(q.shape[0], k_cache.shape[2], int(max_context_len),
+                                               self.fp8, dev.index)
+        elif partition_size is None:
             partition_size = choose_partition(
                 q.shape[0], k_cache.shape[2], max_context_len, k_cache.shape[1], dev,
                 context_lens if context_lens.device.type == "cpu" else None)
@@ -1196,7 +1206,24 @@ class StepPlan:
         sref = ctypes.byref(self._shape)
         self._reshape_args = (_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(k_cache),
                               _ptr(v_cache), ctypes.c_int64(T), sref)
-        if mode == "single":
+        if mode == "weights":
+            B, hkv, tokens = q.shape[0], k_cache.shape[2], block_tables.shape[1] * k_cache.shape[1]
+            weights_out = _weights_pair(weights, weights_out, (B, hkv, tokens), dev, dev.index)
+            self.weights_out = weights_out
+            scales = (ctypes.c_float(k_scale), ctypes.c_float(v_scale)) if self.fp8 else ()
+            if self.fp8:
+                self._reshape_args = (*self._reshape_args[:-1], *scales, sref)
+            workspace, nbytes = _workspace(workspace, self._lib.pa_decode_weights_workspace_size(
+                sref, int(max_context_len), self.partition_size) if B else 1, "pa_decode_weights", dev)
+            self.workspace = workspace
+            self._keep += [workspace, weights, weights_out]
+            self._decode_args = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                                 _ptr(context_lens), ctypes.c_float(scale), *scales,
+                                 ctypes.c_int32(int(max_context_len)),
+                                 ctypes.c_int32(self.partition_size), _ptr(weights),
+                                 _ptr(weights_out), ctypes.c_int64(weights_out.shape[2]),
+                                 _ptr(workspace), ctypes.c_size_t(nbytes), _ptr(self.out), sref)
+        elif mode == "single":
             self._decode_args = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                  _ptr(context_lens), ctypes.c_float(scale), _ptr(self.out), sref)
         elif mode == "balanced":
@@ -1249,11 +1276,14 @@ class StepPlan:
     def reshape_and_cache(self):
         if self.mode in ("fused", "balanced"):
             return                          # part of the fused step
-        _check("pa_reshape_and_cache",
-               self._lib.pa_reshape_and_cache(*self._reshape_args, self._stream()))
+        fn = self._lib.pa_reshape_and_cache_fp8 if self.fp8 else self._lib.pa_reshape_and_cache
+        _check("pa_reshape_and_cache", fn(*self._reshape_args, self._stream()))
 
     def decode(self):
-        if self.mode == "balanced":
+        if self.mode == "weights":
+            fn = self._lib.pa_decode_weights_fp8 if self.fp8 else self._lib.pa_decode_weights
+            _check("pa_decode_weights", fn(*self._decode_args, self._stream()))
+        elif self.mode == "balanced":
             fn = self._lib.pa_decode_step_balanced_fp8 if self.fp8 else \
                 self._lib.pa_decode_step_balanced
             _check("pa_decode_step_balanced", fn(*self._step_args, self._stream()))

@@ -254,3 +254,40 @@ def test_refusals(dev):
                 dict(workspace=torch.zeros(1, dtype=torch.uint8, device=dev))):
         with pytest.raises(lib.PaError):
             lib.prefill_weights(**{**p, **bad})
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_step_plan(dev, fp8):
+    """StepPlan's weights mode: the cache write and the weighing decode, called,
+    and replayed as a graph on new contents, equal the calls one by one."""
+    x = Batch([300, 17, 64], 8, 2, 128, 16, BF16, seed=51, fp8=fp8, stale=False)
+    kn, vn = (torch.randn(3, 2, 128, generator=x.gen).to(BF16).to(dev) for _ in range(2))
+    at = (x.lens - 1).long()
+    slots = (x.tables[torch.arange(3), at // 16].long() * 16 + at % 16).to(dev)
+    start = x.state().nan_to_num(0.0).to(dev)
+
+    def one_by_one(q, weights):
+        k, v = x.k.to(dev), x.v.to(dev)
+        if fp8:
+            lib.reshape_and_cache_fp8(kn, vn, slots, k, v, x.k_scale, x.v_scale)
+        else:
+            lib.reshape_and_cache(kn, vn, slots, k, v)
+        out, w = lib.decode_weights(q, k, v, x.tables.to(dev), x.lens.to(dev), x.scale, 300, weights=weights.clone(),
+                                    **x.scales())
+        return out, w, k
+
+    q, k, v, w = x.q.to(dev), x.k.to(dev), x.v.to(dev), start.clone()
+    plan = lib.StepPlan(q, kn, vn, slots, k, v, x.tables.to(dev), x.lens.to(dev), x.scale, 300, mode="weights",
+                        weights=w, **x.scales())
+    want = one_by_one(q, start)
+    assert same_bits(plan(), want[0]) and same_bits(w, want[1]) and same_bits(k, want[2])
+    plan.capture_graph()
+    q.copy_(torch.randn(q.shape, generator=x.gen))
+    w.copy_(start)
+    want = one_by_one(q, start)
+    assert same_bits(plan.replay(), want[0]) and same_bits(plan.weights_out, want[1])
+    with pytest.raises(ValueError):
+        lib.StepPlan(q, kn, vn, slots, k, v, x.tables.to(dev), x.lens.to(dev), x.scale, 300, mode="weights", **x.scales())
+    with pytest.raises(ValueError):
+        lib.StepPlan(q, kn, vn, slots, k, v, x.tables.to(dev), x.lens.to(dev), x.scale, 300, weights=w, **x.scales())
+    assert lib.read_device_errors(dev) == 0
