@@ -1,4 +1,6 @@
-"""Build libpa.so (the CUDA kernels and their C ABI) in-tree with nvcc.
+"""Build libpa.so (the CUDA kernels and their C ABI) in-tree with nvcc, and
+_native.so, the Python binding of some of its calls, with the host compiler
+against the installed PyTorch.
 
     python -m paged_kv_cache_226_gb300.build [--force]
 
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +24,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libpa.so")
+# csrc/binding.cpp, compiled
+BINDING = os.path.join(CSRC, "binding.cpp")
+NATIVE_PATH = os.path.join(PKG, "_native.so")
 # the same sources with the failure-detection test hooks (include/pa_test.h)
 TEST_BUILD_DIR = os.path.join(PKG, "_build_test")
 TEST_LIB_PATH = os.path.join(PKG, "libpa_test.so")
@@ -53,15 +59,65 @@ def up_to_date(lib_path: str = LIB_PATH) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _native_stamp() -> str:
+    """What _native.so depends on besides its source."""
+    import torch
+    return f"{torch.__version__} {torch.__path__[0]} {sys.version}"
+
+
+def native_up_to_date() -> bool:
+    stamp = os.path.join(BUILD_DIR, "native.stamp")
+    if not (os.path.exists(NATIVE_PATH) and os.path.exists(stamp)):
+        return False
+    with open(stamp) as f:
+        if f.read() != _native_stamp():
+            return False
+    t = os.path.getmtime(NATIVE_PATH)
+    return all(os.path.getmtime(p) <= t
+               for p in [BINDING, os.path.join(INCLUDE, "pa.h"), os.path.abspath(__file__)])
+
+
+def _compile_native() -> str:
+    """binding.cpp to an object file."""
+    import torch
+    inc = os.path.join(torch.__path__[0], "include")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    obj = os.path.join(BUILD_DIR, "binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem",
+           os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-c", BINDING, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_native(obj: str) -> None:
+    import torch
+    tmp = NATIVE_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libpa.so", "-Wl,-rpath,$ORIGIN", "-L",
+           os.path.join(torch.__path__[0], "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE_PATH)
+    with open(os.path.join(BUILD_DIR, "native.stamp"), "w") as f:
+        f.write(_native_stamp())
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(),
           test_hooks: bool = False) -> str:
-    """Build libpa.so (or, with test_hooks, libpa_test.so: the same sources
-    compiled with -DPA_TEST_HOOKS) and return its path."""
+    """Build libpa.so and _native.so (or, with test_hooks, libpa_test.so: the
+    CUDA sources compiled with -DPA_TEST_HOOKS) and return the library's path."""
     lib_path = TEST_LIB_PATH if test_hooks else LIB_PATH
     build_dir = TEST_BUILD_DIR if test_hooks else BUILD_DIR
     if test_hooks:
         extra_flags = (*extra_flags, "-DPA_TEST_HOOKS=1")
-    if not force and up_to_date(lib_path):
+    kernels = force or not up_to_date(lib_path)
+    native = not test_hooks and (force or not native_up_to_date())
+    if not kernels and not native:
         return lib_path
     nvcc = _nvcc()
     os.makedirs(build_dir, exist_ok=True)
@@ -78,14 +134,23 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(),
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        objs = list(ex.map(compile_one, sources()))
+        binding = ex.submit(_compile_native) if native else None
+        objs = list(ex.map(compile_one, sources())) if kernels else []
+    if kernels:
+        _link(nvcc, lib_path, objs)
+    if native:
+        _link_native(binding.result())
+    return lib_path
+
+
+def _link(nvcc: str, lib_path: str, objs) -> None:
     tmp = lib_path + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "--cudart", "static", "-o", tmp, *objs]
+    cmd = [nvcc, *ARCH, "-shared", "--cudart", "static", "-Xlinker",
+           f"-soname={os.path.basename(lib_path)}", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib_path)
-    return lib_path
 
 
 if __name__ == "__main__":

@@ -645,58 +645,32 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
     return inv.to(torch.float32).to(device or "cpu"), mult
 
 
-# These calls are made per layer and step, so their checks are single
-# expressions that touch each tensor property once; what fails goes through
-# the checks that say why.
+_native = None
+
+
+def _load_native():
+    """The binding of the bounded-cache calls (csrc/binding.cpp): their checks
+    and allocations in native code, since a layer makes three of them per step."""
+    global _native
+    load()
+    try:
+        from . import _native as native
+    except ImportError as e:
+        raise ImportError(f"_native.so cannot be loaded ({e}); build it with "
+                          "`python -m paged_kv_cache_226_gb300.build`") from e
+    _native = native
+    return native
+
+
+def _refused(name: str, k_cache: torch.Tensor, status: int) -> None:
+    _check(name + "_fp8" if k_cache.dtype is torch.uint8 else name, status)
+
 
 def _must(t: torch.Tensor, name: str, dtype, device: torch.device, index: int) -> None:
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
             and t.is_contiguous()):
         _need(t, name, dtype, device)
         raise ValueError(f"{name} must be contiguous, {dtype}, on {device}")
-
-
-def _rows(t: torch.Tensor, name: str, heads: int, dim: int, dtype, index: int) -> Tuple[int, int]:
-    """(tokens, token stride) of a [T][heads][dim] tensor whose rows are contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
-        raise ValueError(f"{name} must be [num_tokens][{heads}][{dim}]")
-    s0, s1, s2 = t.stride()
-    if (s2 != 1 and dim > 1) or (s1 != dim and heads > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return shape[0], s0 if shape[0] > 1 else heads * dim
-
-
-def _scales(fp8: bool, k_scale, v_scale) -> None:
-    """The scales go with an E4M3 cache or not at all."""
-    if fp8 and (k_scale is None or v_scale is None):
-        raise ValueError("an FP8 cache needs k_scale and v_scale")
-    if not fp8 and (k_scale is not None or v_scale is not None):
-        raise ValueError("k_scale and v_scale belong to an FP8 cache")
-
-
-def _pools(k_cache: torch.Tensor, v_cache: torch.Tensor):
-    """(device, its index, shape, dtype) of two alike cache tensors."""
-    _need(k_cache, "k_cache")
-    dev, dtype, shape = k_cache.device, k_cache.dtype, k_cache.shape
-    if v_cache is not k_cache:
-        _must(v_cache, "v_cache", dtype, dev, dev.index)
-    if len(shape) != 4 or v_cache.shape != shape:
-        raise ValueError("caches must be [num_blocks][block_size][num_kv_heads][head_dim]")
-    if dtype is not torch.uint8 and dtype not in _DTYPE_CODES:
-        raise TypeError(f"cache dtype must be float16, bfloat16 or uint8 (E4M3), got {dtype}")
-    return dev, dev.index, shape, dtype
-
-
-def _pool_shape(num_seqs: int, num_q_heads: int, pool, max_blocks: int, dtype) -> PaShape:
-    return PaShape(num_seqs, num_q_heads, pool[2], pool[3], pool[1], max_blocks, pool[0],
-                   _DTYPE_CODES[dtype], 0)
 
 
 def _state(t: torch.Tensor, name: str, shape, dtype, device, index: int) -> None:
@@ -730,21 +704,6 @@ def _workspace(workspace: Optional[torch.Tensor], nbytes: int, fn: str, device):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
-
-
-def _call(fn, name: str, device: torch.device, index: int, *args) -> None:
-    """Calls an entry point on the device's current stream, with that device current."""
-    if torch.cuda.current_device() == index:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    if status != PA_OK:
-        _check(name, status)
-
-
 def rope_and_cache(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
                    positions: torch.Tensor, slot_mapping: torch.Tensor, inv_freq: torch.Tensor,
                    k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -759,45 +718,12 @@ def rope_and_cache(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     projection's output will do); ``q=None`` writes the cache only.
     positions, slot_mapping: int64 [T]; inv_freq: fp32 [R/2], the first R dims
     of a head turn (``rope_frequencies``).  ``q_out=q`` turns q in place."""
-    lib = load()
-    dev, idx, pool, dtype = _pools(k_cache, v_cache)
-    fp8 = dtype is torch.uint8
-    _scales(fp8, k_scale, v_scale)
-    hkv, d = pool[2], pool[3]
-    kdt = k.dtype
-    if kdt not in _DTYPE_CODES or not (fp8 or kdt is dtype):
-        raise TypeError(f"k must have the cache's 16-bit dtype, got {kdt}")
-    T, ks = _rows(k, "k", hkv, d, kdt, idx)
-    vt, vs = _rows(v, "v", hkv, d, kdt, idx)
-    _must(positions, "positions", torch.int64, dev, idx)
-    _must(slot_mapping, "slot_mapping", torch.int64, dev, idx)
-    _must(inv_freq, "inv_freq", torch.float32, dev, idx)
-    if vt != T or positions.shape != (T,) or slot_mapping.shape != (T,) or inv_freq.dim() != 1:
-        raise ValueError("v, positions and slot_mapping must have a row per token of k, "
-                         "inv_freq one dimension")
-    hq = qs = os_ = 0
-    if q is not None:
-        hq = q.shape[1] if q.dim() == 3 else 0
-        qt, qs = _rows(q, "q", hq, d, kdt, idx)
-        if q_out is None:
-            q_out = torch.empty((T, hq, d), dtype=kdt, device=dev)
-            ot, os_ = T, hq * d
-        else:
-            ot, os_ = _rows(q_out, "q_out", hq, d, kdt, idx)
-        if qt != T or ot != T:
-            raise ValueError("q and q_out must have a row per token of k")
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    ref = ctypes.byref(_pool_shape(0, hq, pool, 1, kdt))
-    args = (_addr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
-            slot_mapping.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0],
-            1 if interleaved else 0, factor, _addr(q_out), os_, k_cache.data_ptr(),
-            v_cache.data_ptr(), T)
-    if fp8:
-        _call(lib.pa_rope_and_cache_fp8, "pa_rope_and_cache_fp8", dev, idx, *args, k_scale, v_scale, ref)
-    else:
-        _call(lib.pa_rope_and_cache, "pa_rope_and_cache", dev, idx, *args, ref)
-    return q_out
+    r = (_native or _load_native()).rope_and_cache(
+        q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cache, q_out, interleaved, factor,
+        k_scale, v_scale)
+    if r.__class__ is int:
+        _refused("pa_rope_and_cache", k_cache, r)
+    return r
 
 
 @functools.lru_cache(maxsize=1024)
@@ -829,16 +755,6 @@ def weights_partition(num_seqs: int, num_kv_heads: int, max_context_len: int, fp
     return min(size, 1024)
 
 
-def _batch(block_tables: torch.Tensor, context_lens: torch.Tensor, device, index: int) -> Tuple[int, int]:
-    """(sequences, blocks per sequence) of a batch's tables and lengths."""
-    _must(block_tables, "block_tables", torch.int32, device, index)
-    _must(context_lens, "context_lens", torch.int32, device, index)
-    shape = block_tables.shape
-    if len(shape) != 2 or context_lens.shape != shape[:1]:
-        raise ValueError("block_tables must be [num_seqs][blocks], context_lens [num_seqs]")
-    return shape
-
-
 def decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                    block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
                    max_context_len: int, weights: Optional[torch.Tensor] = None,
@@ -851,36 +767,13 @@ def decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     cache); returns (out, weights_out).  The newest token's entry is set, not
     added to; ``weights=None`` starts at zero.  ``weights_out`` defaults to
     ``weights`` (in place), or a new tensor of zeros."""
-    lib = load()
-    dev, idx, pool, dtype = _pools(k_cache, v_cache)
-    fp8 = dtype is torch.uint8
-    _scales(fp8, k_scale, v_scale)
-    B, blocks = _batch(block_tables, context_lens, dev, idx)
-    qdt = q.dtype
-    if qdt not in _DTYPE_CODES or not (fp8 or qdt is dtype):
-        raise TypeError(f"q must have the cache's 16-bit dtype, got {qdt}")
-    _must(q, "q", qdt, dev, idx)
-    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != pool[3]:
-        raise ValueError("q must be [num_seqs][num_q_heads][head_dim]")
-    weights_out = _weights_pair(weights, weights_out, (B, pool[2], blocks * pool[1]), dev, idx)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _must(out, "out", qdt, dev, idx)
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-    if partition_size is None:
-        partition_size = weights_partition(B, pool[2], max_context_len, fp8, idx)
-    ref = ctypes.byref(_pool_shape(B, q.shape[1], pool, blocks, qdt))
-    name = "pa_decode_weights_fp8" if fp8 else "pa_decode_weights"
-    ws, nbytes = _workspace(workspace, lib.pa_decode_weights_workspace_size(
-        ref, max_context_len, partition_size) if B else 1, name, dev)
-    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-            context_lens.data_ptr(), scale, *((k_scale, v_scale) if fp8 else ()), max_context_len,
-            partition_size, _addr(weights), weights_out.data_ptr(), weights_out.shape[2],
-            ws.data_ptr(), nbytes, out.data_ptr(), ref)
-    _call(lib.pa_decode_weights_fp8 if fp8 else lib.pa_decode_weights, name, dev, idx, *args)
-    return out, weights_out
+    r = (_native or _load_native()).decode_weights(
+        q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len, weights,
+        weights_out, out, weights_partition if partition_size is None else partition_size,
+        workspace, k_scale, v_scale)
+    if r.__class__ is int:
+        _refused("pa_decode_weights", k_cache, r)
+    return r
 
 
 def prefill_weights(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -894,24 +787,12 @@ def prefill_weights(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.
     (pa_prefill_weights; ``prefill`` gives the attention itself).  The chunk's
     own tokens are set, not added to.  ``weights_out`` defaults to ``weights``
     (in place), or a new tensor of zeros; returned."""
-    lib = load()
-    dev, idx, pool, dtype = _pools(k_cache, k_cache)
-    if dtype is torch.uint8:
-        raise TypeError("prefill_weights reads a float16 or bfloat16 cache")
-    B, blocks = _batch(block_tables, context_lens, dev, idx)
-    _must(q, "q", dtype, dev, idx)
-    _must(query_start, "query_start", torch.int32, dev, idx)
-    if q.dim() != 3 or q.shape[2] != pool[3] or query_start.shape != (B + 1,):
-        raise ValueError("q must be [total_tokens][Hq][D], query_start [num_seqs + 1]")
-    weights_out = _weights_pair(weights, weights_out, (B, pool[2], blocks * pool[1]), dev, idx)
-    ref = ctypes.byref(_pool_shape(B, q.shape[1], pool, blocks, dtype))
-    ws, nbytes = _workspace(workspace, lib.pa_prefill_weights_workspace_size(
-        ref, max_query_len, max_context_len, window), "pa_prefill_weights", dev)
-    _call(lib.pa_prefill_weights, "pa_prefill_weights", dev, idx, q.data_ptr(), k_cache.data_ptr(),
-          block_tables.data_ptr(), context_lens.data_ptr(), query_start.data_ptr(), scale,
-          q.shape[0], max_query_len, max_context_len, window, _addr(weights),
-          weights_out.data_ptr(), weights_out.shape[2], ws.data_ptr(), nbytes, ref)
-    return weights_out
+    r = (_native or _load_native()).prefill_weights(
+        q, k_cache, block_tables, context_lens, query_start, scale, max_query_len,
+        max_context_len, window, weights, weights_out, workspace)
+    if r.__class__ is int:
+        _refused("pa_prefill_weights", k_cache, r)
+    return r
 
 
 def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -932,42 +813,13 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tens
     (entries of ``positions`` that are set; None: none).  Blocks past
     ceil(new_len / block_size) are free afterwards
     (``PagedKVAllocator.truncate``)."""
-    lib = load()
-    dev, idx, pool, dtype = _pools(k_cache, v_cache)
-    fp8 = dtype is torch.uint8
-    B, blocks = _batch(block_tables, context_lens, dev, idx)
-    shape = (B, pool[2], blocks * pool[1])
-    _state(weights, "weights", shape, torch.float32, dev, idx)
-    _state(positions, "positions", shape, torch.int32, dev, idx)
-    if weights_out is None:
-        weights_out = weights
-    else:
-        _state(weights_out, "weights_out", shape, torch.float32, dev, idx)
-    if positions_out is None:
-        positions_out = positions
-    else:
-        _state(positions_out, "positions_out", shape, torch.int32, dev, idx)
-    width = weights.shape[2]
-    if not width == positions.shape[2] == weights_out.shape[2] == positions_out.shape[2]:
-        raise ValueError("weights, positions and their outputs must have the same shape")
-    if new_lens is None:
-        new_lens = torch.empty_like(context_lens)
-    for t, n in ((seen_lens, "seen_lens"), (new_lens, "new_lens"), (known_lens, "known_lens")):
-        if t is not None or n != "known_lens":
-            _must(t, n, torch.int32, dev, idx)
-            if t.shape != (B,):
-                raise ValueError(f"{n} must be [num_seqs]")
-    if trigger is None:
-        trigger = budget
-    ref = ctypes.byref(_pool_shape(B, pool[2], pool, blocks, torch.float16 if fp8 else dtype))
-    name = "pa_evict_fp8" if fp8 else "pa_evict"
-    ws, nbytes = _workspace(workspace, lib.pa_evict_workspace_size(ref, budget) if B else 1, name, dev)
-    _call(lib.pa_evict_fp8 if fp8 else lib.pa_evict, name, dev, idx, k_cache.data_ptr(),
-          v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
-          seen_lens.data_ptr(), _addr(known_lens), weights.data_ptr(), positions.data_ptr(), width,
-          budget, trigger, sinks, recent, weights_out.data_ptr(), positions_out.data_ptr(),
-          new_lens.data_ptr(), ws.data_ptr(), nbytes, ref)
-    return new_lens, weights_out, positions_out
+    r = (_native or _load_native()).evict(
+        k_cache, v_cache, block_tables, context_lens, seen_lens, budget, weights, positions,
+        known_lens, trigger, sinks, recent, weights_out, positions_out, new_lens, workspace)
+    if r.__class__ is int:
+        _refused("pa_evict", k_cache, r)
+    return (r, weights if weights_out is None else weights_out,
+            positions if positions_out is None else positions_out)
 
 
 STATIC_WORKSPACE_BYTES = 32 << 20

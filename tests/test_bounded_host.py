@@ -187,3 +187,36 @@ def test_plain_eviction_by_hand():
     assert wo[0, 0, :4].tolist() == [0.0, 5.0, 1.0, 3.0]
     blk = int(x.tables[0, 0])
     assert torch.equal(k[blk, 3], x.k[blk, 5]) and torch.equal(v[blk, 2], x.v[blk, 2])
+
+
+def test_binding_refuses_before_the_gpu(pa):
+    """What the Python calls say about arguments that cannot be used at all."""
+    kv = torch.zeros(2, 16, 2, 64, dtype=torch.float16)
+    t = torch.zeros(1, 2, dtype=torch.int32)
+    lens = torch.ones(1, dtype=torch.int32)
+    x = torch.zeros(1, 4, 64, dtype=torch.float16)
+    w = torch.zeros(1, 2, 32)
+    calls = {
+        lib.rope_and_cache: dict(q=x, k=x[:, :2], v=x[:, :2], positions=lens.long(), slot_mapping=lens.long(),
+                                 inv_freq=torch.ones(32), k_cache=kv, v_cache=kv),
+        lib.decode_weights: dict(q=x, k_cache=kv, v_cache=kv, block_tables=t, context_lens=lens, scale=1.0,
+                                 max_context_len=16),
+        lib.prefill_weights: dict(q=x, k_cache=kv, block_tables=t, context_lens=lens, query_start=lens,
+                                  scale=1.0, max_query_len=1, max_context_len=16),
+        lib.evict: dict(k_cache=kv, v_cache=kv, block_tables=t, context_lens=lens, seen_lens=lens, budget=4,
+                        weights=w, positions=w.int()),
+    }
+    for fn, args in calls.items():
+        with pytest.raises(ValueError, match="k_cache must be a CUDA tensor"):
+            fn(**args)
+        for odd in (None, 3, kv.numpy()):
+            with pytest.raises(TypeError, match="k_cache must be a torch.Tensor"):
+                fn(**{**args, "k_cache": odd})
+        with pytest.raises(TypeError):
+            fn()
+    with pytest.raises(TypeError, match="expected 16 arguments"):
+        lib._load_native().evict(kv)
+
+
+def test_binding_is_built_for_this_torch(pa):
+    assert build.native_up_to_date()

@@ -266,3 +266,107 @@ def test_prefill_weights_on_two_streams(dev):
         ww, wb = prefill_reference(x, q, [323, 77])
         within(w, ww, wb, "weights")
     assert lib.read_device_errors(dev) == 0
+
+
+def calls_of(dev, seed):
+    """One call of each operator on a small batch, with every array given."""
+    x = Batch([40, 33], 4, 2, 64, 16, torch.float16, seed=seed, stale=False)
+    k, v, tables, lens = x.k.to(dev), x.v.to(dev), x.tables.to(dev), x.lens.to(dev)
+    q = x.q.to(dev)
+    new = q[:, :2].contiguous()
+    i64 = torch.tensor([3, 20], device=dev)
+    w, p = torch.zeros(2, 2, x.tokens, device=dev), torch.zeros(2, 2, x.tokens, dtype=torch.int32, device=dev)
+    start = torch.tensor([0, 1, 2], dtype=torch.int32, device=dev)
+    inv = lib.rope_frequencies(64)[0].to(dev)
+    return {
+        "rope": (lib.rope_and_cache, dict(q=q, k=new, v=new, positions=i64, slot_mapping=i64, inv_freq=inv,
+                                          k_cache=k, v_cache=v, q_out=torch.empty_like(q))),
+        "decode": (lib.decode_weights, dict(q=q, k_cache=k, v_cache=v, block_tables=tables, context_lens=lens,
+                                            scale=x.scale, max_context_len=40, weights=w,
+                                            weights_out=torch.zeros_like(w), out=torch.empty_like(q),
+                                            workspace=torch.empty(1 << 20, dtype=torch.uint8, device=dev))),
+        "prefill": (lib.prefill_weights, dict(q=q, k_cache=k, block_tables=tables, context_lens=lens,
+                                              query_start=start, scale=x.scale, max_query_len=1,
+                                              max_context_len=40, weights=w, weights_out=torch.zeros_like(w),
+                                              workspace=torch.empty(1 << 20, dtype=torch.uint8, device=dev))),
+        "evict": (lib.evict, dict(k_cache=k, v_cache=v, block_tables=tables, context_lens=lens, seen_lens=lens,
+                                  budget=32, weights=w, positions=p, known_lens=torch.zeros_like(lens),
+                                  weights_out=torch.zeros_like(w), positions_out=torch.zeros_like(p),
+                                  new_lens=torch.empty_like(lens),
+                                  workspace=torch.empty(1 << 20, dtype=torch.uint8, device=dev))),
+    }
+
+
+@pytest.mark.parametrize("name,gives", [("rope", ["q_out"]), ("decode", ["out", "weights_out"]),
+                                        ("prefill", ["weights_out"]),
+                                        ("evict", ["new_lens", "weights_out", "positions_out"])])
+def test_binding_returns_and_references(dev, name, gives):
+    """The given outputs come back as they are; neither a call, nor one that
+    makes its outputs, nor a refused one keeps or drops a reference or memory;
+    what is not an int32 or a number is refused."""
+    import gc
+    import sys
+    fn, args = calls_of(dev, seed=70)[name]
+    got = fn(**args)
+    got = got if isinstance(got, tuple) else (got,)
+    assert len(got) == len(gives) and all(a is args[g] for a, g in zip(got, gives))
+    del got
+    fresh = {k: v for k, v in args.items() if k not in (*gives, "workspace")}
+    made = fn(**fresh)
+    made = made if isinstance(made, tuple) else (made,)
+    for a, g in zip(made, gives):
+        assert a.shape == args[g].shape and a.dtype == args[g].dtype and a.device == args[g].device
+    del made
+    scalar = {"rope": "factor", "decode": "max_context_len", "prefill": "window", "evict": "budget"}[name]
+    bad = [{scalar: "x"}, {"k_cache": args["k_cache"].float()}, {"v_cache" if name != "prefill" else "q": None}]
+    if name != "rope":
+        bad += [{scalar: 1 << 40}, {scalar: 1.5}, {"workspace": torch.empty(64, dtype=torch.uint8)},
+                {"workspace": torch.empty(1 << 20, dtype=torch.uint8, device=dev)[::2]}]
+    def everything():
+        fn(**args)
+        fn(**fresh)
+        for b in bad:
+            with pytest.raises((TypeError, ValueError)):
+                fn(**{**args, **b})
+    for _ in range(3):
+        everything()
+    gc.collect()
+    held = {k: sys.getrefcount(v) for k, v in args.items()}
+    memory = torch.cuda.memory_allocated(dev)
+    for _ in range(50):
+        everything()
+    gc.collect()
+    assert {k: sys.getrefcount(v) for k, v in args.items()} == held
+    assert torch.cuda.memory_allocated(dev) == memory
+    assert lib.read_device_errors(dev) == 0
+
+
+def test_calls_from_threads(dev):
+    """The operators called from four threads, each on a stream of its own,
+    give what one thread gets."""
+    import threading
+    def outcome(seed):
+        made = []
+        s = torch.cuda.Stream(dev)
+        with torch.cuda.stream(s):
+            sets = calls_of(dev, seed)
+            for _ in range(20):
+                for name in ("decode", "prefill"):
+                    fn, args = sets[name]
+                    got = fn(**{k: v for k, v in args.items() if k not in ("out", "weights_out", "weights", "workspace")})
+                    made.append(tuple(got) if isinstance(got, tuple) else (got,))
+            fn, args = sets["evict"]
+            got = fn(**args)
+            made.append(tuple(t.clone() for t in got[:1]) + (args["k_cache"].clone(),))
+        s.synchronize()
+        return [tuple(t.cpu() for t in m) for m in made]
+    want = {seed: outcome(seed) for seed in range(80, 84)}
+    got = {}
+    threads = [threading.Thread(target=lambda i=seed: got.__setitem__(i, outcome(i))) for seed in want]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for seed in want:
+        for a, b in zip(want[seed], got[seed]):
+            assert all(same_bits(x, y) for x, y in zip(a, b))
