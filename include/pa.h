@@ -511,7 +511,7 @@ int pa_decode_weights_fp8(const void* q, const void* k_cache, const void* v_cach
  * L_b.  Values outside these bounds are clamped and set
  * PA_DEVERR_BAD_CONTEXT.  scale must be finite and > 0.  16-bit caches.
  * workspace as in pa_decode_weights, of pa_prefill_weights_workspace_size
- * bytes.  Two to four launches.
+ * bytes.  One to four launches.
  */
 size_t pa_prefill_weights_workspace_size(const pa_shape* shp, int32_t max_query_len,
                                          int32_t max_context_len, int32_t window);

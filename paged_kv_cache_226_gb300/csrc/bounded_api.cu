@@ -302,8 +302,12 @@ int pa_prefill_weights(const void* q, const void* k_cache, const int32_t* block_
     p.scale_log2 = scale * pa::kLog2e;
     p.max_blocks_per_seq = shp->max_blocks_per_seq, p.block_size = shp->block_size;
     p.num_blocks = shp->num_blocks, p.num_tokens = num_tokens;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    bool launched = false;
+    if (lone) e = pa::launch_short_weights(shp->dtype, shp->head_dim, tmk, tmq, p, cs, &launched);
+    if (e != cudaSuccess || launched) return finish(e);
     return finish((lone ? pa::launch_window_weights : pa::launch_prefill_weights)(
-        shp->dtype, shp->head_dim, tmk, tmq, p, static_cast<cudaStream_t>(stream)));
+        shp->dtype, shp->head_dim, tmk, tmq, p, cs));
 }
 
 size_t pa_evict_workspace_size(const pa_shape* shp, int32_t budget) {

@@ -86,6 +86,11 @@ size_t window_weights_plan(PrefillWeightsParams& p, void* workspace);
 cudaError_t launch_window_weights(int dtype, int head_dim, const CUtensorMap& tmk,
                                   const CUtensorMap& tmq, const PrefillWeightsParams& p,
                                   cudaStream_t stream);
+// The same in one launch where the contexts fit the shared memory of one wave
+// (prefill_short.cu); nothing is done where `launched` comes back false.
+cudaError_t launch_short_weights(int dtype, int head_dim, const CUtensorMap& tmk,
+                                 const CUtensorMap& tmq, const PrefillWeightsParams& p,
+                                 cudaStream_t stream, bool* launched);
 cudaError_t launch_prefill_weights(int dtype, int head_dim, const CUtensorMap& tmk,
                                    const CUtensorMap& tmq, const PrefillWeightsParams& p,
                                    cudaStream_t stream);

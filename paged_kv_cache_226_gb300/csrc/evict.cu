@@ -59,10 +59,6 @@ __device__ __forceinline__ int evict_position(const EvictSeq& s, const int32_t* 
 }
 
 // ---- clusters -------------------------------------------------------------
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // Four words at the same shared-memory address in CTA `rank` of the cluster.
 __device__ __forceinline__ uint4 cluster_words(const uint32_t* local, int rank) {
     uint32_t addr;
@@ -415,19 +411,8 @@ __global__ void __launch_bounds__(kMoveThreads)
 
 template <int kThreads>
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.num_kv_heads * p.cluster, p.num_seqs);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = p.cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, evict_select_kernel<kThreads>, p);
+    return launch_clusters(evict_select_kernel<kThreads>, p.cluster,
+                           dim3(p.num_kv_heads * p.cluster, p.num_seqs), dim3(kThreads), 0, stream, p);
 }
 
 cudaError_t launch_evict(const EvictParams& params, cudaStream_t stream) {

@@ -1,9 +1,10 @@
 // Attention weights of a chunk's last queries where those of one KV head fit
 // a single tile of 128 rows (tokens x heads of the group): the observation
-// window of a prompt, or a short chunk.  The mathematics and the two passes
-// are those of prefill_weights.cu; here a query tile meets every key tile of
-// its sequence once per pass, so that the key tiles are what streams and the
-// batch is memory bound: K is read twice, Q next to never.
+// window of a prompt, or a short chunk (a few short contexts are
+// prefill_short.cu's).  The mathematics and the two passes are those of
+// prefill_weights.cu; here a query tile meets every key tile of its sequence
+// once per pass, so that the key tiles are what streams and the batch is
+// memory bound: K is read twice, Q next to never.
 //
 // The key tiles of all (sequence, KV head) rows, in order, are dealt out in
 // equal contiguous ranges to one persistent CTA per SM.  A range meets few

@@ -188,6 +188,42 @@ def test_prefill_weights(dev, dtype, hq, hkv, d, bs, window):
     run_prefill(dev, x, chunks, window, x.state())
 
 
+@pytest.mark.parametrize("hq,hkv,d,dtype,lens", [
+    (4, 1, 128, BF16, [128]),                               # one CTA, one whole tile
+    (4, 1, 128, F16, [256, 1, 129]),                        # two tiles a CTA
+    (3, 1, 64, F16, [257, 0, 512]),                         # clusters of two, some CTAs without tiles
+    (8, 2, 128, BF16, [1024, 1000, 17]),                    # of four
+    (10, 2, 64, BF16, [1100, 40]),                          # of five
+    (7, 1, 128, F16, [2048, 1921, 2000]),                   # of eight
+    (16, 8, 64, F16, [4096]),                               # of eight, four tiles a CTA
+    (8, 1, 128, BF16, [3970, 4096, 255]),
+    (1, 1, 128, BF16, [4097, 130]),                         # too long: two passes
+    (16, 16, 64, F16, [100, 300, 500, 512, 260, 31, 1, 0, 77]),   # 144 pairs: one CTA each
+    (16, 8, 128, BF16, [129 + 7 * i for i in range(24)])])  # 192 pairs: two passes
+@pytest.mark.parametrize("window", [1, 16])
+def test_prefill_weights_one_launch_or_two(dev, hq, hkv, d, dtype, lens, window):
+    """Windows over contexts at the bounds of the one-launch form's clusters."""
+    x = Batch(lens, hq, hkv, d, 16, dtype, seed=hq + len(lens))
+    run_prefill(dev, x, [min(n, 16 + 9 * (i % 3)) for i, n in enumerate(lens)], window, x.state())
+    run_prefill(dev, x, [min(n, 5) for n in lens], 0, None)
+
+
+def test_prefill_weights_one_launch_bad_block(dev):
+    """A block id outside the pool is reported and reads as zeros."""
+    x = Batch([700, 300], 4, 2, 128, 16, F16, seed=33, stale=False)
+    tables = x.tables.clone()
+    x.k[x.tables[0, 5].long()] = 0
+    x.k[x.tables[1, 2].long()] = 0
+    tables[0, 5], tables[1, 2] = x.k.shape[0] + 7, -3
+    start = torch.tensor([0, 8, 16], dtype=torch.int32, device=dev)
+    q = torch.randn(16, 4, 128, generator=x.gen).to(F16).to(dev)
+    w = lib.prefill_weights(q, x.k.to(dev), tables.to(dev), x.lens.to(dev), start, x.scale, 8, 700)
+    torch.cuda.synchronize(dev)
+    assert lib.read_device_errors(dev) == lib.PA_DEVERR_BAD_CONTEXT
+    ww, wb = prefill_reference(x, q.cpu(), [8, 8], 0, None)
+    within(w, ww, wb, "weights")
+
+
 def test_prefill_weights_long(dev):
     x = Batch([3001, 700], 4, 1, 128, 16, BF16, seed=21)
     run_prefill(dev, x, [513, 700], 0, None)
