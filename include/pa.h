@@ -479,7 +479,7 @@ int pa_rope_and_cache_fp8(const void* q, int64_t q_stride, const void* k, int64_
  * max_context_len >= every L_b (tokens past it are not attended),
  * partition_size a multiple of block_size.  workspace: device memory of at
  * least pa_decode_weights_workspace_size bytes, 16-byte aligned, no initial
- * contents; calls that overlap on the GPU must not share it.  Two launches.
+ * contents; calls that overlap on the GPU must not share it.  One or two launches.
  */
 size_t pa_decode_weights_workspace_size(const pa_shape* shp, int32_t max_context_len,
                                         int32_t partition_size);

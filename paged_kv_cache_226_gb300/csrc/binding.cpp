@@ -5,9 +5,8 @@
 // Here the checks of a call read the tensors' fields directly and its arrays
 // are allocated in place.  Measured per call from Python (us; in brackets the
 // same checks written in Python over ctypes): rotary write of 64 tokens 5.4
-// (20.0), decode weights of 4 short sequences 9.1 (27.2), prefill weights of 3
-// short chunks 10.7 (27.6), eviction of 64 sequences by a block 13.4 (22.8);
-// the last two are the kernels' own time.
+// (20.0), decode weights of 4 short sequences, two launches, 9.1 (27.2),
+// eviction of 64 sequences by a block 13.4, the kernel's own time (22.8).
 //
 // Every function takes its arguments by position, checks them in the order
 // given, raises TypeError or ValueError, and enqueues on the current stream of

@@ -132,9 +132,18 @@ int decode_weights(const void* q, const void* k_cache, const void* v_cache,
 #endif
     const dim3 grid(shp->num_seqs, shp->num_kv_heads, w.parts);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    e = fp8 ? pa::launch_decode_fp8(shp->dtype, pa::kModeWeights, tmk, tmv, p, grid, s)
-            : pa::launch_decode(shp->dtype, shp->head_dim, pa::kModeWeights, tmk, tmv, p, grid, s);
-    if (e != cudaSuccess) return finish(e);
+    // One launch, the partitions a cluster that joins them, for contexts of one
+    // partition (us against decode + merge: 1216 pairs of 200 tokens 31.7 and
+    // 35.4, 512 of 1040 53.5 and 55.5) or a few short ones (64 pairs of up to
+    // 250 tokens in four 6.8 and 7.4; 8 pairs 5.9 and 5.6, but a launch less
+    // to make).  Clusters of longer partitions hold their SM slots until the
+    // slowest ends (512 pairs of up to 2048 in two 67 and 57).
+    const bool join = (w.parts == 1 && partition_size <= 1024) || (w.parts <= 4 && partition_size <= 64);
+    const int mode = join ? pa::kModeWeightsJoin : pa::kModeWeights;
+    p.out = out, p.weights = weights, p.weights_out = weights_out, p.weights_stride = weights_stride;
+    e = fp8 ? pa::launch_decode_fp8(shp->dtype, mode, tmk, tmv, p, grid, s)
+            : pa::launch_decode(shp->dtype, shp->head_dim, mode, tmk, tmv, p, grid, s);
+    if (e != cudaSuccess || join) return finish(e);
     pa::WeightsMergeParams m{};
     m.tmp_out = p.tmp_out, m.max_logits = p.max_logits, m.exp_sums = p.exp_sums;
     m.scores = p.scores, m.context_lens = context_lens;

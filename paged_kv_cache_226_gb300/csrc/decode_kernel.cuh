@@ -121,6 +121,118 @@ struct KeepScores {
     }
 };
 
+// Joins the partitions of a (sequence, KV head), one per CTA of the cluster:
+// M and Z of each head from every CTA's (m, l), `out` from their normalised
+// outputs (the items dealt out among the CTAs), and the weights of this CTA's
+// tokens [t_begin, t_end) from the scores that it stored itself:
+//   weights[i] (+)= sum over the group's heads h of 2^(x_i - M_h) / Z_h.
+// `part_out` [G][D] and `part_ml` [kMaxGroup] are in shared memory, this CTA's
+// values at the same place in every CTA, `top` [warps][kMaxGroup] is for M and
+// 1 / Z; by the consumer warps, after the scores and both records have been
+// written by them.
+template <typename T, int D>
+__device__ __forceinline__ void join_weights(const DecodeParams& p, const float* scores, const float* part_out,
+                                             const float2* part_ml, float2* top, int b, int g, int part, int parts,
+                                             int t_begin, int t_end, int L) {
+    const int G = p.group, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kThreads = kConsumerWarps * 32;
+    if (p.max_parts > 1)
+        cluster_barrier();
+    else
+        asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+    auto of = [&](int rank, int h) { return p.max_parts > 1 ? cluster_float2(part_ml + h, rank) : part_ml[h]; };
+    // lane: head lane % 8 of the partitions lane / 8, + 4, ...
+    {
+        float m = -INFINITY, z = 0.f;
+        const int h = lane & (kMaxGroup - 1);
+        if (h < G) {
+            for (int r = lane / kMaxGroup; r < parts; r += 32 / kMaxGroup) {
+                const float2 o = of(r, h);
+                const float n = fmaxf(m, o.x), ref = n == -INFINITY ? 0.f : n;
+                z = z * ex2(m - ref) + o.y * ex2(o.x - ref);
+                m = n;
+            }
+        }
+#pragma unroll
+        for (int d = kMaxGroup; d < 32; d <<= 1) {
+            const float om = __shfl_xor_sync(0xffffffffu, m, d), oz = __shfl_xor_sync(0xffffffffu, z, d);
+            const float n = fmaxf(m, om), ref = n == -INFINITY ? 0.f : n;
+            z = z * ex2(m - ref) + oz * ex2(om - ref);
+            m = n;
+        }
+        if (lane < kMaxGroup) top[warp * kMaxGroup + lane] = make_float2(m, 1.f / z);
+        __syncwarp();
+    }
+    const float2* mine = top + warp * kMaxGroup;
+    const int items = G * (D / 4);                    // 4 output dims per item
+    for (int item = part * kThreads + tid; item < items; item += parts * kThreads) {
+        const int h = item / (D / 4), d = (item - h * (D / 4)) * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int r = 0; r < parts; ++r) {
+            const float2 o = of(r, h);
+            const float* src = part_out + h * D + d;
+            const float4 x = p.max_parts > 1 ? cluster_float4(src, r) : *reinterpret_cast<const float4*>(src);
+            const float w = o.y * ex2(o.x - mine[h].x);
+            acc.x += w * x.x, acc.y += w * x.y, acc.z += w * x.z, acc.w += w * x.w;
+        }
+        const float iz = mine[h].y;
+        *reinterpret_cast<uint2*>(static_cast<T*>(p.out) +
+                                  ((size_t)b * p.num_q_heads + (size_t)g * G + h) * D + d) =
+            make_uint2(Mma<T>::pack(acc.x * iz, acc.y * iz), Mma<T>::pack(acc.z * iz, acc.w * iz));
+    }
+    if (p.max_parts > 1) {
+        __syncwarp();
+        cluster_arrive();                             // the others' shared memory is read
+    }
+    const size_t row = ((size_t)b * p.num_kv_heads + g) * p.weights_stride;
+    const float* before = p.weights ? p.weights + row : nullptr;
+    float* after = p.weights_out + row;
+    auto tokens = [&](auto group) {
+        constexpr int kG = decltype(group)::value, kHeads = kG == 0 ? kMaxGroup : kG;    // 0: any
+        constexpr int kAhead = 16 / kHeads;           // tokens whose loads are in flight together
+        for (int i0 = t_begin + tid; i0 < t_end; i0 += kAhead * kThreads) {
+            float x[kAhead][kHeads], w[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + k * kThreads;
+                const float* src = scores + (size_t)i * G;
+                w[k] = before && i < t_end && i < L - 1 ? before[i] : 0.f;
+#pragma unroll
+                for (int h = 0; h < kHeads; h += kG == 0 ? 1 : 4) {
+                    if constexpr (kG == 0) {
+                        x[k][h] = i < t_end && h < G ? __ldcg(src + h) : -INFINITY;
+                    } else {
+                        const float4 q = i < t_end ? __ldcg(reinterpret_cast<const float4*>(src + h))
+                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+                        x[k][h] = q.x, x[k][h + 1] = q.y, x[k][h + 2] = q.z, x[k][h + 3] = q.w;
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + k * kThreads;
+                if (i >= t_end) break;
+                float sum = 0.f;
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h)
+                    if (kG != 0 || h < G) sum += ex2(x[k][h] - mine[h].x) * mine[h].y;
+                after[i] = w[k] + sum;
+            }
+        }
+    };
+    if (G == 4)
+        tokens(std::integral_constant<int, 4>());
+    else if (G == 8)
+        tokens(std::integral_constant<int, 8>());
+    else
+        tokens(std::integral_constant<int, 0>());
+    if (p.max_parts > 1) {
+        __syncwarp();
+        cluster_wait();
+    }
+}
+
 template <typename T, int D, int kMode, bool kFp8 = false>
 __global__ void __launch_bounds__(kDecodeThreads, kFp8 ? kMinCtasPerSmFp8 : kMinCtasPerSm)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
@@ -132,6 +244,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kFp8 ? kMinCtasPerSmFp8 : kMin
     constexpr int kKSteps = D / 16;     // 16-dim slices of D
 
     constexpr bool kPartitioned = kMode != kModeSingle;
+    constexpr bool kJoin = kMode == kModeWeightsJoin, kWeights = kMode == kModeWeights || kJoin;
     __shared__ __align__(8) uint64_t full_bar[Lay::kRing];
     __shared__ __align__(8) uint64_t empty_bar[Lay::kRing];
     __shared__ int merge_here;          // fused step: this CTA merges the partitions
@@ -161,7 +274,22 @@ __global__ void __launch_bounds__(kDecodeThreads, kFp8 ? kMinCtasPerSmFp8 : kMin
         L = L < 0 ? 0 : max_ctx;
     }
     int t_begin = 0, t_end = L, parts = 1;
-    if (kPartitioned) {
+    if constexpr (kJoin) {
+        // the context cut evenly among the cluster's CTAs, in whole tiles
+        const int attended = (int)min((int64_t)L, (int64_t)p.max_parts * p.partition_tokens);
+        if (attended == 0) {
+            T* out = reinterpret_cast<T*>(p.out) + ((size_t)b * p.num_q_heads + (size_t)g * G) * D;
+            if (part == 0)
+                for (int i = threadIdx.x; i < G * D; i += blockDim.x) out[i] = from_float<T>(0.f);
+            return;
+        }
+        const int tiles = (attended - 1) / kTileTokens + 1;
+        const int tokens = ((tiles - 1) / p.max_parts + 1) * kTileTokens;
+        parts = (attended - 1) / tokens + 1;
+        if (part >= parts) return;
+        t_begin = part * tokens;
+        t_end = min(t_begin + tokens, attended);
+    } else if (kPartitioned) {
         parts = min((L + p.partition_tokens - 1) / p.partition_tokens, p.max_parts);
         t_begin = part * p.partition_tokens;
         if (kMode == kModeStep && L == 0 && part == 0) {
@@ -308,9 +436,9 @@ __global__ void __launch_bounds__(kDecodeThreads, kFp8 ? kMinCtasPerSmFp8 : kMin
     auto qfrag = [&](int kk, uint32_t& b0, uint32_t& b1) { lds64(q_lane + kk * 256, b0, b1); };
     TileState<D> ts;
     ts.reset();
-    using Emit = std::conditional_t<kMode == kModeWeights, KeepScores, NoScores>;
+    using Emit = std::conditional_t<kWeights, KeepScores, NoScores>;
     Emit emit;
-    if constexpr (kMode == kModeWeights)
+    if constexpr (kWeights)
         emit = {p.scores + ((size_t)b * p.num_kv_heads + g) * p.max_parts * p.partition_tokens * G,
                 G, t_end, lane};
 
@@ -450,6 +578,11 @@ __global__ void __launch_bounds__(kDecodeThreads, kFp8 ? kMinCtasPerSmFp8 : kMin
     }
     asm volatile("bar.sync 1, %0;" ::"n"(kConsumerWarps * 32) : "memory");
 
+    // joined in the kernel: the partition's record, behind the merge area
+    float* part_out = mrg + Lay::kMergeBytes / 4;
+    float2* part_ml = reinterpret_cast<float2*>(part_out + kMaxGroup * D);
+    static_assert(!kJoin || Lay::kMergeBytes + kMaxGroup * (D + 2 + 2 * kConsumerWarps) * 4 <= Lay::kBodyBytes, "the record fits");
+    static_assert(Lay::kMergeBytes % 16 == 0, "the record is read in 16-byte words");
     const int tid = threadIdx.x;                      // 0..127
     const int items = G * (D / 4);                    // 4 output dims per item
     for (int item = tid; item < items; item += kConsumerWarps * 32) {
@@ -475,7 +608,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kFp8 ? kMinCtasPerSmFp8 : kMin
         }
         const float inv = (kFp8 ? p.v_scale : 1.f) / den;
         const size_t qh = (size_t)b * p.num_q_heads + (size_t)g * G + h;
-        if (kMode == kModeSplit || kMode == kModeWeights || (kMode == kModeStep && parts > 1)) {
+        if constexpr (kJoin) {
+            *reinterpret_cast<float4*>(part_out + h * D + d) = make_float4(o0 * inv, o1 * inv, o2 * inv, o3 * inv);
+            if (d == 0) part_ml[h] = make_float2(mt, den * ex2(mref - mt));
+        } else if (kMode == kModeSplit || kMode == kModeWeights || (kMode == kModeStep && parts > 1)) {
             const size_t idx = qh * p.max_parts + part;
             *reinterpret_cast<float4*>(p.tmp_out + idx * D + d) =
                 make_float4(o0 * inv, o1 * inv, o2 * inv, o3 * inv);
@@ -489,6 +625,12 @@ __global__ void __launch_bounds__(kDecodeThreads, kFp8 ? kMinCtasPerSmFp8 : kMin
             const uint32_t hi = M::pack(o2 * inv, o3 * inv);
             *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
         }
+    }
+
+    if constexpr (kJoin) {
+        __syncwarp();
+        join_weights<T, D>(p, emit.scores, part_out, part_ml, part_ml + kMaxGroup, b, g, part, parts, t_begin, t_end, L);
+        return;
     }
 
     if (kMode == kModeStep && parts > 1) {
@@ -565,6 +707,10 @@ cudaError_t launch_decode_mode(const CUtensorMap& tmk, const CUtensorMap& tmv,
     cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<T, D, kMode, kFp8>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    if constexpr (kMode == kModeWeightsJoin) {
+        return launch_clusters(paged_decode_kernel<T, D, kMode, kFp8>, dim3(1, 1, grid.z), grid,
+                               dim3(kDecodeThreads), smem, stream, tmk, tmv, p);
+    }
     e = launch_with_pdl(paged_decode_kernel<T, D, kMode, kFp8>, grid, dim3(kDecodeThreads), smem,
                         stream, tmk, tmv, p);
     if (e != cudaSuccess) return e;
@@ -578,6 +724,8 @@ cudaError_t launch_decode_t(int mode, const CUtensorMap& tmk, const CUtensorMap&
     if (mode == kModeStep) return launch_decode_mode<T, D, kModeStep>(tmk, tmv, p, grid, stream);
     if (mode == kModeWeights)
         return launch_decode_mode<T, D, kModeWeights>(tmk, tmv, p, grid, stream);
+    if (mode == kModeWeightsJoin)
+        return launch_decode_mode<T, D, kModeWeightsJoin>(tmk, tmv, p, grid, stream);
     return launch_decode_mode<T, D, kModeSingle>(tmk, tmv, p, grid, stream);
 }
 
@@ -590,6 +738,8 @@ cudaError_t launch_decode_fp8_t(int mode, const CUtensorMap& tmk, const CUtensor
         return launch_decode_mode<T, 128, kModeStep, true>(tmk, tmv, p, grid, stream);
     if (mode == kModeWeights)
         return launch_decode_mode<T, 128, kModeWeights, true>(tmk, tmv, p, grid, stream);
+    if (mode == kModeWeightsJoin)
+        return launch_decode_mode<T, 128, kModeWeightsJoin, true>(tmk, tmv, p, grid, stream);
     return launch_decode_mode<T, 128, kModeSingle, true>(tmk, tmv, p, grid, stream);
 }
 

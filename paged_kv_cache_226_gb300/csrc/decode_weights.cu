@@ -1,5 +1,6 @@
 // Merge of the decode kernel's weights mode: out from the partitions, and the
-// attention weight of every cached token.
+// attention weight of every cached token (short contexts: the decode kernel
+// does this itself, join_weights in decode_kernel.cuh).
 //
 // The decode kernel (weights mode) leaves, per (sequence b, query head h,
 // partition s), m_s = max_i x_i, l_s = sum_i 2^(x_i - m_s) and the partition's

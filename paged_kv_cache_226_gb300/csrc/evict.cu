@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kMoveThreads)
 
 template <int kThreads>
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream) {
-    return launch_clusters(evict_select_kernel<kThreads>, p.cluster,
+    return launch_clusters(evict_select_kernel<kThreads>, dim3(p.cluster),
                            dim3(p.num_kv_heads * p.cluster, p.num_seqs), dim3(kThreads), 0, stream, p);
 }
 

@@ -83,8 +83,12 @@ struct DecodeParams {
     // FP8 (E4M3) cache only: per-tensor scales (k_scale is also folded into scale_log2)
     float k_scale;
     float v_scale;
-    // weights mode only: [B][Hkv][S * partition_tokens][G] scores in log2 units
+    // weights modes only: [B][Hkv][S * partition_tokens][G] scores in log2 units
     float* scores;
+    // joined in the kernel: [B][Hkv][stride], weights null: none yet
+    const float* weights;
+    float* weights_out;
+    int64_t weights_stride;
 #ifdef PA_TEST_HOOKS
     // Test builds only (libpa_test.so): the producer of CTA test_cta (linear
     // index, -1: none) issues no tile from test_tile on, and every pipeline
@@ -139,6 +143,7 @@ constexpr int kModeSingle = 0;   // one CTA per (sequence, KV head), final outpu
 constexpr int kModeSplit = 1;    // one CTA per partition, partial outputs
 constexpr int kModeStep = 2;     // split + cache write of the new token + in-kernel merge
 constexpr int kModeWeights = 3;  // split that also keeps every score (max_logits in log2 units)
+constexpr int kModeWeightsJoin = 4;  // the same, the partitions a cluster that joins them itself
 
 struct ReduceParams {
     const float* tmp_out;

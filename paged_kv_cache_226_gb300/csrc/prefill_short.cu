@@ -194,7 +194,7 @@ cudaError_t launch_short_weights_t(const CUtensorMap& tmk, const CUtensorMap& tm
     const cudaError_t e = cudaFuncSetAttribute(short_weights_kernel<T, D>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kShortSmem);
     if (e != cudaSuccess) return e;
-    return launch_clusters(short_weights_kernel<T, D>, ranks,
+    return launch_clusters(short_weights_kernel<T, D>, dim3(ranks),
                            dim3((unsigned)(p.num_seqs * p.num_kv_heads) * ranks), dim3(kShortThreads),
                            kShortSmem, stream, tmk, tmq, p, ranks);
 }

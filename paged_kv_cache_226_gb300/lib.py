@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import re
 import threading
@@ -731,26 +732,46 @@ def weights_partition(num_seqs: int, num_kv_heads: int, max_context_len: int, fp
                       index: int) -> int:
     """Partition size of ``decode_weights`` on device ``index``.
 
-    A CTA costs its start and its record, so a partition should hold about a
-    slot's share w of the batch's tokens (6 CTAs per SM, every context taken
-    at ``max_context_len``): the next power of two, but not below 1.5
-    sqrt(max_context_len), where the merge of the records takes over, nor
-    above 1024.  From there on the grid's waves count: the contexts cut into
-    as many pieces as 5.2 CTAs per SM allow if those are three or more, at
-    most 1536 tokens over an E4M3 cache, else 1024.  Measured (us, this rule's
-    size against others): 8 pairs of 4096 tokens 8.7 at 128 (512: 13.1); 8 of
-    50,000 43.8 at 512 (1024: 45.2, 4608: 122); 128 of 1000 10.7 at 128 (512:
-    15.4); 128 of 2000 33.0 at 512 (1024: 41.2); 320 of up to 4096 63.9 at
-    1024 (2048: 77.1); E4M3, 256 of 4096 72.5 at 1536 (1024: 79.7)."""
+    A CTA costs its start and its record, and an SM holds 6 at a time.  Where
+    a slot's share of the batch's tokens (every context taken at
+    ``max_context_len``) is at most 1024, the contexts are cut into as many
+    even pieces as the slots hold at once, but not below 1.5
+    sqrt(max_context_len) tokens, 4 where all slots are in use: there the
+    merge of the records takes over.  That is for three pieces or more, since
+    lengths differ, else a piece is the next power of two to the share.  Above
+    1024 the grid's waves count: as many pieces as 5.2 CTAs per SM allow if
+    those are three or more, at most 1536 tokens over an E4M3 cache; else
+    1024, or about 2.75 waves where that would start a second wave that stays
+    almost empty.  Measured (us, this rule's size against others): 8 pairs of
+    4096 tokens 8.7 at 128 (512: 13.1); 8 of 50,000 44.8 at 512 (1024: 45.2);
+    32 of 4000 11.5 at 256 (160: 12.6); 128 of up to 1000 11.3 at 160 (256:
+    12.4, 512: 15.4); 256 of 2048 51.1 at 704 (1024: 52.7); 512 of 2048 97.5
+    at 416 (1024: 111.6); 320 of up to 4096 64.4 at 1024 (2048: 77.1); E4M3:
+    64 of up to 8000 29.0 at 576 (1024: 40.3), 256 of 4096 70.0 at 1408
+    (1024: 79.7)."""
     sms = torch.cuda.get_device_properties(index).multi_processor_count
-    pairs = max(1, num_seqs * num_kv_heads)
-    share = pairs * max_context_len / (sms * CTAS_PER_SM)
+    pairs, slots = max(1, num_seqs * num_kv_heads), sms * CTAS_PER_SM
+    share = pairs * max_context_len / slots
     if share > 1024:
         pieces = (26 * sms) // (5 * pairs)
-        size = 128 * -(-max_context_len // (128 * pieces)) if pieces >= 3 else 1024
-        return min(size, 1536) if fp8 else size
+        if pieces >= 3:
+            size = 128 * -(-max_context_len // (128 * pieces))
+            return min(size, 1536) if fp8 else size
+        waves = pairs * -(-max_context_len // 1024) / slots
+        if 1 < waves < 1.3:
+            pieces = -(-11 * slots // (4 * pairs))
+            return 32 * -(-max_context_len // (32 * pieces))
+        return 1024
     size = 64
-    while size < share or size * size < 2.25 * max_context_len:
+    while size * size < 2.25 * max_context_len:
+        size *= 2
+    pieces = slots // pairs
+    if pieces >= 3:
+        even = 32 * -(-max_context_len // (32 * pieces))
+        if even <= size:
+            return size
+        return min(1024, max(even, 64 * math.ceil(max_context_len ** 0.5 / 16)))
+    while size < share:
         size *= 2
     return min(size, 1024)
 

@@ -92,6 +92,36 @@ def test_decode_weights_in_place_and_defaults(dev):
     assert same_bits(out, out2)
 
 
+@pytest.mark.parametrize("group", [1, 2, 3, 4, 5, 7, 8])
+@pytest.mark.parametrize("d,dtype,fp8", [(64, F16, False), (128, BF16, False), (128, F16, True)])
+def test_decode_weights_one_launch(dev, group, d, dtype, fp8):
+    """Contexts of one partition, or of up to four short ones cut evenly: the
+    partitions are joined in the decode kernel itself."""
+    for lens, partition in (([1, 0, 16, 17, 64, 63, 31, 2], 64), ([128, 3, 65, 0, 97, 113], 64),
+                            ([256, 255, 193, 33, 1, 0, 16], 64), ([700, 0, 1, 1000, 513], 1008), ([90], 32)):
+        x = Batch(lens, 2 * group, 2, d, 16, dtype, seed=group + len(lens), fp8=fp8)
+        run_decode(dev, x, x.state(), partition_size=partition)
+    run_decode(dev, x, None, partition_size=64)
+
+
+def test_decode_weights_bound_below_a_length(dev):
+    """Tokens past the partitions of max_context_len are not attended, in
+    either form, and their entries stay."""
+    x = Batch([400, 100, 192, 193], 8, 2, 128, 16, F16, seed=37, stale=False)
+    args = (x.q.to(dev), x.k.to(dev), x.v.to(dev), x.tables.to(dev), x.lens.to(dev), x.scale, 192)
+    got = []
+    for partition in (64, 32, 192):
+        w = torch.full((4, 2, x.tokens), -7.0, device=dev)
+        out, _ = lib.decode_weights(*args, weights_out=w, partition_size=partition)
+        assert bool((w[0, :, 192:] == -7.0).all()) and bool((w[3, :, 192:] == -7.0).all())
+        got.append((out.float(), w))
+    x.lens = x.lens.clamp(max=192)
+    want, ww, ob, wb = decode_reference(x)
+    for out, w in got:
+        within(out, want, ob, "out")
+        within(_past(x, w, -7.0), ww, wb, "weights")
+
+
 def test_decode_weights_all_empty(dev):
     x = Batch([0, 0], 4, 2, 64, 16, F16, seed=8)
     run_decode(dev, x, None)
