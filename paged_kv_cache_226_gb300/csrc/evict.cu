@@ -9,8 +9,11 @@
 // of the tokens in the cache; their positions travel with them.
 //
 // The choice is a radix select on an order-preserving 32-bit image of the
-// weight (protected tokens above every weight) in digits of 11, 11 and 10
-// bits.  A cluster of CTAs serves one (sequence, KV head), each CTA a
+// weight (protected tokens above every weight) in digits of 8 bits, whose
+// bins one warp scans (64 x 8 rows of 1040 tokens 11.2 us; digits of 11 bits
+// that all warps scan together 13.3, of 8 that each scans for itself 13.0).
+// Bound by instruction issue, half of the slots (27 warps an SM), and the
+// chain of barriers.  A cluster of CTAs serves one (sequence, KV head), each CTA a
 // contiguous slice of the tokens with its images in registers; histograms
 // and counts are exchanged through distributed shared memory, and every CTA
 // draws the same conclusions from them.  Few moves are made by the cluster
@@ -22,7 +25,7 @@ namespace pa {
 
 constexpr uint32_t kProtected = 0xffffffffu;
 constexpr int kEvictKeys = 8;                // images a thread holds
-constexpr int kEvictBins = 2048;
+constexpr int kEvictBins = 256;
 constexpr int kEvictMaxCluster = 8;
 // Moves per CTA that the select kernel makes itself: one round of rows for
 // its warps; more are spread by the move kernel.
@@ -71,29 +74,36 @@ __device__ __forceinline__ uint4 cluster_words(const uint32_t* local, int rank) 
     return v;
 }
 
-// Exclusive prefix of one count per thread over the block, and the total;
-// `sums` holds a word per warp.  Ends with the block in step.
-template <int kThreads>
-__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* sums, uint32_t* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t incl = v;
+// Exclusive prefix over the counts of a chunk's rows of kThreads tokens, warp
+// by warp: line[row * kWarps + warp], `held` rows of them, read by every warp
+// for itself.  at(before, row) is the prefix at this warp's count of that row.
+template <int kWarps>
+struct RowPrefix {
+    static constexpr int kPer = kEvictKeys * kWarps / 32;        // counts of a lane
+    static_assert(kWarps % kPer == 0, "a warp's counts sit at the same place in their lanes' shares");
+    uint32_t before, total;
+    __device__ __forceinline__ RowPrefix(const uint32_t* line, int held) {
+        const int lane = threadIdx.x & 31, own = (threadIdx.x >> 5) % kPer;
+        uint32_t sum = 0, part = 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += u;
-    }
-    __syncthreads();                            // the previous call's reads of sums
-    if (lane == 31) sums[warp] = incl;
-    __syncthreads();
-    uint32_t w = lane < kThreads / 32 ? sums[lane] : 0u, wi = w;
+        for (int k = 0; k < kPer; ++k) {
+            const uint32_t v = lane * kPer + k < held * kWarps ? line[lane * kPer + k] : 0u;
+            part += k < own ? v : 0u;
+            sum += v;
+        }
+        uint32_t incl = sum;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, wi, d);
-        if (lane >= d) wi += u;
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += u;
+        }
+        before = incl - sum + part;
+        total = __shfl_sync(0xffffffffu, incl, 31);
     }
-    *total = __shfl_sync(0xffffffffu, wi, 31);
-    return __shfl_sync(0xffffffffu, wi - w, warp) + incl - v;
-}
+    __device__ __forceinline__ static uint32_t at(uint32_t before, int row) {
+        return __shfl_sync(0xffffffffu, before, (row * kWarps + (threadIdx.x >> 5)) / kPer);
+    }
+};
 
 // ---- moves ----------------------------------------------------------------
 // Moves [n0, n1) of the lists, at most kMost: K and V rows, weight and
@@ -150,17 +160,15 @@ template <int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
     evict_select_kernel(const __grid_constant__ EvictParams p) {
     constexpr int kWarps = kThreads / 32, kChunk = kThreads * kEvictKeys;
-    static_assert(kEvictBins % kThreads == 0, "whole bins to a thread");
-    __shared__ __align__(16) uint32_t hist[3][kEvictBins];
-    __shared__ uint32_t sums[32];
+    __shared__ __align__(16) uint32_t hist[4][kEvictBins], joint[4][kEvictBins];
     __shared__ __align__(16) uint32_t counts[4];    // below left: above T, equal to T; past left: the same
-    __shared__ uint32_t digit_s, above_s, inside_s;
+    __shared__ int4 found[4];                   // per digit: it, tokens above its bin and inside
     __shared__ uint32_t line[2][kEvictKeys * kWarps];
     __shared__ int32_t own_gaps[kEvictOwnMoves], own_movers[kEvictOwnMoves];
     __shared__ MoveRows<kEvictOwnMoves> rows;
     const int C = p.cluster, rank = blockIdx.x % C;
     const int g = blockIdx.x / C, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < 3 * kEvictBins / 4; i += kThreads)
+    for (int i = tid; i < 4 * kEvictBins / 4; i += kThreads)
         reinterpret_cast<uint4*>(&hist[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
     if (tid < 4) counts[tid] = 0;
     grid_dependency_wait();
@@ -188,17 +196,23 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
     uint32_t key[kEvictKeys];
     // rows of kThreads tokens that the chunk at c0 has
     auto rows_of = [&](int c0) { return min(kEvictKeys, (hi - c0 + kThreads - 1) / kThreads); };
-    auto load = [&](int c0) {                   // images of tokens c0 + tid, + kThreads, ...
-        const int n = rows_of(c0);
+    // positions, weights and images of tokens c0 + tid, + kThreads, ...; all
+    // loads requested before the first is used
+    int at[kEvictKeys];
+    float x[kEvictKeys];
+    auto load = [&](int c0) {
+        const int n = rows_of(c0), known = min(hi, s.known), ahead = s.seen - s.L;
 #pragma unroll
         for (int e = 0; e < kEvictKeys; ++e) {
             if (e >= n) break;
             const int i = c0 + e * kThreads + tid;
-            key[e] = 0;
-            if (i < hi) {
-                const int at = evict_position(s, pos, i);
-                key[e] = at < p.sinks || at >= newest ? kProtected : weight_image(w[i]);
-            }
+            at[e] = i < known ? pos[i] : i + ahead;
+            x[e] = i < hi ? w[i] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < kEvictKeys; ++e) {
+            if (e >= n) break;
+            key[e] = at[e] < p.sinks || at[e] >= newest ? kProtected : weight_image(x[e]);
         }
     };
     auto barrier = [&] {
@@ -209,68 +223,67 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
     if (once) load(lo);
     __syncthreads();                            // histograms cleared
     // T, the image of the left-th largest, and how many of its equals stay
-    uint32_t T = 0, want = s.left;
+    uint32_t T = 0, want = s.left, inside = 0;
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), top = pass == 0 ? 32 : (pass == 1 ? 21 : 10);
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
         for (int c0 = lo; c0 < hi; c0 += kChunk) {
             if (!once) load(c0);
             const int n = rows_of(c0);
 #pragma unroll
             for (int e = 0; e < kEvictKeys; ++e) {
                 if (e >= n) break;
-                if (c0 + e * kThreads + tid < hi && (pass == 0 || (key[e] >> top) == (T >> top)))
-                    atomicAdd(&hist[pass][(key[e] >> shift) & (pass == 2 ? 1023u : 2047u)], 1u);
+                if (c0 + e * kThreads + tid < hi && (pass == 0 || (key[e] ^ T) >> shift < 256u))
+                    atomicAdd(&hist[pass][(key[e] >> shift) & 255u], 1u);
             }
         }
         barrier();
-        // bins from the top one down, kEvictBins / kThreads to a thread
-        constexpr int kPer = kEvictBins / kThreads;
-        uint32_t mine[kPer], sum = 0;
-        {
-            // they end at bin kEvictBins - 1 - kPer * tid; 2 or 8 words, read whole
-            const uint32_t* low = &hist[pass][kEvictBins - kPer * (tid + 1)];
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) mine[k] = 0;
-            for (int r = 0; r < C; ++r) {
-                if constexpr (kPer % 4 == 0) {
-#pragma unroll
-                    for (int k = 0; k < kPer; k += 4) {
-                        const uint4 v = C == 1 ? *reinterpret_cast<const uint4*>(low + k) : cluster_words(low + k, r);
-                        mine[kPer - 1 - k] += v.x, mine[kPer - 2 - k] += v.y;
-                        mine[kPer - 3 - k] += v.z, mine[kPer - 4 - k] += v.w;
-                    }
-                } else {
-                    static_assert(kPer == 2, "a pair of bins, from the half of a quad");
-                    uint2 v;
-                    if (C == 1) {
-                        v = *reinterpret_cast<const uint2*>(low);
-                    } else {
-                        const uint4 q = cluster_words(&hist[pass][(kEvictBins - kPer * (tid + 1)) & ~3], r);
-                        v = (tid & 1) ? make_uint2(q.x, q.y) : make_uint2(q.z, q.w);
-                    }
-                    mine[0] += v.y, mine[1] += v.x;
+        if (C > 1) {                            // the cluster's sum
+            if (tid < kEvictBins / 4) {
+                uint4 sum = make_uint4(0u, 0u, 0u, 0u);
+                for (int r = 0; r < C; ++r) {
+                    const uint4 v = cluster_words(&hist[pass][4 * tid], r);
+                    sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
                 }
+                *reinterpret_cast<uint4*>(&joint[pass][4 * tid]) = sum;
             }
+            __syncthreads();
         }
+        // one warp: bins from the top one down, eight to a lane
+        if (warp == 0) {
+            const uint4* low = reinterpret_cast<const uint4*>(&(C > 1 ? joint : hist)[pass][kEvictBins - 8 * (lane + 1)]);
+            const uint4 v0 = low[0], v1 = low[1];
+            const uint32_t bins[8] = {v1.w, v1.z, v1.y, v1.x, v0.w, v0.z, v0.y, v0.x};
+            uint32_t sum = 0;
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) sum += mine[k];
-        uint32_t total;
-        uint32_t before = block_prefix<kThreads>(sum, sums, &total);
+            for (int k = 0; k < 8; ++k) sum += bins[k];
+            uint32_t above = sum;
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            if (before < want && before + mine[k] >= want)
-                digit_s = kEvictBins - 1 - (kPer * tid + k), above_s = before, inside_s = mine[k];
-            before += mine[k];
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xffffffffu, above, d);
+                if (lane >= d) above += u;
+            }
+            const bool mine = above >= want && above - sum < want;
+            above -= sum;
+            int digit = 255 - 8 * lane;
+            uint32_t in = bins[0];
+#pragma unroll
+            for (int k = 1; k < 8; ++k) {           // as long as the bin ends before the want-th
+                const bool past = above + in < want && digit == 256 - 8 * lane - k;
+                if (past) above += in, in = bins[k], --digit;
+            }
+            if (mine) found[pass] = make_int4(digit, (int)above, (int)in, 0);
         }
         __syncthreads();
-        T |= digit_s << shift;
-        want -= above_s;
+        const int4 f = found[pass];
+        T |= (uint32_t)f.x << shift;
+        want -= f.y;
+        inside = f.z;
         // the whole bin stays: its lower bits do not matter
-        if (inside_s == want) break;
+        if (inside == want) break;
     }
     // where every equal stays, none needs its rank among them
-    const bool ranked = inside_s != want;
+    const bool ranked = inside != want;
     // the slices before this one: their equals, gaps and movers
     uint32_t equal = 0, n_gaps = 0, n_movers = 0, moves = 0;
     if (C > 1) {
@@ -314,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
         if (!once) load(c0);
         if (c0 > lo) __syncthreads();           // the previous chunk's reads of line
         const int held = rows_of(c0);
-        uint32_t total, at;
+        uint32_t equals_before = 0;             // of this warp's rows, by lane
         if (ranked) {
             // rank among the equals: rows of kThreads tokens, warps, lanes
 #pragma unroll
@@ -324,12 +337,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
                 if (lane == 0) line[0][e * kWarps + warp] = __popc(eq);
             }
             __syncthreads();
-            at = block_prefix<kThreads>(tid < held * kWarps ? line[0][tid] : 0u, sums, &total);
-            if (tid < held * kWarps) line[0][tid] = equal + at;
-            equal += total;
-            __syncthreads();
+            const RowPrefix<kWarps> ranks(line[0], held);
+            equals_before = equal + ranks.before;
+            equal += ranks.total;
         }
-        uint32_t gap_bits = 0, mover_bits = 0, gap_mask[kEvictKeys], mover_mask[kEvictKeys];
+        uint32_t gap_bits = 0, mover_bits = 0;
 #pragma unroll
         for (int e = 0; e < kEvictKeys; ++e) {
             if (e >= held) break;
@@ -338,40 +350,40 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
             bool keep = in && key[e] >= T;
             if (ranked) {
                 const uint32_t eq = __ballot_sync(0xffffffffu, is_eq);
-                if (is_eq) keep = line[0][e * kWarps + warp] + __popc(eq & ((1u << lane) - 1u)) < want;
+                const uint32_t first = RowPrefix<kWarps>::at(equals_before, e);
+                if (is_eq) keep = first + __popc(eq & ((1u << lane) - 1u)) < want;
             }
             const bool gap = in && i < s.left && !keep, mover = keep && i >= s.left;
-            gap_mask[e] = __ballot_sync(0xffffffffu, gap);
-            mover_mask[e] = __ballot_sync(0xffffffffu, mover);
+            const uint32_t gap_mask = __ballot_sync(0xffffffffu, gap), mover_mask = __ballot_sync(0xffffffffu, mover);
             gap_bits |= (uint32_t)gap << e, mover_bits |= (uint32_t)mover << e;
             // both counts of a chunk fit 16 bits
-            if (lane == 0) line[1][e * kWarps + warp] = __popc(gap_mask[e]) | (__popc(mover_mask[e]) << 16);
+            if (lane == 0) line[1][e * kWarps + warp] = __popc(gap_mask) | (__popc(mover_mask) << 16);
             if (keep && i < s.left) {
-                if (p.weights_out != p.weights) wo[i] = w[i];
-                if (p.positions_out != p.positions || i >= s.known) po[i] = evict_position(s, pos, i);
+                if (p.weights_out != p.weights) wo[i] = x[e];
+                if (p.positions_out != p.positions || i >= s.known) po[i] = at[e];
             }
         }
         __syncthreads();
-        at = block_prefix<kThreads>(tid < held * kWarps ? line[1][tid] : 0u, sums, &total);
-        if (tid < held * kWarps) line[1][tid] = at;
-        __syncthreads();
+        const RowPrefix<kWarps> counted(line[1], held);
 #pragma unroll
         for (int e = 0; e < kEvictKeys; ++e) {
             if (e >= held) break;
             const int i = c0 + e * kThreads + tid;
-            const uint32_t before = line[1][e * kWarps + warp];
+            const uint32_t before = RowPrefix<kWarps>::at(counted.before, e);
+            const uint32_t gap_mask = __ballot_sync(0xffffffffu, (gap_bits >> e) & 1u);
+            const uint32_t mover_mask = __ballot_sync(0xffffffffu, (mover_bits >> e) & 1u);
             if ((gap_bits >> e) & 1u) {
-                const int n = n_gaps + (before & 0xffffu) + __popc(gap_mask[e] & ((1u << lane) - 1u));
+                const int n = n_gaps + (before & 0xffffu) + __popc(gap_mask & ((1u << lane) - 1u));
                 gaps[n] = i;
                 if (n < kEvictOwnMoves) own_gaps[n] = i;
             }
             if ((mover_bits >> e) & 1u) {
-                const int n = n_movers + (before >> 16) + __popc(mover_mask[e] & ((1u << lane) - 1u));
+                const int n = n_movers + (before >> 16) + __popc(mover_mask & ((1u << lane) - 1u));
                 movers[n] = i;
                 if (n < kEvictOwnMoves) own_movers[n] = i;
             }
         }
-        n_gaps += total & 0xffffu, n_movers += total >> 16;
+        n_gaps += counted.total & 0xffffu, n_movers += counted.total >> 16;
     }
     if (C == 1) moves = n_gaps;
     const bool own = moves <= (uint32_t)(kEvictOwnMoves * C);
@@ -418,10 +430,10 @@ cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream) {
 cudaError_t launch_evict(const EvictParams& params, cudaStream_t stream) {
     EvictParams p = params;
     // What the tables can hold decides: 256 threads where that fits their
-    // registers (four such CTAs share an SM; 64 x 8 rows of 1040 tokens 13.2
-    // us, 128 threads of 16 images 18.1, 512 of four 20.0), else 1024, and a
-    // cluster that holds the longest context in registers, up to the portable
-    // size (16 x 8 rows of up to 8192 29.4 us, 512 threads of 16 images 31.6).
+    // registers (four such CTAs share an SM; 64 x 8 rows of 1040 tokens 11.2
+    // us, 128 threads of 16 images 13.8), else 1024, and a cluster that holds
+    // the longest context in registers, up to the portable size (16 x 8 rows
+    // of up to 8192 28.3 us with the moves).
     const int64_t longest = (int64_t)p.max_blocks_per_seq * p.block_size;
     const bool small = longest <= 256 * kEvictKeys;
     const int64_t ctas = (longest + 1024 * kEvictKeys - 1) / (1024 * kEvictKeys);
