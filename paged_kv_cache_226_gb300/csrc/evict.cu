@@ -84,12 +84,22 @@ struct RowPrefix {
     uint32_t before, total;
     __device__ __forceinline__ RowPrefix(const uint32_t* line, int held) {
         const int lane = threadIdx.x & 31, own = (threadIdx.x >> 5) % kPer;
-        uint32_t sum = 0, part = 0;
+        uint32_t v[kPer], sum = 0, part = 0;
+        // a lane's counts are of one row; read in whole words, where single
+        // ones would meet in the same banks
+        if constexpr (kPer == 8) {
+            const uint4 a = reinterpret_cast<const uint4*>(line)[2 * lane], b = reinterpret_cast<const uint4*>(line)[2 * lane + 1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+            static_assert(kPer == 2, "8 or 32 warps");
+            const uint2 a = reinterpret_cast<const uint2*>(line)[lane];
+            v[0] = a.x, v[1] = a.y;
+        }
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const uint32_t v = lane * kPer + k < held * kWarps ? line[lane * kPer + k] : 0u;
-            part += k < own ? v : 0u;
-            sum += v;
+            if (lane * kPer >= held * kWarps) v[k] = 0;
+            part += k < own ? v[k] : 0u;
+            sum += v[k];
         }
         uint32_t incl = sum;
 #pragma unroll
@@ -163,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
     __shared__ __align__(16) uint32_t hist[4][kEvictBins], joint[4][kEvictBins];
     __shared__ __align__(16) uint32_t counts[4];    // below left: above T, equal to T; past left: the same
     __shared__ int4 found[4];                   // per digit: it, tokens above its bin and inside
-    __shared__ uint32_t line[2][kEvictKeys * kWarps];
+    __shared__ __align__(16) uint32_t line[2][kEvictKeys * kWarps];
     __shared__ int32_t own_gaps[kEvictOwnMoves], own_movers[kEvictOwnMoves];
     __shared__ MoveRows<kEvictOwnMoves> rows;
     const int C = p.cluster, rank = blockIdx.x % C;
