@@ -101,8 +101,8 @@ int decode_weights(const void* q, const void* k_cache, const void* v_cache,
     if (fp8 && (st = pa::check_fp8(shp, k_scale, v_scale)) != PA_OK) return st;
     const WeightsWorkspace w = weights_layout(shp, max_context_len, partition_size);
     if (w.parts == 0) return PA_ERR_INVALID_ARG;
-    // grids: a partition, or 1024 tokens of the merge, along z
-    if (w.parts > 65535 || max_context_len / 1024 > 65000) return PA_ERR_UNSUPPORTED;
+    // grids: a partition, or 256 tokens of the merge at least, along z
+    if (w.parts > 65535 || max_context_len / 256 > 65000) return PA_ERR_UNSUPPORTED;
     if (shp->num_seqs == 0) return PA_OK;
     if (!out || !aligned16(out)) return PA_ERR_INVALID_ARG;
     if ((st = check_state(weights, weights_out, weights_stride, shp)) != PA_OK) return st;

@@ -19,8 +19,13 @@
 namespace pa {
 
 constexpr int kMergeThreads = 256;
-constexpr int kMergeTokens = 4;              // tokens of a thread, their scores in flight together
-constexpr int kMergeChunk = kMergeThreads * kMergeTokens;
+// Tokens of a thread, their scores in flight together, and CTAs per SM that
+// the registers are held to.  Many scores a token: one, in eight CTAs (E4M3,
+// 256 pairs of 4096 tokens, decode and merge 68.8 us; two in five 70.7, four
+// in four 70.2).  Four: four in six (512 pairs of up to 2048 56.6, four in
+// four 57.3, two in eight 60.8).
+__host__ __device__ constexpr int merge_tokens(int group) { return group == 8 ? 1 : 4; }
+__host__ __device__ constexpr int merge_ctas(int group) { return group == 8 ? 8 : group == 4 ? 6 : 4; }
 
 // The group's scores of one token; kG = 0: any group, read one by one.
 template <int kG>
@@ -43,11 +48,11 @@ struct TokenScores {
     }
 };
 
-// Grid (sequences, KV heads, 1 + chunks of 1024 tokens): z = 0 merges out,
+// Grid (sequences, KV heads, 1 + chunks of tokens): z = 0 merges out,
 // z = 1 + c adds up the weights of chunk c.  A chunk's scores and earlier
 // weights are requested before the row sums that they wait for are formed.
 template <typename T, int D, int kG>
-__global__ void __launch_bounds__(kMergeThreads)
+__global__ void __launch_bounds__(kMergeThreads, merge_ctas(kG))
     weights_merge_kernel(const __grid_constant__ WeightsMergeParams p) {
     __shared__ float top[kMaxGroup], inv[kMaxGroup];
     __shared__ float4 part_out[kMergeThreads];
@@ -59,6 +64,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     const int parts = min((L + p.partition_tokens - 1) / p.partition_tokens, p.max_parts);
     const int end = min(L, parts * p.partition_tokens);          // tokens attended to
     const size_t qh0 = (size_t)b * p.num_q_heads + (size_t)g * G;
+    constexpr int kMergeTokens = merge_tokens(kG), kMergeChunk = kMergeThreads * kMergeTokens;
     const int t0 = ((int)blockIdx.z - 1) * kMergeChunk + tid;
     if (parts == 0) {
         if (blockIdx.z == 0) {
@@ -162,7 +168,8 @@ cudaError_t launch_weights_merge_g(const WeightsMergeParams& p, dim3 grid, cudaS
 cudaError_t launch_weights_merge(int dtype, int head_dim, const WeightsMergeParams& p,
                                  int num_seqs, cudaStream_t stream) {
     const int longest = (int)std::min<int64_t>((int64_t)p.max_parts * p.partition_tokens, p.max_context);
-    const dim3 grid(num_seqs, p.num_kv_heads, 1 + (longest + kMergeChunk - 1) / kMergeChunk);
+    const int chunk = kMergeThreads * merge_tokens(p.group);
+    const dim3 grid(num_seqs, p.num_kv_heads, 1 + (longest + chunk - 1) / chunk);
     if (dtype == PA_BF16)
         return head_dim == 64 ? launch_weights_merge_g<__nv_bfloat16, 64>(p, grid, stream)
                               : launch_weights_merge_g<__nv_bfloat16, 128>(p, grid, stream);
