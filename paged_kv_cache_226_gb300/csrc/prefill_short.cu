@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     } else if (epilogue && tiles > 0) {
         float m = -INFINITY, z = 0.f;
         if (works) {
-            const int blk = pw_blocks(p, s, b, kt >> 2);
+            const int blk = pw_checked(p, pw_blocks(p, s, b, kt >> 2));
             pw_load_keys<D, 2>(&tmap_k, k_tiles + group * Lay::kTile, &k_full[group], p, s, g, kt, blk, warp & 3, 8, 4);
             const int visible = min(s.L - s.counted + r / G, s.L - 1) - kt * kPwCols;
             if (p.weights && kt * kPwCols + r < s.L - s.C) before = p.weights[at];

@@ -232,9 +232,11 @@ __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
             int quad = -2, blk = 0, blk_next = 0;
             auto to_tile = [&](int kt) {
                 if ((kt >> 2) == quad) return;
-                blk = (kt >> 2) == quad + 1 ? blk_next : pw_blocks(p, walk.s, U.b, kt >> 2);
+                if ((kt >> 2) != quad + 1) blk_next = pw_blocks(p, walk.s, U.b, kt >> 2);
                 quad = kt >> 2;
-                blk_next = pw_blocks(p, walk.s, U.b, quad + 1);
+                const int ahead = pw_blocks(p, walk.s, U.b, quad + 1);
+                blk = pw_checked(p, blk_next);
+                blk_next = ahead;
             };
             if (U.first >= U.last) continue;
             for (int j = 0; ok && j < walk.residents(U); ++j) {

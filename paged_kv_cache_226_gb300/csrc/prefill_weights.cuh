@@ -191,16 +191,20 @@ __device__ __forceinline__ float column_sums(uint32_t tile_addr, const float* ne
 }
 
 // Block ids of key tiles 4 q .. 4 q + 3: lane i has box i % 8 of tile i / 8.
+// Requested here, looked at by pw_checked, so that two requests can be under way.
 __device__ __forceinline__ int pw_blocks(const PrefillWeightsParams& p, const PwSeq& s, int b, int q) {
     const int tok = q * 4 * kPwCols + 16 * (threadIdx.x & 31);
     if (tok < 0 || tok >= s.L) return 0;
-    const int blk = __ldg(p.block_tables + (size_t)b * p.max_blocks_per_seq + tok / p.block_size);
+    return __ldg(p.block_tables + (size_t)b * p.max_blocks_per_seq + tok / p.block_size);
+}
+
+__device__ __forceinline__ int pw_checked(const PrefillWeightsParams& p, int blk) {
     if (blk < 0 || blk >= p.num_blocks) flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
     return blk;
 }
 
 // Boxes from, from + step, ... below `to` (kMost at most) of key tile kt (its tokens through the block table: `blk`
-// as pw_blocks gives it), announced on `bar` and issued; all lanes run along.
+// as pw_checked gives it), announced on `bar` and issued; all lanes run along.
 template <int D, int kMost>
 __device__ __forceinline__ void pw_load_keys(const CUtensorMap* map, uint8_t* dst, uint64_t* bar,
                                              const PrefillWeightsParams& p, const PwSeq& s, int g,

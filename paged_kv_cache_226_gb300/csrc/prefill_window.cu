@@ -42,30 +42,47 @@ struct PwRun {
 // Backward, sequences, heads and tiles are counted from the last.
 template <bool kBackward>
 struct PwRuns {
-    unsigned at, end, base = 0, total = 0, ends = 0;
-    int base_b = -32;
+    unsigned at = 0, end = 0, base = 0, total = 0, ends = 0;
+    int base_b = 0;
     PwSeq mine, s;
 
-    __device__ __forceinline__ PwRuns(unsigned from, unsigned to) : at(from), end(to) {}
+    // The next 32 sequences' tiles: `ends` after each lane's, `total` in all.
+    __device__ __forceinline__ void read(const PrefillWeightsParams& p, bool report) {
+        const int lane = threadIdx.x & 31, i = base_b + lane;
+        ends = 0;
+        if (i < p.num_seqs) {
+            pw_sequence(p, kBackward ? p.num_seqs - 1 - i : i, report, mine);
+            ends = (unsigned)mine.n_kt * p.num_kv_heads;
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const unsigned v = __shfl_up_sync(0xffffffffu, ends, d);
+            if (lane >= d) ends += v;
+        }
+        total = __shfl_sync(0xffffffffu, ends, 31);
+    }
+    // Key tiles of the batch (the count fits 31 bits: checked on the host),
+    // left at the first sequences.
+    __device__ __forceinline__ unsigned count(const PrefillWeightsParams& p, bool report) {
+        unsigned n = 0;
+        for (int b0 = 32; b0 < p.num_seqs; b0 += 32) {
+            const int i = b0 + (int)(threadIdx.x & 31);
+            PwSeq q;
+            q.n_kt = 0;
+            if (i < p.num_seqs) pw_sequence(p, kBackward ? p.num_seqs - 1 - i : i, report, q);
+            n += (unsigned)q.n_kt * p.num_kv_heads;
+        }
+        read(p, report);
+        return __reduce_add_sync(0xffffffffu, n) + total;
+    }
 
     __device__ __forceinline__ bool next(const PrefillWeightsParams& p, PwRun& R) {
         if (at >= end) return false;
-        const int lane = threadIdx.x & 31;
         while (at >= base + total) {
             base += total;
             base_b += 32;
-            const int i = base_b + lane;
-            ends = 0;
-            if (i < p.num_seqs) {
-                pw_sequence(p, kBackward ? p.num_seqs - 1 - i : i, false, mine);
-                ends = (unsigned)mine.n_kt * p.num_kv_heads;
-            }
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const unsigned v = __shfl_up_sync(0xffffffffu, ends, d);
-                if (lane >= d) ends += v;
-            }
-            total = __shfl_sync(0xffffffffu, ends, 31);
+            if (base_b >= p.num_seqs) return false;
+            read(p, false);
         }
         const int who = __ffs(__ballot_sync(0xffffffffu, at - base < ends)) - 1;
         const unsigned before = __shfl_sync(0xffffffffu, ends, max(who - 1, 0));
@@ -98,7 +115,6 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     __shared__ __align__(8) uint64_t k_full[kWkStages], k_empty[kWkStages], q_full[kWqStages], q_empty[kWqStages];
     __shared__ __align__(8) uint64_t s_full[kPwBufs], s_empty[kPwBufs];
     __shared__ uint32_t tmem_base;
-    __shared__ unsigned total_s;
     __shared__ __align__(16) float lse_s[kPwGroups][2][kPwCols];     // pass 2: [group][row parity]
     __shared__ float2 other[2][kPwGroups - 1][kPwRows];              // pass 1: [join parity][group]
     extern __shared__ uint8_t smem_raw[];
@@ -111,7 +127,6 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     uint8_t* q_ring = smem + kWkStages * Lay::kTile;
 
     if (threadIdx.x == 0) {
-        total_s = 0;
         for (int i = 0; i < kWkStages; ++i) mbar_init(&k_full[i], 2), mbar_init(&k_empty[i], 1);
         for (int i = 0; i < kWqStages; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 2);
         for (int i = 0; i < kPwBufs; ++i) mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4);
@@ -126,32 +141,24 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     }
     grid_dependency_wait();
     allow_dependent_launch();
-    __syncthreads();
-    // key tiles of the batch (the count fits 31 bits: checked on the host)
-    {
-        unsigned n = 0;
-        for (int b = threadIdx.x; b < p.num_seqs; b += kWindowThreads) {
-            PwSeq s;
-            pw_sequence(p, b, (kStats || p.max_counted == 0) && blockIdx.x == 0, s);
-            n += (unsigned)s.n_kt * p.num_kv_heads;
-        }
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (lane == 0 && n > 0) atomicAdd(&total_s, n);
-    }
+    PwRuns<!kStats> runs;
+    const unsigned N = runs.count(p, (kStats || p.max_counted == 0) && blockIdx.x == 0 && warp == 0);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
     // CTA c has the tiles [c N / ctas, (c + 1) N / ctas), one at least; CTAs
     // past the number of tiles have none
-    const unsigned N = __shfl_sync(0xffffffffu, total_s, 0), ctas = min((unsigned)gridDim.x, N);
+    const unsigned ctas = min((unsigned)gridDim.x, N);
     const bool idle = blockIdx.x >= ctas;
-    const unsigned from = idle ? 0u : (unsigned)((uint64_t)blockIdx.x * N / ctas);
-    const unsigned to = idle ? 0u : (unsigned)((uint64_t)(blockIdx.x + 1) * N / ctas);
+    if (!idle) {                                 // c N / ctas in 32 bits
+        const unsigned whole = N / ctas, rest = N % ctas;
+        runs.at = blockIdx.x * whole + blockIdx.x * rest / ctas;
+        runs.end = (blockIdx.x + 1) * whole + (blockIdx.x + 1) * rest / ctas;
+    }
     auto cta_of = [&](unsigned tile) { return (int)((((uint64_t)tile + 1) * ctas - 1) / N); };
     // tile of a run's place k
     auto tile_of = [](const PwSeq& s, int k) { return kStats ? k : s.n_kt - 1 - k; };
-    PwRuns<!kStats> runs(from, to);
     PwRun R;
 
     if (warp == 2 || warp == 3 || warp >= kPwLoadersAfter) {
@@ -179,9 +186,11 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
             for (int k = R.k0; ok && k < R.k1; ++k, ++n) {
                 const int kt = tile_of(s, k);
                 if ((kt >> 2) != quad) {
-                    blk = (kt >> 2) == quad + kAhead ? blk_next : pw_blocks(p, s, R.b, kt >> 2);
+                    if ((kt >> 2) != quad + kAhead) blk_next = pw_blocks(p, s, R.b, kt >> 2);
                     quad = kt >> 2;
-                    blk_next = pw_blocks(p, s, R.b, quad + kAhead);
+                    const int ahead = pw_blocks(p, s, R.b, quad + kAhead);
+                    blk = pw_checked(p, blk_next);
+                    blk_next = ahead;
                 }
                 const int st = n % kWkStages;
                 if (who != st && who != 4 + (n & 1)) continue;
