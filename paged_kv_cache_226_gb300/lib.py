@@ -1010,10 +1010,12 @@ class StepPlan:
     reduce), ``"single"`` (reshape_and_cache, decode) and ``"weights"``
     (reshape_and_cache, decode_weights: each step adds the attention weights
     into ``weights``, or reads them there and writes ``weights_out``;
-    ``capture_graph`` makes one such step before it captures).  The work goes to the caller's current stream at call time, which also makes a step capturable into a CUDA graph
-    (``capture_graph``).  The tensors must stay alive and keep their shapes;
-    their contents (new tokens, tables, lengths) may change between steps as
-    long as ``context_lens`` stays within ``max_context_len``.
+    ``capture_graph`` makes one such step before it captures).  The work goes
+    to the caller's current stream at call time, which also makes a step
+    capturable into a CUDA graph (``capture_graph``).  The tensors must stay
+    alive and keep their shapes; their contents (new tokens, tables, lengths)
+    may change between steps as long as ``context_lens`` stays within
+    ``max_context_len``.
 
     In the fused mode q, k_new, v_new, slot_mapping, block_tables,
     context_lens and out may be pinned host tensors: the kernel reads the

@@ -357,3 +357,38 @@ def test_step_plan(dev, fp8):
     with pytest.raises(ValueError):
         lib.StepPlan(q, kn, vn, slots, k, v, x.tables.to(dev), x.lens.to(dev), x.scale, 300, weights=w, **x.scales())
     assert lib.read_device_errors(dev) == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,high", [(8, 2, 64, 250), (8, 2, 128, 900), (32, 8, 128, 3000)])
+def test_captured_calls_follow_the_lengths(dev, hq, hkv, d, high):
+    """Both operators captured once and replayed with other lengths, empty and
+    full ones among them, against eager calls, bit for bit."""
+    x = Batch([high] * 4, hq, hkv, d, 16, F16, seed=41, stale=False)
+    q, k, v, tables = x.q.to(dev), x.k.to(dev), x.v.to(dev), x.tables.to(dev)
+    chunk = torch.randn(64, hq, d, generator=x.gen).to(F16).to(dev)
+    start = torch.tensor([0, 16, 32, 48, 64], dtype=torch.int32, device=dev)
+    lens = x.lens.to(dev)
+    wd, wp = (torch.zeros(4, hkv, x.tokens, device=dev) for _ in range(2))
+    out = torch.empty_like(q)
+
+    def step(a, b, o):
+        lib.decode_weights(q, k, v, tables, lens, x.scale, high, weights_out=a, out=o)
+        lib.prefill_weights(chunk, k, tables, lens, start, x.scale, 16, high, weights_out=b)
+
+    step(wd, wp, out)
+    torch.cuda.synchronize(dev)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(wd, wp, out)
+    for now in ([high, 17, 16, 100], [16, high, 129, 128], [high] * 4, [33, 20, 16, 16]):
+        lens.copy_(torch.tensor(now, dtype=torch.int32))
+        for t in (wd, wp):
+            t.fill_(-7.0)
+        g.replay()
+        torch.cuda.synchronize(dev)
+        a, b, o = (torch.full_like(t, -7.0) for t in (wd, wp, out))
+        step(a, b, o)
+        torch.cuda.synchronize(dev)
+        assert same_bits(wd, a) and same_bits(wp, b) and same_bits(out, o)
+    del g
+    assert lib.read_device_errors(dev) == 0
