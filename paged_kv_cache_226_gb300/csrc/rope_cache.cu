@@ -17,7 +17,7 @@
 namespace pa {
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeCtas = 10;                 // per SM
+constexpr int kRopeCtas = 9;                  // per SM
 
 // Position-independent part of the angle: turns per position, in 2^-64.
 __device__ __forceinline__ int64_t rope_turns(float inv_freq) {
@@ -60,10 +60,15 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale) {
 // token, two 16-byte chunks: the two halves of eight pairs, or two chunks
 // past the rotated dims.  A thread keeps its place u inside the head and
 // walks the heads of its CTA's tokens, q first, kRopeBatch at a time with all
-// their loads in flight; the first batch is requested before the positions
-// have arrived and while cos and sin are formed.
+// their loads in flight, then k and v of a head together; the first batch is
+// requested before the positions have arrived and while cos and sin are formed.
 constexpr int kRopeBatch = 2;
 enum RopeRows { kRopeQ, kRopeK, kRopeV };
+// places of the batch: q takes both for two heads, k and v one each
+template <int kFirst, int kEnd>
+struct RopePlaces {
+    static constexpr int kFrom = kFirst, kTo = kEnd;
+};
 
 template <typename T, int D, bool kFp8, bool kInterleaved, int kTokens>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
@@ -87,14 +92,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
         return tk;
     };
     uint4 v0[kRopeBatch], v1[kRopeBatch];
-    auto load = [&](auto rows, int at) {
-        constexpr int kRows = decltype(rows)::value;
+    auto load = [&](auto rows, auto places, int at) {
+        constexpr int kRows = decltype(rows)::value, kFrom = decltype(places)::kFrom, kTo = decltype(places)::kTo;
         const int heads = kRows == kRopeQ ? p.num_q_heads : p.num_kv_heads;
         const T* base = static_cast<const T*>(kRows == kRopeQ ? p.q : (kRows == kRopeK ? p.k : p.v));
         const int64_t stride = kRows == kRopeQ ? p.q_stride : (kRows == kRopeK ? p.k_stride : p.v_stride);
 #pragma unroll
-        for (int k = 0; k < kRopeBatch; ++k) {
-            const int v = at + k * kHeads;
+        for (int k = kFrom; k < kTo; ++k) {
+            const int v = at + (k - kFrom) * kHeads;
             if (v >= tokens * heads) break;
             const int tk = token_of(v, heads);
             const uint4* src = reinterpret_cast<const uint4*>(base + (t0 + tk) * stride + (v - tk * heads) * D);
@@ -102,12 +107,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
             v1[k] = src[kRows == kRopeV ? 2 * u + 1 : c1];
         }
     };
-    auto store = [&](auto rows, int at) {
-        constexpr int kRows = decltype(rows)::value;
+    auto store = [&](auto rows, auto places, int at) {
+        constexpr int kRows = decltype(rows)::value, kFrom = decltype(places)::kFrom, kTo = decltype(places)::kTo;
         const int heads = kRows == kRopeQ ? p.num_q_heads : p.num_kv_heads;
 #pragma unroll
-        for (int k = 0; k < kRopeBatch; ++k) {
-            const int v = at + k * kHeads;
+        for (int k = kFrom; k < kTo; ++k) {
+            const int v = at + (k - kFrom) * kHeads;
             if (v >= tokens * heads) break;
             const int tk = token_of(v, heads), h = v - tk * heads;
             const int64_t slot = kRows == kRopeQ ? 0 : slot_s[tk];
@@ -164,7 +169,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     using Q = std::integral_constant<int, kRopeQ>;
     using K = std::integral_constant<int, kRopeK>;
     using V = std::integral_constant<int, kRopeV>;
-    load(Q(), first);
+    using All = RopePlaces<0, kRopeBatch>;
+    using First = RopePlaces<0, 1>;
+    using Second = RopePlaces<1, 2>;
+    load(Q(), All(), first);
     const int pairs = p.rotary_dim / 2;
     for (int i = tid; i < tokens * pairs; i += kRopeThreads) {
         const int tk = i / pairs, j = i - tk * pairs;
@@ -176,24 +184,25 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
         if (slot >= p.num_slots) flag_error(p.err, PA_DEVERR_BAD_SLOT);
     }
     __syncthreads();
-    store(Q(), first);
+    store(Q(), All(), first);
     for (int at = first + kRopeBatch * kHeads; at < tokens * p.num_q_heads; at += kRopeBatch * kHeads) {
-        load(Q(), at);
-        store(Q(), at);
+        load(Q(), All(), at);
+        store(Q(), All(), at);
     }
-    for (int at = first; at < tokens * p.num_kv_heads; at += kRopeBatch * kHeads) {
-        load(K(), at);
-        store(K(), at);
-        load(V(), at);
-        store(V(), at);
+    for (int at = first; at < tokens * p.num_kv_heads; at += kHeads) {
+        load(K(), First(), at);
+        load(V(), Second(), at);
+        store(K(), First(), at);
+        store(V(), Second(), at);
     }
 }
 
 // Many small CTAs keep the grid's last wave short: 8192 tokens of 64 + 16
-// heads (336 MB) take 55.1 us with 128 threads, two tokens and ten CTAs an SM
-// (6.1 TB/s, 90 % of the copy rate), 58.9 with 256 threads, four tokens and
-// four CTAs; into an E4M3 cache, 5001 tokens of 32 + 16 heads 22.1 against
-// 24.4.  A single wave of tokens goes one to a CTA, which spreads it wider.
+// heads (336 MB) take 52.8 us with 128 threads, two tokens and nine CTAs an SM
+// (6.4 TB/s, 94 % of the copy rate), 54.3 with ten, 56.0 with eight, 58.9 with
+// 256 threads, four tokens and four CTAs; into an E4M3 cache, 5001 tokens of
+// 32 + 16 heads 21.2, with ten 22.9, with eight 22.2.  A single wave of tokens
+// goes one to a CTA, which spreads it wider.
 template <typename T, int D, bool kFp8, bool kInterleaved>
 cudaError_t launch_rope_i(const RopeParams& p, cudaStream_t stream) {
     const dim3 threads(kRopeThreads);
