@@ -118,6 +118,7 @@ struct EvictParams {
     int budget, trigger, sinks, recent;
     int moves_stride;
     int cluster;                   // CTAs of the select kernel per (sequence, KV head)
+    int own_moves;                 // moves that each makes itself
 };
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);

@@ -27,8 +27,8 @@ constexpr uint32_t kProtected = 0xffffffffu;
 constexpr int kEvictKeys = 8;                // images a thread holds
 constexpr int kEvictBins = 256;
 constexpr int kEvictMaxCluster = 8;
-// Moves per CTA that the select kernel makes itself: one round of rows for
-// its warps; more are spread by the move kernel.
+// Moves per CTA that the select kernel makes itself where its CTAs do not fill
+// the GPU: one round of rows for its warps; more are spread by the move kernel.
 constexpr int kEvictOwnMoves = 64;
 
 // Larger weight, larger image: -0 equals +0, NaN lies below everything.
@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
     __shared__ __align__(16) uint32_t counts[4];    // below left: above T, equal to T; past left: the same
     __shared__ int4 found[4];                   // per digit: it, tokens above its bin and inside
     __shared__ __align__(16) uint32_t line[2][kEvictKeys * kWarps];
-    __shared__ int32_t own_gaps[kEvictOwnMoves], own_movers[kEvictOwnMoves];
-    __shared__ MoveRows<kEvictOwnMoves> rows;
+    __shared__ int32_t own_gaps[kThreads], own_movers[kThreads];
+    __shared__ MoveRows<kThreads> rows;
     const int C = p.cluster, rank = blockIdx.x % C;
     const int g = blockIdx.x / C, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int i = tid; i < 4 * kEvictBins / 4; i += kThreads)
@@ -385,26 +385,28 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1)
             if ((gap_bits >> e) & 1u) {
                 const int n = n_gaps + (before & 0xffffu) + __popc(gap_mask & ((1u << lane) - 1u));
                 gaps[n] = i;
-                if (n < kEvictOwnMoves) own_gaps[n] = i;
+                if (n < kThreads) own_gaps[n] = i;
             }
             if ((mover_bits >> e) & 1u) {
                 const int n = n_movers + (before >> 16) + __popc(mover_mask & ((1u << lane) - 1u));
                 movers[n] = i;
-                if (n < kEvictOwnMoves) own_movers[n] = i;
+                if (n < kThreads) own_movers[n] = i;
             }
         }
         n_gaps += counted.total & 0xffffu, n_movers += counted.total >> 16;
     }
     if (C == 1) moves = n_gaps;
-    const bool own = moves <= (uint32_t)(kEvictOwnMoves * C);
+    const bool own = (int64_t)moves <= (int64_t)p.own_moves * C;
     if (rank == 0 && tid == 0) p.num_moves[pair] = own ? 0 : moves;
     // the lists are complete; also no CTA leaves while another reads its shared memory
     barrier();
     if (!own) return;
-    const int per = ((int)moves + C - 1) / C, n0 = min(rank * per, (int)moves);
-    // a CTA of its own has the lists in shared memory
-    move_rows<kThreads, kEvictOwnMoves>(p, s, b, g, pair, C == 1 ? own_gaps : gaps, C == 1 ? own_movers : movers, n0,
-                        min(n0 + per, (int)moves), rows);
+    const int per = ((int)moves + C - 1) / C, n0 = min(rank * per, (int)moves), n1 = min(n0 + per, (int)moves);
+    // a CTA of its own has the first of the lists in shared memory
+    const bool here = C == 1 && (int)moves <= kThreads;
+    for (int n = n0; n < n1; n += kThreads)
+        move_rows<kThreads, kThreads>(p, s, b, g, pair, here ? own_gaps : gaps, here ? own_movers : movers, n,
+                                      min(n + kThreads, n1), rows);
 }
 
 // 32 moves to 128 threads (17 us of 16 prompts' cut, 116 MB read and written,
@@ -444,13 +446,18 @@ cudaError_t launch_evict(const EvictParams& params, cudaStream_t stream) {
     // registers (four such CTAs share an SM; 64 x 8 rows of 1040 tokens 11.1
     // us, 128 threads of 16 images 13.8), else 1024, and a cluster that holds
     // the longest context in registers, up to the portable size (16 x 8 rows
-    // of up to 8192 27.5 us with the moves).
+    // of up to 8192 25.3 us with the moves).
     const int64_t longest = (int64_t)p.max_blocks_per_seq * p.block_size;
     const bool small = longest <= 256 * kEvictKeys;
     const int64_t ctas = (longest + 1024 * kEvictKeys - 1) / (1024 * kEvictKeys);
     p.cluster = small ? 1 : (int)(ctas < kEvictMaxCluster ? ctas : kEvictMaxCluster);
+    // Rows that fill three quarters of the SMs' select CTAs move everything
+    // themselves, those done early beside the others' selects (128 rows of up
+    // to 8192 25.3 us, with the move kernel 27.5; 64 rows 22.6 against 19.2).
+    const int64_t pairs = (int64_t)p.num_seqs * p.num_kv_heads;
+    p.own_moves = !small && p.cluster == 1 && pairs >= 114 ? INT32_MAX : kEvictOwnMoves;
     cudaError_t e = small ? launch_evict_select<256>(p, stream) : launch_evict_select<1024>(p, stream);
-    if (e != cudaSuccess || p.moves_stride <= kEvictOwnMoves * p.cluster) return e;
+    if (e != cudaSuccess || p.moves_stride <= (int64_t)p.own_moves * p.cluster) return e;
     const dim3 grid((p.moves_stride + kMoveBatch - 1) / kMoveBatch, p.num_kv_heads, p.num_seqs);
     return launch_with_pdl(evict_move_kernel, grid, dim3(kMoveThreads), 0, stream, p);
 }

@@ -120,6 +120,21 @@ def test_slices_of_every_cluster_size(dev, n, budget):
     run(dev, x, w, positions, None, x.lens.clone(), budget, sinks=2, recent=60)
 
 
+@pytest.mark.parametrize("seqs,hkv,fp8,budget", [(29, 4, False, 64), (57, 2, False, 1500), (57, 2, True, 2000),
+                                                 (28, 4, False, 1500)])
+def test_full_grids_move_by_themselves(dev, seqs, hkv, fp8, budget):
+    """Enough rows to fill the GPU (and just too few): each CTA makes all of
+    its moves, up to and past one round of its threads."""
+    lens = [2049 + (i * 977) % 2900 for i in range(seqs - 4)] + [0, 1, budget, budget + 1]
+    x = Batch(lens, hkv, hkv, 128 if fp8 else 64, 16, F16, seed=seqs + budget, fp8=fp8, stale=False)
+    positions = torch.zeros(seqs, hkv, x.tokens, dtype=torch.int32)
+    w = x.state().nan_to_num(0.25)
+    w *= torch.linspace(0.01, 1.0, x.tokens)             # the heavy ones at the end: many moves
+    run(dev, x, w, positions, None, x.lens.clone(), budget, sinks=4, recent=40)
+    positions, known, seen = earlier_cut(x, 20)
+    run(dev, x, w, positions, known, seen, budget, sinks=4, recent=40, in_place=True)
+
+
 def test_bad_tables_and_lengths_are_bounded(dev):
     """Moves through a block id outside the pool are left out and reported;
     a length past the table is clamped."""
