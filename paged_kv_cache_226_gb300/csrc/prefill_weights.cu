@@ -24,16 +24,15 @@
 // resident tiles (operand A) and streams others (operand B) past both, so
 // that a streamed tile is loaded once for two products; one persistent CTA
 // per SM walks its units, its rings running on from one unit to the next.
-// Pass 1 has six warps that load with TMA: two for each stage of the K ring
-// (half of the 16-token boxes each, through the block table: a box costs its
-// warp some 120 cycles), three of them also for a stage each of the Q ring
-// (one box of tokens x heads per 64 dims); pass 2, whose K tiles stay for a
-// unit, has one warp for each ring.  Two warps issue the MMAs, one for
-// each resident tile, into two 128-column buffers each: a single issuer
-// spends 1,060 cycles on its waits and commits per tile, twice what the
-// product takes.  Four groups of four warps take the finished tiles.  Rows of
-// Q past a sequence's chunk and K rows past its end may hold anything: they
-// only reach their own lane or column, which is masked.
+// Pass 1 has three warps that load with TMA, one for each stage of the K ring
+// (16-token boxes through the block table: a box costs its warp some 120
+// cycles) and of the Q ring (one box of tokens x heads per 64 dims); pass 2,
+// whose K tiles stay for a unit, has one warp for each ring.  Two warps issue
+// the MMAs, one for each resident tile, into two 128-column buffers each: a
+// single issuer spends 1,060 cycles on its waits and commits per tile, twice
+// what the product takes.  Four groups of four warps take the finished tiles.
+// Rows of Q past a sequence's chunk and K rows past its end may hold anything:
+// they only reach their own lane or column, which is masked.
 //
 // Measured (two chunks of 2048 on contexts of 2048 and 16384, 32 heads over 8,
 // D 128, bf16): 190 us for pass 1 and 199 for pass 2, 1.40 PFLOP/s over both;
@@ -147,10 +146,10 @@ __device__ __forceinline__ float joined_lse(const PrefillWeightsParams& p, const
     return r < tokens * p.group ? m + log2f(z) : INFINITY;
 }
 
-// Pass 1 loads a K tile per step, pass 2 two per unit: six loading warps (80
-// registers a thread) and two (96, which the column sums need: where they
-// spilled, pass 2 took 303 us against 222 then).
-__host__ __device__ constexpr int pw_loaders(bool stats) { return stats ? 6 : 2; }
+// Pass 1 loads a K tile per step, pass 2 two per unit: three loading warps and
+// two.  (Six, sharing the boxes of a K stage, are no faster, and leave pass 2
+// 80 registers a thread, where its column sums spill: 303 us against 222 then.)
+__host__ __device__ constexpr int pw_loaders(bool stats) { return stats ? 3 : 2; }
 
 template <typename T, int D, bool kStats>
 __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
@@ -178,7 +177,7 @@ __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
         // pass 1 has two loaders for each K stage; a resident tile has one issuer, a streamed
         // tile both
         for (int i = 0; i < kA; ++i) mbar_init(&a_full[i], 1), mbar_init(&a_empty[i], 1);
-        for (int i = 0; i < kB; ++i) mbar_init(&b_full[i], kStats ? 2 : 1), mbar_init(&b_empty[i], 2);
+        for (int i = 0; i < kB; ++i) mbar_init(&b_full[i], 1), mbar_init(&b_empty[i], 2);
         for (int i = 0; i < kPwBufs; ++i) mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4);
         fence_barrier_init();
     }
@@ -203,11 +202,11 @@ __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
         // phase: a parity says no more than that, and a loader that had not
         // waited for that phase would take the one before it for its own.
         // ------------------------------------------------------------------
-        // Pass 1: warp w has Q stage w (of three) and half of the boxes of K
-        // stage w % 3.  Pass 2: warp 0 has the Q stages, warp 1 the K stages.
+        // Pass 1: warp w has stage w of either ring.  Pass 2: warp 0 has the Q
+        // stages, warp 1 the K stages.
         const int who = warp < 4 ? warp - 2 : warp - kPwLoadersAfter + 2;
         auto mine_a = [&](int n) { return kStats ? n % kA == who : who == 1; };
-        auto mine_b = [&](int n) { return kStats ? n % kB == who % 3 : who == 0; };
+        auto mine_b = [&](int n) { return kStats ? n % kB == who : who == 0; };
         if (lane == 0) prefetch_tensor_map(&tmap_q), prefetch_tensor_map(&tmap_k);
         // waits for stage n % stages to be free
         auto open = [&](uint64_t* empty, int stages, int n) -> bool {
@@ -216,8 +215,7 @@ __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
         auto load_k = [&](uint8_t* dst, uint64_t* full, uint64_t* empty, int stages, int n,
                           const PwSeq& s, const PwUnit& U, int kt, int blk) -> bool {
             if (!open(empty, stages, n)) return false;
-            pw_load_keys<D, kStats ? 4 : 8>(&tmap_k, dst + (n % stages) * Lay::kTile, &full[n % stages], p, s,
-                                            U.g, kt, blk, kStats ? who / 3 : 0, 8, kStats ? 2 : 1);
+            pw_load_keys<D, 8>(&tmap_k, dst + (n % stages) * Lay::kTile, &full[n % stages], p, s, U.g, kt, blk, 0, 8, 1);
             return true;
         };
         auto load_q = [&](uint8_t* dst, uint64_t* full, uint64_t* empty, int stages, int n,
@@ -232,7 +230,7 @@ __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
         PwUnit U;
         int na = 0, nb = 0, at_b = -1, at_g = -1, at_qt = -1;
         bool ok = true;
-        static_assert(kA == 3 && kB == 3 && pw_loaders(true) == 6, "two loaders for each K stage");
+        static_assert(kA == 3 && kB == 3 && pw_loaders(true) == 3, "a loader for each stage");
         while (ok && walk.next(p, U)) {
             // block ids of the current four key tiles and of the next four
             int quad = -2, blk = 0, blk_next = 0;

@@ -14,7 +14,7 @@ constexpr int kPwCols = 128;                   // columns: rows of a streamed ti
 constexpr int kPwBufs = 4;                     // accumulators in tensor memory
 constexpr int kPwGroups = 4;                   // epilogue groups of four warps, one per buffer
 // Warps 0 and 1 issue MMAs, 2 and 3 load, 4 .. 19 are the epilogue's, and
-// where six warps load, 20 .. 23 do too.
+// where more warps load, 20 and up do too.
 constexpr int kPwLoadersAfter = 4 + 4 * kPwGroups;
 __host__ __device__ constexpr int pw_threads(int loaders) {
     return (kPwLoadersAfter + loaders - 2) * 32;
