@@ -35,9 +35,9 @@
 // they only reach their own lane or column, which is masked.
 //
 // Measured (two chunks of 2048 on contexts of 2048 and 16384, 32 heads over 8,
-// D 128, bf16): 190 us for pass 1 and 199 for pass 2, 1.40 PFLOP/s over both;
+// D 128, bf16): 189 us for pass 1 and 199 for pass 2, 1.41 PFLOP/s over both;
 // the tensor pipe is busy 62 % of the time, the exponentials' unit 64 %, issue
-// slots 64 / 60 %: bound by how the four groups of epilogue warps overlap,
+// slots 62 / 60 %: bound by how the four groups of epilogue warps overlap,
 // whose instructions per score are few but for the exponential.
 //
 // Every mbarrier wait gives up after 1 s and flags PA_DEVERR_WAIT_TIMEOUT;

@@ -22,7 +22,7 @@
 // every wait follows the wait for the phase before.
 //
 // Measured (32 queries of 4 heads on each of 16 x 8 rows of 2048 to 8192
-// tokens, D 128, fp16): 56.7 us; a pass streams K in 22 us (7.9 TB/s), and
+// tokens, D 128, fp16): 56.4 us; a pass streams K in 22 us (7.9 TB/s), and
 // takes 6 more until its first tile is there and where its CTAs end.
 #include <algorithm>
 
