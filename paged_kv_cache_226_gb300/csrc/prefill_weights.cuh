@@ -35,11 +35,15 @@ struct PwSeq {
     int n_qt, n_kt;                // query and key tiles
 };
 
+// kL2: lengths (and block ids below) read past L1, by a kernel that runs ahead
+// of the one before it (prefill_window.cu).
+template <bool kL2 = false>
 __device__ __forceinline__ void pw_sequence(const PrefillWeightsParams& p, int b, bool report,
                                             PwSeq& s) {
-    int L = p.context_lens[b];
-    const int64_t start = p.query_start[b];
-    int64_t C = (int64_t)p.query_start[b + 1] - start;
+    auto at = [](const int32_t* x) { return kL2 ? __ldcg(x) : *x; };
+    int L = at(p.context_lens + b);
+    const int64_t start = at(p.query_start + b);
+    int64_t C = (int64_t)at(p.query_start + b + 1) - start;
     bool bad = false;
     if (L < 0 || L > p.max_context) bad = true, L = L < 0 ? 0 : p.max_context;
     if (C < 0 || C > L) bad = true, C = C < 0 ? 0 : L;
@@ -192,10 +196,12 @@ __device__ __forceinline__ float column_sums(uint32_t tile_addr, const float* ne
 
 // Block ids of key tiles 4 q .. 4 q + 3: lane i has box i % 8 of tile i / 8.
 // Requested here, looked at by pw_checked, so that two requests can be under way.
+template <bool kL2 = false>
 __device__ __forceinline__ int pw_blocks(const PrefillWeightsParams& p, const PwSeq& s, int b, int q) {
     const int tok = q * 4 * kPwCols + 16 * (threadIdx.x & 31);
     if (tok < 0 || tok >= s.L) return 0;
-    return __ldg(p.block_tables + (size_t)b * p.max_blocks_per_seq + tok / p.block_size);
+    const int32_t* at = p.block_tables + (size_t)b * p.max_blocks_per_seq + tok / p.block_size;
+    return kL2 ? __ldcg(at) : __ldg(at);
 }
 
 __device__ __forceinline__ int pw_checked(const PrefillWeightsParams& p, int blk) {

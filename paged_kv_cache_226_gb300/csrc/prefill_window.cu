@@ -22,8 +22,9 @@
 // every wait follows the wait for the phase before.
 //
 // Measured (32 queries of 4 heads on each of 16 x 8 rows of 2048 to 8192
-// tokens, D 128, fp16): 56.4 us; a pass streams K in 22 us (7.9 TB/s), and
-// takes 6 more until its first tile is there and where its CTAs end.
+// tokens, D 128, fp16): 54.9 us; a pass streams K in 22 us (7.9 TB/s), and
+// takes some 5 more until its first tile is there and where its CTAs end,
+// which pass 2 overlaps with the end of pass 1 (58.6 us where it does not).
 #include <algorithm>
 
 #include "prefill_weights.cuh"
@@ -55,7 +56,7 @@ struct PwRuns {
         const int lane = threadIdx.x & 31, i = base_b + lane;
         ends = 0;
         if (i < p.num_seqs) {
-            pw_sequence(p, kBackward ? p.num_seqs - 1 - i : i, report, mine);
+            pw_sequence<kBackward>(p, kBackward ? p.num_seqs - 1 - i : i, report, mine);
             ends = (unsigned)mine.n_kt * p.num_kv_heads;
         }
 #pragma unroll
@@ -73,7 +74,7 @@ struct PwRuns {
             const int i = b0 + (int)(threadIdx.x & 31);
             PwSeq q;
             q.n_kt = 0;
-            if (i < p.num_seqs) pw_sequence(p, kBackward ? p.num_seqs - 1 - i : i, report, q);
+            if (i < p.num_seqs) pw_sequence<kBackward>(p, kBackward ? p.num_seqs - 1 - i : i, report, q);
             n += (unsigned)q.n_kt * p.num_kv_heads;
         }
         read(p, report);
@@ -143,7 +144,12 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
             reinterpret_cast<uint4*>(q_ring)[i] = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
     }
-    grid_dependency_wait();
+    // Pass 2 runs ahead of the end of pass 1 on whatever pass 1 does not write.
+    // What came before pass 1 has ended, since pass 1 lets its dependents go
+    // only after it has waited for that; lengths and tables are read from L2,
+    // where it is.
+    const bool ahead = !kStats && p.max_counted > 0;
+    if (!ahead) grid_dependency_wait();
     allow_dependent_launch();
     PwRuns<!kStats> runs;
     const unsigned N = runs.count(p, (kStats || p.max_counted == 0) && blockIdx.x == 0 && warp == 0);
@@ -190,11 +196,11 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
             for (int k = R.k0; ok && k < R.k1; ++k, ++n) {
                 const int kt = tile_of(s, k);
                 if ((kt >> 2) != quad) {
-                    if ((kt >> 2) != quad + kAhead) blk_next = pw_blocks(p, s, R.b, kt >> 2);
+                    if ((kt >> 2) != quad + kAhead) blk_next = pw_blocks<!kStats>(p, s, R.b, kt >> 2);
                     quad = kt >> 2;
-                    const int ahead = pw_blocks(p, s, R.b, quad + kAhead);
+                    const int after = pw_blocks<!kStats>(p, s, R.b, quad + kAhead);
                     blk = pw_checked(p, blk_next);
-                    blk_next = ahead;
+                    blk_next = after;
                 }
                 const int st = n % kWkStages;
                 if (who != st && who != 4 + (n & 1)) continue;
@@ -259,6 +265,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[group]);
         };
+        if (ahead) grid_dependency_wait();      // the records, and weights_out
         const int max_records = p.key_chunks;
         int n = 0, mine = 0, joins = 0, rows = 0;
         while (runs.next(p, R)) {
