@@ -476,8 +476,11 @@ int pa_rope_and_cache_fp8(const void* q, int64_t q_stride, const void* k, int64_
  *   weights_out[b][g][i] = weights[b][g][i] + sum over the group of p[h][i]
  * for i < L_b; the newest token, i = L_b - 1, has nothing added up yet and
  * gets the sum alone.  weights may be null (nothing added up yet).
- * max_context_len >= every L_b (tokens past it are not attended),
- * partition_size a multiple of block_size.  workspace: device memory of at
+ * Softmax statistics and weights are in fp32; p meets V in two fp16 or three
+ * bf16 parts, which hold it to 2^-22 (and to 2^-32 of the row's largest).
+ * max_context_len >= every L_b (tokens past its partitions are not attended,
+ * and their entries not written), partition_size a multiple of block_size.
+ * workspace: device memory of at
  * least pa_decode_weights_workspace_size bytes, 16-byte aligned, no initial
  * contents; calls that overlap on the GPU must not share it.  One or two launches.
  */

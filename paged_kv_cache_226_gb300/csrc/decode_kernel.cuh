@@ -22,8 +22,8 @@
 //   and denominator share the same reference max;
 //   P is rounded to the cache's 16-bit type -- for fp16 once (the row sum l
 //   accumulates the rounded values), for bf16 as a hi + lo pair of bf16
-//   values whose sum carries P to ~2^-17 -- transposed in registers with
-//   movmatrix, and O^T[d][h] += V^T[d][:] . P^T[:][h] with fp32 accumulation.
+//   values whose sum carries P to ~2^-17, and in the weights modes with one
+//   such part more -- transposed in registers with movmatrix, and O^T[d][h] += V^T[d][:] . P^T[:][h] with fp32 accumulation.
 // The consumer warps' (m, l, O) are merged through shared memory at the end;
 // a partitioned CTA writes a record, and in the fused step the last one of
 // a (sequence, KV head) merges the records.

@@ -32,13 +32,23 @@ constexpr float kRescaleThresholdLog2 = 8.0f;        // rescale when the max gro
 // emit(tok0, x) with x[0], x[1] token tok0 + r8 and x[2], x[3] token
 // tok0 + r8 + 8, heads 2c4 and 2c4 + 1, in log2 units.  This one keeps none.
 // Where scores are kept for attention weights, the row sums are of P before
-// its rounding, and a 16-bit cache's P is a hi + lo pair for fp16 too (no
-// slower: 64 ragged sequences 56.3 us against 55.9); over an E4M3 cache P
-// stays rounded once (the pair costs 92 us against 78 on 32 x 4096 tokens).
+// its rounding, and P reaches the tensor cores in as many parts as carry its
+// 24 bits: hi + lo in fp16 (also over an E4M3 cache, 32 x 4096 tokens 71.2 us,
+// with P rounded once 69.8), three in bf16 (8 long contexts 228.6 us, with two
+// 226.5).
+// fp16 parts end at 2^-25, so the reference is there kept 2^7 below the
+// maximum (P up to 2^15): what is lost is a token's weight below 2^-32 of the
+// largest.
 struct NoScores {
     static constexpr bool kKeep = false;
     __device__ __forceinline__ void operator()(int, const float (&)[4]) const {}
 };
+
+// How far below the maximum the reference of P's exponentials is kept (log2).
+template <typename T, bool kKeep>
+__host__ __device__ constexpr float p_reference_below() {
+    return kKeep && std::is_same<T, __half>::value ? 7.f : 0.f;
+}
 
 template <int D>
 struct TileState {
@@ -220,28 +230,17 @@ __device__ __forceinline__ void fp8_load_v(uint4 (&v)[4], const uint8_t* vtile, 
     }
 }
 
-// O^T slab n += V^T . P^T from the staged codes (two tokens' bytes paired by prmt).
-__device__ __forceinline__ void fp8_pv_slab(float (&acc)[4], const uint4 (&v)[4], int n,
-                                            uint32_t pb0, uint32_t pb1) {
-    const int j = n >> 1;
-    const uint32_t sel = (n & 1) ? 0x7362u : 0x5140u;   // bytes (2h, 2h+1) of two tokens
-    const uint32_t x01 = prmt(word_of(v[0], j), word_of(v[1], j), sel);
-    const uint32_t x23 = prmt(word_of(v[2], j), word_of(v[3], j), sel);
-    uint32_t a0, a1, a2, a3;
-    e4m3x4_to_f16x2x2(x01, a0, a1);
-    e4m3x4_to_f16x2x2(x23, a2, a3);
-    Mma<__half>::run(acc, a0, a1, a2, a3, pb0, pb1);
-}
-
 // Raises the reference maxima when this step's maxima xa, xb (log2 units, per
 // head pair, already reduced over the warp) exceed them by more than 2^8.
+template <bool kKeep>
 __device__ __forceinline__ void fp8_raise(TileState<128>& s, float xa, float xb) {
+    constexpr float kBelow = p_reference_below<__half, kKeep>();
     s.tA = fmaxf(s.tA, xa);
     s.tB = fmaxf(s.tB, xb);
-    const bool raiseA = xa > s.mA + kRescaleThresholdLog2;
-    const bool raiseB = xb > s.mB + kRescaleThresholdLog2;
+    const bool raiseA = xa > s.mA + (kBelow + kRescaleThresholdLog2);
+    const bool raiseB = xb > s.mB + (kBelow + kRescaleThresholdLog2);
     if (__any_sync(0xffffffffu, raiseA || raiseB)) {
-        const float nA = raiseA ? xa : s.mA, nB = raiseB ? xb : s.mB;
+        const float nA = raiseA ? xa - kBelow : s.mA, nB = raiseB ? xb - kBelow : s.mB;
         const float fA = ex2(s.mA - nA), fB = ex2(s.mB - nB);
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
@@ -269,26 +268,46 @@ __device__ __forceinline__ void fp8_mask(float (&x)[4], const float (&sc)[4], in
     }
 }
 
-// P of a tile in fp16 (added into the row sums: the rounded values, or with
-// kExactSums the values before rounding), transposed into P^T fragments.
-template <bool kExactSums>
-__device__ __forceinline__ void fp8_probs(TileState<128>& s, const float (&x)[4], uint32_t& pb0,
-                                          uint32_t& pb1) {
-    using M = Mma<__half>;
-    const float e0 = ex2(x[0] - s.mA), e1 = ex2(x[1] - s.mB);
-    const float e2 = ex2(x[2] - s.mA), e3 = ex2(x[3] - s.mB);
-    const uint32_t p01 = M::pack(e0, e1);
-    const uint32_t p23 = M::pack(e2, e3);
-    if (kExactSums) {
-        s.lA += e0 + e2;
-        s.lB += e1 + e3;
-    } else {
+// P of a tile in fp16, transposed into P^T fragments: rounded once, and the
+// rounded values added into the row sums, or with kKeep a hi + lo pair, and
+// the values before rounding added.
+template <bool kKeep>
+struct Fp8Probs {
+    uint32_t hi0, hi1, lo0, lo1;
+    __device__ __forceinline__ Fp8Probs(TileState<128>& s, const float (&x)[4]) {
+        using M = Mma<__half>;
+        const float e0 = ex2(x[0] - s.mA), e1 = ex2(x[1] - s.mB);
+        const float e2 = ex2(x[2] - s.mA), e3 = ex2(x[3] - s.mB);
+        const uint32_t p01 = M::pack(e0, e1);
+        const uint32_t p23 = M::pack(e2, e3);
         const float2 u = M::unpack(p01), w = M::unpack(p23);
-        s.lA += u.x + w.x;
-        s.lB += u.y + w.y;
+        if constexpr (kKeep) {
+            lo0 = movmatrix_trans(M::pack(e0 - u.x, e1 - u.y));
+            lo1 = movmatrix_trans(M::pack(e2 - w.x, e3 - w.y));
+            s.lA += e0 + e2;
+            s.lB += e1 + e3;
+        } else {
+            s.lA += u.x + w.x;
+            s.lB += u.y + w.y;
+        }
+        hi0 = movmatrix_trans(p01);
+        hi1 = movmatrix_trans(p23);
     }
-    pb0 = movmatrix_trans(p01);
-    pb1 = movmatrix_trans(p23);
+};
+
+// O^T slab n += V^T . P^T from the staged codes (two tokens' bytes paired by prmt).
+template <bool kKeep>
+__device__ __forceinline__ void fp8_pv_slab(float (&acc)[4], const uint4 (&v)[4], int n,
+                                            const Fp8Probs<kKeep>& p) {
+    const int j = n >> 1;
+    const uint32_t sel = (n & 1) ? 0x7362u : 0x5140u;   // bytes (2h, 2h+1) of two tokens
+    const uint32_t x01 = prmt(word_of(v[0], j), word_of(v[1], j), sel);
+    const uint32_t x23 = prmt(word_of(v[2], j), word_of(v[3], j), sel);
+    uint32_t a0, a1, a2, a3;
+    e4m3x4_to_f16x2x2(x01, a0, a1);
+    e4m3x4_to_f16x2x2(x23, a2, a3);
+    Mma<__half>::run(acc, a0, a1, a2, a3, p.hi0, p.hi1);
+    if constexpr (kKeep) Mma<__half>::run(acc, a0, a1, a2, a3, p.lo0, p.lo1);
 }
 
 __device__ __forceinline__ void warp_max_pairs(float& xa, float& xb) {
@@ -326,18 +345,19 @@ __device__ __forceinline__ void attend_tile_fp8(TileState<128>& s, QFrag&& qfrag
     emit(tok0, x);
     float xa = fmaxf(x[0], x[2]), xb = fmaxf(x[1], x[3]);
     warp_max_pairs(xa, xb);
-    fp8_raise(s, xa, xb);
-    uint32_t pb0, pb1;
-    fp8_probs<Emit::kKeep>(s, x, pb0, pb1);
+    fp8_raise<Emit::kKeep>(s, xa, xb);
+    const Fp8Probs<Emit::kKeep> p(s, x);
 #pragma unroll
-    for (int n = 0; n < 8; ++n) fp8_pv_slab(s.acc[n], v, n, pb0, pb1);
+    for (int n = 0; n < 8; ++n) fp8_pv_slab(s.acc[n], v, n, p);
 }
 
 // Attends two FP8 tiles at once: tile 0 (tokens tok0 .. tok0+15) and tile 1
 // (the next 16), both masked from t_end on.  Their score chains interleave,
 // one max reduction and one rescale test cover both, and each accumulator
 // slab takes both P V products, so the per-tile chain of dependent steps is
-// about halved.  release() runs once both tiles' codes are in registers.
+// about halved.  release() runs once both tiles' codes are in registers.  Where
+// scores are kept, V is read only when its P is there: with both tiles' V in
+// registers beside P's two parts they spill (78.5 us against 71.2).
 template <typename QFrag, typename Release, typename Emit = NoScores>
 __device__ __forceinline__ void attend_pair_fp8(TileState<128>& s, QFrag&& qfrag,
                                                 const uint8_t* ktile0, const uint8_t* vtile0,
@@ -355,27 +375,36 @@ __device__ __forceinline__ void attend_pair_fp8(TileState<128>& s, QFrag&& qfrag
         fp8_score_step(sc0, klo0, khi0, kk, b0, b1);
         fp8_score_step(sc1, klo1, khi1, kk, b0, b1);
     }
-    uint4 v0[4], v1[4];
-    fp8_load_v(v0, vtile0, tok0, t_end, lane);
-    fp8_load_v(v1, vtile1, tok0 + kTileTokens, t_end, lane);
-    release();
-
     float x[4], y[4];
     fp8_mask(x, sc0, tok0, t_end, scale_log2, lane);
     fp8_mask(y, sc1, tok0 + kTileTokens, t_end, scale_log2, lane);
+    uint4 v0[4], v1[4];
+    if constexpr (!Emit::kKeep) {
+        fp8_load_v(v0, vtile0, tok0, t_end, lane);
+        fp8_load_v(v1, vtile1, tok0 + kTileTokens, t_end, lane);
+        release();
+    }
     emit(tok0, x);
     emit(tok0 + kTileTokens, y);
     float xa = fmaxf(fmaxf(x[0], x[2]), fmaxf(y[0], y[2]));
     float xb = fmaxf(fmaxf(x[1], x[3]), fmaxf(y[1], y[3]));
     warp_max_pairs(xa, xb);
-    fp8_raise(s, xa, xb);
-    uint32_t pb0, pb1, qb0, qb1;
-    fp8_probs<Emit::kKeep>(s, x, pb0, pb1);
-    fp8_probs<Emit::kKeep>(s, y, qb0, qb1);
+    fp8_raise<Emit::kKeep>(s, xa, xb);
+    const Fp8Probs<Emit::kKeep> p0(s, x), p1(s, y);
+    if constexpr (Emit::kKeep) {
+        fp8_load_v(v0, vtile0, tok0, t_end, lane);
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-        fp8_pv_slab(s.acc[n], v0, n, pb0, pb1);
-        fp8_pv_slab(s.acc[n], v1, n, qb0, qb1);
+        for (int n = 0; n < 8; ++n) fp8_pv_slab(s.acc[n], v0, n, p0);
+        fp8_load_v(v1, vtile1, tok0 + kTileTokens, t_end, lane);
+        release();
+#pragma unroll
+        for (int n = 0; n < 8; ++n) fp8_pv_slab(s.acc[n], v1, n, p1);
+    } else {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            fp8_pv_slab(s.acc[n], v0, n, p0);
+            fp8_pv_slab(s.acc[n], v1, n, p1);
+        }
     }
 }
 
@@ -396,7 +425,9 @@ __device__ __forceinline__ void attend_tile(TileState<D>& s, QFrag&& qfrag,
                                             float scale_log2, int lane, Emit emit = Emit()) {
     using M = Mma<T>;
     constexpr int kKSteps = D / 16;
-    constexpr bool kSplitP = std::is_same<T, __nv_bfloat16>::value || Emit::kKeep;
+    // parts of P: one fp16 value, a bf16 pair, and one more where scores are kept
+    constexpr int kParts = (std::is_same<T, __nv_bfloat16>::value ? 2 : 1) + Emit::kKeep;
+    constexpr float kBelow = p_reference_below<T, Emit::kKeep>();
     const int r8 = lane >> 2;
     // ldmatrix row addresses: matrix j = lane/8 supplies row lane%8.
     // K (A operand, no transpose): j -> (tokens 8*(j&1).., dims hi = j>>1)
@@ -437,10 +468,10 @@ __device__ __forceinline__ void attend_tile(TileState<D>& s, QFrag&& qfrag,
     }
     s.tA = fmaxf(s.tA, xa);
     s.tB = fmaxf(s.tB, xb);
-    const bool raiseA = xa > s.mA + kRescaleThresholdLog2;
-    const bool raiseB = xb > s.mB + kRescaleThresholdLog2;
+    const bool raiseA = xa > s.mA + (kBelow + kRescaleThresholdLog2);
+    const bool raiseB = xb > s.mB + (kBelow + kRescaleThresholdLog2);
     if (__any_sync(0xffffffffu, raiseA || raiseB)) {
-        const float nA = raiseA ? xa : s.mA, nB = raiseB ? xb : s.mB;
+        const float nA = raiseA ? xa - kBelow : s.mA, nB = raiseB ? xb - kBelow : s.mB;
         const float fA = ex2(s.mA - nA), fB = ex2(s.mB - nB);
 #pragma unroll
         for (int n = 0; n < kKSteps; ++n) {
@@ -457,23 +488,23 @@ __device__ __forceinline__ void attend_tile(TileState<D>& s, QFrag&& qfrag,
     // P in the 16-bit type; P^T fragments by an in-register transpose
     const float e0 = ex2(x0 - s.mA), e1 = ex2(x1 - s.mB);   // token r8
     const float e2 = ex2(x2 - s.mA), e3 = ex2(x3 - s.mB);   // token r8+8
-    const uint32_t p01 = M::pack(e0, e1);
-    const uint32_t p23 = M::pack(e2, e3);
-    const uint32_t pb0 = movmatrix_trans(p01);   // (head r8, tokens 2c4..+1)
-    const uint32_t pb1 = movmatrix_trans(p23);   // (head r8, tokens 8+2c4..+1)
-    uint32_t pl0 = 0u, pl1 = 0u;
-    if (kSplitP) {
+    uint32_t pb[kParts][2];        // [][0]: (head r8, tokens 2c4..+1), [][1]: (head r8, tokens 8+2c4..+1)
+    float r0 = e0, r1 = e1, r2 = e2, r3 = e3;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+        const uint32_t p01 = M::pack(r0, r1), p23 = M::pack(r2, r3);
         const float2 u = M::unpack(p01), w = M::unpack(p23);
-        pl0 = movmatrix_trans(M::pack(e0 - u.x, e1 - u.y));
-        pl1 = movmatrix_trans(M::pack(e2 - w.x, e3 - w.y));
+        pb[i][0] = movmatrix_trans(p01);
+        pb[i][1] = movmatrix_trans(p23);
+        if (kParts == 1) {
+            s.lA += u.x + w.x;
+            s.lB += u.y + w.y;
+        }
+        r0 -= u.x, r1 -= u.y, r2 -= w.x, r3 -= w.y;
     }
-    if (kSplitP) {
+    if (kParts > 1) {
         s.lA += e0 + e2;
         s.lB += e1 + e3;
-    } else {
-        const float2 u = M::unpack(p01), w = M::unpack(p23);
-        s.lA += u.x + w.x;
-        s.lB += u.y + w.y;
     }
 
     // ragged tail: zero V rows past the end so that 0 * V stays 0
@@ -499,8 +530,8 @@ __device__ __forceinline__ void attend_tile(TileState<D>& s, QFrag&& qfrag,
                               (((chunk & 7) ^ (v_tok & 7)) << 4);
         uint32_t a0, a1, a2, a3;
         ldsm_x4_trans(addr, a0, a1, a2, a3);
-        M::run(s.acc[n], a0, a1, a2, a3, pb0, pb1);
-        if (kSplitP) M::run(s.acc[n], a0, a1, a2, a3, pl0, pl1);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) M::run(s.acc[n], a0, a1, a2, a3, pb[i][0], pb[i][1]);
     }
 }
 

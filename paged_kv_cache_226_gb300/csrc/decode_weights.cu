@@ -11,8 +11,8 @@
 // where the newest token (i = L - 1) has nothing added up yet and is set.
 // The sums l_s are of the unrounded exponentials, so that the weights hold
 // fp32 accuracy.  Bound by the scores, read back from L2, and by the start of
-// a launch of few microseconds: 7 to 11 us of 57 (64 ragged sequences), 68 (E4M3)
-// and 226 (8 long ones).
+// a launch of few microseconds: 7 to 11 us of 57 (64 ragged sequences), 71 (E4M3)
+// and 229 (8 long ones).
 #include <algorithm>
 
 #include "bounded_internal.h"

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from bounded_util import Batch, decode_reference, prefill_reference, same_bits, within
+from bounded_util import Batch, decode_reference, half_step, prefill_reference, same_bits, within
 from paged_kv_cache_226_gb300 import build, lib
 
 pytestmark = pytest.mark.gpu
@@ -392,3 +392,65 @@ def test_captured_calls_follow_the_lengths(dev, hq, hkv, d, high):
         assert same_bits(wd, a) and same_bits(wp, b) and same_bits(out, o)
     del g
     assert lib.read_device_errors(dev) == 0
+
+
+def _crafted(kind, k, v, group=4):
+    """One sequence of tokens whose K has k[i] and whose V has v[i] in its first dim (zero elsewhere),
+    read by queries that are one in that dim: out[0, :, 0] is sum p v."""
+    dtype, fp8 = {"fp16": (F16, False), "bf16": (BF16, False), "e4m3": (F16, True)}[kind]
+    x = Batch([len(k)], group, 1, 128, 16, dtype, seed=1, fp8=fp8, stale=False)
+    x.k_scale, x.v_scale = (1.0, 1.0) if fp8 else (None, None)
+    at = torch.arange(len(k))
+    for cache, values in ((x.k, k), (x.v, v)):
+        cache.zero_()
+        row = torch.tensor(values, dtype=torch.float32)
+        row = row.to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else row.to(dtype)
+        cache[x.tables[0, at // 16].long(), at % 16, 0, 0] = row
+    x.q.zero_()
+    x.q[:, :, 0] = 1
+    return x
+
+
+def _first_dim(dev, x, partition):
+    out, _ = lib.decode_weights(x.q.to(dev), x.k.to(dev), x.v.to(dev), x.tables.to(dev), x.lens.to(dev),
+                                x.scale, int(x.lens.max()), partition_size=partition, **x.scales())
+    torch.cuda.synchronize(dev)
+    assert lib.read_device_errors(dev) == 0
+    return out[0, :, 0].double().cpu()
+
+
+@pytest.mark.parametrize("partition", [16, 64, 1024])
+@pytest.mark.parametrize("kind,high,low", [("e4m3", 0.0, 0.97 * 2.0 ** -12), ("fp16", 0.0, 0.97 * 2.0 ** -12),
+                                           ("fp16", 2.0 ** -12, 0.9 * 2.0 ** -20), ("e4m3", 0.0, 0.9 * 2.0 ** -18),
+                                           ("bf16", 2.0 ** -10, 0.97 * 2.0 ** -18)])
+def test_decode_probabilities_hold_32_bits(dev, kind, high, low, partition):
+    """Probabilities of 1/2 + high + low beside ones of 1, the values chosen so
+    that all but `low` cancels: a P in fewer bits than the plain form's loses it.
+
+    P carries at most 2^-21 of itself (the scale in log2 units 2^-23, the
+    difference to a reference 2^7 below 2^-22, the exponential 2^-22.5), the
+    parts of the split 2^-22 and the sums 2^-23 of their terms, which are 1 at
+    most: 2^-20 in all."""
+    p = 0.5 + high + low
+    x = _crafted(kind, [0.0, -1.0, -1.0, 0.0] * 20, [-1.0, 1.0, 1.0, -2 * high] * 20)
+    x.scale = float(np.float32(-np.log(p)))
+    p = float(np.exp(-x.scale))
+    want = (2 * p - 1 - 2 * high) / (2 + 2 * p)
+    got = _first_dim(dev, x, partition)
+    assert bool(((got - want).abs() <= half_step(x.dtype) * abs(want) + 2.0 ** -20 + (kind != "bf16") * 2.0 ** -25).all()), \
+        (got.tolist(), want)
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16", "e4m3"])
+@pytest.mark.parametrize("n,partition", [(1000, 1008), (4000, 4096)])
+def test_decode_small_probabilities_add_up(dev, kind, n, partition):
+    """One heavy token of value 0 and n light ones of weight 2^-26 and value 1:
+    the light ones' sum is the output.  Each may lose 2^-32 of the largest
+    weight, and 2^-20 of itself; an fp16 output has steps of 2^-24."""
+    x = _crafted(kind, [0.0] + [-1.0] * n, [0.0] + [1.0] * n)
+    x.scale = float(np.float32(26 * np.log(2)))
+    p = float(np.exp(-x.scale))
+    want = n * p / (1 + n * p)
+    got = _first_dim(dev, x, partition)
+    bound = (half_step(x.dtype) + 2.0 ** -20) * want + n * 2.0 ** -32 + (kind != "bf16") * 2.0 ** -25
+    assert bool(((got - want).abs() <= bound).all()), (got.tolist(), want, bound)
