@@ -1009,12 +1009,11 @@ class StepPlan:
     pa_decode_step launch), ``"split"`` (reshape_and_cache, decode_split,
     reduce), ``"single"`` (reshape_and_cache, decode) and ``"weights"``
     (reshape_and_cache, decode_weights: each step adds the attention weights
-    into ``weights``, or reads them there and writes ``weights_out``;
-    ``capture_graph`` makes one such step before it captures).  The work goes
-    to the caller's current stream at call time, which also makes a step
-    capturable into a CUDA graph (``capture_graph``).  The tensors must stay
-    alive and keep their shapes; their contents (new tokens, tables, lengths)
-    may change between steps as long as ``context_lens`` stays within
+    into ``weights``, or reads them there and writes ``weights_out``).  The
+    work goes to the caller's current stream at call time, which also makes a
+    step capturable into a CUDA graph (``capture_graph``).  The tensors must
+    stay alive and keep their shapes; their contents (new tokens, tables,
+    lengths) may change between steps as long as ``context_lens`` stays within
     ``max_context_len``.
 
     In the fused mode q, k_new, v_new, slot_mapping, block_tables,
@@ -1098,6 +1097,7 @@ class StepPlan:
                                  ctypes.c_int32(self.partition_size), _ptr(weights),
                                  _ptr(weights_out), ctypes.c_int64(weights_out.shape[2]),
                                  _ptr(workspace), ctypes.c_size_t(nbytes), _ptr(self.out), sref)
+            self._weights_out_at = len(self._decode_args) - 6
         elif mode == "single":
             self._decode_args = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                  _ptr(context_lens), ctypes.c_float(scale), _ptr(self.out), sref)
@@ -1156,8 +1156,7 @@ class StepPlan:
 
     def decode(self):
         if self.mode == "weights":
-            fn = self._lib.pa_decode_weights_fp8 if self.fp8 else self._lib.pa_decode_weights
-            _check("pa_decode_weights", fn(*self._decode_args, self._stream()))
+            self._decode_weights(self._decode_args)
         elif self.mode == "balanced":
             fn = self._lib.pa_decode_step_balanced_fp8 if self.fp8 else \
                 self._lib.pa_decode_step_balanced
@@ -1173,6 +1172,21 @@ class StepPlan:
             _check("pa_decode_split",
                    self._lib.pa_decode_split(*self._decode_args, self._stream()))
 
+    def _decode_weights(self, args):
+        fn = self._lib.pa_decode_weights_fp8 if self.fp8 else self._lib.pa_decode_weights
+        _check("pa_decode_weights", fn(*args, self._stream()))
+
+    def _warm(self):
+        """The step without a lasting effect: its cache write and its output are
+        those of the next step too, but weights that are added up go elsewhere."""
+        if self.mode != "weights":
+            self()
+            return
+        i = self._weights_out_at
+        scratch = torch.empty_like(self.weights_out)
+        self.reshape_and_cache()
+        self._decode_weights((*self._decode_args[:i], _ptr(scratch), *self._decode_args[i + 1:]))
+
     def reduce(self):
         if self.mode == "split":
             _check("pa_reduce", self._lib.pa_reduce(*self._reduce_args, self._stream()))
@@ -1184,18 +1198,19 @@ class StepPlan:
         return self.out
 
     def capture_graph(self, before=None, after=None) -> "torch.cuda.CUDAGraph":
-        """Capture one step into a CUDA graph (replayed by ``replay``).
+        """Capture one step into a CUDA graph (replayed by ``replay``).  The
+        step itself is not made: ``weights`` are as they were.
 
         ``before`` / ``after`` are called inside the capture around the step,
         e.g. ``InputStaging.upload`` and the copy of ``out`` to pinned host
         memory, so that a replay uploads, computes and reads back in one
-        graph launch."""
+        graph launch; they are called once before the capture too."""
         s = torch.cuda.Stream(self.device)
         s.wait_stream(torch.cuda.current_stream(self.device))
         with torch.cuda.stream(s):                   # warm the lazy set-up outside capture,
             if before is not None:                   # with the same inputs the graph sees
                 before()
-            self()
+            self._warm()
             if after is not None:
                 after()
         torch.cuda.current_stream(self.device).wait_stream(s)

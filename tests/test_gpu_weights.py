@@ -454,3 +454,37 @@ def test_decode_small_probabilities_add_up(dev, kind, n, partition):
     got = _first_dim(dev, x, partition)
     bound = (half_step(x.dtype) + 2.0 ** -20) * want + n * 2.0 ** -32 + (kind != "bf16") * 2.0 ** -25
     assert bool(((got - want).abs() <= bound).all()), (got.tolist(), want, bound)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("apart", [False, True])
+def test_step_plan_capture_makes_no_step(dev, fp8, apart):
+    """A capture leaves the weights as they were, asked for or made by the
+    first replay; each replay is exactly one step."""
+    x = Batch([300, 17, 64], 8, 2, 128, 16, BF16, seed=52, fp8=fp8, stale=False)
+    kn, vn = (torch.randn(3, 2, 128, generator=x.gen).to(BF16).to(dev) for _ in range(2))
+    at = (x.lens - 1).long()
+    slots = (x.tables[torch.arange(3), at // 16].long() * 16 + at % 16).to(dev)
+    start = x.state().nan_to_num(0.0).to(dev)
+
+    def plan():
+        w = start.clone()
+        out = torch.full_like(w, -7.0) if apart else None
+        return w, lib.StepPlan(x.q.to(dev), kn, vn, slots, x.k.to(dev), x.v.to(dev), x.tables.to(dev),
+                               x.lens.to(dev), x.scale, 300, mode="weights", weights=w, weights_out=out,
+                               **x.scales())
+
+    w, eager = plan()
+    once = eager().clone(), eager.weights_out.clone()
+    twice = eager().clone(), eager.weights_out.clone()
+    for captured in (False, True):
+        w, p = plan()
+        if captured:
+            p.capture_graph()
+            p.capture_graph()
+            assert same_bits(w, start) and (not apart or bool((p.weights_out == -7.0).all()))
+        assert same_bits(p.replay(), once[0]) and same_bits(p.weights_out, once[1])
+        assert same_bits(p.replay(), twice[0]) and same_bits(p.weights_out, twice[1])
+        assert not apart or same_bits(w, start)
+    torch.cuda.synchronize(dev)
+    assert lib.read_device_errors(dev) == 0
