@@ -1009,8 +1009,10 @@ class StepPlan:
     pa_decode_step launch), ``"split"`` (reshape_and_cache, decode_split,
     reduce), ``"single"`` (reshape_and_cache, decode) and ``"weights"``
     (reshape_and_cache, decode_weights: each step adds the attention weights
-    into ``weights``, or reads them there and writes ``weights_out``).  The
-    work goes to the caller's current stream at call time, which also makes a
+    into ``weights``, or reads them there and writes ``weights_out``; with
+    ``k_new``, ``v_new`` and ``slot_mapping`` None the step is decode_weights
+    alone, for keys that ``rope_and_cache`` has turned and cached: the plan's
+    own cache write would put the unturned ones over them).  The work goes to the caller's current stream at call time, which also makes a
     step capturable into a CUDA graph (``capture_graph``).  The tensors must
     stay alive and keep their shapes; their contents (new tokens, tables,
     lengths) may change between steps as long as ``context_lens`` stays within
@@ -1053,11 +1055,16 @@ class StepPlan:
             shp, dev = _fp8_common(q, k_cache, v_cache, block_tables, context_lens, host_ok)
         else:
             shp, dev = _decode_common(q, k_cache, v_cache, block_tables, context_lens, host_ok)
-        for t, n in ((k_new, "k_new"), (v_new, "v_new")):
-            _need(t, n, q.dtype, dev, host_ok)
-        _need(slot_mapping, "slot_mapping", torch.int64, dev, host_ok)
-        T = slot_mapping.shape[0]
-        if k_new.shape != (T, k_cache.shape[2], k_cache.shape[3]) or v_new.shape != k_new.shape:
+        cached = k_new is None and v_new is None and slot_mapping is None
+        if cached and mode != "weights":
+            raise ValueError("k_new, v_new and slot_mapping may be None in mode \"weights\" only")
+        if not cached:
+            for t, n in ((k_new, "k_new"), (v_new, "v_new")):
+                _need(t, n, q.dtype, dev, host_ok)
+            _need(slot_mapping, "slot_mapping", torch.int64, dev, host_ok)
+        T = q.shape[0] if cached else slot_mapping.shape[0]
+        if not cached and (k_new.shape != (T, k_cache.shape[2], k_cache.shape[3]) or
+                           v_new.shape != k_new.shape):
             raise ValueError("k_new and v_new must be [num_tokens][num_kv_heads][head_dim]")
         self.device = dev
         self.out = torch.empty(q.shape, dtype=q.dtype, device=dev) if out is None else out
@@ -1087,6 +1094,8 @@ class StepPlan:
             scales = (ctypes.c_float(k_scale), ctypes.c_float(v_scale)) if self.fp8 else ()
             if self.fp8:
                 self._reshape_args = (*self._reshape_args[:-1], *scales, sref)
+            if cached:
+                self._reshape_args = None
             workspace, nbytes = _workspace(workspace, self._lib.pa_decode_weights_workspace_size(
                 sref, int(max_context_len), self.partition_size) if B else 1, "pa_decode_weights", dev)
             self.workspace = workspace
@@ -1149,8 +1158,8 @@ class StepPlan:
         return ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
 
     def reshape_and_cache(self):
-        if self.mode in ("fused", "balanced"):
-            return                          # part of the fused step
+        if self.mode in ("fused", "balanced") or self._reshape_args is None:
+            return                          # part of the fused step, or done before it
         fn = self._lib.pa_reshape_and_cache_fp8 if self.fp8 else self._lib.pa_reshape_and_cache
         _check("pa_reshape_and_cache", fn(*self._reshape_args, self._stream()))
 

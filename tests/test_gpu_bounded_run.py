@@ -370,3 +370,42 @@ def test_calls_from_threads(dev):
     for seed in want:
         for a, b in zip(want[seed], got[seed]):
             assert all(same_bits(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_step_plan_behind_the_rotary_write(dev, fp8):
+    """A decode step of turned keys: rope_and_cache and a weights plan without
+    new keys, called and replayed in one graph, attend to the turned keys and
+    leave them in the cache."""
+    hq, hkv, d, bs = 8, 2, 128, 16
+    x = Batch([300, 17, 64], hq, hkv, d, bs, torch.float16, seed=53, fp8=fp8, stale=False)
+    qkv = torch.randn(3, (hq + 2 * hkv) * d, generator=x.gen).to(torch.float16).to(dev)
+    q, k, v = (t.view(3, -1, d) for t in qkv.split([hq * d, hkv * d, hkv * d], dim=1))
+    at = (x.lens - 1).long()
+    slots = (x.tables[torch.arange(3), at // bs].long() * bs + at % bs).to(dev)
+    pos, inv = (at + 1000).to(dev), lib.rope_frequencies(d)[0].to(dev)
+    start = x.state().nan_to_num(0.0).to(dev)
+    kc, vc, tables, lens = x.k.to(dev), x.v.to(dev), x.tables.to(dev), x.lens.to(dev)
+    kr, vr = kc.clone(), vc.clone()
+    turned = lib.rope_and_cache(q, k, v, pos, slots, inv, kr, vr, **x.scales())
+    want = lib.decode_weights(turned, kr, vr, tables, lens, x.scale, 300, weights=start.clone(), **x.scales())
+    w, tq = start.clone(), torch.empty_like(turned)
+    plan = lib.StepPlan(tq, None, None, None, kc, vc, tables, lens, x.scale, 300, mode="weights", weights=w,
+                        **x.scales())
+
+    def turn():
+        lib.rope_and_cache(q, k, v, pos, slots, inv, kc, vc, q_out=tq, **x.scales())
+
+    turn()
+    assert same_bits(plan(), want[0]) and same_bits(w, want[1]) and same_bits(kc, kr) and same_bits(vc, vr)
+    plan.capture_graph(before=turn)
+    kc.copy_(x.k), vc.copy_(x.v), w.copy_(start)
+    assert same_bits(plan.replay(), want[0]) and same_bits(w, want[1]) and same_bits(kc, kr) and same_bits(vc, vr)
+    args = (tq, k.contiguous(), v.contiguous(), slots, kc, vc, tables, lens, x.scale, 300)
+    for bad in ((1,), (3,), (1, 2)):                     # all three or none
+        with pytest.raises((ValueError, TypeError)):
+            lib.StepPlan(*[None if i in bad else a for i, a in enumerate(args)], mode="weights", weights=w, **x.scales())
+    with pytest.raises(ValueError):
+        lib.StepPlan(*[None if i in (1, 2, 3) else a for i, a in enumerate(args)], mode="fused", **x.scales())
+    torch.cuda.synchronize(dev)
+    assert lib.read_device_errors(dev) == 0
