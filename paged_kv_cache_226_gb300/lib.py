@@ -637,7 +637,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
             def pair_of(n):             # the pair that turns n times over original_len
                 return rotary_dim * np.log(original_len / (n * 2 * np.pi)) / (2 * np.log(base))
             lo = max(np.floor(pair_of(fast)), 0.0)
-            hi = min(np.ceil(pair_of(slow)), half - 1.0)
+            hi = min(np.ceil(pair_of(slow)), rotary_dim - 1.0)
             keep = 1.0 - ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
             mult = 0.1 * float(np.log(factor)) + 1.0
         inv = inv * keep + inv / factor * (1.0 - keep)

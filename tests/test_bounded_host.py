@@ -220,3 +220,23 @@ def test_binding_refuses_before_the_gpu(pa):
 
 def test_binding_is_built_for_this_torch(pa):
     assert build.native_up_to_date()
+
+
+@pytest.mark.parametrize("rotary,base,original", [(128, 10000.0, 65536), (64, 10000.0, 65536), (128, 10000.0, 4096),
+                                                  (96, 500000.0, 8192), (64, 500.0, 131072)])
+def test_yarn_ramp(rotary, base, original):
+    """The ramp runs from the pair that turns 32 times over the original length
+    to the one that turns once, in whole pairs, also where that one lies past
+    the last of the R/2 pairs (up to R - 1)."""
+    factor = 8.0
+    got, mult = lib.rope_frequencies(rotary, base, "yarn", factor, original_len=original)
+
+    def pair(turns):
+        return rotary * math.log(original / (2 * math.pi * turns)) / (2 * math.log(base))
+
+    first, last = max(math.floor(pair(32)), 0), min(math.ceil(pair(1)), rotary - 1)
+    for i in range(rotary // 2):
+        f = base ** (-2 * i / rotary)
+        share = min(max((i - first) / (last - first), 0.0), 1.0)        # of the stretched frequency
+        assert math.isclose(float(got[i]), f * (1 - share) + f / factor * share, rel_tol=2.0 ** -23), i
+    assert mult == 0.1 * math.log(factor) + 1
