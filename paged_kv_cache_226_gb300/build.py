@@ -96,9 +96,8 @@ def _compile_native() -> str:
 def _link_native(obj: str) -> None:
     import torch
     tmp = NATIVE_PATH + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libpa.so", "-Wl,-rpath,$ORIGIN", "-L",
-           os.path.join(torch.__path__[0], "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
-           "-lc10", "-lc10_cuda"]
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", os.path.join(torch.__path__[0], "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")

@@ -12,7 +12,8 @@
 // given, raises TypeError or ValueError, and enqueues on the current stream of
 // the cache's device.  It returns what the Python function returns, or the
 // entry point's status as an int if that refused.  The interpreter lock is
-// released around allocation and launch, which may wait for the GPU.
+// released around allocation and launch, which may wait for the GPU.  The
+// entry points are those of the library that bind() was given last.
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
@@ -22,6 +23,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <dlfcn.h>
 
 #include <algorithm>
 #include <cstdint>
@@ -37,6 +40,59 @@ using at::Tensor;
 [[noreturn]] void refuse(PyObject* type, const std::string& what) {
     PyErr_SetString(type, what.c_str());
     throw python_error();
+}
+
+// The library's entry points.  A set is made per bind() and kept, so that calls
+// under way in other threads end on the one they began with.
+struct Entries {
+    decltype(&pa_rope_and_cache) rope_and_cache;
+    decltype(&pa_rope_and_cache_fp8) rope_and_cache_fp8;
+    decltype(&pa_decode_weights_workspace_size) decode_weights_workspace_size;
+    decltype(&pa_decode_weights) decode_weights;
+    decltype(&pa_decode_weights_fp8) decode_weights_fp8;
+    decltype(&pa_prefill_weights_workspace_size) prefill_weights_workspace_size;
+    decltype(&pa_prefill_weights) prefill_weights;
+    decltype(&pa_evict_workspace_size) evict_workspace_size;
+    decltype(&pa_evict) evict;
+    decltype(&pa_evict_fp8) evict_fp8;
+};
+
+const Entries* g_entries = nullptr;
+
+const Entries& entries() {
+    if (!g_entries) refuse(PyExc_RuntimeError, "no library is bound");
+    return *g_entries;
+}
+
+template <typename F>
+void find(void* handle, const char* name, F& f) {
+    f = reinterpret_cast<F>(dlsym(handle, name));
+    if (!f) refuse(PyExc_ImportError, std::string("the library has no ") + name);
+}
+
+// (handle): the dlopen handle of the library to call, which must stay open.
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 1) refuse(PyExc_TypeError, "expected 1 argument");
+    void* handle = PyLong_AsVoidPtr(a[0]);
+    if (!handle) {
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "no library handle");
+        throw python_error();
+    }
+    Entries e;
+    find(handle, "pa_rope_and_cache", e.rope_and_cache);
+    find(handle, "pa_rope_and_cache_fp8", e.rope_and_cache_fp8);
+    find(handle, "pa_decode_weights_workspace_size", e.decode_weights_workspace_size);
+    find(handle, "pa_decode_weights", e.decode_weights);
+    find(handle, "pa_decode_weights_fp8", e.decode_weights_fp8);
+    find(handle, "pa_prefill_weights_workspace_size", e.prefill_weights_workspace_size);
+    find(handle, "pa_prefill_weights", e.prefill_weights);
+    find(handle, "pa_evict_workspace_size", e.evict_workspace_size);
+    find(handle, "pa_evict", e.evict);
+    find(handle, "pa_evict_fp8", e.evict_fp8);
+    g_entries = new Entries(e);
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
 }
 
 std::string dtype_name(at::ScalarType t) {
@@ -266,6 +322,7 @@ void expect(Py_ssize_t got, Py_ssize_t want) {
 PyObject* rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     expect(n, 13);
+    const Entries& lib = entries();
     const Pools p(a[6], a[7]);
     const Scales s(p.fp8, a[11], a[12]);
     const at::ScalarType dt = tensor(a[1], "k").scalar_type();
@@ -315,12 +372,12 @@ PyObject* rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t* sp = (const int64_t*)slot.data_ptr();
         const float* ip = (const float*)inv.data_ptr();
         const int32_t rot = (int32_t)std::min(2 * inv.size(0), kMaxInt32);
-        status = p.fp8 ? pa_rope_and_cache_fp8(q.data, q.stride, k.data, k.stride, v.data, v.stride, pp,
-                                               sp, ip, rot, interleaved, factor, (void*)out.data,
-                                               out.stride, p.k, p.v, T, s.k, s.v, &shp, stream)
-                       : pa_rope_and_cache(q.data, q.stride, k.data, k.stride, v.data, v.stride, pp, sp,
-                                           ip, rot, interleaved, factor, (void*)out.data, out.stride,
-                                           p.k, p.v, T, &shp, stream);
+        status = p.fp8 ? lib.rope_and_cache_fp8(q.data, q.stride, k.data, k.stride, v.data, v.stride, pp,
+                                                sp, ip, rot, interleaved, factor, (void*)out.data,
+                                                out.stride, p.k, p.v, T, s.k, s.v, &shp, stream)
+                       : lib.rope_and_cache(q.data, q.stride, k.data, k.stride, v.data, v.stride, pp, sp,
+                                            ip, rot, interleaved, factor, (void*)out.data, out.stride,
+                                            p.k, p.v, T, &shp, stream);
     }
     if (status != PA_OK) return refused(status);
     if (a[0] == Py_None) Py_RETURN_NONE;
@@ -364,6 +421,7 @@ struct Weights {
 PyObject* decode_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     expect(n, 14);
+    const Entries& lib = entries();
     const Pools p(a[1], a[2]);
     const Scales s(p.fp8, a[12], a[13]);
     const Batch b(a[3], a[4], p.index);
@@ -399,7 +457,7 @@ PyObject* decode_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
     {
         Unlocked u;
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.index);
-        if (!ws.need(b.seqs ? pa_decode_weights_workspace_size(&shp, longest, partition) : 1)) {
+        if (!ws.need(b.seqs ? lib.decode_weights_workspace_size(&shp, longest, partition) : 1)) {
             status = PA_ERR_INVALID_ARG;
         } else {
             w.make(b, p);
@@ -408,12 +466,12 @@ PyObject* decode_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 out = made.data_ptr();
             }
             void* stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)p.index).stream();
-            status = p.fp8 ? pa_decode_weights_fp8(q.data_ptr(), p.k, p.v, b.tables, b.lens, scale, s.k,
-                                                   s.v, longest, partition, w.in, w.out, w.stride,
-                                                   ws.data, ws.bytes, out, &shp, stream)
-                           : pa_decode_weights(q.data_ptr(), p.k, p.v, b.tables, b.lens, scale, longest,
-                                               partition, w.in, w.out, w.stride, ws.data, ws.bytes,
-                                               out, &shp, stream);
+            status = p.fp8 ? lib.decode_weights_fp8(q.data_ptr(), p.k, p.v, b.tables, b.lens, scale, s.k,
+                                                    s.v, longest, partition, w.in, w.out, w.stride,
+                                                    ws.data, ws.bytes, out, &shp, stream)
+                           : lib.decode_weights(q.data_ptr(), p.k, p.v, b.tables, b.lens, scale, longest,
+                                                partition, w.in, w.out, w.stride, ws.data, ws.bytes,
+                                                out, &shp, stream);
         }
         ws.own.clear();
     }
@@ -427,6 +485,7 @@ PyObject* decode_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* prefill_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     expect(n, 12);
+    const Entries& lib = entries();
     const Pools p(a[1], a[1]);
     if (p.fp8) refuse(PyExc_TypeError, "prefill_weights reads a float16 or bfloat16 cache");
     const Batch b(a[2], a[3], p.index);
@@ -445,15 +504,15 @@ PyObject* prefill_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
     {
         Unlocked u;
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.index);
-        if (!ws.need(pa_prefill_weights_workspace_size(&shp, longest_chunk, longest, window))) {
+        if (!ws.need(lib.prefill_weights_workspace_size(&shp, longest_chunk, longest, window))) {
             status = PA_ERR_INVALID_ARG;
         } else {
             w.make(b, p);
             void* stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)p.index).stream();
-            status = pa_prefill_weights(q.data_ptr(), p.k, b.tables, b.lens,
-                                        (const int32_t*)start.data_ptr(), scale, q.size(0),
-                                        longest_chunk, longest, window, w.in, w.out, w.stride, ws.data,
-                                        ws.bytes, &shp, stream);
+            status = lib.prefill_weights(q.data_ptr(), p.k, b.tables, b.lens,
+                                         (const int32_t*)start.data_ptr(), scale, q.size(0),
+                                         longest_chunk, longest, window, w.in, w.out, w.stride, ws.data,
+                                         ws.bytes, &shp, stream);
         }
         ws.own.clear();
     }
@@ -468,6 +527,7 @@ PyObject* prefill_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     expect(n, 16);
+    const Entries& lib = entries();
     const Pools p(a[0], a[1]);
     const Batch b(a[2], a[3], p.index);
     const Tensor& w = state(a[6], "weights", b, p, at::kFloat);
@@ -493,7 +553,7 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     {
         Unlocked u;
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.index);
-        if (!ws.need(b.seqs ? pa_evict_workspace_size(&shp, budget) : 1)) {
+        if (!ws.need(b.seqs ? lib.evict_workspace_size(&shp, budget) : 1)) {
             status = PA_ERR_INVALID_ARG;
         } else {
             if (a[14] == Py_None) {
@@ -501,7 +561,7 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 fresh = (int32_t*)made.data_ptr();
             }
             void* stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)p.index).stream();
-            status = (p.fp8 ? pa_evict_fp8 : pa_evict)(
+            status = (p.fp8 ? lib.evict_fp8 : lib.evict)(
                 p.k, p.v, b.tables, b.lens, (const int32_t*)seen.data_ptr(), known,
                 (const float*)w.data_ptr(), (const int32_t*)pos.data_ptr(), width, budget, trigger,
                 sinks, recent, (float*)wo.data_ptr(), (int32_t*)po.data_ptr(), fresh, ws.data, ws.bytes,
@@ -520,7 +580,7 @@ constexpr PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {method<rope_and_cache>("rope_and_cache"), method<decode_weights>("decode_weights"),
-                         method<prefill_weights>("prefill_weights"), method<evict>("evict"),
+                         method<prefill_weights>("prefill_weights"), method<evict>("evict"), method<bind>("bind"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_native", "Binding of the bounded-cache operators.", -1,

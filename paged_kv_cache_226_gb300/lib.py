@@ -647,19 +647,22 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
 
 
 _native = None
+_bound = object()        # the library that _native calls
 
 
 def _load_native():
-    """The binding of the bounded-cache calls (csrc/binding.cpp): their checks
-    and allocations in native code, since a layer makes three of them per step."""
-    global _native
-    load()
+    """The binding of the bounded-cache calls (csrc/binding.cpp), set to call
+    the loaded library: their checks and allocations in native code, since a
+    layer makes three of them per step."""
+    global _native, _bound
+    lib = load()
     try:
         from . import _native as native
     except ImportError as e:
         raise ImportError(f"_native.so cannot be loaded ({e}); build it with "
                           "`python -m paged_kv_cache_226_gb300.build`") from e
-    _native = native
+    native.bind(lib._handle)
+    _native, _bound = native, lib
     return native
 
 
@@ -719,7 +722,7 @@ def rope_and_cache(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     projection's output will do); ``q=None`` writes the cache only.
     positions, slot_mapping: int64 [T]; inv_freq: fp32 [R/2], the first R dims
     of a head turn (``rope_frequencies``).  ``q_out=q`` turns q in place."""
-    r = (_native or _load_native()).rope_and_cache(
+    r = (_native if _bound is _lib else _load_native()).rope_and_cache(
         q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cache, q_out, interleaved, factor,
         k_scale, v_scale)
     if r.__class__ is int:
@@ -788,7 +791,7 @@ def decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     cache); returns (out, weights_out).  The newest token's entry is set, not
     added to; ``weights=None`` starts at zero.  ``weights_out`` defaults to
     ``weights`` (in place), or a new tensor of zeros."""
-    r = (_native or _load_native()).decode_weights(
+    r = (_native if _bound is _lib else _load_native()).decode_weights(
         q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len, weights,
         weights_out, out, weights_partition if partition_size is None else partition_size,
         workspace, k_scale, v_scale)
@@ -808,7 +811,7 @@ def prefill_weights(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.
     (pa_prefill_weights; ``prefill`` gives the attention itself).  The chunk's
     own tokens are set, not added to.  ``weights_out`` defaults to ``weights``
     (in place), or a new tensor of zeros; returned."""
-    r = (_native or _load_native()).prefill_weights(
+    r = (_native if _bound is _lib else _load_native()).prefill_weights(
         q, k_cache, block_tables, context_lens, query_start, scale, max_query_len,
         max_context_len, window, weights, weights_out, workspace)
     if r.__class__ is int:
@@ -834,7 +837,7 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tens
     (entries of ``positions`` that are set; None: none).  Blocks past
     ceil(new_len / block_size) are free afterwards
     (``PagedKVAllocator.truncate``)."""
-    r = (_native or _load_native()).evict(
+    r = (_native if _bound is _lib else _load_native()).evict(
         k_cache, v_cache, block_tables, context_lens, seen_lens, budget, weights, positions,
         known_lens, trigger, sinks, recent, weights_out, positions_out, new_lens, workspace)
     if r.__class__ is int:
@@ -1004,18 +1007,19 @@ class InputStaging:
 class StepPlan:
     """One decode layer-step with its arguments marshalled once.
 
-    Holds the C-ABI argument lists of the step for fixed tensors, so that
-    each launch costs one ctypes call.  Modes: ``"fused"`` (the default: one
+    Holds the C-ABI argument lists of the step for fixed tensors, so that each
+    launch costs one ctypes call. Modes: ``"fused"`` (the default: one
     pa_decode_step launch), ``"split"`` (reshape_and_cache, decode_split,
     reduce), ``"single"`` (reshape_and_cache, decode) and ``"weights"``
     (reshape_and_cache, decode_weights: each step adds the attention weights
     into ``weights``, or reads them there and writes ``weights_out``; with
     ``k_new``, ``v_new`` and ``slot_mapping`` None the step is decode_weights
     alone, for keys that ``rope_and_cache`` has turned and cached: the plan's
-    own cache write would put the unturned ones over them).  The work goes to the caller's current stream at call time, which also makes a
-    step capturable into a CUDA graph (``capture_graph``).  The tensors must
-    stay alive and keep their shapes; their contents (new tokens, tables,
-    lengths) may change between steps as long as ``context_lens`` stays within
+    own cache write would put the unturned ones over them). The work goes to
+    the caller's current stream at call time, which also makes a step
+    capturable into a CUDA graph (``capture_graph``). The tensors must stay
+    alive and keep their shapes; their contents (new tokens, tables, lengths)
+    may change between steps as long as ``context_lens`` stays within
     ``max_context_len``.
 
     In the fused mode q, k_new, v_new, slot_mapping, block_tables,

@@ -240,3 +240,24 @@ def test_yarn_ramp(rotary, base, original):
         share = min(max((i - first) / (last - first), 0.0), 1.0)        # of the stretched frequency
         assert math.isclose(float(got[i]), f * (1 - share) + f / factor * share, rel_tol=2.0 ** -23), i
     assert mult == 0.1 * math.log(factor) + 1
+
+
+def test_binding_calls_the_loaded_library(pa, monkeypatch):
+    """What the four calls enqueue, and the error bits that they set, belong to
+    the library that every other call uses."""
+    native = lib._load_native()
+    assert lib._bound is pa
+    other = ctypes.CDLL(lib.LIB_PATH)                  # a handle of its own
+    monkeypatch.setattr(lib, "_lib", other)
+    with pytest.raises(TypeError):
+        lib.evict(*[None] * 7, torch.zeros(1))
+    assert lib._bound is other and lib._native is native
+    monkeypatch.undo()
+    with pytest.raises(TypeError):
+        lib.prefill_weights(*[None] * 8)
+    assert lib._bound is pa
+    for bad in (0, "x", None):
+        with pytest.raises((TypeError, ValueError)):
+            native.bind(bad)
+    with pytest.raises(ImportError, match="pa_rope_and_cache"):
+        native.bind(ctypes.CDLL(None)._handle)
