@@ -223,6 +223,10 @@ int pa::encode_query_map(CUtensorMap* map, const void* q, const pa_shape* s, int
     return r == CUDA_SUCCESS ? PA_OK : PA_ERR_INVALID_ARG;
 }
 
+#ifdef PA_TEST_HOOKS
+pa::TestFault pa::test_fault() { return {g_test_cta, g_test_tile, g_test_wait_limit_ns}; }
+#endif
+
 void pa::record_cuda_error(int cuda_error) { t_last_cuda_error = cuda_error; }
 
 cudaError_t pa::current_context(void** ctx) {

@@ -128,7 +128,8 @@ int decode_weights(const void* q, const void* k_cache, const void* v_cache,
     p.exp_sums = reinterpret_cast<float*>(base + w.sums);
     p.scores = reinterpret_cast<float*>(base + w.scores);
 #ifdef PA_TEST_HOOKS
-    p.test_cta = -1, p.test_wait_limit_ns = pa::kWaitLimitNs;
+    const pa::TestFault fault = pa::test_fault();
+    p.test_cta = fault.cta, p.test_tile = fault.tile, p.test_wait_limit_ns = fault.wait_limit_ns;
 #endif
     const dim3 grid(shp->num_seqs, shp->num_kv_heads, w.parts);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -311,6 +312,10 @@ int pa_prefill_weights(const void* q, const void* k_cache, const int32_t* block_
     p.scale_log2 = scale * pa::kLog2e;
     p.max_blocks_per_seq = shp->max_blocks_per_seq, p.block_size = shp->block_size;
     p.num_blocks = shp->num_blocks, p.num_tokens = num_tokens;
+#ifdef PA_TEST_HOOKS
+    const pa::TestFault fault = pa::test_fault();
+    p.test_cta = fault.cta, p.test_tile = fault.tile, p.test_wait_limit_ns = fault.wait_limit_ns;
+#endif
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     bool launched = false;
     if (lone) e = pa::launch_short_weights(shp->dtype, shp->head_dim, tmk, tmq, p, cs, &launched);

@@ -76,6 +76,12 @@ struct PrefillWeightsParams {
     float2* stats;                 // [key_chunks] x the same: maximum and sum
     float* columns;                // [query_chunks][B][Hkv][columns_stride]
     int columns_stride;
+#ifdef PA_TEST_HOOKS
+    // Test builds only: CTA test_cta's loaders issue no streamed tile from
+    // test_tile on, and waits give up after test_wait_limit_ns.
+    int test_cta, test_tile;
+    unsigned long long test_wait_limit_ns;
+#endif
 };
 
 // Chooses the chunks, lays out the workspace and returns its bytes (needs

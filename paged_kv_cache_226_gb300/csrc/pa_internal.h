@@ -200,6 +200,15 @@ int encode_query_map(CUtensorMap* map, const void* q, const pa_shape* shp, int64
 // Device address of the error word on the current device.
 cudaError_t error_word(int** out);
 
+#ifdef PA_TEST_HOOKS
+// Test builds only: the wait fault of pa_test_set_wait_fault (include/pa_test.h).
+struct TestFault {
+    int cta, tile;
+    unsigned long long wait_limit_ns;
+};
+TestFault test_fault();
+#endif
+
 // Sets the value pa_last_cuda_error() reports on this host thread.
 void record_cuda_error(int cuda_error);
 

@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     using Lay = PwLayout<D>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t kId = idesc_f16(kPwRows, kPwCols, kBf16, false);
-    __shared__ __align__(8) uint64_t q_full, k_full[kTiles], s_full[kTiles], s_empty[kTiles];
+    __shared__ __align__(8) uint64_t q_full, k_full[kTiles], s_full[kTiles], s_empty[kTiles], done;
     __shared__ uint32_t tmem_base;
     __shared__ float2 stats_s[kTiles][kPwRows];                  // per tile: a row's maximum and sum
     __shared__ float2 joined[kPwRows];                           // of the CTA's tiles
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     const int G = p.group, q_rows = p.tile_tokens * G;           // rows of the query box, <= 128
 
     if (threadIdx.x == 0) {
-        mbar_init(&q_full, 1);
+        mbar_init(&q_full, 1), mbar_init(&done, 1);
         for (int i = 0; i < kTiles; ++i)
             mbar_init(&k_full[i], 4), mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4);
         fence_barrier_init();
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     const size_t at = (size_t)pair * p.weights_stride + kt * kPwCols + r;
     float before = 0.f;
     auto wait = [&](uint64_t* bar, int phase) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase));
+        ok = ok && pw_wait(p, bar, phase);
         tc_fence_after_sync();
     };
     auto release = [&] {                                         // the tile is in registers
@@ -115,11 +115,13 @@ __global__ void __launch_bounds__(kShortThreads, 1)
             wait(&s_empty[i], 0);
             if (ok) pw_product<D>(tmem + kPwCols * i, dk + i * (Lay::kTile >> 4), dq, kId, &s_full[i]);
         }
+        ok = pw_products_done(p, &done) && ok;
     } else if (epilogue && tiles > 0) {
         float m = -INFINITY, z = 0.f;
         if (works) {
             const int blk = pw_checked(p, pw_blocks(p, s, b, kt >> 2));
-            pw_load_keys<D, 2>(&tmap_k, k_tiles + group * Lay::kTile, &k_full[group], p, s, g, kt, blk, warp & 3, 8, 4);
+            if (!pw_withheld(p, group))
+                pw_load_keys<D, 2>(&tmap_k, k_tiles + group * Lay::kTile, &k_full[group], p, s, g, kt, blk, warp & 3, 8, 4);
             const int visible = min(s.L - s.counted + r / G, s.L - 1) - kt * kPwCols;
             if (p.weights && kt * kPwCols + r < s.L - s.C) before = p.weights[at];
             wait(&s_full[group], 0);
@@ -160,14 +162,15 @@ __global__ void __launch_bounds__(kShortThreads, 1)
         if (works) {
             const int key = kt * kPwCols + r;
             const int lo = (key - (s.L - s.counted)) * G, hi = s.counted * G;
-            auto done = [] {};
+            auto nothing = [] {};
             float w;
             wait(&s_full[group], 1);
             if (s.counted == p.tile_tokens && __all_sync(0xffffffffu, lo <= 0))
-                w = column_sums<false>(tile_addr, neg_lse, sl2, lo, hi, done);
+                w = column_sums<false>(tile_addr, neg_lse, sl2, lo, hi, nothing);
             else
-                w = column_sums<true>(tile_addr, neg_lse, sl2, lo, hi, done);
+                w = column_sums<true>(tile_addr, neg_lse, sl2, lo, hi, nothing);
             if (key < s.L && ok) p.weights_out[at] = before + w;
+            ok = pw_wait(p, &k_full[group], 0) && ok;            // the copies have landed
         }
     } else if (epilogue && s.counted == 0) {
         // nothing is added: what was there is carried over

@@ -41,8 +41,9 @@
 // whose instructions per score are few but for the exponential.
 //
 // Every mbarrier wait gives up after 1 s and flags PA_DEVERR_WAIT_TIMEOUT;
-// the epilogue warps then run their remaining steps without waiting, and
-// tensor memory is always released.
+// the epilogue warps then run their remaining steps without waiting.  Loaders
+// and issuers end only when their last copies and products have landed (or
+// have not for 1 s), and tensor memory is always released.
 #include <algorithm>
 
 #include "prefill_weights.cuh"
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
     constexpr int kA = 3, kB = 3;
     static_assert(kA + kB == Lay::kStages, "the rings share the CTA's tiles");
     __shared__ __align__(8) uint64_t a_full[kA], a_empty[kA], b_full[kB], b_empty[kB];
-    __shared__ __align__(8) uint64_t s_full[kPwBufs], s_empty[kPwBufs];
+    __shared__ __align__(8) uint64_t s_full[kPwBufs], s_empty[kPwBufs], done[2];
     __shared__ uint32_t tmem_base;
     __shared__ __align__(16) float4 lse_s[4 * kPwGroups][2][kPwCols / 4];   // pass 2: [warp][tile parity]
     __shared__ float2 other[2][2][kPwRows];                          // [join parity][resident tile]
@@ -174,11 +175,11 @@ __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
     const int q_rows = p.tile_tokens * G;                    // rows of a query tile, <= 128
 
     if (threadIdx.x == 0) {
-        // pass 1 has two loaders for each K stage; a resident tile has one issuer, a streamed
-        // tile both
+        // a stage has one loader; a resident tile has one issuer, a streamed tile both
         for (int i = 0; i < kA; ++i) mbar_init(&a_full[i], 1), mbar_init(&a_empty[i], 1);
         for (int i = 0; i < kB; ++i) mbar_init(&b_full[i], 1), mbar_init(&b_empty[i], 2);
         for (int i = 0; i < kPwBufs; ++i) mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4);
+        for (int i = 0; i < 2; ++i) mbar_init(&done[i], 1);
         fence_barrier_init();
     }
     if (warp == 0) tmem_alloc(&tmem_base, kPwBufs * kPwCols);
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
         if (lane == 0) prefetch_tensor_map(&tmap_q), prefetch_tensor_map(&tmap_k);
         // waits for stage n % stages to be free
         auto open = [&](uint64_t* empty, int stages, int n) -> bool {
-            return n < stages || __all_sync(0xffffffffu, mbar_wait(&empty[n % stages], ((n / stages) - 1) & 1));
+            return n < stages || pw_wait(p, &empty[n % stages], n / stages - 1);
         };
         auto load_k = [&](uint8_t* dst, uint64_t* full, uint64_t* empty, int stages, int n,
                           const PwSeq& s, const PwUnit& U, int kt, int blk) -> bool {
@@ -229,9 +230,9 @@ __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
         PwWalk<kStats> walk;
         PwUnit U;
         int na = 0, nb = 0, at_b = -1, at_g = -1, at_qt = -1;
-        bool ok = true;
+        bool ok = true, held = false;
         static_assert(kA == 3 && kB == 3 && pw_loaders(true) == 3, "a loader for each stage");
-        while (ok && walk.next(p, U)) {
+        while (ok && !held && walk.next(p, U)) {
             // block ids of the current four key tiles and of the next four
             int quad = -2, blk = 0, blk_next = 0;
             auto to_tile = [&](int kt) {
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
                 if (mine_a(na))
                     ok = kStats ? load_q(a_ring, a_full, a_empty, kA, na, walk.s, U, 2 * U.a + j)
                                 : load_k(a_ring, a_full, a_empty, kA, na, walk.s, U, 2 * U.a + j, blk);
-                ++na;
+                na += ok;
             }
             for (int i = U.first; ok && i < U.last; ++i) {
                 if (kStats) {
@@ -257,12 +258,18 @@ __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
                     if (U.b == at_b && U.g == at_g && i == at_qt) continue;     // still there
                     at_b = U.b, at_g = U.g, at_qt = i;
                 }
+                if (mine_b(nb) && pw_withheld(p, nb)) {
+                    held = true;
+                    break;
+                }
                 if (mine_b(nb))
                     ok = kStats ? load_k(b_ring, b_full, b_empty, kB, nb, walk.s, U, i, blk)
                                 : load_q(b_ring, b_full, b_empty, kB, nb, walk.s, U, i);
-                ++nb;
+                nb += ok;
             }
         }
+        ok = pw_landed(p, a_full, kA, na, mine_a) && ok;
+        ok = pw_landed(p, b_full, kB, nb, mine_b) && ok;
         if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
     } else if (warp < 2) {
         // ------------------------------------------------------------------
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
         int used[2] = {0, 0};                               // products so far in each buffer
         bool ok = true;
         auto wait = [&](uint64_t* bar, int phase) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1));
+            ok = ok && pw_wait(p, bar, phase);
         };
         while (ok && walk.next(p, U)) {
             if (U.first >= U.last) continue;
@@ -310,6 +317,7 @@ __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
             __syncwarp();
             na += residents;
         }
+        ok = pw_products_done(p, &done[warp]) && ok;
         if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
     } else {
         // ------------------------------------------------------------------
@@ -324,7 +332,7 @@ __global__ void __launch_bounds__(pw_threads(pw_loaders(kStats)), 1)
         const uint64_t sl2 = f32x2_pack(sl, sl);
         bool failed = false;
         auto wait = [&](int n) {                // the group's n-th tile
-            if (!failed && !__all_sync(0xffffffffu, mbar_wait(&s_full[group], n & 1))) failed = true;
+            if (!failed && !pw_wait(p, &s_full[group], n)) failed = true;
             tc_fence_after_sync();
         };
         auto release = [&] {                    // the tile is in registers

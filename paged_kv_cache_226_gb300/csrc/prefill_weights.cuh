@@ -29,6 +29,44 @@ struct PwLayout {
     static constexpr int kDynamicSmem = kStages * kTile + 1024;
 };
 
+// The wait limit of a kernel's barriers, and whether streamed tile n of this
+// CTA is withheld from it (test builds only).
+#ifdef PA_TEST_HOOKS
+__device__ __forceinline__ uint64_t pw_wait_limit(const PrefillWeightsParams& p) { return p.test_wait_limit_ns; }
+__device__ __forceinline__ bool pw_withheld(const PrefillWeightsParams& p, int n) {
+    return (int)blockIdx.x == p.test_cta && n >= p.test_tile;
+}
+#else
+__device__ __forceinline__ constexpr uint64_t pw_wait_limit(const PrefillWeightsParams&) { return kWaitLimitNs; }
+__device__ __forceinline__ constexpr bool pw_withheld(const PrefillWeightsParams&, int) { return false; }
+#endif
+
+// mbar_wait for all lanes of a warp.
+__device__ __forceinline__ bool pw_wait(const PrefillWeightsParams& p, uint64_t* bar, int phase) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, pw_wait_limit(p)));
+}
+
+// The end of a loader: tiles 0 .. n - 1 went to stages n % stages, this warp
+// having issued those of the stages that mine() names.  The last of each has
+// landed before the CTA's shared memory is given up, whatever became of those
+// who wait for them.
+template <typename Mine>
+__device__ __forceinline__ bool pw_landed(const PrefillWeightsParams& p, uint64_t* full, int stages, int n,
+                                          Mine&& mine) {
+    bool ok = true;
+    for (int st = 0; st < stages && st < n; ++st)
+        if (mine(st)) ok = pw_wait(p, &full[st], (n - 1 - st) / stages) && ok;
+    return ok;
+}
+
+// The end of an issuer: its products are done before tensor memory and their
+// operands are given up.
+__device__ __forceinline__ bool pw_products_done(const PrefillWeightsParams& p, uint64_t* bar) {
+    if (elect_one()) mma_commit(bar);
+    __syncwarp();
+    return pw_wait(p, bar, 0);
+}
+
 struct PwSeq {
     int L, C, counted;             // context, chunk, counted queries
     int q0;                        // row of the first counted query in q

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     static_assert(kWkStages + kWqStages == Lay::kStages, "the rings share the CTA's tiles");
     __shared__ __align__(8) uint64_t k_full[kWkStages], k_empty[kWkStages], q_full[kWqStages], q_empty[kWqStages];
-    __shared__ __align__(8) uint64_t s_full[kPwBufs], s_empty[kPwBufs];
+    __shared__ __align__(8) uint64_t s_full[kPwBufs], s_empty[kPwBufs], done[2];
     __shared__ uint32_t tmem_base;
     __shared__ __align__(16) float lse_s[kPwGroups][2][kPwCols];     // pass 2: [group][row parity]
     __shared__ float2 other[2][kPwGroups - 1][kPwRows];              // pass 1: [join parity][group]
@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         for (int i = 0; i < kWkStages; ++i) mbar_init(&k_full[i], 2), mbar_init(&k_empty[i], 1);
         for (int i = 0; i < kWqStages; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 2);
         for (int i = 0; i < kPwBufs; ++i) mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4);
+        for (int i = 0; i < 2; ++i) mbar_init(&done[i], 1);
         fence_barrier_init();
     }
     if (warp == 0) tmem_alloc(&tmem_base, kPwBufs * kPwCols);
@@ -179,13 +180,13 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         const int who = warp < 4 ? warp - 2 : warp - kPwLoadersAfter + 2;
         if (lane == 0) prefetch_tensor_map(&tmap_q), prefetch_tensor_map(&tmap_k);
         int n = 0, nq = 0;                                  // key and query tiles so far
-        bool ok = true;
-        while (ok && runs.next(p, R)) {
+        bool ok = true, held = false;
+        while (ok && !held && runs.next(p, R)) {
             const PwSeq& s = runs.s;
             if (s.counted == 0) continue;
             if (who == 0) {
                 const int st = nq % kWqStages;
-                if (nq >= kWqStages) ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[st], (nq / kWqStages - 1) & 1));
+                if (nq >= kWqStages) ok = pw_wait(p, &q_empty[st], nq / kWqStages - 1);
                 if (!ok) break;
                 pw_load_queries<D>(&tmap_q, q_ring + st * Lay::kTile, &q_full[st], p, s, R.g, 0);
             }
@@ -204,12 +205,15 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
                 }
                 const int st = n % kWkStages;
                 if (who != st && who != 4 + (n & 1)) continue;
-                if (n >= kWkStages) ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[st], (n / kWkStages - 1) & 1));
-                if (ok)
-                    pw_load_keys<D, 4>(&tmap_k, k_ring + st * Lay::kTile, &k_full[st], p, s, R.g, kt, blk,
-                                    who < 4 ? 0 : 4, who < 4 ? 4 : 8, 1);
+                if (n >= kWkStages) ok = pw_wait(p, &k_empty[st], n / kWkStages - 1);
+                held = pw_withheld(p, n);
+                if (!ok || held) break;
+                pw_load_keys<D, 4>(&tmap_k, k_ring + st * Lay::kTile, &k_full[st], p, s, R.g, kt, blk,
+                                   who < 4 ? 0 : 4, who < 4 ? 4 : 8, 1);
             }
         }
+        ok = pw_landed(p, k_full, kWkStages, n, [&](int st) { return who == st || who == 4 + (st & 1); }) && ok;
+        ok = pw_landed(p, q_full, kWqStages, nq, [&](int) { return who == 0; }) && ok;
         if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
     } else if (warp < 2) {
         // ------------------------------------------------------------------
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         int n = 0, nq = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, int phase) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1));
+            ok = ok && pw_wait(p, bar, phase);
         };
         while (ok && runs.next(p, R)) {
             if (runs.s.counted == 0) continue;
@@ -243,6 +247,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
             __syncwarp();
             ++nq;
         }
+        ok = pw_products_done(p, &done[warp]) && ok;
         if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
     } else {
         // ------------------------------------------------------------------
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         const uint64_t sl2 = f32x2_pack(sl, sl);
         bool failed = false;
         auto wait = [&](int t) {                // the group's t-th tile
-            if (!failed && !__all_sync(0xffffffffu, mbar_wait(&s_full[group], t & 1))) failed = true;
+            if (!failed && !pw_wait(p, &s_full[group], t)) failed = true;
             tc_fence_after_sync();
         };
         auto release = [&] {                    // the tile is in registers
