@@ -195,3 +195,16 @@ def test_side_stream(dev):
     s.wait_stream(torch.cuda.current_stream(dev))
     with torch.cuda.stream(s):
         check(dev, 37, 8, 2, 128, 16, torch.float16, 128, False, seed=11)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,hq,hkv,d,dtype,rotary,fp8,padding", [
+    (1368, 8, 2, 64, torch.float16, 64, False, 0),          # the last count that goes one token to a CTA
+    (1369, 8, 2, 64, torch.float16, 64, False, 0),          # two, and an odd one at the end
+    (1370, 6, 3, 128, torch.bfloat16, 128, False, 5), (3001, 5, 1, 128, torch.float16, 96, False, 40),
+    (1369, 4, 4, 128, torch.bfloat16, 128, True, 0), (3001, 8, 2, 128, torch.float16, 64, True, 7)])
+def test_rope_packed_prompts(dev, T, hq, hkv, d, dtype, rotary, fp8, padding, interleaved):
+    """More tokens than fit the GPU one to a CTA."""
+    check(dev, T, hq, hkv, d, 16, dtype, rotary, interleaved, seed=T, fp8=fp8, padding=padding)
+    check(dev, T, hq, hkv, d, 32, dtype, rotary, interleaved, seed=T + 1, fp8=fp8, padding=padding, in_place=True)
+    check(dev, T, hq, hkv, d, 16, dtype, rotary, interleaved, seed=T + 2, fp8=fp8, padding=padding, no_q=True)

@@ -488,3 +488,62 @@ def test_step_plan_capture_makes_no_step(dev, fp8, apart):
         assert not apart or same_bits(w, start)
     torch.cuda.synchronize(dev)
     assert lib.read_device_errors(dev) == 0
+
+
+# More sequences than a warp walks at a time: ragged, some empty, a whole group of 32 empty.
+MANY = {33: [37 * i % 301 for i in range(33)], 70: [53 * i % 401 for i in range(70)],
+        100: [0 if 32 <= i < 64 else 29 * i % 257 for i in range(100)],
+        97: [0] * 32 + [41 * i % 200 for i in range(65)]}
+
+
+@pytest.mark.parametrize("n", sorted(MANY))
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(4, 2, 64, F16), (8, 2, 128, BF16)])
+def test_prefill_weights_many_sequences(dev, n, hq, hkv, d, dtype):
+    """Whole chunks (several query tiles) and windows in two passes."""
+    lens = MANY[n]
+    x = Batch(lens, hq, hkv, d, 16, dtype, seed=n)
+    run_prefill(dev, x, [min(m, 90 + 7 * (i % 3)) for i, m in enumerate(lens)], 0, x.state())
+    lens = [m + 4200 * (i == n // 2) for i, m in enumerate(lens)]         # one too long for the one-launch form
+    x = Batch(lens, hq, hkv, d, 16, dtype, seed=n + 1)
+    run_prefill(dev, x, [min(m, 20 + i % 5) for i, m in enumerate(lens)], 9, x.state())
+    run_prefill(dev, x, [min(m, i % 4) for i, m in enumerate(lens)], 0, None)
+
+
+def test_window_behind_writers_of_its_inputs(dev):
+    """The two passes of a window start early on K, Q, lengths and tables:
+    what the kernels directly in front of the call wrote is what they read.
+    Eight rounds on a stream without a synchronisation, every round on other
+    contents, the writers copies and the cache write of a step."""
+    hq, hkv, d, rounds = 8, 2, 128, 8
+    xs = [Batch([5000 + 300 * (r % 3), 4100, 700 * (r % 2)], hq, hkv, d, 16, F16, seed=60 + r, stale=False,
+                slack_width=60) for r in range(rounds)]
+    blocks, width = max(x.k.shape[0] for x in xs), max(x.width for x in xs)
+    chunks, qs = [32, 20, 0], []
+    start = torch.tensor([0, 32, 52, 52], dtype=torch.int32, device=dev)
+    for x in xs:
+        x.k = torch.cat([x.k, torch.zeros(blocks - x.k.shape[0], 16, hkv, d, dtype=F16)])
+        x.tables = torch.cat([x.tables.clamp(max=blocks - 1),
+                              torch.zeros(3, width - x.width, dtype=torch.int32)], 1).contiguous()
+        x.width, x.tokens = width, width * 16
+        qs.append(torch.randn(52, hq, d, generator=x.gen).to(F16))
+    on = [(x.k.to(dev), q.to(dev), x.tables.to(dev), x.lens.to(dev)) for x, q in zip(xs, qs)]
+    last = [torch.tensor([int(x.tables[b, (int(n) - 1) // 16]) * 16 + (int(n) - 1) % 16 if n else -1
+                          for b, n in enumerate(x.lens)], device=dev) for x in xs]
+    k, q, tables, lens = (torch.zeros_like(t) for t in on[0])
+    v = torch.zeros_like(k)
+    new = [torch.randn(3, hkv, d, generator=x.gen).to(F16) for x in xs]
+    newd = [t.to(dev) for t in new]
+    got = [torch.zeros(3, hkv, width * 16, device=dev) for _ in xs]
+    torch.cuda.synchronize(dev)
+    for r in range(rounds):
+        tables.copy_(on[r][2]), lens.copy_(on[r][3]), q.copy_(on[r][1]), k.copy_(on[r][0])
+        lib.reshape_and_cache(newd[r], newd[r], last[r], k, v)            # the newest keys, just before
+        lib.prefill_weights(q, k, tables, lens, start, xs[r].scale, 32, 5600, window=16, weights_out=got[r])
+    torch.cuda.synchronize(dev)
+    for x, qq, w, t in zip(xs, qs, got, new):
+        for b, n in enumerate(x.lens.tolist()):
+            if n:
+                x.k[int(x.tables[b, (n - 1) // 16]), (n - 1) % 16] = t[b]
+        ww, wb = prefill_reference(x, qq, chunks, 16)
+        within(w, ww, wb, "weights")
+    assert lib.read_device_errors(dev) == 0
