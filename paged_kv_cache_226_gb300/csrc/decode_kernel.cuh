@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kFp8 ? kMinCtasPerSmFp8 : kMin
         int blk = entry(lane);
         int blk_next = entry(32 + lane);
         bool ok = true;
+        int issued = 0;
         for (int i0 = 0; i0 < issue_end && ok; i0 += 32) {
             if (i0 > 0) {
                 blk = blk_next;
@@ -391,8 +392,14 @@ __global__ void __launch_bounds__(kDecodeThreads, kFp8 ? kMinCtasPerSmFp8 : kMin
                                    hh * Lay::kBoxBytes;
                     tma_load_4d(dst, tmap, &full_bar[st], hh * kBoxElems, g, sub, pblk);
                 }
+                issued = i0 + min(k + kBatch, cnt);
             }
         }
+        // The last copy into each stage (lane) has landed before the CTA's
+        // shared memory is given up, also where a consumer has given up on it.
+        if (lane < Lay::kRing && lane < issued &&
+            !mbar_wait(&full_bar[lane], ((issued - 1 - lane) / Lay::kRing) & 1, PA_DECODE_WAIT_LIMIT(p)))
+            flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
         return;
     }
 
