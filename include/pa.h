@@ -441,8 +441,10 @@ int pa_decode_step(const void* q, const void* k, const void* v, const int64_t* s
  * q_out, turned k rows and v rows to cache slot slot_mapping[t], which is
  * treated as in pa_reshape_and_cache (slots that are not negative must
  * differ).  Scaling of the positions for long contexts is part of inv_freq
- * and factor.  Angles are reduced exactly for any int64 position and any
- * inv_freq; the products are in fp32 and each result is rounded once.
+ * and factor.  The angle is taken in turns, whole ones dropped in integers, at
+ * any int64 position and finite inv_freq: it is off by at most 2^-52 of
+ * position * inv_freq, 2^-64 turns per position, and 2^-26 turns; the products
+ * are in fp32 and each result is rounded once.
  * q, k, v: row t starts t * stride elements on, [heads][head_dim] inside (so
  * they may be slices of one projection's output); strides are multiples of 8
  * elements, of at least a row.  q may be null (keys only: q_stride, q_out

@@ -6,9 +6,11 @@
 //   a' = f (a cos t - b sin t),  b' = f (b cos t + a sin t),
 // with pairs (i, i + R/2) or, interleaved, (2i, 2i + 1).  The angle is kept
 // in turns as 64-bit fixed point: inv_freq / 2 pi times 2^64, times the
-// position in wrapping integer arithmetic, so whole turns drop out exactly
-// and the error is 2^-53 of the unreduced angle plus 2^-33 turns, at any
-// position.  Products and sums are in fp32; each result is rounded once.
+// position in wrapping integer arithmetic, so whole turns drop out exactly.
+// The error is that of the turns per position, 2^-52 of the unreduced angle
+// (1 / 2 pi and the product in 64 bits) and 2^-64 turns per position, and the
+// phase's rounding to fp32, 2^-26 turns.  Products and sums are in fp32; each
+// result is rounded once.
 #include <type_traits>
 
 #include "bounded_internal.h"
