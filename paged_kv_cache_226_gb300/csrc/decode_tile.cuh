@@ -33,9 +33,15 @@ constexpr float kRescaleThresholdLog2 = 8.0f;        // rescale when the max gro
 // tok0 + r8 + 8, heads 2c4 and 2c4 + 1, in log2 units.  This one keeps none.
 // Where scores are kept for attention weights, the row sums are of P before
 // its rounding, and P reaches the tensor cores in as many parts as carry its
-// 24 bits: hi + lo in fp16 (also over an E4M3 cache, 32 x 4096 tokens 71.2 us,
-// with P rounded once 69.8), three in bf16 (8 long contexts 228.6 us, with two
-// 226.5).
+// 24 bits: hi + lo in fp16 (also over an E4M3 cache, 32 x 4096 tokens 70.7 us,
+// with P rounded once 68.9), three in bf16.  The tensor cores cut off what a
+// sum cannot hold, always toward zero, so over a 16-bit cache a tile's products
+// are summed from zero and added to the accumulator by a rounding add: into
+// the accumulator itself 4000 tokens cost 5e-6 of O, 16,000 1.5e-5, which
+// shows in 0.4 and 1.3 % of its roundings to bf16 (8 long contexts 229 us;
+// without, and with two parts, 224; 64 ragged 57.6 and 57.0).  An E4M3 cache
+// goes without (74.5 us, the registers spill): its partitions are 1536 tokens
+// at most, unless the caller chose others.
 // fp16 parts end at 2^-25, so the reference is there kept 2^7 below the
 // maximum (P up to 2^15): what is lost is a token's weight below 2^-32 of the
 // largest.
@@ -530,8 +536,16 @@ __device__ __forceinline__ void attend_tile(TileState<D>& s, QFrag&& qfrag,
                               (((chunk & 7) ^ (v_tok & 7)) << 4);
         uint32_t a0, a1, a2, a3;
         ldsm_x4_trans(addr, a0, a1, a2, a3);
+        if constexpr (Emit::kKeep) {             // the smallest parts first
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < kParts; ++i) M::run(s.acc[n], a0, a1, a2, a3, pb[i][0], pb[i][1]);
+            for (int i = kParts - 1; i >= 0; --i) M::run(sum, a0, a1, a2, a3, pb[i][0], pb[i][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s.acc[n][i] += sum[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) M::run(s.acc[n], a0, a1, a2, a3, pb[i][0], pb[i][1]);
+        }
     }
 }
 

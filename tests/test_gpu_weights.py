@@ -547,3 +547,19 @@ def test_window_behind_writers_of_its_inputs(dev):
         ww, wb = prefill_reference(x, qq, chunks, 16)
         within(w, ww, wb, "weights")
     assert lib.read_device_errors(dev) == 0
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+def test_decode_sums_do_not_drift(dev, kind):
+    """8192 tokens of value 1, then the same keys again with value -1, in one
+    partition: the sum climbs and comes back to zero.  Sums that are cut off
+    toward zero lose on both ways, some 2^-25 of the sum at each of 512 tiles
+    per warp, about 2^-17 of all the weight.  Rounded sums are off by sqrt(512)
+    steps of 2^-25 at most, six times that for safety by 2^-18.5 of half the
+    largest sum, which is half the weight of a warp's tiles: 2^-20.5."""
+    n = 8192
+    k = torch.randn(n, generator=torch.Generator().manual_seed(9)).tolist()
+    x = _crafted(kind, k + k, [1.0] * n + [-1.0] * n)
+    x.scale = 0.25
+    got = _first_dim(dev, x, 2 * n)
+    assert bool((got.abs() <= 2.0 ** -20.5).all()), got.tolist()
