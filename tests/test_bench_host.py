@@ -143,3 +143,21 @@ def test_choose_partition_counts_ragged_contexts():
     assert lib.choose_partition(8, 8, 49152, context_lens=torch.tensor(lens)) == 1024
     # empty contexts add no CTAs: 8 x 48 = 384 at 1024 tokens, 8 x 96 = 768 > 729 at 512
     assert lib.choose_partition(8, 8, 49152, context_lens=[0] * 7 + [49152]) == 1024
+
+
+def test_traffic_records_are_of_the_present_sources():
+    """A DRAM-traffic record counts only while the sources it was taken on are
+    unchanged; a line of the benchmark without it says nothing of traffic."""
+    import glob
+    import json
+
+    import bench
+
+    records = sorted(glob.glob(os.path.join(bench.ROOT, "profiles", "*.json")))
+    assert records
+    for path in records:
+        with open(path) as f:
+            r = json.load(f)
+        assert os.path.basename(path) == f"{r['kernel']}_{r['workload']}.json"
+        assert bench.profiled_traffic(r["workload"], r["kernel"], r.get("partition_tokens")) == \
+            r["dram_read"] + r["dram_write"] > 0, f"{path}: take it again with its command"
