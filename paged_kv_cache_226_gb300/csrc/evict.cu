@@ -446,14 +446,15 @@ cudaError_t launch_evict(const EvictParams& params, cudaStream_t stream) {
     // registers (four such CTAs share an SM; 64 x 8 rows of 1040 tokens 11.1
     // us, 128 threads of 16 images 13.8), else 1024, and a cluster that holds
     // the longest context in registers, up to the portable size (16 x 8 rows
-    // of up to 8192 25.3 us with the moves).
+    // of up to 8192 25.3 us with the moves in a graph, 28 called on cold caches).
     const int64_t longest = (int64_t)p.max_blocks_per_seq * p.block_size;
     const bool small = longest <= 256 * kEvictKeys;
     const int64_t ctas = (longest + 1024 * kEvictKeys - 1) / (1024 * kEvictKeys);
     p.cluster = small ? 1 : (int)(ctas < kEvictMaxCluster ? ctas : kEvictMaxCluster);
     // Rows that fill three quarters of the SMs' select CTAs move everything
     // themselves, those done early beside the others' selects (128 rows of up
-    // to 8192 25.3 us, with the move kernel 27.5; 64 rows 22.6 against 19.2).
+    // to 8192, in a graph, 25.3 us, with the move kernel 27.5; 64 rows 22.6
+    // against 19.2).
     const int64_t pairs = (int64_t)p.num_seqs * p.num_kv_heads;
     p.own_moves = !small && p.cluster == 1 && pairs >= 114 ? INT32_MAX : kEvictOwnMoves;
     cudaError_t e = small ? launch_evict_select<256>(p, stream) : launch_evict_select<1024>(p, stream);

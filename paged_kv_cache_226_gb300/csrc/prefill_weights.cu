@@ -34,9 +34,10 @@
 // Rows of Q past a sequence's chunk and K rows past its end may hold anything:
 // they only reach their own lane or column, which is masked.
 //
-// Measured (two chunks of 2048 on contexts of 2048 and 16384, 32 heads over 8,
-// D 128, bf16): 189 us for pass 1 and 199 for pass 2, 1.41 PFLOP/s over both;
-// the tensor pipe is busy 62 % of the time, the exponentials' unit 64 %, issue
+// Measured (chunks of 2048 and 1920 on contexts of 2048 and 16384, 32 heads
+// over 8, D 128, bf16): 189 us for pass 1 and 199 for pass 2, 1.34 PFLOP/s over
+// both, in a graph whose replays find part of K and Q in L2; called back to
+// back on cold caches 412 to 420 us in all.  The tensor pipe is busy 62 % of the time, the exponentials' unit 64 %, issue
 // slots 62 / 60 %: bound by how the four groups of epilogue warps overlap,
 // whose instructions per score are few but for the exponential.
 //

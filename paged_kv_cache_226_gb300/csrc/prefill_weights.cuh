@@ -156,7 +156,7 @@ __device__ __forceinline__ void fold_scores(float& m, float& z, const uint32_t (
 
 // Pass 1: folds a tile's row (keys up to `visible` with kMask) into (m, z).
 // kAhead: 32 columns at a time, the next ones arriving meanwhile, where few
-// tiles are in work at once (a window's pass: 57.1 us in all against 60.9);
+// tiles are in work at once (a window, in a graph: 57.1 us against 60.9);
 // else 64 at once, which takes fewer instructions (large chunks: 190 against
 // 193.5 us).
 template <bool kMask, bool kAhead, typename Release>

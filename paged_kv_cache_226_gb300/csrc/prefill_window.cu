@@ -22,9 +22,11 @@
 // every wait follows the wait for the phase before.
 //
 // Measured (32 queries of 4 heads on each of 16 x 8 rows of 2048 to 8192
-// tokens, D 128, fp16): 54.9 us; a pass streams K in 22 us (7.9 TB/s), and
-// takes some 5 more until its first tile is there and where its CTAs end,
-// which pass 2 overlaps with the end of pass 1 (58.6 us where it does not).
+// tokens, D 128, fp16): 60.4 us a call on cold caches.  Alone and cold the
+// passes take 36.5 and 35.6 us, 175 MB each at 62 % of the DRAM peak, some 5 us
+// of which pass before the first tile is there and where the CTAs end; pass 2
+// overlaps that with the end of pass 1 (replays of a graph, part of K in L2:
+// 54.8 us, and 58.6 where it does not).
 #include <algorithm>
 
 #include "prefill_weights.cuh"
