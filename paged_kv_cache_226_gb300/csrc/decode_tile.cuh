@@ -40,8 +40,9 @@ constexpr float kRescaleThresholdLog2 = 8.0f;        // rescale when the max gro
 // the accumulator itself 4000 tokens cost 5e-6 of O, 16,000 1.5e-5, which
 // shows in 0.4 and 1.3 % of its roundings to bf16 (8 long contexts 229 us;
 // without, and with two parts, 224; 64 ragged 57.6 and 57.0).  An E4M3 cache
-// goes without (74.5 us, the registers spill): its partitions are 1536 tokens
-// at most, unless the caller chose others.
+// goes without (74.5 us, the registers spill): its partitions are some 1500
+// tokens at most (2048 from contexts of half a million on), where that costs
+// 2e-6, unless the caller chose longer ones.
 // fp16 parts end at 2^-25, so the reference is there kept 2^7 below the
 // maximum (P up to 2^15): what is lost is a token's weight below 2^-32 of the
 // largest.
