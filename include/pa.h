@@ -72,6 +72,7 @@ typedef enum { PA_FP16 = 0, PA_BF16 = 1 } pa_dtype;
 #define PA_DEVERR_WAIT_TIMEOUT   0x1  /* a pipeline wait gave up after ~1 s */
 #define PA_DEVERR_BAD_CONTEXT    0x2  /* a context length was clamped */
 #define PA_DEVERR_BAD_SLOT       0x4  /* a slot past the pool was skipped */
+#define PA_DEVERR_BAD_INDEX      0x8  /* an axis, a parent or a path entry was set aside */
 
 typedef struct {
     int32_t num_seqs;
@@ -564,6 +565,131 @@ int pa_evict_fp8(void* k_cache, void* v_cache, const int32_t* block_tables,
                  int32_t trigger, int32_t sinks, int32_t recent, float* weights_out,
                  int32_t* positions_out, int32_t* new_lens, void* workspace,
                  size_t workspace_bytes, const pa_shape* shp, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Speculative decoding: a tree of drafted tokens per sequence
+ * ---------------------------------------------------------------------------
+ * The pages leave speculative decoding to the engine; what it asks of a paged
+ * cache is below.  In a verification step sequence b has C_b = query_start[b + 1] - query_start[b] nodes, the last
+ * C_b of its L_b cached tokens: node i is row query_start[b] + i of the batch
+ * and stands at cache index L_b - C_b + i.  Node 0 is the sequence's newest
+ * token, the others are drafted after it: parents[row] < i is the node (of the
+ * same sequence) that node i follows, negative: the context itself.  A parent
+ * that is not below its node counts as negative and sets PA_DEVERR_BAD_INDEX.
+ * Sequences have at most PA_TREE_NODES nodes; more are cut off and set
+ * PA_DEVERR_BAD_CONTEXT, as do a C_b below 0 or above L_b and rows outside
+ * [0, num_tokens).  A step: pa_norm_rope_and_cache (or pa_rope_and_cache) and
+ * pa_tree_attention in every layer, then pa_accept_tree and pa_commit_path.
+ */
+#define PA_TREE_NODES 128
+
+/*
+ * pa_norm_rope_and_cache: pa_rope_and_cache with the heads of q and k
+ * normalised first and positions on several axes.  For every head x of q or k
+ *   y[d] = weight[d] * x[d] / sqrt(mean_d(x[d]^2) + eps)
+ * in fp32, not rounded before it is turned; q_weight and k_weight [head_dim]
+ * of type T, null: ones.  Pair i turns by positions[axes[i]][t] * inv_freq[i]:
+ * positions is [num_axes][num_tokens] int64, axes [rotary_dim / 2] int32
+ * (null: all 0), 1 <= num_axes <= 8; an axis outside them counts as 0 and sets
+ * PA_DEVERR_BAD_INDEX.  eps must be finite and not negative.  Everything else
+ * is as in pa_rope_and_cache.
+ */
+int pa_norm_rope_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, const void* q_weight,
+                           const void* k_weight, float eps, const int64_t* positions,
+                           int32_t num_axes, const int32_t* axes, const int64_t* slot_mapping,
+                           const float* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                           float factor, void* q_out, int64_t q_out_stride, void* k_cache,
+                           void* v_cache, int64_t num_tokens, const pa_shape* shp, void* stream);
+
+/* pa_norm_rope_and_cache into an E4M3 cache, quantised from fp32. */
+int pa_norm_rope_and_cache_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                               const void* v, int64_t v_stride, const void* q_weight,
+                               const void* k_weight, float eps, const int64_t* positions,
+                               int32_t num_axes, const int32_t* axes, const int64_t* slot_mapping,
+                               const float* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                               float factor, void* q_out, int64_t q_out_stride, void* k_cache,
+                               void* v_cache, int64_t num_tokens, float k_scale, float v_scale,
+                               const pa_shape* shp, void* stream);
+
+/*
+ * pa_tree_attention: attention of the trees' nodes over the cache, which
+ * holds their K and V already.  Node i of sequence b sees the L_b - C_b tokens
+ * before the tree, its ancestors and itself:
+ *   out[row][h] = sum_j p_j V_j,  p = softmax_j(scale * q[row][h] . K_j).
+ * q, out [num_tokens][num_q_heads][head_dim]; rows behind the last sequence
+ * are not written.  parents [num_tokens] int32, null: every node follows the
+ * one before it (a line of drafted tokens, or the chunks of pa_prefill).
+ * scale must be finite and > 0.  max_query_len >= every C_b, at most
+ * PA_TREE_NODES (else PA_ERR_UNSUPPORTED); max_context_len >= every L_b;
+ * values outside these bounds are clamped and set PA_DEVERR_BAD_CONTEXT.
+ * Softmax statistics, p and the sums are in fp32, and out is
+ * rounded once.  A token that a node does not see has no part in its row, also
+ * where its K or V is not finite.
+ * workspace: device memory of at least pa_tree_attention_workspace_size bytes,
+ * 16-byte aligned, no initial contents; calls that overlap on the GPU must
+ * not share it.  One or two launches.
+ */
+size_t pa_tree_attention_workspace_size(const pa_shape* shp, int32_t max_query_len,
+                                        int32_t max_context_len);
+int pa_tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                      const int32_t* block_tables, const int32_t* context_lens,
+                      const int32_t* query_start, const int32_t* parents, float scale,
+                      int64_t num_tokens, int32_t max_query_len, int32_t max_context_len,
+                      void* workspace, size_t workspace_bytes, void* out, const pa_shape* shp,
+                      void* stream);
+
+/* pa_tree_attention over an E4M3 cache. */
+int pa_tree_attention_fp8(const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* block_tables, const int32_t* context_lens,
+                          const int32_t* query_start, const int32_t* parents, float scale,
+                          float k_scale, float v_scale, int64_t num_tokens, int32_t max_query_len,
+                          int32_t max_context_len, void* workspace, size_t workspace_bytes,
+                          void* out, const pa_shape* shp, void* stream);
+
+/*
+ * pa_accept_tree: the longest path of drafted tokens that the model agrees
+ * with.  target[row] is the token that the model gives after node `row`,
+ * draft[row] the token of the node itself.  Node 0 is accepted; any other with
+ * a parent is where its parent is and draft[node] = target[parent].  Of the
+ * accepted nodes the deepest, the lowest among equals, ends the path:
+ *   path[b][0 .. path_lens[b] - 1]  its ancestors and itself, from node 0 on
+ *   path[b][path_lens[b] ..]        -1, up to max_query_len
+ *   next[b]                         target of the path's end
+ * A sequence without nodes gets length 0 and next -1.  draft, target, parents:
+ * [num_tokens]; path [num_seqs][max_query_len], 1 <= max_query_len <=
+ * PA_TREE_NODES.  One launch.
+ */
+int pa_accept_tree(const int64_t* draft, const int64_t* target, const int32_t* parents,
+                   const int32_t* query_start, int32_t num_seqs, int64_t num_tokens,
+                   int32_t max_query_len, int32_t* path, int32_t* path_lens, int64_t* next,
+                   void* stream);
+
+/*
+ * pa_commit_path: keeps of each tree the path's nodes, in the caches of all
+ * layers.  With base = L_b - C_b the K and V rows of node path[b][j] move to
+ * cache index base + j, and
+ *   new_lens[b] = base + path_lens[b].
+ * A path is ascending (as pa_accept_tree gives it) within [0, C_b); one that
+ * is not, or longer than C_b, sets PA_DEVERR_BAD_INDEX, and its sequence is
+ * left as it is (new_lens[b] = L_b).  path [num_seqs][path_stride] int32.
+ * k_caches, v_caches: host arrays of num_layers (at most 1024) device pointers,
+ * one cache pair per layer, all of the shape shp and of the same block tables;
+ * no cache may be listed twice.  The blocks that hold a tree must not be shared with
+ * another sequence.  A block id outside the pool sets PA_DEVERR_BAD_CONTEXT
+ * and its rows are not moved.  new_lens must not be an input array.  One
+ * launch for every 64 layers.  pa_commit_path_fp8: the same on E4M3 caches.
+ */
+int pa_commit_path(void* const* k_caches, void* const* v_caches, int32_t num_layers,
+                   const int32_t* block_tables, const int32_t* context_lens,
+                   const int32_t* query_start, const int32_t* path, int32_t path_stride,
+                   const int32_t* path_lens, int32_t* new_lens, const pa_shape* shp, void* stream);
+int pa_commit_path_fp8(void* const* k_caches, void* const* v_caches, int32_t num_layers,
+                       const int32_t* block_tables, const int32_t* context_lens,
+                       const int32_t* query_start, const int32_t* path, int32_t path_stride,
+                       const int32_t* path_lens, int32_t* new_lens, const pa_shape* shp,
+                       void* stream);
 
 /* Static description of a status code. */
 const char* pa_status_string(int status);

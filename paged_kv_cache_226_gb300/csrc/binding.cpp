@@ -1,4 +1,5 @@
-// Python binding of the bounded-cache operators (CPython and torch C++ API).
+// Python binding of the bounded-cache operators and of those of speculative
+// decoding (CPython and torch C++ API).
 //
 // A layer makes three of these calls per step and the small ones are a launch
 // or two of 2 to 6 us, so what a call costs on the host is what it costs.
@@ -30,6 +31,7 @@
 #include <cstdint>
 #include <limits>
 #include <string>
+#include <vector>
 
 #include "pa.h"
 
@@ -55,6 +57,14 @@ struct Entries {
     decltype(&pa_evict_workspace_size) evict_workspace_size;
     decltype(&pa_evict) evict;
     decltype(&pa_evict_fp8) evict_fp8;
+    decltype(&pa_norm_rope_and_cache) norm_rope_and_cache;
+    decltype(&pa_norm_rope_and_cache_fp8) norm_rope_and_cache_fp8;
+    decltype(&pa_tree_attention_workspace_size) tree_attention_workspace_size;
+    decltype(&pa_tree_attention) tree_attention;
+    decltype(&pa_tree_attention_fp8) tree_attention_fp8;
+    decltype(&pa_accept_tree) accept_tree;
+    decltype(&pa_commit_path) commit_path;
+    decltype(&pa_commit_path_fp8) commit_path_fp8;
 };
 
 const Entries* g_entries = nullptr;
@@ -90,6 +100,14 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     find(handle, "pa_evict_workspace_size", e.evict_workspace_size);
     find(handle, "pa_evict", e.evict);
     find(handle, "pa_evict_fp8", e.evict_fp8);
+    find(handle, "pa_norm_rope_and_cache", e.norm_rope_and_cache);
+    find(handle, "pa_norm_rope_and_cache_fp8", e.norm_rope_and_cache_fp8);
+    find(handle, "pa_tree_attention_workspace_size", e.tree_attention_workspace_size);
+    find(handle, "pa_tree_attention", e.tree_attention);
+    find(handle, "pa_tree_attention_fp8", e.tree_attention_fp8);
+    find(handle, "pa_accept_tree", e.accept_tree);
+    find(handle, "pa_commit_path", e.commit_path);
+    find(handle, "pa_commit_path_fp8", e.commit_path_fp8);
     g_entries = new Entries(e);
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
@@ -163,6 +181,14 @@ const Tensor& per_sequence(PyObject* o, const char* name, int64_t n, int index) 
     if (t.dim() != 1 || t.size(0) != n)
         refuse(PyExc_ValueError, std::string(name) + " must be an int32 [" + std::to_string(n) + "]");
     return t;
+}
+
+// An array of one entry per token.
+const void* per_token(PyObject* o, const char* name, at::ScalarType dtype, int64_t n, int index) {
+    const Tensor& t = dense(o, name, dtype, index);
+    if (t.dim() != 1 || t.size(0) != n)
+        refuse(PyExc_ValueError, std::string(name) + " must be [" + std::to_string(n) + "]");
+    return t.data_ptr();
 }
 
 // [T][heads][dim], the heads of a token contiguous.
@@ -317,6 +343,69 @@ void expect(Py_ssize_t got, Py_ssize_t want) {
     if (got != want) refuse(PyExc_TypeError, "expected " + std::to_string(want) + " arguments");
 }
 
+// The arguments that rotary writes share, checked: rows of q, k and v, slots
+// and frequencies, and where the turned q goes.
+struct RopeCall {
+    const Pools& p;
+    at::ScalarType dt;
+    Rows k, v, q{nullptr, 0, 0}, out{nullptr, 0, 0};
+    const int64_t* slots;
+    const float* inv_freq;
+    int64_t T, half, hq = 0;
+    int interleaved;
+    float factor;
+    bool given, make;
+    Tensor made;
+
+    RopeCall(const Pools& pools, PyObject* qo, PyObject* ko, PyObject* vo, PyObject* so, PyObject* fo,
+             PyObject* oo, PyObject* io, PyObject* mo)
+        : p(pools), dt(tensor(ko, "k").scalar_type()) {
+        if (!is_16bit(dt) || !(p.fp8 || dt == p.dtype))
+            refuse(PyExc_TypeError, "k must have the cache's 16-bit dtype, got " + dtype_name(dt));
+        k = rows(ko, "k", p.heads, p.dim, dt, p.index);
+        v = rows(vo, "v", p.heads, p.dim, dt, p.index);
+        const Tensor& slot = dense(so, "slot_mapping", at::kLong, p.index);
+        const Tensor& inv = dense(fo, "inv_freq", at::kFloat, p.index);
+        T = q.tokens = out.tokens = k.tokens;
+        if (v.tokens != T || slot.dim() != 1 || slot.size(0) != T || inv.dim() != 1)
+            refuse(PyExc_ValueError, "v, positions and slot_mapping must have a row per token of k, "
+                                     "inv_freq one dimension");
+        slots = (const int64_t*)slot.data_ptr(), inv_freq = (const float*)inv.data_ptr();
+        half = inv.size(0);
+        given = qo != Py_None, make = given && oo == Py_None;
+        if (given) {
+            const Tensor& qt = tensor(qo, "q");
+            hq = qt.dim() == 3 ? qt.size(1) : 0;
+            q = rows(qo, "q", hq, p.dim, dt, p.index);
+            if (make)
+                out.stride = hq * p.dim;
+            else
+                out = rows(oo, "q_out", hq, p.dim, dt, p.index);
+            if (q.tokens != T || out.tokens != T)
+                refuse(PyExc_ValueError, "q and q_out must have a row per token of k");
+        } else if (oo != Py_None) {
+            refuse(PyExc_ValueError, "q_out needs q");
+        }
+        interleaved = PyObject_IsTrue(io);
+        if (interleaved < 0) throw python_error();
+        factor = real(mo);
+    }
+    int32_t rotary_dim() const { return (int32_t)std::min(2 * half, kMaxInt32); }
+    // the current stream, with q_out allocated on it if the call makes one
+    void* begin() {
+        if (make) {
+            made = at::empty({T, hq, p.dim}, p.options(dt));
+            out.data = made.data_ptr();
+        }
+        return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)p.index).stream();
+    }
+    PyObject* result(int status, PyObject* oo) {
+        if (status != PA_OK) return refused(status);
+        if (!given) Py_RETURN_NONE;
+        return same_or_new(oo, made);
+    }
+};
+
 // (q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cache, q_out,
 //  interleaved, factor, k_scale, v_scale) -> q_out
 PyObject* rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -325,63 +414,84 @@ PyObject* rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Entries& lib = entries();
     const Pools p(a[6], a[7]);
     const Scales s(p.fp8, a[11], a[12]);
-    const at::ScalarType dt = tensor(a[1], "k").scalar_type();
-    if (!is_16bit(dt) || !(p.fp8 || dt == p.dtype))
-        refuse(PyExc_TypeError, "k must have the cache's 16-bit dtype, got " + dtype_name(dt));
-    const Rows k = rows(a[1], "k", p.heads, p.dim, dt, p.index);
-    const Rows v = rows(a[2], "v", p.heads, p.dim, dt, p.index);
+    RopeCall c(p, a[0], a[1], a[2], a[4], a[5], a[8], a[9], a[10]);
     const Tensor& pos = dense(a[3], "positions", at::kLong, p.index);
-    const Tensor& slot = dense(a[4], "slot_mapping", at::kLong, p.index);
-    const Tensor& inv = dense(a[5], "inv_freq", at::kFloat, p.index);
-    const int64_t T = k.tokens;
-    if (v.tokens != T || pos.dim() != 1 || pos.size(0) != T || slot.dim() != 1 || slot.size(0) != T ||
-        inv.dim() != 1)
-        refuse(PyExc_ValueError, "v, positions and slot_mapping must have a row per token of k, "
-                                 "inv_freq one dimension");
-    Rows q{nullptr, T, 0}, out{nullptr, T, 0};
-    int64_t hq = 0;
-    const bool make = a[0] != Py_None && a[8] == Py_None;
-    if (a[0] != Py_None) {
-        const Tensor& qt = tensor(a[0], "q");
-        hq = qt.dim() == 3 ? qt.size(1) : 0;
-        q = rows(a[0], "q", hq, p.dim, dt, p.index);
-        if (make)
-            out.stride = hq * p.dim;
-        else
-            out = rows(a[8], "q_out", hq, p.dim, dt, p.index);
-        if (q.tokens != T || out.tokens != T)
-            refuse(PyExc_ValueError, "q and q_out must have a row per token of k");
-    } else if (a[8] != Py_None) {
-        refuse(PyExc_ValueError, "q_out needs q");
-    }
-    const int interleaved = PyObject_IsTrue(a[9]);
-    if (interleaved < 0) throw python_error();
-    const float factor = real(a[10]);
-    const pa_shape shp = p.shape(0, hq, 1, dt);
-    Tensor made;
+    if (pos.dim() != 1 || pos.size(0) != c.T)
+        refuse(PyExc_ValueError, "positions must have a row per token of k");
+    const pa_shape shp = p.shape(0, c.hq, 1, c.dt);
     int status;
     {
         Unlocked u;
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.index);
-        if (make) {
-            made = at::empty({T, hq, p.dim}, p.options(dt));
-            out.data = made.data_ptr();
-        }
-        void* stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)p.index).stream();
+        void* stream = c.begin();
         const int64_t* pp = (const int64_t*)pos.data_ptr();
-        const int64_t* sp = (const int64_t*)slot.data_ptr();
-        const float* ip = (const float*)inv.data_ptr();
-        const int32_t rot = (int32_t)std::min(2 * inv.size(0), kMaxInt32);
-        status = p.fp8 ? lib.rope_and_cache_fp8(q.data, q.stride, k.data, k.stride, v.data, v.stride, pp,
-                                                sp, ip, rot, interleaved, factor, (void*)out.data,
-                                                out.stride, p.k, p.v, T, s.k, s.v, &shp, stream)
-                       : lib.rope_and_cache(q.data, q.stride, k.data, k.stride, v.data, v.stride, pp, sp,
-                                            ip, rot, interleaved, factor, (void*)out.data, out.stride,
-                                            p.k, p.v, T, &shp, stream);
+        status = p.fp8 ? lib.rope_and_cache_fp8(c.q.data, c.q.stride, c.k.data, c.k.stride, c.v.data,
+                                                c.v.stride, pp, c.slots, c.inv_freq, c.rotary_dim(),
+                                                c.interleaved, c.factor, (void*)c.out.data, c.out.stride,
+                                                p.k, p.v, c.T, s.k, s.v, &shp, stream)
+                       : lib.rope_and_cache(c.q.data, c.q.stride, c.k.data, c.k.stride, c.v.data,
+                                            c.v.stride, pp, c.slots, c.inv_freq, c.rotary_dim(),
+                                            c.interleaved, c.factor, (void*)c.out.data, c.out.stride,
+                                            p.k, p.v, c.T, &shp, stream);
     }
-    if (status != PA_OK) return refused(status);
-    if (a[0] == Py_None) Py_RETURN_NONE;
-    return same_or_new(a[8], made);
+    return c.result(status, a[8]);
+    END_HANDLE_TH_ERRORS
+}
+
+// A norm's weights, or null.
+const void* norm_weight(PyObject* o, const char* name, const RopeCall& c) {
+    if (o == Py_None) return nullptr;
+    const Tensor& t = dense(o, name, c.dt, c.p.index);
+    if (t.dim() != 1 || t.size(0) != c.p.dim)
+        refuse(PyExc_ValueError, std::string(name) + " must be [" + std::to_string(c.p.dim) + "]");
+    return t.data_ptr();
+}
+
+// (q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cache, q_weight,
+//  k_weight, eps, axes, q_out, interleaved, factor, k_scale, v_scale) -> q_out
+PyObject* norm_rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 17);
+    const Entries& lib = entries();
+    const Pools p(a[6], a[7]);
+    const Scales s(p.fp8, a[15], a[16]);
+    RopeCall c(p, a[0], a[1], a[2], a[4], a[5], a[12], a[13], a[14]);
+    const void* qw = norm_weight(a[8], "q_weight", c);
+    const void* kw = norm_weight(a[9], "k_weight", c);
+    const float eps = real(a[10]);
+    const Tensor& pos = dense(a[3], "positions", at::kLong, p.index);
+    const bool several = pos.dim() == 2;
+    if ((pos.dim() != 1 && !several) || pos.size(several) != c.T || (several && pos.size(0) > kMaxInt32))
+        refuse(PyExc_ValueError, "positions must be [num_tokens] or [axes][num_tokens]");
+    if (several != (a[11] != Py_None))
+        refuse(PyExc_ValueError, "axes belong to positions of several axes");
+    const int32_t* axes = nullptr;
+    if (several) {
+        const Tensor& t = dense(a[11], "axes", at::kInt, p.index);
+        if (t.dim() != 1 || t.size(0) != c.half)
+            refuse(PyExc_ValueError, "axes must have an entry per entry of inv_freq");
+        axes = (const int32_t*)t.data_ptr();
+    }
+    const pa_shape shp = p.shape(0, c.hq, 1, c.dt);
+    int status;
+    {
+        Unlocked u;
+        c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.index);
+        void* stream = c.begin();
+        const int64_t* pp = (const int64_t*)pos.data_ptr();
+        const int32_t num_axes = several ? (int32_t)pos.size(0) : 1;
+        status = p.fp8 ? lib.norm_rope_and_cache_fp8(c.q.data, c.q.stride, c.k.data, c.k.stride, c.v.data,
+                                                     c.v.stride, qw, kw, eps, pp, num_axes, axes, c.slots,
+                                                     c.inv_freq, c.rotary_dim(), c.interleaved, c.factor,
+                                                     (void*)c.out.data, c.out.stride, p.k, p.v, c.T, s.k,
+                                                     s.v, &shp, stream)
+                       : lib.norm_rope_and_cache(c.q.data, c.q.stride, c.k.data, c.k.stride, c.v.data,
+                                                 c.v.stride, qw, kw, eps, pp, num_axes, axes, c.slots,
+                                                 c.inv_freq, c.rotary_dim(), c.interleaved, c.factor,
+                                                 (void*)c.out.data, c.out.stride, p.k, p.v, c.T, &shp,
+                                                 stream);
+    }
+    return c.result(status, a[12]);
     END_HANDLE_TH_ERRORS
 }
 
@@ -574,6 +684,167 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// The batch's int32 [num_seqs + 1] starts.
+const int32_t* starts(PyObject* o, int64_t seqs, int index) {
+    const Tensor& t = dense(o, "query_start", at::kInt, index);
+    if (t.dim() != 1 || t.size(0) != seqs + 1)
+        refuse(PyExc_ValueError, "query_start must be [num_seqs + 1]");
+    return (const int32_t*)t.data_ptr();
+}
+
+// (q, k_cache, v_cache, block_tables, context_lens, query_start, parents,
+//  scale, max_query_len, max_context_len, out, workspace, k_scale, v_scale)
+// -> out
+PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 14);
+    const Entries& lib = entries();
+    const Pools p(a[1], a[2]);
+    const Scales s(p.fp8, a[12], a[13]);
+    const Batch b(a[3], a[4], p.index);
+    const at::ScalarType dt = tensor(a[0], "q").scalar_type();
+    if (!is_16bit(dt) || !(p.fp8 || dt == p.dtype))
+        refuse(PyExc_TypeError, "q must have the cache's 16-bit dtype, got " + dtype_name(dt));
+    const Tensor& q = dense(a[0], "q", dt, p.index);
+    if (q.dim() != 3 || q.size(2) != p.dim)
+        refuse(PyExc_ValueError, "q must be [num_tokens][num_q_heads][head_dim]");
+    const int32_t* start = starts(a[5], b.seqs, p.index);
+    const int32_t* parents = nullptr;
+    if (a[6] != Py_None) parents = (const int32_t*)per_token(a[6], "parents", at::kInt, q.size(0), p.index);
+    const float scale = real(a[7]);
+    const int32_t largest = int32(a[8], "max_query_len"), longest = int32(a[9], "max_context_len");
+    void* out = nullptr;
+    if (a[10] != Py_None) {
+        const Tensor& t = dense(a[10], "out", dt, p.index);
+        if (t.sizes() != q.sizes()) refuse(PyExc_ValueError, "out must have q's shape");
+        out = t.data_ptr();
+    }
+    Workspace ws(a[11], p.index);
+    const pa_shape shp = p.shape(b.seqs, q.size(1), b.blocks, dt);
+    Tensor made;
+    int status;
+    {
+        Unlocked u;
+        c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.index);
+        // 0 bytes: the entry point says what it refuses
+        ws.need(lib.tree_attention_workspace_size(&shp, largest, longest));
+        if (a[10] == Py_None) {
+            made = at::empty(q.sizes(), p.options(dt));
+            out = made.data_ptr();
+        }
+        void* stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)p.index).stream();
+        status = p.fp8 ? lib.tree_attention_fp8(q.data_ptr(), p.k, p.v, b.tables, b.lens, start, parents, scale,
+                                                s.k, s.v, q.size(0), largest, longest, ws.data, ws.bytes, out,
+                                                &shp, stream)
+                       : lib.tree_attention(q.data_ptr(), p.k, p.v, b.tables, b.lens, start, parents, scale,
+                                            q.size(0), largest, longest, ws.data, ws.bytes, out, &shp, stream);
+        ws.own.clear();
+    }
+    if (status != PA_OK) return refused(status);
+    return same_or_new(a[10], made);
+    END_HANDLE_TH_ERRORS
+}
+
+// (draft_tokens, target_tokens, parents, query_start, max_query_len)
+// -> (path, path_lens, next_tokens)
+PyObject* accept_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 5);
+    const Entries& lib = entries();
+    const Tensor& draft = dense(a[0], "draft_tokens");
+    if (draft.scalar_type() != at::kLong || draft.dim() != 1)
+        refuse(PyExc_TypeError, "draft_tokens must be an int64 [num_tokens]");
+    const int index = (int)draft.get_device();
+    const int64_t T = draft.size(0);
+    const int64_t* target = (const int64_t*)per_token(a[1], "target_tokens", at::kLong, T, index);
+    const int32_t* parents = nullptr;
+    if (a[2] != Py_None) parents = (const int32_t*)per_token(a[2], "parents", at::kInt, T, index);
+    const Tensor& start = dense(a[3], "query_start", at::kInt, index);
+    if (start.dim() != 1 || start.size(0) < 1 || start.size(0) - 1 > kMaxInt32)
+        refuse(PyExc_ValueError, "query_start must be [num_seqs + 1]");
+    const int64_t seqs = start.size(0) - 1;
+    const int32_t largest = int32(a[4], "max_query_len");
+    Tensor path, lens, next;
+    int status;
+    {
+        Unlocked u;
+        c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
+        const auto on = at::TensorOptions().device(at::kCUDA, (c10::DeviceIndex)index);
+        if (largest >= 1 && largest <= PA_TREE_NODES) {
+            path = at::empty({seqs, largest}, on.dtype(at::kInt));
+            lens = at::empty({seqs}, on.dtype(at::kInt));
+            next = at::empty({seqs}, on.dtype(at::kLong));
+        }
+        void* stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream();
+        status = lib.accept_tree((const int64_t*)draft.data_ptr(), target, parents, (const int32_t*)start.data_ptr(),
+                                 (int32_t)seqs, T, largest, path.defined() ? (int32_t*)path.data_ptr() : nullptr,
+                                 path.defined() ? (int32_t*)lens.data_ptr() : nullptr,
+                                 path.defined() ? (int64_t*)next.data_ptr() : nullptr, stream);
+    }
+    if (status != PA_OK) return refused(status);
+    PyObject* first = pair(THPVariable_Wrap(std::move(path)), THPVariable_Wrap(std::move(lens)));
+    PyObject* last = THPVariable_Wrap(std::move(next));
+    PyObject* t = first && last ? PyTuple_Pack(3, PyTuple_GET_ITEM(first, 0), PyTuple_GET_ITEM(first, 1), last) : nullptr;
+    Py_XDECREF(first);
+    Py_XDECREF(last);
+    return t;
+    END_HANDLE_TH_ERRORS
+}
+
+// (k_caches, v_caches, block_tables, context_lens, query_start, path,
+//  path_lens, new_lens) -> new_lens.  k_caches, v_caches: tuples, or a cache each.
+PyObject* commit_path(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 8);
+    const Entries& lib = entries();
+    PyObject* const* ks = a;
+    PyObject* const* vs = a + 1;
+    Py_ssize_t layers = 1;
+    if (PyTuple_Check(a[0]) || PyTuple_Check(a[1])) {
+        if (!PyTuple_Check(a[0]) || !PyTuple_Check(a[1]) || PyTuple_GET_SIZE(a[0]) != PyTuple_GET_SIZE(a[1]))
+            refuse(PyExc_ValueError, "k_caches and v_caches must have a cache for every layer");
+        layers = PyTuple_GET_SIZE(a[0]);
+        if (layers == 0) refuse(PyExc_ValueError, "k_caches must not be empty");
+        ks = &PyTuple_GET_ITEM(a[0], 0), vs = &PyTuple_GET_ITEM(a[1], 0);
+    }
+    const Pools p(ks[0], vs[0]);
+    std::vector<void*> k(layers, p.k), v(layers, p.v);
+    const at::IntArrayRef sizes = THPVariable_Unpack(ks[0]).sizes();
+    for (Py_ssize_t i = 1; i < layers; ++i) {
+        const Tensor& kt = dense(ks[i], "k_cache", THPVariable_Unpack(ks[0]).scalar_type(), p.index);
+        const Tensor& vt = dense(vs[i], "v_cache", THPVariable_Unpack(ks[0]).scalar_type(), p.index);
+        if (kt.sizes() != sizes || vt.sizes() != sizes)
+            refuse(PyExc_ValueError, "the caches of all layers must have the same shape");
+        k[i] = kt.data_ptr(), v[i] = vt.data_ptr();
+    }
+    const Batch b(a[2], a[3], p.index);
+    const int32_t* start = starts(a[4], b.seqs, p.index);
+    const Tensor& path = dense(a[5], "path", at::kInt, p.index);
+    if (path.dim() != 2 || path.size(0) != b.seqs || path.size(1) > kMaxInt32)
+        refuse(PyExc_ValueError, "path must be [num_seqs][nodes]");
+    const int32_t* lens = (const int32_t*)per_sequence(a[6], "path_lens", b.seqs, p.index).data_ptr();
+    int32_t* fresh = nullptr;
+    if (a[7] != Py_None) fresh = (int32_t*)per_sequence(a[7], "new_lens", b.seqs, p.index).data_ptr();
+    const pa_shape shp = p.shape(b.seqs, p.heads, b.blocks, p.fp8 ? at::kHalf : p.dtype);
+    Tensor made;
+    int status;
+    {
+        Unlocked u;
+        c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.index);
+        if (a[7] == Py_None) {
+            made = at::empty({b.seqs}, p.options(at::kInt));
+            fresh = (int32_t*)made.data_ptr();
+        }
+        void* stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)p.index).stream();
+        status = (p.fp8 ? lib.commit_path_fp8 : lib.commit_path)(
+            k.data(), v.data(), (int32_t)std::min<Py_ssize_t>(layers, kMaxInt32), b.tables, b.lens, start,
+            (const int32_t*)path.data_ptr(), (int32_t)path.size(1), lens, fresh, &shp, stream);
+    }
+    if (status != PA_OK) return refused(status);
+    return same_or_new(a[7], made);
+    END_HANDLE_TH_ERRORS
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 constexpr PyMethodDef method(const char* name) {
     return {name, (PyCFunction)(void (*)())F, METH_FASTCALL, nullptr};
@@ -581,9 +852,11 @@ constexpr PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {method<rope_and_cache>("rope_and_cache"), method<decode_weights>("decode_weights"),
                          method<prefill_weights>("prefill_weights"), method<evict>("evict"), method<bind>("bind"),
+                         method<norm_rope_and_cache>("norm_rope_and_cache"), method<tree_attention>("tree_attention"),
+                         method<accept_tree>("accept_tree"), method<commit_path>("commit_path"),
                          {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_native", "Binding of the bounded-cache operators.", -1,
+PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_native", "Binding of the bounded-cache and speculative-decoding operators.", -1,
                           methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

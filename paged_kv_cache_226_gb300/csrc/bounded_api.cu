@@ -17,11 +17,20 @@ int finish(cudaError_t e) {
     return PA_ERR_CUDA;
 }
 
+// What a rotary write behind a norm has besides.
+struct Norm {
+    const void *q_weight, *k_weight;
+    float eps;
+    int32_t num_axes;
+    const int32_t* axes;
+};
+
+// norm null: pa_rope_and_cache
 int rope_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                    int64_t v_stride, const int64_t* positions, const int64_t* slot_mapping,
                    const float* inv_freq, int32_t rotary_dim, int32_t interleaved, float factor,
                    void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache,
-                   int64_t num_tokens, bool fp8, float k_scale, float v_scale,
+                   int64_t num_tokens, bool fp8, float k_scale, float v_scale, const Norm* norm,
                    const pa_shape* shp, void* stream) {
     int st = pa::check_shape(shp, false);
     if (st != PA_OK) return st;
@@ -29,6 +38,9 @@ int rope_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_str
     if (num_tokens < 0 || num_tokens > 0x7fffffffll) return PA_ERR_INVALID_ARG;
     if (rotary_dim < 0 || rotary_dim > shp->head_dim || (interleaved != 0 && interleaved != 1) ||
         !std::isfinite(factor))
+        return PA_ERR_INVALID_ARG;
+    if (norm && (norm->num_axes < 1 || norm->num_axes > 8 || !(norm->eps >= 0.f) || !std::isfinite(norm->eps) ||
+                 !aligned16(norm->q_weight) || !aligned16(norm->k_weight) || !aligned4(norm->axes)))
         return PA_ERR_INVALID_ARG;
     if (rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
     if (q && shp->num_q_heads <= 0) return PA_ERR_INVALID_ARG;
@@ -58,8 +70,12 @@ int rope_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_str
     p.num_tokens = num_tokens, p.num_slots = shp->num_blocks * shp->block_size;
     p.num_q_heads = q ? shp->num_q_heads : 0, p.num_kv_heads = shp->num_kv_heads;
     p.rotary_dim = rotary_dim, p.factor = factor, p.k_scale = k_scale, p.v_scale = v_scale;
-    return finish(pa::launch_rope_and_cache(shp->dtype, shp->head_dim, fp8, interleaved != 0, p,
-                                            static_cast<cudaStream_t>(stream)));
+    if (norm) {
+        p.q_weight = norm->q_weight, p.k_weight = norm->k_weight, p.eps = norm->eps;
+        p.axes = norm->axes, p.num_axes = norm->num_axes;
+    }
+    return finish(pa::launch_rope_and_cache(shp->dtype, shp->head_dim, fp8, interleaved != 0, norm != nullptr,
+                                            p, static_cast<cudaStream_t>(stream)));
 }
 
 // Parts of the decode-weights workspace, each 256-byte aligned.
@@ -224,7 +240,7 @@ int pa_rope_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_
                       void* stream) {
     return rope_and_cache(q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping, inv_freq,
                           rotary_dim, interleaved, factor, q_out, q_out_stride, k_cache, v_cache,
-                          num_tokens, false, 1.f, 1.f, shp, stream);
+                          num_tokens, false, 1.f, 1.f, nullptr, shp, stream);
 }
 
 int pa_rope_and_cache_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -235,7 +251,34 @@ int pa_rope_and_cache_fp8(const void* q, int64_t q_stride, const void* k, int64_
                           float v_scale, const pa_shape* shp, void* stream) {
     return rope_and_cache(q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping, inv_freq,
                           rotary_dim, interleaved, factor, q_out, q_out_stride, k_cache, v_cache,
-                          num_tokens, true, k_scale, v_scale, shp, stream);
+                          num_tokens, true, k_scale, v_scale, nullptr, shp, stream);
+}
+
+int pa_norm_rope_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, const void* q_weight,
+                           const void* k_weight, float eps, const int64_t* positions,
+                           int32_t num_axes, const int32_t* axes, const int64_t* slot_mapping,
+                           const float* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                           float factor, void* q_out, int64_t q_out_stride, void* k_cache,
+                           void* v_cache, int64_t num_tokens, const pa_shape* shp, void* stream) {
+    const Norm norm{q_weight, k_weight, eps, num_axes, axes};
+    return rope_and_cache(q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping, inv_freq,
+                          rotary_dim, interleaved, factor, q_out, q_out_stride, k_cache, v_cache,
+                          num_tokens, false, 1.f, 1.f, &norm, shp, stream);
+}
+
+int pa_norm_rope_and_cache_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                               const void* v, int64_t v_stride, const void* q_weight,
+                               const void* k_weight, float eps, const int64_t* positions,
+                               int32_t num_axes, const int32_t* axes, const int64_t* slot_mapping,
+                               const float* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                               float factor, void* q_out, int64_t q_out_stride, void* k_cache,
+                               void* v_cache, int64_t num_tokens, float k_scale, float v_scale,
+                               const pa_shape* shp, void* stream) {
+    const Norm norm{q_weight, k_weight, eps, num_axes, axes};
+    return rope_and_cache(q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping, inv_freq,
+                          rotary_dim, interleaved, factor, q_out, q_out_stride, k_cache, v_cache,
+                          num_tokens, true, k_scale, v_scale, &norm, shp, stream);
 }
 
 size_t pa_decode_weights_workspace_size(const pa_shape* shp, int32_t max_context_len,

@@ -26,9 +26,16 @@ struct RopeParams {
     int rotary_dim;
     float factor;
     float k_scale, v_scale;        // E4M3 cache only
+    // behind a norm per head only
+    const void* q_weight;          // [D], null: ones
+    const void* k_weight;
+    float eps;
+    const int32_t* axes;           // [rotary_dim / 2], null: axis 0; positions are [num_axes][T]
+    int num_axes;
 };
 
-cudaError_t launch_rope_and_cache(int dtype, int head_dim, bool fp8, bool interleaved,
+// norm: heads of q and k normalised first, positions on several axes.
+cudaError_t launch_rope_and_cache(int dtype, int head_dim, bool fp8, bool interleaved, bool norm,
                                   const RopeParams& p, cudaStream_t stream);
 
 // Merge of the partitions written by the decode kernel's weights mode, and

@@ -11,6 +11,11 @@
 // (1 / 2 pi and the product in 64 bits) and 2^-64 turns per position, and the
 // phase's rounding to fp32, 2^-26 turns.  Products and sums are in fp32; each
 // result is rounded once.
+//
+// With kNorm each head x of q and k is first taken to w x / sqrt(mean x^2 +
+// eps), in fp32 and not rounded in between, and a pair's position is that of
+// its axis.  The D / 16 threads that hold a head add up its squares by
+// shuffles among themselves.
 #include <type_traits>
 
 #include "bounded_internal.h"
@@ -20,6 +25,7 @@ namespace pa {
 
 constexpr int kRopeThreads = 128;
 constexpr int kRopeCtas = 9;                  // per SM
+constexpr int kNormCtas = 8;                  // the same behind a norm
 
 // Position-independent part of the angle: turns per position, in 2^-64.
 __device__ __forceinline__ int64_t rope_turns(float inv_freq) {
@@ -72,12 +78,13 @@ struct RopePlaces {
     static constexpr int kFrom = kFirst, kTo = kEnd;
 };
 
-template <typename T, int D, bool kFp8, bool kInterleaved, int kTokens>
-__global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
+template <typename T, int D, bool kFp8, bool kInterleaved, bool kNorm, int kTokens>
+__global__ void __launch_bounds__(kRopeThreads, kNorm ? kNormCtas : kRopeCtas)
     rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
     constexpr int kUnits = D / 16, kHeads = kRopeThreads / kUnits;      // items side by side
     __shared__ __align__(16) float2 cs[kTokens][D / 2];
     __shared__ int64_t slot_s[kTokens];
+    __shared__ __align__(16) float weight_s[kNorm ? 2 : 1][kNorm ? D : 1];      // of q, of k
     grid_dependency_wait();
     allow_dependent_launch();
     const int tid = threadIdx.x, u = tid % kUnits, first = tid / kUnits;
@@ -121,9 +128,28 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
             if (slot < 0) continue;
             constexpr bool kCodes = kFp8 && kRows != kRopeQ;
             float x0[8], x1[8];
-            if (kCodes || (kRows != kRopeV && rot)) {
+            if (kCodes || (kRows != kRopeV && (rot || kNorm))) {
                 unpack8<T>(v0[k], x0);
                 unpack8<T>(v1[k], x1);
+            }
+            if constexpr (kNorm && kRows != kRopeV) {
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum = fmaf(x0[j], x0[j], fmaf(x1[j], x1[j], sum));
+                // the head's threads run together
+                const uint32_t head = ((1u << kUnits) - 1u) << ((int)(threadIdx.x & 31u) & ~(kUnits - 1));
+#pragma unroll
+                for (int d = kUnits / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(head, sum, d);
+                const float inv = rsqrtf(fmaf(sum, 1.f / D, p.eps));
+                const float4* w = reinterpret_cast<const float4*>(weight_s[kRows]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float4 a = w[2 * c0 + j], b = w[2 * c1 + j];
+                    x0[4 * j] *= inv * a.x, x0[4 * j + 1] *= inv * a.y;
+                    x0[4 * j + 2] *= inv * a.z, x0[4 * j + 3] *= inv * a.w;
+                    x1[4 * j] *= inv * b.x, x1[4 * j + 1] *= inv * b.y;
+                    x1[4 * j + 2] *= inv * b.z, x1[4 * j + 3] *= inv * b.w;
+                }
             }
             if (kRows != kRopeV && rot) {
                 const float4* a = reinterpret_cast<const float4*>(&cs[tk][8 * u]);     // two pairs each
@@ -145,8 +171,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
                         x0[2 * j] = r0, x0[2 * j + 1] = r1;
                     }
                 }
-                if (!kCodes) v0[k] = pack8<T>(x0), v1[k] = pack8<T>(x1);
             }
+            if (!kCodes && kRows != kRopeV && (rot || kNorm)) v0[k] = pack8<T>(x0), v1[k] = pack8<T>(x1);
             const int d0 = kRows == kRopeV ? 2 * u : c0, d1 = kRows == kRopeV ? 2 * u + 1 : c1;
             if (kRows == kRopeQ) {
                 uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) + (t0 + tk) * p.q_out_stride + h * D);
@@ -178,7 +204,22 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     const int pairs = p.rotary_dim / 2;
     for (int i = tid; i < tokens * pairs; i += kRopeThreads) {
         const int tk = i / pairs, j = i - tk * pairs;
-        cs[tk][j] = rope_cos_sin(rope_turns(p.inv_freq[j]), p.positions[t0 + tk], p.factor);
+        int64_t row = t0 + tk;
+        if constexpr (kNorm) {
+            const int axis = p.axes ? p.axes[j] : 0;
+            if (axis >= 0 && axis < p.num_axes)
+                row += axis * p.num_tokens;
+            else
+                flag_error(p.err, PA_DEVERR_BAD_INDEX);
+        }
+        cs[tk][j] = rope_cos_sin(rope_turns(p.inv_freq[j]), p.positions[row], p.factor);
+    }
+    if constexpr (kNorm) {
+        static_assert(kRopeThreads >= D, "a thread per weight");
+        if (tid < D) {
+            weight_s[kRopeQ][tid] = p.q_weight ? (float)static_cast<const T*>(p.q_weight)[tid] : 1.f;
+            weight_s[kRopeK][tid] = p.k_weight ? (float)static_cast<const T*>(p.k_weight)[tid] : 1.f;
+        }
     }
     if (tid < tokens) {
         const int64_t slot = p.slots[t0 + tid];
@@ -205,31 +246,33 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
 // 256 threads, four tokens and four CTAs; into an E4M3 cache, 5001 tokens of
 // 32 + 16 heads 21.2, with ten 22.9, with eight 22.2.  A single wave of tokens
 // goes one to a CTA, which spreads it wider.
-template <typename T, int D, bool kFp8, bool kInterleaved>
+template <typename T, int D, bool kFp8, bool kInterleaved, bool kNorm>
 cudaError_t launch_rope_i(const RopeParams& p, cudaStream_t stream) {
     const dim3 threads(kRopeThreads);
     if (p.num_tokens <= 152 * kRopeCtas)
-        return launch_with_pdl(rope_and_cache_kernel<T, D, kFp8, kInterleaved, 1>, dim3((unsigned)p.num_tokens),
-                               threads, 0, stream, p);
-    return launch_with_pdl(rope_and_cache_kernel<T, D, kFp8, kInterleaved, 2>,
+        return launch_with_pdl(rope_and_cache_kernel<T, D, kFp8, kInterleaved, kNorm, 1>,
+                               dim3((unsigned)p.num_tokens), threads, 0, stream, p);
+    return launch_with_pdl(rope_and_cache_kernel<T, D, kFp8, kInterleaved, kNorm, 2>,
                            dim3((unsigned)((p.num_tokens + 1) / 2)), threads, 0, stream, p);
 }
 
 template <typename T, int D, bool kFp8>
-cudaError_t launch_rope_t(bool interleaved, const RopeParams& p, cudaStream_t stream) {
-    return interleaved ? launch_rope_i<T, D, kFp8, true>(p, stream)
-                       : launch_rope_i<T, D, kFp8, false>(p, stream);
+cudaError_t launch_rope_t(bool interleaved, bool norm, const RopeParams& p, cudaStream_t stream) {
+    if (norm) return interleaved ? launch_rope_i<T, D, kFp8, true, true>(p, stream)
+                                 : launch_rope_i<T, D, kFp8, false, true>(p, stream);
+    return interleaved ? launch_rope_i<T, D, kFp8, true, false>(p, stream)
+                       : launch_rope_i<T, D, kFp8, false, false>(p, stream);
 }
 
-cudaError_t launch_rope_and_cache(int dtype, int head_dim, bool fp8, bool interleaved,
+cudaError_t launch_rope_and_cache(int dtype, int head_dim, bool fp8, bool interleaved, bool norm,
                                   const RopeParams& p, cudaStream_t stream) {
     const bool bf16 = dtype == PA_BF16;
-    if (fp8) return bf16 ? launch_rope_t<__nv_bfloat16, 128, true>(interleaved, p, stream)
-                         : launch_rope_t<__half, 128, true>(interleaved, p, stream);
-    if (head_dim == 64) return bf16 ? launch_rope_t<__nv_bfloat16, 64, false>(interleaved, p, stream)
-                                    : launch_rope_t<__half, 64, false>(interleaved, p, stream);
-    return bf16 ? launch_rope_t<__nv_bfloat16, 128, false>(interleaved, p, stream)
-                : launch_rope_t<__half, 128, false>(interleaved, p, stream);
+    if (fp8) return bf16 ? launch_rope_t<__nv_bfloat16, 128, true>(interleaved, norm, p, stream)
+                         : launch_rope_t<__half, 128, true>(interleaved, norm, p, stream);
+    if (head_dim == 64) return bf16 ? launch_rope_t<__nv_bfloat16, 64, false>(interleaved, norm, p, stream)
+                                    : launch_rope_t<__half, 64, false>(interleaved, norm, p, stream);
+    return bf16 ? launch_rope_t<__nv_bfloat16, 128, false>(interleaved, norm, p, stream)
+                : launch_rope_t<__half, 128, false>(interleaved, norm, p, stream);
 }
 
 }  // namespace pa

@@ -1,0 +1,70 @@
+// Parameters and launchers of the operators of speculative decoding: attention
+// of a tree of drafted tokens (tree_attention.cu), the accepted path and its
+// commit (tree_path.cu).  Rotary positions behind a norm per head are in
+// rope_cache.cu.
+#pragma once
+
+#include "pa_internal.h"
+
+namespace pa {
+
+struct TreeParams {
+    const void* q;                 // [T][Hq][D]
+    const void* k_cache;
+    const void* v_cache;
+    void* out;                     // [T][Hq][D]
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* query_start;    // [B + 1]
+    const int32_t* parents;        // [T], null: a line
+    int* err;
+    float scale_log2;              // scale * k_scale * log2(e)
+    float v_scale;
+    int num_seqs, num_q_heads, num_kv_heads, group;
+    int max_blocks_per_seq, block_size;
+    int64_t num_blocks;
+    int64_t num_tokens;            // rows of q
+    int max_context;               // smaller of the table's and the caller's bound
+    int max_query;                 // nodes per sequence at most
+};
+
+cudaError_t launch_tree_attention(int dtype, int head_dim, bool fp8, const TreeParams& p,
+                                  cudaStream_t stream);
+
+struct AcceptParams {
+    const int64_t* draft;          // [T]
+    const int64_t* target;         // [T]
+    const int32_t* parents;        // [T]
+    const int32_t* query_start;    // [B + 1]
+    int32_t* path;                 // [B][max_query]
+    int32_t* path_lens;            // [B]
+    int64_t* next;                 // [B]
+    int* err;
+    int64_t num_tokens;
+    int num_seqs, max_query;
+};
+
+cudaError_t launch_accept_tree(const AcceptParams& p, cudaStream_t stream);
+
+constexpr int kCommitLayers = 64;  // per launch: their pointers are kernel arguments
+
+struct CommitParams {
+    void* caches[2 * kCommitLayers];   // K of each layer, then V
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* query_start;
+    const int32_t* path;           // [B][path_stride]
+    const int32_t* path_lens;
+    int32_t* new_lens;
+    int* err;
+    int num_caches, num_seqs;
+    int path_stride;
+    int max_blocks_per_seq, block_size;
+    int64_t num_blocks;
+    int row_vectors;               // 16-byte vectors of a token's row in one cache
+    bool report;                   // the launch that writes new_lens and flags errors
+};
+
+cudaError_t launch_commit_path(const CommitParams& p, cudaStream_t stream);
+
+}  // namespace pa

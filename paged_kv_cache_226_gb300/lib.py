@@ -24,7 +24,8 @@ HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "pa.h")
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA = range(5)
 PA_FP16, PA_BF16 = 0, 1
-PA_DEVERR_WAIT_TIMEOUT, PA_DEVERR_BAD_CONTEXT, PA_DEVERR_BAD_SLOT = 1, 2, 4
+PA_DEVERR_WAIT_TIMEOUT, PA_DEVERR_BAD_CONTEXT, PA_DEVERR_BAD_SLOT, PA_DEVERR_BAD_INDEX = 1, 2, 4, 8
+TREE_NODES = 128             # PA_TREE_NODES
 DEFAULT_PARTITION = 512
 
 _DTYPE_CODES = {torch.float16: PA_FP16, torch.bfloat16: PA_BF16}
@@ -115,8 +116,18 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.pa_evict_workspace_size.argtypes = [S, I32]
         for fn in (lib.pa_evict, lib.pa_evict_fp8):
             fn.argtypes = [V, V, V, V, V, V, V, V, I64, I32, I32, I32, I32, V, V, V, V, Z, S, V]
+        norm = [V, I64, V, I64, V, I64, V, V, F, V, I32, V, V, V, I32, I32, F, V, I64, V, V, I64]
+        lib.pa_norm_rope_and_cache.argtypes = [*norm, S, V]
+        lib.pa_norm_rope_and_cache_fp8.argtypes = [*norm, F, F, S, V]
+        lib.pa_tree_attention_workspace_size.argtypes = [S, I32, I32]
+        lib.pa_tree_attention.argtypes = [V, V, V, V, V, V, V, F, I64, I32, I32, V, Z, V, S, V]
+        lib.pa_tree_attention_fp8.argtypes = [V, V, V, V, V, V, V, F, F, F, I64, I32, I32, V, Z, V,
+                                              S, V]
+        lib.pa_accept_tree.argtypes = [V, V, V, V, I32, I64, I32, V, V, V, V]
+        for fn in (lib.pa_commit_path, lib.pa_commit_path_fp8):
+            fn.argtypes = [V, V, I32, V, V, V, V, I32, V, V, S, V]
         for fn in ("pa_decode_weights_workspace_size", "pa_prefill_weights_workspace_size",
-                   "pa_evict_workspace_size"):
+                   "pa_evict_workspace_size", "pa_tree_attention_workspace_size"):
             getattr(lib, fn).restype = Z
         lib.pa_status_string.argtypes = [ctypes.c_int]
         lib.pa_status_string.restype = ctypes.c_char_p
@@ -651,7 +662,7 @@ _bound = object()        # the library that _native calls
 
 
 def _load_native():
-    """The binding of the bounded-cache calls (csrc/binding.cpp), set to call
+    """The binding of the bounded-cache and tree calls (csrc/binding.cpp), set to call
     the loaded library: their checks and allocations in native code, since a
     layer makes three of them per step."""
     global _native, _bound
@@ -844,6 +855,96 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tens
         _refused("pa_evict", k_cache, r)
     return (r, weights if weights_out is None else weights_out,
             positions if positions_out is None else positions_out)
+
+
+# ---- speculative decoding: a tree of drafted tokens per sequence --------------
+#
+# Node i of sequence b is row query_start[b] + i of the batch and the cached
+# token L_b - C_b + i; parents name a node's predecessor within its tree.
+
+def norm_rope_and_cache(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                        positions: torch.Tensor, slot_mapping: torch.Tensor,
+                        inv_freq: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        q_weight: Optional[torch.Tensor] = None,
+                        k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                        axes: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                        interleaved: bool = False, factor: float = 1.0,
+                        k_scale: Optional[float] = None,
+                        v_scale: Optional[float] = None) -> Optional[torch.Tensor]:
+    """``rope_and_cache`` behind a norm of every head of q and k
+    (pa_norm_rope_and_cache, or its E4M3 form for a uint8 cache): x becomes
+    weight * x / sqrt(mean(x^2) + eps), then turns; returns the turned q.
+
+    q_weight, k_weight: [D] of q's dtype (None: ones).  positions: int64 [T], or
+    [A][T] with ``axes``, int32 [R/2]: the axis whose positions turn pair i
+    (time, height and width of an image's patches, for instance)."""
+    r = (_native if _bound is _lib else _load_native()).norm_rope_and_cache(
+        q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cache, q_weight, k_weight, eps, axes,
+        q_out, interleaved, factor, k_scale, v_scale)
+    if r.__class__ is int:
+        _refused("pa_norm_rope_and_cache", k_cache, r)
+    return r
+
+
+def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_tables: torch.Tensor, context_lens: torch.Tensor,
+                   query_start: torch.Tensor, parents: Optional[torch.Tensor], scale: float,
+                   max_query_len: int, max_context_len: int, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, k_scale: Optional[float] = None,
+                   v_scale: Optional[float] = None) -> torch.Tensor:
+    """Attention of trees of drafted tokens over the cache, which holds their
+    keys and values (pa_tree_attention, or its E4M3 form for a uint8 cache):
+    each node sees the context, its ancestors and itself.
+
+    q, out: [total_tokens][Hq][D]; query_start: int32 [B + 1]; parents: int32
+    [total_tokens], the node of the same tree that a node follows (below its
+    own index; negative: the context), None: every tree is a line.  Trees have
+    at most 128 nodes; context_lens counts them."""
+    r = (_native if _bound is _lib else _load_native()).tree_attention(
+        q, k_cache, v_cache, block_tables, context_lens, query_start, parents, scale, max_query_len,
+        max_context_len, out, workspace, k_scale, v_scale)
+    if r.__class__ is int:
+        _refused("pa_tree_attention", k_cache, r)
+    return r
+
+
+def accept_tree(draft_tokens: torch.Tensor, target_tokens: torch.Tensor,
+                parents: Optional[torch.Tensor], query_start: torch.Tensor, max_query_len: int
+                ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The longest path of drafted tokens that the model agrees with
+    (pa_accept_tree): (path, path_lens, next_tokens).
+
+    draft_tokens: int64 [total_tokens], each node's token (node 0: the newest
+    one, always kept); target_tokens: int64 [total_tokens], what the model gives
+    after each node; parents, query_start: as for ``tree_attention``.  path:
+    int32 [B][max_query_len], node indexes from node 0 on, -1 behind them;
+    next_tokens: int64 [B], the model's token after the path's end."""
+    r = (_native if _bound is _lib else _load_native()).accept_tree(
+        draft_tokens, target_tokens, parents, query_start, max_query_len)
+    if r.__class__ is int:
+        _check("pa_accept_tree", r)
+    return r
+
+
+def commit_path(k_caches, v_caches, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                query_start: torch.Tensor, path: torch.Tensor, path_lens: torch.Tensor,
+                new_lens: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Keep of each tree the path's nodes: their rows close up behind the
+    context in the caches of all layers (pa_commit_path; pa_commit_path_fp8 for
+    uint8 caches), in place; returns the new context lengths, int32 [B].
+
+    k_caches, v_caches: a cache each, or sequences of one per layer; path,
+    path_lens: as ``accept_tree`` gives them.  Blocks past ceil(new_len /
+    block_size) are free afterwards (``PagedKVAllocator.truncate``)."""
+    if not isinstance(k_caches, torch.Tensor):
+        k_caches = tuple(k_caches)
+    if not isinstance(v_caches, torch.Tensor):
+        v_caches = tuple(v_caches)
+    r = (_native if _bound is _lib else _load_native()).commit_path(
+        k_caches, v_caches, block_tables, context_lens, query_start, path, path_lens, new_lens)
+    if r.__class__ is int:
+        _refused("pa_commit_path", k_caches if isinstance(k_caches, torch.Tensor) else k_caches[0], r)
+    return r
 
 
 STATIC_WORKSPACE_BYTES = 32 << 20
