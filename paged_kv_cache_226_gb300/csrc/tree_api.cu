@@ -48,11 +48,15 @@ int tree_attention(const void* q, const void* k_cache, const void* v_cache, cons
     if (!query_start || !aligned(query_start, 4) || !aligned(parents, 4) || !aligned(q, 16) || !aligned(out, 16) ||
         (num_tokens > 0 && (!q || !out)) || (q != nullptr && q == out))
         return PA_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < pa_tree_attention_workspace_size(shp, max_query_len, max_context_len))
-        return PA_ERR_WORKSPACE;
-    if (!aligned(workspace, 16)) return PA_ERR_INVALID_ARG;
     pa::TreeParams p = tree_sizes(shp, max_query_len, max_context_len);
+    if (!workspace || workspace_bytes < pa::tree_plan(p, shp->head_dim, workspace)) return PA_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return PA_ERR_INVALID_ARG;
     if (num_tokens == 0 || p.max_query == 0) return PA_OK;
+    // key tiles are counted in 32 bits
+    if (((int64_t)p.max_context + 127) / 128 * p.num_seqs * p.num_kv_heads >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+    CUtensorMap tmk, tmv;
+    if ((st = pa::encode_cache_map(&tmk, k_cache, shp, fp8)) != PA_OK) return st;
+    if ((st = pa::encode_cache_map(&tmv, v_cache, shp, fp8)) != PA_OK) return st;
     cudaError_t e = pa::error_word(&p.err);
     if (e != cudaSuccess) return finish(e);
     p.q = q, p.k_cache = k_cache, p.v_cache = v_cache, p.out = out;
@@ -61,7 +65,12 @@ int tree_attention(const void* q, const void* k_cache, const void* v_cache, cons
     p.scale_log2 = scale * (fp8 ? k_scale : 1.f) * pa::kLog2e, p.v_scale = v_scale;
     p.max_blocks_per_seq = shp->max_blocks_per_seq, p.block_size = shp->block_size;
     p.num_blocks = shp->num_blocks, p.num_tokens = num_tokens;
-    return finish(pa::launch_tree_attention(shp->dtype, shp->head_dim, fp8, p, static_cast<cudaStream_t>(stream)));
+#ifdef PA_TEST_HOOKS
+    const pa::TestFault fault = pa::test_fault();
+    p.test_cta = fault.cta, p.test_tile = fault.tile, p.test_wait_limit_ns = fault.wait_limit_ns;
+#endif
+    return finish(pa::launch_tree_attention(shp->dtype, shp->head_dim, fp8, tmk, tmv, p,
+                                            static_cast<cudaStream_t>(stream)));
 }
 
 int commit_path(void* const* k_caches, void* const* v_caches, int32_t num_layers, const int32_t* block_tables,
@@ -113,7 +122,8 @@ extern "C" {
 
 size_t pa_tree_attention_workspace_size(const pa_shape* shp, int32_t max_query_len, int32_t max_context_len) {
     if (pa::check_shape(shp, true) != PA_OK || check_tree(max_query_len, max_context_len) != PA_OK) return 0;
-    return 16;
+    pa::TreeParams p = tree_sizes(shp, max_query_len, max_context_len);
+    return pa::tree_plan(p, shp->head_dim, nullptr);
 }
 
 int pa_tree_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,

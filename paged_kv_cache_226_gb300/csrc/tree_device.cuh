@@ -45,12 +45,13 @@ struct TreeLine {
 // masks and parents double their reach in every round (node i's line joins
 // its parent's, its parent becomes the parent's parent), so a tree of any
 // depth takes at most seven.  `barrier` synchronises the threads and returns
-// whether any of them passed true.
+// whether any of them passed true.  When the last thread has left, room.line
+// holds every node's line; nobody may still read the room at the call.
 constexpr int kLineThreads = PA_TREE_NODES;
 
 struct LineRoom {
-    uint4 line[2][PA_TREE_NODES];
-    short above[2][PA_TREE_NODES];
+    uint4 line[PA_TREE_NODES];
+    signed char above[PA_TREE_NODES];
 };
 
 template <typename Barrier>
@@ -58,19 +59,18 @@ __device__ __forceinline__ TreeLine tree_line(LineRoom& room, int i, int C, int 
     uint32_t w[kLineWords];
 #pragma unroll
     for (int k = 0; k < kLineWords; ++k) w[k] = i < C && (i >> 5) == k ? 1u << (i & 31) : 0u;
-    int up = i < C ? parent : -1;
-    room.line[0][i] = make_uint4(w[0], w[1], w[2], w[3]);
-    room.above[0][i] = (short)up;
-    int now = 0;
+    int up = i < C && parent >= 0 ? parent : -1;
+    room.line[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    room.above[i] = (signed char)up;
     while (barrier(up >= 0)) {
         if (up >= 0) {
-            const uint4 o = room.line[now][up];
+            const uint4 o = room.line[up];
             w[0] |= o.x, w[1] |= o.y, w[2] |= o.z, w[3] |= o.w;
-            up = room.above[now][up];
+            up = room.above[up];
         }
-        now ^= 1;
-        room.line[now][i] = make_uint4(w[0], w[1], w[2], w[3]);
-        room.above[now][i] = (short)up;
+        barrier(false);
+        room.line[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        room.above[i] = (signed char)up;
     }
     return TreeLine{{w[0], w[1], w[2], w[3]}};
 }

@@ -26,10 +26,25 @@ struct TreeParams {
     int64_t num_tokens;            // rows of q
     int max_context;               // smaller of the table's and the caller's bound
     int max_query;                 // nodes per sequence at most
+    // filled by tree_plan
+    int lanes;                     // CTAs side by side on the same keys, 256 rows of queries each
+    int ctas;                      // of a lane at most
+    bool whole;                    // CTAs are dealt whole (sequence, KV head) pairs
+    float* rec_o;                  // [ctas][lanes][2][2][128][D]
+    float2* rec_ml;                // the same without D: reference (log2 units) and sum
+#ifdef PA_TEST_HOOKS
+    // Test builds only: CTA test_cta's loaders issue no tile from test_tile
+    // on, and waits give up after test_wait_limit_ns.
+    int test_cta, test_tile;
+    unsigned long long test_wait_limit_ns;
+#endif
 };
 
-cudaError_t launch_tree_attention(int dtype, int head_dim, bool fp8, const TreeParams& p,
-                                  cudaStream_t stream);
+// Lays out the work and the workspace, whose bytes it returns (needs the
+// sizes: num_seqs, num_kv_heads, group, max_context, max_query).
+size_t tree_plan(TreeParams& p, int head_dim, void* workspace);
+cudaError_t launch_tree_attention(int dtype, int head_dim, bool fp8, const CUtensorMap& tmk,
+                                  const CUtensorMap& tmv, const TreeParams& p, cudaStream_t stream);
 
 struct AcceptParams {
     const int64_t* draft;          // [T]
