@@ -54,9 +54,11 @@ int tree_attention(const void* q, const void* k_cache, const void* v_cache, cons
     if (num_tokens == 0 || p.max_query == 0) return PA_OK;
     // key tiles are counted in 32 bits
     if (((int64_t)p.max_context + 127) / 128 * p.num_seqs * p.num_kv_heads >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
-    CUtensorMap tmk, tmv;
+    CUtensorMap tmk, tmv, tmq;
     if ((st = pa::encode_cache_map(&tmk, k_cache, shp, fp8)) != PA_OK) return st;
     if ((st = pa::encode_cache_map(&tmv, v_cache, shp, fp8)) != PA_OK) return st;
+    if ((st = pa::encode_query_map(&tmq, q, shp, num_tokens, p.group, pa::tree_nodes_per_tile(p.group))) != PA_OK)
+        return st;
     cudaError_t e = pa::error_word(&p.err);
     if (e != cudaSuccess) return finish(e);
     p.q = q, p.k_cache = k_cache, p.v_cache = v_cache, p.out = out;
@@ -69,7 +71,7 @@ int tree_attention(const void* q, const void* k_cache, const void* v_cache, cons
     const pa::TestFault fault = pa::test_fault();
     p.test_cta = fault.cta, p.test_tile = fault.tile, p.test_wait_limit_ns = fault.wait_limit_ns;
 #endif
-    return finish(pa::launch_tree_attention(shp->dtype, shp->head_dim, fp8, tmk, tmv, p,
+    return finish(pa::launch_tree_attention(shp->dtype, shp->head_dim, fp8, tmk, tmv, tmq, p,
                                             static_cast<cudaStream_t>(stream)));
 }
 

@@ -27,12 +27,15 @@
 // The key tiles of all pairs, in order, are dealt out to persistent CTAs in
 // equal ranges, or, where contexts are short, whole pairs are.  A pair that
 // more than one CTA meets leaves records (O, m, sum), joined by a second
-// kernel.  What bounds it: K and V come once from HBM (512 B a token and KV
-// head at D 128) and 256 rows cost 8 D operations a byte, 2/3 of the tensor
-// cores' time at that rate; a row tile of its own costs a third.
+// kernel.  K and V come once from HBM, 512 B a token and KV head at D 128;
+// the products cost 12 D operations (P in two parts) for each row and token.
 //
-// Warps: 0 loads K tiles and 2 V tiles, 1 issues S and 3 P V, 4 .. 7 are slot
-// 0's softmax and 8 .. 11 slot 1's.  Every barrier's waits follow each other
+// An E4M3 cache's codes are brought to the 16-bit type (exactly) by three
+// warps between the loaders' ring and the operands'.
+//
+// Warps: 0 loads K tiles (and the query tiles) and 2 V tiles, 1 issues S and 3
+// P V, 4 .. 7 are slot 0's softmax and 8 .. 11 slot 1's, 12 makes the trees'
+// lines, 13 .. 15 convert codes.  Every barrier's waits follow each other
 // phase by phase: a tile's ring stage is its running number modulo the ring,
 // and a slot's barriers count the slot's own tiles.
 #include "decode_tile.cuh"
@@ -43,39 +46,54 @@ namespace pa {
 
 constexpr int kTrRows = 128;
 constexpr int kTrKeys = 128;
-constexpr int kTrKStages = 3;
-constexpr int kTrVStages = 2;
 constexpr int kTrSlots = 2;
-constexpr int kTrThreads = (4 + 4 * kTrSlots) * 32;
+constexpr int kTrQStages = 2;
+constexpr int kTrCodeStages = 2;               // of K and of V each
+constexpr int kTrSoftmaxWarps = 4 * kTrSlots;
+constexpr int kTrLineWarp = 4 + kTrSoftmaxWarps;
+constexpr int kTrConverters = 3;
+constexpr int kTrThreads = (kTrLineWarp + 1 + kTrConverters) * 32;
+// Registers: 512 threads are launched with 128 each; the softmax warps take
+// over what the others give up.
+constexpr int kTrControlRegs = 56, kTrSoftmaxRegs = 200;
+static_assert(kTrThreads == 512 && 2 * (kTrControlRegs + kTrSoftmaxRegs) <= 4 * 128, "registers of the CTA");
 constexpr int kTrCtas = 152;                   // one per SM
-constexpr int kTrMinTiles = 4;                 // key tiles of a CTA at least, where there are records
+constexpr int kTrMinTiles = 4;                 // weight of a CTA's range at least, where there are records
 constexpr int kTrWholeTiles = 4;               // longest contexts, in tiles, whose pairs stay whole
+constexpr int kTrPairWeight = 1;               // of a pair beside its key tiles, in the dealing
 
-template <int D>
+// Shared memory: query tiles, operand tiles, codes.
+template <int D, bool kFp8>
 struct TrLayout {
+    static constexpr int kKStages = kFp8 ? 1 : 3, kVStages = 2;
     static constexpr int kHalves = D / kBoxElems;
     static constexpr int kHalf = kTrRows * 128;               // 64 dims of 128 rows
     static constexpr int kTile = kHalves * kHalf;
+    static constexpr int kCodes = kTrRows * 128;              // 128 codes of 128 rows
     static constexpr int kQ = 0;
-    static constexpr int kK = kQ + kTrSlots * kTile;
-    static constexpr int kV = kK + kTrKStages * kTile;
-    static constexpr int kRoom = kV + kTrVStages * kTile;
+    static constexpr int kK = kQ + kTrQStages * kTile;
+    static constexpr int kV = kK + kKStages * kTile;
+    static constexpr int kKCodes = kV + kVStages * kTile;
+    static constexpr int kVCodes = kKCodes + (kFp8 ? kTrCodeStages * kCodes : 0);
+    static constexpr int kRoom = kVCodes + (kFp8 ? kTrCodeStages * kCodes : 0);
 };
 
 // Behind the tiles.
 struct TrRoom {
     union {
-        LineRoom lines;                        // a pair's, at its begin
-        float2 ml[kTrSlots][kTrRows];          // the slots' statistics, at its end
+        uint4 line[PA_TREE_NODES];             // a piece's lines, until they are read
+        float2 ml[kTrSlots][kTrRows];          // the slots' statistics, at a joined piece's end
     };
-    uint64_t k_full[kTrKStages], k_empty[kTrKStages], v_full[kTrVStages], v_empty[kTrVStages];
-    uint64_t q_full[kTrSlots], s_full[kTrSlots], p_full[kTrSlots], o_done[kTrSlots], done[2];
+    uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
+    uint64_t kc_full[kTrCodeStages], kc_empty[kTrCodeStages], vc_full[kTrCodeStages], vc_empty[kTrCodeStages];
+    uint64_t q_full[kTrQStages], q_empty[kTrQStages], lines_full, lines_empty;
+    uint64_t s_full[kTrSlots], p_full[kTrSlots], o_done[kTrSlots], done[2];
     uint32_t tmem;
 };
 
-template <int D>
-constexpr int tr_smem() { return TrLayout<D>::kRoom + (int)sizeof(TrRoom); }
-static_assert(tr_smem<128>() <= 232448, "shared memory over the per-CTA limit");
+template <int D, bool kFp8>
+constexpr int tr_smem() { return TrLayout<D, kFp8>::kRoom + (int)sizeof(TrRoom); }
+static_assert(tr_smem<128, false>() <= 232448 && tr_smem<128, true>() <= 232448, "shared memory over the per-CTA limit");
 
 #ifdef PA_TEST_HOOKS
 __device__ __forceinline__ uint64_t tr_wait_limit(const TreeParams& p) { return p.test_wait_limit_ns; }
@@ -92,26 +110,45 @@ __device__ __forceinline__ bool tr_wait(const TreeParams& p, uint64_t* bar, int 
     return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, tr_wait_limit(p)));
 }
 
-// A run of key tiles [k0, k1) of one pair of n tiles, the pair's first being
-// number `begin` of all.
+// A run of key tiles [k0, k1) of one pair of n tiles.
 struct TrPiece {
     int b, g, k0, k1, n;
-    unsigned begin;
     TreeSeq s;
+    bool share;                    // each slot has a query tile, and all key tiles
+    bool alone;                    // the slots do not join: shared, or a single tile
+    int owner;                     // the slot of a single tile
+
+    // The slot that takes key tile k where it is not both.
+    __device__ __forceinline__ int slot_of(int k) const { return alone ? owner : (k - k0) & 1; }
+    __device__ __forceinline__ bool has(int slot, int k) const { return share || slot_of(k) == slot; }
+    // A slot's tiles.
+    __device__ __forceinline__ int own(int slot) const {
+        return share ? k1 - k0 : (alone ? (int)(owner == slot) : (k1 - k0 + 1 - slot) / 2);
+    }
+    // The first slot's first tile or the second's.
+    __device__ __forceinline__ bool first(int slot, int k) const { return share || alone ? k == k0 : k - k0 == slot; }
+    __device__ __forceinline__ int query_tiles() const { return share ? 2 : 1; }
 };
 
+// Nodes of a query tile.
+__device__ __forceinline__ int tr_nodes_per_tile(int group) { return kTrRows / group; }
+
 // Walks a range of the batch's key tiles (or, with p.whole, of its pairs),
-// pair by pair; all lanes of a warp together, which hold 32 sequences at a time.
+// pair by pair; all lanes of a warp together, which hold 32 sequences at a
+// time.  A pair weighs its tiles and kTrPairWeight, which come first.
 struct TrWalk {
     unsigned at = 0, end = 0, base = 0, total = 0, ends = 0;
-    int base_b = 0;
+    int base_b = 0, turn = 0;
     TreeSeq mine;
 
     static __device__ __forceinline__ int tiles(const TreeSeq& s) {
         return s.C > 0 ? (s.L + kTrKeys - 1) / kTrKeys : 0;
     }
+    static __device__ __forceinline__ unsigned each(const TreeParams& p, const TreeSeq& s) {
+        return s.C > 0 ? (p.whole ? 1u : (unsigned)(tiles(s) + kTrPairWeight)) : 0u;
+    }
     static __device__ __forceinline__ unsigned weight(const TreeParams& p, const TreeSeq& s) {
-        return (unsigned)(p.whole ? s.C > 0 : tiles(s)) * p.num_kv_heads;
+        return each(p, s) * p.num_kv_heads;
     }
     __device__ __forceinline__ void read(const TreeParams& p, bool report) {
         const int lane = threadIdx.x & 31, b = base_b + lane;
@@ -134,39 +171,50 @@ struct TrWalk {
         read(p, report);
         return __reduce_add_sync(0xffffffffu, n) + total;
     }
-    __device__ __forceinline__ bool next(const TreeParams& p, TrPiece& P) {
-        if (at >= end) return false;
-        while (at >= base + total) {
-            base += total;
-            base_b += 32;
-            if (base_b >= p.num_seqs) return false;
-            read(p, false);
+    // The next piece with work in lane `side`.
+    __device__ __forceinline__ bool next(const TreeParams& p, int side, TrPiece& P) {
+        while (at < end) {
+            while (at >= base + total) {
+                base += total;
+                base_b += 32;
+                if (base_b >= p.num_seqs) return false;
+                read(p, false);
+            }
+            const int who = __ffs(__ballot_sync(0xffffffffu, at - base < ends)) - 1;
+            const unsigned before = __shfl_sync(0xffffffffu, ends, max(who - 1, 0));
+            P.s.L = __shfl_sync(0xffffffffu, mine.L, who);
+            P.s.C = __shfl_sync(0xffffffffu, mine.C, who);
+            P.s.q0 = __shfl_sync(0xffffffffu, mine.q0, who);
+            P.n = tiles(P.s);
+            const unsigned first = base + (who > 0 ? before : 0u), off = at - first;
+            const unsigned one = each(p, P.s), pair = off / one, in = off - pair * one;
+            P.b = base_b + who;
+            P.g = (int)pair;
+            if (p.whole) {
+                P.k0 = 0, P.k1 = P.n;
+                ++at;
+            } else {
+                const unsigned stop = min(one, in + (end - at));
+                P.k0 = max((int)in - kTrPairWeight, 0);
+                P.k1 = (int)stop - kTrPairWeight;
+                at += stop - in;
+                if (P.k1 <= P.k0) continue;
+            }
+            // query tiles 2 side and 2 side + 1
+            const int per = tr_nodes_per_tile(p.group);
+            const int query_tiles = (P.s.C + per - 1) / per - kTrSlots * side;
+            if (query_tiles <= 0) continue;
+            P.share = query_tiles >= kTrSlots;
+            P.alone = P.share || P.k1 - P.k0 == 1;
+            P.owner = turn;
+            if (P.alone && !P.share) turn ^= 1;
+            return true;
         }
-        const int who = __ffs(__ballot_sync(0xffffffffu, at - base < ends)) - 1;
-        const unsigned before = __shfl_sync(0xffffffffu, ends, max(who - 1, 0));
-        P.s.L = __shfl_sync(0xffffffffu, mine.L, who);
-        P.s.C = __shfl_sync(0xffffffffu, mine.C, who);
-        P.s.q0 = __shfl_sync(0xffffffffu, mine.q0, who);
-        P.n = tiles(P.s);
-        const unsigned first = base + (who > 0 ? before : 0u), off = at - first;
-        const unsigned each = p.whole ? 1u : (unsigned)P.n, pair = off / each;
-        P.b = base_b + who;
-        P.g = (int)pair;
-        P.begin = first + pair * each;
-        if (p.whole) {
-            P.k0 = 0, P.k1 = P.n;
-            ++at;
-        } else {
-            P.k0 = (int)(at - P.begin);
-            P.k1 = (int)min((unsigned)P.n, P.k0 + (end - at));
-            at += P.k1 - P.k0;
-        }
-        return true;
+        return false;
     }
 };
 
-// How N tiles (or pairs) are dealt to the CTAs of a lane: CTA c has
-// [c N / ctas, (c + 1) N / ctas).
+// How weight N is dealt to the CTAs of a lane: CTA c has [c N / ctas, (c + 1) N / ctas).
 struct TrDeal {
     unsigned N, ctas;
     __device__ __forceinline__ TrDeal(const TreeParams& p, unsigned n) : N(n) {
@@ -176,21 +224,12 @@ struct TrDeal {
         const unsigned each = N / ctas, rest = N % ctas;
         return c * each + c * rest / ctas;
     }
-    __device__ __forceinline__ unsigned cta_of(unsigned tile) const {
-        return (unsigned)((((uint64_t)tile + 1) * ctas - 1) / N);
+    __device__ __forceinline__ unsigned cta_of(unsigned at) const {
+        return (unsigned)((((uint64_t)at + 1) * ctas - 1) / N);
     }
 };
 
-// Rows of query tile t of a tree of C nodes.
-__device__ __forceinline__ int tr_nodes_per_tile(int group) { return kTrRows / group; }
-
-// The slots' use of a pair in this lane: query tiles 2 lane and 2 lane + 1.
-__device__ __forceinline__ int tr_query_tiles(const TreeParams& p, int C, int lane) {
-    const int per = tr_nodes_per_tile(p.group);
-    return min(kTrSlots, (C + per - 1) / per - kTrSlots * lane);
-}
-
-// One operand of P V's first factor type: hi + lo parts of two probabilities.
+// Two probabilities as hi + lo parts of the 16-bit type.
 template <typename M>
 __device__ __forceinline__ void split_pair(float p0, float p1, uint32_t& hi, uint32_t& lo) {
     hi = M::pack(p0, p1);
@@ -227,6 +266,22 @@ __device__ __forceinline__ uint32_t seen_word(const TreeLine& line, int off) {
     return __funnelshift_r(word(i), word(i + 1), off & 31);
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
+
 // 16-bit elements that are not finite, at their sign bits.
 template <typename T>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
@@ -234,15 +289,71 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
     return ((w & 0x7fff7fffu) + kStep) & 0x80008000u;
 }
 
-template <typename T, int D>
+// The lines of a tree's C nodes, a warp making them: lane i has nodes i, i +
+// 32, ... and their masks.  Masks and parents double their reach in every
+// round, as in tree_line.
+__device__ __forceinline__ void warp_lines(uint32_t (&w)[kLineWords][kLineWords], int (&up)[kLineWords], int C) {
+    const int lane = threadIdx.x & 31, sets = (C + 31) / 32;
+#pragma unroll
+    for (int i = 0; i < kLineWords; ++i) {
+#pragma unroll
+        for (int k = 0; k < kLineWords; ++k) w[i][k] = i == k && lane + 32 * i < C ? 1u << lane : 0u;
+    }
+    for (;;) {
+        bool more = false;
+#pragma unroll
+        for (int i = 0; i < kLineWords; ++i) more |= up[i] >= 0;
+        if (!__any_sync(0xffffffffu, more)) return;
+        uint32_t add[kLineWords][kLineWords];
+        int to[kLineWords];
+#pragma unroll
+        for (int i = 0; i < kLineWords; ++i) {
+            to[i] = -1;
+#pragma unroll
+            for (int k = 0; k < kLineWords; ++k) add[i][k] = 0u;
+            if (i >= sets) continue;
+#pragma unroll
+            for (int set = 0; set <= i; ++set) {             // parents stand before their nodes
+                const bool here = up[i] >= 0 && (up[i] >> 5) == set;
+                const int from = up[i] & 31;
+#pragma unroll
+                for (int k = 0; k <= set; ++k) {
+                    const uint32_t x = __shfl_sync(0xffffffffu, w[set][k], from);
+                    if (here) add[i][k] = x;
+                }
+                const int x = __shfl_sync(0xffffffffu, up[set], from);
+                if (here) to[i] = x;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kLineWords; ++i) {
+            up[i] = to[i];
+#pragma unroll
+            for (int k = 0; k < kLineWords; ++k) w[i][k] |= add[i][k];
+        }
+    }
+}
+
+// By the four warps of a group together, in a branch of their own: what follows
+// a join of branches would be held to the smaller count.
+__device__ __forceinline__ void control_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTrControlRegs));
+}
+
+__device__ __forceinline__ void softmax_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTrSoftmaxRegs));
+}
+
+template <typename T, int D, bool kFp8>
 __global__ void __launch_bounds__(kTrThreads, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
                           const __grid_constant__ CUtensorMap tmap_v,
+                          const __grid_constant__ CUtensorMap tmap_q,
                           const __grid_constant__ TreeParams p) {
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     // how far below the maximum the reference is set, and the growth that sets it anew
     constexpr float kBelow = kBf16 ? 0.f : 7.f, kRaise = kBelow + kRescaleThresholdLog2;
-    using Lay = TrLayout<D>;
+    using Lay = TrLayout<D, kFp8>;
     using M = Mma<T>;
     extern __shared__ __align__(1024) uint8_t smem[];        // the kernel has no other
     TrRoom& room = *reinterpret_cast<TrRoom*>(smem + Lay::kRoom);
@@ -252,10 +363,18 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     const int G = p.group, per_tile = tr_nodes_per_tile(G);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kTrKStages; ++i) mbar_init(&room.k_full[i], 1), mbar_init(&room.k_empty[i], 1);
-        for (int i = 0; i < kTrVStages; ++i) mbar_init(&room.v_full[i], 1), mbar_init(&room.v_empty[i], 1);
+        for (int i = 0; i < Lay::kKStages; ++i)
+            mbar_init(&room.k_full[i], kFp8 ? kTrConverters : 1), mbar_init(&room.k_empty[i], 1);
+        for (int i = 0; i < Lay::kVStages; ++i)
+            mbar_init(&room.v_full[i], kFp8 ? kTrConverters : 1), mbar_init(&room.v_empty[i], 1);
+        for (int i = 0; kFp8 && i < kTrCodeStages; ++i) {
+            mbar_init(&room.kc_full[i], 1), mbar_init(&room.kc_empty[i], kTrConverters);
+            mbar_init(&room.vc_full[i], 1), mbar_init(&room.vc_empty[i], kTrConverters);
+        }
+        for (int i = 0; i < kTrQStages; ++i) mbar_init(&room.q_full[i], 1), mbar_init(&room.q_empty[i], 1);
+        mbar_init(&room.lines_full, 1), mbar_init(&room.lines_empty, kTrSoftmaxWarps);
         for (int i = 0; i < kTrSlots; ++i) {
-            mbar_init(&room.q_full[i], 4), mbar_init(&room.p_full[i], 4);
+            mbar_init(&room.p_full[i], 4);
             mbar_init(&room.s_full[i], 1), mbar_init(&room.o_done[i], 1);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&room.done[i], 1);
@@ -271,24 +390,28 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, room.tmem, 0);
     if (cta < deal.ctas) walk.at = deal.begin(cta), walk.end = deal.begin(cta + 1);
-    const unsigned range_begin = walk.at;
     TrPiece P;
 
+    if (warp < 4) {
+    control_registers();
     if (warp == 0 || warp == 2) {
         // ------------------------------------------------------------------
         // loaders: K and V tiles, each at its own pace and on into the next
-        // pair's; lane i has box i of eight
+        // pair's; lane i has box i of eight.  Warp 0 also loads a piece's
+        // query tiles, before its keys.
         // ------------------------------------------------------------------
-        const CUtensorMap* map = warp == 0 ? &tmap_k : &tmap_v;
-        uint64_t* full = warp == 0 ? room.k_full : room.v_full;
-        uint64_t* empty = warp == 0 ? room.k_empty : room.v_empty;
-        uint8_t* ring = smem + (warp == 0 ? Lay::kK : Lay::kV);
-        const int stages = warp == 0 ? kTrKStages : kTrVStages;
+        const bool keys = warp == 0;
+        const CUtensorMap* map = keys ? &tmap_k : &tmap_v;
+        uint64_t* full = kFp8 ? (keys ? room.kc_full : room.vc_full) : (keys ? room.k_full : room.v_full);
+        uint64_t* empty = kFp8 ? (keys ? room.kc_empty : room.vc_empty) : (keys ? room.k_empty : room.v_empty);
+        uint8_t* ring = smem + (kFp8 ? (keys ? Lay::kKCodes : Lay::kVCodes) : (keys ? Lay::kK : Lay::kV));
+        const int stages = kFp8 ? kTrCodeStages : (keys ? Lay::kKStages : Lay::kVStages);
+        constexpr int kStage = kFp8 ? Lay::kCodes : Lay::kTile, kBoxes = kFp8 ? 1 : Lay::kHalves;
         if (lane == 0) prefetch_tensor_map(map);
-        int n = 0;
+        if (keys && lane == 0) prefetch_tensor_map(&tmap_q);
+        int n = 0, nq = 0;
         bool ok = true, held = false;
-        while (ok && !held && walk.next(p, P)) {
-            if (tr_query_tiles(p, P.s.C, side) <= 0) continue;
+        while (ok && !held && walk.next(p, side, P)) {
             const int32_t* table = p.block_tables + (size_t)P.b * p.max_blocks_per_seq;
             // block ids: lane i has box i % 8 of tile i / 8 of four, the next
             // four tiles' requested while these are loaded
@@ -297,6 +420,19 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 return tok < P.s.L ? __ldg(table + tok / p.block_size) : 0;
             };
             int blk = 0, ahead = ids(P.k0);
+            for (int i = 0; keys && ok && i < P.query_tiles(); ++i, ++nq) {
+                const int st = nq % kTrQStages;
+                if (nq >= kTrQStages) ok = tr_wait(p, &room.q_empty[st], nq / kTrQStages - 1);
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&room.q_full[st], (uint32_t)(per_tile * G * Lay::kHalves * 128));
+#pragma unroll
+                    for (int h = 0; h < Lay::kHalves; ++h)
+                        tma_load_3d(smem + Lay::kQ + st * Lay::kTile + h * Lay::kHalf, &tmap_q, &room.q_full[st],
+                                    h * kBoxElems, P.g * G, P.s.q0 + (kTrSlots * side + i) * per_tile);
+                }
+                __syncwarp();
+            }
             for (int k = P.k0; ok && k < P.k1; ++k, ++n) {
                 const int in = (k - P.k0) & 3;
                 if (in == 0) {
@@ -310,13 +446,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 held = tr_withheld(p, n);
                 if (!ok || held) break;
                 const int boxes = min(8, (P.s.L - k * kTrKeys + 15) / 16);
-                if (elect_one()) mbar_arrive_expect_tx(&full[st], (uint32_t)(boxes * Lay::kHalves * kBox16Bytes));
+                if (elect_one()) mbar_arrive_expect_tx(&full[st], (uint32_t)(boxes * kBoxes * kBox16Bytes));
                 __syncwarp();
                 const int id = __shfl_sync(0xffffffffu, blk, in * 8 + (lane & 7));
                 if (lane < boxes) {
-                    uint8_t* dst = ring + st * Lay::kTile + lane * kBox16Bytes;
+                    uint8_t* dst = ring + st * kStage + lane * kBox16Bytes;
 #pragma unroll
-                    for (int h = 0; h < Lay::kHalves; ++h)
+                    for (int h = 0; h < kBoxes; ++h)
                         tma_load_4d(dst + h * Lay::kHalf, map, &full[st], h * kBoxElems, P.g,
                                     (16 * lane) & (p.block_size - 1), id);
                 }
@@ -325,8 +461,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         }
         // the last copies have landed before the CTA gives its memory up
         for (int st = 0; st < stages && st < n; ++st) ok = tr_wait(p, &full[st], (n - 1 - st) / stages) && ok;
+        for (int st = 0; st < kTrQStages && st < nq; ++st)
+            ok = tr_wait(p, &room.q_full[st], (nq - 1 - st) / kTrQStages) && ok;
         if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
-    } else if (warp == 1 || warp == 3) {
+    } else {
         // ------------------------------------------------------------------
         // issuers: S (warp 1) and P V (warp 3), tile by tile and slot by slot.
         // A slot's S overwrites its P, so it waits for the P V before.
@@ -337,43 +475,43 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const uint64_t dq = smem_desc_sw128(smem_u32(smem + Lay::kQ), 16, 1024);
         const uint64_t dk = smem_desc_sw128(smem_u32(smem + Lay::kK), 16, 1024);
         const uint64_t dv = smem_desc_sw128(smem_u32(smem + Lay::kV), Lay::kHalf, 1024);
-        int n = 0, tiles[kTrSlots] = {0, 0}, queries[kTrSlots] = {0, 0};
+        int n = 0, nq = 0, tiles[kTrSlots] = {0, 0};
         bool ok = true;
         auto wait = [&](uint64_t* bar, int phase) { ok = ok && tr_wait(p, bar, phase); };
-        while (ok && walk.next(p, P)) {
-            const int query_tiles = tr_query_tiles(p, P.s.C, side);
-            if (query_tiles <= 0) continue;
-            const bool share = query_tiles == kTrSlots;
+        while (ok && walk.next(p, side, P)) {
+            for (int i = 0; scores && i < P.query_tiles(); ++i)
+                wait(&room.q_full[(nq + i) % kTrQStages], (nq + i) / kTrQStages);
             for (int k = P.k0; ok && k < P.k1; ++k, ++n) {
-                const int ks = n % kTrKStages, vs = n % kTrVStages;
+                const int ks = n % Lay::kKStages, vs = n % Lay::kVStages;
 #pragma unroll
                 for (int slot = 0; slot < kTrSlots; ++slot) {
-                    if (!share && ((k - P.k0) & 1) != slot) continue;
-                    const bool first = share ? k == P.k0 : k - P.k0 == slot;
-                    const bool last = !share || slot == kTrSlots - 1;          // user of this tile
+                    if (!P.has(slot, k)) continue;
+                    const bool last = !P.share || slot == kTrSlots - 1;        // user of this tile
                     const int t = tiles[slot]++;
                     if (scores) {
-                        if (first) wait(&room.q_full[slot], queries[slot]++);
-                        wait(&room.k_full[ks], n / kTrKStages);
+                        wait(&room.k_full[ks], n / Lay::kKStages);
                         if (t > 0) wait(&room.o_done[slot], t - 1);
                         if (!ok) break;
                         tc_fence_after_sync();
+                        const uint64_t q = dq + (nq + (P.share ? slot : 0)) % kTrQStages * (Lay::kTile >> 4);
+                        const uint64_t key = dk + ks * (Lay::kTile >> 4);
                         if (elect_one()) {
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
                                 const uint64_t off = (kk >> 2) * (Lay::kHalf >> 4) + (kk & 3) * 2;
-                                mma_f16_ss(tmem + kTrKeys * slot, dq + slot * (Lay::kTile >> 4) + off,
-                                           dk + ks * (Lay::kTile >> 4) + off, kIdS, kk > 0);
+                                mma_f16_ss(tmem + kTrKeys * slot, q + off, key + off, kIdS, kk > 0);
                             }
                             mma_commit(&room.s_full[slot]);
                             if (last) mma_commit(&room.k_empty[ks]);
                         }
                         __syncwarp();
                     } else {
+                        const bool first = P.first(slot, k);
+                        wait(&room.v_full[vs], n / Lay::kVStages);
                         wait(&room.p_full[slot], t);
-                        wait(&room.v_full[vs], n / kTrVStages);
                         if (!ok) break;
                         tc_fence_after_sync();
+                        const uint64_t value = dv + vs * (Lay::kTile >> 4);
                         if (elect_one()) {
                             // keys 32 c .. 32 c + 31: hi parts in columns 32 c ..
                             // 32 c + 15, lo parts in the next sixteen
@@ -383,8 +521,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                                 for (int part = 0; part < 2; ++part)
                                     mma_f16_ts(tmem + 2 * kTrKeys + D * slot,
                                                tmem + kTrKeys * slot + 32 * (kk >> 1) + 8 * (kk & 1) + 16 * part,
-                                               dv + vs * (Lay::kTile >> 4) + kk * (16 * 128 >> 4), kIdPV,
-                                               !first || kk > 0 || part > 0);
+                                               value + kk * (16 * 128 >> 4), kIdPV, !first || kk > 0 || part > 0);
                             }
                             mma_commit(&room.o_done[slot]);
                             if (last) mma_commit(&room.v_empty[vs]);
@@ -393,13 +530,107 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     }
                 }
             }
+            if (scores && ok && elect_one()) {
+                for (int i = 0; i < P.query_tiles(); ++i) mma_commit(&room.q_empty[(nq + i) % kTrQStages]);
+            }
+            __syncwarp();
+            nq += P.query_tiles();
         }
         // the products are done before tensor memory and operands are given up
         if (elect_one()) mma_commit(&room.done[warp >> 1]);
         __syncwarp();
         ok = tr_wait(p, &room.done[warp >> 1], 0) && ok;
         if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
+    }
+    } else if (warp >= kTrLineWarp) {
+    control_registers();
+    if (warp == kTrLineWarp) {
+        // ------------------------------------------------------------------
+        // the trees' lines, a piece ahead of those who read them
+        // ------------------------------------------------------------------
+        bool ok = true;
+        for (int i = 0; ok && walk.next(p, side, P); ++i) {
+            uint32_t w[kLineWords][kLineWords] = {};
+            const bool tree = P.k1 * kTrKeys > P.s.L - P.s.C;      // the piece has some of it
+            if (tree) {
+                int up[kLineWords];
+#pragma unroll
+                for (int j = 0; j < kLineWords; ++j) {
+                    const int node = lane + 32 * j;
+                    up[j] = node < P.s.C ? tree_parent(p.parents, P.s.q0, node, p.err) : -1;
+                }
+                warp_lines(w, up, P.s.C);
+            }
+            if (i > 0) ok = tr_wait(p, &room.lines_empty, i - 1);
+            if (!ok) break;
+            if (tree) {
+#pragma unroll
+                for (int j = 0; j < kLineWords; ++j) room.line[lane + 32 * j] = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&room.lines_full);
+        }
+        if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
     } else {
+        // ------------------------------------------------------------------
+        // converters: a K tile's codes, then its V tile's, 16 at a time
+        // ------------------------------------------------------------------
+        if constexpr (kFp8) {
+            const int who = threadIdx.x - (kTrLineWarp + 1) * 32;
+            int n = 0;
+            bool ok = true;
+            while (ok && walk.next(p, side, P)) {
+                for (int k = P.k0; ok && k < P.k1; ++k, ++n) {
+#pragma unroll 1
+                    for (int kind = 0; ok && kind < 2; ++kind) {
+                        const int cs = n % kTrCodeStages;
+                        const int stages = kind == 0 ? Lay::kKStages : Lay::kVStages, st = n % stages;
+                        uint64_t* empty = kind == 0 ? &room.k_empty[st] : &room.v_empty[st];
+                        ok = tr_wait(p, kind == 0 ? &room.kc_full[cs] : &room.vc_full[cs], n / kTrCodeStages);
+                        if (ok && n >= stages) ok = tr_wait(p, empty, n / stages - 1);
+                        if (!ok) break;
+                        const uint8_t* src = smem + (kind == 0 ? Lay::kKCodes : Lay::kVCodes) + cs * Lay::kCodes;
+                        uint8_t* dst = smem + (kind == 0 ? Lay::kK : Lay::kV) + st * Lay::kTile;
+#pragma unroll 4
+                        for (int i = who; i < kTrKeys * 8; i += kTrConverters * 32) {
+                            const int r = i >> 3, c = i & 7;
+                            const uint4 x = lds128(src + r * 128 + ((c ^ (r & 7)) << 4));
+                            uint32_t y[8];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t codes = word_of(x, j);
+                                if constexpr (kBf16) {
+                                    y[2 * j] = e4m3x2_to<T>((uint16_t)(codes & 0xffffu));
+                                    y[2 * j + 1] = e4m3x2_to<T>((uint16_t)(codes >> 16));
+                                } else {
+                                    e4m3x4_to_f16x2x2(codes, y[2 * j], y[2 * j + 1]);
+                                }
+                            }
+                            // chunks 2c and 2c + 1 of the row's 16; the upper half's
+                            // threads store them the other way round, off the lower's banks
+                            uint8_t* row = dst + (c >> 2) * Lay::kHalf + r * 128;
+                            const int first = c >> 2;
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int which = j ^ first, chunk = ((2 * c + which) & 7) ^ (r & 7);
+                                const uint4 v = which ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
+                                *reinterpret_cast<uint4*>(row + (chunk << 4)) = v;
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(kind == 0 ? &room.k_full[st] : &room.v_full[st]);
+                            mbar_arrive(kind == 0 ? &room.kc_empty[cs] : &room.vc_empty[cs]);
+                        }
+                    }
+                }
+            }
+            if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
+        }
+    }
+    } else {
+        softmax_registers();
         // ------------------------------------------------------------------
         // softmax and epilogue: this thread owns row r of its slot's tiles
         // ------------------------------------------------------------------
@@ -409,6 +640,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const uint32_t tS = tmem + kTrKeys * slot + lanes_at;
         const uint32_t tO = tmem + 2 * kTrKeys + lanes_at;         // slot 0's, slot 1's D columns on
         const int barrier = 1 + slot, both = 3;                    // named barriers
+        const int in_tile = r / G, head = r - in_tile * G;
         const float sl = p.scale_log2;
         const uint64_t sl2 = f32x2_pack(sl, sl);
         bool failed = false;                  // a wait ran out: finish the loops without waiting
@@ -416,65 +648,45 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             if (!failed && !tr_wait(p, bar, phase)) failed = true;
         };
         int n = 0, t = 0;                     // tiles of the CTA and of the slot so far
-        while (walk.next(p, P)) {
-            const int query_tiles = tr_query_tiles(p, P.s.C, side);
-            if (query_tiles <= 0) continue;
-            const bool share = query_tiles == kTrSlots;
+        for (int piece = 0; walk.next(p, side, P); ++piece) {
             const int base = P.s.L - P.s.C;
-            const bool tree = P.k1 * kTrKeys > base;               // the piece has some of the tree
-            const int in_tile = r / G;
-            const int node = (kTrSlots * side + (share ? slot : 0)) * per_tile + in_tile;
+            const int count = P.k1 - P.k0, own = P.own(slot);
+            const int node = (kTrSlots * side + (P.share ? slot : 0)) * per_tile + in_tile;
             const bool valid = in_tile < per_tile && node < P.s.C;
             const bool live = __any_sync(0xffffffffu, valid);      // a warp without rows only keeps step
-            const int64_t row = (int64_t)(P.s.q0 + node) * p.num_q_heads + P.g * G + (r - in_tile * G);
-            const int count = P.k1 - P.k0;
-            const int own = share ? count : (count + 1 - slot) / 2;
-            // this row of Q (zero where there is none), laid out like a K tile
-            if (own > 0) {
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + row * D);
-                uint8_t* dst = smem + Lay::kQ + slot * Lay::kTile;
-#pragma unroll
-                for (int c0 = 0; c0 < D / 8; c0 += 8) {
-                    uint4 v[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) v[c] = valid ? __ldg(src + c0 + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4*>(dst + (c0 >> 3) * Lay::kHalf + r * 128 + ((c ^ (r & 7)) << 4)) = v[c];
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&room.q_full[slot]);
-            }
             TreeLine line{};
-            if (tree) {
-                // the tree's lines, made by slot 0 for both; the next pair's
-                // come after another barrier that both slots meet
-                if (slot == 0) {
-                    const int up = r < P.s.C ? tree_parent(p.parents, P.s.q0, r, p.err) : -1;
-                    tree_line(room.lines, r, P.s.C, up, [&](bool more) { return bar_or(barrier, kTrRows, more); });
-                }
-                bar_sync(both, 2 * kTrRows);
-                if (valid) {
-                    const uint4 w = room.lines.line[node];
-                    line = TreeLine{{w.x, w.y, w.z, w.w}};
+            wait(&room.lines_full, piece);
+            if (valid && P.k1 * kTrKeys > base) {
+                const uint4 w = room.line[node];
+                line = TreeLine{{w.x, w.y, w.z, w.w}};
+            }
+            if (P.alone) {                                         // else the statistics come there first
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&room.lines_empty);
+                if (own == 0) {
+                    n += count;
+                    continue;
                 }
             }
             float m = -INFINITY, l = 0.f;
             bool bad = false;                 // V of the tree has elements that are not finite
             for (int k = P.k0, j = 0; k < P.k1; ++k, ++n) {
-                if (!share && ((k - P.k0) & 1) != slot) continue;
-                const int key0 = k * kTrKeys, vs = n % kTrVStages;
+                if (!P.has(slot, k)) continue;
+                const int key0 = k * kTrKeys, vs = n % Lay::kVStages;
                 const bool masked = key0 + kTrKeys > base;
+                // S waited for this slot's P V before, so that V of the tile two
+                // before this one, in the same stage, has been there too: the
+                // wait for V below cannot take its phase for this tile's
+                wait(&room.s_full[slot], t);
+                tc_fence_after_sync();
                 if (masked) {
                     // V rows past the context may hold anything: clear them.
                     // Of the tree's, elements that are not finite are cleared
                     // too, since the tensor cores would carry them into rows
                     // that do not see them; rows that do get them back below.
-                    const bool mine = !share || slot == 0;
                     bool odd = false;
-                    if (mine) {
-                        wait(&room.v_full[vs], n / kTrVStages);
+                    if (!P.share || slot == 0) {
+                        wait(&room.v_full[vs], n / Lay::kVStages);
                         uint8_t* vd = smem + Lay::kV + vs * Lay::kTile + r * 128;
                         const int key = key0 + r;
                         if (key >= P.s.L) {
@@ -485,7 +697,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                             uint32_t any = 0u;
 #pragma unroll
                             for (int c = 0; c < D / 8; ++c) {
-                                const uint4 w = *reinterpret_cast<const uint4*>(vd + (c >> 3) * Lay::kHalf + ((c & 7) << 4));
+                                // each row's chunks from another one on: no two on one bank
+                                const uint4 w = lds128(vd + (c >> 3) * Lay::kHalf + (((c ^ r) & 7) << 4));
                                 any |= not_finite<T>(w.x) | not_finite<T>(w.y) | not_finite<T>(w.z) | not_finite<T>(w.w);
                             }
                             if (any != 0u) {
@@ -499,79 +712,68 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         }
                         fence_proxy_async_smem();
                     }
-                    bad |= share ? bar_or(both, 2 * kTrRows, odd) : bar_or(barrier, kTrRows, odd);
+                    bad |= P.share ? bar_or(both, 2 * kTrRows, odd) : bar_or(barrier, kTrRows, odd);
                 }
-                wait(&room.s_full[slot], t);
-                tc_fence_after_sync();
                 if (live) {
-                    uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+                    uint32_t x[kTrKeys];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * c));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(x + 32 * c));
                     if (masked) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) seen[c] = seen_word(line, key0 + 32 * c - base);
-                    }
-                    auto hide = [&](uint32_t(&v)[32], int c) {
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t seen = seen_word(line, key0 + 32 * c - base);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = (seen[c] >> e) & 1u ? v[e] : 0xff800000u;
-                    };
-                    // the row's maximum on the raw scores (the scale is positive)
-                    float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    uint32_t v[2][32];
-                    tmem_ld32(tS, v[0]);
-                    tmem_wait_ld(v[0]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t(&x)[32] = v[c & 1];
-                        if (c < 3) tmem_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
-                        if (masked) hide(x, c);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                pm[i] = fmaxf(fmaxf(pm[i], __uint_as_float(x[e + i])), __uint_as_float(x[e + 4 + i]));
+                            for (int e = 0; e < 32; ++e) x[32 * c + e] = (seen >> e) & 1u ? x[32 * c + e] : 0xff800000u;
                         }
-                        if (c < 3) tmem_wait_ld(v[(c + 1) & 1]);
                     }
-                    const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * sl;
+                    // the row's maximum on the raw scores (the scale is positive)
+                    float pm[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) pm[e] = __uint_as_float(x[e]);
+#pragma unroll
+                    for (int e = 8; e < kTrKeys; e += 8) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) pm[i] = fmaxf(pm[i], __uint_as_float(x[e + i]));
+                    }
+                    const float mx = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
+                                           fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7]))) * sl;
                     const bool raise = mx > m + kRaise;            // the first finite maximum, too
-                    const float m_new = raise ? mx - kBelow : m;
                     if (__any_sync(0xffffffffu, raise)) {
+                        const float m_new = raise ? mx - kBelow : m;
                         const float f = raise ? ex2(m - m_new) : 1.f;
                         l *= f;
+                        m = m_new;
                         if (j > 0) {                               // the P V before is done: S waited for it
                             wait(&room.o_done[slot], t - 1);
                             tc_fence_after_sync();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + D * slot + c, o);
+                                tmem_wait_ld16(o);
 #pragma unroll
-                            for (int c = 0; c < D / 32; ++c) {
-                                tmem_ld32(tO + D * slot + 32 * c, v[0]);
-                                tmem_wait_ld(v[0]);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) v[0][e] = __float_as_uint(__uint_as_float(v[0][e]) * f);
-                                tmem_st32(tO + D * slot + 32 * c, v[0]);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st16(tO + D * slot + c, o);
                             }
                         }
-                        m = m_new;
                     }
                     const float ref = m == -INFINITY ? 0.f : m;    // nothing seen yet
                     const uint64_t neg2 = f32x2_pack(-ref, -ref);
                     uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
-                    tmem_ld32(tS, v[0]);
-                    tmem_wait_ld(v[0]);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t(&x)[32] = v[c & 1];
-                        if (c < 3) tmem_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
-                        if (masked) hide(x, c);
                         uint32_t parts[32];                        // hi, then lo
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float a0, a1;
-                            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
-                                                   sl2, neg2), a0, a1);
+                            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[32 * c + 2 * i]),
+                                                              __uint_as_float(x[32 * c + 2 * i + 1])), sl2, neg2), a0, a1);
                             const float p0 = ex2(a0), p1 = ex2(a1);
                             ps[i & 3] = f32x2_add(ps[i & 3], f32x2_pack(p0, p1));
                             split_pair<M>(p0, p1, parts[i], parts[16 + i]);
                         }
-                        if (c < 3) tmem_wait_ld(v[(c + 1) & 1]);
                         tmem_st32(tS + 32 * c, parts);
                     }
                     float q8[8];
@@ -585,14 +787,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 if (lane == 0) mbar_arrive(&room.p_full[slot]);
                 ++t, ++j;
             }
-            // ---- the pair's (or piece's) end --------------------------------
+            // ---- the piece's end ----------------------------------------------
             if (own > 0) wait(&room.o_done[slot], t - 1);
             tc_fence_after_sync();
             const bool full = count == P.n;
-            const int64_t rec = (((int64_t)cta * p.lanes + side) * 2 + (P.begin < range_begin ? 0 : 1)) * kTrSlots +
-                                (share ? slot : 0);
-            float w0 = 1.f, w1 = 0.f, M_ = m;
-            if (!share) {
+            const int64_t rec = (((int64_t)cta * p.lanes + side) * 2 + (P.k0 > 0 ? 0 : 1)) * kTrSlots + (P.share ? slot : 0);
+            float w0 = slot == 0 ? 1.f : 0.f, w1 = 1.f - w0, top = m;
+            if (!P.alone) {
                 // both slots have this row: joined, a half of the dims each
                 bar_sync(both, 2 * kTrRows);                       // the lines are not read any more
                 room.ml[slot][r] = make_float2(m, l);
@@ -600,46 +801,36 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 bad = bar_or(both, 2 * kTrRows, bad);
                 tc_fence_after_sync();
                 const float2 a = room.ml[0][r], b = room.ml[1][r];
-                M_ = fmaxf(a.x, b.x);
-                const float ref = M_ == -INFINITY ? 0.f : M_;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&room.lines_empty);
+                top = fmaxf(a.x, b.x);
+                const float ref = top == -INFINITY ? 0.f : top;
                 w0 = ex2(a.x - ref), w1 = ex2(b.x - ref);
                 l = a.y * w0 + b.y * w1;
-            } else if (slot == 1) {
-                w0 = 0.f, w1 = 1.f;
             }
-            const int from = share ? 0 : slot * (D / 2), to = share ? D : from + D / 2;
-            const float norm = full ? 1.f / l : 1.f;
-            const bool use0 = !share || slot == 0, use1 = share ? slot == 1 : count > 1;
+            const int from = P.alone ? 0 : slot * (D / 2), to = P.alone ? D : from + D / 2;
+            const float norm = full ? (kFp8 ? p.v_scale : 1.f) / l : 1.f;
+            const bool use0 = !P.alone || slot == 0, use1 = !P.alone || slot == 1;
             w0 *= norm, w1 *= norm;
+            const int64_t row = (int64_t)(P.s.q0 + node) * p.num_q_heads + P.g * G + head;
 #pragma unroll 1
             for (int d = from; live && d < to; d += 32) {
-                uint32_t v[2][32];
-                if (use0) tmem_ld32(tO + d, v[0]);
-                if (use1) tmem_ld32(tO + D + d, v[1]);
-                tmem_wait_ld(v[0]);
-                tmem_wait_ld(v[1]);
                 float o[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    o[e] = (use0 ? __uint_as_float(v[0][e]) * w0 : 0.f) + (use1 ? __uint_as_float(v[1][e]) * w1 : 0.f);
-                if (bad && valid) {
-                    // what was taken out of V, for a row that sees it: the sums
-                    // are what adding it gives
-                    for (int i = 0; i < P.s.C; ++i) {
-                        const int key = base + i;
-                        if (!line.has(i) || key < P.k0 * kTrKeys || key >= P.k1 * kTrKeys) continue;
-                        const int blk = p.block_tables[(size_t)P.b * p.max_blocks_per_seq + key / p.block_size];
-                        if (blk < 0 || blk >= p.num_blocks) continue;
-                        const T* src = static_cast<const T*>(p.v_cache) +
-                                       (((int64_t)blk * p.block_size + key % p.block_size) * p.num_kv_heads + P.g) * D + d;
+                for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                uint32_t v[32];
+                if (use0) {
+                    tmem_ld32(tO + d, v);
+                    tmem_wait_ld(v);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float x = (float)src[e];
-                            if (!isfinite(x)) o[e] += x;
-                        }
-                    }
+                    for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * w0;
                 }
-                __syncwarp();
+                if (use1) {
+                    tmem_ld32(tO + D + d, v);
+                    tmem_wait_ld(v);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(v[e]), w1, o[e]);
+                }
                 if (!valid || failed) {
                 } else if (full) {
                     uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * D + d);
@@ -655,10 +846,36 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 }
                 __syncwarp();
             }
-            if (!full && valid && !failed && (share || slot == 0)) p.rec_ml[rec * kTrRows + r] = make_float2(M_, l);
-            // O of both slots is read, and the statistics: the next pair may begin
+            if (bad && valid && !failed) {
+                // what was taken out of V, for a row that sees it: the sums are
+                // what adding it gives
+                for (int i = 0; i < P.s.C; ++i) {
+                    const int key = base + i;
+                    if (!line.has(i) || key < P.k0 * kTrKeys || key >= P.k1 * kTrKeys) continue;
+                    const int blk = p.block_tables[(size_t)P.b * p.max_blocks_per_seq + key / p.block_size];
+                    if (blk < 0 || blk >= p.num_blocks) continue;
+                    const int64_t at = (((int64_t)blk * p.block_size + key % p.block_size) * p.num_kv_heads + P.g) * D;
+#pragma unroll 1
+                    for (int d = from; d < to; ++d) {
+                        float y;
+                        if constexpr (kFp8)
+                            y = (static_cast<const uint8_t*>(p.v_cache)[at + d] & 0x7f) == 0x7f ? NAN : 0.f;
+                        else
+                            y = (float)static_cast<const T*>(p.v_cache)[at + d];
+                        if (isfinite(y)) continue;
+                        if (full) {
+                            T& o = static_cast<T*>(p.out)[row * D + d];
+                            o = from_float<T>((float)o + y);
+                        } else {
+                            p.rec_o[(rec * kTrRows + r) * D + d] += y;
+                        }
+                    }
+                }
+            }
+            if (!full && valid && !failed && (P.alone || slot == 0)) p.rec_ml[rec * kTrRows + r] = make_float2(top, l);
+            // O of both slots is read: the next piece's products may overwrite it
             tc_fence_before_sync();
-            if (!share) bar_sync(both, 2 * kTrRows);
+            if (!P.alone) bar_sync(both, 2 * kTrRows);
         }
         if (failed && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
     }
@@ -677,7 +894,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 constexpr int kTrMergeThreads = 256;
 constexpr int kTrMergeRows = 32;               // of a CTA
 
-template <typename T, int D>
+template <typename T, int D, bool kFp8>
 __global__ void __launch_bounds__(kTrMergeThreads)
     tree_merge_kernel(const __grid_constant__ TreeParams p) {
     constexpr int kDims = D / 32;
@@ -697,12 +914,12 @@ __global__ void __launch_bounds__(kTrMergeThreads)
         if (i < b) before += w;
     }
     const TrDeal deal(p, __reduce_add_sync(0xffffffffu, all));
-    const unsigned tiles = TrWalk::tiles(s), begin = __reduce_add_sync(0xffffffffu, before) + g * tiles;
-    const unsigned c0 = deal.cta_of(begin), c1 = deal.cta_of(begin + tiles - 1);
+    const unsigned each = TrWalk::each(p, s), begin = __reduce_add_sync(0xffffffffu, before) + g * each;
+    const unsigned c0 = deal.cta_of(begin + kTrPairWeight), c1 = deal.cta_of(begin + each - 1);
     if (c0 == c1) return;                      // written by that CTA
     const int side = tile / kTrSlots;
-    const int query_tiles = tr_query_tiles(p, s.C, side);
-    const int slot = query_tiles == kTrSlots ? tile % kTrSlots : 0;
+    // query tiles 2 side and 2 side + 1 are the slots', a last one alone is the first's
+    const int slot = tile % kTrSlots;
     for (int r = r0 + warp; r < r0 + kTrMergeRows; r += kTrMergeThreads / 32) {
         const int in_tile = r / G, node = tile * per_tile + in_tile;
         if (in_tile >= per_tile || node >= s.C) break;
@@ -715,7 +932,7 @@ __global__ void __launch_bounds__(kTrMergeThreads)
             for (int i = 0; i < kAhead; ++i) {
                 ml[i] = make_float2(-INFINITY, 0.f);
                 if (c + i > c1) continue;
-                const int64_t rec = (((int64_t)(c + i) * p.lanes + side) * 2 + (begin < deal.begin(c + i) ? 0 : 1)) * kTrSlots + slot;
+                const int64_t rec = (((int64_t)(c + i) * p.lanes + side) * 2 + (c + i == c0 ? 1 : 0)) * kTrSlots + slot;
                 ml[i] = p.rec_ml[rec * kTrRows + r];
                 const float* src = p.rec_o + (rec * kTrRows + r) * D + kDims * lane;
                 if constexpr (kDims == 4) {
@@ -743,7 +960,7 @@ __global__ void __launch_bounds__(kTrMergeThreads)
                 for (int k = 0; k < kDims; ++k) o[k] += w * v[i][k];
             }
         }
-        const float norm = 1.f / l;
+        const float norm = (kFp8 ? p.v_scale : 1.f) / l;
         T* dst = static_cast<T*>(p.out) + ((int64_t)(s.q0 + node) * p.num_q_heads + g * G + (r - in_tile * G)) * D + kDims * lane;
         using M = Mma<T>;
         if constexpr (kDims == 4)
@@ -760,7 +977,7 @@ size_t tree_plan(TreeParams& p, int head_dim, void* workspace) {
     const int tiles = (p.max_context + kTrKeys - 1) / kTrKeys;
     p.lanes = query_tiles > kTrSlots ? (query_tiles + kTrSlots - 1) / kTrSlots : 1;
     p.whole = tiles <= kTrWholeTiles;
-    const int64_t most = p.whole ? pairs : (pairs * tiles + kTrMinTiles - 1) / kTrMinTiles;
+    const int64_t most = p.whole ? pairs : (pairs * (tiles + kTrPairWeight) + kTrMinTiles - 1) / kTrMinTiles;
     p.ctas = (int)(most < kTrCtas / p.lanes ? (most > 0 ? most : 1) : kTrCtas / p.lanes);
     const size_t rows = p.whole ? 0 : (size_t)p.ctas * p.lanes * 2 * kTrSlots * kTrRows;
     p.rec_o = static_cast<float*>(workspace);
@@ -768,30 +985,33 @@ size_t tree_plan(TreeParams& p, int head_dim, void* workspace) {
     return rows * (head_dim * sizeof(float) + sizeof(float2)) + 16;
 }
 
-cudaError_t launch_tree_codes(int dtype, const TreeParams& p, cudaStream_t stream);
-
-template <typename T, int D>
-cudaError_t launch_tree_t(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreeParams& p, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         tr_smem<D>());
+template <typename T, int D, bool kFp8>
+cudaError_t launch_tree_t(const CUtensorMap& tmk, const CUtensorMap& tmv, const CUtensorMap& tmq, const TreeParams& p,
+                          cudaStream_t stream) {
+    constexpr int kSmem = tr_smem<D, kFp8>();
+    cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<T, D, kFp8>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_with_pdl(tree_attention_kernel<T, D>, dim3((unsigned)(p.ctas * p.lanes)), dim3(kTrThreads), tr_smem<D>(),
-                        stream, tmk, tmv, p);
+    e = launch_with_pdl(tree_attention_kernel<T, D, kFp8>, dim3((unsigned)(p.ctas * p.lanes)), dim3(kTrThreads), kSmem,
+                        stream, tmk, tmv, tmq, p);
     if (e != cudaSuccess || p.whole) return e;
     const int per_tile = kTrRows / p.group, query_tiles = (p.max_query + per_tile - 1) / per_tile;
-    return launch_with_pdl(tree_merge_kernel<T, D>,
+    return launch_with_pdl(tree_merge_kernel<T, D, kFp8>,
                            dim3((unsigned)(p.num_seqs * p.num_kv_heads), (unsigned)(query_tiles * (kTrRows / kTrMergeRows))),
                            dim3(kTrMergeThreads), 0, stream, p);
 }
 
-cudaError_t launch_tree_attention(int dtype, int head_dim, bool fp8, const CUtensorMap& tmk,
-                                  const CUtensorMap& tmv, const TreeParams& p, cudaStream_t stream) {
+cudaError_t launch_tree_attention(int dtype, int head_dim, bool fp8, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                                  const CUtensorMap& tmq, const TreeParams& p, cudaStream_t stream) {
     const bool bf16 = dtype == PA_BF16;
-    if (fp8) return launch_tree_codes(dtype, p, stream);
-    if (head_dim == 64) return bf16 ? launch_tree_t<__nv_bfloat16, 64>(tmk, tmv, p, stream)
-                                    : launch_tree_t<__half, 64>(tmk, tmv, p, stream);
-    return bf16 ? launch_tree_t<__nv_bfloat16, 128>(tmk, tmv, p, stream)
-                : launch_tree_t<__half, 128>(tmk, tmv, p, stream);
+    if (fp8) return bf16 ? launch_tree_t<__nv_bfloat16, 128, true>(tmk, tmv, tmq, p, stream)
+                         : launch_tree_t<__half, 128, true>(tmk, tmv, tmq, p, stream);
+    if (head_dim == 64) return bf16 ? launch_tree_t<__nv_bfloat16, 64, false>(tmk, tmv, tmq, p, stream)
+                                    : launch_tree_t<__half, 64, false>(tmk, tmv, tmq, p, stream);
+    return bf16 ? launch_tree_t<__nv_bfloat16, 128, false>(tmk, tmv, tmq, p, stream)
+                : launch_tree_t<__half, 128, false>(tmk, tmv, tmq, p, stream);
 }
+
+int tree_nodes_per_tile(int group) { return kTrRows / group; }
 
 }  // namespace pa

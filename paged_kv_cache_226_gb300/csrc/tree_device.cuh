@@ -38,7 +38,10 @@ constexpr int kLineWords = PA_TREE_NODES / 32;
 // A node's line: itself and its ancestors, a bit per node.
 struct TreeLine {
     uint32_t w[kLineWords];
-    __device__ __forceinline__ bool has(int i) const { return (w[i >> 5] >> (i & 31)) & 1u; }
+    __device__ __forceinline__ bool has(int i) const {
+        const uint32_t lo = i & 32 ? w[1] : w[0], hi = i & 32 ? w[3] : w[2];
+        return ((i & 64 ? hi : lo) >> (i & 31)) & 1u;
+    }
 };
 
 // The lines of a tree's C nodes, thread `i` of kLineThreads making node i's:

@@ -44,7 +44,10 @@ struct TreeParams {
 // sizes: num_seqs, num_kv_heads, group, max_context, max_query).
 size_t tree_plan(TreeParams& p, int head_dim, void* workspace);
 cudaError_t launch_tree_attention(int dtype, int head_dim, bool fp8, const CUtensorMap& tmk,
-                                  const CUtensorMap& tmv, const TreeParams& p, cudaStream_t stream);
+                                  const CUtensorMap& tmv, const CUtensorMap& tmq, const TreeParams& p,
+                                  cudaStream_t stream);
+// Nodes of a query tile, the box of its map.
+int tree_nodes_per_tile(int group);
 
 struct AcceptParams {
     const int64_t* draft;          // [T]
