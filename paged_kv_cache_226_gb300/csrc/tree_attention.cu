@@ -87,7 +87,7 @@ struct TrRoom {
     uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
     uint64_t kc_full[kTrCodeStages], kc_empty[kTrCodeStages], vc_full[kTrCodeStages], vc_empty[kTrCodeStages];
     uint64_t q_full[kTrQStages], q_empty[kTrQStages], lines_full, lines_empty;
-    uint64_t s_full[kTrSlots], p_full[kTrSlots], o_done[kTrSlots], done[2];
+    uint64_t s_full[kTrSlots], p_full[kTrSlots][2], o_done[kTrSlots], done[2];
     uint32_t tmem;
 };
 
@@ -109,6 +109,15 @@ __device__ __forceinline__ constexpr bool tr_withheld(const TreeParams&, int) { 
 __device__ __forceinline__ bool tr_wait(const TreeParams& p, uint64_t* bar, int phase) {
     return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, tr_wait_limit(p)));
 }
+
+// A ring's stage and lap, tile by tile.
+template <int kStages>
+struct TrRing {
+    int at = 0, lap = 0;
+    __device__ __forceinline__ void step() {
+        if (++at == kStages) at = 0, ++lap;
+    }
+};
 
 // A run of key tiles [k0, k1) of one pair of n tiles.
 struct TrPiece {
@@ -235,7 +244,7 @@ __device__ __forceinline__ void split_pair(float p0, float p1, uint32_t& hi, uin
     hi = M::pack(p0, p1);
     const float2 u = M::unpack(hi);
     float d0, d1;
-    f32x2_unpack(f32x2_add(f32x2_pack(p0, p1), f32x2_pack(-u.x, -u.y)), d0, d1);
+    f32x2_unpack(f32x2_fma(f32x2_pack(u.x, u.y), f32x2_pack(-1.f, -1.f), f32x2_pack(p0, p1)), d0, d1);
     lo = M::pack(d0, d1);
 }
 
@@ -374,7 +383,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         for (int i = 0; i < kTrQStages; ++i) mbar_init(&room.q_full[i], 1), mbar_init(&room.q_empty[i], 1);
         mbar_init(&room.lines_full, 1), mbar_init(&room.lines_empty, kTrSoftmaxWarps);
         for (int i = 0; i < kTrSlots; ++i) {
-            mbar_init(&room.p_full[i], 4);
+            mbar_init(&room.p_full[i][0], 4), mbar_init(&room.p_full[i][1], 4);
             mbar_init(&room.s_full[i], 1), mbar_init(&room.o_done[i], 1);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&room.done[i], 1);
@@ -400,70 +409,82 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         // pair's; lane i has box i of eight.  Warp 0 also loads a piece's
         // query tiles, before its keys.
         // ------------------------------------------------------------------
-        const bool keys = warp == 0;
-        const CUtensorMap* map = keys ? &tmap_k : &tmap_v;
-        uint64_t* full = kFp8 ? (keys ? room.kc_full : room.vc_full) : (keys ? room.k_full : room.v_full);
-        uint64_t* empty = kFp8 ? (keys ? room.kc_empty : room.vc_empty) : (keys ? room.k_empty : room.v_empty);
-        uint8_t* ring = smem + (kFp8 ? (keys ? Lay::kKCodes : Lay::kVCodes) : (keys ? Lay::kK : Lay::kV));
-        const int stages = kFp8 ? kTrCodeStages : (keys ? Lay::kKStages : Lay::kVStages);
-        constexpr int kStage = kFp8 ? Lay::kCodes : Lay::kTile, kBoxes = kFp8 ? 1 : Lay::kHalves;
-        if (lane == 0) prefetch_tensor_map(map);
-        if (keys && lane == 0) prefetch_tensor_map(&tmap_q);
-        int n = 0, nq = 0;
-        bool ok = true, held = false;
-        while (ok && !held && walk.next(p, side, P)) {
-            const int32_t* table = p.block_tables + (size_t)P.b * p.max_blocks_per_seq;
-            // block ids: lane i has box i % 8 of tile i / 8 of four, the next
-            // four tiles' requested while these are loaded
-            auto ids = [&](int k) {
-                const int tok = k * kTrKeys + 16 * lane;
-                return tok < P.s.L ? __ldg(table + tok / p.block_size) : 0;
-            };
-            int blk = 0, ahead = ids(P.k0);
-            for (int i = 0; keys && ok && i < P.query_tiles(); ++i, ++nq) {
-                const int st = nq % kTrQStages;
-                if (nq >= kTrQStages) ok = tr_wait(p, &room.q_empty[st], nq / kTrQStages - 1);
-                if (!ok) break;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(&room.q_full[st], (uint32_t)(per_tile * G * Lay::kHalves * 128));
+        auto load = [&](auto kind) {
+            constexpr bool keys = decltype(kind)::value;
+            constexpr int kStages = kFp8 ? kTrCodeStages : (keys ? Lay::kKStages : Lay::kVStages);
+            constexpr int kStage = kFp8 ? Lay::kCodes : Lay::kTile, kBoxes = kFp8 ? 1 : Lay::kHalves;
+            const CUtensorMap* map = keys ? &tmap_k : &tmap_v;
+            uint64_t* full = kFp8 ? (keys ? room.kc_full : room.vc_full) : (keys ? room.k_full : room.v_full);
+            uint64_t* empty = kFp8 ? (keys ? room.kc_empty : room.vc_empty) : (keys ? room.k_empty : room.v_empty);
+            uint8_t* ring = smem + (kFp8 ? (keys ? Lay::kKCodes : Lay::kVCodes) : (keys ? Lay::kK : Lay::kV));
+            if (lane == 0) prefetch_tensor_map(map);
+            if (keys && lane == 0) prefetch_tensor_map(&tmap_q);
+            const int block_shift = p.block_size == 16 ? 4 : 5, sub = (16 * lane) & (p.block_size - 1);
+            int n = 0;
+            TrRing<kStages> at;
+            TrRing<kTrQStages> q;
+            bool ok = true, held = false;
+            while (ok && !held && walk.next(p, side, P)) {
+                const int32_t* table = p.block_tables + (size_t)P.b * p.max_blocks_per_seq;
+                // block ids: lane i has box i % 8 of tile i / 8 of four, the next
+                // four tiles' requested while these are loaded
+                auto ids = [&](int k) {
+                    const int tok = k * kTrKeys + 16 * lane;
+                    return tok < P.s.L ? __ldg(table + (tok >> block_shift)) : 0;
+                };
+                int blk = 0, ahead = ids(P.k0);
+                for (int i = 0; keys && ok && i < P.query_tiles(); ++i, q.step()) {
+                    if (q.lap > 0) ok = tr_wait(p, &room.q_empty[q.at], q.lap - 1);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&room.q_full[q.at], (uint32_t)(per_tile * G * Lay::kHalves * 128));
 #pragma unroll
-                    for (int h = 0; h < Lay::kHalves; ++h)
-                        tma_load_3d(smem + Lay::kQ + st * Lay::kTile + h * Lay::kHalf, &tmap_q, &room.q_full[st],
-                                    h * kBoxElems, P.g * G, P.s.q0 + (kTrSlots * side + i) * per_tile);
+                        for (int h = 0; h < Lay::kHalves; ++h)
+                            tma_load_3d(smem + Lay::kQ + q.at * Lay::kTile + h * Lay::kHalf, &tmap_q, &room.q_full[q.at],
+                                        h * kBoxElems, P.g * G, P.s.q0 + (kTrSlots * side + i) * per_tile);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-            }
-            for (int k = P.k0; ok && k < P.k1; ++k, ++n) {
-                const int in = (k - P.k0) & 3;
-                if (in == 0) {
-                    blk = ahead;
-                    ahead = ids(k + 4);
-                    if (16 * lane + k * kTrKeys < min(P.s.L, P.k1 * kTrKeys) && (blk < 0 || blk >= p.num_blocks))
-                        flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
-                }
-                const int st = n % stages;
-                if (n >= stages) ok = tr_wait(p, &empty[st], n / stages - 1);
-                held = tr_withheld(p, n);
-                if (!ok || held) break;
-                const int boxes = min(8, (P.s.L - k * kTrKeys + 15) / 16);
-                if (elect_one()) mbar_arrive_expect_tx(&full[st], (uint32_t)(boxes * kBoxes * kBox16Bytes));
-                __syncwarp();
-                const int id = __shfl_sync(0xffffffffu, blk, in * 8 + (lane & 7));
-                if (lane < boxes) {
-                    uint8_t* dst = ring + st * kStage + lane * kBox16Bytes;
+                for (int k = P.k0; ok && k < P.k1; ++k, ++n, at.step()) {
+                    const int in = (k - P.k0) & 3;
+                    if (in == 0) {
+                        blk = ahead;
+                        ahead = ids(k + 4);
+                        if (16 * lane + k * kTrKeys < min(P.s.L, P.k1 * kTrKeys) && (blk < 0 || blk >= p.num_blocks))
+                            flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
+                    }
+                    if (at.lap > 0) ok = tr_wait(p, &empty[at.at], at.lap - 1);
+                    held = tr_withheld(p, n);
+                    if (!ok || held) break;
+                    const int boxes = min(8, (P.s.L - k * kTrKeys + 15) / 16);
+                    if (elect_one()) mbar_arrive_expect_tx(&full[at.at], (uint32_t)(boxes * kBoxes * kBox16Bytes));
+                    __syncwarp();
+                    const int id = __shfl_sync(0xffffffffu, blk, in * 8 + (lane & 7));
+                    if (lane < boxes) {
+                        uint8_t* dst = ring + at.at * kStage + lane * kBox16Bytes;
 #pragma unroll
-                    for (int h = 0; h < kBoxes; ++h)
-                        tma_load_4d(dst + h * Lay::kHalf, map, &full[st], h * kBoxElems, P.g,
-                                    (16 * lane) & (p.block_size - 1), id);
+                        for (int h = 0; h < kBoxes; ++h)
+                            tma_load_4d(dst + h * Lay::kHalf, map, &full[at.at], h * kBoxElems, P.g, sub, id);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
-        }
-        // the last copies have landed before the CTA gives its memory up
-        for (int st = 0; st < stages && st < n; ++st) ok = tr_wait(p, &full[st], (n - 1 - st) / stages) && ok;
-        for (int st = 0; st < kTrQStages && st < nq; ++st)
-            ok = tr_wait(p, &room.q_full[st], (nq - 1 - st) / kTrQStages) && ok;
-        if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
+            // the last copies have landed before the CTA gives its memory up:
+            // the stages of this lap, then the others of the lap before
+            for (int st = 0; st < kStages; ++st) {
+                const int lap = st < at.at ? at.lap : at.lap - 1;
+                if (lap >= 0) ok = tr_wait(p, &full[st], lap) && ok;
+            }
+            for (int st = 0; keys && st < kTrQStages; ++st) {
+                const int lap = st < q.at ? q.lap : q.lap - 1;
+                if (lap >= 0) ok = tr_wait(p, &room.q_full[st], lap) && ok;
+            }
+            if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
+        };
+        if (warp == 0)
+            load(std::true_type());
+        else
+            load(std::false_type());
     } else {
         // ------------------------------------------------------------------
         // issuers: S (warp 1) and P V (warp 3), tile by tile and slot by slot.
@@ -471,70 +492,85 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         // ------------------------------------------------------------------
         constexpr uint32_t kIdS = idesc_f16(kTrRows, kTrKeys, kBf16, false);
         constexpr uint32_t kIdPV = idesc_f16(kTrRows, D, kBf16, true);
-        const bool scores = warp == 1;
         const uint64_t dq = smem_desc_sw128(smem_u32(smem + Lay::kQ), 16, 1024);
         const uint64_t dk = smem_desc_sw128(smem_u32(smem + Lay::kK), 16, 1024);
         const uint64_t dv = smem_desc_sw128(smem_u32(smem + Lay::kV), Lay::kHalf, 1024);
-        int n = 0, nq = 0, tiles[kTrSlots] = {0, 0};
+        int tiles[kTrSlots] = {0, 0};
         bool ok = true;
         auto wait = [&](uint64_t* bar, int phase) { ok = ok && tr_wait(p, bar, phase); };
-        while (ok && walk.next(p, side, P)) {
-            for (int i = 0; scores && i < P.query_tiles(); ++i)
-                wait(&room.q_full[(nq + i) % kTrQStages], (nq + i) / kTrQStages);
-            for (int k = P.k0; ok && k < P.k1; ++k, ++n) {
-                const int ks = n % Lay::kKStages, vs = n % Lay::kVStages;
+        if (warp == 1) {
+            TrRing<Lay::kKStages> at;
+            TrRing<kTrQStages> q;
+            while (ok && walk.next(p, side, P)) {
+                const TrRing<kTrQStages> q0 = q;
+                for (int i = 0; i < P.query_tiles(); ++i, q.step()) wait(&room.q_full[q.at], q.lap);
+                for (int k = P.k0; ok && k < P.k1; ++k, at.step()) {
+                    wait(&room.k_full[at.at], at.lap);
 #pragma unroll
-                for (int slot = 0; slot < kTrSlots; ++slot) {
-                    if (!P.has(slot, k)) continue;
-                    const bool last = !P.share || slot == kTrSlots - 1;        // user of this tile
-                    const int t = tiles[slot]++;
-                    if (scores) {
-                        wait(&room.k_full[ks], n / Lay::kKStages);
-                        if (t > 0) wait(&room.o_done[slot], t - 1);
+                    for (int slot = 0; slot < kTrSlots; ++slot) {
+                        if (!P.has(slot, k)) continue;
+                        if (tiles[slot] > 0) wait(&room.o_done[slot], tiles[slot] - 1);
                         if (!ok) break;
+                        ++tiles[slot];
                         tc_fence_after_sync();
-                        const uint64_t q = dq + (nq + (P.share ? slot : 0)) % kTrQStages * (Lay::kTile >> 4);
-                        const uint64_t key = dk + ks * (Lay::kTile >> 4);
+                        const uint64_t query = dq + ((q0.at + (P.share ? slot : 0)) & (kTrQStages - 1)) * (Lay::kTile >> 4);
+                        const uint64_t key = dk + at.at * (Lay::kTile >> 4);
                         if (elect_one()) {
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
                                 const uint64_t off = (kk >> 2) * (Lay::kHalf >> 4) + (kk & 3) * 2;
-                                mma_f16_ss(tmem + kTrKeys * slot, q + off, key + off, kIdS, kk > 0);
+                                mma_f16_ss(tmem + kTrKeys * slot, query + off, key + off, kIdS, kk > 0);
                             }
                             mma_commit(&room.s_full[slot]);
-                            if (last) mma_commit(&room.k_empty[ks]);
-                        }
-                        __syncwarp();
-                    } else {
-                        const bool first = P.first(slot, k);
-                        wait(&room.v_full[vs], n / Lay::kVStages);
-                        wait(&room.p_full[slot], t);
-                        if (!ok) break;
-                        tc_fence_after_sync();
-                        const uint64_t value = dv + vs * (Lay::kTile >> 4);
-                        if (elect_one()) {
-                            // keys 32 c .. 32 c + 31: hi parts in columns 32 c ..
-                            // 32 c + 15, lo parts in the next sixteen
-#pragma unroll
-                            for (int kk = 0; kk < kTrKeys / 16; ++kk) {
-#pragma unroll
-                                for (int part = 0; part < 2; ++part)
-                                    mma_f16_ts(tmem + 2 * kTrKeys + D * slot,
-                                               tmem + kTrKeys * slot + 32 * (kk >> 1) + 8 * (kk & 1) + 16 * part,
-                                               value + kk * (16 * 128 >> 4), kIdPV, !first || kk > 0 || part > 0);
-                            }
-                            mma_commit(&room.o_done[slot]);
-                            if (last) mma_commit(&room.v_empty[vs]);
+                            if (!P.share || slot == kTrSlots - 1) mma_commit(&room.k_empty[at.at]);     // its last user
                         }
                         __syncwarp();
                     }
                 }
+                if (ok && elect_one()) {
+                    mma_commit(&room.q_empty[q0.at]);
+                    if (P.share) mma_commit(&room.q_empty[q0.at ^ 1]);
+                }
+                __syncwarp();
             }
-            if (scores && ok && elect_one()) {
-                for (int i = 0; i < P.query_tiles(); ++i) mma_commit(&room.q_empty[(nq + i) % kTrQStages]);
+        } else {
+            TrRing<Lay::kVStages> at;
+            while (ok && walk.next(p, side, P)) {
+                for (int k = P.k0; ok && k < P.k1; ++k, at.step()) {
+                    wait(&room.v_full[at.at], at.lap);
+                    const uint64_t value = dv + at.at * (Lay::kTile >> 4);
+#pragma unroll
+                    for (int slot = 0; slot < kTrSlots; ++slot) {
+                        if (!P.has(slot, k)) continue;
+                        const bool first = P.first(slot, k);
+                        const int t = tiles[slot]++;
+                        // half the keys at a time, as P comes
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            wait(&room.p_full[slot][half], t);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            if (elect_one()) {
+                                // keys 16 kk .. 16 kk + 15: hi parts in columns 16 kk ..
+                                // 16 kk + 7, lo parts in the next eight
+#pragma unroll
+                                for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {
+#pragma unroll
+                                    for (int part = 0; part < 2; ++part)
+                                        mma_f16_ts(tmem + 2 * kTrKeys + D * slot, tmem + kTrKeys * slot + 16 * kk + 8 * part,
+                                                   value + kk * (16 * 128 >> 4), kIdPV, !first || kk > 0 || part > 0);
+                                }
+                                if (half == 1) {
+                                    mma_commit(&room.o_done[slot]);
+                                    if (!P.share || slot == kTrSlots - 1) mma_commit(&room.v_empty[at.at]);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) break;
+                    }
+                }
             }
-            __syncwarp();
-            nq += P.query_tiles();
         }
         // the products are done before tensor memory and operands are given up
         if (elect_one()) mma_commit(&room.done[warp >> 1]);
@@ -763,28 +799,36 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     const uint64_t neg2 = f32x2_pack(-ref, -ref);
                     uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t parts[32];                        // hi, then lo
+                    for (int c = 0; c < kTrKeys / 16; ++c) {
+                        uint32_t parts[16];                        // hi, then lo
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < 8; ++i) {
                             float a0, a1;
-                            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[32 * c + 2 * i]),
-                                                              __uint_as_float(x[32 * c + 2 * i + 1])), sl2, neg2), a0, a1);
+                            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[16 * c + 2 * i]),
+                                                              __uint_as_float(x[16 * c + 2 * i + 1])), sl2, neg2), a0, a1);
                             const float p0 = ex2(a0), p1 = ex2(a1);
                             ps[i & 3] = f32x2_add(ps[i & 3], f32x2_pack(p0, p1));
-                            split_pair<M>(p0, p1, parts[i], parts[16 + i]);
+                            split_pair<M>(p0, p1, parts[i], parts[8 + i]);
                         }
-                        tmem_st32(tS + 32 * c, parts);
+                        tmem_st16(tS + 16 * c, parts);
+                        if (c == kTrKeys / 32 - 1) {               // the first half may go
+                            tmem_wait_st();
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&room.p_full[slot][0]);
+                        }
                     }
                     float q8[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) f32x2_unpack(ps[e], q8[2 * e], q8[2 * e + 1]);
                     l += ((q8[0] + q8[1]) + (q8[2] + q8[3])) + ((q8[4] + q8[5]) + (q8[6] + q8[7]));
                     tmem_wait_st();
+                } else if (lane == 0) {
+                    mbar_arrive(&room.p_full[slot][0]);
                 }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&room.p_full[slot]);
+                if (lane == 0) mbar_arrive(&room.p_full[slot][1]);
                 ++t, ++j;
             }
             // ---- the piece's end ----------------------------------------------
