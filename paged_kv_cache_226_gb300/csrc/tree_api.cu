@@ -53,7 +53,8 @@ int tree_attention(const void* q, const void* k_cache, const void* v_cache, cons
     if (!aligned(workspace, 16)) return PA_ERR_INVALID_ARG;
     if (num_tokens == 0 || p.max_query == 0) return PA_OK;
     // key tiles are counted in 32 bits
-    if (((int64_t)p.max_context + 127) / 128 * p.num_seqs * p.num_kv_heads >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+    if (((int64_t)p.max_context / pa::kTreeKeys + 4) * p.num_seqs * p.num_kv_heads >= (1ll << 31))
+        return PA_ERR_UNSUPPORTED;
     CUtensorMap tmk, tmv, tmq;
     if ((st = pa::encode_cache_map(&tmk, k_cache, shp, fp8)) != PA_OK) return st;
     if ((st = pa::encode_cache_map(&tmv, v_cache, shp, fp8)) != PA_OK) return st;

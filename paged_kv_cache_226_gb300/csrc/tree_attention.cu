@@ -6,38 +6,44 @@
 //
 // The rows of a (sequence, KV head) pair, its nodes times the G query heads
 // that read the KV head, are cut into tiles of 128 rows (128 / G nodes), and
-// its keys into tiles of 128.  A CTA has two slots, each with a query tile, a
-// score tile S (probabilities P over it) and an output O in tensor memory, and
-// four softmax warps, a thread per row.  Where a pair has two query tiles, each
-// slot has one and every K / V tile serves both; where it has one, both slots
-// have it and take the key tiles in turn.  So one slot's softmax runs beside
-// the other's products either way, and K and V are read once for 256 rows.
-// More rows than that go to CTAs side by side ("lanes") that walk the same
-// keys at the same time, so that the second reads them from L2.
+// its keys into tiles of 64.  A CTA has two slots, each with a query tile, two
+// score tiles S (probabilities P over them) and an output O in tensor memory,
+// and four softmax warps, a thread per row.  Where a pair has two query tiles,
+// each slot has one and every K / V tile serves both; where it has one, both
+// slots take its key tiles in turn, or, where those are few, one slot takes
+// them all and the other the next pair's.  So one slot's softmax runs beside
+// the other's products, and K and V are read once for 256 rows.  More rows
+// than that go to CTAs side by side ("lanes") that walk the same keys at the
+// same time, so that the second reads them from L2.
 //
-//   S = Q K^T           128 x 128 x D, operands in shared memory
+//   S = Q K^T           128 x 64 x D, operands in shared memory
 //   P = 2^(S - m)       m a reference of the row's maximum, raised only when
 //                       that grows by more than 2^8 (O is rescaled then); P
 //                       goes back over S as two parts of the 16-bit type that
 //                       together hold it to 2^-17 (bf16) or 2^-21 (fp16, whose
 //                       reference stays 2^7 below the maximum so that small P
 //                       are not lost below its range)
-//   O += P V            128 x D x 128 for each part, P from tensor memory
+//   O += P V            128 x D x 64 for each part, P from tensor memory
+//
+// A tile passes from products to softmax, to products and back in some 1900
+// cycles beside the work itself, so a slot needs two tiles under way: with one
+// S of 128 keys per slot 8 heads x 4 sequences of 32k to 50k tokens at 240 rows
+// took 190 us (134 with no softmax and half of P V), with one of 64 keys 227.
 //
 // The key tiles of all pairs, in order, are dealt out to persistent CTAs in
 // equal ranges, or, where contexts are short, whole pairs are.  A pair that
 // more than one CTA meets leaves records (O, m, sum), joined by a second
 // kernel.  K and V come once from HBM, 512 B a token and KV head at D 128;
-// the products cost 12 D operations (P in two parts) for each row and token.
+// the products cost 6 D operations (P in two parts) for each row and token.
 //
 // An E4M3 cache's codes are brought to the 16-bit type (exactly) by three
 // warps between the loaders' ring and the operands'.
 //
-// Warps: 0 loads K tiles (and the query tiles) and 2 V tiles, 1 issues S and 3
-// P V, 4 .. 7 are slot 0's softmax and 8 .. 11 slot 1's, 12 makes the trees'
-// lines, 13 .. 15 convert codes.  Every barrier's waits follow each other
-// phase by phase: a tile's ring stage is its running number modulo the ring,
-// and a slot's barriers count the slot's own tiles.
+// Warps: 0 loads K tiles and 2 V tiles, 1 issues S and 3 P V, 4 .. 7 are slot
+// 0's softmax and 8 .. 11 slot 1's, 12 makes the trees' lines, 13 .. 15
+// convert codes.  A barrier's parity tells a phase from the one before it
+// alone, so whoever waits for a phase has seen that the one before is over: by
+// waiting for every phase in turn, or as the comments at the waits say.
 #include "decode_tile.cuh"
 #include "tc_device.cuh"
 #include "tree_device.cuh"
@@ -45,10 +51,9 @@
 namespace pa {
 
 constexpr int kTrRows = 128;
-constexpr int kTrKeys = 128;
+constexpr int kTrKeys = kTreeKeys;
 constexpr int kTrSlots = 2;
 constexpr int kTrQStages = 2;
-constexpr int kTrCodeStages = 2;               // of K and of V each
 constexpr int kTrSoftmaxWarps = 4 * kTrSlots;
 constexpr int kTrLineWarp = 4 + kTrSoftmaxWarps;
 constexpr int kTrConverters = 3;
@@ -58,25 +63,31 @@ constexpr int kTrThreads = (kTrLineWarp + 1 + kTrConverters) * 32;
 constexpr int kTrControlRegs = 56, kTrSoftmaxRegs = 200;
 static_assert(kTrThreads == 512 && 2 * (kTrControlRegs + kTrSoftmaxRegs) <= 4 * 128, "registers of the CTA");
 constexpr int kTrCtas = 152;                   // one per SM
-constexpr int kTrMinTiles = 4;                 // weight of a CTA's range at least, where there are records
-constexpr int kTrWholeTiles = 4;               // longest contexts, in tiles, whose pairs stay whole
-constexpr int kTrPairWeight = 1;               // of a pair beside its key tiles, in the dealing
+constexpr int kTrMinTiles = 8;                 // weight of a CTA's range at least, where there are records
+constexpr int kTrWholeTiles = 8;               // longest contexts, in tiles, whose pairs stay whole
+constexpr int kTrPairWeight = 2;               // of a pair beside its key tiles, in the dealing
+constexpr int kTrSoloTiles = 2;                // of a piece that one slot takes alone
 
 // Shared memory: query tiles, operand tiles, codes.
 template <int D, bool kFp8>
 struct TrLayout {
-    static constexpr int kKStages = kFp8 ? 1 : 3, kVStages = 2;
+    static constexpr int kKStages = kFp8 ? 2 : 5, kVStages = kFp8 ? 3 : 5;
+    static constexpr int kCodeStages = kFp8 ? 5 : 0;          // of K and of V each
     static constexpr int kHalves = D / kBoxElems;
-    static constexpr int kHalf = kTrRows * 128;               // 64 dims of 128 rows
+    static constexpr int kHalf = kTrKeys * 128;               // 64 dims of 64 rows
     static constexpr int kTile = kHalves * kHalf;
-    static constexpr int kCodes = kTrRows * 128;              // 128 codes of 128 rows
+    static constexpr int kCodes = kTrKeys * 128;              // 128 codes of 64 rows
+    static constexpr int kQHalf = kTrRows * 128, kQTile = kHalves * kQHalf;
     static constexpr int kQ = 0;
-    static constexpr int kK = kQ + kTrQStages * kTile;
+    static constexpr int kK = kQ + kTrQStages * kQTile;
     static constexpr int kV = kK + kKStages * kTile;
     static constexpr int kKCodes = kV + kVStages * kTile;
-    static constexpr int kVCodes = kKCodes + (kFp8 ? kTrCodeStages * kCodes : 0);
-    static constexpr int kRoom = kVCodes + (kFp8 ? kTrCodeStages * kCodes : 0);
+    static constexpr int kVCodes = kKCodes + kCodeStages * kCodes;
+    static constexpr int kRoom = kVCodes + kCodeStages * kCodes;
 };
+
+// Tensor memory: a slot's two S, a slot's O.
+constexpr int kTrS = 0, kTrO = 2 * kTrSlots * kTrKeys;
 
 // Behind the tiles.
 struct TrRoom {
@@ -84,16 +95,17 @@ struct TrRoom {
         uint4 line[PA_TREE_NODES];             // a piece's lines, until they are read
         float2 ml[kTrSlots][kTrRows];          // the slots' statistics, at a joined piece's end
     };
-    uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
-    uint64_t kc_full[kTrCodeStages], kc_empty[kTrCodeStages], vc_full[kTrCodeStages], vc_empty[kTrCodeStages];
+    uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
+    uint64_t kc_full[5], kc_empty[5], vc_full[5], vc_empty[5];
     uint64_t q_full[kTrQStages], q_empty[kTrQStages], lines_full, lines_empty;
-    uint64_t s_full[kTrSlots], p_full[kTrSlots][2], o_done[kTrSlots], done[2];
+    uint64_t s_full[kTrSlots][2], p_full[kTrSlots][2], o_done[kTrSlots][2], done[2];
     uint32_t tmem;
 };
 
 template <int D, bool kFp8>
 constexpr int tr_smem() { return TrLayout<D, kFp8>::kRoom + (int)sizeof(TrRoom); }
-static_assert(tr_smem<128, false>() <= 232448 && tr_smem<128, true>() <= 232448, "shared memory over the per-CTA limit");
+static_assert(tr_smem<128, false>() <= 232448 && tr_smem<128, true>() <= 232448 && tr_smem<64, false>() <= 232448,
+              "shared memory over the per-CTA limit");
 
 #ifdef PA_TEST_HOOKS
 __device__ __forceinline__ uint64_t tr_wait_limit(const TreeParams& p) { return p.test_wait_limit_ns; }
@@ -124,19 +136,19 @@ struct TrPiece {
     int b, g, k0, k1, n;
     TreeSeq s;
     bool share;                    // each slot has a query tile, and all key tiles
-    bool alone;                    // the slots do not join: shared, or a single tile
-    int owner;                     // the slot of a single tile
+    bool alone;                    // the slots do not join: shared, or few tiles
+    int owner;                     // the slot of those few
 
     // The slot that takes key tile k where it is not both.
     __device__ __forceinline__ int slot_of(int k) const { return alone ? owner : (k - k0) & 1; }
     __device__ __forceinline__ bool has(int slot, int k) const { return share || slot_of(k) == slot; }
     // A slot's tiles.
     __device__ __forceinline__ int own(int slot) const {
-        return share ? k1 - k0 : (alone ? (int)(owner == slot) : (k1 - k0 + 1 - slot) / 2);
+        return share ? k1 - k0 : (alone ? (owner == slot ? k1 - k0 : 0) : (k1 - k0 + 1 - slot) / 2);
     }
-    // The first slot's first tile or the second's.
-    __device__ __forceinline__ bool first(int slot, int k) const { return share || alone ? k == k0 : k - k0 == slot; }
     __device__ __forceinline__ int query_tiles() const { return share ? 2 : 1; }
+    // Whether key tile k is the slot's first.
+    __device__ __forceinline__ bool first(int slot, int k) const { return share || alone ? k == k0 : k - k0 == slot; }
 };
 
 // Nodes of a query tile.
@@ -214,7 +226,7 @@ struct TrWalk {
             const int query_tiles = (P.s.C + per - 1) / per - kTrSlots * side;
             if (query_tiles <= 0) continue;
             P.share = query_tiles >= kTrSlots;
-            P.alone = P.share || P.k1 - P.k0 == 1;
+            P.alone = P.share || P.k1 - P.k0 <= kTrSoloTiles;
             P.owner = turn;
             if (P.alone && !P.share) turn ^= 1;
             return true;
@@ -273,22 +285,6 @@ __device__ __forceinline__ uint32_t seen_word(const TreeLine& line, int off) {
     };
     const int i = off >> 5;
     return __funnelshift_r(word(i), word(i + 1), off & 31);
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&v)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-                 :
-                 : "memory");
 }
 
 // 16-bit elements that are not finite, at their sign bits.
@@ -372,19 +368,18 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     const int G = p.group, per_tile = tr_nodes_per_tile(G);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < Lay::kKStages; ++i)
-            mbar_init(&room.k_full[i], kFp8 ? kTrConverters : 1), mbar_init(&room.k_empty[i], 1);
-        for (int i = 0; i < Lay::kVStages; ++i)
-            mbar_init(&room.v_full[i], kFp8 ? kTrConverters : 1), mbar_init(&room.v_empty[i], 1);
-        for (int i = 0; kFp8 && i < kTrCodeStages; ++i) {
+        constexpr int kFillers = kFp8 ? kTrConverters : 1;
+        for (int i = 0; i < Lay::kKStages; ++i) mbar_init(&room.k_full[i], kFillers), mbar_init(&room.k_empty[i], 1);
+        for (int i = 0; i < Lay::kVStages; ++i) mbar_init(&room.v_full[i], kFillers), mbar_init(&room.v_empty[i], 1);
+        for (int i = 0; i < Lay::kCodeStages; ++i) {
             mbar_init(&room.kc_full[i], 1), mbar_init(&room.kc_empty[i], kTrConverters);
             mbar_init(&room.vc_full[i], 1), mbar_init(&room.vc_empty[i], kTrConverters);
         }
         for (int i = 0; i < kTrQStages; ++i) mbar_init(&room.q_full[i], 1), mbar_init(&room.q_empty[i], 1);
         mbar_init(&room.lines_full, 1), mbar_init(&room.lines_empty, kTrSoftmaxWarps);
         for (int i = 0; i < kTrSlots; ++i) {
-            mbar_init(&room.p_full[i][0], 4), mbar_init(&room.p_full[i][1], 4);
-            mbar_init(&room.s_full[i], 1), mbar_init(&room.o_done[i], 1);
+            for (int j = 0; j < 2; ++j)
+                mbar_init(&room.s_full[i][j], 1), mbar_init(&room.p_full[i][j], 4), mbar_init(&room.o_done[i][j], 1);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&room.done[i], 1);
         fence_barrier_init();
@@ -402,234 +397,233 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     TrPiece P;
 
     if (warp < 4) {
-    control_registers();
-    if (warp == 0 || warp == 2) {
-        // ------------------------------------------------------------------
-        // loaders: K and V tiles, each at its own pace and on into the next
-        // pair's; lane i has box i of eight.  Warp 0 also loads a piece's
-        // query tiles, before its keys.
-        // ------------------------------------------------------------------
-        auto load = [&](auto kind) {
-            constexpr bool keys = decltype(kind)::value;
-            constexpr int kStages = kFp8 ? kTrCodeStages : (keys ? Lay::kKStages : Lay::kVStages);
-            constexpr int kStage = kFp8 ? Lay::kCodes : Lay::kTile, kBoxes = kFp8 ? 1 : Lay::kHalves;
-            const CUtensorMap* map = keys ? &tmap_k : &tmap_v;
-            uint64_t* full = kFp8 ? (keys ? room.kc_full : room.vc_full) : (keys ? room.k_full : room.v_full);
-            uint64_t* empty = kFp8 ? (keys ? room.kc_empty : room.vc_empty) : (keys ? room.k_empty : room.v_empty);
-            uint8_t* ring = smem + (kFp8 ? (keys ? Lay::kKCodes : Lay::kVCodes) : (keys ? Lay::kK : Lay::kV));
-            if (lane == 0) prefetch_tensor_map(map);
-            if (keys && lane == 0) prefetch_tensor_map(&tmap_q);
-            const int block_shift = p.block_size == 16 ? 4 : 5, sub = (16 * lane) & (p.block_size - 1);
-            int n = 0;
-            TrRing<kStages> at;
-            TrRing<kTrQStages> q;
-            bool ok = true, held = false;
-            while (ok && !held && walk.next(p, side, P)) {
-                const int32_t* table = p.block_tables + (size_t)P.b * p.max_blocks_per_seq;
-                // block ids: lane i has box i % 8 of tile i / 8 of four, the next
-                // four tiles' requested while these are loaded
-                auto ids = [&](int k) {
-                    const int tok = k * kTrKeys + 16 * lane;
-                    return tok < P.s.L ? __ldg(table + (tok >> block_shift)) : 0;
-                };
-                int blk = 0, ahead = ids(P.k0);
-                for (int i = 0; keys && ok && i < P.query_tiles(); ++i, q.step()) {
-                    if (q.lap > 0) ok = tr_wait(p, &room.q_empty[q.at], q.lap - 1);
-                    if (!ok) break;
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&room.q_full[q.at], (uint32_t)(per_tile * G * Lay::kHalves * 128));
-#pragma unroll
-                        for (int h = 0; h < Lay::kHalves; ++h)
-                            tma_load_3d(smem + Lay::kQ + q.at * Lay::kTile + h * Lay::kHalf, &tmap_q, &room.q_full[q.at],
-                                        h * kBoxElems, P.g * G, P.s.q0 + (kTrSlots * side + i) * per_tile);
-                    }
-                    __syncwarp();
-                }
-                for (int k = P.k0; ok && k < P.k1; ++k, ++n, at.step()) {
-                    const int in = (k - P.k0) & 3;
-                    if (in == 0) {
-                        blk = ahead;
-                        ahead = ids(k + 4);
-                        if (16 * lane + k * kTrKeys < min(P.s.L, P.k1 * kTrKeys) && (blk < 0 || blk >= p.num_blocks))
-                            flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
-                    }
-                    if (at.lap > 0) ok = tr_wait(p, &empty[at.at], at.lap - 1);
-                    held = tr_withheld(p, n);
-                    if (!ok || held) break;
-                    const int boxes = min(8, (P.s.L - k * kTrKeys + 15) / 16);
-                    if (elect_one()) mbar_arrive_expect_tx(&full[at.at], (uint32_t)(boxes * kBoxes * kBox16Bytes));
-                    __syncwarp();
-                    const int id = __shfl_sync(0xffffffffu, blk, in * 8 + (lane & 7));
-                    if (lane < boxes) {
-                        uint8_t* dst = ring + at.at * kStage + lane * kBox16Bytes;
-#pragma unroll
-                        for (int h = 0; h < kBoxes; ++h)
-                            tma_load_4d(dst + h * Lay::kHalf, map, &full[at.at], h * kBoxElems, P.g, sub, id);
-                    }
-                    __syncwarp();
-                }
-            }
-            // the last copies have landed before the CTA gives its memory up:
-            // the stages of this lap, then the others of the lap before
-            for (int st = 0; st < kStages; ++st) {
-                const int lap = st < at.at ? at.lap : at.lap - 1;
-                if (lap >= 0) ok = tr_wait(p, &full[st], lap) && ok;
-            }
-            for (int st = 0; keys && st < kTrQStages; ++st) {
-                const int lap = st < q.at ? q.lap : q.lap - 1;
-                if (lap >= 0) ok = tr_wait(p, &room.q_full[st], lap) && ok;
-            }
-            if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
-        };
-        if (warp == 0)
-            load(std::true_type());
-        else
-            load(std::false_type());
-    } else {
-        // ------------------------------------------------------------------
-        // issuers: S (warp 1) and P V (warp 3), tile by tile and slot by slot.
-        // A slot's S overwrites its P, so it waits for the P V before.
-        // ------------------------------------------------------------------
-        constexpr uint32_t kIdS = idesc_f16(kTrRows, kTrKeys, kBf16, false);
-        constexpr uint32_t kIdPV = idesc_f16(kTrRows, D, kBf16, true);
-        const uint64_t dq = smem_desc_sw128(smem_u32(smem + Lay::kQ), 16, 1024);
-        const uint64_t dk = smem_desc_sw128(smem_u32(smem + Lay::kK), 16, 1024);
-        const uint64_t dv = smem_desc_sw128(smem_u32(smem + Lay::kV), Lay::kHalf, 1024);
-        int tiles[kTrSlots] = {0, 0};
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, int phase) { ok = ok && tr_wait(p, bar, phase); };
-        if (warp == 1) {
-            TrRing<Lay::kKStages> at;
-            TrRing<kTrQStages> q;
-            while (ok && walk.next(p, side, P)) {
-                const TrRing<kTrQStages> q0 = q;
-                for (int i = 0; i < P.query_tiles(); ++i, q.step()) wait(&room.q_full[q.at], q.lap);
-                for (int k = P.k0; ok && k < P.k1; ++k, at.step()) {
-                    wait(&room.k_full[at.at], at.lap);
-#pragma unroll
-                    for (int slot = 0; slot < kTrSlots; ++slot) {
-                        if (!P.has(slot, k)) continue;
-                        if (tiles[slot] > 0) wait(&room.o_done[slot], tiles[slot] - 1);
+        control_registers();
+        if (warp == 0 || warp == 2) {
+            // --------------------------------------------------------------
+            // loaders: K (and query) tiles and V tiles, each at its own pace
+            // and on into the next pair's; lane i has box i % 4, dims 64 (i / 4) on
+            // --------------------------------------------------------------
+            auto load = [&](auto kind) {
+                constexpr bool keys = decltype(kind)::value;
+                constexpr int kStages = kFp8 ? Lay::kCodeStages : (keys ? Lay::kKStages : Lay::kVStages);
+                constexpr int kStage = kFp8 ? Lay::kCodes : Lay::kTile, kBoxes = kFp8 ? 1 : Lay::kHalves;
+                const CUtensorMap* map = keys ? &tmap_k : &tmap_v;
+                uint64_t* full = kFp8 ? (keys ? room.kc_full : room.vc_full) : (keys ? room.k_full : room.v_full);
+                uint64_t* empty = kFp8 ? (keys ? room.kc_empty : room.vc_empty) : (keys ? room.k_empty : room.v_empty);
+                uint8_t* ring = smem + (kFp8 ? (keys ? Lay::kKCodes : Lay::kVCodes) : (keys ? Lay::kK : Lay::kV));
+                if (lane == 0) prefetch_tensor_map(map);
+                const int block_shift = p.block_size == 16 ? 4 : 5;
+                const int box = lane & 3, dims = lane >> 2, sub = (16 * box) & (p.block_size - 1);
+                uint8_t* dst = ring + dims * Lay::kHalf + box * kBox16Bytes;
+                int n = 0;
+                TrRing<kStages> at;
+                TrRing<kTrQStages> q;
+                bool ok = true, held = false;
+                if (keys && lane == 0) prefetch_tensor_map(&tmap_q);
+                while (ok && !held && walk.next(p, side, P)) {
+                    const int32_t* table = p.block_tables + (size_t)P.b * p.max_blocks_per_seq;
+                    // block ids: lane i has box i % 4 of tile i / 4 of eight, the
+                    // next eight tiles' requested while these are loaded
+                    auto ids = [&](int k) {
+                        const int tok = k * kTrKeys + 16 * lane;
+                        return tok < P.s.L ? __ldg(table + (tok >> block_shift)) : 0;
+                    };
+                    int blk = 0, ahead = ids(P.k0);
+                    // the piece's query tiles come before its keys
+                    for (int i = 0; keys && ok && i < P.query_tiles(); ++i, q.step()) {
+                        if (q.lap > 0) ok = tr_wait(p, &room.q_empty[q.at], q.lap - 1);
                         if (!ok) break;
-                        ++tiles[slot];
-                        tc_fence_after_sync();
-                        const uint64_t query = dq + ((q0.at + (P.share ? slot : 0)) & (kTrQStages - 1)) * (Lay::kTile >> 4);
-                        const uint64_t key = dk + at.at * (Lay::kTile >> 4);
                         if (elect_one()) {
+                            mbar_arrive_expect_tx(&room.q_full[q.at], (uint32_t)(per_tile * G * Lay::kHalves * 128));
 #pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint64_t off = (kk >> 2) * (Lay::kHalf >> 4) + (kk & 3) * 2;
-                                mma_f16_ss(tmem + kTrKeys * slot, query + off, key + off, kIdS, kk > 0);
-                            }
-                            mma_commit(&room.s_full[slot]);
-                            if (!P.share || slot == kTrSlots - 1) mma_commit(&room.k_empty[at.at]);     // its last user
+                            for (int h = 0; h < Lay::kHalves; ++h)
+                                tma_load_3d(smem + Lay::kQ + q.at * Lay::kQTile + h * Lay::kQHalf, &tmap_q, &room.q_full[q.at],
+                                            h * kBoxElems, P.g * G, P.s.q0 + (kTrSlots * side + i) * per_tile);
                         }
                         __syncwarp();
                     }
+                    for (int k = P.k0; ok && k < P.k1; ++k, ++n, at.step()) {
+                        const int in = (k - P.k0) & 7;
+                        if (in == 0) {
+                            blk = ahead;
+                            ahead = ids(k + 8);
+                            if (16 * lane + k * kTrKeys < min(P.s.L, P.k1 * kTrKeys) && (blk < 0 || blk >= p.num_blocks))
+                                flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
+                        }
+                        if (at.lap > 0) ok = tr_wait(p, &empty[at.at], at.lap - 1);
+                        held = tr_withheld(p, n);
+                        if (!ok || held) break;
+                        const int boxes = min(4, (P.s.L - k * kTrKeys + 15) / 16);
+                        if (elect_one()) mbar_arrive_expect_tx(&full[at.at], (uint32_t)(boxes * kBoxes * kBox16Bytes));
+                        __syncwarp();
+                        const int id = __shfl_sync(0xffffffffu, blk, in * 4 + box);
+                        if (dims < kBoxes && box < boxes)
+                            tma_load_4d(dst + at.at * kStage, map, &full[at.at], dims * kBoxElems, P.g, sub, id);
+                        __syncwarp();
+                    }
                 }
-                if (ok && elect_one()) {
-                    mma_commit(&room.q_empty[q0.at]);
-                    if (P.share) mma_commit(&room.q_empty[q0.at ^ 1]);
+                // the last copies have landed before the CTA gives its memory up:
+                // the stages of this lap, then the others of the lap before
+                for (int st = 0; st < kStages; ++st) {
+                    const int lap = st < at.at ? at.lap : at.lap - 1;
+                    if (lap >= 0) ok = tr_wait(p, &full[st], lap) && ok;
                 }
-                __syncwarp();
-            }
+                for (int st = 0; keys && st < kTrQStages; ++st) {
+                    const int lap = st < q.at ? q.lap : q.lap - 1;
+                    if (lap >= 0) ok = tr_wait(p, &room.q_full[st], lap) && ok;
+                }
+                if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
+            };
+            if (warp == 0)
+                load(std::true_type());
+            else
+                load(std::false_type());
         } else {
-            TrRing<Lay::kVStages> at;
-            while (ok && walk.next(p, side, P)) {
-                for (int k = P.k0; ok && k < P.k1; ++k, at.step()) {
-                    wait(&room.v_full[at.at], at.lap);
-                    const uint64_t value = dv + at.at * (Lay::kTile >> 4);
+            // --------------------------------------------------------------
+            // issuers: S (warp 1) and P V (warp 3), tile by tile and slot by
+            // slot.  S overwrites the P of two tiles before, so it waits for that P V.
+            // --------------------------------------------------------------
+            constexpr uint32_t kIdS = idesc_f16(kTrRows, kTrKeys, kBf16, false);
+            constexpr uint32_t kIdPV = idesc_f16(kTrRows, D, kBf16, true);
+            const uint64_t dq = smem_desc_sw128(smem_u32(smem + Lay::kQ), 16, 1024);
+            const uint64_t dk = smem_desc_sw128(smem_u32(smem + Lay::kK), 16, 1024);
+            const uint64_t dv = smem_desc_sw128(smem_u32(smem + Lay::kV), Lay::kHalf, 1024);
+            int tiles[kTrSlots] = {0, 0};
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, int phase) { ok = ok && tr_wait(p, bar, phase); };
+            if (warp == 1) {
+                TrRing<Lay::kKStages> at;
+                TrRing<kTrQStages> q;
+                while (ok && walk.next(p, side, P)) {
+                    const int q0 = q.at;
+                    for (int i = 0; i < P.query_tiles(); ++i, q.step()) wait(&room.q_full[q.at], q.lap);
+                    for (int k = P.k0; ok && k < P.k1; ++k, at.step()) {
+                        wait(&room.k_full[at.at], at.lap);
+                        const uint64_t key = dk + at.at * (Lay::kTile >> 4);
 #pragma unroll
-                    for (int slot = 0; slot < kTrSlots; ++slot) {
-                        if (!P.has(slot, k)) continue;
-                        const bool first = P.first(slot, k);
-                        const int t = tiles[slot]++;
-                        // half the keys at a time, as P comes
+                        for (int slot = 0; slot < kTrSlots; ++slot) {
+                            if (!P.has(slot, k)) continue;
+                            const int t = tiles[slot]++, buf = t & 1;
+                            if (t > 1) wait(&room.o_done[slot][buf], (t >> 1) - 1);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            const uint64_t query = dq + (P.share ? q0 ^ slot : q0) * (Lay::kQTile >> 4);
+                            if (elect_one()) {
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            wait(&room.p_full[slot][half], t);
+                                for (int kk = 0; kk < D / 16; ++kk)
+                                    mma_f16_ss(tmem + kTrS + kTrKeys * (2 * slot + buf),
+                                               query + (kk >> 2) * (Lay::kQHalf >> 4) + (kk & 3) * 2,
+                                               key + (kk >> 2) * (Lay::kHalf >> 4) + (kk & 3) * 2, kIdS, kk > 0);
+                                mma_commit(&room.s_full[slot][buf]);
+                                if (!P.share || slot == kTrSlots - 1) mma_commit(&room.k_empty[at.at]);     // its last user
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (ok && elect_one()) {
+                        mma_commit(&room.q_empty[q0]);
+                        if (P.share) mma_commit(&room.q_empty[q0 ^ 1]);
+                    }
+                    __syncwarp();
+                }
+            } else {
+                TrRing<Lay::kVStages> at;
+                while (ok && walk.next(p, side, P)) {
+                    for (int k = P.k0; ok && k < P.k1; ++k, at.step()) {
+                        wait(&room.v_full[at.at], at.lap);
+                        const uint64_t value = dv + at.at * (Lay::kTile >> 4);
+#pragma unroll
+                        for (int slot = 0; slot < kTrSlots; ++slot) {
+                            if (!P.has(slot, k)) continue;
+                            const bool first = P.first(slot, k);
+                            const int t = tiles[slot]++, buf = t & 1;
+                            wait(&room.p_full[slot][buf], t >> 1);
                             if (!ok) break;
                             tc_fence_after_sync();
                             if (elect_one()) {
                                 // keys 16 kk .. 16 kk + 15: hi parts in columns 16 kk ..
                                 // 16 kk + 7, lo parts in the next eight
 #pragma unroll
-                                for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {
+                                for (int kk = 0; kk < kTrKeys / 16; ++kk) {
 #pragma unroll
                                     for (int part = 0; part < 2; ++part)
-                                        mma_f16_ts(tmem + 2 * kTrKeys + D * slot, tmem + kTrKeys * slot + 16 * kk + 8 * part,
+                                        mma_f16_ts(tmem + kTrO + D * slot,
+                                                   tmem + kTrS + kTrKeys * (2 * slot + buf) + 16 * kk + 8 * part,
                                                    value + kk * (16 * 128 >> 4), kIdPV, !first || kk > 0 || part > 0);
                                 }
-                                if (half == 1) {
-                                    mma_commit(&room.o_done[slot]);
-                                    if (!P.share || slot == kTrSlots - 1) mma_commit(&room.v_empty[at.at]);
-                                }
+                                mma_commit(&room.o_done[slot][buf]);
+                                if (!P.share || slot == kTrSlots - 1) mma_commit(&room.v_empty[at.at]);
                             }
                             __syncwarp();
                         }
-                        if (!ok) break;
                     }
                 }
             }
-        }
-        // the products are done before tensor memory and operands are given up
-        if (elect_one()) mma_commit(&room.done[warp >> 1]);
-        __syncwarp();
-        ok = tr_wait(p, &room.done[warp >> 1], 0) && ok;
-        if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
-    }
-    } else if (warp >= kTrLineWarp) {
-    control_registers();
-    if (warp == kTrLineWarp) {
-        // ------------------------------------------------------------------
-        // the trees' lines, a piece ahead of those who read them
-        // ------------------------------------------------------------------
-        bool ok = true;
-        for (int i = 0; ok && walk.next(p, side, P); ++i) {
-            uint32_t w[kLineWords][kLineWords] = {};
-            const bool tree = P.k1 * kTrKeys > P.s.L - P.s.C;      // the piece has some of it
-            if (tree) {
-                int up[kLineWords];
-#pragma unroll
-                for (int j = 0; j < kLineWords; ++j) {
-                    const int node = lane + 32 * j;
-                    up[j] = node < P.s.C ? tree_parent(p.parents, P.s.q0, node, p.err) : -1;
-                }
-                warp_lines(w, up, P.s.C);
-            }
-            if (i > 0) ok = tr_wait(p, &room.lines_empty, i - 1);
-            if (!ok) break;
-            if (tree) {
-#pragma unroll
-                for (int j = 0; j < kLineWords; ++j) room.line[lane + 32 * j] = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
-            }
+            // the products are done before tensor memory and operands are given up
+            if (elect_one()) mma_commit(&room.done[warp >> 1]);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&room.lines_full);
+            ok = tr_wait(p, &room.done[warp >> 1], 0) && ok;
+            if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
         }
-        if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
-    } else {
-        // ------------------------------------------------------------------
-        // converters: a K tile's codes, then its V tile's, 16 at a time
-        // ------------------------------------------------------------------
-        if constexpr (kFp8) {
-            const int who = threadIdx.x - (kTrLineWarp + 1) * 32;
-            int n = 0;
+    } else if (warp >= kTrLineWarp) {
+        control_registers();
+        if (warp == kTrLineWarp) {
+            // --------------------------------------------------------------
+            // the trees' lines, a piece ahead of those who read them
+            // --------------------------------------------------------------
+            bool ok = true;
+            for (int i = 0; ok && walk.next(p, side, P); ++i) {
+                uint32_t w[kLineWords][kLineWords] = {};
+                const bool tree = P.k1 * kTrKeys > P.s.L - P.s.C;      // the piece has some of it
+                if (tree) {
+                    int up[kLineWords];
+#pragma unroll
+                    for (int j = 0; j < kLineWords; ++j) {
+                        const int node = lane + 32 * j;
+                        up[j] = node < P.s.C ? tree_parent(p.parents, P.s.q0, node, p.err) : -1;
+                    }
+                    warp_lines(w, up, P.s.C);
+                }
+                if (i > 0) ok = tr_wait(p, &room.lines_empty, i - 1);
+                if (!ok) break;
+                if (tree) {
+#pragma unroll
+                    for (int j = 0; j < kLineWords; ++j)
+                        room.line[lane + 32 * j] = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&room.lines_full);
+            }
+            if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
+        } else if constexpr (kFp8) {
+            // --------------------------------------------------------------
+            // converters: a K tile's codes, then its V tile's.  A pass brings 16
+            // codes a lane of four rows; lanes are laid out so that eight
+            // neighbours read and write different banks: four chunks of a row
+            // beside the other four of the next.
+            // --------------------------------------------------------------
+            const int who = warp - kTrLineWarp - 1;
+            const int c = lane & 7, upper = c >> 2;
+            const int r4 = 2 * (lane >> 4) + (upper ^ ((lane >> 3) & 1));
+            int turn = who;                                            // passes deal out evenly over the tiles
+            TrRing<Lay::kKStages> k_at;
+            TrRing<Lay::kVStages> v_at;
+            TrRing<Lay::kCodeStages> at;
             bool ok = true;
             while (ok && walk.next(p, side, P)) {
-                for (int k = P.k0; ok && k < P.k1; ++k, ++n) {
+                for (int k = P.k0; ok && k < P.k1; ++k, k_at.step(), v_at.step(), at.step()) {
 #pragma unroll 1
                     for (int kind = 0; ok && kind < 2; ++kind) {
-                        const int cs = n % kTrCodeStages;
-                        const int stages = kind == 0 ? Lay::kKStages : Lay::kVStages, st = n % stages;
-                        uint64_t* empty = kind == 0 ? &room.k_empty[st] : &room.v_empty[st];
-                        ok = tr_wait(p, kind == 0 ? &room.kc_full[cs] : &room.vc_full[cs], n / kTrCodeStages);
-                        if (ok && n >= stages) ok = tr_wait(p, empty, n / stages - 1);
+                        const bool keys = kind == 0;
+                        const int st = keys ? k_at.at : v_at.at, lap = keys ? k_at.lap : v_at.lap;
+                        ok = tr_wait(p, keys ? &room.kc_full[at.at] : &room.vc_full[at.at], at.lap);
+                        if (ok && lap > 0) ok = tr_wait(p, keys ? &room.k_empty[st] : &room.v_empty[st], lap - 1);
                         if (!ok) break;
-                        const uint8_t* src = smem + (kind == 0 ? Lay::kKCodes : Lay::kVCodes) + cs * Lay::kCodes;
-                        uint8_t* dst = smem + (kind == 0 ? Lay::kK : Lay::kV) + st * Lay::kTile;
-#pragma unroll 4
-                        for (int i = who; i < kTrKeys * 8; i += kTrConverters * 32) {
-                            const int r = i >> 3, c = i & 7;
+                        const uint8_t* src = smem + (keys ? Lay::kKCodes : Lay::kVCodes) + at.at * Lay::kCodes;
+                        uint8_t* dst = smem + (keys ? Lay::kK : Lay::kV) + st * Lay::kTile + upper * Lay::kHalf;
+#pragma unroll 2
+                        for (int i = turn; i < kTrKeys / 4; i += kTrConverters) {
+                            const int r = 4 * i + r4;
                             const uint4 x = lds128(src + r * 128 + ((c ^ (r & 7)) << 4));
                             uint32_t y[8];
 #pragma unroll
@@ -642,29 +636,23 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                                     e4m3x4_to_f16x2x2(codes, y[2 * j], y[2 * j + 1]);
                                 }
                             }
-                            // chunks 2c and 2c + 1 of the row's 16; the upper half's
-                            // threads store them the other way round, off the lower's banks
-                            uint8_t* row = dst + (c >> 2) * Lay::kHalf + r * 128;
-                            const int first = c >> 2;
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const int which = j ^ first, chunk = ((2 * c + which) & 7) ^ (r & 7);
-                                const uint4 v = which ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
-                                *reinterpret_cast<uint4*>(row + (chunk << 4)) = v;
-                            }
+                            // chunks 2c and 2c + 1 of the row's 16
+                            const int chunk = ((2 * c) & 7) ^ (r & 7);
+                            *reinterpret_cast<uint4*>(dst + r * 128 + (chunk << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4*>(dst + r * 128 + ((chunk ^ 1) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
                         }
+                        turn = turn == 0 ? kTrConverters - 1 : turn - 1;      // 16 passes are 1 modulo 3
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive(kind == 0 ? &room.k_full[st] : &room.v_full[st]);
-                            mbar_arrive(kind == 0 ? &room.kc_empty[cs] : &room.vc_empty[cs]);
+                            mbar_arrive(keys ? &room.k_full[st] : &room.v_full[st]);
+                            mbar_arrive(keys ? &room.kc_empty[at.at] : &room.vc_empty[at.at]);
                         }
                     }
                 }
             }
             if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
         }
-    }
     } else {
         softmax_registers();
         // ------------------------------------------------------------------
@@ -673,8 +661,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const int slot = (warp >> 2) - 1;
         const int r = (warp & 3) * 32 + lane;
         const uint32_t lanes_at = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + kTrKeys * slot + lanes_at;
-        const uint32_t tO = tmem + 2 * kTrKeys + lanes_at;         // slot 0's, slot 1's D columns on
+        const uint32_t tO = tmem + kTrO + lanes_at;                // slot 0's, slot 1's D columns on
         const int barrier = 1 + slot, both = 3;                    // named barriers
         const int in_tile = r / G, head = r - in_tile * G;
         const float sl = p.scale_log2;
@@ -683,11 +670,15 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         auto wait = [&](uint64_t* bar, int phase) {
             if (!failed && !tr_wait(p, bar, phase)) failed = true;
         };
+        auto node_of = [&](const TrPiece& X) { return (kTrSlots * side + (X.share ? slot : 0)) * per_tile + in_tile; };
+        auto row_of = [&](const TrPiece& X) {
+            return (int64_t)(X.s.q0 + node_of(X)) * p.num_q_heads + X.g * G + head;
+        };
         int n = 0, t = 0;                     // tiles of the CTA and of the slot so far
         for (int piece = 0; walk.next(p, side, P); ++piece) {
             const int base = P.s.L - P.s.C;
             const int count = P.k1 - P.k0, own = P.own(slot);
-            const int node = (kTrSlots * side + (P.share ? slot : 0)) * per_tile + in_tile;
+            const int node = node_of(P);
             const bool valid = in_tile < per_tile && node < P.s.C;
             const bool live = __any_sync(0xffffffffu, valid);      // a warp without rows only keeps step
             TreeLine line{};
@@ -699,50 +690,49 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             if (P.alone) {                                         // else the statistics come there first
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&room.lines_empty);
-                if (own == 0) {
-                    n += count;
-                    continue;
-                }
             }
             float m = -INFINITY, l = 0.f;
             bool bad = false;                 // V of the tree has elements that are not finite
-            for (int k = P.k0, j = 0; k < P.k1; ++k, ++n) {
+            for (int k = P.k0, j = 0; own > 0 && k < P.k1; ++k) {
                 if (!P.has(slot, k)) continue;
-                const int key0 = k * kTrKeys, vs = n % Lay::kVStages;
+                const int key0 = k * kTrKeys;
                 const bool masked = key0 + kTrKeys > base;
-                // S waited for this slot's P V before, so that V of the tile two
-                // before this one, in the same stage, has been there too: the
-                // wait for V below cannot take its phase for this tile's
-                wait(&room.s_full[slot], t);
+                const uint32_t tS = tmem + kTrS + kTrKeys * (2 * slot + (t & 1)) + lanes_at;
+                wait(&room.s_full[slot][t & 1], t >> 1);
                 tc_fence_after_sync();
                 if (masked) {
                     // V rows past the context may hold anything: clear them.
                     // Of the tree's, elements that are not finite are cleared
                     // too, since the tensor cores would carry them into rows
                     // that do not see them; rows that do get them back below.
+                    // Thread r has half r / 64 of key r % 64.  The phase before
+                    // of V's barrier is over once this slot's P V before is done:
+                    // that was at most three tiles back (kTrSoloTiles), and the
+                    // rings have three stages at least.
                     bool odd = false;
                     if (!P.share || slot == 0) {
-                        wait(&room.v_full[vs], n / Lay::kVStages);
-                        uint8_t* vd = smem + Lay::kV + vs * Lay::kTile + r * 128;
-                        const int key = key0 + r;
-                        if (key >= P.s.L) {
+                        static_assert(Lay::kVStages > kTrSoloTiles, "a phase could be taken for another");
+                        const int tile = n + (k - P.k0), vs = tile % Lay::kVStages;
+                        if (t > 0) wait(&room.o_done[slot][(t - 1) & 1], (t - 1) >> 1);
+                        wait(&room.v_full[vs], tile / Lay::kVStages);
+                        const int key = key0 + (r & 63);
+                        uint8_t* vd = smem + Lay::kV + vs * Lay::kTile + (D == 128 ? (r >> 6) * Lay::kHalf : 0) + (r & 63) * 128;
+                        if (D == 64 && r >= 64) {
+                        } else if (key >= P.s.L) {
 #pragma unroll
-                            for (int c = 0; c < D / 8; ++c)
-                                *reinterpret_cast<uint4*>(vd + (c >> 3) * Lay::kHalf + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vd + (((c ^ r) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
                         } else if (key >= base) {
                             uint32_t any = 0u;
 #pragma unroll
-                            for (int c = 0; c < D / 8; ++c) {
-                                // each row's chunks from another one on: no two on one bank
-                                const uint4 w = lds128(vd + (c >> 3) * Lay::kHalf + (((c ^ r) & 7) << 4));
+                            for (int c = 0; c < 8; ++c) {
+                                const uint4 w = lds128(vd + (((c ^ r) & 7) << 4));
                                 any |= not_finite<T>(w.x) | not_finite<T>(w.y) | not_finite<T>(w.z) | not_finite<T>(w.w);
                             }
                             if (any != 0u) {
                                 odd = true;
-                                for (int c = 0; c < D / 2; ++c) {
-                                    uint32_t* w = reinterpret_cast<uint32_t*>(vd + (c >> 5) * Lay::kHalf) + (c & 31);
-                                    const uint32_t x = not_finite<T>(*w);
-                                    *w &= ~(((x >> 15) & 0x00010001u) * 0xffffu);
+                                for (int c = 0; c < 32; ++c) {
+                                    uint32_t* w = reinterpret_cast<uint32_t*>(vd) + c;
+                                    *w &= ~(((not_finite<T>(*w) >> 15) & 0x00010001u) * 0xffffu);
                                 }
                             }
                         }
@@ -753,15 +743,15 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 if (live) {
                     uint32_t x[kTrKeys];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * c));
+                    for (int c = 0; c < kTrKeys; c += 32) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(x + c));
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(x + 32 * c));
+                    for (int c = 0; c < kTrKeys; c += 32) tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(x + c));
                     if (masked) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t seen = seen_word(line, key0 + 32 * c - base);
+                        for (int c = 0; c < kTrKeys; c += 32) {
+                            const uint32_t seen = seen_word(line, key0 + c - base);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[32 * c + e] = (seen >> e) & 1u ? x[32 * c + e] : 0xff800000u;
+                            for (int e = 0; e < 32; ++e) x[c + e] = (seen >> e) & 1u ? x[c + e] : 0xff800000u;
                         }
                     }
                     // the row's maximum on the raw scores (the scale is positive)
@@ -781,17 +771,17 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         const float f = raise ? ex2(m - m_new) : 1.f;
                         l *= f;
                         m = m_new;
-                        if (j > 0) {                               // the P V before is done: S waited for it
-                            wait(&room.o_done[slot], t - 1);
+                        if (j > 0) {
+                            wait(&room.o_done[slot][(t - 1) & 1], (t - 1) >> 1);
                             tc_fence_after_sync();
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                uint32_t o[16];
-                                tmem_ld16(tO + D * slot + c, o);
-                                tmem_wait_ld16(o);
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(tO + D * slot + c, o);
+                                tmem_wait_ld(o);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st16(tO + D * slot + c, o);
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st32(tO + D * slot + c, o);
                             }
                         }
                     }
@@ -811,115 +801,111 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                             split_pair<M>(p0, p1, parts[i], parts[8 + i]);
                         }
                         tmem_st16(tS + 16 * c, parts);
-                        if (c == kTrKeys / 32 - 1) {               // the first half may go
-                            tmem_wait_st();
-                            tc_fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&room.p_full[slot][0]);
-                        }
                     }
                     float q8[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) f32x2_unpack(ps[e], q8[2 * e], q8[2 * e + 1]);
                     l += ((q8[0] + q8[1]) + (q8[2] + q8[3])) + ((q8[4] + q8[5]) + (q8[6] + q8[7]));
                     tmem_wait_st();
-                } else if (lane == 0) {
-                    mbar_arrive(&room.p_full[slot][0]);
                 }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&room.p_full[slot][1]);
+                if (lane == 0) mbar_arrive(&room.p_full[slot][t & 1]);
                 ++t, ++j;
             }
-            // ---- the piece's end ----------------------------------------------
-            if (own > 0) wait(&room.o_done[slot], t - 1);
-            tc_fence_after_sync();
-            const bool full = count == P.n;
-            const int64_t rec = (((int64_t)cta * p.lanes + side) * 2 + (P.k0 > 0 ? 0 : 1)) * kTrSlots + (P.share ? slot : 0);
-            float w0 = slot == 0 ? 1.f : 0.f, w1 = 1.f - w0, top = m;
-            if (!P.alone) {
-                // both slots have this row: joined, a half of the dims each
-                bar_sync(both, 2 * kTrRows);                       // the lines are not read any more
-                room.ml[slot][r] = make_float2(m, l);
-                tc_fence_before_sync();
-                bad = bar_or(both, 2 * kTrRows, bad);
+            n += count;
+            // ---- the piece's end ------------------------------------------------
+            if (own > 0) {
+                wait(&room.o_done[slot][(t - 1) & 1], (t - 1) >> 1);
                 tc_fence_after_sync();
-                const float2 a = room.ml[0][r], b = room.ml[1][r];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&room.lines_empty);
-                top = fmaxf(a.x, b.x);
-                const float ref = top == -INFINITY ? 0.f : top;
-                w0 = ex2(a.x - ref), w1 = ex2(b.x - ref);
-                l = a.y * w0 + b.y * w1;
-            }
-            const int from = P.alone ? 0 : slot * (D / 2), to = P.alone ? D : from + D / 2;
-            const float norm = full ? (kFp8 ? p.v_scale : 1.f) / l : 1.f;
-            const bool use0 = !P.alone || slot == 0, use1 = !P.alone || slot == 1;
-            w0 *= norm, w1 *= norm;
-            const int64_t row = (int64_t)(P.s.q0 + node) * p.num_q_heads + P.g * G + head;
+                const bool full = count == P.n;
+                const int64_t rec = (((int64_t)cta * p.lanes + side) * 2 + (P.k0 > 0 ? 0 : 1)) * kTrSlots + (P.share ? slot : 0);
+                float w0 = slot == 0 ? 1.f : 0.f, w1 = 1.f - w0, top = m;
+                if (!P.alone) {
+                    // both slots have this row: joined, a half of the dims each
+                    bar_sync(both, 2 * kTrRows);                   // the lines are not read any more
+                    room.ml[slot][r] = make_float2(m, l);
+                    tc_fence_before_sync();
+                    bad = bar_or(both, 2 * kTrRows, bad);
+                    tc_fence_after_sync();
+                    const float2 a = room.ml[0][r], b = room.ml[1][r];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&room.lines_empty);
+                    top = fmaxf(a.x, b.x);
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    w0 = ex2(a.x - ref), w1 = ex2(b.x - ref);
+                    l = a.y * w0 + b.y * w1;
+                }
+                const int from = P.alone ? 0 : slot * (D / 2), to = P.alone ? D : from + D / 2;
+                const float norm = full ? (kFp8 ? p.v_scale : 1.f) / l : 1.f;
+                const bool use0 = !P.alone || slot == 0, use1 = !P.alone || slot == 1;
+                w0 *= norm, w1 *= norm;
+                const int64_t row = row_of(P);
 #pragma unroll 1
-            for (int d = from; live && d < to; d += 32) {
-                float o[32];
+                for (int d = from; live && d < to; d += 32) {
+                    float o[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                uint32_t v[32];
-                if (use0) {
-                    tmem_ld32(tO + d, v);
-                    tmem_wait_ld(v);
+                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                    uint32_t v[32];
+                    if (use0) {
+                        tmem_ld32(tO + d, v);
+                        tmem_wait_ld(v);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * w0;
+                        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * w0;
+                    }
+                    if (use1) {
+                        tmem_ld32(tO + D + d, v);
+                        tmem_wait_ld(v);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(v[e]), w1, o[e]);
+                    }
+                    if (!valid || failed) {
+                    } else if (full) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * D + d);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            dst[q] = make_uint4(M::pack(o[8 * q], o[8 * q + 1]), M::pack(o[8 * q + 2], o[8 * q + 3]),
+                                                M::pack(o[8 * q + 4], o[8 * q + 5]), M::pack(o[8 * q + 6], o[8 * q + 7]));
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(p.rec_o + (rec * kTrRows + r) * D + d);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                    }
+                    __syncwarp();
                 }
-                if (use1) {
-                    tmem_ld32(tO + D + d, v);
-                    tmem_wait_ld(v);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(v[e]), w1, o[e]);
-                }
-                if (!valid || failed) {
-                } else if (full) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * D + d);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        dst[q] = make_uint4(M::pack(o[8 * q], o[8 * q + 1]), M::pack(o[8 * q + 2], o[8 * q + 3]),
-                                            M::pack(o[8 * q + 4], o[8 * q + 5]), M::pack(o[8 * q + 6], o[8 * q + 7]));
-                } else {
-                    float4* dst = reinterpret_cast<float4*>(p.rec_o + (rec * kTrRows + r) * D + d);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-                }
-                __syncwarp();
-            }
-            if (bad && valid && !failed) {
-                // what was taken out of V, for a row that sees it: the sums are
-                // what adding it gives
-                for (int i = 0; i < P.s.C; ++i) {
-                    const int key = base + i;
-                    if (!line.has(i) || key < P.k0 * kTrKeys || key >= P.k1 * kTrKeys) continue;
-                    const int blk = p.block_tables[(size_t)P.b * p.max_blocks_per_seq + key / p.block_size];
-                    if (blk < 0 || blk >= p.num_blocks) continue;
-                    const int64_t at = (((int64_t)blk * p.block_size + key % p.block_size) * p.num_kv_heads + P.g) * D;
+                if (bad && valid && !failed) {
+                    // what was taken out of V, for a row that sees it: the sums are
+                    // what adding it gives
+                    for (int i = 0; i < P.s.C; ++i) {
+                        const int key = base + i;
+                        if (!line.has(i) || key < P.k0 * kTrKeys || key >= P.k1 * kTrKeys) continue;
+                        const int blk = p.block_tables[(size_t)P.b * p.max_blocks_per_seq + key / p.block_size];
+                        if (blk < 0 || blk >= p.num_blocks) continue;
+                        const int64_t at = (((int64_t)blk * p.block_size + key % p.block_size) * p.num_kv_heads + P.g) * D;
 #pragma unroll 1
-                    for (int d = from; d < to; ++d) {
-                        float y;
-                        if constexpr (kFp8)
-                            y = (static_cast<const uint8_t*>(p.v_cache)[at + d] & 0x7f) == 0x7f ? NAN : 0.f;
-                        else
-                            y = (float)static_cast<const T*>(p.v_cache)[at + d];
-                        if (isfinite(y)) continue;
-                        if (full) {
-                            T& o = static_cast<T*>(p.out)[row * D + d];
-                            o = from_float<T>((float)o + y);
-                        } else {
-                            p.rec_o[(rec * kTrRows + r) * D + d] += y;
+                        for (int d = from; d < to; ++d) {
+                            float y;
+                            if constexpr (kFp8)
+                                y = (static_cast<const uint8_t*>(p.v_cache)[at + d] & 0x7f) == 0x7f ? NAN : 0.f;
+                            else
+                                y = (float)static_cast<const T*>(p.v_cache)[at + d];
+                            if (isfinite(y)) continue;
+                            if (full) {
+                                T& o = static_cast<T*>(p.out)[row * D + d];
+                                o = from_float<T>((float)o + y);
+                            } else {
+                                p.rec_o[(rec * kTrRows + r) * D + d] += y;
+                            }
                         }
                     }
                 }
+                if (!full && valid && !failed && (P.alone || slot == 0)) p.rec_ml[rec * kTrRows + r] = make_float2(top, l);
+                // O of both slots is read: the next piece's products may overwrite it
+                tc_fence_before_sync();
+                if (!P.alone) bar_sync(both, 2 * kTrRows);
+                __syncwarp();
             }
-            if (!full && valid && !failed && (P.alone || slot == 0)) p.rec_ml[rec * kTrRows + r] = make_float2(top, l);
-            // O of both slots is read: the next piece's products may overwrite it
-            tc_fence_before_sync();
-            if (!P.alone) bar_sync(both, 2 * kTrRows);
         }
         if (failed && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
     }
@@ -1045,8 +1031,9 @@ cudaError_t launch_tree_t(const CUtensorMap& tmk, const CUtensorMap& tmv, const 
                            dim3(kTrMergeThreads), 0, stream, p);
 }
 
-cudaError_t launch_tree_attention(int dtype, int head_dim, bool fp8, const CUtensorMap& tmk, const CUtensorMap& tmv,
-                                  const CUtensorMap& tmq, const TreeParams& p, cudaStream_t stream) {
+cudaError_t launch_tree_attention(int dtype, int head_dim, bool fp8, const CUtensorMap& tmk,
+                                  const CUtensorMap& tmv, const CUtensorMap& tmq, const TreeParams& p,
+                                  cudaStream_t stream) {
     const bool bf16 = dtype == PA_BF16;
     if (fp8) return bf16 ? launch_tree_t<__nv_bfloat16, 128, true>(tmk, tmv, tmq, p, stream)
                          : launch_tree_t<__half, 128, true>(tmk, tmv, tmq, p, stream);

@@ -46,8 +46,10 @@ size_t tree_plan(TreeParams& p, int head_dim, void* workspace);
 cudaError_t launch_tree_attention(int dtype, int head_dim, bool fp8, const CUtensorMap& tmk,
                                   const CUtensorMap& tmv, const CUtensorMap& tmq, const TreeParams& p,
                                   cudaStream_t stream);
-// Nodes of a query tile, the box of its map.
+// Nodes of a query tile: the box of its map.
 int tree_nodes_per_tile(int group);
+// Keys of a tile: the tiles of a call are counted in 31 bits.
+constexpr int kTreeKeys = 64;
 
 struct AcceptParams {
     const int64_t* draft;          // [T]
