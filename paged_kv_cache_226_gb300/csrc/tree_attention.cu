@@ -13,8 +13,8 @@
 // slots take its key tiles in turn, or, where those are few, one slot takes
 // them all and the other the next pair's.  So one slot's softmax runs beside
 // the other's products, and K and V are read once for 256 rows.  More rows
-// than that go to CTAs side by side ("lanes") that walk the same keys at the
-// same time, so that the second reads them from L2.
+// than that go to CTAs side by side that walk the same keys at the same time,
+// so that the second reads them from L2.
 //
 //   S = Q K^T           128 x 64 x D, operands in shared memory
 //   P = 2^(S - m)       m a reference of the row's maximum, raised only when
@@ -30,18 +30,23 @@
 // S of 128 keys per slot 8 heads x 4 sequences of 32k to 50k tokens at 240 rows
 // took 190 us (134 with no softmax and half of P V), with one of 64 keys 227.
 //
-// The key tiles of all pairs, in order, are dealt out to persistent CTAs in
-// equal ranges, or, where contexts are short, whole pairs are.  A pair that
-// more than one CTA meets leaves records (O, m, sum), joined by a second
+// The CTAs side by side, one for each 256 rows and KV head (or so many KV
+// heads as divide the SMs well), make a lane.  The key tiles of all sequences,
+// in order, are dealt out to the lanes in equal ranges, or, where contexts are
+// short, whole pairs are.  KV heads walk along together because their rows are
+// neighbours in memory (4 x 32k to 50k tokens, 8 heads, without the softmax
+// 130 us, with a range of its own for each head 122).  A pair that
+// more than one lane meets leaves records (O, m, sum), joined by a second
 // kernel.  K and V come once from HBM, 512 B a token and KV head at D 128;
 // the products cost 6 D operations (P in two parts) for each row and token.
 //
-// An E4M3 cache's codes are brought to the 16-bit type (exactly) by three
+// An E4M3 cache's codes are brought to the 16-bit type (exactly) by four
 // warps between the loaders' ring and the operands'.
 //
-// Warps: 0 loads K tiles and 2 V tiles, 1 issues S and 3 P V, 4 .. 7 are slot
-// 0's softmax and 8 .. 11 slot 1's, 12 makes the trees' lines, 13 .. 15
-// convert codes.  A barrier's parity tells a phase from the one before it
+// Warps: 0 loads K tiles and 2 V tiles, 1 and 3 issue the slots' S, 13 and 14
+// their P V, 4 .. 7 are slot 0's softmax and 8 .. 11 slot 1's, 12 makes the
+// trees' lines, 16 .. 19 convert codes.  (An issuer takes some 1200 cycles
+// for a tile's S beside these warps, so one for both slots would hold them up.)  A barrier's parity tells a phase from the one before it
 // alone, so whoever waits for a phase has seen that the one before is over: by
 // waiting for every phase in turn, or as the comments at the waits say.
 #include "decode_tile.cuh"
@@ -56,12 +61,15 @@ constexpr int kTrSlots = 2;
 constexpr int kTrQStages = 2;
 constexpr int kTrSoftmaxWarps = 4 * kTrSlots;
 constexpr int kTrLineWarp = 4 + kTrSoftmaxWarps;
-constexpr int kTrConverters = 3;
-constexpr int kTrThreads = (kTrLineWarp + 1 + kTrConverters) * 32;
-// Registers: 512 threads are launched with 128 each; the softmax warps take
-// over what the others give up.
-constexpr int kTrControlRegs = 56, kTrSoftmaxRegs = 200;
-static_assert(kTrThreads == 512 && 2 * (kTrControlRegs + kTrSoftmaxRegs) <= 4 * 128, "registers of the CTA");
+constexpr int kTrConvertWarp = 4 + kTrLineWarp;
+constexpr int kTrConverters = 4;               // E4M3 only
+__host__ __device__ constexpr int tr_threads(bool fp8) { return (kTrConvertWarp + (fp8 ? kTrConverters : 0)) * 32; }
+// Registers: 512 threads are launched with 128 each (640 with 96); the softmax
+// warps take over what the others give up.
+constexpr int kTrControlRegs = 56;
+__host__ __device__ constexpr int tr_softmax_regs(bool fp8) { return fp8 ? 152 : 200; }
+static_assert(256 * tr_softmax_regs(false) + 256 * kTrControlRegs <= 512 * 128 &&
+              256 * tr_softmax_regs(true) + 384 * kTrControlRegs <= 640 * 96, "registers of the CTA");
 constexpr int kTrCtas = 152;                   // one per SM
 constexpr int kTrMinTiles = 8;                 // weight of a CTA's range at least, where there are records
 constexpr int kTrWholeTiles = 8;               // longest contexts, in tiles, whose pairs stay whole
@@ -98,7 +106,7 @@ struct TrRoom {
     uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
     uint64_t kc_full[5], kc_empty[5], vc_full[5], vc_empty[5];
     uint64_t q_full[kTrQStages], q_empty[kTrQStages], lines_full, lines_empty;
-    uint64_t s_full[kTrSlots][2], p_full[kTrSlots][2], o_done[kTrSlots][2], done[2];
+    uint64_t s_full[kTrSlots][2], p_full[kTrSlots][2], o_done[kTrSlots][2], done[2 * kTrSlots];
     uint32_t tmem;
 };
 
@@ -169,7 +177,7 @@ struct TrWalk {
         return s.C > 0 ? (p.whole ? 1u : (unsigned)(tiles(s) + kTrPairWeight)) : 0u;
     }
     static __device__ __forceinline__ unsigned weight(const TreeParams& p, const TreeSeq& s) {
-        return each(p, s) * p.num_kv_heads;
+        return each(p, s) * (p.num_kv_heads / p.heads);
     }
     __device__ __forceinline__ void read(const TreeParams& p, bool report) {
         const int lane = threadIdx.x & 31, b = base_b + lane;
@@ -192,8 +200,9 @@ struct TrWalk {
         read(p, report);
         return __reduce_add_sync(0xffffffffu, n) + total;
     }
-    // The next piece with work in lane `side`.
-    __device__ __forceinline__ bool next(const TreeParams& p, int side, TrPiece& P) {
+    // The next piece with work for the CTA of query tiles `side` and KV heads
+    // head, head + p.heads, ...
+    __device__ __forceinline__ bool next(const TreeParams& p, int side, int head, TrPiece& P) {
         while (at < end) {
             while (at >= base + total) {
                 base += total;
@@ -210,7 +219,7 @@ struct TrWalk {
             const unsigned first = base + (who > 0 ? before : 0u), off = at - first;
             const unsigned one = each(p, P.s), pair = off / one, in = off - pair * one;
             P.b = base_b + who;
-            P.g = (int)pair;
+            P.g = head + (int)pair * p.heads;
             if (p.whole) {
                 P.k0 = 0, P.k1 = P.n;
                 ++at;
@@ -235,7 +244,7 @@ struct TrWalk {
     }
 };
 
-// How weight N is dealt to the CTAs of a lane: CTA c has [c N / ctas, (c + 1) N / ctas).
+// How weight N is dealt to the lanes: lane c has [c N / ctas, (c + 1) N / ctas).
 struct TrDeal {
     unsigned N, ctas;
     __device__ __forceinline__ TrDeal(const TreeParams& p, unsigned n) : N(n) {
@@ -345,12 +354,13 @@ __device__ __forceinline__ void control_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTrControlRegs));
 }
 
+template <int kRegs>
 __device__ __forceinline__ void softmax_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTrSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 template <typename T, int D, bool kFp8>
-__global__ void __launch_bounds__(kTrThreads, 1)
+__global__ void __launch_bounds__(tr_threads(kFp8), 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_k,
                           const __grid_constant__ CUtensorMap tmap_v,
                           const __grid_constant__ CUtensorMap tmap_q,
@@ -363,25 +373,26 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];        // the kernel has no other
     TrRoom& room = *reinterpret_cast<TrRoom*>(smem + Lay::kRoom);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int side = blockIdx.x % p.lanes;                   // the lane of CTAs
-    const unsigned cta = blockIdx.x / p.lanes;
+    // CTA of the lane, and lane
+    const int head = blockIdx.x % p.heads, side = blockIdx.x / p.heads % p.sides;
+    const unsigned cta = blockIdx.x / p.heads / p.sides;
     const int G = p.group, per_tile = tr_nodes_per_tile(G);
 
     if (threadIdx.x == 0) {
         constexpr int kFillers = kFp8 ? kTrConverters : 1;
-        for (int i = 0; i < Lay::kKStages; ++i) mbar_init(&room.k_full[i], kFillers), mbar_init(&room.k_empty[i], 1);
-        for (int i = 0; i < Lay::kVStages; ++i) mbar_init(&room.v_full[i], kFillers), mbar_init(&room.v_empty[i], 1);
+        for (int i = 0; i < Lay::kKStages; ++i) mbar_init(&room.k_full[i], kFillers), mbar_init(&room.k_empty[i], kTrSlots);
+        for (int i = 0; i < Lay::kVStages; ++i) mbar_init(&room.v_full[i], kFillers), mbar_init(&room.v_empty[i], kTrSlots);
         for (int i = 0; i < Lay::kCodeStages; ++i) {
             mbar_init(&room.kc_full[i], 1), mbar_init(&room.kc_empty[i], kTrConverters);
             mbar_init(&room.vc_full[i], 1), mbar_init(&room.vc_empty[i], kTrConverters);
         }
-        for (int i = 0; i < kTrQStages; ++i) mbar_init(&room.q_full[i], 1), mbar_init(&room.q_empty[i], 1);
+        for (int i = 0; i < kTrQStages; ++i) mbar_init(&room.q_full[i], 1), mbar_init(&room.q_empty[i], kTrSlots);
         mbar_init(&room.lines_full, 1), mbar_init(&room.lines_empty, kTrSoftmaxWarps);
         for (int i = 0; i < kTrSlots; ++i) {
             for (int j = 0; j < 2; ++j)
                 mbar_init(&room.s_full[i][j], 1), mbar_init(&room.p_full[i][j], 4), mbar_init(&room.o_done[i][j], 1);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(&room.done[i], 1);
+        for (int i = 0; i < 2 * kTrSlots; ++i) mbar_init(&room.done[i], 1);
         fence_barrier_init();
     }
     if (warp == 1) tmem_alloc(&room.tmem, 512);
@@ -420,7 +431,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 TrRing<kTrQStages> q;
                 bool ok = true, held = false;
                 if (keys && lane == 0) prefetch_tensor_map(&tmap_q);
-                while (ok && !held && walk.next(p, side, P)) {
+                while (ok && !held && walk.next(p, side, head, P)) {
                     const int32_t* table = p.block_tables + (size_t)P.b * p.max_blocks_per_seq;
                     // block ids: lane i has box i % 4 of tile i / 4 of eight, the
                     // next eight tiles' requested while these are loaded
@@ -480,99 +491,67 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 load(std::false_type());
         } else {
             // --------------------------------------------------------------
-            // issuers: S (warp 1) and P V (warp 3), tile by tile and slot by
-            // slot.  S overwrites the P of two tiles before, so it waits for that P V.
+            // issuers of S: S overwrites the P of two tiles before, so it
+            // waits for that P V.  Both see every stage full before they give
+            // it back, whether it is theirs or not, so neither can give back
+            // the next tile in its place.
             // --------------------------------------------------------------
-            constexpr uint32_t kIdS = idesc_f16(kTrRows, kTrKeys, kBf16, false);
-            constexpr uint32_t kIdPV = idesc_f16(kTrRows, D, kBf16, true);
+            constexpr uint32_t kId = idesc_f16(kTrRows, kTrKeys, kBf16, false);
+            const int slot = warp >> 1;
             const uint64_t dq = smem_desc_sw128(smem_u32(smem + Lay::kQ), 16, 1024);
             const uint64_t dk = smem_desc_sw128(smem_u32(smem + Lay::kK), 16, 1024);
-            const uint64_t dv = smem_desc_sw128(smem_u32(smem + Lay::kV), Lay::kHalf, 1024);
-            int tiles[kTrSlots] = {0, 0};
+            const uint32_t s0 = tmem + kTrS + 2 * kTrKeys * slot;
+            TrRing<Lay::kKStages> at;
+            TrRing<kTrQStages> q;
+            int t = 0;
             bool ok = true;
             auto wait = [&](uint64_t* bar, int phase) { ok = ok && tr_wait(p, bar, phase); };
-            if (warp == 1) {
-                TrRing<Lay::kKStages> at;
-                TrRing<kTrQStages> q;
-                while (ok && walk.next(p, side, P)) {
-                    const int q0 = q.at;
-                    for (int i = 0; i < P.query_tiles(); ++i, q.step()) wait(&room.q_full[q.at], q.lap);
-                    for (int k = P.k0; ok && k < P.k1; ++k, at.step()) {
-                        wait(&room.k_full[at.at], at.lap);
+            while (ok && walk.next(p, side, head, P)) {
+                const int q0 = q.at;
+                for (int i = 0; i < P.query_tiles(); ++i, q.step()) wait(&room.q_full[q.at], q.lap);
+                const uint64_t query = dq + (P.share ? q0 ^ slot : q0) * (Lay::kQTile >> 4);
+                for (int k = P.k0; ok && k < P.k1; ++k, at.step()) {
+                    wait(&room.k_full[at.at], at.lap);
+                    if (P.has(slot, k)) {
+                        const int buf = t & 1;
+                        if (t > 1) wait(&room.o_done[slot][buf], (t >> 1) - 1);
+                        if (!ok) break;
+                        ++t;
+                        tc_fence_after_sync();
                         const uint64_t key = dk + at.at * (Lay::kTile >> 4);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int slot = 0; slot < kTrSlots; ++slot) {
-                            if (!P.has(slot, k)) continue;
-                            const int t = tiles[slot]++, buf = t & 1;
-                            if (t > 1) wait(&room.o_done[slot][buf], (t >> 1) - 1);
-                            if (!ok) break;
-                            tc_fence_after_sync();
-                            const uint64_t query = dq + (P.share ? q0 ^ slot : q0) * (Lay::kQTile >> 4);
-                            if (elect_one()) {
-#pragma unroll
-                                for (int kk = 0; kk < D / 16; ++kk)
-                                    mma_f16_ss(tmem + kTrS + kTrKeys * (2 * slot + buf),
-                                               query + (kk >> 2) * (Lay::kQHalf >> 4) + (kk & 3) * 2,
-                                               key + (kk >> 2) * (Lay::kHalf >> 4) + (kk & 3) * 2, kIdS, kk > 0);
-                                mma_commit(&room.s_full[slot][buf]);
-                                if (!P.share || slot == kTrSlots - 1) mma_commit(&room.k_empty[at.at]);     // its last user
-                            }
-                            __syncwarp();
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                mma_f16_ss(s0 + kTrKeys * buf, query + (kk >> 2) * (Lay::kQHalf >> 4) + (kk & 3) * 2,
+                                           key + (kk >> 2) * (Lay::kHalf >> 4) + (kk & 3) * 2, kId, kk > 0);
+                            mma_commit(&room.s_full[slot][buf]);
+                            mma_commit(&room.k_empty[at.at]);
                         }
-                    }
-                    if (ok && elect_one()) {
-                        mma_commit(&room.q_empty[q0]);
-                        if (P.share) mma_commit(&room.q_empty[q0 ^ 1]);
+                    } else if (ok && elect_one()) {
+                        mbar_arrive(&room.k_empty[at.at]);
                     }
                     __syncwarp();
                 }
-            } else {
-                TrRing<Lay::kVStages> at;
-                while (ok && walk.next(p, side, P)) {
-                    for (int k = P.k0; ok && k < P.k1; ++k, at.step()) {
-                        wait(&room.v_full[at.at], at.lap);
-                        const uint64_t value = dv + at.at * (Lay::kTile >> 4);
-#pragma unroll
-                        for (int slot = 0; slot < kTrSlots; ++slot) {
-                            if (!P.has(slot, k)) continue;
-                            const bool first = P.first(slot, k);
-                            const int t = tiles[slot]++, buf = t & 1;
-                            wait(&room.p_full[slot][buf], t >> 1);
-                            if (!ok) break;
-                            tc_fence_after_sync();
-                            if (elect_one()) {
-                                // keys 16 kk .. 16 kk + 15: hi parts in columns 16 kk ..
-                                // 16 kk + 7, lo parts in the next eight
-#pragma unroll
-                                for (int kk = 0; kk < kTrKeys / 16; ++kk) {
-#pragma unroll
-                                    for (int part = 0; part < 2; ++part)
-                                        mma_f16_ts(tmem + kTrO + D * slot,
-                                                   tmem + kTrS + kTrKeys * (2 * slot + buf) + 16 * kk + 8 * part,
-                                                   value + kk * (16 * 128 >> 4), kIdPV, !first || kk > 0 || part > 0);
-                                }
-                                mma_commit(&room.o_done[slot][buf]);
-                                if (!P.share || slot == kTrSlots - 1) mma_commit(&room.v_empty[at.at]);
-                            }
-                            __syncwarp();
-                        }
-                    }
+                if (ok && elect_one()) {
+                    mma_commit(&room.q_empty[q0]);
+                    if (P.share) mma_commit(&room.q_empty[q0 ^ 1]);
                 }
+                __syncwarp();
             }
             // the products are done before tensor memory and operands are given up
-            if (elect_one()) mma_commit(&room.done[warp >> 1]);
+            if (elect_one()) mma_commit(&room.done[slot]);
             __syncwarp();
-            ok = tr_wait(p, &room.done[warp >> 1], 0) && ok;
+            ok = tr_wait(p, &room.done[slot], 0) && ok;
             if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
         }
-    } else if (warp >= kTrLineWarp) {
+    } else if (warp >= kTrLineWarp && warp < kTrConvertWarp) {
         control_registers();
         if (warp == kTrLineWarp) {
             // --------------------------------------------------------------
             // the trees' lines, a piece ahead of those who read them
             // --------------------------------------------------------------
             bool ok = true;
-            for (int i = 0; ok && walk.next(p, side, P); ++i) {
+            for (int i = 0; ok && walk.next(p, side, head, P); ++i) {
                 uint32_t w[kLineWords][kLineWords] = {};
                 const bool tree = P.k1 * kTrKeys > P.s.L - P.s.C;      // the piece has some of it
                 if (tree) {
@@ -595,22 +574,70 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 if (lane == 0) mbar_arrive(&room.lines_full);
             }
             if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
-        } else if constexpr (kFp8) {
+        } else if (warp <= kTrLineWarp + kTrSlots) {
+            // --------------------------------------------------------------
+            // issuers of P V
+            // --------------------------------------------------------------
+            constexpr uint32_t kId = idesc_f16(kTrRows, D, kBf16, true);
+            const int slot = warp - kTrLineWarp - 1;
+            const uint64_t dv = smem_desc_sw128(smem_u32(smem + Lay::kV), Lay::kHalf, 1024);
+            const uint32_t o = tmem + kTrO + D * slot, p0 = tmem + kTrS + 2 * kTrKeys * slot;
+            TrRing<Lay::kVStages> at;
+            int t = 0;
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, int phase) { ok = ok && tr_wait(p, bar, phase); };
+            while (ok && walk.next(p, side, head, P)) {
+                for (int k = P.k0; ok && k < P.k1; ++k, at.step()) {
+                    wait(&room.v_full[at.at], at.lap);
+                    if (P.has(slot, k)) {
+                        const int buf = t & 1;
+                        wait(&room.p_full[slot][buf], t >> 1);
+                        if (!ok) break;
+                        ++t;
+                        tc_fence_after_sync();
+                        const uint64_t value = dv + at.at * (Lay::kTile >> 4);
+                        const bool first = P.first(slot, k);
+                        if (elect_one()) {
+                            // keys 16 kk .. 16 kk + 15: hi parts in columns 16 kk ..
+                            // 16 kk + 7, lo parts in the next eight
+#pragma unroll
+                            for (int kk = 0; kk < kTrKeys / 16; ++kk) {
+#pragma unroll
+                                for (int part = 0; part < 2; ++part)
+                                    mma_f16_ts(o, p0 + kTrKeys * buf + 16 * kk + 8 * part, value + kk * (16 * 128 >> 4), kId,
+                                               !first || kk > 0 || part > 0);
+                            }
+                            mma_commit(&room.o_done[slot][buf]);
+                            mma_commit(&room.v_empty[at.at]);
+                        }
+                    } else if (ok && elect_one()) {
+                        mbar_arrive(&room.v_empty[at.at]);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (elect_one()) mma_commit(&room.done[kTrSlots + slot]);
+            __syncwarp();
+            ok = tr_wait(p, &room.done[kTrSlots + slot], 0) && ok;
+            if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
+        }
+    } else if (warp >= kTrConvertWarp) {
+        control_registers();
+        if constexpr (kFp8) {
             // --------------------------------------------------------------
             // converters: a K tile's codes, then its V tile's.  A pass brings 16
             // codes a lane of four rows; lanes are laid out so that eight
             // neighbours read and write different banks: four chunks of a row
             // beside the other four of the next.
             // --------------------------------------------------------------
-            const int who = warp - kTrLineWarp - 1;
+            const int who = warp - kTrConvertWarp;
             const int c = lane & 7, upper = c >> 2;
             const int r4 = 2 * (lane >> 4) + (upper ^ ((lane >> 3) & 1));
-            int turn = who;                                            // passes deal out evenly over the tiles
             TrRing<Lay::kKStages> k_at;
             TrRing<Lay::kVStages> v_at;
             TrRing<Lay::kCodeStages> at;
             bool ok = true;
-            while (ok && walk.next(p, side, P)) {
+            while (ok && walk.next(p, side, head, P)) {
                 for (int k = P.k0; ok && k < P.k1; ++k, k_at.step(), v_at.step(), at.step()) {
 #pragma unroll 1
                     for (int kind = 0; ok && kind < 2; ++kind) {
@@ -622,7 +649,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         const uint8_t* src = smem + (keys ? Lay::kKCodes : Lay::kVCodes) + at.at * Lay::kCodes;
                         uint8_t* dst = smem + (keys ? Lay::kK : Lay::kV) + st * Lay::kTile + upper * Lay::kHalf;
 #pragma unroll 2
-                        for (int i = turn; i < kTrKeys / 4; i += kTrConverters) {
+                        for (int i = who; i < kTrKeys / 4; i += kTrConverters) {
                             const int r = 4 * i + r4;
                             const uint4 x = lds128(src + r * 128 + ((c ^ (r & 7)) << 4));
                             uint32_t y[8];
@@ -641,7 +668,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                             *reinterpret_cast<uint4*>(dst + r * 128 + (chunk << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
                             *reinterpret_cast<uint4*>(dst + r * 128 + ((chunk ^ 1) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
                         }
-                        turn = turn == 0 ? kTrConverters - 1 : turn - 1;      // 16 passes are 1 modulo 3
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -654,7 +680,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
         }
     } else {
-        softmax_registers();
+        softmax_registers<tr_softmax_regs(kFp8)>();
         // ------------------------------------------------------------------
         // softmax and epilogue: this thread owns row r of its slot's tiles
         // ------------------------------------------------------------------
@@ -663,7 +689,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const uint32_t lanes_at = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tO = tmem + kTrO + lanes_at;                // slot 0's, slot 1's D columns on
         const int barrier = 1 + slot, both = 3;                    // named barriers
-        const int in_tile = r / G, head = r - in_tile * G;
+        const int in_tile = r / G, in_group = r - in_tile * G;
         const float sl = p.scale_log2;
         const uint64_t sl2 = f32x2_pack(sl, sl);
         bool failed = false;                  // a wait ran out: finish the loops without waiting
@@ -672,10 +698,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         };
         auto node_of = [&](const TrPiece& X) { return (kTrSlots * side + (X.share ? slot : 0)) * per_tile + in_tile; };
         auto row_of = [&](const TrPiece& X) {
-            return (int64_t)(X.s.q0 + node_of(X)) * p.num_q_heads + X.g * G + head;
+            return (int64_t)(X.s.q0 + node_of(X)) * p.num_q_heads + X.g * G + in_group;
         };
         int n = 0, t = 0;                     // tiles of the CTA and of the slot so far
-        for (int piece = 0; walk.next(p, side, P); ++piece) {
+        for (int piece = 0; walk.next(p, side, head, P); ++piece) {
             const int base = P.s.L - P.s.C;
             const int count = P.k1 - P.k0, own = P.own(slot);
             const int node = node_of(P);
@@ -819,7 +845,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 wait(&room.o_done[slot][(t - 1) & 1], (t - 1) >> 1);
                 tc_fence_after_sync();
                 const bool full = count == P.n;
-                const int64_t rec = (((int64_t)cta * p.lanes + side) * 2 + (P.k0 > 0 ? 0 : 1)) * kTrSlots + (P.share ? slot : 0);
+                const int64_t rec = ((int64_t)blockIdx.x * 2 + (P.k0 > 0 ? 0 : 1)) * kTrSlots + (P.share ? slot : 0);
                 float w0 = slot == 0 ? 1.f : 0.f, w1 = 1.f - w0, top = m;
                 if (!P.alone) {
                     // both slots have this row: joined, a half of the dims each
@@ -944,7 +970,7 @@ __global__ void __launch_bounds__(kTrMergeThreads)
         if (i < b) before += w;
     }
     const TrDeal deal(p, __reduce_add_sync(0xffffffffu, all));
-    const unsigned each = TrWalk::each(p, s), begin = __reduce_add_sync(0xffffffffu, before) + g * each;
+    const unsigned each = TrWalk::each(p, s), begin = __reduce_add_sync(0xffffffffu, before) + g / p.heads * each;
     const unsigned c0 = deal.cta_of(begin + kTrPairWeight), c1 = deal.cta_of(begin + each - 1);
     if (c0 == c1) return;                      // written by that CTA
     const int side = tile / kTrSlots;
@@ -962,7 +988,7 @@ __global__ void __launch_bounds__(kTrMergeThreads)
             for (int i = 0; i < kAhead; ++i) {
                 ml[i] = make_float2(-INFINITY, 0.f);
                 if (c + i > c1) continue;
-                const int64_t rec = (((int64_t)(c + i) * p.lanes + side) * 2 + (c + i == c0 ? 1 : 0)) * kTrSlots + slot;
+                const int64_t rec = ((((int64_t)(c + i) * p.sides + side) * p.heads + g % p.heads) * 2 + (c + i == c0 ? 1 : 0)) * kTrSlots + slot;
                 ml[i] = p.rec_ml[rec * kTrRows + r];
                 const float* src = p.rec_o + (rec * kTrRows + r) * D + kDims * lane;
                 if constexpr (kDims == 4) {
@@ -1003,13 +1029,18 @@ __global__ void __launch_bounds__(kTrMergeThreads)
 size_t tree_plan(TreeParams& p, int head_dim, void* workspace) {
     const int per_tile = kTrRows / p.group;
     const int query_tiles = (p.max_query + per_tile - 1) / per_tile;
-    const int64_t pairs = (int64_t)p.num_seqs * p.num_kv_heads;
     const int tiles = (p.max_context + kTrKeys - 1) / kTrKeys;
-    p.lanes = query_tiles > kTrSlots ? (query_tiles + kTrSlots - 1) / kTrSlots : 1;
+    p.sides = query_tiles > kTrSlots ? (query_tiles + kTrSlots - 1) / kTrSlots : 1;
+    // as many KV heads side by side as leave at most 4 % of the SMs without a CTA
+    p.heads = 1;
+    for (int d = 2; d <= p.num_kv_heads && d * p.sides <= kTrCtas; ++d)
+        if (p.num_kv_heads % d == 0 && kTrCtas / (d * p.sides) * (d * p.sides) * 25 >= kTrCtas * 24) p.heads = d;
     p.whole = tiles <= kTrWholeTiles;
+    const int64_t pairs = (int64_t)p.num_seqs * (p.num_kv_heads / p.heads);       // of a lane's CTA
     const int64_t most = p.whole ? pairs : (pairs * (tiles + kTrPairWeight) + kTrMinTiles - 1) / kTrMinTiles;
-    p.ctas = (int)(most < kTrCtas / p.lanes ? (most > 0 ? most : 1) : kTrCtas / p.lanes);
-    const size_t rows = p.whole ? 0 : (size_t)p.ctas * p.lanes * 2 * kTrSlots * kTrRows;
+    const int lanes = kTrCtas / (p.heads * p.sides);
+    p.ctas = (int)(most < lanes ? (most > 0 ? most : 1) : lanes);
+    const size_t rows = p.whole ? 0 : (size_t)p.ctas * p.heads * p.sides * 2 * kTrSlots * kTrRows;
     p.rec_o = static_cast<float*>(workspace);
     p.rec_ml = reinterpret_cast<float2*>(p.rec_o + rows * head_dim);
     return rows * (head_dim * sizeof(float) + sizeof(float2)) + 16;
@@ -1022,7 +1053,7 @@ cudaError_t launch_tree_t(const CUtensorMap& tmk, const CUtensorMap& tmv, const 
     cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<T, D, kFp8>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_with_pdl(tree_attention_kernel<T, D, kFp8>, dim3((unsigned)(p.ctas * p.lanes)), dim3(kTrThreads), kSmem,
+    e = launch_with_pdl(tree_attention_kernel<T, D, kFp8>, dim3((unsigned)(p.ctas * p.sides * p.heads)), dim3(tr_threads(kFp8)), kSmem,
                         stream, tmk, tmv, tmq, p);
     if (e != cudaSuccess || p.whole) return e;
     const int per_tile = kTrRows / p.group, query_tiles = (p.max_query + per_tile - 1) / per_tile;

@@ -27,10 +27,10 @@ struct TreeParams {
     int max_context;               // smaller of the table's and the caller's bound
     int max_query;                 // nodes per sequence at most
     // filled by tree_plan
-    int lanes;                     // CTAs side by side on the same keys, 256 rows of queries each
-    int ctas;                      // of a lane at most
-    bool whole;                    // CTAs are dealt whole (sequence, KV head) pairs
-    float* rec_o;                  // [ctas][lanes][2][2][128][D]
+    int sides, heads;              // a lane's CTAs: sides (256 rows of queries each) x KV heads
+    int ctas;                      // lanes
+    bool whole;                    // lanes are dealt whole sequences
+    float* rec_o;                  // [ctas][sides][heads][2][2][128][D]
     float2* rec_ml;                // the same without D: reference (log2 units) and sum
 #ifdef PA_TEST_HOOKS
     // Test builds only: CTA test_cta's loaders issue no tile from test_tile
