@@ -49,6 +49,8 @@
 // for a tile's S beside these warps, so one for both slots would hold them up.)  A barrier's parity tells a phase from the one before it
 // alone, so whoever waits for a phase has seen that the one before is over: by
 // waiting for every phase in turn, or as the comments at the waits say.
+#include <algorithm>
+
 #include "decode_tile.cuh"
 #include "tc_device.cuh"
 #include "tree_device.cuh"
@@ -142,6 +144,7 @@ struct TrRing {
 // A run of key tiles [k0, k1) of one pair of n tiles.
 struct TrPiece {
     int b, g, k0, k1, n;
+    int query;                     // query tiles of this CTA
     TreeSeq s;
     bool share;                    // each slot has a query tile, and all key tiles
     bool alone;                    // the slots do not join: shared, or few tiles
@@ -155,6 +158,7 @@ struct TrPiece {
         return share ? k1 - k0 : (alone ? (owner == slot ? k1 - k0 : 0) : (k1 - k0 + 1 - slot) / 2);
     }
     __device__ __forceinline__ int query_tiles() const { return share ? 2 : 1; }
+    __device__ __forceinline__ bool rows(int slot) const { return slot < query; }
     // Whether key tile k is the slot's first.
     __device__ __forceinline__ bool first(int slot, int k) const { return share || alone ? k == k0 : k - k0 == slot; }
 };
@@ -200,41 +204,48 @@ struct TrWalk {
         read(p, report);
         return __reduce_add_sync(0xffffffffu, n) + total;
     }
-    // The next piece with work for the CTA of query tiles `side` and KV heads
-    // head, head + p.heads, ...
+    // The pair at `at`, for query tiles `side` and KV heads head, head + p.heads,
+    // ..., its first weight and all of it; its rows and slots of this CTA.
+    __device__ __forceinline__ bool find(const TreeParams& p, int side, int head, TrPiece& P, unsigned& begin,
+                                         unsigned& one) {
+        while (at >= base + total) {
+            base += total;
+            base_b += 32;
+            if (base_b >= p.num_seqs) return false;
+            read(p, false);
+        }
+        const int who = __ffs(__ballot_sync(0xffffffffu, at - base < ends)) - 1;
+        const unsigned before = __shfl_sync(0xffffffffu, ends, max(who - 1, 0));
+        P.s.L = __shfl_sync(0xffffffffu, mine.L, who);
+        P.s.C = __shfl_sync(0xffffffffu, mine.C, who);
+        P.s.q0 = __shfl_sync(0xffffffffu, mine.q0, who);
+        P.n = tiles(P.s);
+        one = each(p, P.s);
+        const unsigned first = base + (who > 0 ? before : 0u), pair = (at - first) / one;
+        begin = first + pair * one;
+        P.b = base_b + who;
+        P.g = head + (int)pair * p.heads;
+        const int per = tr_nodes_per_tile(p.group);              // query tiles 2 side and 2 side + 1
+        P.query = min((P.s.C + per - 1) / per - kTrSlots * side, kTrSlots);
+        P.share = P.query == kTrSlots;
+        return true;
+    }
+    // The next piece with work for that CTA.
     __device__ __forceinline__ bool next(const TreeParams& p, int side, int head, TrPiece& P) {
         while (at < end) {
-            while (at >= base + total) {
-                base += total;
-                base_b += 32;
-                if (base_b >= p.num_seqs) return false;
-                read(p, false);
-            }
-            const int who = __ffs(__ballot_sync(0xffffffffu, at - base < ends)) - 1;
-            const unsigned before = __shfl_sync(0xffffffffu, ends, max(who - 1, 0));
-            P.s.L = __shfl_sync(0xffffffffu, mine.L, who);
-            P.s.C = __shfl_sync(0xffffffffu, mine.C, who);
-            P.s.q0 = __shfl_sync(0xffffffffu, mine.q0, who);
-            P.n = tiles(P.s);
-            const unsigned first = base + (who > 0 ? before : 0u), off = at - first;
-            const unsigned one = each(p, P.s), pair = off / one, in = off - pair * one;
-            P.b = base_b + who;
-            P.g = head + (int)pair * p.heads;
+            unsigned begin, one;
+            if (!find(p, side, head, P, begin, one)) return false;
             if (p.whole) {
                 P.k0 = 0, P.k1 = P.n;
                 ++at;
             } else {
-                const unsigned stop = min(one, in + (end - at));
+                const unsigned in = at - begin, stop = min(one, in + (end - at));
                 P.k0 = max((int)in - kTrPairWeight, 0);
                 P.k1 = (int)stop - kTrPairWeight;
                 at += stop - in;
                 if (P.k1 <= P.k0) continue;
             }
-            // query tiles 2 side and 2 side + 1
-            const int per = tr_nodes_per_tile(p.group);
-            const int query_tiles = (P.s.C + per - 1) / per - kTrSlots * side;
-            if (query_tiles <= 0) continue;
-            P.share = query_tiles >= kTrSlots;
+            if (P.query <= 0) continue;
             P.alone = P.share || P.k1 - P.k0 <= kTrSoloTiles;
             P.owner = turn;
             if (P.alone && !P.share) turn ^= 1;
@@ -379,12 +390,11 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
     const int G = p.group, per_tile = tr_nodes_per_tile(G);
 
     if (threadIdx.x == 0) {
-        constexpr int kFillers = kFp8 ? kTrConverters : 1;
-        for (int i = 0; i < Lay::kKStages; ++i) mbar_init(&room.k_full[i], kFillers), mbar_init(&room.k_empty[i], kTrSlots);
-        for (int i = 0; i < Lay::kVStages; ++i) mbar_init(&room.v_full[i], kFillers), mbar_init(&room.v_empty[i], kTrSlots);
+        for (int i = 0; i < Lay::kKStages; ++i) mbar_init(&room.k_full[i], 1), mbar_init(&room.k_empty[i], kTrSlots);
+        for (int i = 0; i < Lay::kVStages; ++i) mbar_init(&room.v_full[i], 1), mbar_init(&room.v_empty[i], kTrSlots);
         for (int i = 0; i < Lay::kCodeStages; ++i) {
-            mbar_init(&room.kc_full[i], 1), mbar_init(&room.kc_empty[i], kTrConverters);
-            mbar_init(&room.vc_full[i], 1), mbar_init(&room.vc_empty[i], kTrConverters);
+            mbar_init(&room.kc_full[i], 1), mbar_init(&room.kc_empty[i], 1);
+            mbar_init(&room.vc_full[i], 1), mbar_init(&room.vc_empty[i], 1);
         }
         for (int i = 0; i < kTrQStages; ++i) mbar_init(&room.q_full[i], 1), mbar_init(&room.q_empty[i], kTrSlots);
         mbar_init(&room.lines_full, 1), mbar_init(&room.lines_empty, kTrSoftmaxWarps);
@@ -625,56 +635,76 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
         control_registers();
         if constexpr (kFp8) {
             // --------------------------------------------------------------
-            // converters: a K tile's codes, then its V tile's.  A pass brings 16
-            // codes a lane of four rows; lanes are laid out so that eight
-            // neighbours read and write different banks: four chunks of a row
-            // beside the other four of the next.
+            // converters, a warp for the even tiles' K, one for their V, and
+            // two for the odd tiles'.  A pass brings 16 codes a lane of four
+            // rows; lanes are laid out so that eight neighbours read and write
+            // different banks: four chunks of a row beside the other four of
+            // the next.
+            // Each warp sees every other use of some stages.  Where it waits
+            // for the operands' stage first, the products of two (K) or three
+            // (V) tiles back are over, hence every tile before them converted,
+            // and so the use before of the codes' stage is; of V's operand
+            // stages that holds by this warp's wait a tile before.
             // --------------------------------------------------------------
+            static_assert(kTrConverters == 4 && Lay::kKStages == 2 && Lay::kVStages == 3 && Lay::kCodeStages >= 4,
+                          "see above");
             const int who = warp - kTrConvertWarp;
+            const bool keys = (who & 1) == 0;
             const int c = lane & 7, upper = c >> 2;
             const int r4 = 2 * (lane >> 4) + (upper ^ ((lane >> 3) & 1));
-            TrRing<Lay::kKStages> k_at;
-            TrRing<Lay::kVStages> v_at;
+            uint64_t* const codes_full = keys ? room.kc_full : room.vc_full;
+            uint64_t* const codes_empty = keys ? room.kc_empty : room.vc_empty;
+            uint64_t* const full = keys ? room.k_full : room.v_full;
+            uint64_t* const empty = keys ? room.k_empty : room.v_empty;
+            const int stages = keys ? Lay::kKStages : Lay::kVStages;
+            // bits of the row's number that the swizzles use are those of r4,
+            // and of pass & 1 for the next four rows
+            const uint8_t* const src0 = smem + (keys ? Lay::kKCodes : Lay::kVCodes) + r4 * 128;
+            uint8_t* const dst0 = smem + (keys ? Lay::kK : Lay::kV) + upper * Lay::kHalf + r4 * 128;
+            int n = 0, st = 0, lap = 0;
             TrRing<Lay::kCodeStages> at;
             bool ok = true;
             while (ok && walk.next(p, side, head, P)) {
-                for (int k = P.k0; ok && k < P.k1; ++k, k_at.step(), v_at.step(), at.step()) {
-#pragma unroll 1
-                    for (int kind = 0; ok && kind < 2; ++kind) {
-                        const bool keys = kind == 0;
-                        const int st = keys ? k_at.at : v_at.at, lap = keys ? k_at.lap : v_at.lap;
-                        ok = tr_wait(p, keys ? &room.kc_full[at.at] : &room.vc_full[at.at], at.lap);
-                        if (ok && lap > 0) ok = tr_wait(p, keys ? &room.k_empty[st] : &room.v_empty[st], lap - 1);
+                for (int k = P.k0; ok && k < P.k1; ++k, ++n, at.step()) {
+                    if ((n & 1) == (who >> 1)) {
+                        if (lap > 0) ok = tr_wait(p, &empty[st], lap - 1);
+                        if (ok) ok = tr_wait(p, &codes_full[at.at], at.lap);
                         if (!ok) break;
-                        const uint8_t* src = smem + (keys ? Lay::kKCodes : Lay::kVCodes) + at.at * Lay::kCodes;
-                        uint8_t* dst = smem + (keys ? Lay::kK : Lay::kV) + st * Lay::kTile + upper * Lay::kHalf;
-#pragma unroll 2
-                        for (int i = who; i < kTrKeys / 4; i += kTrConverters) {
-                            const int r = 4 * i + r4;
-                            const uint4 x = lds128(src + r * 128 + ((c ^ (r & 7)) << 4));
-                            uint32_t y[8];
+                        const uint8_t* src = src0 + at.at * Lay::kCodes;
+                        uint8_t* dst = dst0 + st * Lay::kTile;
+#pragma unroll 1
+                        for (int i = 0; i < kTrKeys / 16; ++i, src += 16 * 128, dst += 16 * 128) {
+                            uint4 x[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                x[j] = lds128(src + j * 512 + ((c ^ ((r4 + 4 * j) & 7)) << 4));
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const uint32_t codes = word_of(x, j);
-                                if constexpr (kBf16) {
-                                    y[2 * j] = e4m3x2_to<T>((uint16_t)(codes & 0xffffu));
-                                    y[2 * j + 1] = e4m3x2_to<T>((uint16_t)(codes >> 16));
-                                } else {
-                                    e4m3x4_to_f16x2x2(codes, y[2 * j], y[2 * j + 1]);
+                                uint32_t y[8];
+#pragma unroll
+                                for (int w = 0; w < 4; ++w) {
+                                    const uint32_t codes = word_of(x[j], w);
+                                    if constexpr (kBf16) {
+                                        y[2 * w] = e4m3x2_to<T>((uint16_t)(codes & 0xffffu));
+                                        y[2 * w + 1] = e4m3x2_to<T>((uint16_t)(codes >> 16));
+                                    } else {
+                                        e4m3x4_to_f16x2x2(codes, y[2 * w], y[2 * w + 1]);
+                                    }
                                 }
+                                // chunks 2c and 2c + 1 of the row's 16
+                                const int chunk = ((2 * c) & 7) ^ ((r4 + 4 * j) & 7);
+                                *reinterpret_cast<uint4*>(dst + j * 512 + (chunk << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                                *reinterpret_cast<uint4*>(dst + j * 512 + ((chunk ^ 1) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
                             }
-                            // chunks 2c and 2c + 1 of the row's 16
-                            const int chunk = ((2 * c) & 7) ^ (r & 7);
-                            *reinterpret_cast<uint4*>(dst + r * 128 + (chunk << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                            *reinterpret_cast<uint4*>(dst + r * 128 + ((chunk ^ 1) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive(keys ? &room.k_full[st] : &room.v_full[st]);
-                            mbar_arrive(keys ? &room.kc_empty[at.at] : &room.vc_empty[at.at]);
+                            mbar_arrive(&full[st]);
+                            mbar_arrive(&codes_empty[at.at]);
                         }
                     }
+                    if (++st == stages) st = 0, ++lap;
                 }
             }
             if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
@@ -945,52 +975,58 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
     }
 }
 
-// Joins the records of the pairs that more than one CTA met: a warp per row,
-// D / 32 dims a lane.
+// Joins the records of the pairs that more than one lane met: a CTA for some
+// rows of the pair that the range of lane blockIdx.x + 1 begins in, where that
+// is the first range to begin there; a warp per row, D / 32 dims a lane.  Which
+// pair that is it finds while the attention kernel ends: lengths and trees are
+// not written by it, and it has waited for whoever wrote them.
 constexpr int kTrMergeThreads = 256;
-constexpr int kTrMergeRows = 32;               // of a CTA
+constexpr int kTrMergeRows = 16;               // of a CTA
 
 template <typename T, int D, bool kFp8>
 __global__ void __launch_bounds__(kTrMergeThreads)
     tree_merge_kernel(const __grid_constant__ TreeParams p) {
     constexpr int kDims = D / 32;
-    grid_dependency_wait();
     allow_dependent_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.x / p.num_kv_heads, g = blockIdx.x % p.num_kv_heads;
-    const int tile = blockIdx.y / (kTrRows / kTrMergeRows), r0 = blockIdx.y % (kTrRows / kTrMergeRows) * kTrMergeRows;
-    const TreeSeq s = tree_sequence(p, b, false);
-    const int G = p.group, per_tile = tr_nodes_per_tile(G);
-    if (tile * per_tile >= s.C || r0 >= min(per_tile, s.C - tile * per_tile) * G) return;
-    // tiles in all, and before this sequence
-    unsigned all = 0, before = 0;
-    for (int i = lane; i < p.num_seqs; i += 32) {
-        const unsigned w = TrWalk::weight(p, tree_sequence(p, i, false));
-        all += w;
-        if (i < b) before += w;
+    const int head = blockIdx.y % p.heads, side = blockIdx.y / p.heads;
+    const int slot = blockIdx.z / (kTrRows / kTrMergeRows), r0 = blockIdx.z % (kTrRows / kTrMergeRows) * kTrMergeRows;
+    TrWalk walk;
+    const TrDeal deal(p, walk.count(p, false));
+    const unsigned mine = blockIdx.x + 1;
+    TrPiece P;
+    bool join = mine < deal.ctas;
+    unsigned c1 = mine;
+    if (join) {
+        // the pair at the range's begin (one CTA's rows of it: all its tiles)
+        walk.at = deal.begin(mine);
+        walk.end = deal.N;
+        unsigned begin = 0, each = 1;
+        join = walk.find(p, side, head, P, begin, each);
+        // lanes before the first tile's, and after the last's, have nothing of it
+        join = join && deal.cta_of(begin + kTrPairWeight) == mine - 1;
+        c1 = deal.cta_of(begin + each - 1);
+        join = join && c1 >= mine && P.rows(slot);
     }
-    const TrDeal deal(p, __reduce_add_sync(0xffffffffu, all));
-    const unsigned each = TrWalk::each(p, s), begin = __reduce_add_sync(0xffffffffu, before) + g / p.heads * each;
-    const unsigned c0 = deal.cta_of(begin + kTrPairWeight), c1 = deal.cta_of(begin + each - 1);
-    if (c0 == c1) return;                      // written by that CTA
-    const int side = tile / kTrSlots;
-    // query tiles 2 side and 2 side + 1 are the slots', a last one alone is the first's
-    const int slot = tile % kTrSlots;
+    grid_dependency_wait();
+    if (!join) return;
+    const int G = p.group, per_tile = tr_nodes_per_tile(G);
     for (int r = r0 + warp; r < r0 + kTrMergeRows; r += kTrMergeThreads / 32) {
-        const int in_tile = r / G, node = tile * per_tile + in_tile;
-        if (in_tile >= per_tile || node >= s.C) break;
+        const int in_tile = r / G, node = (kTrSlots * side + slot) * per_tile + in_tile;
+        if (in_tile >= per_tile || node >= P.s.C) break;
         float m = -INFINITY, l = 0.f, o[kDims] = {};
         constexpr int kAhead = 4;
-        for (unsigned c = c0; c <= c1; c += kAhead) {
+        for (unsigned c = mine - 1; c <= c1; c += kAhead) {
             float2 ml[kAhead];
             float v[kAhead][kDims];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 ml[i] = make_float2(-INFINITY, 0.f);
                 if (c + i > c1) continue;
-                const int64_t rec = ((((int64_t)(c + i) * p.sides + side) * p.heads + g % p.heads) * 2 + (c + i == c0 ? 1 : 0)) * kTrSlots + slot;
-                ml[i] = p.rec_ml[rec * kTrRows + r];
-                const float* src = p.rec_o + (rec * kTrRows + r) * D + kDims * lane;
+                const int64_t cta = ((int64_t)(c + i) * p.sides + side) * p.heads + head;
+                const int64_t rec = ((cta * 2 + (c + i == mine - 1 ? 1 : 0)) * kTrSlots + slot) * kTrRows + r;
+                ml[i] = p.rec_ml[rec];
+                const float* src = p.rec_o + rec * D + kDims * lane;
                 if constexpr (kDims == 4) {
                     const float4 x = *reinterpret_cast<const float4*>(src);
                     v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
@@ -1017,7 +1053,7 @@ __global__ void __launch_bounds__(kTrMergeThreads)
             }
         }
         const float norm = (kFp8 ? p.v_scale : 1.f) / l;
-        T* dst = static_cast<T*>(p.out) + ((int64_t)(s.q0 + node) * p.num_q_heads + g * G + (r - in_tile * G)) * D + kDims * lane;
+        T* dst = static_cast<T*>(p.out) + ((int64_t)(P.s.q0 + node) * p.num_q_heads + P.g * G + (r - in_tile * G)) * D + kDims * lane;
         using M = Mma<T>;
         if constexpr (kDims == 4)
             *reinterpret_cast<uint2*>(dst) = make_uint2(M::pack(o[0] * norm, o[1] * norm), M::pack(o[2] * norm, o[3] * norm));
@@ -1056,9 +1092,12 @@ cudaError_t launch_tree_t(const CUtensorMap& tmk, const CUtensorMap& tmv, const 
     e = launch_with_pdl(tree_attention_kernel<T, D, kFp8>, dim3((unsigned)(p.ctas * p.sides * p.heads)), dim3(tr_threads(kFp8)), kSmem,
                         stream, tmk, tmv, tmq, p);
     if (e != cudaSuccess || p.whole) return e;
-    const int per_tile = kTrRows / p.group, query_tiles = (p.max_query + per_tile - 1) / per_tile;
+    if (p.ctas == 1) return e;
+    const int rows = std::min(kTrRows / p.group, p.max_query) * p.group;          // of a query tile at most
+    const int slots = p.max_query * p.group > kTrRows / p.group * p.group ? kTrSlots : 1;
+    const int chunks = slots == 1 ? (rows + kTrMergeRows - 1) / kTrMergeRows : kTrSlots * (kTrRows / kTrMergeRows);
     return launch_with_pdl(tree_merge_kernel<T, D, kFp8>,
-                           dim3((unsigned)(p.num_seqs * p.num_kv_heads), (unsigned)(query_tiles * (kTrRows / kTrMergeRows))),
+                           dim3((unsigned)(p.ctas - 1), (unsigned)(p.heads * p.sides), (unsigned)chunks),
                            dim3(kTrMergeThreads), 0, stream, p);
 }
 
