@@ -624,8 +624,9 @@ int pa_norm_rope_and_cache_fp8(const void* q, int64_t q_stride, const void* k, i
  * scale must be finite and > 0.  max_query_len >= every C_b, at most
  * PA_TREE_NODES (else PA_ERR_UNSUPPORTED); max_context_len >= every L_b;
  * values outside these bounds are clamped and set PA_DEVERR_BAD_CONTEXT.
- * Softmax statistics, p and the sums are in fp32, and out is
- * rounded once.  A token that a node does not see has no part in its row, also
+ * Softmax statistics and sums are in fp32; p meets V in two parts of the
+ * 16-bit type, which hold it to 2^-15 (bf16) or 2^-22 (fp16; and to 2^-31 of
+ * the row's largest), and out is rounded once.  A token that a node does not see has no part in its row, also
  * where its K or V is not finite.
  * workspace: device memory of at least pa_tree_attention_workspace_size bytes,
  * 16-byte aligned, no initial contents; calls that overlap on the GPU must

@@ -20,7 +20,7 @@
 //   P = 2^(S - m)       m a reference of the row's maximum, raised only when
 //                       that grows by more than 2^8 (O is rescaled then); P
 //                       goes back over S as two parts of the 16-bit type that
-//                       together hold it to 2^-17 (bf16) or 2^-21 (fp16, whose
+//                       together hold it to 2^-15 (bf16) or 2^-22 (fp16, whose
 //                       reference stays 2^7 below the maximum so that small P
 //                       are not lost below its range)
 //   O += P V            128 x D x 64 for each part, P from tensor memory
@@ -75,7 +75,7 @@ static_assert(256 * tr_softmax_regs(false) + 256 * kTrControlRegs <= 512 * 128 &
 constexpr int kTrCtas = 152;                   // one per SM
 constexpr int kTrMinTiles = 8;                 // weight of a CTA's range at least, where there are records
 constexpr int kTrWholeTiles = 8;               // longest contexts, in tiles, whose pairs stay whole
-constexpr int kTrPairWeight = 2;               // of a pair beside its key tiles, in the dealing
+constexpr int kTrPairWeight = 4;               // of a pair beside its key tiles, in the dealing
 constexpr int kTrSoloTiles = 2;                // of a piece that one slot takes alone
 
 // Shared memory: query tiles, operand tiles, codes.
@@ -169,6 +169,7 @@ __device__ __forceinline__ int tr_nodes_per_tile(int group) { return kTrRows / g
 // Walks a range of the batch's key tiles (or, with p.whole, of its pairs),
 // pair by pair; all lanes of a warp together, which hold 32 sequences at a
 // time.  A pair weighs its tiles and kTrPairWeight, which come first.
+template <bool kL2 = false>
 struct TrWalk {
     unsigned at = 0, end = 0, base = 0, total = 0, ends = 0;
     int base_b = 0, turn = 0;
@@ -187,7 +188,7 @@ struct TrWalk {
         const int lane = threadIdx.x & 31, b = base_b + lane;
         ends = 0;
         if (b < p.num_seqs) {
-            mine = tree_sequence(p, b, report);
+            mine = tree_sequence<kL2>(p, b, report);
             ends = weight(p, mine);
         }
 #pragma unroll
@@ -199,9 +200,13 @@ struct TrWalk {
     }
     // All there is (31 bits: checked on the host), left at the first sequences.
     __device__ __forceinline__ unsigned count(const TreeParams& p, bool report) {
-        unsigned n = 0;
-        for (int b = 32 + (int)(threadIdx.x & 31); b < p.num_seqs; b += 32) n += weight(p, tree_sequence(p, b, report));
+        const int b1 = 32 + (int)(threadIdx.x & 31);
+        TreeSeq next;
+        next.C = 0;
+        if (b1 < p.num_seqs) next = tree_sequence<kL2>(p, b1, report);       // under way beside the first
         read(p, report);
+        unsigned n = weight(p, next);
+        for (int b = b1 + 32; b < p.num_seqs; b += 32) n += weight(p, tree_sequence<kL2>(p, b, report));
         return __reduce_add_sync(0xffffffffu, n) + total;
     }
     // The pair at `at`, for query tiles `side` and KV heads head, head + p.heads,
@@ -270,13 +275,22 @@ struct TrDeal {
     }
 };
 
-// Two probabilities as hi + lo parts of the 16-bit type.
-template <typename M>
+// Two probabilities as hi + lo parts of the 16-bit type.  A bf16 hi is p cut to
+// its upper half, so that lo does not wait for a conversion; for fp16 the
+// rounded one is the quicker.
+template <typename T>
 __device__ __forceinline__ void split_pair(float p0, float p1, uint32_t& hi, uint32_t& lo) {
-    hi = M::pack(p0, p1);
-    const float2 u = M::unpack(hi);
+    using M = Mma<T>;
+    float2 h;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        hi = prmt(__float_as_uint(p0), __float_as_uint(p1), 0x7632u);
+        h.x = __uint_as_float(__float_as_uint(p0) & 0xffff0000u), h.y = __uint_as_float(__float_as_uint(p1) & 0xffff0000u);
+    } else {
+        hi = M::pack(p0, p1);
+        h = M::unpack(hi);
+    }
     float d0, d1;
-    f32x2_unpack(f32x2_fma(f32x2_pack(u.x, u.y), f32x2_pack(-1.f, -1.f), f32x2_pack(p0, p1)), d0, d1);
+    f32x2_unpack(f32x2_fma(f32x2_pack(h.x, h.y), f32x2_pack(-1.f, -1.f), f32x2_pack(p0, p1)), d0, d1);
     lo = M::pack(d0, d1);
 }
 
@@ -408,7 +422,7 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
     if (warp == 1) tmem_alloc(&room.tmem, 512);
     grid_dependency_wait();
     allow_dependent_launch();
-    TrWalk walk;
+    TrWalk<> walk;
     const TrDeal deal(p, walk.count(p, blockIdx.x == 0 && warp == 0));
     tc_fence_before_sync();
     __syncthreads();
@@ -756,46 +770,6 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                 const uint32_t tS = tmem + kTrS + kTrKeys * (2 * slot + (t & 1)) + lanes_at;
                 wait(&room.s_full[slot][t & 1], t >> 1);
                 tc_fence_after_sync();
-                if (masked) {
-                    // V rows past the context may hold anything: clear them.
-                    // Of the tree's, elements that are not finite are cleared
-                    // too, since the tensor cores would carry them into rows
-                    // that do not see them; rows that do get them back below.
-                    // Thread r has half r / 64 of key r % 64.  The phase before
-                    // of V's barrier is over once this slot's P V before is done:
-                    // that was at most three tiles back (kTrSoloTiles), and the
-                    // rings have three stages at least.
-                    bool odd = false;
-                    if (!P.share || slot == 0) {
-                        static_assert(Lay::kVStages > kTrSoloTiles, "a phase could be taken for another");
-                        const int tile = n + (k - P.k0), vs = tile % Lay::kVStages;
-                        if (t > 0) wait(&room.o_done[slot][(t - 1) & 1], (t - 1) >> 1);
-                        wait(&room.v_full[vs], tile / Lay::kVStages);
-                        const int key = key0 + (r & 63);
-                        uint8_t* vd = smem + Lay::kV + vs * Lay::kTile + (D == 128 ? (r >> 6) * Lay::kHalf : 0) + (r & 63) * 128;
-                        if (D == 64 && r >= 64) {
-                        } else if (key >= P.s.L) {
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vd + (((c ^ r) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                        } else if (key >= base) {
-                            uint32_t any = 0u;
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                const uint4 w = lds128(vd + (((c ^ r) & 7) << 4));
-                                any |= not_finite<T>(w.x) | not_finite<T>(w.y) | not_finite<T>(w.z) | not_finite<T>(w.w);
-                            }
-                            if (any != 0u) {
-                                odd = true;
-                                for (int c = 0; c < 32; ++c) {
-                                    uint32_t* w = reinterpret_cast<uint32_t*>(vd) + c;
-                                    *w &= ~(((not_finite<T>(*w) >> 15) & 0x00010001u) * 0xffffu);
-                                }
-                            }
-                        }
-                        fence_proxy_async_smem();
-                    }
-                    bad |= P.share ? bar_or(both, 2 * kTrRows, odd) : bar_or(barrier, kTrRows, odd);
-                }
                 if (live) {
                     uint32_t x[kTrKeys];
 #pragma unroll
@@ -854,7 +828,7 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                                                               __uint_as_float(x[16 * c + 2 * i + 1])), sl2, neg2), a0, a1);
                             const float p0 = ex2(a0), p1 = ex2(a1);
                             ps[i & 3] = f32x2_add(ps[i & 3], f32x2_pack(p0, p1));
-                            split_pair<M>(p0, p1, parts[i], parts[8 + i]);
+                            split_pair<T>(p0, p1, parts[i], parts[8 + i]);
                         }
                         tmem_st16(tS + 16 * c, parts);
                     }
@@ -863,6 +837,46 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                     for (int e = 0; e < 4; ++e) f32x2_unpack(ps[e], q8[2 * e], q8[2 * e + 1]);
                     l += ((q8[0] + q8[1]) + (q8[2] + q8[3])) + ((q8[4] + q8[5]) + (q8[6] + q8[7]));
                     tmem_wait_st();
+                }
+                if (masked) {
+                    // V rows past the context may hold anything: clear them.
+                    // Of the tree's, elements that are not finite are cleared
+                    // too, since the tensor cores would carry them into rows
+                    // that do not see them; rows that do get them back below.
+                    // Thread r has half r / 64 of key r % 64.  The phase before
+                    // of V's barrier is over once this slot's P V before is done:
+                    // that was at most three tiles back (kTrSoloTiles), and the
+                    // rings have three stages at least.
+                    bool odd = false;
+                    if (!P.share || slot == 0) {
+                        static_assert(Lay::kVStages > kTrSoloTiles, "a phase could be taken for another");
+                        const int tile = n + (k - P.k0), vs = tile % Lay::kVStages;
+                        if (t > 0) wait(&room.o_done[slot][(t - 1) & 1], (t - 1) >> 1);
+                        wait(&room.v_full[vs], tile / Lay::kVStages);
+                        const int key = key0 + (r & 63);
+                        uint8_t* vd = smem + Lay::kV + vs * Lay::kTile + (D == 128 ? (r >> 6) * Lay::kHalf : 0) + (r & 63) * 128;
+                        if (D == 64 && r >= 64) {
+                        } else if (key >= P.s.L) {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vd + (((c ^ r) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                        } else if (key >= base) {
+                            uint32_t any = 0u;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const uint4 w = lds128(vd + (((c ^ r) & 7) << 4));
+                                any |= not_finite<T>(w.x) | not_finite<T>(w.y) | not_finite<T>(w.z) | not_finite<T>(w.w);
+                            }
+                            if (any != 0u) {
+                                odd = true;
+                                for (int c = 0; c < 32; ++c) {
+                                    uint32_t* w = reinterpret_cast<uint32_t*>(vd) + c;
+                                    *w &= ~(((not_finite<T>(*w) >> 15) & 0x00010001u) * 0xffffu);
+                                }
+                            }
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    bad |= P.share ? bar_or(both, 2 * kTrRows, odd) : bar_or(barrier, kTrRows, odd);
                 }
                 tc_fence_before_sync();
                 __syncwarp();
@@ -991,7 +1005,7 @@ __global__ void __launch_bounds__(kTrMergeThreads)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.y % p.heads, side = blockIdx.y / p.heads;
     const int slot = blockIdx.z / (kTrRows / kTrMergeRows), r0 = blockIdx.z % (kTrRows / kTrMergeRows) * kTrMergeRows;
-    TrWalk walk;
+    TrWalk<true> walk;
     const TrDeal deal(p, walk.count(p, false));
     const unsigned mine = blockIdx.x + 1;
     TrPiece P;

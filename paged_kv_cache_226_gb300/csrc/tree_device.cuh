@@ -23,12 +23,16 @@ __device__ __forceinline__ void tree_rows(int start, int end, int64_t num_tokens
     s.q0 = start, s.C = (int)c;
 }
 
+// kL2: read past L1, by a kernel that runs ahead of the one before it.
+template <bool kL2 = false>
 __device__ __forceinline__ TreeSeq tree_sequence(const TreeParams& p, int b, bool report) {
+    auto at = [](const int32_t* x) { return kL2 ? __ldcg(x) : *x; };
     TreeSeq s;
     bool bad = false;
-    s.L = p.context_lens[b];
+    s.L = at(p.context_lens + b);
+    const int start = at(p.query_start + b), end = at(p.query_start + b + 1);
     if (s.L < 0 || s.L > p.max_context) bad = true, s.L = s.L < 0 ? 0 : p.max_context;
-    tree_rows(p.query_start[b], p.query_start[b + 1], p.num_tokens, min(p.max_query, s.L), s, bad);
+    tree_rows(start, end, p.num_tokens, min(p.max_query, s.L), s, bad);
     if (bad && report) flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
     return s;
 }

@@ -41,13 +41,16 @@ def tree_reference(x: Batch, q, nodes, parents):
     A score carries an error of at most 2^-20 (2 + A) in log2 units, A = log2(e)
     scale max_i sum_d |q_d K_id| (fp32 accumulation of D products, the scale and
     the exponential), so a weight is off by that share, and out by that share of
-    sum p |v|, by p's two parts (2^-17 of it, and 2^-31 of the largest weight,
-    which is at most 1, for each of n tokens), by the sums (2^-23 of a partial
+    sum p |v|, by p's two parts (the first leaves up to 2^-7 of it (bf16, cut off)
+    or 2^-11 (fp16, rounded), the second is off by 2^-8 or 2^-11 of that: 2^-15
+    or 2^-22; and 2^-31 of the largest weight, which is at most 1, for each of n
+    tokens), by the sums (2^-23 of a partial
     sum for each step of 8 tokens or more, and for the joins), and by its own
     rounding."""
     out = torch.zeros(len(q), x.hq, x.d, dtype=torch.float64)
     bound = torch.zeros_like(out)
     g, at = x.hq // x.hkv, 0
+    parts = 2.0 ** -15 if x.dtype == torch.bfloat16 else 2.0 ** -22
     for b, c in enumerate(nodes):
         n = int(x.lens[b])
         if c == 0:
@@ -67,7 +70,7 @@ def tree_reference(x: Batch, q, nodes, parents):
             vt = torch.nn.functional.pad(vv, (0, 0, 0, 128 * tiles - m)).view(tiles, 128, -1)
             partial = (pt @ vt).cumsum(0).abs().amax(0) + (pt @ vt.abs()).amax(0)
             bound[at:at + c, h] = half_step(x.dtype) * out[at:at + c, h].abs() + 2.0 ** -24 + \
-                (2.0 ** -20 * (2 + a) + 2.0 ** -17) * (p @ vv.abs()) + \
+                (2.0 ** -20 * (2 + a) + parts) * (p @ vv.abs()) + \
                 2.0 ** -31 * m * vv.abs().amax() + 2.0 ** -23 * (m / 8 + 16) * partial
         at += c
     return out, bound
