@@ -763,17 +763,23 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
             }
             float m = -INFINITY, l = 0.f;
             bool bad = false;                 // V of the tree has elements that are not finite
+            bool ahead = false;               // the tile's scores have been requested
+            uint32_t x[kTrKeys];
             for (int k = P.k0, j = 0; own > 0 && k < P.k1; ++k) {
                 if (!P.has(slot, k)) continue;
                 const int key0 = k * kTrKeys;
                 const bool masked = key0 + kTrKeys > base;
                 const uint32_t tS = tmem + kTrS + kTrKeys * (2 * slot + (t & 1)) + lanes_at;
-                wait(&room.s_full[slot][t & 1], t >> 1);
-                tc_fence_after_sync();
-                if (live) {
-                    uint32_t x[kTrKeys];
+                auto request = [&](uint32_t at) {
 #pragma unroll
-                    for (int c = 0; c < kTrKeys; c += 32) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(x + c));
+                    for (int c = 0; c < kTrKeys; c += 32) tmem_ld32(at + c, *reinterpret_cast<uint32_t(*)[32]>(x + c));
+                };
+                if (!ahead) {
+                    wait(&room.s_full[slot][t & 1], t >> 1);
+                    tc_fence_after_sync();
+                    if (live) request(tS);
+                }
+                if (live) {
 #pragma unroll
                     for (int c = 0; c < kTrKeys; c += 32) tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(x + c));
                     if (masked) {
@@ -836,6 +842,13 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) f32x2_unpack(ps[e], q8[2 * e], q8[2 * e + 1]);
                     l += ((q8[0] + q8[1]) + (q8[2] + q8[3])) + ((q8[4] + q8[5]) + (q8[6] + q8[7]));
+                    // the next tile's scores, where they are there already
+                    ahead = j + 1 < own &&
+                            __all_sync(0xffffffffu, mbar_test_wait(&room.s_full[slot][(t + 1) & 1], ((t + 1) >> 1) & 1));
+                    if (ahead) {
+                        tc_fence_after_sync();
+                        request(tmem + kTrS + kTrKeys * (2 * slot + ((t + 1) & 1)) + lanes_at);
+                    }
                     tmem_wait_st();
                 }
                 if (masked) {
