@@ -23,8 +23,8 @@ extern "C" {
  * tiles run out, set PA_DEVERR_WAIT_TIMEOUT in the device error word and
  * end.  The results of that launch are not defined; the fused step's
  * counters must be zeroed again before the next step.
- * The kernels of pa_prefill_weights do the same: in each, CTA `cta` (x of its
- * grid) loads no streamed tile from its tile `tile` on.  Returns PA_OK, or
+ * The kernels of pa_prefill_weights and of pa_tree_attention do the same: in
+ * each, CTA `cta` (x of its grid) loads no streamed tile from its tile `tile` on.  Returns PA_OK, or
  * PA_ERR_INVALID_ARG for a zero limit.
  */
 int pa_test_set_wait_fault(int32_t cta, int32_t tile, unsigned long long wait_limit_ns);

@@ -745,6 +745,15 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// A contiguous CUDA tensor from element `at` of a storage on.
+Tensor part_of(const c10::Storage& room, at::ScalarType dtype, int64_t at, at::IntArrayRef sizes) {
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(room), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                        c10::scalarTypeToTypeMeta(dtype));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+    t.unsafeGetTensorImpl()->set_storage_offset(at);
+    return t;
+}
+
 // (draft_tokens, target_tokens, parents, query_start, max_query_len)
 // -> (path, path_lens, next_tokens)
 PyObject* accept_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -769,11 +778,15 @@ PyObject* accept_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     {
         Unlocked u;
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
-        const auto on = at::TensorOptions().device(at::kCUDA, (c10::DeviceIndex)index);
         if (largest >= 1 && largest <= PA_TREE_NODES) {
-            path = at::empty({seqs, largest}, on.dtype(at::kInt));
-            lens = at::empty({seqs}, on.dtype(at::kInt));
-            next = at::empty({seqs}, on.dtype(at::kLong));
+            // one allocation for the three (each by itself: 1.5 us a call more apiece)
+            const size_t bytes = 8 * (size_t)seqs + 4 * (size_t)seqs * (largest + 1);
+            c10::Allocator* const a = c10::cuda::CUDACachingAllocator::get();
+            const c10::Storage room(c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes,
+                                                                         a->allocate(bytes), a, false));
+            next = part_of(room, at::kLong, 0, {seqs});
+            path = part_of(room, at::kInt, 2 * seqs, {seqs, largest});
+            lens = part_of(room, at::kInt, 2 * seqs + seqs * largest, {seqs});
         }
         void* stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream();
         status = lib.accept_tree((const int64_t*)draft.data_ptr(), target, parents, (const int32_t*)start.data_ptr(),

@@ -25,7 +25,8 @@ namespace pa {
 
 constexpr int kRopeThreads = 128;
 constexpr int kRopeCtas = 9;                  // per SM
-constexpr int kNormCtas = 8;                  // the same behind a norm
+// The same behind a norm, whose sums and weights take registers.
+__host__ __device__ constexpr int norm_ctas(bool fp8) { return fp8 ? 9 : 8; }
 
 // Position-independent part of the angle: turns per position, in 2^-64.
 __device__ __forceinline__ int64_t rope_turns(float inv_freq) {
@@ -79,12 +80,14 @@ struct RopePlaces {
 };
 
 template <typename T, int D, bool kFp8, bool kInterleaved, bool kNorm, int kTokens>
-__global__ void __launch_bounds__(kRopeThreads, kNorm ? kNormCtas : kRopeCtas)
+__global__ void __launch_bounds__(kRopeThreads, kNorm ? norm_ctas(kFp8) : kRopeCtas)
     rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
     constexpr int kUnits = D / 16, kHeads = kRopeThreads / kUnits;      // items side by side
-    __shared__ __align__(16) float2 cs[kTokens][D / 2];
+    // cos and sin of pairs 8 u + 2 j and the next, and weights 8 c + 4 j .. + 3,
+    // at [j][u] and [j][c]: a head's threads read neighbouring words
+    __shared__ __align__(16) float4 cs[kTokens][4][kUnits];
     __shared__ int64_t slot_s[kTokens];
-    __shared__ __align__(16) float weight_s[kNorm ? 2 : 1][kNorm ? D : 1];      // of q, of k
+    __shared__ __align__(16) float4 weight_s[kNorm ? 2 : 1][2][kNorm ? D / 8 : 1];      // of q, of k
     grid_dependency_wait();
     allow_dependent_launch();
     const int tid = threadIdx.x, u = tid % kUnits, first = tid / kUnits;
@@ -141,10 +144,9 @@ __global__ void __launch_bounds__(kRopeThreads, kNorm ? kNormCtas : kRopeCtas)
 #pragma unroll
                 for (int d = kUnits / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(head, sum, d);
                 const float inv = rsqrtf(fmaf(sum, 1.f / D, p.eps));
-                const float4* w = reinterpret_cast<const float4*>(weight_s[kRows]);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float4 a = w[2 * c0 + j], b = w[2 * c1 + j];
+                    const float4 a = weight_s[kRows][j][c0], b = weight_s[kRows][j][c1];
                     x0[4 * j] *= inv * a.x, x0[4 * j + 1] *= inv * a.y;
                     x0[4 * j + 2] *= inv * a.z, x0[4 * j + 3] *= inv * a.w;
                     x1[4 * j] *= inv * b.x, x1[4 * j + 1] *= inv * b.y;
@@ -152,10 +154,9 @@ __global__ void __launch_bounds__(kRopeThreads, kNorm ? kNormCtas : kRopeCtas)
                 }
             }
             if (kRows != kRopeV && rot) {
-                const float4* a = reinterpret_cast<const float4*>(&cs[tk][8 * u]);     // two pairs each
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float4 w = a[j];
+                    const float4 w = cs[tk][j][u];                                     // two pairs
                     if (kInterleaved) {
                         float(&x)[8] = j < 2 ? x0 : x1;
                         const int o = 4 * (j & 1);
@@ -212,13 +213,16 @@ __global__ void __launch_bounds__(kRopeThreads, kNorm ? kNormCtas : kRopeCtas)
             else
                 flag_error(p.err, PA_DEVERR_BAD_INDEX);
         }
-        cs[tk][j] = rope_cos_sin(rope_turns(p.inv_freq[j]), p.positions[row], p.factor);
+        reinterpret_cast<float2*>(&cs[tk][j % 8 / 2][j / 8])[j & 1] =
+            rope_cos_sin(rope_turns(p.inv_freq[j]), p.positions[row], p.factor);
     }
     if constexpr (kNorm) {
         static_assert(kRopeThreads >= D, "a thread per weight");
         if (tid < D) {
-            weight_s[kRopeQ][tid] = p.q_weight ? (float)static_cast<const T*>(p.q_weight)[tid] : 1.f;
-            weight_s[kRopeK][tid] = p.k_weight ? (float)static_cast<const T*>(p.k_weight)[tid] : 1.f;
+            const float wq = p.q_weight ? (float)static_cast<const T*>(p.q_weight)[tid] : 1.f;
+            const float wk = p.k_weight ? (float)static_cast<const T*>(p.k_weight)[tid] : 1.f;
+            reinterpret_cast<float*>(&weight_s[kRopeQ][tid % 8 / 4][tid / 8])[tid & 3] = wq;
+            reinterpret_cast<float*>(&weight_s[kRopeK][tid % 8 / 4][tid / 8])[tid & 3] = wk;
         }
     }
     if (tid < tokens) {
@@ -241,11 +245,13 @@ __global__ void __launch_bounds__(kRopeThreads, kNorm ? kNormCtas : kRopeCtas)
 }
 
 // Many small CTAs keep the grid's last wave short: 8192 tokens of 64 + 16
-// heads (336 MB) take 52.8 us with 128 threads, two tokens and nine CTAs an SM
-// (6.4 TB/s, 94 % of the copy rate), 54.3 with ten, 56.0 with eight, 58.9 with
-// 256 threads, four tokens and four CTAs; into an E4M3 cache, 5001 tokens of
-// 32 + 16 heads 21.2, with ten 22.9, with eight 22.2.  A single wave of tokens
-// goes one to a CTA, which spreads it wider.
+// heads (336 MB) take 52.2 us with 128 threads, two tokens and nine CTAs an SM
+// (6.4 TB/s, 95 % of the copy rate; 58.9 with 256 threads, four tokens and four
+// CTAs); into an E4M3 cache, 5001 tokens of 32 + 16 heads 20.7 (with eight
+// CTAs 21.8).  Behind a norm the same take 54.8 us (ten CTAs 59.8, four tokens
+// 68) and 25.9 (eight 26.7, ten 30.9); with cos, sin and weights in the order
+// of the pairs, a head's threads on the same banks, they took 65.5 and 30.4.
+// A single wave of tokens goes one to a CTA, which spreads it wider.
 template <typename T, int D, bool kFp8, bool kInterleaved, bool kNorm>
 cudaError_t launch_rope_i(const RopeParams& p, cudaStream_t stream) {
     const dim3 threads(kRopeThreads);
