@@ -68,8 +68,8 @@ constexpr int kTrConverters = 4;               // E4M3 only
 __host__ __device__ constexpr int tr_threads(bool fp8) { return (kTrConvertWarp + (fp8 ? kTrConverters : 0)) * 32; }
 // Registers: 512 threads are launched with 128 each (640 with 96); the softmax
 // warps take over what the others give up.
-constexpr int kTrControlRegs = 56;
-__host__ __device__ constexpr int tr_softmax_regs(bool fp8) { return fp8 ? 152 : 200; }
+constexpr int kTrControlRegs = 72;
+__host__ __device__ constexpr int tr_softmax_regs(bool fp8) { return fp8 ? 128 : 184; }
 static_assert(256 * tr_softmax_regs(false) + 256 * kTrControlRegs <= 512 * 128 &&
               256 * tr_softmax_regs(true) + 384 * kTrControlRegs <= 640 * 96, "registers of the CTA");
 constexpr int kTrCtas = 152;                   // one per SM
@@ -81,8 +81,8 @@ constexpr int kTrSoloTiles = 2;                // of a piece that one slot takes
 // Shared memory: query tiles, operand tiles, codes.
 template <int D, bool kFp8>
 struct TrLayout {
-    static constexpr int kKStages = kFp8 ? 2 : 5, kVStages = kFp8 ? 3 : 5;
-    static constexpr int kCodeStages = kFp8 ? 5 : 0;          // of K and of V each
+    static constexpr int kKStages = kFp8 ? 3 : 5, kVStages = kFp8 ? 3 : 5;
+    static constexpr int kCodeStages = kFp8 ? 4 : 0;          // of K and of V each
     static constexpr int kHalves = D / kBoxElems;
     static constexpr int kHalf = kTrKeys * 128;               // 64 dims of 64 rows
     static constexpr int kTile = kHalves * kHalf;
@@ -106,7 +106,7 @@ struct TrRoom {
         float2 ml[kTrSlots][kTrRows];          // the slots' statistics, at a joined piece's end
     };
     uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
-    uint64_t kc_full[5], kc_empty[5], vc_full[5], vc_empty[5];
+    uint64_t kc_full[4], kc_empty[4], vc_full[4], vc_empty[4];
     uint64_t q_full[kTrQStages], q_empty[kTrQStages], lines_full, lines_empty;
     uint64_t s_full[kTrSlots][2], p_full[kTrSlots][2], o_done[kTrSlots][2], done[2 * kTrSlots];
     uint32_t tmem;
@@ -654,13 +654,14 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
             // rows; lanes are laid out so that eight neighbours read and write
             // different banks: four chunks of a row beside the other four of
             // the next.
-            // Each warp sees every other use of some stages.  Where it waits
-            // for the operands' stage first, the products of two (K) or three
-            // (V) tiles back are over, hence every tile before them converted,
-            // and so the use before of the codes' stage is; of V's operand
-            // stages that holds by this warp's wait a tile before.
+            // Each warp sees every other use of a stage.  The use before of the
+            // operands' stage, three tiles back, is given back at this wait;
+            // that the one before that was is known from this warp's wait a
+            // tile of its own back, for the products five tiles back.  They
+            // also say that every tile up to three back is converted, and so
+            // that the use before of the codes' stage, four tiles back, is over.
             // --------------------------------------------------------------
-            static_assert(kTrConverters == 4 && Lay::kKStages == 2 && Lay::kVStages == 3 && Lay::kCodeStages >= 4,
+            static_assert(kTrConverters == 4 && Lay::kKStages == 3 && Lay::kVStages == 3 && Lay::kCodeStages >= 4,
                           "see above");
             const int who = warp - kTrConvertWarp;
             const bool keys = (who & 1) == 0;
@@ -763,44 +764,37 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
             }
             float m = -INFINITY, l = 0.f;
             bool bad = false;                 // V of the tree has elements that are not finite
-            bool ahead = false;               // the tile's scores have been requested
-            uint32_t x[kTrKeys];
             for (int k = P.k0, j = 0; own > 0 && k < P.k1; ++k) {
                 if (!P.has(slot, k)) continue;
                 const int key0 = k * kTrKeys;
                 const bool masked = key0 + kTrKeys > base;
                 const uint32_t tS = tmem + kTrS + kTrKeys * (2 * slot + (t & 1)) + lanes_at;
-                auto request = [&](uint32_t at) {
-#pragma unroll
-                    for (int c = 0; c < kTrKeys; c += 32) tmem_ld32(at + c, *reinterpret_cast<uint32_t(*)[32]>(x + c));
-                };
-                if (!ahead) {
-                    wait(&room.s_full[slot][t & 1], t >> 1);
-                    tc_fence_after_sync();
-                    if (live) request(tS);
-                }
+                wait(&room.s_full[slot][t & 1], t >> 1);
+                tc_fence_after_sync();
                 if (live) {
+                    auto hide = [&](uint32_t(&v)[32], int c) {
+                        const uint32_t seen = seen_word(line, key0 + c - base);
 #pragma unroll
-                    for (int c = 0; c < kTrKeys; c += 32) tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(x + c));
-                    if (masked) {
+                        for (int e = 0; e < 32; ++e) v[e] = (seen >> e) & 1u ? v[e] : 0xff800000u;
+                    };
+                    // The row's maximum on the raw scores (the scale is positive),
+                    // then P, 32 keys at a time and each time from tensor memory:
+                    // held between the two they cost registers and, unrolled,
+                    // instruction cache (E4M3 96 us, so 93).
+                    float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int c = 0; c < kTrKeys; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(tS + c, v);
+                        tmem_wait_ld(v);
+                        if (masked) hide(v, c);
 #pragma unroll
-                        for (int c = 0; c < kTrKeys; c += 32) {
-                            const uint32_t seen = seen_word(line, key0 + c - base);
+                        for (int e = 0; e < 32; e += 4) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[c + e] = (seen >> e) & 1u ? x[c + e] : 0xff800000u;
+                            for (int i = 0; i < 4; ++i) pm[i] = fmaxf(pm[i], __uint_as_float(v[e + i]));
                         }
                     }
-                    // the row's maximum on the raw scores (the scale is positive)
-                    float pm[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) pm[e] = __uint_as_float(x[e]);
-#pragma unroll
-                    for (int e = 8; e < kTrKeys; e += 8) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) pm[i] = fmaxf(pm[i], __uint_as_float(x[e + i]));
-                    }
-                    const float mx = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
-                                           fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7]))) * sl;
+                    const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * sl;
                     const bool raise = mx > m + kRaise;            // the first finite maximum, too
                     if (__any_sync(0xffffffffu, raise)) {
                         const float m_new = raise ? mx - kBelow : m;
@@ -824,31 +818,32 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                     const float ref = m == -INFINITY ? 0.f : m;    // nothing seen yet
                     const uint64_t neg2 = f32x2_pack(-ref, -ref);
                     uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 1
+                    for (int c = 0; c < kTrKeys; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(tS + c, v);
+                        tmem_wait_ld(v);
+                        if (masked) hide(v, c);
 #pragma unroll
-                    for (int c = 0; c < kTrKeys / 16; ++c) {
-                        uint32_t parts[16];                        // hi, then lo
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t parts[16];                    // hi, then lo
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            float a0, a1;
-                            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[16 * c + 2 * i]),
-                                                              __uint_as_float(x[16 * c + 2 * i + 1])), sl2, neg2), a0, a1);
-                            const float p0 = ex2(a0), p1 = ex2(a1);
-                            ps[i & 3] = f32x2_add(ps[i & 3], f32x2_pack(p0, p1));
-                            split_pair<T>(p0, p1, parts[i], parts[8 + i]);
+                            for (int i = 0; i < 8; ++i) {
+                                float a0, a1;
+                                f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[16 * h + 2 * i]),
+                                                                  __uint_as_float(v[16 * h + 2 * i + 1])), sl2, neg2), a0, a1);
+                                const float p0 = ex2(a0), p1 = ex2(a1);
+                                ps[i & 3] = f32x2_add(ps[i & 3], f32x2_pack(p0, p1));
+                                split_pair<T>(p0, p1, parts[i], parts[8 + i]);
+                            }
+                            tmem_st16(tS + c + 16 * h, parts);
                         }
-                        tmem_st16(tS + 16 * c, parts);
                     }
                     float q8[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) f32x2_unpack(ps[e], q8[2 * e], q8[2 * e + 1]);
                     l += ((q8[0] + q8[1]) + (q8[2] + q8[3])) + ((q8[4] + q8[5]) + (q8[6] + q8[7]));
                     // the next tile's scores, where they are there already
-                    ahead = j + 1 < own &&
-                            __all_sync(0xffffffffu, mbar_test_wait(&room.s_full[slot][(t + 1) & 1], ((t + 1) >> 1) & 1));
-                    if (ahead) {
-                        tc_fence_after_sync();
-                        request(tmem + kTrS + kTrKeys * (2 * slot + ((t + 1) & 1)) + lanes_at);
-                    }
                     tmem_wait_st();
                 }
                 if (masked) {
