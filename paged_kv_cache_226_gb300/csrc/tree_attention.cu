@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
         fence_barrier_init();
     }
     if (warp == 1) tmem_alloc(&room.tmem, 512);
+    if (threadIdx.x == 64) prefetch_tensor_map(&tmap_q), prefetch_tensor_map(&tmap_k), prefetch_tensor_map(&tmap_v);
     grid_dependency_wait();
     allow_dependent_launch();
     TrWalk<> walk;
@@ -446,7 +447,6 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                 uint64_t* full = kFp8 ? (keys ? room.kc_full : room.vc_full) : (keys ? room.k_full : room.v_full);
                 uint64_t* empty = kFp8 ? (keys ? room.kc_empty : room.vc_empty) : (keys ? room.k_empty : room.v_empty);
                 uint8_t* ring = smem + (kFp8 ? (keys ? Lay::kKCodes : Lay::kVCodes) : (keys ? Lay::kK : Lay::kV));
-                if (lane == 0) prefetch_tensor_map(map);
                 const int block_shift = p.block_size == 16 ? 4 : 5;
                 const int box = lane & 3, dims = lane >> 2, sub = (16 * box) & (p.block_size - 1);
                 uint8_t* dst = ring + dims * Lay::kHalf + box * kBox16Bytes;
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                 TrRing<kStages> at;
                 TrRing<kTrQStages> q;
                 bool ok = true, held = false;
-                if (keys && lane == 0) prefetch_tensor_map(&tmap_q);
+
                 while (ok && !held && walk.next(p, side, head, P)) {
                     const int32_t* table = p.block_tables + (size_t)P.b * p.max_blocks_per_seq;
                     // block ids: lane i has box i % 4 of tile i / 4 of eight, the
@@ -752,22 +752,33 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
             const int node = node_of(P);
             const bool valid = in_tile < per_tile && node < P.s.C;
             const bool live = __any_sync(0xffffffffu, valid);      // a warp without rows only keeps step
+            // this row's line, read where the first key of the tree comes
             TreeLine line{};
-            wait(&room.lines_full, piece);
-            if (valid && P.k1 * kTrKeys > base) {
-                const uint4 w = room.line[node];
-                line = TreeLine{{w.x, w.y, w.z, w.w}};
-            }
-            if (P.alone) {                                         // else the statistics come there first
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&room.lines_empty);
+            bool taken = false;
+            auto take_line = [&] {
+                wait(&room.lines_full, piece);
+                if (valid && P.k1 * kTrKeys > base) {
+                    const uint4 w = room.line[node];
+                    line = TreeLine{{w.x, w.y, w.z, w.w}};
+                }
+                if (P.alone) {                                     // else the statistics come there first
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&room.lines_empty);
+                }
+                taken = true;
+            };
+            if (own == 0) {
+                take_line();
+                n += count;
+                continue;
             }
             float m = -INFINITY, l = 0.f;
             bool bad = false;                 // V of the tree has elements that are not finite
-            for (int k = P.k0, j = 0; own > 0 && k < P.k1; ++k) {
+            for (int k = P.k0, j = 0; k < P.k1; ++k) {
                 if (!P.has(slot, k)) continue;
                 const int key0 = k * kTrKeys;
                 const bool masked = key0 + kTrKeys > base;
+                if (masked && !taken) take_line();
                 const uint32_t tS = tmem + kTrS + kTrKeys * (2 * slot + (t & 1)) + lanes_at;
                 wait(&room.s_full[slot][t & 1], t >> 1);
                 tc_fence_after_sync();
@@ -893,6 +904,7 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
             }
             n += count;
             // ---- the piece's end ------------------------------------------------
+            if (!taken) take_line();
             if (own > 0) {
                 wait(&room.o_done[slot][(t - 1) & 1], (t - 1) >> 1);
                 tc_fence_after_sync();
@@ -945,10 +957,11 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                             dst[q] = make_uint4(M::pack(o[8 * q], o[8 * q + 1]), M::pack(o[8 * q + 2], o[8 * q + 3]),
                                                 M::pack(o[8 * q + 4], o[8 * q + 5]), M::pack(o[8 * q + 6], o[8 * q + 7]));
                     } else {
-                        float4* dst = reinterpret_cast<float4*>(p.rec_o + (rec * kTrRows + r) * D + d);
+                        // [D / 4][row][4]: a warp writes whole lines
+                        float4* dst = reinterpret_cast<float4*>(p.rec_o) + (rec * (D / 4) + d / 4) * kTrRows + r;
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
-                            dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                            dst[q * kTrRows] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
                     }
                     __syncwarp();
                 }
@@ -973,7 +986,7 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                                 T& o = static_cast<T*>(p.out)[row * D + d];
                                 o = from_float<T>((float)o + y);
                             } else {
-                                p.rec_o[(rec * kTrRows + r) * D + d] += y;
+                                p.rec_o[((rec * (D / 4) + d / 4) * kTrRows + r) * 4 + d % 4] += y;
                             }
                         }
                     }
@@ -999,20 +1012,22 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
 
 // Joins the records of the pairs that more than one lane met: a CTA for some
 // rows of the pair that the range of lane blockIdx.x + 1 begins in, where that
-// is the first range to begin there; a warp per row, D / 32 dims a lane.  Which
+// is the first range to begin there; a lane per row, eight dims each.  Which
 // pair that is it finds while the attention kernel ends: lengths and trees are
 // not written by it, and it has waited for whoever wrote them.
 constexpr int kTrMergeThreads = 256;
-constexpr int kTrMergeRows = 16;               // of a CTA
+constexpr int kTrMergeDims = 8;                // of a thread
 
 template <typename T, int D, bool kFp8>
 __global__ void __launch_bounds__(kTrMergeThreads)
     tree_merge_kernel(const __grid_constant__ TreeParams p) {
-    constexpr int kDims = D / 32;
     allow_dependent_launch();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.y % p.heads, side = blockIdx.y / p.heads;
-    const int slot = blockIdx.z / (kTrRows / kTrMergeRows), r0 = blockIdx.z % (kTrRows / kTrMergeRows) * kTrMergeRows;
+    // (dims, rows) of this thread: 32 rows a warp, the dims of a row in D / 8 warps
+    constexpr int kParts = D / kTrMergeDims;
+    const int at = blockIdx.z * (kTrMergeThreads / 32) + (int)(threadIdx.x >> 5);
+    const int d = at % kParts * kTrMergeDims, row = at / kParts * 32 + (int)(threadIdx.x & 31);
+    const int slot = row / kTrRows, r = row % kTrRows;
     TrWalk<true> walk;
     const TrDeal deal(p, walk.count(p, false));
     const unsigned mine = blockIdx.x + 1;
@@ -1033,55 +1048,45 @@ __global__ void __launch_bounds__(kTrMergeThreads)
     grid_dependency_wait();
     if (!join) return;
     const int G = p.group, per_tile = tr_nodes_per_tile(G);
-    for (int r = r0 + warp; r < r0 + kTrMergeRows; r += kTrMergeThreads / 32) {
-        const int in_tile = r / G, node = (kTrSlots * side + slot) * per_tile + in_tile;
-        if (in_tile >= per_tile || node >= P.s.C) break;
-        float m = -INFINITY, l = 0.f, o[kDims] = {};
-        constexpr int kAhead = 4;
-        for (unsigned c = mine - 1; c <= c1; c += kAhead) {
-            float2 ml[kAhead];
-            float v[kAhead][kDims];
+    const int in_tile = r / G, node = (kTrSlots * side + slot) * per_tile + in_tile;
+    if (in_tile >= per_tile || node >= P.s.C) return;
+    float m = -INFINITY, l = 0.f, o[kTrMergeDims] = {};
+    constexpr int kAhead = 4;
+    for (unsigned c = mine - 1; c <= c1; c += kAhead) {
+        float2 ml[kAhead];
+        float4 v[kAhead][2];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                ml[i] = make_float2(-INFINITY, 0.f);
-                if (c + i > c1) continue;
-                const int64_t cta = ((int64_t)(c + i) * p.sides + side) * p.heads + head;
-                const int64_t rec = ((cta * 2 + (c + i == mine - 1 ? 1 : 0)) * kTrSlots + slot) * kTrRows + r;
-                ml[i] = p.rec_ml[rec];
-                const float* src = p.rec_o + rec * D + kDims * lane;
-                if constexpr (kDims == 4) {
-                    const float4 x = *reinterpret_cast<const float4*>(src);
-                    v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-                } else {
-                    const float2 x = *reinterpret_cast<const float2*>(src);
-                    v[i][0] = x.x, v[i][1] = x.y;
-                }
-            }
-            float top = m;
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) top = fmaxf(top, ml[i].x);
-            const float ref = top == -INFINITY ? 0.f : top, f = ex2(m - ref);
-            m = top;
-            l *= f;
-#pragma unroll
-            for (int k = 0; k < kDims; ++k) o[k] *= f;
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                if (c + i > c1) continue;
-                const float w = ex2(ml[i].x - ref);
-                l += w * ml[i].y;
-#pragma unroll
-                for (int k = 0; k < kDims; ++k) o[k] += w * v[i][k];
-            }
+        for (int i = 0; i < kAhead; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.f);
+            if (c + i > c1) continue;
+            const int64_t cta = ((int64_t)(c + i) * p.sides + side) * p.heads + head;
+            const int64_t rec = (cta * 2 + (c + i == mine - 1 ? 1 : 0)) * kTrSlots + slot;
+            ml[i] = p.rec_ml[rec * kTrRows + r];
+            const float4* src = reinterpret_cast<const float4*>(p.rec_o) + (rec * (D / 4) + d / 4) * kTrRows + r;
+            v[i][0] = src[0], v[i][1] = src[kTrRows];
         }
-        const float norm = (kFp8 ? p.v_scale : 1.f) / l;
-        T* dst = static_cast<T*>(p.out) + ((int64_t)(P.s.q0 + node) * p.num_q_heads + P.g * G + (r - in_tile * G)) * D + kDims * lane;
-        using M = Mma<T>;
-        if constexpr (kDims == 4)
-            *reinterpret_cast<uint2*>(dst) = make_uint2(M::pack(o[0] * norm, o[1] * norm), M::pack(o[2] * norm, o[3] * norm));
-        else
-            *reinterpret_cast<uint32_t*>(dst) = M::pack(o[0] * norm, o[1] * norm);
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) top = fmaxf(top, ml[i].x);
+        const float ref = top == -INFINITY ? 0.f : top, f = ex2(m - ref);
+        m = top;
+        l *= f;
+#pragma unroll
+        for (int k = 0; k < kTrMergeDims; ++k) o[k] *= f;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (c + i > c1) continue;
+            const float w = ex2(ml[i].x - ref);
+            l += w * ml[i].y;
+            o[0] += w * v[i][0].x, o[1] += w * v[i][0].y, o[2] += w * v[i][0].z, o[3] += w * v[i][0].w;
+            o[4] += w * v[i][1].x, o[5] += w * v[i][1].y, o[6] += w * v[i][1].z, o[7] += w * v[i][1].w;
+        }
     }
+    using M = Mma<T>;
+    const float norm = (kFp8 ? p.v_scale : 1.f) / l;
+    T* dst = static_cast<T*>(p.out) + ((int64_t)(P.s.q0 + node) * p.num_q_heads + P.g * G + (r - in_tile * G)) * D + d;
+    *reinterpret_cast<uint4*>(dst) = make_uint4(M::pack(o[0] * norm, o[1] * norm), M::pack(o[2] * norm, o[3] * norm),
+                                                M::pack(o[4] * norm, o[5] * norm), M::pack(o[6] * norm, o[7] * norm));
 }
 
 size_t tree_plan(TreeParams& p, int head_dim, void* workspace) {
@@ -1115,9 +1120,10 @@ cudaError_t launch_tree_t(const CUtensorMap& tmk, const CUtensorMap& tmv, const 
                         stream, tmk, tmv, tmq, p);
     if (e != cudaSuccess || p.whole) return e;
     if (p.ctas == 1) return e;
-    const int rows = std::min(kTrRows / p.group, p.max_query) * p.group;          // of a query tile at most
-    const int slots = p.max_query * p.group > kTrRows / p.group * p.group ? kTrSlots : 1;
-    const int chunks = slots == 1 ? (rows + kTrMergeRows - 1) / kTrMergeRows : kTrSlots * (kTrRows / kTrMergeRows);
+    // rows of the slots, by 32
+    const int per_tile = kTrRows / p.group;
+    const int rows = p.max_query > per_tile ? kTrSlots * kTrRows : (p.max_query * p.group + 31) / 32 * 32;
+    const int chunks = (rows / 32 * (D / kTrMergeDims) + kTrMergeThreads / 32 - 1) / (kTrMergeThreads / 32);
     return launch_with_pdl(tree_merge_kernel<T, D, kFp8>,
                            dim3((unsigned)(p.ctas - 1), (unsigned)(p.heads * p.sides), (unsigned)chunks),
                            dim3(kTrMergeThreads), 0, stream, p);
