@@ -1012,11 +1012,20 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
 
 // Joins the records of the pairs that more than one lane met: a CTA for some
 // rows of the pair that the range of lane blockIdx.x + 1 begins in, where that
-// is the first range to begin there; a lane per row, eight dims each.  Which
+// is the first range to begin there, or of pair blockIdx.x where there are few
+// pairs (tr_merge_pairs); a lane per row, eight dims each.  Which
 // pair that is it finds while the attention kernel ends: lengths and trees are
 // not written by it, and it has waited for whoever wrote them.
 constexpr int kTrMergeThreads = 256;
 constexpr int kTrMergeDims = 8;                // of a thread
+
+// Whether the joining grid goes by pairs, which finds its place with one load a
+// lane, or by ranges, which walks.  One pair on 19 ranges 58.9 us by pairs and
+// 65.0 by ranges (50,000 tokens), 20.3 and 23.9 (4096), four 14.1 and 15.1; 16
+// pairs on 19 ranges 26.4 and 22.9: by pairs where there are two ranges a pair.
+__host__ __device__ __forceinline__ bool tr_merge_pairs(const TreeParams& p) {
+    return (int64_t)p.num_seqs * (p.num_kv_heads / p.heads) * 2 < p.ctas;
+}
 
 template <typename T, int D, bool kFp8>
 __global__ void __launch_bounds__(kTrMergeThreads)
@@ -1030,20 +1039,29 @@ __global__ void __launch_bounds__(kTrMergeThreads)
     const int slot = row / kTrRows, r = row % kTrRows;
     TrWalk<true> walk;
     const TrDeal deal(p, walk.count(p, false));
-    const unsigned mine = blockIdx.x + 1;
     TrPiece P;
-    bool join = mine < deal.ctas;
-    unsigned c1 = mine;
+    unsigned begin, each, c0, c1 = 0;
+    bool join;
+    if (tr_merge_pairs(p)) {
+        const int per_seq = p.num_kv_heads / p.heads;
+        P.b = blockIdx.x / per_seq;
+        P.s = tree_sequence<true>(p, P.b, false);
+        P.g = head + (int)blockIdx.x % per_seq * p.heads;
+        unsigned before = 0;
+        for (int i = threadIdx.x & 31; i < P.b; i += 32) before += TrWalk<true>::weight(p, tree_sequence<true>(p, i, false));
+        each = TrWalk<true>::each(p, P.s);
+        begin = __reduce_add_sync(0xffffffffu, before) + (unsigned)(blockIdx.x % per_seq) * each;
+        join = P.s.C > 0;
+    } else {
+        walk.at = deal.begin(min(blockIdx.x + 1, deal.ctas));
+        join = blockIdx.x + 1 < deal.ctas && walk.find(p, side, head, P, begin, each);
+    }
     if (join) {
-        // the pair at the range's begin (one CTA's rows of it: all its tiles)
-        walk.at = deal.begin(mine);
-        walk.end = deal.N;
-        unsigned begin = 0, each = 1;
-        join = walk.find(p, side, head, P, begin, each);
-        // lanes before the first tile's, and after the last's, have nothing of it
-        join = join && deal.cta_of(begin + kTrPairWeight) == mine - 1;
-        c1 = deal.cta_of(begin + each - 1);
-        join = join && c1 >= mine && P.rows(slot);
+        // from the lane that has the first tile to the one that has the last
+        c0 = deal.cta_of(begin + kTrPairWeight), c1 = deal.cta_of(begin + each - 1);
+        join = c1 > c0 && (tr_merge_pairs(p) || c0 == blockIdx.x);
+        const int per_tile = tr_nodes_per_tile(p.group);
+        join = join && (kTrSlots * side + slot) * per_tile < P.s.C;
     }
     grid_dependency_wait();
     if (!join) return;
@@ -1052,7 +1070,7 @@ __global__ void __launch_bounds__(kTrMergeThreads)
     if (in_tile >= per_tile || node >= P.s.C) return;
     float m = -INFINITY, l = 0.f, o[kTrMergeDims] = {};
     constexpr int kAhead = 4;
-    for (unsigned c = mine - 1; c <= c1; c += kAhead) {
+    for (unsigned c = c0; c <= c1; c += kAhead) {
         float2 ml[kAhead];
         float4 v[kAhead][2];
 #pragma unroll
@@ -1060,7 +1078,7 @@ __global__ void __launch_bounds__(kTrMergeThreads)
             ml[i] = make_float2(-INFINITY, 0.f);
             if (c + i > c1) continue;
             const int64_t cta = ((int64_t)(c + i) * p.sides + side) * p.heads + head;
-            const int64_t rec = (cta * 2 + (c + i == mine - 1 ? 1 : 0)) * kTrSlots + slot;
+            const int64_t rec = (cta * 2 + (c + i == c0 ? 1 : 0)) * kTrSlots + slot;
             ml[i] = p.rec_ml[rec * kTrRows + r];
             const float4* src = reinterpret_cast<const float4*>(p.rec_o) + (rec * (D / 4) + d / 4) * kTrRows + r;
             v[i][0] = src[0], v[i][1] = src[kTrRows];
@@ -1125,7 +1143,8 @@ cudaError_t launch_tree_t(const CUtensorMap& tmk, const CUtensorMap& tmv, const 
     const int rows = p.max_query > per_tile ? kTrSlots * kTrRows : (p.max_query * p.group + 31) / 32 * 32;
     const int chunks = (rows / 32 * (D / kTrMergeDims) + kTrMergeThreads / 32 - 1) / (kTrMergeThreads / 32);
     return launch_with_pdl(tree_merge_kernel<T, D, kFp8>,
-                           dim3((unsigned)(p.ctas - 1), (unsigned)(p.heads * p.sides), (unsigned)chunks),
+                           dim3((unsigned)(tr_merge_pairs(p) ? p.num_seqs * (p.num_kv_heads / p.heads) : p.ctas - 1),
+                                (unsigned)(p.heads * p.sides), (unsigned)chunks),
                            dim3(kTrMergeThreads), 0, stream, p);
 }
 
