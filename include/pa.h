@@ -571,9 +571,10 @@ int pa_evict_fp8(void* k_cache, void* v_cache, const int32_t* block_tables,
  * Speculative decoding: a tree of drafted tokens per sequence
  * ---------------------------------------------------------------------------
  * The pages leave speculative decoding to the engine; what it asks of a paged
- * cache is below.  In a verification step sequence b has C_b = query_start[b + 1] - query_start[b] nodes, the last
- * C_b of its L_b cached tokens: node i is row query_start[b] + i of the batch
- * and stands at cache index L_b - C_b + i.  Node 0 is the sequence's newest
+ * cache is below.  In a verification step sequence b has C_b nodes, C_b being
+ * query_start[b + 1] - query_start[b]: the last C_b of its L_b cached tokens.
+ * Node i is row query_start[b] + i of the batch and stands at cache index
+ * L_b - C_b + i.  Node 0 is the sequence's newest
  * token, the others are drafted after it: parents[row] < i is the node (of the
  * same sequence) that node i follows, negative: the context itself.  A parent
  * that is not below its node counts as negative and sets PA_DEVERR_BAD_INDEX.
@@ -618,16 +619,18 @@ int pa_norm_rope_and_cache_fp8(const void* q, int64_t q_stride, const void* k, i
  * holds their K and V already.  Node i of sequence b sees the L_b - C_b tokens
  * before the tree, its ancestors and itself:
  *   out[row][h] = sum_j p_j V_j,  p = softmax_j(scale * q[row][h] . K_j).
- * q, out [num_tokens][num_q_heads][head_dim]; rows behind the last sequence
- * are not written.  parents [num_tokens] int32, null: every node follows the
+ * q, out [num_tokens][num_q_heads][head_dim], not overlapping; rows behind the
+ * last sequence are not written.  parents [num_tokens] int32, null: every node follows the
  * one before it (a line of drafted tokens, or the chunks of pa_prefill).
- * scale must be finite and > 0.  max_query_len >= every C_b, at most
- * PA_TREE_NODES (else PA_ERR_UNSUPPORTED); max_context_len >= every L_b;
- * values outside these bounds are clamped and set PA_DEVERR_BAD_CONTEXT.
+ * scale must be > 0, and finite also times log2(e) (and k_scale).
+ * max_query_len >= every C_b, at most PA_TREE_NODES (else PA_ERR_UNSUPPORTED);
+ * max_context_len >= every L_b; values outside these bounds are clamped and set
+ * PA_DEVERR_BAD_CONTEXT.
  * Softmax statistics and sums are in fp32; p meets V in two parts of the
  * 16-bit type, which hold it to 2^-15 (bf16) or 2^-22 (fp16; and to 2^-31 of
- * the row's largest), and out is rounded once.  A token that a node does not see has no part in its row, also
- * where its K or V is not finite.
+ * the row's largest), and out is rounded once.  A token that a node does not
+ * see has no part in its row, also where its K or V is not finite; an infinite
+ * V that it does see makes these elements of its row infinite or NaN.
  * workspace: device memory of at least pa_tree_attention_workspace_size bytes,
  * 16-byte aligned, no initial contents; calls that overlap on the GPU must
  * not share it.  One or two launches.
@@ -677,10 +680,10 @@ int pa_accept_tree(const int64_t* draft, const int64_t* target, const int32_t* p
  * left as it is (new_lens[b] = L_b).  path [num_seqs][path_stride] int32.
  * k_caches, v_caches: host arrays of num_layers (at most 1024) device pointers,
  * one cache pair per layer, all of the shape shp and of the same block tables;
- * no cache may be listed twice.  The blocks that hold a tree must not be shared with
- * another sequence.  A block id outside the pool sets PA_DEVERR_BAD_CONTEXT
- * and its rows are not moved.  new_lens must not be an input array.  One
- * launch for every 64 layers.  pa_commit_path_fp8: the same on E4M3 caches.
+ * no cache may be listed twice or lie over another.  The blocks that hold a
+ * tree must not be shared with another sequence.  A block id outside the pool
+ * sets PA_DEVERR_BAD_CONTEXT and its rows are not moved.  new_lens must not be
+ * an input array.  One launch for every 64 layers.  pa_commit_path_fp8: the same on E4M3 caches.
  */
 int pa_commit_path(void* const* k_caches, void* const* v_caches, int32_t num_layers,
                    const int32_t* block_tables, const int32_t* context_lens,

@@ -11,6 +11,12 @@ constexpr int kMaxLayers = 1024;         // of one pa_commit_path
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Whether two buffers of `bytes` bytes have some in common.
+bool overlap(const void* a, const void* b, uint64_t bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x == y || (x < y ? y - x : x - y) < bytes;
+}
+
 int finish(cudaError_t e) {
     if (e == cudaSuccess) return PA_OK;
     pa::record_cuda_error(static_cast<int>(e));
@@ -41,20 +47,21 @@ int tree_attention(const void* q, const void* k_cache, const void* v_cache, cons
     int st = pa::check_decode_args(k_cache, k_cache, v_cache, block_tables, context_lens, shp);
     if (st != PA_OK) return st;
     if (fp8 && (st = pa::check_fp8(shp, k_scale, v_scale)) != PA_OK) return st;
-    if (num_tokens < 0 || num_tokens > 0x7fffffffll || !(scale > 0.f) || !std::isfinite(scale))
+    const float scale_log2 = scale * (fp8 ? k_scale : 1.f) * pa::kLog2e;
+    if (num_tokens < 0 || num_tokens > 0x7fffffffll || !(scale > 0.f) || !std::isfinite(scale_log2))
         return PA_ERR_INVALID_ARG;
     if ((st = check_tree(max_query_len, max_context_len)) != PA_OK) return st;
     if (shp->num_seqs == 0) return PA_OK;
     if (!query_start || !aligned(query_start, 4) || !aligned(parents, 4) || !aligned(q, 16) || !aligned(out, 16) ||
-        (num_tokens > 0 && (!q || !out)) || (q != nullptr && q == out))
+        (num_tokens > 0 &&
+         (!q || !out || overlap(q, out, 2ull * num_tokens * shp->num_q_heads * shp->head_dim))))
         return PA_ERR_INVALID_ARG;
     pa::TreeParams p = tree_sizes(shp, max_query_len, max_context_len);
     if (!workspace || workspace_bytes < pa::tree_plan(p, shp->head_dim, workspace)) return PA_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return PA_ERR_INVALID_ARG;
     if (num_tokens == 0 || p.max_query == 0) return PA_OK;
-    // key tiles are counted in 32 bits
-    if (((int64_t)p.max_context / pa::kTreeKeys + 4) * p.num_seqs * p.num_kv_heads >= (1ll << 31))
-        return PA_ERR_UNSUPPORTED;
+    const int64_t tiles = (p.max_context + pa::kTreeKeys - 1) / pa::kTreeKeys;
+    if ((tiles + pa::kTreePairWeight) * p.num_seqs * p.num_kv_heads >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
     CUtensorMap tmk, tmv, tmq;
     if ((st = pa::encode_cache_map(&tmk, k_cache, shp, fp8)) != PA_OK) return st;
     if ((st = pa::encode_cache_map(&tmv, v_cache, shp, fp8)) != PA_OK) return st;
@@ -65,7 +72,7 @@ int tree_attention(const void* q, const void* k_cache, const void* v_cache, cons
     p.q = q, p.k_cache = k_cache, p.v_cache = v_cache, p.out = out;
     p.block_tables = block_tables, p.context_lens = context_lens, p.query_start = query_start;
     p.parents = parents;
-    p.scale_log2 = scale * (fp8 ? k_scale : 1.f) * pa::kLog2e, p.v_scale = v_scale;
+    p.scale_log2 = scale_log2, p.v_scale = v_scale;
     p.max_blocks_per_seq = shp->max_blocks_per_seq, p.block_size = shp->block_size;
     p.num_blocks = shp->num_blocks, p.num_tokens = num_tokens;
 #ifdef PA_TEST_HOOKS
@@ -93,13 +100,15 @@ int commit_path(void* const* k_caches, void* const* v_caches, int32_t num_layers
         if (!aligned(a, 4)) return PA_ERR_INVALID_ARG;
     for (const int32_t* a : {block_tables, context_lens, query_start, path, path_lens})
         if (a == new_lens) return PA_ERR_INVALID_ARG;
-    // no cache twice: two CTAs would move the same rows
+    // no cache twice and none over another: two CTAs would move the same rows
+    const uint64_t bytes = (uint64_t)shp->num_blocks * shp->block_size * shp->num_kv_heads * shp->head_dim * (fp8 ? 1 : 2);
     void* all[2 * kMaxLayers];
     void** const end = std::copy(v_caches, v_caches + num_layers, std::copy(k_caches, k_caches + num_layers, all));
     for (void** c = all; c < end; ++c)
         if (!*c || !aligned(*c, 16)) return PA_ERR_INVALID_ARG;
     std::sort(all, end);
-    if (std::adjacent_find(all, end) != end) return PA_ERR_INVALID_ARG;
+    if (std::adjacent_find(all, end, [&](void* a, void* b) { return overlap(a, b, bytes); }) != end)
+        return PA_ERR_INVALID_ARG;
     pa::CommitParams p{};
     cudaError_t e = pa::error_word(&p.err);
     if (e != cudaSuccess) return finish(e);

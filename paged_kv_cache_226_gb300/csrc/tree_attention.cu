@@ -75,7 +75,7 @@ static_assert(256 * tr_softmax_regs(false) + 256 * kTrControlRegs <= 512 * 128 &
 constexpr int kTrCtas = 152;                   // one per SM
 constexpr int kTrMinTiles = 8;                 // weight of a CTA's range at least, where there are records
 constexpr int kTrWholeTiles = 8;               // longest contexts, in tiles, whose pairs stay whole
-constexpr int kTrPairWeight = 4;               // of a pair beside its key tiles, in the dealing
+constexpr int kTrPairWeight = kTreePairWeight;
 constexpr int kTrSoloTiles = 2;                // of a piece that one slot takes alone
 
 // Shared memory: query tiles, operand tiles, codes.
@@ -575,6 +575,7 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
             // the trees' lines, a piece ahead of those who read them
             // --------------------------------------------------------------
             bool ok = true;
+            int before = 0;                                        // key tiles of the piece before
             for (int i = 0; ok && walk.next(p, side, head, P); ++i) {
                 uint32_t w[kLineWords][kLineWords] = {};
                 const bool tree = P.k1 * kTrKeys > P.s.L - P.s.C;      // the piece has some of it
@@ -587,7 +588,11 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                     }
                     warp_lines(w, up, P.s.C);
                 }
+                // the room is free where the piece before ends, which may be long:
+                // another limit for every 2^17 of its tiles
                 if (i > 0) ok = tr_wait(p, &room.lines_empty, i - 1);
+                for (int more = before >> 17; !ok && more > 0; --more) ok = tr_wait(p, &room.lines_empty, i - 1);
+                before = P.k1 - P.k0;
                 if (!ok) break;
                 if (tree) {
 #pragma unroll

@@ -48,8 +48,10 @@ cudaError_t launch_tree_attention(int dtype, int head_dim, bool fp8, const CUten
                                   cudaStream_t stream);
 // Nodes of a query tile: the box of its map.
 int tree_nodes_per_tile(int group);
-// Keys of a tile: the tiles of a call are counted in 31 bits.
+// Keys of a tile, and what a (sequence, KV head) pair weighs beside its tiles
+// in the dealing.  The weight of a call is counted in 31 bits.
 constexpr int kTreeKeys = 64;
+constexpr int kTreePairWeight = 4;
 
 struct AcceptParams {
     const int64_t* draft;          // [T]

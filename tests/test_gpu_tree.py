@@ -252,6 +252,47 @@ def test_tree_long(dev, dtype, fp8):
     check_tree(dev, [9000, 5003], [12, 40], 8, 2, 128, 16, dtype, fp8=fp8, seed=2)
 
 
+@pytest.mark.parametrize("lens,nodes,hq,hkv,d,fp8", [
+    ([6000], [9], 32, 32, 64, False),                      # KV heads of several lanes, joined pair by pair
+    ([3001, 0, 2400], [30, 0, 17], 32, 16, 128, False),
+    ([5000], [128], 16, 2, 128, False),                    # four CTAs side by side, 152 / 8 ranges
+    ([4100], [100], 7, 1, 128, True),
+    ([700 + 13 * i for i in range(16)], [1 + 3 * i for i in range(16)], 16, 8, 128, True),
+    ([600 + 41 * i for i in range(9)], [5] * 9, 20, 5, 64, False)])
+def test_tree_ranges_that_meet_in_pairs(dev, lens, nodes, hq, hkv, d, fp8):
+    check_tree(dev, lens, nodes, hq, hkv, d, 16, torch.bfloat16, fp8=fp8, seed=hkv, behind=2)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tree_shared_and_repeated_blocks(dev, fp8):
+    """Sequences with the same context, and a context that has one block over and over."""
+    x = Batch([900, 900, 900], 8, 2, 128, 16, torch.bfloat16, seed=3, fp8=fp8, stale=False)
+    nodes = [20, 33, 8]
+    shared = (900 - max(nodes)) // 16
+    x.tables[1, :shared] = x.tables[0, :shared]
+    x.tables[2, :shared] = x.tables[0, 0]
+    q = torch.randn(sum(nodes), 8, 128, generator=x.gen).to(torch.bfloat16)
+    parents = random_parents(nodes, x.gen)
+    want, bound = tree_reference(x, q, nodes, parents)
+    got = lib.tree_attention(q.to(dev), x.k.to(dev), x.v.to(dev), x.tables.to(dev), x.lens.to(dev), starts(nodes).to(dev),
+                             parents.to(dev), x.scale, 33, 900, **x.scales())
+    within(got, want, bound, "out")
+    assert lib.read_device_errors(dev) == 0
+
+
+def test_tree_strangers_are_refused(dev):
+    """Rows that are not dense, out over q, on the host, or of another shape."""
+    x = Batch([40], 4, 2, 64, 16, torch.float16, seed=1, stale=False)
+    room = torch.zeros(12, 4, 64, dtype=torch.float16, device=dev)
+    args = [x.k.to(dev), x.v.to(dev), x.tables.to(dev), x.lens.to(dev), starts([8]).to(dev), None, x.scale, 8, 40]
+    for q, out in ((room[::2], None), (room[:8], room[2:10]), (room[2:10], room[:8]), (room[:8], room[:8]),
+                   (room[:8], room[:8].cpu()), (room[:8], room[8:]), (room[:8].cpu(), None),
+                   (room[:8].transpose(1, 2).contiguous().transpose(1, 2), None)):
+        with pytest.raises((ValueError, lib.PaError)):
+            lib.tree_attention(q, *args, out=out)
+    assert bool((room == 0).all()) and lib.read_device_errors(dev) == 0
+
+
 def test_tree_many_sequences(dev):
     """More sequences than a warp walks at a time, every other length, empty ones among them."""
     n = 75

@@ -83,6 +83,25 @@ def test_tree_checks(pa):
     assert tree(pa, max_q=0) == lib.PA_OK and tree(pa, max_ctx=0) == lib.PA_OK
 
 
+def test_tree_sizes_and_overlaps(pa):
+    assert tree(pa, scale=3e38) == BAD and tree(pa, scale=1e30, fp8=(1e10, 1.0), shp=shape(head_dim=128)) == BAD
+    row = 8 * 128 * 2
+    for off in (16, row, 9 * row - 16):
+        assert tree(pa, T=9, q=ctypes.c_void_p(1 << 20), out=ctypes.c_void_p((1 << 20) + off)) == BAD
+        assert tree(pa, T=9, q=ctypes.c_void_p((1 << 20) + off), out=ctypes.c_void_p(1 << 20)) == BAD
+    # one KV head and 2^30 tokens: 2^24 key tiles and the pair, 128 sequences of them are too many
+    big = shape(num_seqs=128, num_q_heads=1, num_kv_heads=1, block_size=16, max_blocks_per_seq=1 << 26)
+    n = pa.pa_tree_attention_workspace_size(big, 8, 1 << 30)
+    assert n > 0 and tree(pa, big, n=n, max_ctx=1 << 30) == UNSUPPORTED
+
+
+def test_commit_refuses_caches_over_one_another(pa):
+    size, at = 16 * 16 * 2 * 128 * 2, 1 << 24
+    for off in (16, size - 16):
+        assert commit(pa, ks=(at,), vs=(at + off,)) == BAD
+        assert commit(pa, ks=(at + off, 1 << 26), vs=(1 << 27, at)) == BAD
+
+
 def accept(pa, **kw):
     a = dict(draft=FAKE, target=FAKE, par=FAKE, qs=FAKE, B=2, T=9, max_q=8, path=FAKE, lens=FAKE, next=FAKE)
     a.update(kw)
