@@ -620,12 +620,13 @@ int pa_norm_rope_and_cache_fp8(const void* q, int64_t q_stride, const void* k, i
  * before the tree, its ancestors and itself:
  *   out[row][h] = sum_j p_j V_j,  p = softmax_j(scale * q[row][h] . K_j).
  * q, out [num_tokens][num_q_heads][head_dim], not overlapping; rows behind the
- * last sequence are not written.  parents [num_tokens] int32, null: every node follows the
- * one before it (a line of drafted tokens, or the chunks of pa_prefill).
- * scale must be > 0, and finite also times log2(e) (and k_scale).
+ * last sequence are not written.  parents [num_tokens] int32, null: every node
+ * follows the one before it (a line of drafted tokens, or the chunks of
+ * pa_prefill).  scale must be > 0, and finite also times log2(e) (and k_scale).
  * max_query_len >= every C_b, at most PA_TREE_NODES (else PA_ERR_UNSUPPORTED);
- * max_context_len >= every L_b; values outside these bounds are clamped and set
- * PA_DEVERR_BAD_CONTEXT.
+ * max_context_len >= every L_b; values outside these bounds are clamped and
+ * set PA_DEVERR_BAD_CONTEXT.  Bounds that come to 2^31 key tiles of 64 or more
+ * over all sequences and KV heads, four added to each, are PA_ERR_UNSUPPORTED.
  * Softmax statistics and sums are in fp32; p meets V in two parts of the
  * 16-bit type, which hold it to 2^-15 (bf16) or 2^-22 (fp16; and to 2^-31 of
  * the row's largest), and out is rounded once.  A token that a node does not
@@ -683,7 +684,8 @@ int pa_accept_tree(const int64_t* draft, const int64_t* target, const int32_t* p
  * no cache may be listed twice or lie over another.  The blocks that hold a
  * tree must not be shared with another sequence.  A block id outside the pool
  * sets PA_DEVERR_BAD_CONTEXT and its rows are not moved.  new_lens must not be
- * an input array.  One launch for every 64 layers.  pa_commit_path_fp8: the same on E4M3 caches.
+ * an input array.  One launch for every 64 layers.  pa_commit_path_fp8: the
+ * same on E4M3 caches.
  */
 int pa_commit_path(void* const* k_caches, void* const* v_caches, int32_t num_layers,
                    const int32_t* block_tables, const int32_t* context_lens,

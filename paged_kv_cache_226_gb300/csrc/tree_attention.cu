@@ -1032,20 +1032,19 @@ __host__ __device__ __forceinline__ bool tr_merge_pairs(const TreeParams& p) {
     return (int64_t)p.num_seqs * (p.num_kv_heads / p.heads) * 2 < p.ctas;
 }
 
-template <typename T, int D, bool kFp8>
-__global__ void __launch_bounds__(kTrMergeThreads)
-    tree_merge_kernel(const __grid_constant__ TreeParams p) {
-    allow_dependent_launch();
-    const int head = blockIdx.y % p.heads, side = blockIdx.y / p.heads;
-    // (dims, rows) of this thread: 32 rows a warp, the dims of a row in D / 8 warps
-    constexpr int kParts = D / kTrMergeDims;
-    const int at = blockIdx.z * (kTrMergeThreads / 32) + (int)(threadIdx.x >> 5);
-    const int d = at % kParts * kTrMergeDims, row = at / kParts * 32 + (int)(threadIdx.x & 31);
-    const int slot = row / kTrRows, r = row % kTrRows;
+// A pair to join: its lanes [c0, c1], nodes (none: nothing to join) and their
+// first row, and KV head.
+struct TrJoin {
+    unsigned c0, c1;
+    int C, q0, g;
+};
+
+// By a warp.
+__device__ __forceinline__ TrJoin tree_join(const TreeParams& p, int side, int head) {
     TrWalk<true> walk;
     const TrDeal deal(p, walk.count(p, false));
     TrPiece P;
-    unsigned begin, each, c0, c1 = 0;
+    unsigned begin = 0, each = 0;
     bool join;
     if (tr_merge_pairs(p)) {
         const int per_seq = p.num_kv_heads / p.heads;
@@ -1061,18 +1060,39 @@ __global__ void __launch_bounds__(kTrMergeThreads)
         walk.at = deal.begin(min(blockIdx.x + 1, deal.ctas));
         join = blockIdx.x + 1 < deal.ctas && walk.find(p, side, head, P, begin, each);
     }
-    if (join) {
-        // from the lane that has the first tile to the one that has the last
-        c0 = deal.cta_of(begin + kTrPairWeight), c1 = deal.cta_of(begin + each - 1);
-        join = c1 > c0 && (tr_merge_pairs(p) || c0 == blockIdx.x);
-        const int per_tile = tr_nodes_per_tile(p.group);
-        join = join && (kTrSlots * side + slot) * per_tile < P.s.C;
+    TrJoin x{0u, 0u, 0, 0, 0};
+    if (!join) return x;
+    // from the lane that has the first tile to the one that has the last
+    x.c0 = deal.cta_of(begin + kTrPairWeight), x.c1 = deal.cta_of(begin + each - 1);
+    x.q0 = P.s.q0, x.g = P.g;
+    if (x.c1 > x.c0 && (tr_merge_pairs(p) || x.c0 == blockIdx.x)) x.C = P.s.C;
+    return x;
+}
+
+template <typename T, int D, bool kFp8>
+__global__ void __launch_bounds__(kTrMergeThreads)
+    tree_merge_kernel(const __grid_constant__ TreeParams p) {
+    allow_dependent_launch();
+    const int head = blockIdx.y % p.heads, side = blockIdx.y / p.heads;
+    // (dims, rows) of this thread: 32 rows a warp, the dims of a row in D / 8 warps
+    constexpr int kParts = D / kTrMergeDims;
+    const int at = blockIdx.z * (kTrMergeThreads / 32) + (int)(threadIdx.x >> 5);
+    const int d = at % kParts * kTrMergeDims, row = at / kParts * 32 + (int)(threadIdx.x & 31);
+    const int slot = row / kTrRows, r = row % kTrRows;
+    // a warp finds the pair for all: every warp by itself, 4600 of them read the
+    // same few lines of the L2
+    __shared__ TrJoin found;
+    if (threadIdx.x < 32) {
+        const TrJoin x = tree_join(p, side, head);
+        if (threadIdx.x == 0) found = x;
     }
+    __syncthreads();
+    const TrJoin J = found;
     grid_dependency_wait();
-    if (!join) return;
     const int G = p.group, per_tile = tr_nodes_per_tile(G);
     const int in_tile = r / G, node = (kTrSlots * side + slot) * per_tile + in_tile;
-    if (in_tile >= per_tile || node >= P.s.C) return;
+    if (in_tile >= per_tile || node >= J.C) return;
+    const unsigned c0 = J.c0, c1 = J.c1;
     float m = -INFINITY, l = 0.f, o[kTrMergeDims] = {};
     constexpr int kAhead = 4;
     for (unsigned c = c0; c <= c1; c += kAhead) {
@@ -1107,7 +1127,7 @@ __global__ void __launch_bounds__(kTrMergeThreads)
     }
     using M = Mma<T>;
     const float norm = (kFp8 ? p.v_scale : 1.f) / l;
-    T* dst = static_cast<T*>(p.out) + ((int64_t)(P.s.q0 + node) * p.num_q_heads + P.g * G + (r - in_tile * G)) * D + d;
+    T* dst = static_cast<T*>(p.out) + ((int64_t)(J.q0 + node) * p.num_q_heads + J.g * G + (r - in_tile * G)) * D + d;
     *reinterpret_cast<uint4*>(dst) = make_uint4(M::pack(o[0] * norm, o[1] * norm), M::pack(o[2] * norm, o[3] * norm),
                                                 M::pack(o[4] * norm, o[5] * norm), M::pack(o[6] * norm, o[7] * norm));
 }
