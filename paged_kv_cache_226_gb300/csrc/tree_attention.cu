@@ -1028,6 +1028,10 @@ constexpr int kTrMergeDims = 8;                // of a thread
 // lane, or by ranges, which walks.  One pair on 19 ranges 58.9 us by pairs and
 // 65.0 by ranges (50,000 tokens), 20.3 and 23.9 (4096), four 14.1 and 15.1; 16
 // pairs on 19 ranges 26.4 and 22.9: by pairs where there are two ranges a pair.
+// A pair then has many records, and eight are requested at a time (one KV head,
+// 50,000 tokens: four 28.2 us, eight 24.8); by ranges it has two or three, and
+// the CTAs are small enough to be there all at once (64 of up to 2048 tokens,
+// three CTAs an SM 62.6 us, five 61.0).
 __host__ __device__ __forceinline__ bool tr_merge_pairs(const TreeParams& p) {
     return (int64_t)p.num_seqs * (p.num_kv_heads / p.heads) * 2 < p.ctas;
 }
@@ -1040,13 +1044,14 @@ struct TrJoin {
 };
 
 // By a warp.
+template <bool kPairs>
 __device__ __forceinline__ TrJoin tree_join(const TreeParams& p, int side, int head) {
     TrWalk<true> walk;
     const TrDeal deal(p, walk.count(p, false));
     TrPiece P;
     unsigned begin = 0, each = 0;
     bool join;
-    if (tr_merge_pairs(p)) {
+    if (kPairs) {
         const int per_seq = p.num_kv_heads / p.heads;
         P.b = blockIdx.x / per_seq;
         P.s = tree_sequence<true>(p, P.b, false);
@@ -1065,12 +1070,12 @@ __device__ __forceinline__ TrJoin tree_join(const TreeParams& p, int side, int h
     // from the lane that has the first tile to the one that has the last
     x.c0 = deal.cta_of(begin + kTrPairWeight), x.c1 = deal.cta_of(begin + each - 1);
     x.q0 = P.s.q0, x.g = P.g;
-    if (x.c1 > x.c0 && (tr_merge_pairs(p) || x.c0 == blockIdx.x)) x.C = P.s.C;
+    if (x.c1 > x.c0 && (kPairs || x.c0 == blockIdx.x)) x.C = P.s.C;
     return x;
 }
 
-template <typename T, int D, bool kFp8>
-__global__ void __launch_bounds__(kTrMergeThreads)
+template <typename T, int D, bool kFp8, bool kPairs>
+__global__ void __launch_bounds__(kTrMergeThreads, kPairs ? 2 : 5)
     tree_merge_kernel(const __grid_constant__ TreeParams p) {
     allow_dependent_launch();
     const int head = blockIdx.y % p.heads, side = blockIdx.y / p.heads;
@@ -1083,18 +1088,21 @@ __global__ void __launch_bounds__(kTrMergeThreads)
     // same few lines of the L2
     __shared__ TrJoin found;
     if (threadIdx.x < 32) {
-        const TrJoin x = tree_join(p, side, head);
+        const TrJoin x = tree_join<kPairs>(p, side, head);
         if (threadIdx.x == 0) found = x;
     }
     __syncthreads();
     const TrJoin J = found;
+    // whoever has nothing to join makes room, but the grid is not over before
+    // the attention kernel is: its first CTA waits
+    if (J.C == 0 && (blockIdx.x | blockIdx.y | blockIdx.z) != 0) return;
     grid_dependency_wait();
     const int G = p.group, per_tile = tr_nodes_per_tile(G);
     const int in_tile = r / G, node = (kTrSlots * side + slot) * per_tile + in_tile;
     if (in_tile >= per_tile || node >= J.C) return;
     const unsigned c0 = J.c0, c1 = J.c1;
     float m = -INFINITY, l = 0.f, o[kTrMergeDims] = {};
-    constexpr int kAhead = 4;
+    constexpr int kAhead = kPairs ? 8 : 2;
     for (unsigned c = c0; c <= c1; c += kAhead) {
         float2 ml[kAhead];
         float4 v[kAhead][2];
@@ -1167,8 +1175,9 @@ cudaError_t launch_tree_t(const CUtensorMap& tmk, const CUtensorMap& tmv, const 
     const int per_tile = kTrRows / p.group;
     const int rows = p.max_query > per_tile ? kTrSlots * kTrRows : (p.max_query * p.group + 31) / 32 * 32;
     const int chunks = (rows / 32 * (D / kTrMergeDims) + kTrMergeThreads / 32 - 1) / (kTrMergeThreads / 32);
-    return launch_with_pdl(tree_merge_kernel<T, D, kFp8>,
-                           dim3((unsigned)(tr_merge_pairs(p) ? p.num_seqs * (p.num_kv_heads / p.heads) : p.ctas - 1),
+    const bool pairs = tr_merge_pairs(p);
+    return launch_with_pdl(pairs ? tree_merge_kernel<T, D, kFp8, true> : tree_merge_kernel<T, D, kFp8, false>,
+                           dim3((unsigned)(pairs ? p.num_seqs * (p.num_kv_heads / p.heads) : p.ctas - 1),
                                 (unsigned)(p.heads * p.sides), (unsigned)chunks),
                            dim3(kTrMergeThreads), 0, stream, p);
 }
