@@ -28,29 +28,45 @@
 // A tile passes from products to softmax, to products and back in some 1900
 // cycles beside the work itself, so a slot needs two tiles under way: with one
 // S of 128 keys per slot 8 heads x 4 sequences of 32k to 50k tokens at 240 rows
-// took 190 us (134 with no softmax and half of P V), with one of 64 keys 227.
+// took 190 us, with one of 64 keys 227, with two of 64 keys 168 (now 156).
+// Rows that leave half of the tile empty stay so: twice the same 64 rows, the
+// lower with one part of P and the upper with the other, take half of the P V
+// products, but put softmax warps beside the issuers (32 sequences over an
+// E4M3 cache below 95 us, so 85).
 //
 // The CTAs side by side, one for each 256 rows and KV head (or so many KV
 // heads as divide the SMs well), make a lane.  The key tiles of all sequences,
 // in order, are dealt out to the lanes in equal ranges, or, where contexts are
 // short, whole pairs are.  KV heads walk along together because their rows are
 // neighbours in memory (4 x 32k to 50k tokens, 8 heads, without the softmax
-// 130 us, with a range of its own for each head 122).  A pair that
-// more than one lane meets leaves records (O, m, sum), joined by a second
-// kernel.  K and V come once from HBM, 512 B a token and KV head at D 128;
-// the products cost 6 D operations (P in two parts) for each row and token.
+// 122 us, with a range of its own for each head 130).  A pair that more than
+// one lane meets leaves records (O, m, sum), joined by a second kernel.
+//
+// What bounds it: K and V come once from HBM, 512 B a token and KV head at
+// D 128 in 16 bits, and the products cost 6 D operations (P in two parts) for
+// each row and token: to some 190 rows a KV head the bytes are the longer,
+// above them the products.  Measured, back to back:
+//   64 x 128 .. 2048 tokens, 64 rows, 8 KV heads    60.5 us   301 MB, 5.0 TB/s
+//   16 x 2k .. 8k, 512 rows                          165 us   tensor pipe 78 %
+//   4 x 32k .. 50k, 240 rows                         156 us   tensor pipe 82 %
+//   32 x 4096, E4M3, 64 rows                          85 us   277 MB, 3.3 TB/s
+// Of the first some 8 us pass until the first scores are there and 4 between
+// the last output and the join's end; its loads alone took 49.  The last has
+// 54 % of the tensor pipe and 43 % of the issue slots: without its softmax 69.
 //
 // An E4M3 cache's codes are brought to the 16-bit type (exactly) by four
-// warps between the loaders' ring and the operands'.
+// warps between the loaders' ring and the operands' (no conversion at all would
+// leave the time as it is).
 //
-// Warps: 0 loads K tiles and 2 V tiles, 1 and 3 issue the slots' S, 13 and 14
+// Warps: 0 loads K tiles and 2 V tiles, 1 and 3 issue the slots' S, 14 and 15
 // their P V, 4 .. 7 are slot 0's softmax and 8 .. 11 slot 1's, 12 makes the
-// trees' lines, 16 .. 19 convert codes.  (An issuer takes some 1200 cycles
-// for a tile's S beside these warps, so one for both slots would hold them up.)  A barrier's parity tells a phase from the one before it
-// alone, so whoever waits for a phase has seen that the one before is over: by
-// waiting for every phase in turn, or as the comments at the waits say.
-#include <algorithm>
-
+// trees' lines, 16 .. 19 convert codes.  An issuer takes some 1200 cycles for a
+// tile's S beside these warps, so one for both slots would hold them up, and
+// which scheduler it shares with whom counts (S of both slots by 2 and 3, or
+// P V by 12 and 13: 160 to 165 us for the third case).  A barrier's parity
+// tells a phase from the one before it alone, so whoever waits for a phase has
+// seen that the one before is over: by waiting for every phase in turn, or as
+// the comments at the waits say.
 #include "decode_tile.cuh"
 #include "tc_device.cuh"
 #include "tree_device.cuh"
@@ -63,7 +79,8 @@ constexpr int kTrSlots = 2;
 constexpr int kTrQStages = 2;
 constexpr int kTrSoftmaxWarps = 4 * kTrSlots;
 constexpr int kTrLineWarp = 4 + kTrSoftmaxWarps;
-constexpr int kTrConvertWarp = 4 + kTrLineWarp;
+constexpr int kTrValueWarp = kTrLineWarp + 2;  // issuers of P V
+constexpr int kTrConvertWarp = kTrValueWarp + kTrSlots;
 constexpr int kTrConverters = 4;               // E4M3 only
 __host__ __device__ constexpr int tr_threads(bool fp8) { return (kTrConvertWarp + (fp8 ? kTrConverters : 0)) * 32; }
 // Registers: 512 threads are launched with 128 each (640 with 96); the softmax
@@ -73,10 +90,19 @@ __host__ __device__ constexpr int tr_softmax_regs(bool fp8) { return fp8 ? 128 :
 static_assert(256 * tr_softmax_regs(false) + 256 * kTrControlRegs <= 512 * 128 &&
               256 * tr_softmax_regs(true) + 384 * kTrControlRegs <= 640 * 96, "registers of the CTA");
 constexpr int kTrCtas = 152;                   // one per SM
-constexpr int kTrMinTiles = 8;                 // weight of a CTA's range at least, where there are records
-constexpr int kTrWholeTiles = 8;               // longest contexts, in tiles, whose pairs stay whole
+// A lane's range weighs that much at least, so that not every lane has a record
+// of the same few tiles (one KV head, 50,000 tokens: 4 took 51 us, 6 33, 8 28).
+constexpr int kTrMinTiles = 8;
+// The longest contexts, in tiles, whose pairs stay whole: no records, but uneven
+// lanes (16 x 300 .. 512 tokens: whole 12.4 us, dealt out 19.3; 64 x up to 2048:
+// whole 91 us, dealt out 61).
+constexpr int kTrWholeTiles = 8;
+// What a pair weighs beside its tiles (64 x 128 .. 2048 tokens: 2 took 77 us,
+// 4 73; 3 and 6 within 1 % of 4).
 constexpr int kTrPairWeight = kTreePairWeight;
-constexpr int kTrSoloTiles = 2;                // of a piece that one slot takes alone
+// The longest piece that one slot takes alone, while the other takes the next:
+// joining costs two barriers of the CTA, and V's ring has a stage more at least.
+constexpr int kTrSoloTiles = 2;
 
 // Shared memory: query tiles, operand tiles, codes.
 template <int D, bool kFp8>
@@ -603,12 +629,12 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                 if (lane == 0) mbar_arrive(&room.lines_full);
             }
             if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
-        } else if (warp <= kTrLineWarp + kTrSlots) {
+        } else if (warp >= kTrValueWarp) {
             // --------------------------------------------------------------
             // issuers of P V
             // --------------------------------------------------------------
             constexpr uint32_t kId = idesc_f16(kTrRows, D, kBf16, true);
-            const int slot = warp - kTrLineWarp - 1;
+            const int slot = warp - kTrValueWarp;
             const uint64_t dv = smem_desc_sw128(smem_u32(smem + Lay::kV), Lay::kHalf, 1024);
             const uint32_t o = tmem + kTrO + D * slot, p0 = tmem + kTrS + 2 * kTrKeys * slot;
             TrRing<Lay::kVStages> at;
