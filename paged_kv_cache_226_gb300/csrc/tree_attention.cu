@@ -28,7 +28,7 @@
 // A tile passes from products to softmax, to products and back in some 1900
 // cycles beside the work itself, so a slot needs two tiles under way: with one
 // S of 128 keys per slot 8 heads x 4 sequences of 32k to 50k tokens at 240 rows
-// took 190 us, with one of 64 keys 227, with two of 64 keys 168 (now 156).
+// took 190 us, with one of 64 keys 227, with two of 64 keys 186 (now 156).
 // Rows that leave half of the tile empty stay so: twice the same 64 rows, the
 // lower with one part of P and the upper with the other, take half of the P V
 // products, but put softmax warps beside the issuers (32 sequences over an
@@ -38,7 +38,7 @@
 // heads as divide the SMs well), make a lane.  The key tiles of all sequences,
 // in order, are dealt out to the lanes in equal ranges, or, where contexts are
 // short, whole pairs are.  KV heads walk along together because their rows are
-// neighbours in memory (4 x 32k to 50k tokens, 8 heads, without the softmax
+// neighbours in memory (4 x 32k to 50k tokens, 8 heads, without the products
 // 122 us, with a range of its own for each head 130).  A pair that more than
 // one lane meets leaves records (O, m, sum), joined by a second kernel.
 //
