@@ -586,3 +586,46 @@ def test_commit_bad_paths_are_left_alone(dev):
         lib.commit_path([k, v], [v, k[:1]], *args, n.to(dev))
     with pytest.raises(TypeError):
         lib.commit_path(k, v, *args[:3], path.long().to(dev), n.to(dev))
+
+
+def test_empty_batches(dev):
+    """No sequences, or no tokens, in every call of the step."""
+    kc = torch.zeros(4, 16, 2, 64, dtype=torch.float16, device=dev)
+    none = torch.zeros(0, dtype=torch.int32, device=dev)
+    start, tables = torch.zeros(1, dtype=torch.int32, device=dev), torch.zeros(0, 3, dtype=torch.int32, device=dev)
+    rows = torch.zeros(0, 4, 64, dtype=torch.float16, device=dev)
+    out = lib.tree_attention(rows, kc, kc, tables, none, start, none, 0.1, 4, 48)
+    assert out.shape == rows.shape
+    path, lens, following = lib.accept_tree(none.long(), none.long(), none, start, 4)
+    assert path.shape == (0, 4) and lens.shape == (0,) and following.shape == (0,)
+    assert path.dtype == lens.dtype == torch.int32 and following.dtype == torch.int64
+    assert lib.commit_path(kc, kc.clone(), tables, none, start, path, lens).shape == (0,)
+    q = lib.norm_rope_and_cache(rows, rows[:, :2], rows[:, :2], none.long(), none.long(), torch.ones(32, device=dev), kc, kc)
+    assert q.shape == rows.shape
+    # sequences, but no nodes: nothing is accepted and nothing moves
+    two = torch.tensor([0, 0, 0], dtype=torch.int32, device=dev)
+    held, tables = torch.tensor([20, 0], dtype=torch.int32, device=dev), torch.zeros(2, 3, dtype=torch.int32, device=dev)
+    path, lens, following = lib.accept_tree(none.long(), none.long(), None, two, 4)
+    assert path.tolist() == [[-1] * 4] * 2 and lens.tolist() == [0, 0] and following.tolist() == [-1, -1]
+    assert lib.commit_path(kc, kc.clone(), tables, held, two, path, lens).tolist() == [20, 0]
+    assert lib.tree_attention(rows, kc, kc, tables, held, two, None, 0.1, 4, 48).shape == rows.shape
+    assert bool((kc == 0).all()) and lib.read_device_errors(dev) == 0
+
+
+def test_acceptance_results_are_ordinary_tensors(dev):
+    """Three parts of one allocation: each can be written, kept and computed with by itself."""
+    nodes = [5, 3]
+    draft, target = torch.arange(8, device=dev), torch.arange(8, device=dev) + 1
+    parents = torch.tensor([-1, 0, 1, 2, 3, -1, 0, 1], dtype=torch.int32, device=dev)
+    path, lens, following = lib.accept_tree(draft, target, parents, starts(nodes).to(dev), 5)
+    assert lens.tolist() == [5, 3] and following.tolist() == [5, 8]
+    kept = following.clone()
+    path.fill_(7)
+    lens += 1
+    assert following.tolist() == kept.tolist() and lens.tolist() == [6, 4] and path.sum().item() == 70
+    w = torch.ones(2, device=dev, requires_grad=True)
+    (w * lens).sum().backward()
+    assert w.grad.tolist() == [6.0, 4.0]
+    with torch.inference_mode():
+        again, _, _ = lib.accept_tree(draft, target, parents, starts(nodes).to(dev), 5)
+    assert again.tolist() == [[0, 1, 2, 3, 4], [0, 1, 2, -1, -1]]
