@@ -634,7 +634,8 @@ int pa_norm_rope_and_cache_fp8(const void* q, int64_t q_stride, const void* k, i
  * V that it does see makes these elements of its row infinite or NaN.
  * workspace: device memory of at least pa_tree_attention_workspace_size bytes,
  * 16-byte aligned, no initial contents; calls that overlap on the GPU must
- * not share it.  One or two launches.
+ * not share it.  What is enough for a batch is enough for fewer sequences and
+ * shorter contexts of the same heads and max_query_len.  One or two launches.
  */
 size_t pa_tree_attention_workspace_size(const pa_shape* shp, int32_t max_query_len,
                                         int32_t max_context_len);

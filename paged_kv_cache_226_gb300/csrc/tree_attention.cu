@@ -95,9 +95,12 @@ constexpr int kTrCtas = 152;                   // one per SM
 // of the same few tiles (one KV head, 50,000 tokens: 4 took 51 us, 6 33, 8 28).
 constexpr int kTrMinTiles = 8;
 // The longest contexts, in tiles, whose pairs stay whole: no records, but uneven
-// lanes (16 x 300 .. 512 tokens: whole 12.4 us, dealt out 19.3; 64 x up to 2048:
-// whole 91 us, dealt out 61).
-constexpr int kTrWholeTiles = 8;
+// lanes (16 x 300 .. 512 tokens: whole 12.4 us, dealt out 18.1; 64 x up to 1000:
+// whole 52.8 us, dealt out 46.0; up to 2048: 91 and 61).  Where most lanes have
+// a pair each and none has two, longer ones do too (16 x 800 .. 1000 tokens:
+// whole 18.7 us, dealt out 22.9; 20 pairs on the 19 lanes 30.0 and 25.1, one
+// pair of 760 tokens 19.9 and 17.8).
+constexpr int kTrWholeTiles = 8, kTrWholeTilesAlone = 16;
 // What a pair weighs beside its tiles (64 x 128 .. 2048 tokens: 2 took 77 us,
 // 4 73; 3 and 6 within 1 % of 4).
 constexpr int kTrPairWeight = kTreePairWeight;
@@ -1190,12 +1193,14 @@ size_t tree_plan(TreeParams& p, int head_dim, void* workspace) {
     p.heads = 1;
     for (int d = 2; d <= p.num_kv_heads && d * p.sides <= kTrCtas; ++d)
         if (p.num_kv_heads % d == 0 && kTrCtas / (d * p.sides) * (d * p.sides) * 25 >= kTrCtas * 24) p.heads = d;
-    p.whole = tiles <= kTrWholeTiles;
-    const int64_t pairs = (int64_t)p.num_seqs * (p.num_kv_heads / p.heads);       // of a lane's CTA
-    const int64_t most = p.whole ? pairs : (pairs * (tiles + kTrPairWeight) + kTrMinTiles - 1) / kTrMinTiles;
     const int lanes = kTrCtas / (p.heads * p.sides);
-    p.ctas = (int)(most < lanes ? (most > 0 ? most : 1) : lanes);
-    const size_t rows = p.whole ? 0 : (size_t)p.ctas * p.heads * p.sides * 2 * kTrSlots * kTrRows;
+    const int64_t pairs = (int64_t)p.num_seqs * (p.num_kv_heads / p.heads);       // of a lane's CTA
+    p.whole = tiles <= (pairs <= lanes && 2 * pairs > lanes ? kTrWholeTilesAlone : kTrWholeTiles);
+    auto of_lanes = [&](int64_t most) { return (int)(most < lanes ? (most > 0 ? most : 1) : lanes); };
+    const int dealt = of_lanes((pairs * (tiles + kTrPairWeight) + kTrMinTiles - 1) / kTrMinTiles);
+    p.ctas = p.whole ? of_lanes(pairs) : dealt;
+    // as if dealt out: what is enough for a batch is enough with fewer sequences
+    const size_t rows = tiles <= kTrWholeTiles ? 0 : (size_t)dealt * p.heads * p.sides * 2 * kTrSlots * kTrRows;
     p.rec_o = static_cast<float*>(workspace);
     p.rec_ml = reinterpret_cast<float2*>(p.rec_o + rows * head_dim);
     return rows * (head_dim * sizeof(float) + sizeof(float2)) + 16;

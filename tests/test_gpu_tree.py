@@ -263,6 +263,15 @@ def test_tree_ranges_that_meet_in_pairs(dev, lens, nodes, hq, hkv, d, fp8):
     check_tree(dev, lens, nodes, hq, hkv, d, 16, torch.bfloat16, fp8=fp8, seed=hkv, behind=2)
 
 
+@pytest.mark.parametrize("seqs,hq,hkv,d,longest", [(16, 8, 8, 64, 1024), (16, 8, 8, 64, 1025), (10, 8, 8, 128, 1000),
+                                                   (9, 8, 8, 128, 1000), (20, 16, 8, 64, 1000), (8, 16, 2, 128, 700)])
+def test_tree_lanes_with_a_pair_each(dev, seqs, hq, hkv, d, longest):
+    """As many pairs as there are lanes, some fewer and some more, of up to 16 key tiles and one more."""
+    lens = [longest - 97 * i % 600 for i in range(seqs)]
+    nodes = [1 + 11 * i % 60 for i in range(seqs)]
+    check_tree(dev, lens, nodes, hq, hkv, d, 16, torch.float16, seed=seqs)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_tree_shared_and_repeated_blocks(dev, fp8):
     """Sequences with the same context, and a context that has one block over and over."""

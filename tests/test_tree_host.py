@@ -95,6 +95,21 @@ def test_tree_sizes_and_overlaps(pa):
     assert n > 0 and tree(pa, big, n=n, max_ctx=1 << 30) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("heads,kv_heads,nodes", [(8, 8, 16), (64, 8, 64), (16, 2, 128), (32, 32, 8), (5, 5, 3)])
+def test_tree_workspace_grows_with_the_batch(pa, heads, kv_heads, nodes):
+    """What is enough for a batch is enough for fewer sequences or shorter contexts."""
+    for blocks in (1, 8, 32, 33, 48, 64, 65, 500):
+        sizes = [pa.pa_tree_attention_workspace_size(
+            shape(num_seqs=n, num_q_heads=heads, num_kv_heads=kv_heads, block_size=16, max_blocks_per_seq=blocks),
+            nodes, 16 * blocks) for n in range(40)]
+        assert sizes == sorted(sizes) and sizes[0] >= 16
+    for n in (1, 9, 16, 40):
+        sizes = [pa.pa_tree_attention_workspace_size(
+            shape(num_seqs=n, num_q_heads=heads, num_kv_heads=kv_heads, block_size=16, max_blocks_per_seq=500),
+            nodes, longest) for longest in range(0, 8000, 61)]
+        assert sizes == sorted(sizes)
+
+
 def test_commit_refuses_caches_over_one_another(pa):
     size, at = 16 * 16 * 2 * 128 * 2, 1 << 24
     for off in (16, size - 16):
