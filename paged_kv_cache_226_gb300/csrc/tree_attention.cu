@@ -113,6 +113,9 @@ template <int D, bool kFp8>
 struct TrLayout {
     static constexpr int kKStages = kFp8 ? 3 : 5, kVStages = kFp8 ? 3 : 5;
     static constexpr int kCodeStages = kFp8 ? 4 : 0;          // of K and of V each
+    // barriers that say an operand stage is free again: over E4M3 two a stage,
+    // for every other use (the converters' comment says why)
+    static constexpr int kKEmpties = kFp8 ? 2 * kKStages : kKStages, kVEmpties = kFp8 ? 2 * kVStages : kVStages;
     static constexpr int kHalves = D / kBoxElems;
     static constexpr int kHalf = kTrKeys * 128;               // 64 dims of 64 rows
     static constexpr int kTile = kHalves * kHalf;
@@ -135,7 +138,7 @@ struct TrRoom {
         uint4 line[PA_TREE_NODES];             // a piece's lines, until they are read
         float2 ml[kTrSlots][kTrRows];          // the slots' statistics, at a joined piece's end
     };
-    uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
+    uint64_t k_full[5], k_empty[6], v_full[5], v_empty[6];
     uint64_t kc_full[4], kc_empty[4], vc_full[4], vc_empty[4];
     uint64_t q_full[kTrQStages], q_empty[kTrQStages], lines_full, lines_empty;
     uint64_t s_full[kTrSlots][2], p_full[kTrSlots][2], o_done[kTrSlots][2], done[2 * kTrSlots];
@@ -434,8 +437,10 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
     const int G = p.group, per_tile = tr_nodes_per_tile(G);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < Lay::kKStages; ++i) mbar_init(&room.k_full[i], 1), mbar_init(&room.k_empty[i], kTrSlots);
-        for (int i = 0; i < Lay::kVStages; ++i) mbar_init(&room.v_full[i], 1), mbar_init(&room.v_empty[i], kTrSlots);
+        for (int i = 0; i < Lay::kKStages; ++i) mbar_init(&room.k_full[i], 1);
+        for (int i = 0; i < Lay::kVStages; ++i) mbar_init(&room.v_full[i], 1);
+        for (int i = 0; i < Lay::kKEmpties; ++i) mbar_init(&room.k_empty[i], kTrSlots);
+        for (int i = 0; i < Lay::kVEmpties; ++i) mbar_init(&room.v_empty[i], kTrSlots);
         for (int i = 0; i < Lay::kCodeStages; ++i) {
             mbar_init(&room.kc_full[i], 1), mbar_init(&room.kc_empty[i], 1);
             mbar_init(&room.vc_full[i], 1), mbar_init(&room.vc_empty[i], 1);
@@ -556,6 +561,7 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
             const uint64_t dk = smem_desc_sw128(smem_u32(smem + Lay::kK), 16, 1024);
             const uint32_t s0 = tmem + kTrS + 2 * kTrKeys * slot;
             TrRing<Lay::kKStages> at;
+            TrRing<Lay::kKEmpties> back;
             TrRing<kTrQStages> q;
             int t = 0;
             bool ok = true;
@@ -564,7 +570,7 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                 const int q0 = q.at;
                 for (int i = 0; i < P.query_tiles(); ++i, q.step()) wait(&room.q_full[q.at], q.lap);
                 const uint64_t query = dq + (P.share ? q0 ^ slot : q0) * (Lay::kQTile >> 4);
-                for (int k = P.k0; ok && k < P.k1; ++k, at.step()) {
+                for (int k = P.k0; ok && k < P.k1; ++k, at.step(), back.step()) {
                     wait(&room.k_full[at.at], at.lap);
                     if (P.has(slot, k)) {
                         const int buf = t & 1;
@@ -579,10 +585,10 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                                 mma_f16_ss(s0 + kTrKeys * buf, query + (kk >> 2) * (Lay::kQHalf >> 4) + (kk & 3) * 2,
                                            key + (kk >> 2) * (Lay::kHalf >> 4) + (kk & 3) * 2, kId, kk > 0);
                             mma_commit(&room.s_full[slot][buf]);
-                            mma_commit(&room.k_empty[at.at]);
+                            mma_commit(&room.k_empty[back.at]);
                         }
                     } else if (ok && elect_one()) {
-                        mbar_arrive(&room.k_empty[at.at]);
+                        mbar_arrive(&room.k_empty[back.at]);
                     }
                     __syncwarp();
                 }
@@ -642,11 +648,12 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
             const uint64_t dv = smem_desc_sw128(smem_u32(smem + Lay::kV), Lay::kHalf, 1024);
             const uint32_t o = tmem + kTrO + D * slot, p0 = tmem + kTrS + 2 * kTrKeys * slot;
             TrRing<Lay::kVStages> at;
+            TrRing<Lay::kVEmpties> back;
             int t = 0;
             bool ok = true;
             auto wait = [&](uint64_t* bar, int phase) { ok = ok && tr_wait(p, bar, phase); };
             while (ok && walk.next(p, side, head, P)) {
-                for (int k = P.k0; ok && k < P.k1; ++k, at.step()) {
+                for (int k = P.k0; ok && k < P.k1; ++k, at.step(), back.step()) {
                     wait(&room.v_full[at.at], at.lap);
                     if (P.has(slot, k)) {
                         const int buf = t & 1;
@@ -667,10 +674,10 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                                                !first || kk > 0 || part > 0);
                             }
                             mma_commit(&room.o_done[slot][buf]);
-                            mma_commit(&room.v_empty[at.at]);
+                            mma_commit(&room.v_empty[back.at]);
                         }
                     } else if (ok && elect_one()) {
-                        mbar_arrive(&room.v_empty[at.at]);
+                        mbar_arrive(&room.v_empty[back.at]);
                     }
                     __syncwarp();
                 }
@@ -689,15 +696,18 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
             // rows; lanes are laid out so that eight neighbours read and write
             // different banks: four chunks of a row beside the other four of
             // the next.
-            // Each warp sees every other use of a stage.  The use before of the
-            // operands' stage, three tiles back, is given back at this wait;
-            // that the one before that was is known from this warp's wait a
-            // tile of its own back, for the products five tiles back.  They
-            // also say that every tile up to three back is converted, and so
-            // that the use before of the codes' stage, four tiles back, is over.
+            // Each warp sees every other use of an operand stage only, and the
+            // slots give a stage back in no order (whoever took no part in it
+            // at once, beside products under way): one barrier a stage could
+            // have two phases open that a parity does not tell apart.  So tile
+            // n comes back on barrier n modulo twice the stages, whose tiles
+            // are all one warp's: tile n waits for tile n - S on barrier
+            // (n + S) mod 2 S, each of its phases in turn, and the next of them,
+            // for tile n + S, needs tile n converted.  A stage of codes, their
+            // number being even, is one warp's too.
             // --------------------------------------------------------------
-            static_assert(kTrConverters == 4 && Lay::kKStages == 3 && Lay::kVStages == 3 && Lay::kCodeStages >= 4,
-                          "see above");
+            static_assert(kTrConverters == 4 && Lay::kCodeStages % 2 == 0 && Lay::kKStages == Lay::kVStages &&
+                          Lay::kKEmpties == 2 * Lay::kKStages && Lay::kVEmpties == 2 * Lay::kVStages, "see above");
             const int who = warp - kTrConvertWarp;
             const bool keys = (who & 1) == 0;
             const int c = lane & 7, upper = c >> 2;
@@ -706,18 +716,22 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
             uint64_t* const codes_empty = keys ? room.kc_empty : room.vc_empty;
             uint64_t* const full = keys ? room.k_full : room.v_full;
             uint64_t* const empty = keys ? room.k_empty : room.v_empty;
-            const int stages = keys ? Lay::kKStages : Lay::kVStages;
+            constexpr int kStages = Lay::kKStages;
             // bits of the row's number that the swizzles use are those of r4,
             // and of pass & 1 for the next four rows
             const uint8_t* const src0 = smem + (keys ? Lay::kKCodes : Lay::kVCodes) + r4 * 128;
             uint8_t* const dst0 = smem + (keys ? Lay::kK : Lay::kV) + upper * Lay::kHalf + r4 * 128;
-            int n = 0, st = 0, lap = 0;
+            int n = 0;
+            TrRing<2 * kStages> to;
             TrRing<Lay::kCodeStages> at;
             bool ok = true;
             while (ok && walk.next(p, side, head, P)) {
-                for (int k = P.k0; ok && k < P.k1; ++k, ++n, at.step()) {
+                for (int k = P.k0; ok && k < P.k1; ++k, ++n, at.step(), to.step()) {
                     if ((n & 1) == (who >> 1)) {
-                        if (lap > 0) ok = tr_wait(p, &empty[st], lap - 1);
+                        const bool upper_lap = to.at >= kStages;
+                        const int st = upper_lap ? to.at - kStages : to.at;
+                        if (upper_lap || to.lap > 0)
+                            ok = tr_wait(p, &empty[upper_lap ? st : st + kStages], upper_lap ? to.lap : to.lap - 1);
                         if (ok) ok = tr_wait(p, &codes_full[at.at], at.lap);
                         if (!ok) break;
                         const uint8_t* src = src0 + at.at * Lay::kCodes;
@@ -768,7 +782,6 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                             mbar_arrive(&codes_empty[at.at]);
                         }
                     }
-                    if (++st == stages) st = 0, ++lap;
                 }
             }
             if (!ok && lane == 0) flag_error(p.err, PA_DEVERR_WAIT_TIMEOUT);
