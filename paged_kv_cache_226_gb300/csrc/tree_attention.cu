@@ -105,7 +105,7 @@ constexpr int kTrWholeTiles = 8, kTrWholeTilesAlone = 16;
 // 4 73; 3 and 6 within 1 % of 4).
 constexpr int kTrPairWeight = kTreePairWeight;
 // The longest piece that one slot takes alone, while the other takes the next:
-// joining costs two barriers of the CTA, and V's ring has a stage more at least.
+// joining costs two barriers of the CTA.
 constexpr int kTrSoloTiles = 2;
 
 // Shared memory: query tiles, operand tiles, codes.
@@ -141,7 +141,7 @@ struct TrRoom {
     uint64_t k_full[5], k_empty[6], v_full[5], v_empty[6];
     uint64_t kc_full[4], kc_empty[4], vc_full[4], vc_empty[4];
     uint64_t q_full[kTrQStages], q_empty[kTrQStages], lines_full, lines_empty;
-    uint64_t s_full[kTrSlots][2], p_full[kTrSlots][2], o_done[kTrSlots][2], done[2 * kTrSlots];
+    uint64_t s_full[kTrSlots][2], p_full[kTrSlots][2], o_done[kTrSlots][2], v_there[kTrSlots], done[2 * kTrSlots];
     uint32_t tmem;
 };
 
@@ -192,6 +192,10 @@ struct TrPiece {
     }
     __device__ __forceinline__ int query_tiles() const { return share ? 2 : 1; }
     __device__ __forceinline__ bool rows(int slot) const { return slot < query; }
+    // Whether key tile k has tokens of the tree, or ends behind it.
+    __device__ __forceinline__ bool masked(int k) const { return (k + 1) * kTrKeys > s.L - s.C; }
+    // The slot whose softmax warps clear V of such a tile.
+    __device__ __forceinline__ bool clears(int slot) const { return !share || slot == 0; }
     // Whether key tile k is the slot's first.
     __device__ __forceinline__ bool first(int slot, int k) const { return share || alone ? k == k0 : k - k0 == slot; }
 };
@@ -448,6 +452,7 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
         for (int i = 0; i < kTrQStages; ++i) mbar_init(&room.q_full[i], 1), mbar_init(&room.q_empty[i], kTrSlots);
         mbar_init(&room.lines_full, 1), mbar_init(&room.lines_empty, kTrSoftmaxWarps);
         for (int i = 0; i < kTrSlots; ++i) {
+            mbar_init(&room.v_there[i], 1);
             for (int j = 0; j < 2; ++j)
                 mbar_init(&room.s_full[i][j], 1), mbar_init(&room.p_full[i][j], 4), mbar_init(&room.o_done[i][j], 1);
         }
@@ -657,6 +662,8 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                     wait(&room.v_full[at.at], at.lap);
                     if (P.has(slot, k)) {
                         const int buf = t & 1;
+                        if (ok && P.masked(k) && P.clears(slot) && elect_one()) mbar_arrive(&room.v_there[slot]);
+                        __syncwarp();
                         wait(&room.p_full[slot][buf], t >> 1);
                         if (!ok) break;
                         ++t;
@@ -808,6 +815,7 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
             return (int64_t)(X.s.q0 + node_of(X)) * p.num_q_heads + X.g * G + in_group;
         };
         int n = 0, t = 0;                     // tiles of the CTA and of the slot so far
+        int cleared = 0;                      // of those, V's that this slot has cleared
         for (int piece = 0; walk.next(p, side, head, P); ++piece) {
             const int base = P.s.L - P.s.C;
             const int count = P.k1 - P.k0, own = P.own(slot);
@@ -839,7 +847,7 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
             for (int k = P.k0, j = 0; k < P.k1; ++k) {
                 if (!P.has(slot, k)) continue;
                 const int key0 = k * kTrKeys;
-                const bool masked = key0 + kTrKeys > base;
+                const bool masked = P.masked(k);
                 if (masked && !taken) take_line();
                 const uint32_t tS = tmem + kTrS + kTrKeys * (2 * slot + (t & 1)) + lanes_at;
                 wait(&room.s_full[slot][t & 1], t >> 1);
@@ -924,15 +932,16 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                     // Of the tree's, elements that are not finite are cleared
                     // too, since the tensor cores would carry them into rows
                     // that do not see them; rows that do get them back below.
-                    // Thread r has half r / 64 of key r % 64.  The phase before
-                    // of V's barrier is over once this slot's P V before is done:
-                    // that was at most three tiles back (kTrSoloTiles), and the
-                    // rings have three stages at least.
+                    // Thread r has half r / 64 of key r % 64.  That the tile is
+                    // there its issuer of P V says, which waits for every phase
+                    // of V's barriers in turn: this slot's tile before may be
+                    // five back (the last but one of a piece, two that the
+                    // other slot took alone, the first of this one), so a
+                    // parity alone could be that of an earlier tile.
                     bool odd = false;
-                    if (!P.share || slot == 0) {
-                        static_assert(Lay::kVStages > kTrSoloTiles, "a phase could be taken for another");
+                    if (P.clears(slot)) {
                         const int tile = n + (k - P.k0), vs = tile % Lay::kVStages;
-                        if (t > 0) wait(&room.o_done[slot][(t - 1) & 1], (t - 1) >> 1);
+                        wait(&room.v_there[slot], cleared++);
                         wait(&room.v_full[vs], tile / Lay::kVStages);
                         const int key = key0 + (r & 63);
                         uint8_t* vd = smem + Lay::kV + vs * Lay::kTile + (D == 128 ? (r >> 6) * Lay::kHalf : 0) + (r & 63) * 128;
