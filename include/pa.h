@@ -629,7 +629,9 @@ int pa_norm_rope_and_cache_fp8(const void* q, int64_t q_stride, const void* k, i
  * over all sequences and KV heads, four added to each, are PA_ERR_UNSUPPORTED.
  * Softmax statistics and sums are in fp32; p meets V in two parts of the
  * 16-bit type, which hold it to 2^-15 (bf16) or 2^-22 (fp16; and to 2^-31 of
- * the row's largest), and out is rounded once.  A token that a node does not
+ * the row's largest).  The tensor cores cut sums off toward zero, for up to 128
+ * key tiles before a rounding add: at most 2^-13 of sum_j p_j |V_j| (measured
+ * 5e-5), at any context length.  out is rounded once.  A token that a node does not
  * see has no part in its row, also where its K or V is not finite; an infinite
  * V that it does see makes these elements of its row infinite or NaN.
  * workspace: device memory of at least pa_tree_attention_workspace_size bytes,

@@ -107,6 +107,15 @@ constexpr int kTrPairWeight = kTreePairWeight;
 // The longest piece that one slot takes alone, while the other takes the next:
 // joining costs two barriers of the CTA.
 constexpr int kTrSoloTiles = 2;
+// Tiles of a slot whose products add up in tensor memory.  The tensor cores cut
+// each sum off toward zero, eight times a tile, which takes some 4e-7 of O a
+// tile (0.4 % after 10,000); after so many tiles O is added, rounded, to what
+// the softmax warps hold in the workspace and begins anew, so that it loses
+// 5e-5, a fifth of fp16's smallest rounding error, however long the context.
+// 4 x 32k to 50k tokens, some 135 tiles a CTA, in long runs: 64 190 us, 128
+// 186, 256 184, as without.
+constexpr int kTrRun = 128;
+static_assert(kTrRun >= kTrWholeTilesAlone, "whole pairs have no workspace");
 
 // Shared memory: query tiles, operand tiles, codes.
 template <int D, bool kFp8>
@@ -196,8 +205,6 @@ struct TrPiece {
     __device__ __forceinline__ bool masked(int k) const { return (k + 1) * kTrKeys > s.L - s.C; }
     // The slot whose softmax warps clear V of such a tile.
     __device__ __forceinline__ bool clears(int slot) const { return !share || slot == 0; }
-    // Whether key tile k is the slot's first.
-    __device__ __forceinline__ bool first(int slot, int k) const { return share || alone ? k == k0 : k - k0 == slot; }
 };
 
 // Nodes of a query tile.
@@ -658,6 +665,7 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
             bool ok = true;
             auto wait = [&](uint64_t* bar, int phase) { ok = ok && tr_wait(p, bar, phase); };
             while (ok && walk.next(p, side, head, P)) {
+                int j = 0;                                             // tiles of the slot
                 for (int k = P.k0; ok && k < P.k1; ++k, at.step(), back.step()) {
                     wait(&room.v_full[at.at], at.lap);
                     if (P.has(slot, k)) {
@@ -669,7 +677,7 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                         ++t;
                         tc_fence_after_sync();
                         const uint64_t value = dv + at.at * (Lay::kTile >> 4);
-                        const bool first = P.first(slot, k);
+                        const bool first = j++ % kTrRun == 0;
                         if (elect_one()) {
                             // keys 16 kk .. 16 kk + 15: hi parts in columns 16 kk ..
                             // 16 kk + 7, lo parts in the next eight
@@ -843,135 +851,173 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                 continue;
             }
             float m = -INFINITY, l = 0.f;
+            float held_m = -INFINITY, held_l = 0.f;                // of the runs before this one
             bool bad = false;                 // V of the tree has elements that are not finite
-            for (int k = P.k0, j = 0; k < P.k1; ++k) {
-                if (!P.has(slot, k)) continue;
-                const int key0 = k * kTrKeys;
-                const bool masked = P.masked(k);
-                if (masked && !taken) take_line();
-                const uint32_t tS = tmem + kTrS + kTrKeys * (2 * slot + (t & 1)) + lanes_at;
-                wait(&room.s_full[slot][t & 1], t >> 1);
-                tc_fence_after_sync();
-                if (live) {
-                    auto hide = [&](uint32_t(&v)[32], int c) {
-                        const uint32_t seen = seen_word(line, key0 + c - base);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = (seen >> e) & 1u ? v[e] : 0xff800000u;
-                    };
-                    // The row's maximum on the raw scores (the scale is positive),
-                    // then P, 32 keys at a time and each time from tensor memory:
-                    // held between the two they cost registers and, unrolled,
-                    // instruction cache (E4M3 96 us, so 93).
-                    float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            // this row's O of those runs, [D / 4][row][4] as in a record; the
+            // piece's own record is written when it has been read
+            float4* const held = reinterpret_cast<float4*>(p.rec_o) +
+                                 (((int64_t)blockIdx.x * 2 + (P.k0 > 0 ? 0 : 1)) * kTrSlots + slot) * (D / 4) * kTrRows + r;
+            // What is held in terms of the present reference.
+            auto held_scale = [&] { return held_m == m ? 1.f : ex2(held_m - m); };
+            const int run = P.share ? kTrRun : 2 * kTrRun;         // of keys: kTrRun tiles of the slot
+            const int skip = P.share || P.alone ? 0 : slot;        // to the slot's first tile
+            for (int k0 = P.k0; k0 + skip < P.k1; k0 += run) {
+                if (k0 > P.k0 && live) {
+                    // the run before: added to those before it
+                    wait(&room.o_done[slot][(t - 1) & 1], (t - 1) >> 1);
+                    tc_fence_after_sync();
+                    const float f = held_scale();
 #pragma unroll 1
-                    for (int c = 0; c < kTrKeys; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(tS + c, v);
-                        tmem_wait_ld(v);
-                        if (masked) hide(v, c);
+                    for (int d = 0; d < D; d += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + D * slot + d, o);
+                        tmem_wait_ld(o);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) pm[i] = fmaxf(pm[i], __uint_as_float(v[e + i]));
-                        }
-                    }
-                    const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * sl;
-                    const bool raise = mx > m + kRaise;            // the first finite maximum, too
-                    if (__any_sync(0xffffffffu, raise)) {
-                        const float m_new = raise ? mx - kBelow : m;
-                        const float f = raise ? ex2(m - m_new) : 1.f;
-                        l *= f;
-                        m = m_new;
-                        if (j > 0) {
-                            wait(&room.o_done[slot][(t - 1) & 1], (t - 1) >> 1);
-                            tc_fence_after_sync();
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t o[32];
-                                tmem_ld32(tO + D * slot + c, o);
-                                tmem_wait_ld(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st32(tO + D * slot + c, o);
+                        for (int q = 0; q < 8; ++q) {
+                            float4 x = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                                                   __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
+                            float4* at = held + (d / 4 + q) * kTrRows;
+                            if (k0 > P.k0 + run) {
+                                const float4 y = *at;
+                                x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y);
+                                x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
                             }
+                            *at = x;
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.f : m;    // nothing seen yet
-                    const uint64_t neg2 = f32x2_pack(-ref, -ref);
-                    uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll 1
-                    for (int c = 0; c < kTrKeys; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(tS + c, v);
-                        tmem_wait_ld(v);
-                        if (masked) hide(v, c);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t parts[16];                    // hi, then lo
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                float a0, a1;
-                                f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[16 * h + 2 * i]),
-                                                                  __uint_as_float(v[16 * h + 2 * i + 1])), sl2, neg2), a0, a1);
-                                const float p0 = ex2(a0), p1 = ex2(a1);
-                                ps[i & 3] = f32x2_add(ps[i & 3], f32x2_pack(p0, p1));
-                                split_pair<T>(p0, p1, parts[i], parts[8 + i]);
-                            }
-                            tmem_st16(tS + c + 16 * h, parts);
-                        }
-                    }
-                    float q8[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) f32x2_unpack(ps[e], q8[2 * e], q8[2 * e + 1]);
-                    l += ((q8[0] + q8[1]) + (q8[2] + q8[3])) + ((q8[4] + q8[5]) + (q8[6] + q8[7]));
-                    // the next tile's scores, where they are there already
-                    tmem_wait_st();
+                    held_l = fmaf(held_l, f, l), l = 0.f, held_m = m;
                 }
-                if (masked) {
-                    // V rows past the context may hold anything: clear them.
-                    // Of the tree's, elements that are not finite are cleared
-                    // too, since the tensor cores would carry them into rows
-                    // that do not see them; rows that do get them back below.
-                    // Thread r has half r / 64 of key r % 64.  That the tile is
-                    // there its issuer of P V says, which waits for every phase
-                    // of V's barriers in turn: this slot's tile before may be
-                    // five back (the last but one of a piece, two that the
-                    // other slot took alone, the first of this one), so a
-                    // parity alone could be that of an earlier tile.
-                    bool odd = false;
-                    if (P.clears(slot)) {
-                        const int tile = n + (k - P.k0), vs = tile % Lay::kVStages;
-                        wait(&room.v_there[slot], cleared++);
-                        wait(&room.v_full[vs], tile / Lay::kVStages);
-                        const int key = key0 + (r & 63);
-                        uint8_t* vd = smem + Lay::kV + vs * Lay::kTile + (D == 128 ? (r >> 6) * Lay::kHalf : 0) + (r & 63) * 128;
-                        if (D == 64 && r >= 64) {
-                        } else if (key >= P.s.L) {
+                for (int k = k0, j = 0; k < min(k0 + run, P.k1); ++k) {
+                    if (!P.has(slot, k)) continue;
+                    const int key0 = k * kTrKeys;
+                    const bool masked = P.masked(k);
+                    if (masked && !taken) take_line();
+                    const uint32_t tS = tmem + kTrS + kTrKeys * (2 * slot + (t & 1)) + lanes_at;
+                    wait(&room.s_full[slot][t & 1], t >> 1);
+                    tc_fence_after_sync();
+                    if (live) {
+                        auto hide = [&](uint32_t(&v)[32], int c) {
+                            const uint32_t seen = seen_word(line, key0 + c - base);
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vd + (((c ^ r) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                        } else if (key >= base) {
-                            uint32_t any = 0u;
+                            for (int e = 0; e < 32; ++e) v[e] = (seen >> e) & 1u ? v[e] : 0xff800000u;
+                        };
+                        // The row's maximum on the raw scores (the scale is positive),
+                        // then P, 32 keys at a time and each time from tensor memory:
+                        // held between the two they cost registers and, unrolled,
+                        // instruction cache (E4M3 96 us, so 93).
+                        float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                        for (int c = 0; c < kTrKeys; c += 32) {
+                            uint32_t v[32];
+                            tmem_ld32(tS + c, v);
+                            tmem_wait_ld(v);
+                            if (masked) hide(v, c);
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                const uint4 w = lds128(vd + (((c ^ r) & 7) << 4));
-                                any |= not_finite<T>(w.x) | not_finite<T>(w.y) | not_finite<T>(w.z) | not_finite<T>(w.w);
+                            for (int e = 0; e < 32; e += 4) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) pm[i] = fmaxf(pm[i], __uint_as_float(v[e + i]));
                             }
-                            if (any != 0u) {
-                                odd = true;
-                                for (int c = 0; c < 32; ++c) {
-                                    uint32_t* w = reinterpret_cast<uint32_t*>(vd) + c;
-                                    *w &= ~(((not_finite<T>(*w) >> 15) & 0x00010001u) * 0xffffu);
+                        }
+                        const float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * sl;
+                        const bool raise = mx > m + kRaise;            // the first finite maximum, too
+                        if (__any_sync(0xffffffffu, raise)) {
+                            const float m_new = raise ? mx - kBelow : m;
+                            const float f = raise ? ex2(m - m_new) : 1.f;
+                            l *= f;
+                            m = m_new;
+                            if (j > 0) {
+                                wait(&room.o_done[slot][(t - 1) & 1], (t - 1) >> 1);
+                                tc_fence_after_sync();
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 32) {
+                                    uint32_t o[32];
+                                    tmem_ld32(tO + D * slot + c, o);
+                                    tmem_wait_ld(o);
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                    tmem_st32(tO + D * slot + c, o);
                                 }
                             }
                         }
-                        fence_proxy_async_smem();
+                        const float ref = m == -INFINITY ? 0.f : m;    // nothing seen yet
+                        const uint64_t neg2 = f32x2_pack(-ref, -ref);
+                        uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 1
+                        for (int c = 0; c < kTrKeys; c += 32) {
+                            uint32_t v[32];
+                            tmem_ld32(tS + c, v);
+                            tmem_wait_ld(v);
+                            if (masked) hide(v, c);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t parts[16];                    // hi, then lo
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    float a0, a1;
+                                    f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(v[16 * h + 2 * i]),
+                                                                      __uint_as_float(v[16 * h + 2 * i + 1])), sl2, neg2), a0, a1);
+                                    const float p0 = ex2(a0), p1 = ex2(a1);
+                                    ps[i & 3] = f32x2_add(ps[i & 3], f32x2_pack(p0, p1));
+                                    split_pair<T>(p0, p1, parts[i], parts[8 + i]);
+                                }
+                                tmem_st16(tS + c + 16 * h, parts);
+                            }
+                        }
+                        float q8[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) f32x2_unpack(ps[e], q8[2 * e], q8[2 * e + 1]);
+                        l += ((q8[0] + q8[1]) + (q8[2] + q8[3])) + ((q8[4] + q8[5]) + (q8[6] + q8[7]));
+                        // the next tile's scores, where they are there already
+                        tmem_wait_st();
                     }
-                    bad |= P.share ? bar_or(both, 2 * kTrRows, odd) : bar_or(barrier, kTrRows, odd);
+                    if (masked) {
+                        // V rows past the context may hold anything: clear them.
+                        // Of the tree's, elements that are not finite are cleared
+                        // too, since the tensor cores would carry them into rows
+                        // that do not see them; rows that do get them back below.
+                        // Thread r has half r / 64 of key r % 64.  That the tile is
+                        // there its issuer of P V says, which waits for every phase
+                        // of V's barriers in turn: this slot's tile before may be
+                        // five back (the last but one of a piece, two that the
+                        // other slot took alone, the first of this one), so a
+                        // parity alone could be that of an earlier tile.
+                        bool odd = false;
+                        if (P.clears(slot)) {
+                            const int tile = n + (k - P.k0), vs = tile % Lay::kVStages;
+                            wait(&room.v_there[slot], cleared++);
+                            wait(&room.v_full[vs], tile / Lay::kVStages);
+                            const int key = key0 + (r & 63);
+                            uint8_t* vd = smem + Lay::kV + vs * Lay::kTile + (D == 128 ? (r >> 6) * Lay::kHalf : 0) +
+                                          (r & 63) * 128;
+                            if (D == 64 && r >= 64) {
+                            } else if (key >= P.s.L) {
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    *reinterpret_cast<uint4*>(vd + (((c ^ r) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                            } else if (key >= base) {
+                                uint32_t any = 0u;
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    const uint4 w = lds128(vd + (((c ^ r) & 7) << 4));
+                                    any |= not_finite<T>(w.x) | not_finite<T>(w.y) | not_finite<T>(w.z) | not_finite<T>(w.w);
+                                }
+                                if (any != 0u) {
+                                    odd = true;
+                                    for (int c = 0; c < 32; ++c) {
+                                        uint32_t* w = reinterpret_cast<uint32_t*>(vd) + c;
+                                        *w &= ~(((not_finite<T>(*w) >> 15) & 0x00010001u) * 0xffffu);
+                                    }
+                                }
+                            }
+                            fence_proxy_async_smem();
+                        }
+                        bad |= P.share ? bar_or(both, 2 * kTrRows, odd) : bar_or(barrier, kTrRows, odd);
+                    }
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&room.p_full[slot][t & 1]);
+                    ++t, ++j;
                 }
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&room.p_full[slot][t & 1]);
-                ++t, ++j;
             }
             n += count;
             // ---- the piece's end ------------------------------------------------
@@ -979,6 +1025,26 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
             if (own > 0) {
                 wait(&room.o_done[slot][(t - 1) & 1], (t - 1) >> 1);
                 tc_fence_after_sync();
+                if (live && own > kTrRun) {
+                    const float f = held_scale();
+#pragma unroll 1
+                    for (int d = 0; d < D; d += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + D * slot + d, o);
+                        tmem_wait_ld(o);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const float4 y = held[(d / 4 + q) * kTrRows];
+                            o[4 * q] = __float_as_uint(fmaf(y.x, f, __uint_as_float(o[4 * q])));
+                            o[4 * q + 1] = __float_as_uint(fmaf(y.y, f, __uint_as_float(o[4 * q + 1])));
+                            o[4 * q + 2] = __float_as_uint(fmaf(y.z, f, __uint_as_float(o[4 * q + 2])));
+                            o[4 * q + 3] = __float_as_uint(fmaf(y.w, f, __uint_as_float(o[4 * q + 3])));
+                        }
+                        tmem_st32(tO + D * slot + d, o);
+                    }
+                    tmem_wait_st();
+                    l = fmaf(held_l, f, l);
+                }
                 const bool full = count == P.n;
                 const int64_t rec = ((int64_t)blockIdx.x * 2 + (P.k0 > 0 ? 0 : 1)) * kTrSlots + (P.share ? slot : 0);
                 float w0 = slot == 0 ? 1.f : 0.f, w1 = 1.f - w0, top = m;

@@ -30,8 +30,8 @@ struct TreeParams {
     int sides, heads;              // a lane's CTAs: sides (256 rows of queries each) x KV heads
     int ctas;                      // lanes
     bool whole;                    // lanes are dealt whole sequences
-    float* rec_o;                  // [ctas][sides][heads][2][2][128][D]
-    float2* rec_ml;                // the same without D: reference (log2 units) and sum
+    float* rec_o;                  // [ctas][sides][heads][2][2][D / 4][128][4]
+    float2* rec_ml;                // [ctas][sides][heads][2][2][128]: reference (log2 units) and sum
 #ifdef PA_TEST_HOOKS
     // Test builds only: CTA test_cta's loaders issue no tile from test_tile
     // on, and waits give up after test_wait_limit_ns.
