@@ -578,7 +578,9 @@ int pa_evict_fp8(void* k_cache, void* v_cache, const int32_t* block_tables,
  * token, the others are drafted after it: parents[row] < i is the node (of the
  * same sequence) that node i follows, negative: the context itself.  A parent
  * that is not below its node counts as negative and sets PA_DEVERR_BAD_INDEX.
- * Sequences have at most PA_TREE_NODES nodes; more are cut off and set
+ * Sequences have at most PA_TREE_NODES nodes (and max_query_len, where a call
+ * has it); those past the first so many are cut off: their rows are not written
+ * and the others' results are what they would be.  That sets
  * PA_DEVERR_BAD_CONTEXT, as do a C_b below 0 or above L_b and rows outside
  * [0, num_tokens).  A step: pa_norm_rope_and_cache (or pa_rope_and_cache) and
  * pa_tree_attention in every layer, then pa_accept_tree and pa_commit_path.

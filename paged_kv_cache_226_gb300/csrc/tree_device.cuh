@@ -32,7 +32,10 @@ __device__ __forceinline__ TreeSeq tree_sequence(const TreeParams& p, int b, boo
     s.L = at(p.context_lens + b);
     const int start = at(p.query_start + b), end = at(p.query_start + b + 1);
     if (s.L < 0 || s.L > p.max_context) bad = true, s.L = s.L < 0 ? 0 : p.max_context;
-    tree_rows(start, end, p.num_tokens, min(p.max_query, s.L), s, bad);
+    tree_rows(start, end, p.num_tokens, s.L, s, bad);
+    // nodes past the first max_query are cut off, with their tokens: the others
+    // stay where they are
+    if (s.C > p.max_query) bad = true, s.L -= s.C - p.max_query, s.C = p.max_query;
     if (bad && report) flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
     return s;
 }
