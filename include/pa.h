@@ -683,7 +683,10 @@ int pa_accept_tree(const int64_t* draft, const int64_t* target, const int32_t* p
  *   new_lens[b] = base + path_lens[b].
  * A path is ascending (as pa_accept_tree gives it) within [0, C_b); one that
  * is not, or longer than C_b, sets PA_DEVERR_BAD_INDEX, and its sequence is
- * left as it is (new_lens[b] = L_b).  path [num_seqs][path_stride] int32.
+ * left as it is (new_lens[b] = L_b).  So is, with PA_DEVERR_BAD_CONTEXT, one
+ * whose L_b is not within its table (new_lens[b] is clamped to that) or whose
+ * C_b is below 0 or above L_b.  Of a tree with more than PA_TREE_NODES nodes the
+ * first so many can be kept.  path [num_seqs][path_stride] int32.
  * k_caches, v_caches: host arrays of num_layers (at most 1024) device pointers,
  * one cache pair per layer, all of the shape shp and of the same block tables;
  * no cache may be listed twice or lie over another.  The blocks that hold a

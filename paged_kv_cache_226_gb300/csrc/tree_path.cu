@@ -94,16 +94,16 @@ __global__ void __launch_bounds__(kCommitThreads)
     const int entry = t < p.path_stride ? p.path[(int64_t)b * p.path_stride + t] : -1;
     const int before = t > 0 && t < p.path_stride ? p.path[(int64_t)b * p.path_stride + t - 1] : -1;
     int64_t C = (int64_t)p.query_start[b + 1] - p.query_start[b];
-    bool bad = false;
-    if (L < 0 || L > max_context) bad = true, L = L < 0 ? 0 : max_context;
-    if (C < 0 || C > L) bad = true, C = C < 0 ? 0 : L;
-    if (bad && report && t == 0) flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
-    const int base = L - (int)C;
-    const bool wrong = n < 0 || n > C || n > p.path_stride || n > PA_TREE_NODES ||
-                       (t < n && (entry <= before || entry >= C));
-    const bool refused = __syncthreads_or(wrong) != 0;
+    // where the tree lies is not known, and nothing moves
+    bool nowhere = false;
+    if (L < 0 || L > max_context) nowhere = true, L = L < 0 ? 0 : max_context;
+    if (C < 0 || C > L) nowhere = true, C = 0;
+    const int base = L - (int)C, nodes = min((int)C, PA_TREE_NODES);
+    if ((nowhere || nodes < C) && report && t == 0) flag_error(p.err, PA_DEVERR_BAD_CONTEXT);
+    const bool wrong = n < 0 || n > nodes || n > p.path_stride || (t < n && (entry <= before || entry >= nodes));
+    const bool refused = __syncthreads_or(wrong) != 0 || nowhere;
     if (report && t == 0) {
-        if (refused) flag_error(p.err, PA_DEVERR_BAD_INDEX);
+        if (refused && !nowhere) flag_error(p.err, PA_DEVERR_BAD_INDEX);
         p.new_lens[b] = refused ? L : base + n;
     }
     if (refused) return;
