@@ -624,7 +624,8 @@ int pa_norm_rope_and_cache_fp8(const void* q, int64_t q_stride, const void* k, i
  * q, out [num_tokens][num_q_heads][head_dim], not overlapping; rows behind the
  * last sequence are not written.  parents [num_tokens] int32, null: every node
  * follows the one before it (a line of drafted tokens, or the chunks of
- * pa_prefill).  scale must be > 0, and finite also times log2(e) (and k_scale).
+ * pa_prefill).  scale times log2(e) (and k_scale) must be a normal positive fp32
+ * number.
  * max_query_len >= every C_b, at most PA_TREE_NODES (else PA_ERR_UNSUPPORTED);
  * max_context_len >= every L_b; values outside these bounds are clamped and
  * set PA_DEVERR_BAD_CONTEXT.  Bounds that come to 2^31 key tiles of 64 or more

@@ -1,6 +1,7 @@
 // C-ABI entry points of the operators of speculative decoding: host-side
 // validation and dispatch.  Declarations and contracts: include/pa.h.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "tree_internal.h"
@@ -48,7 +49,8 @@ int tree_attention(const void* q, const void* k_cache, const void* v_cache, cons
     if (st != PA_OK) return st;
     if (fp8 && (st = pa::check_fp8(shp, k_scale, v_scale)) != PA_OK) return st;
     const float scale_log2 = scale * (fp8 ? k_scale : 1.f) * pa::kLog2e;
-    if (num_tokens < 0 || num_tokens > 0x7fffffffll || !(scale > 0.f) || !std::isfinite(scale_log2))
+    // a product that is zero would make NaN of scores that the mask sets to minus infinity
+    if (num_tokens < 0 || num_tokens > 0x7fffffffll || !(scale_log2 >= FLT_MIN) || !std::isfinite(scale_log2))
         return PA_ERR_INVALID_ARG;
     if ((st = check_tree(max_query_len, max_context_len)) != PA_OK) return st;
     if (shp->num_seqs == 0) return PA_OK;

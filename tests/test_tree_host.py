@@ -207,3 +207,18 @@ def test_plain_acceptance_by_hand():
 def test_plain_visibility_by_hand():
     seen = tu.visible([-1, 0, 0, 2], 6, 4)
     assert seen.int().tolist() == [[1, 1, 1, 0, 0, 0], [1, 1, 1, 1, 0, 0], [1, 1, 1, 0, 1, 0], [1, 1, 1, 0, 1, 1]]
+
+
+@pytest.mark.parametrize("scale,k_scale", [(1e-25, 1e-25), (1e-20, 1e-19), (1e-38, 0.1), (1e-45, 1.0), (-1e-20, 1.0),
+                                           (1e30, 1e10), (float("nan"), 1.0)])
+def test_scales_whose_product_leaves_fp32(pa, scale, k_scale):
+    assert tree(pa, scale=scale, fp8=(k_scale, 1.0)) == BAD
+    if k_scale == 1.0:
+        assert tree(pa, scale=scale) == BAD
+
+
+def test_the_smallest_scale(pa):
+    """Accepted up to the workspace's check, which comes after the scales'."""
+    assert tree(pa, scale=2e-38, ws=None) == lib.PA_ERR_WORKSPACE
+    assert tree(pa, scale=2e-19, fp8=(1e-19, 1.0), ws=None) == lib.PA_ERR_WORKSPACE
+    assert tree(pa, scale=2e-39, ws=None) == BAD
