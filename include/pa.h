@@ -670,7 +670,8 @@ int pa_tree_attention_fp8(const void* q, const void* k_cache, const void* v_cach
  *   next[b]                         target of the path's end
  * A sequence without nodes gets length 0 and next -1.  draft, target, parents:
  * [num_tokens]; path [num_seqs][max_query_len], 1 <= max_query_len <=
- * PA_TREE_NODES.  One launch.
+ * PA_TREE_NODES.  path, path_lens and next must not overlap the inputs or one
+ * another.  One launch.
  */
 int pa_accept_tree(const int64_t* draft, const int64_t* target, const int32_t* parents,
                    const int32_t* query_start, int32_t num_seqs, int64_t num_tokens,
@@ -692,8 +693,8 @@ int pa_accept_tree(const int64_t* draft, const int64_t* target, const int32_t* p
  * one cache pair per layer, all of the shape shp and of the same block tables;
  * no cache may be listed twice or lie over another.  The blocks that hold a
  * tree must not be shared with another sequence.  A block id outside the pool
- * sets PA_DEVERR_BAD_CONTEXT and its rows are not moved.  new_lens must not be
- * an input array.  One launch for every 64 layers.  pa_commit_path_fp8: the
+ * sets PA_DEVERR_BAD_CONTEXT and its rows are not moved.  new_lens must not
+ * overlap an input array.  One launch for every 64 layers.  pa_commit_path_fp8: the
  * same on E4M3 caches.
  */
 int pa_commit_path(void* const* k_caches, void* const* v_caches, int32_t num_layers,

@@ -18,6 +18,29 @@ bool overlap(const void* a, const void* b, uint64_t bytes) {
     return x == y || (x < y ? y - x : x - y) < bytes;
 }
 
+// A buffer of `count` elements of `size` bytes.
+struct Span {
+    const void* at;
+    int64_t count;
+    int size;
+    bool meets(const Span& o) const {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(at), y = reinterpret_cast<uintptr_t>(o.at);
+        return count > 0 && o.count > 0 && x < y + (uint64_t)o.count * o.size && y < x + (uint64_t)count * size;
+    }
+};
+
+// Whether an output lies over an input or over another output.
+template <size_t kOutputs, size_t kInputs>
+bool written_over(const Span (&outputs)[kOutputs], const Span (&inputs)[kInputs]) {
+    for (size_t i = 0; i < kOutputs; ++i) {
+        for (const Span& in : inputs)
+            if (in.at && outputs[i].meets(in)) return true;
+        for (size_t j = 0; j < i; ++j)
+            if (outputs[i].meets(outputs[j])) return true;
+    }
+    return false;
+}
+
 int finish(cudaError_t e) {
     if (e == cudaSuccess) return PA_OK;
     pa::record_cuda_error(static_cast<int>(e));
@@ -100,8 +123,11 @@ int commit_path(void* const* k_caches, void* const* v_caches, int32_t num_layers
         return PA_ERR_INVALID_ARG;
     for (const int32_t* a : {block_tables, context_lens, query_start, path, path_lens, (const int32_t*)new_lens})
         if (!aligned(a, 4)) return PA_ERR_INVALID_ARG;
-    for (const int32_t* a : {block_tables, context_lens, query_start, path, path_lens})
-        if (a == new_lens) return PA_ERR_INVALID_ARG;
+    // other CTAs, and the launches of further layers, read the inputs still
+    const int64_t B = shp->num_seqs;
+    if (written_over({{new_lens, B, 4}}, {{block_tables, B * shp->max_blocks_per_seq, 4}, {context_lens, B, 4},
+                                          {query_start, B + 1, 4}, {path, B * path_stride, 4}, {path_lens, B, 4}}))
+        return PA_ERR_INVALID_ARG;
     // no cache twice and none over another: two CTAs would move the same rows
     const uint64_t bytes = (uint64_t)shp->num_blocks * shp->block_size * shp->num_kv_heads * shp->head_dim * (fp8 ? 1 : 2);
     void* all[2 * kMaxLayers];
@@ -170,6 +196,10 @@ int pa_accept_tree(const int64_t* draft, const int64_t* target, const int32_t* p
         return PA_ERR_INVALID_ARG;
     if (!aligned(draft, 8) || !aligned(target, 8) || !aligned(next, 8) || !aligned(parents, 4) ||
         !aligned(query_start, 4) || !aligned(path, 4) || !aligned(path_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    const int64_t B = num_seqs;
+    if (written_over({{path, B * max_query_len, 4}, {path_lens, B, 4}, {next, B, 8}},
+                     {{draft, num_tokens, 8}, {target, num_tokens, 8}, {parents, num_tokens, 4}, {query_start, B + 1, 4}}))
         return PA_ERR_INVALID_ARG;
     pa::AcceptParams p{};
     cudaError_t e = pa::error_word(&p.err);

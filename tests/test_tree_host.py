@@ -222,3 +222,22 @@ def test_the_smallest_scale(pa):
     assert tree(pa, scale=2e-38, ws=None) == lib.PA_ERR_WORKSPACE
     assert tree(pa, scale=2e-19, fp8=(1e-19, 1.0), ws=None) == lib.PA_ERR_WORKSPACE
     assert tree(pa, scale=2e-39, ws=None) == BAD
+
+
+def test_outputs_over_inputs_are_refused(pa):
+    """Entry points that would read what another CTA, or the launch before, has written."""
+    at = 1 << 20
+    pointers = dict(bt=at, cl=2 * at, qs=3 * at, path=4 * at, lens=5 * at)          # of 2 sequences, 4 blocks, 8 nodes
+    for name, size in dict(bt=32, cl=8, qs=12, path=64, lens=8).items():
+        for off in (-4, 0, size - 4):
+            assert commit(pa, ks=(64 * at,), vs=(128 * at,), **{k: ctypes.c_void_p(v) for k, v in pointers.items()},
+                          new=ctypes.c_void_p(pointers[name] + off)) == BAD, (name, off)
+    pointers = dict(draft=at, target=2 * at, par=3 * at, qs=4 * at, path=5 * at, lens=6 * at, next=7 * at)
+    sizes = dict(draft=72, target=72, par=36, qs=12, path=64, lens=8, next=16)      # of 9 nodes, 8 a path
+    for out in ("path", "lens", "next"):
+        for name, size in sizes.items():
+            for off in (8 - sizes[out], 0, size // 8 * 8 - 8):
+                if name == out:
+                    continue
+                args = {**pointers, out: pointers[name] + off}
+                assert accept(pa, **{k: ctypes.c_void_p(v) for k, v in args.items()}) == BAD, (out, name, off)
