@@ -56,8 +56,7 @@
 //
 // An E4M3 cache's codes are brought to the 16-bit type (exactly) by four
 // warps between the loaders' ring and the operands'.  Eight warps, each with
-// half a tile, took 76.8 us for the first case over E4M3 in bf16 (four 77.7),
-// but 79.6 in fp16 (78.0).
+// half a tile, were within 2 % either way for the first case over E4M3.
 //
 // Warps: 0 loads K tiles and 2 V tiles, 1 and 3 issue the slots' S, 14 and 15
 // their P V, 4 .. 7 are slot 0's softmax and 8 .. 11 slot 1's, 12 makes the
@@ -751,26 +750,14 @@ __global__ void __launch_bounds__(tr_threads(kFp8), 1)
                         if (!ok) break;
                         const uint8_t* src = src0 + at.at * Lay::kCodes;
                         uint8_t* dst = dst0 + st * Lay::kTile;
-                        auto codes_of = [&](const uint8_t* at, int j) {
-                            return lds128(at + j * 512 + ((c ^ ((r4 + 4 * j) & 7)) << 4));
-                        };
-                        // Four instructions a pair of codes in bf16: there the
-                        // next pass's codes are requested a pass ahead (64 x up
-                        // to 2048 tokens 85.3 us, so 77.7; 4 x 32k to 50k 180,
-                        // so 173).  One in fp16, which is slower so (78.0, 81.2).
-                        constexpr bool kAhead = kBf16;
-                        uint4 ahead[4];
-#pragma unroll
-                        for (int j = 0; kAhead && j < 4; ++j) ahead[j] = codes_of(src, j);
+                        // Four instructions a pair of codes in bf16, one in fp16.
+                        // Requesting the next pass's codes a pass ahead takes
+                        // longer (64 x up to 2048 tokens in bf16 87.4 us, so 79.2).
 #pragma unroll 1
                         for (int i = 0; i < kTrKeys / 16; ++i, src += 16 * 128, dst += 16 * 128) {
                             uint4 x[4];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) x[j] = kAhead ? ahead[j] : codes_of(src, j);
-                            if (kAhead && i + 1 < kTrKeys / 16) {
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) ahead[j] = codes_of(src + 16 * 128, j);
-                            }
+                            for (int j = 0; j < 4; ++j) x[j] = lds128(src + j * 512 + ((c ^ ((r4 + 4 * j) & 7)) << 4));
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 uint32_t y[8];
