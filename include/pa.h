@@ -591,8 +591,9 @@ int pa_evict_fp8(void* k_cache, void* v_cache, const int32_t* block_tables,
  * pa_norm_rope_and_cache: pa_rope_and_cache with the heads of q and k
  * normalised first and positions on several axes.  For every head x of q or k
  *   y[d] = weight[d] * x[d] / sqrt(mean_d(x[d]^2) + eps)
- * in fp32, not rounded before it is turned; q_weight and k_weight [head_dim]
- * of type T, null: ones.  Pair i turns by positions[axes[i]][t] * inv_freq[i]:
+ * in fp32, not rounded before it is turned (values past 2^60 make squares that
+ * leave fp32 and a head of zeros; a head of zeros with eps = 0 is NaN, as the
+ * formula has it); q_weight and k_weight [head_dim] of type T, null: ones.  Pair i turns by positions[axes[i]][t] * inv_freq[i]:
  * positions is [num_axes][num_tokens] int64, axes [rotary_dim / 2] int32
  * (null: all 0), 1 <= num_axes <= 8; an axis outside them counts as 0 and sets
  * PA_DEVERR_BAD_INDEX.  eps must be finite and not negative.  Everything else

@@ -23,16 +23,19 @@
 //                       together hold it to 2^-15 (bf16) or 2^-22 (fp16, whose
 //                       reference stays 2^7 below the maximum so that small P
 //                       are not lost below its range)
-//   O += P V            128 x D x 64 for each part, P from tensor memory
+//   O += P V            128 x D x 64 for each part, P from tensor memory, cut off
+//                       toward zero for 128 key tiles, then added by rounding.  A
+//                       third part of P (2^-22 in bf16 too) would be a third more
+//                       products, which is what bounds wide and long batches
 //
 // A tile passes from products to softmax, to products and back in some 1900
 // cycles beside the work itself, so a slot needs two tiles under way: with one
 // S of 128 keys per slot 8 heads x 4 sequences of 32k to 50k tokens at 240 rows
-// took 190 us, with one of 64 keys 227, with two of 64 keys 186 (now 156).
+// took 190 us, with one of 64 keys 227, with two of 64 keys 186 (now 163).
 // Rows that leave half of the tile empty stay so: twice the same 64 rows, the
 // lower with one part of P and the upper with the other, take half of the P V
 // products, but put softmax warps beside the issuers (32 sequences over an
-// E4M3 cache below 95 us, so 85).
+// E4M3 cache below 95 us, 85 without).
 //
 // The CTAs side by side, one for each 256 rows and KV head (or so many KV
 // heads as divide the SMs well), make a lane.  The key tiles of all sequences,
@@ -45,14 +48,17 @@
 // What bounds it: K and V come once from HBM, 512 B a token and KV head at
 // D 128 in 16 bits, and the products cost 6 D operations (P in two parts) for
 // each row and token: to some 190 rows a KV head the bytes are the longer,
-// above them the products.  Measured, back to back:
-//   64 x 128 .. 2048 tokens, 64 rows, 8 KV heads    60.5 us   301 MB, 5.0 TB/s
-//   16 x 2k .. 8k, 512 rows                          165 us   tensor pipe 78 %
-//   4 x 32k .. 50k, 240 rows                         156 us   tensor pipe 82 %
-//   32 x 4096, E4M3, 64 rows                          85 us   277 MB, 3.3 TB/s
+// above them the products.  Measured back to back, 40 calls at a time, and for
+// seconds on end, where the power limit lowers the clock under dense products:
+//   64 x 128 .. 2048 tokens, 64 rows, 8 KV heads    60.7, 61 us    301 MB, 5.0 TB/s
+//   16 x 2k .. 8k, 512 rows                          167, 190 us   tensor pipe 78 %
+//   4 x 32k .. 50k, 240 rows                         163, 186 us   tensor pipe 80 %
+//   32 x 4096, E4M3, 64 rows                          81, 83 us    277 MB, 3.4 TB/s
+//   the first over E4M3, fp16 and bf16              73.3, 79.5 us  159 MB, 2.0 TB/s
 // Of the first some 8 us pass until the first scores are there and 4 between
-// the last output and the join's end; its loads alone took 49.  The last has
-// 54 % of the tensor pipe and 43 % of the issue slots: without its softmax 69.
+// the last output and the join's end; its loads alone took 49.  The fourth has
+// 56 % of the tensor pipe and 45 % of the issue slots: without its softmax 69,
+// when it took 85.
 //
 // An E4M3 cache's codes are brought to the 16-bit type (exactly) by four
 // warps between the loaders' ring and the operands'.  Eight warps, each with
@@ -63,7 +69,7 @@
 // trees' lines, 16 .. 19 convert codes.  An issuer takes some 1200 cycles for a
 // tile's S beside these warps, so one for both slots would hold them up, and
 // which scheduler it shares with whom counts (S of both slots by 2 and 3, or
-// P V by 12 and 13: 160 to 165 us for the third case).  A barrier's parity
+// P V by 12 and 13: 160 to 165 us for the third case, then 156).  A barrier's parity
 // tells a phase from the one before it alone, so whoever waits for a phase has
 // seen that the one before is over: by waiting for every phase in turn, or as
 // the comments at the waits say.
